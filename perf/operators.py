@@ -263,7 +263,7 @@ def _prepare_rope(c, seed):
     if own:
         from serving_attention_gb300 import step
 
-        s["setup"] = step.rope_setup(D, c["rot"], interleaved=c["interleaved"], theta=c["theta"], scaling=c["scaling"],
+        s["setup"] = step.rotary_setup(D, c["rot"], interleaved=c["interleaved"], theta=c["theta"], scaling=c["scaling"],
                                      factor=c["factor"], original_positions=8192)
     return s
 
