@@ -98,7 +98,12 @@ typedef struct {
     int32_t rope_max_positions;
     float rope_theta;
     float rope_scale;
-    int32_t reserved;
+    /* 1: plans for fi_batch_paged_attention_run_differential (fi_diff.h), the
+     * difference of two softmax maps per query head; the other runs refuse
+     * them (0, the default: ordinary attention).  A sliding window and sink
+     * tokens apply; a soft-cap, RoPE or a cascade plan with it are
+     * FI_ERR_UNSUPPORTED, other values FI_ERR_INVALID_ARG. */
+    int32_t differential;
 } fi_plan_config;
 
 /* Plain data returned by fi_plan; passed to run by value semantics. */
@@ -112,7 +117,8 @@ typedef struct {
     int32_t chunk_decode;        /* KV tokens per chunk chosen for 16-row tiles */
     int32_t chunk_prefill;       /* KV tokens per chunk chosen for 256-row tiles */
     int32_t num_decode_items, num_prefill_items;
-    int32_t variant;             /* bit 0: logits soft-cap; bit 1: sliding window (and sink) mask; bit 2: RoPE */
+    int32_t variant;             /* bit 0: logits soft-cap; bit 1: sliding window (and sink) mask; bit 2: RoPE;
+                                    bit 3: differential */
     int64_t int_ws_bytes_used;   /* bytes of the int workspace written (and copied) by the plan */
     int64_t max_partial_rows;    /* capacity of the float workspace, from the config */
     int32_t num_late_merge_units; /* split units of prefill-class tiles: merged by a second launch */

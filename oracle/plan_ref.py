@@ -52,11 +52,15 @@ Rule:
     the fixed per-item latency of the kernel.  Items are sorted by
     (-cost, -T, b, hk, qt, chunk) and each goes to the CTA with the smallest
     load, ties to the smaller CTA index (longest processing time first).
+    Differential plans (two softmax maps per row): prefill-class tiles hold
+    128 rows, no multi-head units, every chunk of a merge unit takes 2 * rows
+    partial rows, and every merge unit carries the late flag.
  6. Output: header (with the variant: window, sink, soft-cap bits, and for
     RoPE its position capacity, theta and scale bits and the table offset;
     then the count of late units, the partial rows used, the batch's query
     tokens, the cascade fields, the count of 16-row items and the most rows of
-    a cascade merge entry (0 without cascade)), per-CTA
+    a cascade merge entry (0 without cascade; of a merge unit in a differential plan, which has a magic of its
+    own)), per-CTA
     CSR offsets, items in CTA order (an item: its 8 fields, its request's
     table entry, H for a multi-head unit or 0, three zeros; within a CTA the 256-row items first,
     then the 16-row items, each in the order dealt), merge units, zeroed merge
@@ -68,8 +72,8 @@ import heapq
 
 import numpy as np
 
-MAGIC = 0x46495031
-TILE_DECODE, TILE_PREFILL = 16, 256
+MAGIC, MAGIC_DIFF = 0x46495031, 0x46495044
+TILE_DECODE, TILE_PREFILL, TILE_PREFILL_DIFF = 16, 256, 128
 HEADER_INTS = 32
 ROPE_PAIRS = 64
 ITEM_INTS = 16
@@ -117,6 +121,11 @@ def _config_status(cfg, head_dim, num_qo_heads, num_kv_heads, page_size, causal)
     if window < -1 or sink < 0 or not (cap >= 0.0) or cap == float("inf"):
         return INVALID_ARG
     rope_max = cfg.get("rope_max_positions", 0)
+    diff = cfg.get("differential", 0)
+    if diff not in (0, 1):
+        return INVALID_ARG
+    if diff and (cap > 0.0 or rope_max > 0):
+        return UNSUPPORTED
     theta = float(np.float32(cfg.get("rope_theta", 10000.0)))
     rscale = float(np.float32(cfg.get("rope_scale", 1.0)))
     if rope_max < 0 or (rope_max > 0 and not (0 < theta < float("inf") and 0 < rscale < float("inf"))):
@@ -195,7 +204,7 @@ def make_cascade_plan(cfg: dict, shared_qo_indptr, shared_kv_indptr, shared_kv_i
         return st, None, None
     if not _pow2_page(shared_page_size):
         return UNSUPPORTED, None, None
-    if cfg.get("window_left", -1) >= 0 or cfg.get("rope_max_positions", 0) > 0:
+    if cfg.get("window_left", -1) >= 0 or cfg.get("rope_max_positions", 0) > 0 or cfg.get("differential", 0):
         return UNSUPPORTED, None, None
     batch = len(qo_indptr) - 1
     if batch + num_shared > cfg["max_batch"]:
@@ -237,6 +246,9 @@ def _plan(cfg, reqs, num_shared, shared_page_size, block_of, total_qo, num_qo_he
     theta = float(np.float32(cfg.get("rope_theta", 10000.0)))
     rscale = float(np.float32(cfg.get("rope_scale", 1.0)))
     batch = len(reqs)
+    diff = bool(cfg.get("differential", 0))
+    # rows of a tile: with two maps per row, the two 128-row halves of a prefill tile are the maps
+    height = {TILE_DECODE: TILE_DECODE, TILE_PREFILL: TILE_PREFILL_DIFF if diff else TILE_PREFILL}
     C = cfg["num_ctas"]
     lq = [r[1] for r in reqs]
     lkv = [r[3] for r in reqs]
@@ -278,10 +290,10 @@ def _plan(cfg, reqs, num_shared, shared_page_size, block_of, total_qo, num_qo_he
         T = tile_of(b)
         cache_page = shared_page_size if b < num_shared else page_size
         heads = mh if (T == TILE_DECODE and lq[b] == 1 and cache_page == 1 and rope_max == 0
-                       and b >= num_shared) else 1
+                       and b >= num_shared and not diff) else 1
         for hk in range(0, num_kv_heads, heads):
-            for qt in range(_ceil_div(R, T)):
-                r0, r1 = (0, R * heads) if heads > 1 else (qt * T, min(R, (qt + 1) * T))
+            for qt in range(_ceil_div(R, height[T])):
+                r0, r1 = (0, R * heads) if heads > 1 else (qt * height[T], min(R, (qt + 1) * height[T]))
                 rng = ranges_of(b, T, r0, r1, heads)
                 unit_at[(b, hk, qt)] = len(units)
                 units.append((b, hk, qt, T, r0, r1, rng, heads))
@@ -313,14 +325,14 @@ def _plan(cfg, reqs, num_shared, shared_page_size, block_of, total_qo, num_qo_he
         pieces = [(s_ + i * ck, min(e_, s_ + (i + 1) * ck))
                   for s_, e_ in rng for i in range(_ceil_div(e_ - s_, ck))]
         n = max(1, len(pieces))
-        nrows = r1 - r0
+        nrows = (r1 - r0) * (2 if diff else 1)  # partial rows of a chunk: one per row and map
         base, m = -1, -1
         if n > 1 or cascade:
             base = part_rows
             part_rows += n * nrows
         if n > 1 and not cascade:
             m = len(merges)
-            merges.append((b, hk, r0, r1, n, base, 0 if T == TILE_DECODE else 1, 0))
+            merges.append((b, hk, r0, r1, n, base, 0 if T == TILE_DECODE and not diff else 1, 0))
         unit_parts.append((base, n))
         for i, (k0, k1) in enumerate(pieces or [(0, 0)]):
             cost = ((k1 - k0) * heads + ITEM_COST_TOKENS) * weight[T]
@@ -384,13 +396,13 @@ def _plan(cfg, reqs, num_shared, shared_page_size, block_of, total_qo, num_qo_he
 
     rope_off = (int_workspace_ints(cfg) * 4 + 255) // 256 * 256 // 4 if rope_max > 0 else 0
     n_dec = sum(1 for _, f in items if lq[f[0]] * group <= 16)
-    ws[:HEADER_INTS] = [MAGIC, n_items, n_merge, C, batch, causal, off_cta, off_items, off_merge,
+    ws[:HEADER_INTS] = [MAGIC_DIFF if diff else MAGIC, n_items, n_merge, C, batch, causal, off_cta, off_items, off_merge,
                         off_cnt, off_req, 0, num_qo_heads, num_kv_heads, page_size, total_ints,
                         window, sink, bits(cap), rope_max,
                         bits(theta) if rope_max > 0 else 0, bits(rscale) if rope_max > 0 else 0, rope_off,
                         sum(1 for m in merges if m[6]), part_rows, total_qo, num_shared,
                         off_cascade if cascade else 0, len(entries), shared_page_size if cascade else 0, n_dec,
-                        max((e[3] - e[2] for e in entries), default=0)]
+                        max((m[3] - m[2] for m in merges) if diff else (e[3] - e[2] for e in entries), default=0)]
     pos = 0
     for c in range(C):
         ws[off_cta + c] = pos
@@ -413,7 +425,8 @@ def _plan(cfg, reqs, num_shared, shared_page_size, block_of, total_qo, num_qo_he
                 head_dim=head_dim, page_size=page_size, causal=causal, chunk_decode=chunk[16],
                 chunk_prefill=chunk[TILE_PREFILL], num_decode_items=n_dec, num_prefill_items=n_items - n_dec,
                 int_ws_bytes_used=4 * total_ints, max_partial_rows=cfg["max_partial_rows"],
-                variant=(1 if cap > 0 else 0) | (2 if window >= 0 else 0) | (4 if rope_max > 0 else 0),
+                variant=(1 if cap > 0 else 0) | (2 if window >= 0 else 0) | (4 if rope_max > 0 else 0)
+                | (8 if diff else 0),
                 num_shared=num_shared, num_cascade_merges=len(entries), prefill_caches=prefill_caches)
     return OK, ws, info
 

@@ -39,10 +39,10 @@ class PlanConfig(ctypes.Structure):
                 ("decode_cost_weight", ctypes.c_int32), ("prefill_cost_weight", ctypes.c_int32),
                 ("split_factor", ctypes.c_int32), ("window_left", ctypes.c_int32), ("sink_tokens", ctypes.c_int32),
                 ("logits_soft_cap", ctypes.c_float), ("rope_max_positions", ctypes.c_int32),
-                ("rope_theta", ctypes.c_float), ("rope_scale", ctypes.c_float), ("reserved", ctypes.c_int32)]
+                ("rope_theta", ctypes.c_float), ("rope_scale", ctypes.c_float), ("differential", ctypes.c_int32)]
 
     def as_dict(self) -> dict:
-        return {f: getattr(self, f) for f, _ in self._fields_ if f != "reserved"}
+        return {f: getattr(self, f) for f, _ in self._fields_}
 
 
 class PlanInfo(ctypes.Structure):
@@ -146,7 +146,7 @@ def make_plan_config(num_ctas: int, **overrides) -> PlanConfig:
     cfg = PlanConfig(num_ctas=num_ctas, max_batch=8192, max_items=1 << 17, max_merge_units=1 << 15,
                      max_partial_rows=1 << 19, decode_min_chunk=256, prefill_min_chunk=1024, decode_cost_weight=8,
                      prefill_cost_weight=9, split_factor=1, window_left=-1, sink_tokens=0, logits_soft_cap=0.0,
-                     rope_max_positions=0, rope_theta=10000.0, rope_scale=1.0)
+                     rope_max_positions=0, rope_theta=10000.0, rope_scale=1.0, differential=0)
     for k, v in overrides.items():
         setattr(cfg, k, v)
     return cfg

@@ -532,6 +532,7 @@ extern "C" fi_status fi_default_plan_config(int device, fi_plan_config* out) {
   out->rope_max_positions = 0;
   out->rope_theta = 10000.f;
   out->rope_scale = 1.f;
+  out->differential = 0;
   return FI_OK;
 }
 
@@ -745,6 +746,7 @@ fi_status run_impl(const fi_plan_info* info, const void* q, int64_t q_stride_tok
   if (info->num_ctas < 1 || q_num_tokens < 1 || !std::isfinite(sm_scale)) return FI_ERR_INVALID_ARG;
   if (info->num_partial_rows > 0 && !float_workspace_dev) return FI_ERR_INVALID_ARG;
   if (info->num_shared > 0 && !shared) return FI_ERR_INVALID_ARG;  // a cascade plan needs the shared cache
+  if (info->variant & 8) return FI_ERR_INVALID_ARG;  // a differential plan has a run of its own
   if (info->head_dim != kHeadDim) return FI_ERR_UNSUPPORTED;
   if (dtype != FI_FP16 && dtype != FI_BF16) return FI_ERR_UNSUPPORTED;
   if (info->num_kv_heads < 1 || info->num_qo_heads % info->num_kv_heads) return FI_ERR_UNSUPPORTED;

@@ -12,7 +12,7 @@
 //
 // Rule (this library's reading of that goal; the pages give no cost model):
 //  * request b -> R = qo_len * G packed rows (row t*G+g = token t, head hk*G+g);
-//    tile T = 16 when R <= 16, else 256;
+//    tile T = 16 when R <= 16, else 256 (128 with differential attention);
 //  * unit (b, hk, q-tile) with its visible KV ranges: [0, hi) with hi the
 //    bottom-right causal end; with a sliding window W and S sink tokens, the
 //    window range starts at the first token's q_pos - W rounded down to the
@@ -171,6 +171,8 @@ fi_status check_config(const fi_plan_config* cfg, int32_t head_dim, int32_t num_
   if (cfg->decode_min_chunk < 1 || cfg->prefill_min_chunk < 1) return FI_ERR_INVALID_ARG;
   const float cap = cfg->logits_soft_cap;
   if (cfg->window_left < -1 || cfg->sink_tokens < 0 || !(cap >= 0.f) || cap == HUGE_VALF) return FI_ERR_INVALID_ARG;
+  if (cfg->differential != 0 && cfg->differential != 1) return FI_ERR_INVALID_ARG;
+  if (cfg->differential && (cap > 0.f || cfg->rope_max_positions > 0)) return FI_ERR_UNSUPPORTED;
   const int32_t rope_max = cfg->rope_max_positions;
   if (rope_max < 0 || (rope_max > 0 && !(cfg->rope_theta > 0.f && cfg->rope_theta < HUGE_VALF &&
                                          cfg->rope_scale > 0.f && cfg->rope_scale < HUGE_VALF)))
@@ -192,6 +194,13 @@ fi_status plan_requests(const fi_plan_config* cfg, const std::vector<Req>& reqs,
   const int32_t window = cfg->window_left, sink = cfg->sink_tokens;
   const float cap = cfg->logits_soft_cap;
   const int32_t rope_max = cfg->rope_max_positions;
+  // Differential attention: each packed row has two softmax maps, so a
+  // prefill-class tile holds 128 rows (the two M tiles of the tensor-core path
+  // are the two maps of the same rows) and a row's partial state takes two
+  // partial rows, the maps' blocks of a chunk one after the other.
+  const bool diff = cfg->differential != 0;
+  const int32_t maps = diff ? 2 : 1;
+  const int32_t prefill_rows = diff ? FI_TILE_PREFILL_DIFF : FI_TILE_PREFILL;
   // Chunk boundaries fall on pages of every cache the plan reads.
   const int32_t max_page = std::max(page_size, cascade ? shared_page_size : page_size);
 
@@ -207,14 +216,15 @@ fi_status plan_requests(const fi_plan_config* cfg, const std::vector<Req>& reqs,
     first_unit[b] = int32_t(units.size());
     const bool causal_b = causal && b >= num_shared;  // a shared block's keys precede all its queries
     const int32_t tile = rows <= FI_TILE_DECODE ? FI_TILE_DECODE : FI_TILE_PREFILL;
-    const int32_t tiles = int32_t(ceil_div(rows, tile));
+    const int32_t height = tile == FI_TILE_DECODE ? FI_TILE_DECODE : prefill_rows;
+    const int32_t tiles = int32_t(ceil_div(rows, height));
     // One query token of the plan's own page-1 cache: fi_mh_heads() KV heads
     // per unit (FI_MH_ROWS packed rows), so that short requests pay the
     // per-item cost once per unit, not once per head, and every TMA box brings
     // one token of all the unit's heads.
     const int32_t cache_page = b < num_shared ? shared_page_size : page_size;
     const int32_t heads = (tile == FI_TILE_DECODE && rq.qo_len == 1 && cache_page == 1 && rope_max == 0 &&
-                           b >= num_shared)
+                           b >= num_shared && !diff)
                               ? fi_mh_heads(group, num_kv_heads)
                               : 1;
     for (int32_t hk = 0; hk < num_kv_heads; hk += heads) {
@@ -225,8 +235,8 @@ fi_status plan_requests(const fi_plan_config* cfg, const std::vector<Req>& reqs,
         u.qt = qt;
         u.tile = tile;
         u.heads = heads;
-        u.row0 = qt * tile;
-        u.row1 = heads > 1 ? int32_t(rows * heads) : int32_t(std::min<int64_t>(rows, int64_t(qt + 1) * tile));
+        u.row0 = qt * height;
+        u.row1 = heads > 1 ? int32_t(rows * heads) : int32_t(std::min<int64_t>(rows, int64_t(qt + 1) * height));
         // query tokens of the unit's first and last rows (a multi-head unit: token 0)
         const int64_t t_first = heads > 1 ? 0 : u.row0 / group, t_last = heads > 1 ? 0 : (u.row1 - 1) / group;
         const int64_t q_first = int64_t(rq.kv_len) - rq.qo_len + t_first;
@@ -293,6 +303,7 @@ fi_status plan_requests(const fi_plan_config* cfg, const std::vector<Req>& reqs,
   std::vector<int64_t> unit_base(units.size(), -1), unit_n(units.size(), 0);
   int64_t partial_rows = 0;
   int32_t n_late = 0;  // merge units of prefill-class tiles, merged after the run
+  int32_t merge_rows_max = 0;  // differential: the merge launch gives each unit this many row tasks
   int32_t prefill_caches = 0;
   for (size_t ui = 0; ui < units.size(); ++ui) {
     const Unit& u = units[ui];
@@ -308,14 +319,15 @@ fi_status plan_requests(const fi_plan_config* cfg, const std::vector<Req>& reqs,
     const int32_t nrows = u.row1 - u.row0;
     if (n > 1 || cascade) {
       base = partial_rows;
-      partial_rows += n * nrows;
+      partial_rows += n * nrows * maps;
     }
     if (n > 1 && !cascade) {
       merge_id = int32_t(merge_rows.size() / FI_MERGE_INTS);
-      const int32_t late = u.tile == FI_TILE_DECODE ? 0 : 1;
+      const int32_t late = u.tile == FI_TILE_DECODE && !diff ? 0 : 1;
       const int32_t m[FI_MERGE_INTS] = {u.b, u.hk, u.row0, u.row1, int32_t(n), int32_t(base), late, 0};
       merge_rows.insert(merge_rows.end(), m, m + FI_MERGE_INTS);
       n_late += late;
+      if (diff) merge_rows_max = std::max(merge_rows_max, nrows);
     }
     unit_base[ui] = base;
     unit_n[ui] = n;
@@ -332,7 +344,7 @@ fi_status plan_requests(const fi_plan_config* cfg, const std::vector<Req>& reqs,
       const Req& rq = reqs[u.b];
       const int32_t f[FI_ITEM_INTS] = {u.b,         u.hk,        u.row0,
                                        u.row1,      int32_t(k0), int32_t(k1),
-                                       base >= 0 ? int32_t(base + i * nrows) : -1, merge_id,
+                                       base >= 0 ? int32_t(base + i * nrows * maps) : -1, merge_id,
                                        rq.qo_start, rq.qo_len,   rq.page_start,
                                        rq.kv_len,   u.heads > 1 ? u.heads : 0, 0,
                                        0,           0};
@@ -460,14 +472,15 @@ fi_status plan_requests(const fi_plan_config* cfg, const std::vector<Req>& reqs,
   }
   const int32_t rope_off = rope_max > 0 ? int32_t(fi_rope_table_offset(fi::plan_capacity_ints(cfg)) / 4) : 0;
   const int32_t header[FI_HEADER_INTS] = {
-      FI_PLAN_MAGIC,        int32_t(n_items),   int32_t(n_merge),   C,
+      diff ? FI_PLAN_MAGIC_DIFF : FI_PLAN_MAGIC, int32_t(n_items),   int32_t(n_merge),   C,
       batch,                causal,             int32_t(off_cta),   int32_t(off_items),
       int32_t(off_merge),   int32_t(off_cnt),   int32_t(off_req),   0,
       num_qo_heads,         num_kv_heads,       page_size,          int32_t(total_ints),
       window,               sink,               cap_bits,           rope_max,
       theta_bits,           scale_bits,         rope_off,           n_late,
       int32_t(partial_rows), total_qo,          num_shared,         cascade ? int32_t(off_cascade) : 0,
-      int32_t(n_cascade),   cascade ? shared_page_size : 0, int32_t(n_decode), cascade_rows_max};
+      int32_t(n_cascade),   cascade ? shared_page_size : 0, int32_t(n_decode),
+      diff ? merge_rows_max : cascade_rows_max};
   std::memcpy(ws, header, sizeof header);
 
   fi_plan_info info;
@@ -489,7 +502,7 @@ fi_status plan_requests(const fi_plan_config* cfg, const std::vector<Req>& reqs,
   info.num_prefill_items = int32_t(n_items - n_decode);
   info.int_ws_bytes_used = total_ints * 4;
   info.max_partial_rows = cfg->max_partial_rows;
-  info.variant = (cap > 0.f ? 1 : 0) | (window >= 0 ? 2 : 0) | (rope_max > 0 ? 4 : 0);
+  info.variant = (cap > 0.f ? 1 : 0) | (window >= 0 ? 2 : 0) | (rope_max > 0 ? 4 : 0) | (diff ? 8 : 0);
   info.num_shared = num_shared;
   info.num_cascade_merges = int32_t(n_cascade);
   info.prefill_caches = prefill_caches;
@@ -532,7 +545,7 @@ extern "C" fi_status fi_plan_cascade_host(
     return FI_ERR_UNSUPPORTED;
   // Positions of the two levels are not tied to one sequence here: the
   // position-dependent variants (sliding window, sink, RoPE) are not offered.
-  if (cfg->window_left >= 0 || cfg->rope_max_positions > 0) return FI_ERR_UNSUPPORTED;
+  if (cfg->window_left >= 0 || cfg->rope_max_positions > 0 || cfg->differential) return FI_ERR_UNSUPPORTED;
   if (int64_t(batch) + num_shared > cfg->max_batch) return FI_ERR_CAPACITY;
   if (workspace_bytes < size_t(fi::plan_capacity_ints(cfg)) * 4) return FI_ERR_CAPACITY;
   std::vector<Req> reqs;

@@ -47,6 +47,11 @@
 //                  fi_rope_init, never part of a plan's copy
 // Every section starts on a multiple of 4 ints (16 bytes).
 //
+// A differential plan (its own magic) counts partial rows per softmax map:
+// chunk i of a merge unit of n rows wrote rows part_base + i * 2n + r for
+// map 1 and part_base + i * 2n + n + r for map 2, and all its merge units are
+// late.
+//
 // Float workspace: partial LSE (natural log) at [0, max_partial_rows), partial
 // O (already divided by its own softmax sum) at
 // fi_partial_o_offset(max_partial_rows), head_dim floats per row.
@@ -54,6 +59,7 @@
 #include <stdint.h>
 
 #define FI_PLAN_MAGIC 0x46495031
+#define FI_PLAN_MAGIC_DIFF 0x46495044  // a differential plan: read by its own run only
 #define FI_HEADER_INTS 32
 #define FI_ITEM_INTS 16
 #define FI_MERGE_INTS 8
@@ -64,6 +70,7 @@
 
 #define FI_TILE_DECODE 16
 #define FI_TILE_PREFILL 256  // two 128-row M tiles sharing each K/V tile
+#define FI_TILE_PREFILL_DIFF 128  // differential: 128 rows, their two softmax maps sharing each K/V tile
 #define FI_GRANULE_DECODE 64
 #define FI_GRANULE_PREFILL 128
 #define FI_ITEM_COST_TOKENS 256  // fixed cost of a work item in the deal, in KV tokens of its class
@@ -102,7 +109,8 @@ enum {
   FI_H_NUM_CASCADE = 28,      // cascade: merge entries
   FI_H_SHARED_PAGE_SIZE = 29, // cascade: page size of the shared KV cache
   FI_H_NUM_DECODE_ITEMS = 30, // items of 16-row tiles (the CUDA-core path)
-  FI_H_CASCADE_ROWS_MAX = 31  // cascade: the most packed rows of one merge entry; 0 otherwise
+  FI_H_CASCADE_ROWS_MAX = 31  // cascade: the most packed rows of one merge entry; differential: of one
+                              // merge unit; 0 otherwise
 };
 
 #define FI_ROPE_PAIRS 64  // dims i and i + 64 of head_dim 128 form a rotated pair
