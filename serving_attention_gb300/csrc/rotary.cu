@@ -1,0 +1,321 @@
+// rotary.cu -- rotary positions of a step's new tokens, and the append of
+// their keys and values to the paged cache.
+//
+// Pair i of a token at position n turns by the angle n f_i.  The rate is kept
+// in turns per position as a 64-bit binary fraction F_i, so n F_i mod 2^64 is
+// the exact fraction of a turn at any position: no table to read, no argument
+// reduction, and the angle of position 10^6 is as exact as that of position
+// 1 (an fp32 product of position and rate is off by 0.06 rad there).
+//
+// Bound by the bytes of q, k and v (each read and written once).  One warp per
+// token, or per part of one when there are few tokens: a lane computes the cos
+// and sin of its pairs once, and uses them for every head.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "../../include/fi_step.h"
+#include "ptx.cuh"
+
+namespace fi {
+namespace {
+
+constexpr int kRotaryWarps = 8;  // warps of a block
+constexpr int kRotaryAhead = 4;  // 16-byte loads a lane has in flight per operand
+
+struct RotaryRows {  // rows of one operand: token t (or cache slot), head h
+  const uint16_t* in;
+  int64_t in_tok, in_head;
+  uint16_t* out;
+  int64_t out_tok, out_head;  // out_tok: elements per token, or per page with slots
+  int64_t out_slot;
+  int32_t heads;
+};
+
+struct RotaryParams {
+  RotaryRows q, k, v;
+  const int32_t* positions;
+  const int32_t* slots;  // null: k goes to row t of k.out
+  int64_t num_slots;
+  int32_t num_tokens, parts;  // warps per token
+  int32_t log2_page;
+  int32_t head_chunks, rot_chunks, v_chunks;  // 16-byte chunks of a head, of its rotated part, of a v row
+  float amplitude;
+  uint64_t turns[FI_ROTARY_MAX_PAIRS];
+};
+
+template <typename T>
+__device__ __forceinline__ void unpack(const uint4& u, float (&f)[8]) {
+  const float2 a = Elem<T>::to_float2(u.x), b = Elem<T>::to_float2(u.y), c = Elem<T>::to_float2(u.z),
+               d = Elem<T>::to_float2(u.w);
+  f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y; f[4] = c.x; f[5] = c.y; f[6] = d.x; f[7] = d.y;
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+  return make_uint4(Elem<T>::from_float2(f[0], f[1]), Elem<T>::from_float2(f[2], f[3]),
+                    Elem<T>::from_float2(f[4], f[5]), Elem<T>::from_float2(f[6], f[7]));
+}
+
+// A task is 16 bytes of one head (interleaved pairs, or a part that is copied)
+// or the two 16-byte chunks that hold 8 pairs (half layout).
+template <typename T, bool kInterleaved>
+__global__ void __launch_bounds__(32 * kRotaryWarps) rotary_kernel(const __grid_constant__ RotaryParams a) {
+  __shared__ float2 s_cs[kRotaryWarps][FI_ROTARY_MAX_PAIRS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t w = int64_t(blockIdx.x) * kRotaryWarps + warp;
+  const int t = int(w / a.parts), part = int(w - int64_t(t) * a.parts);
+  if (t >= a.num_tokens) return;
+  const int32_t pos = __ldg(a.positions + t);
+  const int64_t slot = a.slots ? __ldg(a.slots + t) : t;
+  float2* cs = s_cs[warp];
+  for (int i = lane; i < a.rot_chunks * 4; i += 32) {
+    const uint64_t turn = uint64_t(int64_t(pos)) * a.turns[i];  // modulo one turn
+    float sn, c;
+    sincospif(float(int32_t(turn >> 32)) * 4.6566128730773926e-10f, &sn, &c);  // 2^-31: half turns in [-1, 1]
+    cs[i] = make_float2(c * a.amplitude, sn * a.amplitude);
+  }
+  __syncwarp();
+  const bool store_kv = !a.slots || (slot >= 0 && slot < a.num_slots);
+  const int64_t page = a.slots ? slot >> a.log2_page : slot;
+  const int64_t in_page = a.slots ? slot & ((int64_t(1) << a.log2_page) - 1) : 0;
+
+  const int pair_tasks = kInterleaved ? a.rot_chunks : a.rot_chunks >> 1;
+  const int per_head = pair_tasks + a.head_chunks - a.rot_chunks;
+  const int tasks = (a.q.heads + (store_kv ? a.k.heads : 0)) * per_head;
+  const int step = 32 * a.parts;
+  const uint16_t *q_in = a.q.in + t * a.q.in_tok, *k_in = a.k.in + t * a.k.in_tok;
+  uint16_t *q_out = a.q.out + t * a.q.out_tok, *k_out = a.k.out + page * a.k.out_tok + in_page * a.k.out_slot;
+  for (int i0 = 32 * part + lane; i0 < tasks; i0 += kRotaryAhead * step) {
+    uint4 lo[kRotaryAhead], hi[kRotaryAhead];
+    uint16_t* dst[kRotaryAhead];
+    int chunk[kRotaryAhead];
+#pragma unroll
+    for (int u = 0; u < kRotaryAhead; ++u) {
+      const int i = i0 + u * step;
+      dst[u] = nullptr;
+      if (i < tasks) {
+        const int h = i / per_head, c = i - h * per_head;
+        const bool is_q = h < a.q.heads;
+        const uint16_t* src = is_q ? q_in + h * a.q.in_head : k_in + (h - a.q.heads) * a.k.in_head;
+        dst[u] = is_q ? q_out + h * a.q.out_head : k_out + (h - a.q.heads) * a.k.out_head;
+        chunk[u] = c < pair_tasks ? c : c + a.rot_chunks - pair_tasks;
+        lo[u] = *reinterpret_cast<const uint4*>(src + 8 * chunk[u]);
+        if (!kInterleaved && c < pair_tasks) hi[u] = *reinterpret_cast<const uint4*>(src + 8 * (c + pair_tasks));
+        dst[u] += 8 * chunk[u];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kRotaryAhead; ++u) {
+      if (!dst[u]) continue;
+      if (chunk[u] < pair_tasks) {
+        float x[8];
+        unpack<T>(lo[u], x);
+        if (kInterleaved) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 r = cs[4 * chunk[u] + e];
+            const float x0 = x[2 * e], x1 = x[2 * e + 1];
+            x[2 * e] = x0 * r.x - x1 * r.y;
+            x[2 * e + 1] = x1 * r.x + x0 * r.y;
+          }
+        } else {
+          float y[8];
+          unpack<T>(hi[u], y);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float2 r = cs[8 * chunk[u] + e];
+            const float x0 = x[e], x1 = y[e];
+            x[e] = x0 * r.x - x1 * r.y;
+            y[e] = x1 * r.x + x0 * r.y;
+          }
+          *reinterpret_cast<uint4*>(dst[u] + 8 * pair_tasks) = pack<T>(y);
+        }
+        lo[u] = pack<T>(x);
+      }
+      *reinterpret_cast<uint4*>(dst[u]) = lo[u];
+    }
+  }
+  if (!store_kv || !a.v_chunks) return;
+  const int v_tasks = a.v.heads * a.v_chunks;
+  const uint16_t* v_in = a.v.in + t * a.v.in_tok;
+  uint16_t* v_out = a.v.out + page * a.v.out_tok + in_page * a.v.out_slot;
+  for (int i0 = 32 * part + lane; i0 < v_tasks; i0 += kRotaryAhead * step) {
+    uint4 x[kRotaryAhead];
+    uint16_t* dst[kRotaryAhead];
+#pragma unroll
+    for (int u = 0; u < kRotaryAhead; ++u) {
+      const int i = i0 + u * step;
+      dst[u] = nullptr;
+      if (i < v_tasks) {
+        const int h = i / a.v_chunks, c = i - h * a.v_chunks;
+        x[u] = *reinterpret_cast<const uint4*>(v_in + h * a.v.in_head + 8 * c);
+        dst[u] = v_out + h * a.v.out_head + 8 * c;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kRotaryAhead; ++u)
+      if (dst[u]) *reinterpret_cast<uint4*>(dst[u]) = x[u];
+  }
+}
+
+constexpr int kPartWarps = 4096;  // warps wanted on the card before a token is left to one warp
+
+cudaError_t launch_rotary(RotaryParams& a, const fi_rotary* rot, fi_dtype dtype, cudaStream_t s) {
+  a.head_chunks = rot->head_dim / 8;
+  a.rot_chunks = rot->rot_dim / 8;
+  a.amplitude = rot->amplitude;
+  std::memcpy(a.turns, rot->turns, sizeof(uint64_t) * size_t(rot->rot_dim / 2));
+  // Few tokens: their tasks are spread over more warps, at least one task a lane
+  const int per_head = (rot->interleaved ? a.rot_chunks : a.rot_chunks / 2) + a.head_chunks - a.rot_chunks;
+  const int tasks = (a.q.heads + a.k.heads) * per_head, v_tasks = a.v.heads * a.v_chunks;
+  const int most = ((tasks > v_tasks ? tasks : v_tasks) + 31) / 32;
+  const int want = kPartWarps / a.num_tokens;
+  a.parts = want < 1 ? 1 : want > most ? (most > 0 ? most : 1) : want;
+  const int64_t warps = int64_t(a.num_tokens) * a.parts;
+  const unsigned blocks = unsigned((warps + kRotaryWarps - 1) / kRotaryWarps);
+  const int threads = 32 * kRotaryWarps;
+  if (dtype == FI_BF16) {
+    if (rot->interleaved)
+      rotary_kernel<__nv_bfloat16, true><<<blocks, threads, 0, s>>>(a);
+    else
+      rotary_kernel<__nv_bfloat16, false><<<blocks, threads, 0, s>>>(a);
+  } else {
+    if (rot->interleaved)
+      rotary_kernel<__half, true><<<blocks, threads, 0, s>>>(a);
+    else
+      rotary_kernel<__half, false><<<blocks, threads, 0, s>>>(a);
+  }
+  return cudaGetLastError();
+}
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+bool stride_ok(int64_t elems) { return elems >= 0 && elems % 8 == 0; }
+
+fi_status check_rotary(const fi_rotary* rot, int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                       fi_dtype dtype) {
+  if (!rot || num_tokens < 0 || num_q_heads < 0 || num_kv_heads < 0) return FI_ERR_INVALID_ARG;
+  if (rot->head_dim < 16 || rot->head_dim > 2 * FI_ROTARY_MAX_PAIRS || rot->head_dim % 8 || rot->rot_dim < 16 ||
+      rot->rot_dim > rot->head_dim || rot->rot_dim % 16 || (rot->interleaved != 0 && rot->interleaved != 1))
+    return FI_ERR_UNSUPPORTED;
+  if (num_q_heads > 65536 || num_kv_heads > 65536) return FI_ERR_UNSUPPORTED;
+  return dtype == FI_FP16 || dtype == FI_BF16 ? FI_OK : FI_ERR_UNSUPPORTED;
+}
+
+}  // namespace
+}  // namespace fi
+
+using namespace fi;
+
+extern "C" fi_status fi_rotary_setup(const fi_rotary_config* cfg, fi_rotary* out) {
+  if (!cfg || !out) return FI_ERR_INVALID_ARG;
+  const int D = cfg->head_dim, R = cfg->rot_dim;
+  if (D < 16 || D > 2 * FI_ROTARY_MAX_PAIRS || D % 8 || R < 16 || R > D || R % 16) return FI_ERR_UNSUPPORTED;
+  if (cfg->interleaved != 0 && cfg->interleaved != 1) return FI_ERR_INVALID_ARG;
+  if (cfg->scaling < FI_ROTARY_NONE || cfg->scaling > FI_ROTARY_YARN) return FI_ERR_INVALID_ARG;
+  const double s = cfg->factor, two_pi = 6.283185307179586476925;
+  double theta = cfg->theta;
+  if (!(theta > 1.0 && std::isfinite(theta) && s >= 1.0 && std::isfinite(s))) return FI_ERR_INVALID_ARG;
+  if (!(cfg->amplitude >= 0.f && std::isfinite(cfg->amplitude))) return FI_ERR_INVALID_ARG;
+  const double L = cfg->original_positions, lo = cfg->low_turns, hi = cfg->high_turns;
+  const bool parts = cfg->scaling == FI_ROTARY_BY_PARTS, yarn = cfg->scaling == FI_ROTARY_YARN;
+  if ((parts || yarn) && !(L > 0 && lo > 0 && hi > lo && std::isfinite(hi))) return FI_ERR_INVALID_ARG;
+  if (cfg->scaling == FI_ROTARY_NTK) theta *= std::pow(s, double(R) / double(R - 2));
+  auto dim_of = [&](double turns) { return R * std::log(L / (turns * two_pi)) / (2.0 * std::log(theta)); };
+  double d_lo = 0, d_hi = 0;
+  if (yarn) {
+    d_lo = std::fmax(0.0, std::floor(dim_of(hi)));
+    d_hi = std::fmin(double(R - 1), std::ceil(dim_of(lo)));
+  }
+  std::memset(out, 0, sizeof *out);
+  out->head_dim = D;
+  out->rot_dim = R;
+  out->interleaved = cfg->interleaved;
+  out->amplitude = cfg->amplitude > 0.f ? cfg->amplitude : yarn ? float(0.1 * std::log(s) + 1.0) : 1.f;
+  for (int i = 0; i < R / 2; ++i) {
+    double f = std::pow(theta, -2.0 * i / R);
+    double slow = 0.0;  // share of the slowed rate f / s
+    if (cfg->scaling == FI_ROTARY_LINEAR) slow = 1.0;
+    if (parts) slow = 1.0 - std::fmin(1.0, std::fmax(0.0, (L * f / two_pi - lo) / (hi - lo)));
+    if (yarn) slow = std::fmin(1.0, std::fmax(0.0, (i - d_lo) / (d_hi > d_lo ? d_hi - d_lo : 1e-3)));
+    f = f / s * slow + f * (1.0 - slow);
+    out->turns[i] = uint64_t(std::ldexp(f / two_pi, 64) + 0.5);  // f <= 1, so under a turn
+  }
+  return FI_OK;
+}
+
+extern "C" fi_status fi_rotary_apply(const fi_rotary* rot, const int32_t* positions, int32_t num_tokens,
+                                     const void* q_in, int64_t q_in_stride_tok, int64_t q_in_stride_head, void* q_out,
+                                     int64_t q_out_stride_tok, int64_t q_out_stride_head, int32_t num_q_heads,
+                                     const void* k_in, int64_t k_in_stride_tok, int64_t k_in_stride_head, void* k_out,
+                                     int64_t k_out_stride_tok, int64_t k_out_stride_head, int32_t num_kv_heads,
+                                     fi_dtype dtype, void* stream) {
+  const fi_status st = check_rotary(rot, num_tokens, num_q_heads, num_kv_heads, dtype);
+  if (st != FI_OK) return st;
+  if (!positions || (num_q_heads && (!q_in || !q_out)) || (num_kv_heads && (!k_in || !k_out)))
+    return FI_ERR_INVALID_ARG;
+  if (!aligned(positions, 4)) return FI_ERR_ALIGNMENT;
+  if (num_q_heads && (!aligned(q_in, 16) || !aligned(q_out, 16) || !stride_ok(q_in_stride_tok) ||
+                      !stride_ok(q_in_stride_head) || !stride_ok(q_out_stride_tok) || !stride_ok(q_out_stride_head)))
+    return FI_ERR_ALIGNMENT;
+  if (num_kv_heads && (!aligned(k_in, 16) || !aligned(k_out, 16) || !stride_ok(k_in_stride_tok) ||
+                       !stride_ok(k_in_stride_head) || !stride_ok(k_out_stride_tok) || !stride_ok(k_out_stride_head)))
+    return FI_ERR_ALIGNMENT;
+  if (num_tokens == 0 || num_q_heads + num_kv_heads == 0) return FI_OK;
+  RotaryParams a;
+  std::memset(&a, 0, sizeof a);
+  a.q = {static_cast<const uint16_t*>(q_in), q_in_stride_tok, q_in_stride_head, static_cast<uint16_t*>(q_out),
+         q_out_stride_tok, q_out_stride_head, 0, num_q_heads};
+  a.k = {static_cast<const uint16_t*>(k_in), k_in_stride_tok, k_in_stride_head, static_cast<uint16_t*>(k_out),
+         k_out_stride_tok, k_out_stride_head, 0, num_kv_heads};
+  a.positions = positions;
+  a.num_tokens = num_tokens;
+  return launch_rotary(a, rot, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FI_OK : FI_ERR_CUDA;
+}
+
+extern "C" fi_status fi_rotary_append(const fi_rotary* rot, const int32_t* positions, const int32_t* slots,
+                                      int32_t num_tokens, const void* q_in, int64_t q_in_stride_tok,
+                                      int64_t q_in_stride_head, void* q_out, int64_t q_out_stride_tok,
+                                      int64_t q_out_stride_head, int32_t num_q_heads, const void* k_in,
+                                      int64_t k_in_stride_tok, int64_t k_in_stride_head, const void* v_in,
+                                      int64_t v_in_stride_tok, int64_t v_in_stride_head, int32_t v_dim,
+                                      int32_t num_kv_heads, void* k_cache, const int64_t k_strides[3], void* v_cache,
+                                      const int64_t v_strides[3], int32_t page_size, int32_t num_pages,
+                                      fi_dtype dtype, void* stream) {
+  const fi_status st = check_rotary(rot, num_tokens, num_q_heads, num_kv_heads, dtype);
+  if (st != FI_OK) return st;
+  if (v_dim < 0 || v_dim > 512 || v_dim % 8 || page_size < 1 || page_size > 128 || (page_size & (page_size - 1)))
+    return FI_ERR_UNSUPPORTED;
+  if (!positions || !slots || num_kv_heads < 1 || num_pages < 1 || !k_in || !k_cache || !k_strides ||
+      (num_q_heads && (!q_in || !q_out)) || (v_dim && (!v_in || !v_cache || !v_strides)))
+    return FI_ERR_INVALID_ARG;
+  if (!aligned(positions, 4) || !aligned(slots, 4) || !aligned(k_in, 16) || !aligned(k_cache, 16) ||
+      !stride_ok(k_in_stride_tok) || !stride_ok(k_in_stride_head))
+    return FI_ERR_ALIGNMENT;
+  if (num_q_heads && (!aligned(q_in, 16) || !aligned(q_out, 16) || !stride_ok(q_in_stride_tok) ||
+                      !stride_ok(q_in_stride_head) || !stride_ok(q_out_stride_tok) || !stride_ok(q_out_stride_head)))
+    return FI_ERR_ALIGNMENT;
+  if (v_dim && (!aligned(v_in, 16) || !aligned(v_cache, 16) || !stride_ok(v_in_stride_tok) ||
+                !stride_ok(v_in_stride_head)))
+    return FI_ERR_ALIGNMENT;
+  for (int i = 0; i < 3; ++i)
+    if (!stride_ok(k_strides[i]) || (v_dim && !stride_ok(v_strides[i]))) return FI_ERR_ALIGNMENT;
+  if (num_tokens == 0) return FI_OK;
+  RotaryParams a;
+  std::memset(&a, 0, sizeof a);
+  a.q = {static_cast<const uint16_t*>(q_in), q_in_stride_tok, q_in_stride_head, static_cast<uint16_t*>(q_out),
+         q_out_stride_tok, q_out_stride_head, 0, num_q_heads};
+  a.k = {static_cast<const uint16_t*>(k_in), k_in_stride_tok, k_in_stride_head, static_cast<uint16_t*>(k_cache),
+         k_strides[0], k_strides[2], k_strides[1], num_kv_heads};
+  if (v_dim)
+    a.v = {static_cast<const uint16_t*>(v_in), v_in_stride_tok, v_in_stride_head, static_cast<uint16_t*>(v_cache),
+           v_strides[0], v_strides[2], v_strides[1], num_kv_heads};
+  a.v_chunks = v_dim / 8;
+  a.positions = positions;
+  a.slots = slots;
+  a.num_slots = int64_t(num_pages) * page_size;
+  while ((1 << a.log2_page) < page_size) ++a.log2_page;
+  a.num_tokens = num_tokens;
+  return launch_rotary(a, rot, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FI_OK : FI_ERR_CUDA;
+}

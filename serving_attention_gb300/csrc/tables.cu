@@ -1,0 +1,241 @@
+// tables.cu -- page tables and slot maps of a step, built on the GPU.
+//
+// Three prefix sums over the requests (query tokens, pages, pages taken from
+// the free list), then every page-table entry and every token looked up in
+// them.  One launch without any wait between blocks: each block scans all
+// lengths itself (8 bytes a request, from L2 after the first block), keeps the
+// sums in shared memory and takes its share of the entries.  Bound by latency
+// for a decode step, by the bytes of the page table for a full house.
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cstdint>
+
+#include "../../include/fi_step.h"
+#include "launch.h"
+
+namespace fi {
+namespace {
+
+constexpr int kTableThreads = 512;
+constexpr int kTableWarps = kTableThreads / 32;
+
+struct TableParams {
+  const int32_t *qo_lens, *kv_lens;
+  int32_t batch, log2_page;
+  int32_t* table;
+  int64_t table_stride;
+  int32_t table_width;
+  const int32_t* free_pages;
+  int32_t num_free;
+  const int32_t* free_head;
+  int32_t *qo_indptr, *kv_indptr, *last_page_len, *kv_indices;
+  int32_t max_pages;
+  int32_t *positions, *slots;
+  int32_t max_tokens;
+  int32_t* counts;
+};
+
+struct Sums {
+  int64_t qo, pages, taken;
+};
+
+// The last entry of s[0 .. n] at or below x (s[0] <= x < s[n]).
+__device__ __forceinline__ int find(const int32_t* s, int n, int x) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (s[mid] <= x)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kTableThreads) step_tables_kernel(const __grid_constant__ TableParams a) {
+  extern __shared__ int32_t smem[];
+  const int B = a.batch, P = 1 << a.log2_page, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int32_t *s_qo = smem, *s_kv = smem + B + 1, *s_new = smem + 2 * (B + 1);
+  __shared__ Sums s_warp[kTableWarps];
+  __shared__ int s_bad;
+  if (tid == 0) s_bad = 0;
+  __syncthreads();
+  const int32_t head = a.free_head ? __ldg(a.free_head) : 0;
+  auto pages_of = [&](int32_t len) { return int32_t((int64_t(len) + P - 1) >> a.log2_page); };
+
+  // thread t sums requests [t * per, (t + 1) * per), then the threads are scanned
+  const int per = (B + kTableThreads - 1) / kTableThreads;
+  const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
+  Sums mine{0, 0, 0};
+  bool bad = false;
+  for (int b = b0; b < b1; ++b) {
+    const int32_t q = __ldg(a.qo_lens + b), kv = __ldg(a.kv_lens + b);
+    if (q < 0 || q > kv || int64_t(kv) > (int64_t(a.table_width) << a.log2_page)) {
+      bad = true;
+      continue;
+    }
+    mine.qo += q;
+    mine.pages += pages_of(kv);
+    mine.taken += pages_of(kv) - pages_of(kv - q);
+  }
+  if (bad) s_bad = 1;
+  Sums inc = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, inc.qo, d), y = __shfl_up_sync(0xffffffffu, inc.pages, d),
+                  z = __shfl_up_sync(0xffffffffu, inc.taken, d);
+    if (lane >= d) {
+      inc.qo += x;
+      inc.pages += y;
+      inc.taken += z;
+    }
+  }
+  if (lane == 31) s_warp[warp] = inc;
+  __syncthreads();
+  Sums before{0, 0, 0}, total{0, 0, 0};
+#pragma unroll
+  for (int w = 0; w < kTableWarps; ++w) {
+    const Sums x = s_warp[w];
+    if (w < warp) {
+      before.qo += x.qo;
+      before.pages += x.pages;
+      before.taken += x.taken;
+    }
+    total.qo += x.qo;
+    total.pages += x.pages;
+    total.taken += x.taken;
+  }
+  // Every block sees the same lengths and comes to the same verdict.
+  int status = FI_OK;
+  if (s_bad)
+    status = FI_ERR_INVALID_ARG;
+  else if (total.qo > a.max_tokens || total.pages > a.max_pages || head < 0 || head + total.taken > a.num_free)
+    status = FI_ERR_CAPACITY;
+  if (blockIdx.x == 0 && tid < FI_STEP_COUNTS) {
+    auto cut = [](int64_t x) { return int32_t(x < INT_MAX ? x : INT_MAX); };
+    a.counts[tid] = tid == 0   ? cut(total.qo)
+                    : tid == 1 ? cut(total.pages)
+                    : tid == 2 ? cut(total.taken)
+                    : tid == 3 ? (status == FI_OK ? int32_t(head + total.taken) : head)
+                    : tid == 4 ? status
+                               : 0;
+  }
+  if (status != FI_OK) return;
+  {
+    int32_t qo = int32_t(before.qo + inc.qo - mine.qo), kv = int32_t(before.pages + inc.pages - mine.pages),
+            nw = int32_t(before.taken + inc.taken - mine.taken);
+    for (int b = b0; b < b1; ++b) {
+      s_qo[b] = qo;
+      s_kv[b] = kv;
+      s_new[b] = nw;
+      const int32_t q = __ldg(a.qo_lens + b), len = __ldg(a.kv_lens + b);
+      if (blockIdx.x == 0) {
+        a.qo_indptr[b] = qo;
+        a.kv_indptr[b] = kv;
+        a.last_page_len[b] = len > 0 ? ((len - 1) & (P - 1)) + 1 : 0;
+      }
+      qo += q;
+      kv += pages_of(len);
+      nw += pages_of(len) - pages_of(len - q);
+    }
+    if (tid == 0) {
+      s_qo[B] = int32_t(total.qo);
+      s_kv[B] = int32_t(total.pages);
+      if (blockIdx.x == 0) {
+        a.qo_indptr[B] = int32_t(total.qo);
+        a.kv_indptr[B] = int32_t(total.pages);
+      }
+    }
+  }
+  __syncthreads();
+  // Page p of request b: in the table already, or the free list's (the blocks
+  // that need a new page's id read the list, not one another's table writes).
+  auto page_id = [&](int b, int p, int had) {
+    return p < had ? a.table[b * a.table_stride + p] : __ldg(a.free_pages + head + s_new[b] + (p - had));
+  };
+  const int64_t threads = int64_t(gridDim.x) * kTableThreads, gtid = int64_t(blockIdx.x) * kTableThreads + tid;
+  // Four consecutive entries a thread: one search for the first of them.
+  for (int64_t e0 = 4 * gtid; e0 < total.pages; e0 += 4 * threads) {
+    int b = find(s_kv, B, int(e0));
+    int had = pages_of(__ldg(a.kv_lens + b) - __ldg(a.qo_lens + b));
+    const int n = int(min(int64_t(4), total.pages - e0));
+    for (int u = 0; u < n; ++u) {
+      const int e = int(e0) + u;
+      if (e >= s_kv[b + 1]) {
+        do ++b;
+        while (e >= s_kv[b + 1]);
+        had = pages_of(__ldg(a.kv_lens + b) - __ldg(a.qo_lens + b));
+      }
+      const int p = e - s_kv[b];
+      const int32_t id = page_id(b, p, had);
+      a.kv_indices[e] = id;
+      if (p >= had) a.table[b * a.table_stride + p] = id;
+    }
+  }
+  for (int64_t t = gtid; t < a.max_tokens; t += threads) {
+    int32_t pos = 0, slot = -1;
+    if (t < total.qo) {
+      const int b = find(s_qo, B, int(t));
+      const int32_t old = __ldg(a.kv_lens + b) - __ldg(a.qo_lens + b);
+      pos = old + int32_t(t) - s_qo[b];
+      const int64_t at = int64_t(page_id(b, pos >> a.log2_page, pages_of(old))) * P + (pos & (P - 1));
+      slot = at >= 0 && at <= INT_MAX ? int32_t(at) : -1;
+    }
+    a.positions[t] = pos;
+    a.slots[t] = slot;
+  }
+}
+
+}  // namespace
+}  // namespace fi
+
+using namespace fi;
+
+extern "C" fi_status fi_build_step_tables(const int32_t* qo_lens, const int32_t* kv_lens, int32_t batch,
+                                          int32_t page_size, int32_t* block_table, int64_t block_table_stride,
+                                          int32_t block_table_width, const int32_t* free_pages, int32_t num_free,
+                                          const int32_t* free_head, int32_t* qo_indptr, int32_t* kv_indptr,
+                                          int32_t* last_page_len, int32_t* kv_indices, int32_t max_pages,
+                                          int32_t* positions, int32_t* slots, int32_t max_tokens, int32_t* counts,
+                                          void* stream) {
+  if (!qo_lens || !kv_lens || !block_table || !qo_indptr || !kv_indptr || !last_page_len || !counts || batch < 1 ||
+      block_table_width < 1 || block_table_stride < block_table_width || num_free < 0 || max_pages < 0 ||
+      max_tokens < 0)
+    return FI_ERR_INVALID_ARG;
+  if ((num_free > 0 && (!free_pages || !free_head)) || (max_pages > 0 && !kv_indices) ||
+      (max_tokens > 0 && (!positions || !slots)))
+    return FI_ERR_INVALID_ARG;
+  if (free_head && free_head >= counts && free_head < counts + FI_STEP_COUNTS) return FI_ERR_INVALID_ARG;
+  if (batch > FI_STEP_MAX_BATCH || page_size < 1 || page_size > 128 || (page_size & (page_size - 1)))
+    return FI_ERR_UNSUPPORTED;
+  const uintptr_t all = reinterpret_cast<uintptr_t>(qo_lens) | reinterpret_cast<uintptr_t>(kv_lens) |
+                        reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(free_pages) |
+                        reinterpret_cast<uintptr_t>(free_head) | reinterpret_cast<uintptr_t>(qo_indptr) |
+                        reinterpret_cast<uintptr_t>(kv_indptr) | reinterpret_cast<uintptr_t>(last_page_len) |
+                        reinterpret_cast<uintptr_t>(kv_indices) | reinterpret_cast<uintptr_t>(positions) |
+                        reinterpret_cast<uintptr_t>(slots) | reinterpret_cast<uintptr_t>(counts);
+  if (all & 3u) return FI_ERR_ALIGNMENT;
+  TableParams a{qo_lens,   kv_lens,   batch,         0,          block_table, block_table_stride, block_table_width,
+                free_pages, num_free, free_head,     qo_indptr,  kv_indptr,   last_page_len,      kv_indices,
+                max_pages, positions, slots,         max_tokens, counts};
+  while ((1 << a.log2_page) < page_size) ++a.log2_page;
+  const size_t smem = size_t(3) * (batch + 1) * 4;
+  if (smem > 48 * 1024) {
+    static bool configured[kMaxDevices] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return FI_ERR_CUDA;
+    if (dev < 0 || dev >= kMaxDevices || !configured[dev]) {
+      if (cudaFuncSetAttribute(step_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               3 * (FI_STEP_MAX_BATCH + 1) * 4) != cudaSuccess)
+        return FI_ERR_CUDA;
+      if (dev >= 0 && dev < kMaxDevices) configured[dev] = true;
+    }
+  }
+  // Enough blocks for four entries a thread, at most two per SM.
+  const int64_t work = (int64_t(max_pages) + 3) / 4 + max_tokens;
+  int64_t blocks = (work + kTableThreads - 1) / kTableThreads;
+  blocks = blocks < 1 ? 1 : blocks > 304 ? 304 : blocks;
+  step_tables_kernel<<<unsigned(blocks), kTableThreads, smem, static_cast<cudaStream_t>(stream)>>>(a);
+  return cudaGetLastError() == cudaSuccess ? FI_OK : FI_ERR_CUDA;
+}

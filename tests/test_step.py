@@ -1,0 +1,129 @@
+"""The step operators without a GPU: rotary rates against their definitions,
+and the calls that are refused before any CUDA work."""
+from __future__ import annotations
+
+import ctypes
+import os
+import re
+
+import numpy as np
+import pytest
+
+import serving_attention_gb300 as fi
+from oracle import step as oracle_step
+from serving_attention_gb300 import step
+
+TURN = 2.0 ** 64
+
+
+@pytest.mark.parametrize("rot_dim", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("theta", [10000.0, 500000.0])
+@pytest.mark.parametrize("scaling,factor", [("none", 1.0), ("linear", 4.0), ("ntk", 8.0), ("by_parts", 8.0),
+                                            ("yarn", 16.0), ("yarn", 1.0)])
+def test_rates(rot_dim, theta, scaling, factor):
+    rot = step.rotary_setup(256, rot_dim, theta=theta, scaling=scaling, factor=factor, original_positions=4096)
+    high = 32.0 if scaling == "yarn" else 4.0
+    f, amp = oracle_step.rates(rot_dim, theta, scaling, factor, 4096, 1.0, high)
+    got = np.array([float(rot.turns[i]) for i in range(rot_dim // 2)])
+    want = f / (2 * np.pi) * TURN
+    # pow and log in fp64 (a few steps of 2^-53), and rounding to a whole 2^-64 of a
+    # turn: 0.5 of some 4e7, 1e-8 turns a position, for the slowest pairs
+    assert (np.abs(got - want) <= 0.5 + 1e-12 * want).all()
+    assert abs(rot.amplitude - amp) < 1e-6 and all(rot.turns[i] == 0 for i in range(rot_dim // 2, 128))
+
+
+def test_closed_forms():
+    rot = step.rotary_setup(64)
+    assert abs(rot.turns[0] / TURN - 1 / (2 * np.pi)) < 1e-16
+    plain = [step.rotary_setup(64, scaling=s, factor=1.0, original_positions=4096).turns[:32]
+             for s in ("linear", "ntk", "by_parts", "yarn")]
+    # a factor of 1 changes nothing (the ramp adds one rounding)
+    assert all(abs(a - b) <= b * 2.0 ** -50 for p in plain for a, b in zip(p, rot.turns[:32]))
+    assert step.rotary_setup(64, scaling="yarn", factor=8.0, original_positions=4096, amplitude=2.0).amplitude == 2.0
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(head_dim=264), 2), (dict(head_dim=60), 2), (dict(head_dim=8), 2), (dict(rot_dim=24), 2),
+    (dict(rot_dim=144), 2), (dict(rot_dim=0), 2), (dict(theta=1.0), 1), (dict(theta=float("nan")), 1),
+    (dict(theta=float("inf")), 1), (dict(factor=0.5), 1), (dict(factor=float("inf")), 1), (dict(amplitude=-1.0), 1),
+    (dict(amplitude=float("inf")), 1), (dict(scaling="yarn"), 1), (dict(scaling="by_parts"), 1),
+    (dict(scaling="yarn", original_positions=64, low_turns=0.0), 1),
+    (dict(scaling="by_parts", original_positions=64, low_turns=4.0), 1)])
+def test_setup_refusals(kw, status):
+    with pytest.raises(fi.FIError) as e:
+        step.rotary_setup(**{"head_dim": 128, **kw})
+    assert e.value.status == status
+
+
+def test_setup_refuses_unknown_scaling():
+    with pytest.raises(ValueError):
+        step.rotary_setup(128, scaling="dynamic")
+    cfg = step.RotaryConfig(128, 128, 0, 9, 1e4, 1.0, 0, 1.0, 4.0, 0.0)
+    assert step.load().fi_rotary_setup(ctypes.byref(cfg), ctypes.byref(step.Rotary())) == 1
+    cfg = step.RotaryConfig(128, 128, 2, 0, 1e4, 1.0, 0, 1.0, 4.0, 0.0)
+    assert step.load().fi_rotary_setup(ctypes.byref(cfg), ctypes.byref(step.Rotary())) == 1
+
+
+def _apply(**kw):
+    rot = step.rotary_setup(128)
+    a = dict(rot=ctypes.byref(rot), pos=16, n=4, q=32, qt=1024, qh=128, qo=48, qot=1024, qoh=128, hq=8, k=64, kt=256,
+             kh=128, ko=80, kot=256, koh=128, hk=2, dt=fi.BF16, s=None)
+    a.update(kw)
+    return step.load().fi_rotary_apply(*a.values())
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(rot=None), 1), (dict(pos=None), 1), (dict(n=-1), 1), (dict(q=None), 1), (dict(qo=None), 1), (dict(k=None), 1),
+    (dict(hq=-1), 1), (dict(dt=fi.FP32), 2), (dict(q=34), 4), (dict(qo=40), 4), (dict(k=72), 4), (dict(qt=1020), 4),
+    (dict(koh=-128), 4), (dict(pos=18), 4), (dict(n=0), 0), (dict(hq=0, hk=0), 0)])
+def test_apply_refusals(kw, status):
+    assert _apply(**kw) == status
+
+
+def _append(**kw):
+    rot = step.rotary_setup(128)
+    ks = (ctypes.c_int64 * 3)(4096, 256, 128)
+    a = dict(rot=ctypes.byref(rot), pos=16, slots=16, n=4, q=32, qt=1024, qh=128, qo=48, qot=1024, qoh=128, hq=8, k=64,
+             kt=256, kh=128, v=96, vt=256, vh=128, vd=128, hk=2, kc=112, ks=ks, vc=128, vs=ks, page=16, pages=9,
+             dt=fi.FP16, s=None)
+    a.update(kw)
+    return step.load().fi_rotary_append(*a.values())
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(slots=None), 1), (dict(kc=None), 1), (dict(ks=None), 1), (dict(v=None), 1), (dict(vc=None), 1),
+    (dict(hk=0), 1), (dict(pages=0), 1), (dict(vd=520), 2), (dict(vd=12), 2), (dict(page=24), 2), (dict(page=256), 2),
+    (dict(dt=fi.FP32), 2), (dict(kc=120), 4), (dict(vc=136), 4), (dict(slots=18), 4),
+    (dict(vs=(ctypes.c_int64 * 3)(4096, 250, 128)), 4), (dict(n=0), 0)])
+def test_append_refusals(kw, status):
+    assert _append(**kw) == status
+
+
+def _tables(**kw):
+    a = dict(q=16, kv=32, batch=4, page=16, table=48, stride=8, width=8, free=64, num_free=9, head=80, qp=96, kp=112,
+             last=128, idx=144, max_pages=9, pos=160, slots=176, max_tokens=9, counts=192, s=None)
+    a.update(kw)
+    return step.load().fi_build_step_tables(*a.values())
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(q=None), 1), (dict(table=None), 1), (dict(counts=None), 1), (dict(batch=0), 1), (dict(width=0), 1),
+    (dict(stride=7), 1), (dict(free=None), 1), (dict(head=None), 1), (dict(num_free=-1), 1), (dict(idx=None), 1),
+    (dict(slots=None), 1), (dict(max_tokens=-1), 1), (dict(head=200), 1), (dict(batch=8193), 2), (dict(page=12), 2),
+    (dict(page=256), 2), (dict(pos=162), 4)])
+def test_tables_refusals(kw, status):
+    assert _tables(**kw) == status
+
+
+def test_every_entry_is_declared():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    text = open(os.path.join(root, "include", "fi_step.h")).read()
+    assert set(re.findall(r"^fi_status\s+(fi_\w+)\s*\(", text, re.M)) == set(step.EXPORTS)
+
+
+def test_oracle_tables_by_hand():
+    got = oracle_step.tables([2, 0, 3], [5, 0, 3], [[7, 9, -1], [-1, -1, -1], [-1, -1, -1]], 4, [20, 21, 22], 1, 9, 6)
+    # 3 old keys are one page (7): the fifth key opens page 21, the third request page 22
+    assert got["kv_indices"] == [7, 21, 22] and got["slots"] == [7 * 4 + 3, 21 * 4, 88, 89, 90, -1]
+    assert got["positions"] == [3, 4, 0, 1, 2, 0] and got["last_page_len"] == [1, 0, 3]
+    assert got["counts"] == [5, 3, 2, 3, 0, 0, 0, 0]
