@@ -6,32 +6,17 @@
 #include <cstring>
 
 #include "../../include/fi_diff.h"
-#include "diff_kernel.cuh"
-#include "launch.h"
+#include "diff_launch.h"
 
 namespace fi {
+
+bool make_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, int rank, const uint64_t* dims,
+              const int64_t* strides_elems, const uint32_t* box, CUtensorMapSwizzle swizzle);  // attention.cu
+
 namespace {
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool stride_ok(int64_t elems) { return elems > 0 && (elems * 2) % 16 == 0; }
-
-// The run, then the merge of split units behind it.
-template <typename T>
-cudaError_t launch_diff(const DiffParams& dp, int num_ctas, cudaStream_t stream) {
-  static bool configured[kMaxDevices] = {};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= kMaxDevices || !configured[dev]) {
-    e = cudaFuncSetAttribute(diff_attention_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             int(kDiffSmemBytes));
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < kMaxDevices) configured[dev] = true;
-  }
-  diff_attention_kernel<T><<<num_ctas, kThreads, kDiffSmemBytes, stream>>>(dp);
-  e = cudaGetLastError();
-  return e == cudaSuccess ? launch_behind_run(diff_merge_kernel<T>, 4 * num_ctas, 256, stream, dp) : e;
-}
 
 }  // namespace
 }  // namespace fi
@@ -99,8 +84,31 @@ extern "C" fi_status fi_batch_paged_attention_run_differential(
     dp.k_strides[i] = k_strides[i];
     dp.v_strides[i] = v_strides[i];
   }
+  if (P >= kMinTmaPage) {
+    const CUtensorMapDataType tt =
+        dtype == FI_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const uint64_t kd[4] = {uint64_t(kHeadDim), uint64_t(info->num_kv_heads), uint64_t(P), uint64_t(num_pages)};
+    const int64_t ks[3] = {k_strides[2], k_strides[1], k_strides[0]};  // head, slot, page
+    const int64_t vs[3] = {v_strides[2], v_strides[1], v_strides[0]};
+    const uint32_t kb[4] = {64u, 1u, uint32_t(P), 1u};
+    if (!make_map(&kc.tm_k, tt, k_cache, 4, kd, ks, kb, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_map(&kc.tm_v, tt, v_cache, 4, kd, vs, kb, CU_TENSOR_MAP_SWIZZLE_128B))
+      return FI_ERR_UNSUPPORTED;
+    kc.tc = kTileM % p.group == 0 ? 1 : 0;
+    if (kc.tc) {
+      const uint64_t qd[3] = {uint64_t(kHeadDim), uint64_t(info->num_qo_heads), uint64_t(q_num_tokens)};
+      const int64_t qs[2] = {q_stride_head, q_stride_tok}, os[2] = {o_stride_head, o_stride_tok};
+      const uint32_t qb[3] = {64u, uint32_t(p.group), uint32_t(kTileM / p.group)};
+      if (!make_map(&p.tm_q, tt, q, 3, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B) ||
+          !make_map(&p.tm_o, tt, o, 3, qd, os, qb, CU_TENSOR_MAP_SWIZZLE_128B))
+        return FI_ERR_UNSUPPORTED;
+    }
+  }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = dtype == FI_BF16 ? launch_diff<__nv_bfloat16>(dp, info->num_ctas, s)
-                                         : launch_diff<__half>(dp, info->num_ctas, s);
+  const bool mask = (info->variant & 2) != 0;
+  const cudaError_t e = dtype == FI_BF16 ? (mask ? launch_diff<__nv_bfloat16, true>(dp, info->num_ctas, s)
+                                                 : launch_diff<__nv_bfloat16, false>(dp, info->num_ctas, s))
+                                         : (mask ? launch_diff<__half, true>(dp, info->num_ctas, s)
+                                                 : launch_diff<__half, false>(dp, info->num_ctas, s));
   return e == cudaSuccess ? FI_OK : FI_ERR_CUDA;
 }

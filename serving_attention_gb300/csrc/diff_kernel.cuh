@@ -21,18 +21,10 @@
 //    warps 4..7 map 2 of the same tokens.
 #pragma once
 #include "attention_kernel.cuh"
+#include "diff_params.h"
+#include "diff_prefill.cuh"
 
 namespace fi {
-
-struct DiffParams {
-  RunParams run;
-  const float* lambda;  // [num_qo_heads]
-  const float* norm_w;  // [128] or null: no norm
-  float norm_eps, out_scale;
-  const uint16_t* k;    // the cache, read through its page table
-  const uint16_t* v;
-  int64_t k_strides[3], v_strides[3];  // page, slot, head (elements)
-};
 
 // Stages hold 128 tokens as two 64-dim halves of 128-byte rows, 16-byte
 // chunks XOR-ed with the row (the layout of the 128-byte TMA swizzle), so
@@ -42,12 +34,20 @@ struct DiffBufs {
   uint16_t v[kStages][2][kStageTokens][64];
   float comb[kConsumerWarps][16][64];  // one half (64 dims) of the warps' O rows at a time
 };
-static_assert(sizeof(DiffBufs) <= sizeof(DecodeBufs), "the decode buffers are laid over the run kernel's");
 
 struct alignas(1024) DiffSmem {
-  RunSmem run;
-  float2 comb_ml[kConsumerWarps][16];  // (running max, sum) of the warps' rows
-  __device__ __forceinline__ DiffBufs& bufs() { return *reinterpret_cast<DiffBufs*>(&run); }
+  union {
+    DiffBufs dec;
+    DiffPrefillBufs pf;
+  };
+  union {
+    float stats[4][kTileM];              // tensor-core phase: a row's normalisers (per map), sums of squares (per half)
+    float2 comb_ml[kConsumerWarps][16];  // (running max, sum) of the warps' rows
+  };
+  uint64_t full[kStages], empty[kStages];
+  DiffPrefillBars bars;
+  uint32_t tmem_base;
+  volatile int abort;  // set by the role whose bounded wait ran out
 };
 constexpr size_t kDiffSmemBytes = sizeof(DiffSmem);
 static_assert(kDiffSmemBytes <= 227 * 1024, "shared memory of the differential kernel exceeds one CTA's limit");
@@ -116,7 +116,7 @@ static __device__ void diff_produce(const DiffParams& dp, DiffSmem& sm, int32_t 
                                     int32_t off_items) {
   const RunParams& p = dp.run;
   const KvCache& kc = p.kv[0];
-  DiffBufs& bufs = sm.bufs();
+  DiffBufs& bufs = sm.dec;
   const int lane = threadIdx.x & 31, pw = threadIdx.x >> 5;
   const int c16 = lane & 15, hw = lane >> 4;
   const int lp = kc.log2_page, P = kc.page_size;
@@ -137,7 +137,7 @@ static __device__ void diff_produce(const DiffParams& dp, DiffSmem& sm, int32_t 
         const int s = it % kStages;
         const int32_t cur = next;
         if (st + 1 < nst) next = token_page(st + 1);
-        if (!warp_wait(&sm.run.empty[s], ((it / kStages) & 1) ^ 1, &sm.run.abort)) continue;
+        if (!warp_wait(&sm.empty[s], ((it / kStages) & 1) ^ 1, &sm.abort)) continue;
         const int tok0 = item.kv0 + st * kStageTokens + 32 * pw;
 #pragma unroll 8
         for (int r = 0; r < 16; ++r) {
@@ -153,11 +153,72 @@ static __device__ void diff_produce(const DiffParams& dp, DiffSmem& sm, int32_t 
           cp_async_16(&bufs.k[s][c16 >> 3][row][at], ks, ok ? 16u : 0u);
           cp_async_16(&bufs.v[s][c16 >> 3][row][at], vs, ok ? 16u : 0u);
         }
-        cp_async_mbar_arrive_noinc(&sm.run.full[s]);
+        cp_async_mbar_arrive_noinc(&sm.full[s]);
       }
     }
   }
   cp_async_wait_all();
+}
+
+// Pages of 8 tokens and more: warp 0 brings a stage with one 128-byte swizzled
+// TMA box (64 dims, 1 head, P slots, 1 page) per page, half and tensor -- the
+// boxes of the tensor-core path, in the layout that the copies above write by
+// hand.  Lane l issues pages l, l + 32, ...; the next stage's page ids are
+// loaded one stage ahead; pages past the chunk are addressed out of bounds and
+// arrive as zeros.
+static __device__ void diff_produce_tma(const DiffParams& dp, DiffSmem& sm, int32_t item_begin, int32_t item_end,
+                                        int32_t off_items) {
+  const RunParams& p = dp.run;
+  const KvCache& kc = p.kv[0];
+  DiffBufs& bufs = sm.dec;
+  const int lane = threadIdx.x & 31;
+  const int lp = kc.log2_page, P = kc.page_size, boxes = kStageTokens >> lp;  // 1 to 16
+  if (lane == 0) {
+    tc::prefetch_tensormap(&kc.tm_k);
+    tc::prefetch_tensormap(&kc.tm_v);
+  }
+  uint32_t it = 0;
+  int armed[kStages];
+#pragma unroll
+  for (int s = 0; s < kStages; ++s) armed[s] = -1;
+  for (int32_t i = item_begin; i < item_end; ++i) {
+    const Item item = load_item(p.iws, off_items, i);
+    const int nst = (item.kv1 - item.kv0 + kStageTokens - 1) >> kLog2StageTokens;
+    const int npages = (item.kv1 + P - 1) >> lp;  // of the request, up to the chunk's end
+    const int32_t* pages = kc.kv_indices + item.rq.page_start;
+    auto page_of = [&](int st) -> int32_t {
+      const int pg = ((item.kv0 + st * kStageTokens) >> lp) + lane;
+      return lane < boxes && pg < npages ? __ldg(pages + pg) : kc.num_pages;
+    };
+    const int passes = diff_passes(item.row1 - item.row0);
+    for (int pass = 0; pass < passes; ++pass) {
+      int32_t next = page_of(0);
+      for (int st = 0; st < nst; ++st, ++it) {
+        const int s = it % kStages;
+        const uint32_t ph = (it / kStages) & 1;
+        const int32_t cur = next;
+        if (st + 1 < nst) next = page_of(st + 1);
+        if (!warp_wait(&sm.empty[s], ph ^ 1, &sm.abort)) continue;
+        if (lane == 0) mbar_arrive_expect_tx(&sm.full[s], 2u * kStageTokens * kHeadDim * 2u);
+        __syncwarp();
+        if (lane < boxes) {
+          const int row = lane << lp;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            tc::tma_load_4d(&bufs.k[s][h][row][0], &kc.tm_k, &sm.full[s], 64 * h, item.hk, 0, cur);
+            tc::tma_load_4d(&bufs.v[s][h][row][0], &kc.tm_v, &sm.full[s], 64 * h, item.hk, 0, cur);
+          }
+        }
+        armed[s] = ph;
+      }
+    }
+  }
+  // Every load this warp armed has landed before the CTA leaves.
+  if (lane == 0) {
+    for (int s = 0; s < kStages; ++s)
+      if (armed[s] >= 0) mbar_wait_drain(&sm.full[s], armed[s]);
+  }
+  __syncwarp();
 }
 
 // ---------------------------------------------------------------- consumers
@@ -314,7 +375,7 @@ template <typename T, bool kWide>
 __device__ __forceinline__ uint32_t diff_pass(const DiffParams& dp, DiffSmem& sm, const Item& item, int prow0,
                                               int prows, uint32_t it, int causal, const Variant& var) {
   const RunParams& p = dp.run;
-  DiffBufs& bufs = sm.bufs();
+  DiffBufs& bufs = sm.dec;
   const int cw = (threadIdx.x >> 5) - kFirstConsumerWarp;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int G = p.group;
@@ -358,7 +419,7 @@ __device__ __forceinline__ uint32_t diff_pass(const DiffParams& dp, DiffSmem& sm
   for (int st = 0; st < nst; ++st, ++it) {
     const int s = it % kStages;
     const int j0 = item.kv0 + st * kStageTokens;
-    if (warp_wait(&sm.run.full[s], (it / kStages) & 1, &sm.run.abort)) {
+    if (warp_wait(&sm.full[s], (it / kStages) & 1, &sm.abort)) {
       const uint16_t *ks = &bufs.k[s][0][0][0], *vs = &bufs.v[s][0][0][0];
 #pragma unroll 1
       for (int sl = 0; sl < (kWide ? 2 : 1); ++sl) {
@@ -368,7 +429,7 @@ __device__ __forceinline__ uint32_t diff_pass(const DiffParams& dp, DiffSmem& sm
       }
     }
     __syncwarp();
-    if (lane == 0) mbar_arrive(&sm.run.empty[s]);
+    if (lane == 0) mbar_arrive(&sm.empty[s]);
   }
 
   // Merge of the warps' states, 64 dims at a time through shared memory.
@@ -423,7 +484,7 @@ __device__ __forceinline__ uint32_t diff_pass(const DiffParams& dp, DiffSmem& sm
     }
     named_barrier_sync(1, 32 * kConsumerWarps);
   }
-  if (!sm.run.abort) {
+  if (!sm.abort) {
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
       const int pr = cw + 8 * k;
@@ -470,7 +531,7 @@ __device__ void diff_consume(const DiffParams& dp, DiffSmem& sm, int32_t item_be
 
 // ---------------------------------------------------------------- kernel
 
-template <typename T>
+template <typename T, bool kMask>
 __global__ void __launch_bounds__(kThreads, 1) diff_attention_kernel(const __grid_constant__ DiffParams dp) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   DiffSmem& sm = *reinterpret_cast<DiffSmem*>(smem_raw);
@@ -504,21 +565,79 @@ __global__ void __launch_bounds__(kThreads, 1) diff_attention_kernel(const __gri
   var.cap_a = var.cap_b = 0.f;
   var.rope_table = nullptr;
   const int warp = threadIdx.x >> 5;
+  const int32_t mid = first_cuda_core_item(p, begin, end, off_items, 0, 0);
+  const bool tc_phase = mid > begin;
+  const bool boxes = p.kv[0].page_size >= kMinTmaPage;
+  DiffPrefillBars& bar = sm.bars;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&sm.run.full[s], 32 * kFirstConsumerWarp);  // every copying thread
-      mbar_init(&sm.run.empty[s], kConsumerWarps);
+      mbar_init(&sm.full[s], boxes ? 1 : 32 * kFirstConsumerWarp);  // the producer, or every copying thread
+      mbar_init(&sm.empty[s], kConsumerWarps);
     }
-    sm.run.abort = 0;
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bar.q_full[s], 1);
+      mbar_init(&bar.q_empty[s], 1);
+      mbar_init(&bar.k_full[s], 1);
+      mbar_init(&bar.k_empty[s], 1);
+      mbar_init(&bar.v_full[s], 1);
+      mbar_init(&bar.v_empty[s], 1);
+      mbar_init(&bar.v_clear[s], 1);
+      mbar_init(&bar.o_ready[s], 1);
+      mbar_init(&bar.o_free[s], 8);  // every softmax warp reads both maps' O
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&bar.s_full[s][b], 1);
+        mbar_init(&bar.pv_done[s][b], 1);
+        mbar_init(&bar.p_full[s][b], 4);
+      }
+    }
+    mbar_init(&bar.drain, 1);
+    sm.abort = 0;
     fence_mbar_init();
   }
+  if (tc_phase && warp == kMmaWarp) {
+    tc::tmem_alloc(&sm.tmem_base, kTmemCols);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
   __syncthreads();
-  if (warp < kFirstConsumerWarp)
-    diff_produce(dp, sm, begin, end, off_items);
-  else
-    diff_consume<T>(dp, sm, begin, end, off_items, causal, var);
+  tc::fence_after_sync();
+  if (tc_phase) {  // register budgets of the run kernel (see kRegsLaunch)
+    if (warp < kSoftmaxWarp0) {
+      tc::setmaxnreg_dec<kRegsLoader>();
+      if (warp == 0) {
+        diff_pf_produce<false>(p, sm.pf, bar, &sm.abort, begin, mid, off_items);
+      } else if (warp == kMmaWarp) {
+        diff_pf_mma<T>(p, sm.pf, bar, &sm.abort, sm.tmem_base, begin, mid, off_items);
+        __syncwarp();
+      } else if (warp == kVWarp) {
+        diff_pf_produce<true>(p, sm.pf, bar, &sm.abort, begin, mid, off_items);
+      }
+      tc::fence_before_sync();
+      named_barrier_sync_unaligned(kPhaseBarrier, kThreads);
+      tc::fence_after_sync();
+      tc::setmaxnreg_inc<kRegsLaunch>();
+    } else {
+      tc::setmaxnreg_inc<kRegsSoftmax>();
+      diff_pf_softmax<T, kMask>(dp, sm.pf, bar, sm.stats, &sm.abort, sm.tmem_base, begin, mid, off_items, causal, var);
+      tc::setmaxnreg_dec<kRegsLaunch>();
+      tc::fence_before_sync();
+      named_barrier_sync_unaligned(kPhaseBarrier, kThreads);
+      tc::fence_after_sync();
+    }
+  }
+  if (warp >= kFirstConsumerWarp)
+    diff_consume<T>(dp, sm, mid, end, off_items, causal, var);
+  else if (!boxes)
+    diff_produce(dp, sm, mid, end, off_items);
+  else if (warp == 0)
+    diff_produce_tma(dp, sm, mid, end, off_items);
+  tc::fence_before_sync();
   __syncthreads();
-  if (threadIdx.x == 0 && sm.run.abort) atomicOr(p.iws + FI_H_STATUS, sm.run.abort);
+  if (tc_phase && warp == kMmaWarp) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(sm.tmem_base, kTmemCols);
+  }
+  if (threadIdx.x == 0 && sm.abort) atomicOr(p.iws + FI_H_STATUS, sm.abort);
 }
 
 // Merge of split units, launched behind the run: one warp per packed row, its
