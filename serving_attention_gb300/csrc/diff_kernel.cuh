@@ -40,10 +40,7 @@ struct alignas(1024) DiffSmem {
     DiffBufs dec;
     DiffPrefillBufs pf;
   };
-  union {
-    float stats[4][kTileM];              // tensor-core phase: a row's normalisers (per map), sums of squares (per half)
-    float2 comb_ml[kConsumerWarps][16];  // (running max, sum) of the warps' rows
-  };
+  float2 comb_ml[kConsumerWarps][16];  // (running max, sum) of the warps' rows
   uint64_t full[kStages], empty[kStages];
   DiffPrefillBars bars;
   uint32_t tmem_base;
@@ -355,7 +352,7 @@ __device__ __forceinline__ void diff_store_row(const DiffParams& dp, const float
   float f[4] = {dp.out_scale, dp.out_scale, dp.out_scale, dp.out_scale};
   if (dp.norm_w) {
     const float ss = warp_sum(y[0] * y[0] + y[1] * y[1] + y[2] * y[2] + y[3] * y[3]);
-    const float r = rsqrtf(ss * (1.f / kHeadDim) + dp.norm_eps) * dp.out_scale;
+    const float r = rms_factor(ss, dp.norm_eps) * dp.out_scale;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       f[2 * h] = r * __ldg(dp.norm_w + 64 * h + 2 * lane);
@@ -576,20 +573,20 @@ __global__ void __launch_bounds__(kThreads, 1) diff_attention_kernel(const __gri
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bar.q_full[s], 1);
-      mbar_init(&bar.q_empty[s], 1);
+      mbar_init(&bar.q_empty[s], 2);  // one thread of each softmax warpgroup
       mbar_init(&bar.k_full[s], 1);
       mbar_init(&bar.k_empty[s], 1);
       mbar_init(&bar.v_full[s], 1);
       mbar_init(&bar.v_empty[s], 1);
       mbar_init(&bar.v_clear[s], 1);
-      mbar_init(&bar.o_ready[s], 1);
-      mbar_init(&bar.o_free[s], 8);  // every softmax warp reads both maps' O
-      for (int b = 0; b < 2; ++b) {
-        mbar_init(&bar.s_full[s][b], 1);
-        mbar_init(&bar.pv_done[s][b], 1);
-        mbar_init(&bar.p_full[s][b], 4);
-      }
+      mbar_init(&bar.s_full[s], 1);
+      mbar_init(&bar.s_free[s], 8);  // every softmax warp
+      mbar_init(&bar.p_full[s][0], 4);
+      mbar_init(&bar.p_full[s][1], 4);
+      mbar_init(&bar.p_free[s], 1);
     }
+    mbar_init(&bar.o_ready, 1);
+    mbar_init(&bar.o_free, 8);
     mbar_init(&bar.drain, 1);
     sm.abort = 0;
     fence_mbar_init();
@@ -618,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1) diff_attention_kernel(const __gri
       tc::setmaxnreg_inc<kRegsLaunch>();
     } else {
       tc::setmaxnreg_inc<kRegsSoftmax>();
-      diff_pf_softmax<T, kMask>(dp, sm.pf, bar, sm.stats, &sm.abort, sm.tmem_base, begin, mid, off_items, causal, var);
+      diff_pf_softmax<T, kMask>(dp, sm.pf, bar, &sm.abort, sm.tmem_base, begin, mid, off_items, causal, var);
       tc::setmaxnreg_dec<kRegsLaunch>();
       tc::fence_before_sync();
       named_barrier_sync_unaligned(kPhaseBarrier, kThreads);

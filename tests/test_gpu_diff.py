@@ -44,15 +44,15 @@ def _batch(seed, qo, kv, hq, hkv, page, dtype, causal=0, poison=True):
     return b, lam, w
 
 
-def _run(b, lam, w, cfg, out_scale=1.0, stream=None, ws=None, lse=True):
+def _run(b, lam, w, cfg, out_scale=1.0, stream=None, ws=None, lse=True, eps=1e-5):
     ws = ws or fi.Workspace(cfg, device=DEV)
     info = fi.plan(ws, b.qo_indptr, b.kv_indptr, b.kv_indices, b.last_page_len, b.num_qo_heads, b.num_kv_heads, 128,
                    b.page_size, b.causal, b.num_pages, stream=stream)
     kvi = torch.as_tensor(b.kv_indices if b.kv_indices.size else np.zeros(1, np.int32), device=DEV)
     o = torch.full_like(b.q, float("nan"))
     l = torch.full((*b.q.shape[:2], 2), float("nan"), device=DEV) if lse else None
-    differential.run(ws, info, b.q, b.k, b.v, kvi, lam, o, l, b.sm_scale, norm_weight=w, out_scale=out_scale,
-                     stream=stream)
+    differential.run(ws, info, b.q, b.k, b.v, kvi, lam, o, l, b.sm_scale, norm_weight=w, norm_eps=eps,
+                     out_scale=out_scale, stream=stream)
     return o, l, info, ws, kvi
 
 
@@ -115,6 +115,25 @@ def test_rows_without_keys():
     b, lam, w = _batch(5, [40, 3, 1, 20], [10, 0, 0, 1], 8, 2, 16, "bf16", causal=1)
     o, lse, info, ws, _ = _run(b, lam, w, _config())
     _check(b, lam, w, o, lse, rounded=True)
+
+
+def test_rows_without_keys_and_no_eps():
+    """The norm of a zero row with eps 0 is zero, not 0 / 0."""
+    b, lam, w = _batch(5, [40, 3, 1, 20], [10, 0, 0, 1], 8, 2, 16, "bf16", causal=1)
+    o, lse, *_ = _run(b, lam, w, _config(), eps=0.0)
+    empty = torch.isneginf(lse[:b.total_qo]).all(-1)
+    assert empty.any() and (o[:b.total_qo][empty] == 0).all() and torch.isfinite(o[:b.total_qo]).all()
+
+
+@pytest.mark.parametrize("lam_value", [0.0, 1.0, -1.5, 40.0])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_lambdas(lam_value, dtype):
+    b, lam, w = _batch(6, [1, 70, 130], [500, 300, 2000], 8, 2, 16, dtype, causal=1)
+    lam = torch.full_like(lam, lam_value)
+    for kw in ({}, dict(prefill_min_chunk=128, decode_min_chunk=64, split_factor=16)):
+        o, lse, info, ws, _ = _run(b, lam, None, _config(**kw), 0.5)
+        assert fi.device_status(ws) == 0
+        _check(b, lam, None, o, lse, 0.5, rounded=True)
 
 
 @pytest.mark.parametrize("split", [False, True])
