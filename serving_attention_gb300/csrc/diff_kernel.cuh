@@ -529,7 +529,7 @@ __device__ void diff_consume(const DiffParams& dp, DiffSmem& sm, int32_t item_be
 // ---------------------------------------------------------------- kernel
 
 template <typename T, bool kMask>
-__global__ void __launch_bounds__(kThreads, 1) diff_attention_kernel(const __grid_constant__ DiffParams dp) {
+__global__ void __launch_bounds__(kDiffThreads, 1) diff_attention_kernel(const __grid_constant__ DiffParams dp) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   DiffSmem& sm = *reinterpret_cast<DiffSmem*>(smem_raw);
   const RunParams& p = dp.run;
@@ -573,20 +573,20 @@ __global__ void __launch_bounds__(kThreads, 1) diff_attention_kernel(const __gri
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bar.q_full[s], 1);
-      mbar_init(&bar.q_empty[s], 2);  // one thread of each softmax warpgroup
+      mbar_init(&bar.q_empty[s], 2);  // one thread of each pair of softmax warpgroups
       mbar_init(&bar.k_full[s], 1);
       mbar_init(&bar.k_empty[s], 1);
       mbar_init(&bar.v_full[s], 1);
       mbar_init(&bar.v_empty[s], 1);
       mbar_init(&bar.v_clear[s], 1);
       mbar_init(&bar.s_full[s], 1);
-      mbar_init(&bar.s_free[s], 8);  // every softmax warp
-      mbar_init(&bar.p_full[s][0], 4);
-      mbar_init(&bar.p_full[s][1], 4);
+      mbar_init(&bar.s_free[s], 4 * kDiffGroups);  // every softmax warp
+      mbar_init(&bar.p_full[s][0], 2 * kDiffGroups);
+      mbar_init(&bar.p_full[s][1], 2 * kDiffGroups);
       mbar_init(&bar.p_free[s], 1);
     }
     mbar_init(&bar.o_ready, 1);
-    mbar_init(&bar.o_free, 8);
+    mbar_init(&bar.o_free, 4 * kDiffGroups);
     mbar_init(&bar.drain, 1);
     sm.abort = 0;
     fence_mbar_init();
@@ -598,9 +598,11 @@ __global__ void __launch_bounds__(kThreads, 1) diff_attention_kernel(const __gri
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  if (tc_phase) {  // register budgets of the run kernel (see kRegsLaunch)
+  // Each branch returns to the launch's registers before the code paths meet
+  // (an increase waits for the other warpgroups' release).
+  if (tc_phase) {
     if (warp < kSoftmaxWarp0) {
-      tc::setmaxnreg_dec<kRegsLoader>();
+      tc::setmaxnreg_dec<kDiffRegsLoader>();
       if (warp == 0) {
         diff_pf_produce<false>(p, sm.pf, bar, &sm.abort, begin, mid, off_items);
       } else if (warp == kMmaWarp) {
@@ -610,24 +612,32 @@ __global__ void __launch_bounds__(kThreads, 1) diff_attention_kernel(const __gri
         diff_pf_produce<true>(p, sm.pf, bar, &sm.abort, begin, mid, off_items);
       }
       tc::fence_before_sync();
-      named_barrier_sync_unaligned(kPhaseBarrier, kThreads);
+      named_barrier_sync_unaligned(kPhaseBarrier, kDiffThreads);
       tc::fence_after_sync();
-      tc::setmaxnreg_inc<kRegsLaunch>();
+      tc::setmaxnreg_inc<kDiffRegsLaunch>();
     } else {
-      tc::setmaxnreg_inc<kRegsSoftmax>();
+      tc::setmaxnreg_inc<kDiffRegsSoftmax>();
       diff_pf_softmax<T, kMask>(dp, sm.pf, bar, &sm.abort, sm.tmem_base, begin, mid, off_items, causal, var);
-      tc::setmaxnreg_dec<kRegsLaunch>();
+      tc::setmaxnreg_dec<kDiffRegsLaunch>();
       tc::fence_before_sync();
-      named_barrier_sync_unaligned(kPhaseBarrier, kThreads);
+      named_barrier_sync_unaligned(kPhaseBarrier, kDiffThreads);
       tc::fence_after_sync();
     }
   }
-  if (warp >= kFirstConsumerWarp)
-    diff_consume<T>(dp, sm, mid, end, off_items, causal, var);
-  else if (!boxes)
-    diff_produce(dp, sm, mid, end, off_items);
-  else if (warp == 0)
-    diff_produce_tma(dp, sm, mid, end, off_items);
+  if (mid < end) {
+    if (warp >= kFirstConsumerWarp && warp < kFirstConsumerWarp + kConsumerWarps) {
+      tc::setmaxnreg_inc<kDiffRegsConsumer>();
+      diff_consume<T>(dp, sm, mid, end, off_items, causal, var);
+    } else {
+      tc::setmaxnreg_dec<kDiffRegsOther>();
+      if (warp < kFirstConsumerWarp) {
+        if (!boxes)
+          diff_produce(dp, sm, mid, end, off_items);
+        else if (warp == 0)
+          diff_produce_tma(dp, sm, mid, end, off_items);
+      }
+    }
+  }
   tc::fence_before_sync();
   __syncthreads();
   if (tc_phase && warp == kMmaWarp) {

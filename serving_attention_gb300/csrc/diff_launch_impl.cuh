@@ -14,16 +14,16 @@ cudaError_t launch_diff(const DiffParams& dp, int num_ctas, cudaStream_t stream)
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices || !configured[dev]) {
-    // the tensor-core phase moves registers between warpgroups (see launch_run)
+    // both phases move registers between warpgroups (see launch_run)
     cudaFuncAttributes fa{};
     e = cudaFuncGetAttributes(&fa, kern);
     if (e != cudaSuccess) return e;
-    if (fa.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
+    if (fa.numRegs < kDiffRegsLaunch) return cudaErrorInvalidConfiguration;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kDiffSmemBytes));
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < kMaxDevices) configured[dev] = true;
   }
-  kern<<<num_ctas, kThreads, kDiffSmemBytes, stream>>>(dp);
+  kern<<<num_ctas, kDiffThreads, kDiffSmemBytes, stream>>>(dp);
   e = cudaGetLastError();
   return e == cudaSuccess ? launch_behind_run(diff_merge_kernel<T>, 4 * num_ctas, 256, stream, dp) : e;
 }

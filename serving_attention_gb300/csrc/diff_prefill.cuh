@@ -21,34 +21,48 @@
 // terms, hi + lo, as the merge takes the difference.
 //
 // Roles: warp 0 loads Q (two buffers) and K, warp 2 V, by TMA; warp 1 issues
-// the products; warps 4..7 take keys 0..63 of every 128-key tile for both
-// maps, warps 8..11 keys 64..127 (thread = row = tensor-memory lane).  Tensor
-// memory: S of both maps (128 columns each), O (128), two P buffers (64 each).
-// A thread takes its 128 logits into registers and gives S back, so the next
-// tile's S runs while it computes; P has columns of its own, so nothing waits
-// for P V either.
+// the products; warpgroups of warps 4..7, 8..11, 12..15 and 16..19 take 32
+// keys each of every 128-key tile, for both maps (thread = row =
+// tensor-memory lane).  Tensor memory: S of both maps (128 columns each), O
+// (128), two P buffers (64 each).  A thread takes its 64 logits into registers
+// and gives S back, so the next tile's S runs while it computes; P has columns
+// of its own, so nothing waits for P V either.  Four softmax warps on each
+// scheduler: with two (64 keys each) a warp's waits, loads and stores were
+// not covered, and a step took twice its 1024 cycles of exponentials.
 #pragma once
 #include "attention_kernel.cuh"
 #include "diff_params.h"
 
 namespace fi {
 
-constexpr int kDiffBarrier = 6;  // both softmax warpgroups (1: decode, 3: end of phase, 4 and 5: one warpgroup)
+constexpr int kDiffThreads = 640;
+constexpr int kDiffGroups = 4;                         // softmax warpgroups
+constexpr int kDiffKeys = kTileN / kDiffGroups;        // keys of a tile, and dims of the output, of each
+constexpr int kDiffSoftmaxThreads = 128 * kDiffGroups;
+constexpr int kDiffBarrier = 6;  // all softmax warpgroups (1: decode, 3: end of phase, 4 and 5: two warpgroups)
 constexpr int kDiffTmemO = 256, kDiffTmemP = 384;
+// Register budgets, per thread (see kRegsLaunch): in the tensor-core phase
+// warps 0..3 and the softmax warpgroups, in the decode phase its consumers
+// (two warpgroups) and the other twelve warps.
+constexpr int kDiffRegsLaunch = 96;
+constexpr int kDiffRegsLoader = 64, kDiffRegsSoftmax = 104;
+constexpr int kDiffRegsOther = 48, kDiffRegsConsumer = 168;
+static_assert(kDiffRegsLoader * 128 + kDiffRegsSoftmax * 512 <= kDiffRegsLaunch * kDiffThreads, "exceeds the launch");
+static_assert(kDiffRegsOther * 384 + kDiffRegsConsumer * 256 <= kDiffRegsLaunch * kDiffThreads, "exceeds the launch");
 
 struct DiffPrefillBufs {  // every [128][64] block is a 128-byte swizzled operand half (see PrefillBufs)
   uint16_t q[2][2][kTileM][64];  // [buffer][d half = map][row][dim]; an item's output leaves through its Q buffer
   uint16_t k[2][2][kTileN][64];  // [stage][d half][token][dim]
   uint16_t v[2][2][kTileN][64];
-  float stats[2][4][kTileM];     // [warpgroup][max 1, sum 1, max 2, sum 2][row] over its keys
-  float sq[2][kTileM];           // [dim half][row] sum of squares
+  float stats[kDiffGroups][4][kTileM];  // [warpgroup][max 1, sum 1, max 2, sum 2][row] over its keys
+  float sq[kDiffGroups][kTileM];        // [dim quarter][row] sum of squares
 };
 
 struct DiffPrefillBars {
   uint64_t q_full[2], q_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t v_clear[2];            // a tile's V rows past the request's end cleared
   uint64_t s_full[2], s_free[2];  // [map]
-  uint64_t p_full[2][2];          // [buffer][warpgroup]
+  uint64_t p_full[2][2];          // [buffer][key half]
   uint64_t p_free[2];
   uint64_t o_ready, o_free, drain;
 };
@@ -170,7 +184,7 @@ __device__ void diff_pf_mma(const RunParams& p, DiffPrefillBufs& pf, DiffPrefill
     const uint32_t vp = pv.tail ? (cleared >> st) & 1 : (vt >> 1) & 1;
     const uint64_t bv = dv + 2048u * st;
 #pragma unroll
-    for (int wg = 0; wg < 2; ++wg) {  // the keys of one warpgroup
+    for (int wg = 0; wg < 2; ++wg) {  // the keys of two warpgroups
       uint64_t* const pb = &bar.p_full[b][wg];
       const uint32_t pp = np[b] & 1;
       const bool first = wg == 0;
@@ -255,22 +269,18 @@ __device__ __forceinline__ float rms_factor(float sum_sq, float eps) {
   return ms > 0.f ? rsqrtf(ms) : 0.f;
 }
 
-// Largest of a thread's 64 logits: eight chains of three-input maxima.
-__device__ __forceinline__ float max64(const uint32_t (&v)[2][32]) {
-  auto val = [&](int e) { return __uint_as_float(v[e >> 5][e & 31]); };
+// Largest of a thread's 32 logits: eight chains of three-input maxima.
+__device__ __forceinline__ float max32(const uint32_t (&v)[32]) {
+  auto val = [&](int e) { return __uint_as_float(v[e]); };
   float mx[8];
 #pragma unroll
   for (int a = 0; a < 8; ++a) mx[a] = max3(val(a), val(8 + a), val(16 + a));
 #pragma unroll
-  for (int e = 24; e < 56; e += 16)
-#pragma unroll
-    for (int a = 0; a < 8; ++a) mx[a] = max3(mx[a], val(e + a), val(e + 8 + a));
-#pragma unroll
-  for (int a = 0; a < 8; ++a) mx[a] = fmaxf(mx[a], val(56 + a));
+  for (int a = 0; a < 8; ++a) mx[a] = fmaxf(mx[a], val(24 + a));
   return max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
 }
 
-// The two softmax warpgroups and the end of the items.
+// The softmax warpgroups and the end of the items.
 template <typename T, bool kMask>
 __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffPrefillBars& bar, volatile int* abort,
                                 uint32_t tmem, int32_t b0, int32_t b1, int32_t off_items, int causal,
@@ -279,7 +289,8 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
   const int sw = (threadIdx.x >> 5) - kSoftmaxWarp0, wg = sw >> 2, lane = threadIdx.x & 31;
   const int r = 32 * (sw & 3) + lane;
   const uint32_t tl = tmem + (uint32_t(32 * (sw & 3)) << 16);
-  const bool elected = (threadIdx.x & 127) == 0;
+  const bool elected = (threadIdx.x & 255) == 128;  // one thread of each pair of warpgroups
+  const int half = wg >> 1;                          // of the keys, and of the output's dims
   const int G = p.group;
   const float sc = p.scale_log2;
   const float2 cc = make_float2(sc, sc);
@@ -296,31 +307,25 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
     const int lim = r < nrows ? min(causal ? pos : rq.kv_len - 1, item.kv1 - 1) : -1;
     const int lo = kMask ? window_low(var, pos) : 0;
     const bool live = r < nrows;
-    uint16_t* out = p.o + tok * p.o_stride_tok + int64_t(head) * p.o_stride_head + 64 * wg;
+    uint16_t* out = p.o + tok * p.o_stride_tok + int64_t(head) * p.o_stride_head + kDiffKeys * wg;
     if (ntiles == 0) {  // no key: the output and log-sum-exps of an empty row
       if (live && item.part < 0) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) reinterpret_cast<uint4*>(out)[c] = make_uint4(0u, 0u, 0u, 0u);
-        if (p.lse) p.lse[(tok * p.num_qo_heads + head) * 2 + wg] = -INFINITY;
+        for (int c = 0; c < 4; ++c) reinterpret_cast<uint4*>(out)[c] = make_uint4(0u, 0u, 0u, 0u);
+        if (p.lse && wg < 2) p.lse[(tok * p.num_qo_heads + head) * 2 + wg] = -INFINITY;
       }
       continue;
     }
     bool ok = true;
-    // This warpgroup's 64 logits a map of tile j (kinds 2 and 3: of one map),
+    // This warpgroup's 32 logits a map of tile j (kinds 2 and 3: of one map),
     // masked; S goes back to the MMA warp.  False: no row of the warp sees any.
-    auto load_s = [&](int j, bool m1, bool m2, uint32_t (&a)[2][32], uint32_t (&b)[2][32]) -> bool {
+    auto load_s = [&](int j, bool m1, bool m2, uint32_t (&a)[32], uint32_t (&b)[32]) -> bool {
       if (m1) ok = ok && warp_wait(&bar.s_full[0], ns[0] & 1, abort);
       if (m2) ok = ok && warp_wait(&bar.s_full[1], ns[1] & 1, abort);
       tc::fence_after_sync();
-      const uint32_t col = tl + 64 * wg;
-      if (m1) {
-        tc::tmem_ld32(col, a[0]);
-        tc::tmem_ld32(col + 32, a[1]);
-      }
-      if (m2) {
-        tc::tmem_ld32(col + kTileN, b[0]);
-        tc::tmem_ld32(col + kTileN + 32, b[1]);
-      }
+      const uint32_t col = tl + kDiffKeys * wg;
+      if (m1) tc::tmem_ld32(col, a);
+      if (m2) tc::tmem_ld32(col + kTileN, b);
       tc::tmem_ld_wait();
       tc::fence_before_sync();
       __syncwarp();
@@ -330,18 +335,16 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
       }
       ns[0] += m1;
       ns[1] += m2;
-      const int key0 = item.kv0 + j * kTileN + 64 * wg;
-      if (key0 + 63 > lim || (kMask && key0 < lo)) {
+      const int key0 = item.kv0 + j * kTileN + kDiffKeys * wg;
+      if (key0 + kDiffKeys - 1 > lim || (kMask && key0 < lo)) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int key = key0 + 32 * h + e;
-            if (key > lim || (kMask && key < lo && key >= var.sink)) {
-              if (m1) a[h][e] = 0xff800000u;
-              if (m2) b[h][e] = 0xff800000u;
-            }
+        for (int e = 0; e < 32; ++e) {
+          const int key = key0 + e;
+          if (key > lim || (kMask && key < lo && key >= var.sink)) {
+            if (m1) a[e] = 0xff800000u;
+            if (m2) b[e] = 0xff800000u;
           }
+        }
       }
       return __any_sync(0xffffffffu, key0 <= lim);
     };
@@ -349,11 +352,11 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
     // ---- pass 0: running maximum (log2 domain, moved lazily) and sum per map
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     for (int j = 0; j < ntiles && ok; ++j) {
-      uint32_t s[2][2][32];
+      uint32_t s[2][32];
       if (!load_s(j, true, true, s[0], s[1]) || !ok) continue;
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const float top = max64(s[x]) * sc;
+        const float top = max32(s[x]) * sc;
         const float m_new = top > m[x] + kLazyRescale ? top : m[x];
         l[x] *= m_new == m[x] ? 1.f : ex2(m[x] - m_new);
         m[x] = m_new;
@@ -363,17 +366,17 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
 #pragma unroll
         for (int a = 0; a < 4; ++a) sum[a] = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const float2 y = fma2(make_float2(__uint_as_float(s[x][e >> 4][2 * (e & 15)]),
-                                            __uint_as_float(s[x][e >> 4][2 * (e & 15) + 1])), cc, nms);
+        for (int e = 0; e < 16; ++e) {
+          const float2 y = fma2(make_float2(__uint_as_float(s[x][2 * e]), __uint_as_float(s[x][2 * e + 1])), cc, nms);
           sum[e & 3] = add2(sum[e & 3], make_float2(ex2(y.x), ex2(y.y)));
         }
         const float2 t = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
         l[x] += t.x + t.y;
       }
     }
-    // The two warpgroups' statistics of a row together.  (`stats` of the item
-    // before has been read: this item's S needed its readers' loads.)
+    // The warpgroups' statistics of a row together, in the same order in all.
+    // (`stats` of the item before has been read: this item's S needed its
+    // readers' loads.)
     if (elected && q_held >= 0) {
       tc::bulk_wait_read_all();
       mbar_arrive(&bar.q_empty[q_held]);
@@ -384,21 +387,21 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
       pf.stats[wg][2 * x][r] = m[x];
       pf.stats[wg][2 * x + 1][r] = l[x];
     }
-    named_barrier_sync(kDiffBarrier, kSoftmaxThreads);
-    float log2l[2];
+    named_barrier_sync(kDiffBarrier, kDiffSoftmaxThreads);
+    float log2l[2], lse = -INFINITY;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      const float mo = pf.stats[wg ^ 1][2 * x][r], l_o = pf.stats[wg ^ 1][2 * x + 1][r];
-      const float mm = fmaxf(m[x], mo);
-      // warpgroup 0's term first in both, so that both have the same bits
-      const float w0 = (wg ? l_o : l[x]) * ((wg ? mo : m[x]) == mm ? 1.f : ex2((wg ? mo : m[x]) - mm));
-      const float w1 = (wg ? l[x] : l_o) * ((wg ? m[x] : mo) == mm ? 1.f : ex2((wg ? m[x] : mo) - mm));
-      m[x] = mm;
-      l[x] = mm == -INFINITY ? 0.f : w0 + w1;
-      log2l[x] = l[x] > 0.f ? __log2f(l[x]) : 0.f;
-      if (mm == -INFINITY) m[x] = 0.f;  // an empty row: every weight is 2^-inf
+      float mw[kDiffGroups], mm = -INFINITY, ll = 0.f;
+#pragma unroll
+      for (int w = 0; w < kDiffGroups; ++w) mm = fmaxf(mm, mw[w] = pf.stats[w][2 * x][r]);
+#pragma unroll
+      for (int w = 0; w < kDiffGroups; ++w)
+        if (mw[w] != -INFINITY) ll += pf.stats[w][2 * x + 1][r] * ex2(mw[w] - mm);
+      l[x] = ll;
+      m[x] = mm == -INFINITY ? 0.f : mm;  // an empty row: every weight is 2^-inf
+      log2l[x] = ll > 0.f ? __log2f(ll) : 0.f;
+      if (wg == x && ll > 0.f) lse = (m[x] + log2l[x]) * 0.69314718055994531f;
     }
-    const float lse = l[wg] > 0.f ? (m[wg] + log2l[wg]) * 0.69314718055994531f : -INFINITY;
 
     if (item.part < 0) {
       // ---- pass 1: weights w_1 - lambda w_2, scaled by 2^sigma so that both
@@ -411,70 +414,66 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
       const float2 n1 = make_float2(-a1, -a1), n2 = make_float2(-a2, -a2), nl = make_float2(-lam, -lam);
       for (int j = 0; j < ntiles && ok; ++j) {
         const int b = j & 1;
-        uint32_t s1[2][32], s2[2][32];
+        uint32_t s1[32], s2[32], pk[16];
         const bool any = load_s(j, true, true, s1, s2);
-        uint32_t pk[32];
         if (any) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int h = e >> 4, c = 2 * (e & 15);
-            const float2 x = fma2(make_float2(__uint_as_float(s1[h][c]), __uint_as_float(s1[h][c + 1])), cc, n1);
-            const float2 y = fma2(make_float2(__uint_as_float(s2[h][c]), __uint_as_float(s2[h][c + 1])), cc, n2);
+          for (int e = 0; e < 16; ++e) {
+            const float2 x = fma2(make_float2(__uint_as_float(s1[2 * e]), __uint_as_float(s1[2 * e + 1])), cc, n1);
+            const float2 y = fma2(make_float2(__uint_as_float(s2[2 * e]), __uint_as_float(s2[2 * e + 1])), cc, n2);
             const float2 w = fma2(make_float2(ex2(y.x), ex2(y.y)), nl, make_float2(ex2(x.x), ex2(x.y)));
             pk[e] = tc::pack2<T>(w.x, w.y);
           }
         } else {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) pk[e] = 0u;
+          for (int e = 0; e < 16; ++e) pk[e] = 0u;
         }
         ok = ok && warp_wait(&bar.p_free[b], (np[b] & 1) ^ 1, abort);
         ++np[b];
         tc::fence_after_sync();
-        tc::tmem_st32(tl + kDiffTmemP + 64 * b + 32 * wg, pk);
+        tc::tmem_st16(tl + kDiffTmemP + 64 * b + 16 * wg, pk);
         tc::tmem_st_wait();
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.p_full[b][wg]);
+        if (lane == 0) mbar_arrive(&bar.p_full[b][half]);
       }
-      // ---- the output: this warpgroup's 64 dims of the row
+      // ---- the output: this warpgroup's 32 dims of the row
       ok = ok && warp_wait(&bar.o_ready, no & 1, abort);
       ++no;
       tc::fence_after_sync();
-      uint32_t y[2][32];
-      tc::tmem_ld32(tl + kDiffTmemO + 64 * wg, y[0]);
-      tc::tmem_ld32(tl + kDiffTmemO + 64 * wg + 32, y[1]);
+      uint32_t y[32];
+      tc::tmem_ld32(tl + kDiffTmemO + kDiffKeys * wg, y);
       tc::tmem_ld_wait();
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.o_free);
       const float unscale = l[0] > 0.f ? ex2(-sigma) : 0.f;
       float f = unscale * dp.out_scale;
-      auto val = [&](int e) { return __uint_as_float(y[e >> 5][e & 31]); };
+      auto val = [&](int e) { return __uint_as_float(y[e]); };
       if (dp.norm_w) {
         float ss = 0.f;
 #pragma unroll
-        for (int e = 0; e < 64; ++e) ss += val(e) * val(e);
+        for (int e = 0; e < 32; ++e) ss += val(e) * val(e);
         pf.sq[wg][r] = ss * unscale * unscale;
-        named_barrier_sync(kDiffBarrier, kSoftmaxThreads);
-        f *= rms_factor(pf.sq[0][r] + pf.sq[1][r], dp.norm_eps);
+        named_barrier_sync(kDiffBarrier, kDiffSoftmaxThreads);
+        f *= rms_factor((pf.sq[0][r] + pf.sq[1][r]) + (pf.sq[2][r] + pf.sq[3][r]), dp.norm_eps);
 #pragma unroll
-        for (int e = 0; e < 64; ++e)
-          y[e >> 5][e & 31] = __float_as_uint(val(e) * __ldg(dp.norm_w + 64 * wg + e));
+        for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(val(e) * __ldg(dp.norm_w + kDiffKeys * wg + e));
       }
       auto pack8 = [&](int e) {
         return make_uint4(tc::pack2<T>(val(e) * f, val(e + 1) * f), tc::pack2<T>(val(e + 2) * f, val(e + 3) * f),
                           tc::pack2<T>(val(e + 4) * f, val(e + 5) * f), tc::pack2<T>(val(e + 6) * f, val(e + 7) * f));
       };
       const int qb = ni & 1;
-      if (nrows == kTileM) {  // a whole tile leaves through the item's Q half, by one TMA store
-        uint16_t* stage = &pf.q[qb][wg][0][0];
+      if (nrows == kTileM) {  // a whole tile leaves through the item's Q halves, by one TMA store each
+        uint16_t* stage = &pf.q[qb][half][0][0];
         uint4* my_row = reinterpret_cast<uint4*>(stage + r * 64);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) my_row[c ^ (r & 7)] = pack8(8 * c);
+        for (int c = 0; c < 4; ++c) my_row[(4 * (wg & 1) + c) ^ (r & 7)] = pack8(8 * c);
         fence_proxy_async_smem();
-        named_barrier_sync(kEpilogueBarrier0 + wg, 128);
+        named_barrier_sync(kEpilogueBarrier0 + half, 256);
         if (elected && !*abort) {
-          tc::tma_store_3d(&p.tm_o, stage, 64 * wg, item.hk * G, rq.qo_start + item.row0 / G);
+          tc::tma_store_3d(&p.tm_o, stage, 64 * half, item.hk * G, rq.qo_start + item.row0 / G);
           tc::bulk_commit();
         }
         q_held = qb;
@@ -482,23 +481,21 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
         if (elected) mbar_arrive(&bar.q_empty[qb]);
         if (live && !*abort) {
 #pragma unroll
-          for (int c = 0; c < 8; ++c) reinterpret_cast<uint4*>(out)[c] = pack8(8 * c);
+          for (int c = 0; c < 4; ++c) reinterpret_cast<uint4*>(out)[c] = pack8(8 * c);
         }
       }
-      if (p.lse && live && !*abort) p.lse[(tok * p.num_qo_heads + head) * 2 + wg] = lse;
+      if (p.lse && wg < 2 && live && !*abort) p.lse[(tok * p.num_qo_heads + head) * 2 + wg] = lse;
     } else {
       // ---- passes 2 and 3: each map's partial state, weights as hi + lo
 #pragma unroll 1
       for (int x = 0; x < 2; ++x) {
         const float2 n = make_float2(-m[x], -m[x]);
         for (int j = 0; j < ntiles && ok; ++j) {
-          uint32_t s[2][32];
+          uint32_t s[32], hi[16], low[16];
           const bool any = load_s(j, x == 0, x == 1, s, s);
-          uint32_t hi[32], low[32];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int h = e >> 4, c = 2 * (e & 15);
-            const float2 y = fma2(make_float2(__uint_as_float(s[h][c]), __uint_as_float(s[h][c + 1])), cc, n);
+          for (int e = 0; e < 16; ++e) {
+            const float2 y = fma2(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), cc, n);
             const float2 w = any ? make_float2(ex2(y.x), ex2(y.y)) : make_float2(0.f, 0.f);
             hi[e] = tc::pack2<T>(w.x, w.y);
             const float2 hf = Elem<T>::to_float2(hi[e]);
@@ -509,14 +506,14 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
           ++np[0];
           ++np[1];
           tc::fence_after_sync();
-          tc::tmem_st32(tl + kDiffTmemP + 32 * wg, hi);
-          tc::tmem_st32(tl + kDiffTmemP + 64 + 32 * wg, low);
+          tc::tmem_st16(tl + kDiffTmemP + 16 * wg, hi);
+          tc::tmem_st16(tl + kDiffTmemP + 64 + 16 * wg, low);
           tc::tmem_st_wait();
           tc::fence_before_sync();
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(&bar.p_full[0][wg]);
-            mbar_arrive(&bar.p_full[1][wg]);
+            mbar_arrive(&bar.p_full[0][half]);
+            mbar_arrive(&bar.p_full[1][half]);
           }
         }
         ok = ok && warp_wait(&bar.o_ready, no & 1, abort);
@@ -524,13 +521,11 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
         tc::fence_after_sync();
         const int64_t prw = int64_t(item.part) + x * nrows + r;
         const float inv = l[x] > 0.f ? 1.f / l[x] : 0.f;
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          uint32_t ov[32];
-          tc::tmem_ld32(tl + kDiffTmemO + 64 * wg + 32 * h, ov);
-          tc::tmem_ld_wait();
-          if (!live || *abort) continue;
-          float4* dst = reinterpret_cast<float4*>(p.fws + p.partial_o_offset + prw * kHeadDim + 64 * wg + 32 * h);
+        uint32_t ov[32];
+        tc::tmem_ld32(tl + kDiffTmemO + kDiffKeys * wg, ov);
+        tc::tmem_ld_wait();
+        if (live && !*abort) {
+          float4* dst = reinterpret_cast<float4*>(p.fws + p.partial_o_offset + prw * kHeadDim + kDiffKeys * wg);
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             dst[e] = make_float4(__uint_as_float(ov[4 * e]) * inv, __uint_as_float(ov[4 * e + 1]) * inv,
@@ -541,7 +536,7 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
         if (lane == 0) mbar_arrive(&bar.o_free);
       }
       if (elected) mbar_arrive(&bar.q_empty[ni & 1]);
-      if (live && !*abort) p.fws[int64_t(item.part) + wg * nrows + r] = lse;
+      if (wg < 2 && live && !*abort) p.fws[int64_t(item.part) + wg * nrows + r] = lse;
     }
     ++ni;
   }
