@@ -50,12 +50,28 @@ extern "C" {
  * A workspace that holds another kind of plan, or one that does not fit the
  * launch, records FI_ERR_DEVICE_CHECK and nothing is written.
  */
-fi_status fi_batch_paged_attention_run_differential(
-    const fi_plan_info* info, const void* q, int64_t q_stride_tok, int64_t q_stride_head, int32_t q_num_tokens,
-    const void* k_cache, const int64_t k_strides[3], const void* v_cache, const int64_t v_strides[3],
-    int32_t num_pages, const int32_t* kv_indices_dev, const float* lambda, const float* norm_weight, float norm_eps,
-    float out_scale, void* o, int64_t o_stride_tok, int64_t o_stride_head, float* lse, fi_dtype dtype,
-    float sm_scale, void* int_workspace_dev, void* float_workspace_dev, void* stream);
+typedef struct { /* 8-byte fields but for the fp32 values at the end */
+    const fi_plan_info* info;
+    const void* q;
+    int64_t q_stride_tok, q_stride_head, q_num_tokens;
+    const void* k_cache;
+    int64_t k_strides[3];
+    const void* v_cache;
+    int64_t v_strides[3];
+    int64_t num_pages;
+    const int32_t* kv_indices_dev;
+    const float* lambda;
+    const float* norm_weight;
+    void* o;
+    int64_t o_stride_tok, o_stride_head;
+    float* lse;
+    int64_t dtype;
+    void* int_workspace_dev;
+    void* float_workspace_dev;
+    float sm_scale, norm_eps, out_scale, reserved;
+} fi_differential_args;
+
+fi_status fi_batch_paged_attention_run_differential(const fi_differential_args* args, void* stream);
 
 #ifdef __cplusplus
 }

@@ -6,6 +6,10 @@
  * pointers, a stream is a cudaStream_t passed as void*, every entry returns an
  * fi_status, the caller owns every buffer; no allocation, no synchronisation,
  * no host copy, so every call can be captured in a CUDA graph).
+ *
+ * The calls take their many arguments in a struct of 8-byte fields (pointers
+ * and int64_t), which a binding can fill in one go; the struct itself is read
+ * before the call returns.
  */
 #ifndef FI_STEP_H_
 #define FI_STEP_H_
@@ -59,12 +63,27 @@ extern "C" {
  * counts[0..2] being what the step would need (at most INT32_MAX) and
  * counts[3] = *free_head.
  */
-fi_status fi_build_step_tables(const int32_t* qo_lens, const int32_t* kv_lens, int32_t batch, int32_t page_size,
-                               int32_t* block_table, int64_t block_table_stride, int32_t block_table_width,
-                               const int32_t* free_pages, int32_t num_free, const int32_t* free_head,
-                               int32_t* qo_indptr, int32_t* kv_indptr, int32_t* last_page_len, int32_t* kv_indices,
-                               int32_t max_pages, int32_t* positions, int32_t* slots, int32_t max_tokens,
-                               int32_t* counts, void* stream);
+typedef struct {
+    const int32_t* qo_lens;
+    const int32_t* kv_lens;
+    int64_t batch, page_size;
+    int32_t* block_table;
+    int64_t block_table_stride, block_table_width;
+    const int32_t* free_pages;
+    int64_t num_free;
+    const int32_t* free_head;
+    int32_t* qo_indptr;
+    int32_t* kv_indptr;
+    int32_t* last_page_len;
+    int32_t* kv_indices;
+    int64_t max_pages;
+    int32_t* positions;
+    int32_t* slots;
+    int64_t max_tokens;
+    int32_t* counts;
+} fi_step_tables_args;
+
+fi_status fi_build_step_tables(const fi_step_tables_args* args, void* stream);
 
 #define FI_ROTARY_MAX_PAIRS 128
 
@@ -114,6 +133,13 @@ typedef struct {
     uint64_t turns[FI_ROTARY_MAX_PAIRS];
 } fi_rotary;
 
+/* Rows [tokens, heads, dim] of an operand: strides in elements, the last
+ * dimension contiguous. */
+typedef struct {
+    void* data; /* an input is not written */
+    int64_t stride_tok, stride_head;
+} fi_rows;
+
 /* HOST only (no CUDA call).  FI_ERR_INVALID_ARG for values outside the ranges
  * above, FI_ERR_UNSUPPORTED for dims outside them. */
 fi_status fi_rotary_setup(const fi_rotary_config* cfg, fi_rotary* out);
@@ -123,20 +149,26 @@ fi_status fi_rotary_setup(const fi_rotary_config* cfg, fi_rotary* out);
  * token t becomes (a c - b s, b c + a s) with c and s the cos and sin of
  * positions[t] * f_i times the amplitude; computed in fp32 from an exact
  * angle and rounded once.
- *   q_in [num_tokens, num_q_heads, head_dim], strides (q_in_stride_tok,
- *   q_in_stride_head, 1); q_out likewise; q_out may be q_in (same strides),
- *   otherwise they must not overlap.  num_q_heads may be 0 (q not read).
+ *   q_in, q_out [num_tokens, num_q_heads, head_dim]; q_out may be q_in (same
+ *   strides), otherwise they must not overlap.  num_q_heads may be 0 (q not
+ *   read).
  *   k_in, k_out [num_tokens, num_kv_heads, head_dim] likewise; num_kv_heads
  *   may be 0.
  *   positions int32 [num_tokens], device; any value.
  * dtype FI_FP16 or FI_BF16; base pointers and strides are multiples of 16
  * bytes.  num_tokens 0 does nothing.
  */
-fi_status fi_rotary_apply(const fi_rotary* rot, const int32_t* positions, int32_t num_tokens, const void* q_in,
-                          int64_t q_in_stride_tok, int64_t q_in_stride_head, void* q_out, int64_t q_out_stride_tok,
-                          int64_t q_out_stride_head, int32_t num_q_heads, const void* k_in, int64_t k_in_stride_tok,
-                          int64_t k_in_stride_head, void* k_out, int64_t k_out_stride_tok, int64_t k_out_stride_head,
-                          int32_t num_kv_heads, fi_dtype dtype, void* stream);
+typedef struct {
+    const fi_rotary* rotary;
+    const int32_t* positions;
+    int64_t num_tokens;
+    fi_rows q_in, q_out;
+    int64_t num_q_heads;
+    fi_rows k_in, k_out;
+    int64_t num_kv_heads, dtype;
+} fi_rotary_apply_args;
+
+fi_status fi_rotary_apply(const fi_rotary_apply_args* args, void* stream);
 
 /*
  * fi_rotary_append -- one launch for a step's new tokens: q rotated as by
@@ -153,13 +185,23 @@ fi_status fi_rotary_apply(const fi_rotary* rot, const int32_t* positions, int32_
  * Other arguments, dtypes and alignment as for fi_rotary_apply; page_size a
  * power of two in [1, 128].
  */
-fi_status fi_rotary_append(const fi_rotary* rot, const int32_t* positions, const int32_t* slots, int32_t num_tokens,
-                           const void* q_in, int64_t q_in_stride_tok, int64_t q_in_stride_head, void* q_out,
-                           int64_t q_out_stride_tok, int64_t q_out_stride_head, int32_t num_q_heads,
-                           const void* k_in, int64_t k_in_stride_tok, int64_t k_in_stride_head, const void* v_in,
-                           int64_t v_in_stride_tok, int64_t v_in_stride_head, int32_t v_dim, int32_t num_kv_heads,
-                           void* k_cache, const int64_t k_strides[3], void* v_cache, const int64_t v_strides[3],
-                           int32_t page_size, int32_t num_pages, fi_dtype dtype, void* stream);
+typedef struct {
+    const fi_rotary* rotary;
+    const int32_t* positions;
+    const int32_t* slots;
+    int64_t num_tokens;
+    fi_rows q_in, q_out;
+    int64_t num_q_heads;
+    fi_rows k_in, v_in;
+    int64_t v_dim, num_kv_heads;
+    void* k_cache;
+    int64_t k_strides[3];
+    void* v_cache;
+    int64_t v_strides[3];
+    int64_t page_size, num_pages, dtype;
+} fi_rotary_append_args;
+
+fi_status fi_rotary_append(const fi_rotary_append_args* args, void* stream);
 
 #ifdef __cplusplus
 }

@@ -193,14 +193,27 @@ cudaError_t launch_rotary(RotaryParams& a, const fi_rotary* rot, fi_dtype dtype,
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 bool stride_ok(int64_t elems) { return elems >= 0 && elems % 8 == 0; }
 
-fi_status check_rotary(const fi_rotary* rot, int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
-                       fi_dtype dtype) {
-  if (!rot || num_tokens < 0 || num_q_heads < 0 || num_kv_heads < 0) return FI_ERR_INVALID_ARG;
+fi_status check_rotary(const fi_rotary* rot, int64_t num_tokens, int64_t num_q_heads, int64_t num_kv_heads,
+                       int64_t dtype) {
+  if (!rot || num_tokens < 0 || num_tokens > INT32_MAX || num_q_heads < 0 || num_kv_heads < 0)
+    return FI_ERR_INVALID_ARG;
   if (rot->head_dim < 16 || rot->head_dim > 2 * FI_ROTARY_MAX_PAIRS || rot->head_dim % 8 || rot->rot_dim < 16 ||
       rot->rot_dim > rot->head_dim || rot->rot_dim % 16 || (rot->interleaved != 0 && rot->interleaved != 1))
     return FI_ERR_UNSUPPORTED;
   if (num_q_heads > 65536 || num_kv_heads > 65536) return FI_ERR_UNSUPPORTED;
   return dtype == FI_FP16 || dtype == FI_BF16 ? FI_OK : FI_ERR_UNSUPPORTED;
+}
+
+bool rows_ok(const fi_rows& r) { return aligned(r.data, 16) && stride_ok(r.stride_tok) && stride_ok(r.stride_head); }
+
+RotaryRows rows_of(const fi_rows& in, const fi_rows& out, int64_t heads) {
+  return {static_cast<const uint16_t*>(in.data), in.stride_tok, in.stride_head, static_cast<uint16_t*>(out.data),
+          out.stride_tok, out.stride_head, 0, int32_t(heads)};
+}
+
+RotaryRows rows_to_cache(const fi_rows& in, void* cache, const int64_t strides[3], int64_t heads) {
+  return {static_cast<const uint16_t*>(in.data), in.stride_tok, in.stride_head, static_cast<uint16_t*>(cache),
+          strides[0], strides[2], strides[1], int32_t(heads)};
 }
 
 }  // namespace
@@ -245,77 +258,57 @@ extern "C" fi_status fi_rotary_setup(const fi_rotary_config* cfg, fi_rotary* out
   return FI_OK;
 }
 
-extern "C" fi_status fi_rotary_apply(const fi_rotary* rot, const int32_t* positions, int32_t num_tokens,
-                                     const void* q_in, int64_t q_in_stride_tok, int64_t q_in_stride_head, void* q_out,
-                                     int64_t q_out_stride_tok, int64_t q_out_stride_head, int32_t num_q_heads,
-                                     const void* k_in, int64_t k_in_stride_tok, int64_t k_in_stride_head, void* k_out,
-                                     int64_t k_out_stride_tok, int64_t k_out_stride_head, int32_t num_kv_heads,
-                                     fi_dtype dtype, void* stream) {
-  const fi_status st = check_rotary(rot, num_tokens, num_q_heads, num_kv_heads, dtype);
+extern "C" fi_status fi_rotary_apply(const fi_rotary_apply_args* x, void* stream) {
+  if (!x) return FI_ERR_INVALID_ARG;
+  const fi_status st = check_rotary(x->rotary, x->num_tokens, x->num_q_heads, x->num_kv_heads, x->dtype);
   if (st != FI_OK) return st;
-  if (!positions || (num_q_heads && (!q_in || !q_out)) || (num_kv_heads && (!k_in || !k_out)))
+  const bool q = x->num_q_heads > 0, k = x->num_kv_heads > 0;
+  if (!x->positions || (q && (!x->q_in.data || !x->q_out.data)) || (k && (!x->k_in.data || !x->k_out.data)))
     return FI_ERR_INVALID_ARG;
-  if (!aligned(positions, 4)) return FI_ERR_ALIGNMENT;
-  if (num_q_heads && (!aligned(q_in, 16) || !aligned(q_out, 16) || !stride_ok(q_in_stride_tok) ||
-                      !stride_ok(q_in_stride_head) || !stride_ok(q_out_stride_tok) || !stride_ok(q_out_stride_head)))
+  if (!aligned(x->positions, 4) || (q && (!rows_ok(x->q_in) || !rows_ok(x->q_out))) ||
+      (k && (!rows_ok(x->k_in) || !rows_ok(x->k_out))))
     return FI_ERR_ALIGNMENT;
-  if (num_kv_heads && (!aligned(k_in, 16) || !aligned(k_out, 16) || !stride_ok(k_in_stride_tok) ||
-                       !stride_ok(k_in_stride_head) || !stride_ok(k_out_stride_tok) || !stride_ok(k_out_stride_head)))
-    return FI_ERR_ALIGNMENT;
-  if (num_tokens == 0 || num_q_heads + num_kv_heads == 0) return FI_OK;
+  if (x->num_tokens == 0 || (!q && !k)) return FI_OK;
   RotaryParams a;
   std::memset(&a, 0, sizeof a);
-  a.q = {static_cast<const uint16_t*>(q_in), q_in_stride_tok, q_in_stride_head, static_cast<uint16_t*>(q_out),
-         q_out_stride_tok, q_out_stride_head, 0, num_q_heads};
-  a.k = {static_cast<const uint16_t*>(k_in), k_in_stride_tok, k_in_stride_head, static_cast<uint16_t*>(k_out),
-         k_out_stride_tok, k_out_stride_head, 0, num_kv_heads};
-  a.positions = positions;
-  a.num_tokens = num_tokens;
-  return launch_rotary(a, rot, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FI_OK : FI_ERR_CUDA;
+  a.q = rows_of(x->q_in, x->q_out, x->num_q_heads);
+  a.k = rows_of(x->k_in, x->k_out, x->num_kv_heads);
+  a.positions = x->positions;
+  a.num_tokens = int32_t(x->num_tokens);
+  return launch_rotary(a, x->rotary, fi_dtype(x->dtype), static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? FI_OK
+             : FI_ERR_CUDA;
 }
 
-extern "C" fi_status fi_rotary_append(const fi_rotary* rot, const int32_t* positions, const int32_t* slots,
-                                      int32_t num_tokens, const void* q_in, int64_t q_in_stride_tok,
-                                      int64_t q_in_stride_head, void* q_out, int64_t q_out_stride_tok,
-                                      int64_t q_out_stride_head, int32_t num_q_heads, const void* k_in,
-                                      int64_t k_in_stride_tok, int64_t k_in_stride_head, const void* v_in,
-                                      int64_t v_in_stride_tok, int64_t v_in_stride_head, int32_t v_dim,
-                                      int32_t num_kv_heads, void* k_cache, const int64_t k_strides[3], void* v_cache,
-                                      const int64_t v_strides[3], int32_t page_size, int32_t num_pages,
-                                      fi_dtype dtype, void* stream) {
-  const fi_status st = check_rotary(rot, num_tokens, num_q_heads, num_kv_heads, dtype);
+extern "C" fi_status fi_rotary_append(const fi_rotary_append_args* x, void* stream) {
+  if (!x) return FI_ERR_INVALID_ARG;
+  const fi_status st = check_rotary(x->rotary, x->num_tokens, x->num_q_heads, x->num_kv_heads, x->dtype);
   if (st != FI_OK) return st;
-  if (v_dim < 0 || v_dim > 512 || v_dim % 8 || page_size < 1 || page_size > 128 || (page_size & (page_size - 1)))
-    return FI_ERR_UNSUPPORTED;
-  if (!positions || !slots || num_kv_heads < 1 || num_pages < 1 || !k_in || !k_cache || !k_strides ||
-      (num_q_heads && (!q_in || !q_out)) || (v_dim && (!v_in || !v_cache || !v_strides)))
+  const int64_t P = x->page_size;
+  if (x->v_dim < 0 || x->v_dim > 512 || x->v_dim % 8 || P < 1 || P > 128 || (P & (P - 1))) return FI_ERR_UNSUPPORTED;
+  const bool q = x->num_q_heads > 0, v = x->v_dim > 0;
+  if (!x->positions || !x->slots || x->num_kv_heads < 1 || x->num_pages < 1 || x->num_pages > INT32_MAX ||
+      !x->k_in.data || !x->k_cache || (q && (!x->q_in.data || !x->q_out.data)) ||
+      (v && (!x->v_in.data || !x->v_cache)))
     return FI_ERR_INVALID_ARG;
-  if (!aligned(positions, 4) || !aligned(slots, 4) || !aligned(k_in, 16) || !aligned(k_cache, 16) ||
-      !stride_ok(k_in_stride_tok) || !stride_ok(k_in_stride_head))
-    return FI_ERR_ALIGNMENT;
-  if (num_q_heads && (!aligned(q_in, 16) || !aligned(q_out, 16) || !stride_ok(q_in_stride_tok) ||
-                      !stride_ok(q_in_stride_head) || !stride_ok(q_out_stride_tok) || !stride_ok(q_out_stride_head)))
-    return FI_ERR_ALIGNMENT;
-  if (v_dim && (!aligned(v_in, 16) || !aligned(v_cache, 16) || !stride_ok(v_in_stride_tok) ||
-                !stride_ok(v_in_stride_head)))
+  if (!aligned(x->positions, 4) || !aligned(x->slots, 4) || !rows_ok(x->k_in) || !aligned(x->k_cache, 16) ||
+      (q && (!rows_ok(x->q_in) || !rows_ok(x->q_out))) || (v && (!rows_ok(x->v_in) || !aligned(x->v_cache, 16))))
     return FI_ERR_ALIGNMENT;
   for (int i = 0; i < 3; ++i)
-    if (!stride_ok(k_strides[i]) || (v_dim && !stride_ok(v_strides[i]))) return FI_ERR_ALIGNMENT;
-  if (num_tokens == 0) return FI_OK;
+    if (!stride_ok(x->k_strides[i]) || (v && !stride_ok(x->v_strides[i]))) return FI_ERR_ALIGNMENT;
+  if (x->num_tokens == 0) return FI_OK;
   RotaryParams a;
   std::memset(&a, 0, sizeof a);
-  a.q = {static_cast<const uint16_t*>(q_in), q_in_stride_tok, q_in_stride_head, static_cast<uint16_t*>(q_out),
-         q_out_stride_tok, q_out_stride_head, 0, num_q_heads};
-  a.k = {static_cast<const uint16_t*>(k_in), k_in_stride_tok, k_in_stride_head, static_cast<uint16_t*>(k_cache),
-         k_strides[0], k_strides[2], k_strides[1], num_kv_heads};
-  if (v_dim)
-    a.v = {static_cast<const uint16_t*>(v_in), v_in_stride_tok, v_in_stride_head, static_cast<uint16_t*>(v_cache),
-           v_strides[0], v_strides[2], v_strides[1], num_kv_heads};
-  a.v_chunks = v_dim / 8;
-  a.positions = positions;
-  a.slots = slots;
-  a.num_slots = int64_t(num_pages) * page_size;
-  while ((1 << a.log2_page) < page_size) ++a.log2_page;
-  a.num_tokens = num_tokens;
-  return launch_rotary(a, rot, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FI_OK : FI_ERR_CUDA;
+  a.q = rows_of(x->q_in, x->q_out, x->num_q_heads);
+  a.k = rows_to_cache(x->k_in, x->k_cache, x->k_strides, x->num_kv_heads);
+  if (v) a.v = rows_to_cache(x->v_in, x->v_cache, x->v_strides, x->num_kv_heads);
+  a.v_chunks = int32_t(x->v_dim / 8);
+  a.positions = x->positions;
+  a.slots = x->slots;
+  a.num_slots = x->num_pages * P;
+  while ((1 << a.log2_page) < P) ++a.log2_page;
+  a.num_tokens = int32_t(x->num_tokens);
+  return launch_rotary(a, x->rotary, fi_dtype(x->dtype), static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? FI_OK
+             : FI_ERR_CUDA;
 }

@@ -10,6 +10,7 @@
 
 #include <climits>
 #include <cstdint>
+#include <initializer_list>
 
 #include "../../include/fi_step.h"
 #include "launch.h"
@@ -192,35 +193,37 @@ __global__ void __launch_bounds__(kTableThreads) step_tables_kernel(const __grid
 
 using namespace fi;
 
-extern "C" fi_status fi_build_step_tables(const int32_t* qo_lens, const int32_t* kv_lens, int32_t batch,
-                                          int32_t page_size, int32_t* block_table, int64_t block_table_stride,
-                                          int32_t block_table_width, const int32_t* free_pages, int32_t num_free,
-                                          const int32_t* free_head, int32_t* qo_indptr, int32_t* kv_indptr,
-                                          int32_t* last_page_len, int32_t* kv_indices, int32_t max_pages,
-                                          int32_t* positions, int32_t* slots, int32_t max_tokens, int32_t* counts,
-                                          void* stream) {
-  if (!qo_lens || !kv_lens || !block_table || !qo_indptr || !kv_indptr || !last_page_len || !counts || batch < 1 ||
-      block_table_width < 1 || block_table_stride < block_table_width || num_free < 0 || max_pages < 0 ||
-      max_tokens < 0)
+extern "C" fi_status fi_build_step_tables(const fi_step_tables_args* x, void* stream) {
+  if (!x) return FI_ERR_INVALID_ARG;
+  if (!x->qo_lens || !x->kv_lens || !x->block_table || !x->qo_indptr || !x->kv_indptr || !x->last_page_len ||
+      !x->counts || x->batch < 1 || x->block_table_width < 1 || x->block_table_stride < x->block_table_width ||
+      x->num_free < 0 || x->max_pages < 0 || x->max_tokens < 0)
     return FI_ERR_INVALID_ARG;
-  if ((num_free > 0 && (!free_pages || !free_head)) || (max_pages > 0 && !kv_indices) ||
-      (max_tokens > 0 && (!positions || !slots)))
+  if (x->block_table_width > INT32_MAX || x->num_free > INT32_MAX || x->max_pages > INT32_MAX ||
+      x->max_tokens > INT32_MAX)
     return FI_ERR_INVALID_ARG;
-  if (free_head && free_head >= counts && free_head < counts + FI_STEP_COUNTS) return FI_ERR_INVALID_ARG;
-  if (batch > FI_STEP_MAX_BATCH || page_size < 1 || page_size > 128 || (page_size & (page_size - 1)))
-    return FI_ERR_UNSUPPORTED;
-  const uintptr_t all = reinterpret_cast<uintptr_t>(qo_lens) | reinterpret_cast<uintptr_t>(kv_lens) |
-                        reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(free_pages) |
-                        reinterpret_cast<uintptr_t>(free_head) | reinterpret_cast<uintptr_t>(qo_indptr) |
-                        reinterpret_cast<uintptr_t>(kv_indptr) | reinterpret_cast<uintptr_t>(last_page_len) |
-                        reinterpret_cast<uintptr_t>(kv_indices) | reinterpret_cast<uintptr_t>(positions) |
-                        reinterpret_cast<uintptr_t>(slots) | reinterpret_cast<uintptr_t>(counts);
+  if ((x->num_free > 0 && (!x->free_pages || !x->free_head)) || (x->max_pages > 0 && !x->kv_indices) ||
+      (x->max_tokens > 0 && (!x->positions || !x->slots)))
+    return FI_ERR_INVALID_ARG;
+  if (x->free_head && x->free_head >= x->counts && x->free_head < x->counts + FI_STEP_COUNTS)
+    return FI_ERR_INVALID_ARG;
+  const int64_t P = x->page_size;
+  if (x->batch > FI_STEP_MAX_BATCH || P < 1 || P > 128 || (P & (P - 1))) return FI_ERR_UNSUPPORTED;
+  uintptr_t all = 0;
+  for (const int32_t* ptr : {x->qo_lens, x->kv_lens, static_cast<const int32_t*>(x->block_table), x->free_pages,
+                             x->free_head, static_cast<const int32_t*>(x->qo_indptr),
+                             static_cast<const int32_t*>(x->kv_indptr), static_cast<const int32_t*>(x->last_page_len),
+                             static_cast<const int32_t*>(x->kv_indices), static_cast<const int32_t*>(x->positions),
+                             static_cast<const int32_t*>(x->slots), static_cast<const int32_t*>(x->counts)})
+    all |= reinterpret_cast<uintptr_t>(ptr);
   if (all & 3u) return FI_ERR_ALIGNMENT;
-  TableParams a{qo_lens,   kv_lens,   batch,         0,          block_table, block_table_stride, block_table_width,
-                free_pages, num_free, free_head,     qo_indptr,  kv_indptr,   last_page_len,      kv_indices,
-                max_pages, positions, slots,         max_tokens, counts};
-  while ((1 << a.log2_page) < page_size) ++a.log2_page;
-  const size_t smem = size_t(3) * (batch + 1) * 4;
+  TableParams a{x->qo_lens,       x->kv_lens,        int32_t(x->batch), 0,
+                x->block_table,   x->block_table_stride, int32_t(x->block_table_width),
+                x->free_pages,    int32_t(x->num_free), x->free_head,   x->qo_indptr,
+                x->kv_indptr,     x->last_page_len,  x->kv_indices,     int32_t(x->max_pages),
+                x->positions,     x->slots,          int32_t(x->max_tokens), x->counts};
+  while ((1 << a.log2_page) < P) ++a.log2_page;
+  const size_t smem = size_t(3) * (a.batch + 1) * 4;
   if (smem > 48 * 1024) {
     static bool configured[kMaxDevices] = {};
     int dev = 0;
@@ -233,7 +236,7 @@ extern "C" fi_status fi_build_step_tables(const int32_t* qo_lens, const int32_t*
     }
   }
   // Enough blocks for four entries a thread, at most two per SM.
-  const int64_t work = (int64_t(max_pages) + 3) / 4 + max_tokens;
+  const int64_t work = (int64_t(a.max_pages) + 3) / 4 + a.max_tokens;
   int64_t blocks = (work + kTableThreads - 1) / kTableThreads;
   blocks = blocks < 1 ? 1 : blocks > 304 ? 304 : blocks;
   step_tables_kernel<<<unsigned(blocks), kTableThreads, smem, static_cast<cudaStream_t>(stream)>>>(a);

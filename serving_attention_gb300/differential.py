@@ -7,42 +7,46 @@ fallback.  The plan is the ordinary one, made with differential=1:
     ws = Workspace(cfg)
     info = plan(ws, qo_indptr, kv_indptr, kv_indices, last_page_len, 32, 8, 128, 16, causal=1)
     differential.run(ws, info, q, k_cache, v_cache, kv_indices_dev, lam, o, lse, sm_scale)
+
+A decode step makes its calls within microseconds of each other, so the
+arguments travel as one packed struct and every attribute of a tensor is asked
+for once.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import struct
 
 import torch
 
-from . import _DTYPE, PlanInfo, Workspace, _check, _stream_ptr, load as _load_lib
+from . import _DTYPE, PlanInfo, Workspace, _check, load as _load_lib
 
 EXPORTS = ["fi_batch_paged_attention_run_differential"]
 
-_bound = False
-_Strides = ctypes.c_int64 * 3
+_run = None
+_ARGS = struct.Struct("=24q4f")  # fi_differential_args
 
 
 def load() -> ctypes.CDLL:
-    global _bound
+    global _run
     lib = _load_lib()
-    if not _bound:
-        vp, i32, i64, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
-        lib.fi_batch_paged_attention_run_differential.argtypes = [
-            ctypes.POINTER(PlanInfo), vp, i64, i64, i32, vp, vp, vp, vp, i32, vp, vp, vp, f32, f32, vp, i64, i64, vp,
-            ctypes.c_int, f32, vp, vp, vp]
-        lib.fi_batch_paged_attention_run_differential.restype = ctypes.c_int
-        _bound = True
+    if _run is None:
+        fn = lib.fi_batch_paged_attention_run_differential
+        fn.argtypes, fn.restype = [ctypes.c_char_p, ctypes.c_void_p], ctypes.c_int
+        _run = fn
     return lib
 
 
-def _on_device(device: torch.device):
-    """Launches go to the tensors' device, whichever is current."""
-    if device.type != "cuda":
+def _call(fn, args: bytes, index: int, stream, where: str):
+    """Calls fn on device `index`, whichever is current, and its current stream if none is given."""
+    if index < 0:
         raise TypeError("the tensors must be on a CUDA device")
-    if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+    if index != torch._C._cuda_getDevice():
+        with torch.cuda.device(index):
+            return _call(fn, args, index, stream, where)
+    status = fn(args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
+    if status:
+        _check(status, where)
 
 
 def run(ws: Workspace, info: PlanInfo, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -52,34 +56,46 @@ def run(ws: Workspace, info: PlanInfo, q: torch.Tensor, k_cache: torch.Tensor, v
 
     q, o [tokens, Hq, 128]; caches [pages, page_size, Hkv, 128]; lam fp32 [Hq];
     lse fp32 [tokens, Hq, 2] or None; norm_weight fp32 [128] or None."""
-    lib = load()
-    dtype = _DTYPE.get(q.dtype)
-    if dtype is None or not (q.dtype == k_cache.dtype == v_cache.dtype == o.dtype):
+    if _run is None:
+        load()
+    dtype, index = q.dtype, q.get_device()
+    code = _DTYPE.get(dtype)
+    if code is None or k_cache.dtype is not dtype or v_cache.dtype is not dtype or o.dtype is not dtype:
         raise TypeError("q, k, v and o must share one 16-bit dtype")
-    if kv_indices_dev.dtype != torch.int32 or not kv_indices_dev.is_contiguous():
+    if kv_indices_dev.dtype is not torch.int32 or not kv_indices_dev.is_contiguous():
         raise TypeError("kv_indices must be a contiguous int32 device tensor")
-    f32 = (lam,) if norm_weight is None else (lam, norm_weight)
-    if any(t.dtype != torch.float32 or not t.is_contiguous() for t in f32):
-        raise TypeError("lam and norm_weight must be contiguous fp32")
-    device = q.device
-    if any(t.device != device for t in (k_cache, v_cache, kv_indices_dev, o, ws.int_ws, *f32)):
+    if not (index == k_cache.get_device() == v_cache.get_device() == kv_indices_dev.get_device() == o.get_device() ==
+            lam.get_device() == ws.int_ws.get_device()):
         raise TypeError("all tensors must be on one device")
-    hq, hkv, tokens = info.num_qo_heads, info.num_kv_heads, q.shape[0]
-    if q.shape != (tokens, hq, 128) or o.shape != q.shape or q.stride(2) != 1 or o.stride(2) != 1:
+    if lam.dtype is not torch.float32 or not lam.is_contiguous():
+        raise TypeError("lam must be contiguous fp32")
+    hq = info.num_qo_heads
+    shape, cache = q.shape, k_cache.shape
+    tokens = shape[0]
+    qt, qh, qd = q.stride()
+    ot, oh, od = o.stride()
+    kp, ks, kh, kd = k_cache.stride()
+    vp, vs, vh, vd = v_cache.stride()
+    if shape != (tokens, hq, 128) or o.shape != shape or qd != 1 or od != 1:
         raise ValueError("q and o are [tokens, num_qo_heads, 128], the last dimension contiguous")
-    cache = (k_cache.shape[0], info.page_size, hkv, 128)
-    if k_cache.shape != cache or v_cache.shape != cache or k_cache.stride(3) != 1 or v_cache.stride(3) != 1:
+    if cache != (cache[0], info.page_size, info.num_kv_heads, 128) or v_cache.shape != cache or kd != 1 or vd != 1:
         raise ValueError("the caches are [pages, page_size, num_kv_heads, 128], the last dimension contiguous")
-    if lam.numel() != hq or (norm_weight is not None and norm_weight.numel() != 128):
-        raise ValueError("lam has num_qo_heads entries and norm_weight 128")
-    if lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous() or lse.device != device or
-                            lse.shape != (tokens, hq, 2)):
-        raise ValueError("lse is a contiguous fp32 [tokens, num_qo_heads, 2] tensor")
-    with _on_device(device):
-        st = lib.fi_batch_paged_attention_run_differential(
-            ctypes.byref(info), q.data_ptr(), q.stride(0), q.stride(1), tokens, k_cache.data_ptr(),
-            _Strides(*k_cache.stride()[:3]), v_cache.data_ptr(), _Strides(*v_cache.stride()[:3]), cache[0],
-            kv_indices_dev.data_ptr(), lam.data_ptr(), norm_weight.data_ptr() if norm_weight is not None else None,
-            norm_eps, out_scale, o.data_ptr(), o.stride(0), o.stride(1), lse.data_ptr() if lse is not None else None,
-            dtype, sm_scale, ws.int_ws.data_ptr(), ws.float_ws.data_ptr(), _stream_ptr(stream))
-    _check(st, "fi_batch_paged_attention_run_differential")
+    if lam.numel() != hq:
+        raise ValueError("lam has num_qo_heads entries")
+    w = 0
+    if norm_weight is not None:
+        if norm_weight.dtype is not torch.float32 or not norm_weight.is_contiguous() or norm_weight.numel() != 128 or \
+                norm_weight.get_device() != index:
+            raise ValueError("norm_weight is 128 contiguous fp32 values on the tensors' device")
+        w = norm_weight.data_ptr()
+    lse_ptr = 0
+    if lse is not None:
+        if lse.dtype is not torch.float32 or not lse.is_contiguous() or lse.get_device() != index or \
+                lse.shape != (tokens, hq, 2):
+            raise ValueError("lse is a contiguous fp32 [tokens, num_qo_heads, 2] tensor")
+        lse_ptr = lse.data_ptr()
+    _call(_run, _ARGS.pack(ctypes.addressof(info), q.data_ptr(), qt, qh, tokens, k_cache.data_ptr(), kp, ks, kh,
+                           v_cache.data_ptr(), vp, vs, vh, cache[0], kv_indices_dev.data_ptr(), lam.data_ptr(), w,
+                           o.data_ptr(), ot, oh, lse_ptr, code, ws.int_ws.data_ptr(), ws.float_ws.data_ptr(),
+                           sm_scale, norm_eps, out_scale, 0.0),
+          index, stream, "fi_batch_paged_attention_run_differential")

@@ -10,11 +10,12 @@ append to the paged cache.  Argument marshalling only; there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
-from . import _DTYPE, _check, _stream_ptr, load as _load_lib
-from .differential import _on_device
+from . import _DTYPE, _check, load as _load_lib
+from .differential import _call
 
 EXPORTS = ["fi_build_step_tables", "fi_rotary_setup", "fi_rotary_apply", "fi_rotary_append"]
 SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3, "yarn": 4}
@@ -34,26 +35,23 @@ class Rotary(ctypes.Structure):
                 ("turns", ctypes.c_uint64 * MAX_PAIRS)]
 
 
-_bound = False
-_Strides = ctypes.c_int64 * 3
+_apply = _append = _tables = None
+_APPLY_ARGS = struct.Struct("=18q")   # fi_rotary_apply_args
+_APPEND_ARGS = struct.Struct("=30q")  # fi_rotary_append_args
+_TABLE_ARGS = struct.Struct("=19q")   # fi_step_tables_args
 
 
 def load() -> ctypes.CDLL:
-    global _bound
+    global _apply, _append, _tables
     lib = _load_lib()
-    if not _bound:
-        vp, i32, i64, ci = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int
-        rotp = ctypes.POINTER(Rotary)
-        rows = [vp, i64, i64, vp, i64, i64, i32]
-        lib.fi_rotary_setup.argtypes = [ctypes.POINTER(RotaryConfig), rotp]
-        lib.fi_rotary_apply.argtypes = [rotp, vp, i32, *rows, *rows, ci, vp]
-        lib.fi_rotary_append.argtypes = [rotp, vp, vp, i32, *rows, vp, i64, i64, vp, i64, i64, i32, i32, vp, vp, vp,
-                                         vp, i32, i32, ci, vp]
-        lib.fi_build_step_tables.argtypes = [vp, vp, i32, i32, vp, i64, i32, vp, i32, vp, vp, vp, vp, vp, i32, vp, vp,
-                                             i32, vp, vp]
+    if _tables is None:
+        lib.fi_rotary_setup.argtypes = [ctypes.POINTER(RotaryConfig), ctypes.POINTER(Rotary)]
         for name in EXPORTS:
-            getattr(lib, name).restype = ci
-        _bound = True
+            fn = getattr(lib, name)
+            fn.restype = ctypes.c_int
+            if name != "fi_rotary_setup":
+                fn.argtypes = [ctypes.c_char_p, ctypes.c_void_p]
+        _apply, _append, _tables = lib.fi_rotary_apply, lib.fi_rotary_append, lib.fi_build_step_tables
     return lib
 
 
@@ -75,45 +73,47 @@ def rotary_setup(head_dim: int, rot_dim: int | None = None, interleaved: bool = 
     return rot
 
 
-def _rows(t: torch.Tensor | None, tokens: int, dtype, device, dim: int, what: str):
-    """Checks [tokens, heads, dim] rows; their heads (0 for None)."""
-    if t is None:
-        return 0
-    if t.dtype != dtype or t.device != device:
-        raise TypeError(f"{what} must have the dtype and device of the other tensors")
-    if t.dim() != 3 or t.shape[0] != tokens or t.shape[2] != dim or t.stride(2) != 1:
-        raise ValueError(f"{what} is [tokens, heads, {dim}], the last dimension contiguous")
-    return t.shape[1]
+def _rows(x: torch.Tensor | None, y: torch.Tensor | None, tokens: int, dim: int, dtype, index: int, what: str):
+    """Checks [tokens, heads, dim] rows x and their outputs y: (heads, their fi_rows)."""
+    if x is None or y is None:
+        if x is not y:
+            raise ValueError(f"{what} and its output go together")
+        return 0, 0, 0, 0, 0, 0, 0
+    if x.dtype is not dtype or y.dtype is not dtype or x.get_device() != index or y.get_device() != index:
+        raise TypeError(f"{what} and its output must have the dtype and device of the other tensors")
+    shape = x.shape
+    if len(shape) != 3 or shape[0] != tokens or shape[2] != dim or y.shape != shape:
+        raise ValueError(f"{what} and its output are [tokens, heads, {dim}]")
+    xt, xh, xd = x.stride()
+    yt, yh, yd = y.stride()
+    if xd != 1 or yd != 1:
+        raise ValueError(f"the last dimension of {what} and its output must be contiguous")
+    return shape[1], x.data_ptr(), xt, xh, y.data_ptr(), yt, yh
 
 
-def _index(t: torch.Tensor, device, what: str) -> int:
-    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or t.device != device:
+def _index(t: torch.Tensor, index: int, what: str) -> int:
+    if t.dtype is not torch.int32 or t.dim() != 1 or not t.is_contiguous() or t.get_device() != index:
         raise TypeError(f"{what} must be a contiguous int32 vector on the tensors' device")
     return t.shape[0]
-
-
-def _ptr(t: torch.Tensor | None):
-    return (t.data_ptr(), t.stride(0), t.stride(1)) if t is not None else (None, 0, 0)
 
 
 def rotate(rot: Rotary, positions: torch.Tensor, q: torch.Tensor | None, q_out: torch.Tensor | None,
            k: torch.Tensor | None = None, k_out: torch.Tensor | None = None, stream=None):
     """Rotate q into q_out and k into k_out ([tokens, heads, head_dim]; an output may be its input)."""
+    if _apply is None:
+        load()
     some = q if q is not None else k
     if some is None:
         raise ValueError("q or k is needed")
-    dtype, device = some.dtype, some.device
-    if dtype not in _DTYPE:
+    dtype, index = some.dtype, some.get_device()
+    code = _DTYPE.get(dtype)
+    if code is None:
         raise TypeError(f"unsupported dtype {dtype}")
-    tokens = _index(positions, device, "positions")
-    hq, hk = (_rows(t, tokens, dtype, device, rot.head_dim, n) for t, n in ((q, "q"), (k, "k")))
-    if _rows(q_out, tokens, dtype, device, rot.head_dim, "q_out") != hq or \
-            _rows(k_out, tokens, dtype, device, rot.head_dim, "k_out") != hk:
-        raise ValueError("q_out and k_out have the shapes of q and k")
-    with _on_device(device):
-        st = load().fi_rotary_apply(ctypes.byref(rot), positions.data_ptr(), tokens, *_ptr(q), *_ptr(q_out), hq,
-                                    *_ptr(k), *_ptr(k_out), hk, _DTYPE[dtype], _stream_ptr(stream))
-    _check(st, "fi_rotary_apply")
+    tokens, dim = _index(positions, index, "positions"), rot.head_dim
+    hq, *q_rows = _rows(q, q_out, tokens, dim, dtype, index, "q")
+    hk, *k_rows = _rows(k, k_out, tokens, dim, dtype, index, "k")
+    _call(_apply, _APPLY_ARGS.pack(ctypes.addressof(rot), positions.data_ptr(), tokens, *q_rows, hq, *k_rows, hk, code),
+          index, stream, "fi_rotary_apply")
 
 
 def append(rot: Rotary, positions: torch.Tensor, slots: torch.Tensor, q: torch.Tensor | None,
@@ -122,36 +122,46 @@ def append(rot: Rotary, positions: torch.Tensor, slots: torch.Tensor, q: torch.T
     """Rotate q into q_out and k into k_cache, and copy v into v_cache, token t
     at slot slots[t] = page * page_size + slot (outside the cache: not written).
     Caches [pages, page_size, heads, dim]."""
-    dtype, device = k.dtype, k.device
-    if dtype not in _DTYPE:
+    if _append is None:
+        load()
+    dtype, index = k.dtype, k.get_device()
+    code = _DTYPE.get(dtype)
+    if code is None:
         raise TypeError(f"unsupported dtype {dtype}")
-    tokens = _index(positions, device, "positions")
-    if _index(slots, device, "slots") != tokens:
+    tokens, dim = _index(positions, index, "positions"), rot.head_dim
+    if _index(slots, index, "slots") != tokens:
         raise ValueError("positions and slots have one entry per token")
-    hq = _rows(q, tokens, dtype, device, rot.head_dim, "q")
-    if _rows(q_out, tokens, dtype, device, rot.head_dim, "q_out") != hq:
-        raise ValueError("q_out has the shape of q")
-    hk = _rows(k, tokens, dtype, device, rot.head_dim, "k")
-    v_dim = 0 if v is None else v.shape[2]
-    if v is not None and _rows(v, tokens, dtype, device, v_dim, "v") != hk:
-        raise ValueError("v has the heads of k")
-    if (v is None) != (v_cache is None):
-        raise ValueError("v and v_cache go together")
-    for c, dim in ((k_cache, rot.head_dim), (v_cache, v_dim)):
-        if c is None:
-            continue
-        if c.dtype != dtype or c.device != device:
-            raise TypeError("the caches must have the dtype and device of the other tensors")
-        if c.dim() != 4 or c.shape[:2] != k_cache.shape[:2] or c.shape[2] != hk or c.shape[3] != dim or c.stride(3) != 1:
-            raise ValueError("the caches are [pages, page_size, heads, dim], the last dimension contiguous")
-    with _on_device(device):
-        st = load().fi_rotary_append(
-            ctypes.byref(rot), positions.data_ptr(), slots.data_ptr(), tokens, *_ptr(q), *_ptr(q_out), hq, *_ptr(k),
-            *_ptr(v), v_dim, hk, k_cache.data_ptr(), _Strides(*k_cache.stride()[:3]),
-            v_cache.data_ptr() if v_cache is not None else None,
-            _Strides(*v_cache.stride()[:3]) if v_cache is not None else None, k_cache.shape[1], k_cache.shape[0],
-            _DTYPE[dtype], _stream_ptr(stream))
-    _check(st, "fi_rotary_append")
+    hq, *q_rows = _rows(q, q_out, tokens, dim, dtype, index, "q")
+    k_shape, cache = k.shape, k_cache.shape
+    kt, kh, kd = k.stride()
+    kcp, kcs, kch, kcd = k_cache.stride()
+    if len(k_shape) != 3 or k_shape[0] != tokens or k_shape[2] != dim or kd != 1:
+        raise ValueError(f"k is [tokens, heads, {dim}], the last dimension contiguous")
+    hk = k_shape[1]
+    if k_cache.dtype is not dtype or k_cache.get_device() != index:
+        raise TypeError("the caches must have the dtype and device of the other tensors")
+    pages, page_size = cache[0], cache[1]
+    if cache[2] != hk or cache[3] != dim or kcd != 1:
+        raise ValueError("k_cache is [pages, page_size, heads of k, head_dim], the last dimension contiguous")
+    if v is None or v_cache is None:
+        if v is not v_cache:
+            raise ValueError("v and v_cache go together")
+        v_dim = vt = vh = vcp = vcs = vch = v_ptr = vc_ptr = 0
+    else:
+        if v.dtype is not dtype or v_cache.dtype is not dtype or v.get_device() != index or \
+                v_cache.get_device() != index:
+            raise TypeError("v and v_cache must have the dtype and device of the other tensors")
+        v_dim = v.shape[-1]
+        vt, vh, vd = v.stride()
+        vcp, vcs, vch, vcd = v_cache.stride()
+        if v.shape != (tokens, hk, v_dim) or v_cache.shape != (pages, page_size, hk, v_dim) or vd != 1 or vcd != 1:
+            raise ValueError("v is [tokens, heads of k, v_dim] and v_cache [pages, page_size, heads, v_dim], the last "
+                             "dimension contiguous")
+        v_ptr, vc_ptr = v.data_ptr(), v_cache.data_ptr()
+    _call(_append, _APPEND_ARGS.pack(ctypes.addressof(rot), positions.data_ptr(), slots.data_ptr(), tokens, *q_rows, hq,
+                                     k.data_ptr(), kt, kh, v_ptr, vt, vh, v_dim, hk, k_cache.data_ptr(), kcp, kcs, kch,
+                                     vc_ptr, vcp, vcs, vch, page_size, pages, code),
+          index, stream, "fi_rotary_append")
 
 
 # ------------------------------------------------------------------ tables
@@ -175,29 +185,32 @@ def build_tables(tables: StepTables, qo_lens: torch.Tensor, kv_lens: torch.Tenso
     """Give out the step's new pages and fill `tables`, on the GPU (no host read).
     block_table int32 [batch, width] (rows may be strided) is updated in place;
     free_head int32 [1] is not: the next step's is counts[3:4]."""
-    device = qo_lens.device
-    batch = _index(qo_lens, device, "qo_lens")
-    if _index(kv_lens, device, "kv_lens") != batch:
+    if _tables is None:
+        load()
+    index = qo_lens.get_device()
+    batch = _index(qo_lens, index, "qo_lens")
+    if _index(kv_lens, index, "kv_lens") != batch:
         raise ValueError("qo_lens and kv_lens have one entry per request")
-    if batch > tables.max_batch:
-        raise ValueError("more requests than the tables hold")
-    if tables.counts.device != device:
-        raise TypeError("the tables must be on the lengths' device")
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.device != device or \
-            block_table.shape[0] < batch or block_table.stride(1) != 1:
-        raise TypeError("block_table is an int32 [batch, width] tensor, rows contiguous")
-    if (free_pages is None) != (free_head is None):
-        raise ValueError("free_pages and free_head go together")
-    num_free = 0 if free_pages is None else _index(free_pages, device, "free_pages")
-    if free_head is not None and _index(free_head, device, "free_head") != 1:
-        raise ValueError("free_head has one entry")
     t = tables
-    with _on_device(device):
-        st = load().fi_build_step_tables(
-            qo_lens.data_ptr(), kv_lens.data_ptr(), batch, page_size, block_table.data_ptr(), block_table.stride(0),
-            block_table.shape[1], free_pages.data_ptr() if num_free else None, num_free,
-            free_head.data_ptr() if free_head is not None else None, t.qo_indptr.data_ptr(), t.kv_indptr.data_ptr(),
-            t.last_page_len.data_ptr(), t.kv_indices.data_ptr() if t.max_pages else None, t.max_pages,
-            t.positions.data_ptr() if t.max_tokens else None, t.slots.data_ptr() if t.max_tokens else None,
-            t.max_tokens, t.counts.data_ptr(), _stream_ptr(stream))
-    _check(st, "fi_build_step_tables")
+    if batch > t.max_batch:
+        raise ValueError("more requests than the tables hold")
+    rows, width = block_table.shape
+    row_stride, one = block_table.stride()
+    if block_table.dtype is not torch.int32 or block_table.get_device() != index or rows < batch or one != 1:
+        raise TypeError("block_table is an int32 [batch, width] tensor on the lengths' device, rows contiguous")
+    if t.counts.get_device() != index:
+        raise TypeError("the tables must be on the lengths' device")
+    num_free = pages_ptr = head_ptr = 0
+    if free_pages is not None and free_head is not None:
+        num_free, pages_ptr, head_ptr = _index(free_pages, index, "free_pages"), free_pages.data_ptr(), \
+            free_head.data_ptr()
+        if _index(free_head, index, "free_head") != 1:
+            raise ValueError("free_head has one entry")
+    elif free_pages is not free_head:
+        raise ValueError("free_pages and free_head go together")
+    _call(_tables, _TABLE_ARGS.pack(qo_lens.data_ptr(), kv_lens.data_ptr(), batch, page_size, block_table.data_ptr(),
+                                    row_stride if rows > 1 else max(row_stride, width), width, pages_ptr, num_free,
+                                    head_ptr, t.qo_indptr.data_ptr(), t.kv_indptr.data_ptr(),
+                                    t.last_page_len.data_ptr(), t.kv_indices.data_ptr(), t.max_pages,
+                                    t.positions.data_ptr(), t.slots.data_ptr(), t.max_tokens, t.counts.data_ptr()),
+          index, stream, "fi_build_step_tables")

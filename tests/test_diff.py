@@ -108,34 +108,35 @@ def test_cascade_refuses_differential():
     assert fi.plan_cascade_host(cfg, *one, 16, *one, 8, 2, 128, 16, 0)[0] == 2
 
 
-def _args(**kw):
+def _run(**kw):
+    """The status of a call whose pointers are fake: every case returns before any CUDA call."""
     info = fi.PlanInfo(num_ctas=1, head_dim=128, page_size=16, num_qo_heads=8, num_kv_heads=2, variant=8)
-    ks = (ctypes.c_int64 * 3)(4096, 256, 128)
-    # the pointers are fake: every case returns before any CUDA call
-    a = dict(info=ctypes.byref(info), q=16, qt=1024, qh=128, n=4, k=32, ks=ks, v=64, vs=ks, pages=10, idx=48, lam=80,
-             w=96, eps=1e-5, scale=1.0, o=112, ot=1024, oh=128, lse=128, dt=fi.BF16, sm=0.1, iws=144, fws=160, s=None)
-    a.update(kw)
-    return info, list(a.values())
+    a = dict(info=ctypes.addressof(info), q=16, qt=1024, qh=128, n=4, k=32, k0=4096, k1=256, k2=128, v=64, v0=4096,
+             v1=256, v2=128, pages=10, idx=48, lam=80, w=96, o=112, ot=1024, oh=128, lse=128, dt=fi.BF16, iws=144,
+             fws=160, sm=0.1, eps=1e-5, scale=1.0, reserved=0.0)
+    for name, value in kw.items():
+        if name in a:
+            a[name] = value
+        else:
+            setattr(info, name, value)
+    lib = differential.load()
+    return lib.fi_batch_paged_attention_run_differential(differential._ARGS.pack(*a.values()), None)
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(info=None), 1), (dict(q=None), 1), (dict(lam=None), 1), (dict(iws=None), 1), (dict(k=None), 1),
-    (dict(idx=None), 1), (dict(pages=0), 1), (dict(n=0), 1), (dict(sm=float("nan")), 1),
-    (dict(scale=float("inf")), 1), (dict(eps=-1.0), 1), (dict(eps=float("nan")), 1), (dict(dt=fi.FP32), 2),
-    (dict(q=18), 4), (dict(o=120), 4), (dict(lam=82), 4), (dict(lse=130), 4), (dict(qt=1020), 4), (dict(oh=0), 4),
-    (dict(ks=(ctypes.c_int64 * 3)(4096, 250, 128)), 4), (dict(vs=(ctypes.c_int64 * 3)(4096, 256, -128)), 4)])
+    (dict(info=0), 1), (dict(q=0), 1), (dict(o=0), 1), (dict(lam=0), 1), (dict(iws=0), 1), (dict(k=0), 1),
+    (dict(v=0), 1), (dict(idx=0), 1), (dict(pages=0), 1), (dict(pages=1 << 31), 1), (dict(n=0), 1),
+    (dict(sm=float("nan")), 1), (dict(scale=float("inf")), 1), (dict(eps=-1.0), 1), (dict(eps=float("nan")), 1),
+    (dict(dt=fi.FP32), 2), (dict(q=18), 4), (dict(o=120), 4), (dict(lam=82), 4), (dict(lse=130), 4),
+    (dict(qt=1020), 4), (dict(oh=0), 4), (dict(k1=250), 4), (dict(v2=-128), 4),
+    (dict(variant=0), 1), (dict(variant=4), 1), (dict(num_ctas=0), 1), (dict(head_dim=64), 2),
+    (dict(page_size=24), 2), (dict(num_kv_heads=3), 2), (dict(fws=0, num_partial_rows=4), 1)])
 def test_run_refusals(kw, status):
-    _, args = _args(**kw)
-    assert differential.load().fi_batch_paged_attention_run_differential(*args) == status
+    assert _run(**kw) == status
 
 
-@pytest.mark.parametrize("field,value,status", [("variant", 0, 1), ("variant", 4, 1), ("num_ctas", 0, 1),
-                                                ("head_dim", 64, 2), ("page_size", 24, 2), ("num_kv_heads", 3, 2)])
-def test_run_refuses_other_plans(field, value, status):
-    info, args = _args()
-    setattr(info, field, value)
-    args[0] = ctypes.byref(info)
-    assert differential.load().fi_batch_paged_attention_run_differential(*args) == status
+def test_run_refuses_no_arguments():
+    assert differential.load().fi_batch_paged_attention_run_differential(None, None) == 1
 
 
 def test_ordinary_run_refuses_a_differential_plan():
@@ -145,21 +146,32 @@ def test_ordinary_run_refuses_a_differential_plan():
                                                   1024, 128, None, fi.BF16, 0.1, 96, 112, None) == 1
 
 
-def test_split_plan_needs_the_float_workspace():
-    info, args = _args(fws=None)
-    info.num_partial_rows = 4
-    args[0] = ctypes.byref(info)
-    assert differential.load().fi_batch_paged_attention_run_differential(*args) == 1
-
-
 def test_binding_refuses_cpu_tensors():
     class Ws:
-        int_ws = torch.zeros(4, dtype=torch.int32)
+        int_ws, float_ws = torch.zeros(4, dtype=torch.int32), torch.zeros(4)
+
     info = fi.PlanInfo(num_ctas=1, head_dim=128, page_size=16, num_qo_heads=2, num_kv_heads=1, variant=8)
     q = torch.zeros(1, 2, 128, dtype=torch.float16)
     c = torch.zeros(1, 16, 1, 128, dtype=torch.float16)
+    idx, lam = torch.zeros(1, dtype=torch.int32), torch.zeros(2)
     with pytest.raises(TypeError):
-        differential.run(Ws(), info, q, c, c, torch.zeros(1, dtype=torch.int32), torch.zeros(2), q, None, 0.1)
+        differential.run(Ws(), info, q, c, c, idx, lam, q, None, 0.1)
+    with pytest.raises(TypeError):
+        differential.run(Ws(), info, q, c.bfloat16(), c, idx, lam, q, None, 0.1)
+    with pytest.raises(TypeError):
+        differential.run(Ws(), info, q, c, c, idx.long(), lam, q, None, 0.1)
+    with pytest.raises(TypeError):
+        differential.run(Ws(), info, q, c, c, idx, lam.half(), q, None, 0.1)
+    with pytest.raises(ValueError):
+        differential.run(Ws(), info, q[:, :1], c, c, idx, lam, q, None, 0.1)
+    with pytest.raises(ValueError):
+        differential.run(Ws(), info, q, c[:, :8], c, idx, lam, q, None, 0.1)
+    with pytest.raises(ValueError):
+        differential.run(Ws(), info, q, c, c, idx, torch.zeros(3), q, None, 0.1)
+    with pytest.raises(ValueError):
+        differential.run(Ws(), info, q, c, c, idx, lam, q, torch.zeros(1, 2), 0.1)
+    with pytest.raises(ValueError):
+        differential.run(Ws(), info, q, c, c, idx, lam, q, None, 0.1, norm_weight=torch.ones(64))
 
 
 def test_every_entry_is_declared():

@@ -8,6 +8,7 @@ import re
 
 import numpy as np
 import pytest
+import torch
 
 import serving_attention_gb300 as fi
 from oracle import step as oracle_step
@@ -64,55 +65,101 @@ def test_setup_refuses_unknown_scaling():
     assert step.load().fi_rotary_setup(ctypes.byref(cfg), ctypes.byref(step.Rotary())) == 1
 
 
+# The pointers are fake: every case returns before any CUDA call.
 def _apply(**kw):
     rot = step.rotary_setup(128)
-    a = dict(rot=ctypes.byref(rot), pos=16, n=4, q=32, qt=1024, qh=128, qo=48, qot=1024, qoh=128, hq=8, k=64, kt=256,
-             kh=128, ko=80, kot=256, koh=128, hk=2, dt=fi.BF16, s=None)
+    a = dict(rot=ctypes.addressof(rot), pos=16, n=4, q=32, qt=1024, qh=128, qo=48, qot=1024, qoh=128, hq=8, k=64, kt=256,
+             kh=128, ko=80, kot=256, koh=128, hk=2, dt=fi.BF16)
     a.update(kw)
-    return step.load().fi_rotary_apply(*a.values())
+    return step.load().fi_rotary_apply(step._APPLY_ARGS.pack(*a.values()), None)
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(rot=None), 1), (dict(pos=None), 1), (dict(n=-1), 1), (dict(q=None), 1), (dict(qo=None), 1), (dict(k=None), 1),
-    (dict(hq=-1), 1), (dict(dt=fi.FP32), 2), (dict(q=34), 4), (dict(qo=40), 4), (dict(k=72), 4), (dict(qt=1020), 4),
-    (dict(koh=-128), 4), (dict(pos=18), 4), (dict(n=0), 0), (dict(hq=0, hk=0), 0)])
+    (dict(rot=0), 1), (dict(pos=0), 1), (dict(n=-1), 1), (dict(n=1 << 31), 1), (dict(q=0), 1), (dict(qo=0), 1),
+    (dict(k=0), 1), (dict(hq=-1), 1), (dict(dt=fi.FP32), 2), (dict(q=34), 4), (dict(qo=40), 4), (dict(k=72), 4),
+    (dict(qt=1020), 4), (dict(koh=-128), 4), (dict(pos=18), 4), (dict(n=0), 0), (dict(hq=0, hk=0), 0)])
 def test_apply_refusals(kw, status):
     assert _apply(**kw) == status
 
 
 def _append(**kw):
     rot = step.rotary_setup(128)
-    ks = (ctypes.c_int64 * 3)(4096, 256, 128)
-    a = dict(rot=ctypes.byref(rot), pos=16, slots=16, n=4, q=32, qt=1024, qh=128, qo=48, qot=1024, qoh=128, hq=8, k=64,
-             kt=256, kh=128, v=96, vt=256, vh=128, vd=128, hk=2, kc=112, ks=ks, vc=128, vs=ks, page=16, pages=9,
-             dt=fi.FP16, s=None)
+    a = dict(rot=ctypes.addressof(rot), pos=16, slots=16, n=4, q=32, qt=1024, qh=128, qo=48, qot=1024, qoh=128, hq=8,
+             k=64, kt=256, kh=128, v=96, vt=256, vh=128, vd=128, hk=2, kc=112, k0=4096, k1=256, k2=128, vc=128,
+             v0=4096, v1=256, v2=128, page=16, pages=9, dt=fi.FP16)
     a.update(kw)
-    return step.load().fi_rotary_append(*a.values())
+    return step.load().fi_rotary_append(step._APPEND_ARGS.pack(*a.values()), None)
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(slots=None), 1), (dict(kc=None), 1), (dict(ks=None), 1), (dict(v=None), 1), (dict(vc=None), 1),
-    (dict(hk=0), 1), (dict(pages=0), 1), (dict(vd=520), 2), (dict(vd=12), 2), (dict(page=24), 2), (dict(page=256), 2),
-    (dict(dt=fi.FP32), 2), (dict(kc=120), 4), (dict(vc=136), 4), (dict(slots=18), 4),
-    (dict(vs=(ctypes.c_int64 * 3)(4096, 250, 128)), 4), (dict(n=0), 0)])
+    (dict(slots=0), 1), (dict(kc=0), 1), (dict(k=0), 1), (dict(v=0), 1), (dict(vc=0), 1), (dict(hk=0), 1),
+    (dict(pages=0), 1), (dict(pages=1 << 31), 1), (dict(vd=520), 2), (dict(vd=12), 2), (dict(page=24), 2),
+    (dict(page=256), 2), (dict(dt=fi.FP32), 2), (dict(kc=120), 4), (dict(vc=136), 4), (dict(slots=18), 4),
+    (dict(v1=250), 4), (dict(k0=-8), 4), (dict(n=0), 0)])
 def test_append_refusals(kw, status):
     assert _append(**kw) == status
 
 
 def _tables(**kw):
     a = dict(q=16, kv=32, batch=4, page=16, table=48, stride=8, width=8, free=64, num_free=9, head=80, qp=96, kp=112,
-             last=128, idx=144, max_pages=9, pos=160, slots=176, max_tokens=9, counts=192, s=None)
+             last=128, idx=144, max_pages=9, pos=160, slots=176, max_tokens=9, counts=192)
     a.update(kw)
-    return step.load().fi_build_step_tables(*a.values())
+    return step.load().fi_build_step_tables(step._TABLE_ARGS.pack(*a.values()), None)
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(q=None), 1), (dict(table=None), 1), (dict(counts=None), 1), (dict(batch=0), 1), (dict(width=0), 1),
-    (dict(stride=7), 1), (dict(free=None), 1), (dict(head=None), 1), (dict(num_free=-1), 1), (dict(idx=None), 1),
-    (dict(slots=None), 1), (dict(max_tokens=-1), 1), (dict(head=200), 1), (dict(batch=8193), 2), (dict(page=12), 2),
-    (dict(page=256), 2), (dict(pos=162), 4)])
+    (dict(q=0), 1), (dict(table=0), 1), (dict(counts=0), 1), (dict(batch=0), 1), (dict(width=0), 1),
+    (dict(stride=7), 1), (dict(free=0), 1), (dict(head=0), 1), (dict(num_free=-1), 1), (dict(idx=0), 1),
+    (dict(slots=0), 1), (dict(max_tokens=-1), 1), (dict(max_pages=1 << 31), 1), (dict(head=200), 1),
+    (dict(batch=8193), 2), (dict(page=12), 2), (dict(page=256), 2), (dict(pos=162), 4)])
 def test_tables_refusals(kw, status):
     assert _tables(**kw) == status
+
+
+def test_calls_refuse_no_arguments():
+    lib = step.load()
+    assert lib.fi_rotary_apply(None, None) == lib.fi_rotary_append(None, None) == 1
+    assert lib.fi_build_step_tables(None, None) == 1
+
+
+def test_bindings_refuse_wrong_tensors():
+    rot = step.rotary_setup(64)
+    q, pos, slots = torch.zeros(3, 2, 64).half(), torch.zeros(3, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
+    cache = torch.zeros(2, 16, 2, 64).half()
+    with pytest.raises(TypeError):  # not on a GPU
+        step.rotate(rot, pos, q, q)
+    with pytest.raises(TypeError):
+        step.append(rot, pos, slots, q, q, q, q, cache, cache)
+    with pytest.raises(ValueError):
+        step.rotate(rot, pos, None, None)
+    with pytest.raises(ValueError):
+        step.rotate(rot, pos, q, None)
+    with pytest.raises(ValueError):
+        step.rotate(rot, pos, q[..., :32], q[..., :32])
+    with pytest.raises(TypeError):
+        step.rotate(rot, pos.long(), q, q)
+    with pytest.raises(TypeError):
+        step.rotate(rot, pos, q, q.float())
+    with pytest.raises(TypeError):
+        step.rotate(rot, pos, q.double(), q.double())
+    with pytest.raises(ValueError):
+        step.append(rot, pos, slots[:2], q, q, q, q, cache, cache)
+    with pytest.raises(ValueError):
+        step.append(rot, pos, slots, q, q, q, None, cache, cache)
+    with pytest.raises(ValueError):
+        step.append(rot, pos, slots, q, q, q[:, :1], q[:, :1], cache, cache)
+    t = step.StepTables(2, 4, 4, "cpu")
+    lens, table = torch.ones(2, dtype=torch.int32), torch.zeros(2, 3, dtype=torch.int32)
+    with pytest.raises(TypeError):
+        step.build_tables(t, lens, lens, table, 16)
+    with pytest.raises(ValueError):
+        step.build_tables(t, lens, lens[:1], table, 16)
+    with pytest.raises(ValueError):
+        step.build_tables(step.StepTables(1, 4, 4, "cpu"), lens, lens, table, 16)
+    with pytest.raises(ValueError):
+        step.build_tables(t, lens, lens, table, 16, lens, None)
+    with pytest.raises(TypeError):
+        step.build_tables(t, lens, lens, table.t(), 16)
 
 
 def test_every_entry_is_declared():
