@@ -8,8 +8,10 @@
 // 1 (an fp32 product of position and rate is off by 0.06 rad there).
 //
 // Bound by the bytes of q, k and v (each read and written once).  One warp per
-// token, or per part of one when there are few tokens: a lane computes the cos
-// and sin of its pairs once, and uses them for every head.
+// token, or per part of one when there are few tokens.  A lane keeps to one
+// place of a head (8 pairs, or a 16-byte piece that is copied), so its cos and
+// sin stay in registers while it goes from head to head; the values of the
+// first heads and of v are loaded before the angles are computed.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -23,7 +25,8 @@ namespace fi {
 namespace {
 
 constexpr int kRotaryWarps = 8;  // warps of a block
-constexpr int kRotaryAhead = 4;  // 16-byte loads a lane has in flight per operand
+constexpr int kRotaryAhead = 2;  // heads a lane has in flight
+constexpr int kValueAhead = 4;   // 16-byte pieces of v a lane has in flight
 
 struct RotaryRows {  // rows of one operand: token t (or cache slot), head h
   const uint16_t* in;
@@ -58,10 +61,11 @@ __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
                     Elem<T>::from_float2(f[4], f[5]), Elem<T>::from_float2(f[6], f[7]));
 }
 
-// A task is 16 bytes of one head (interleaved pairs, or a part that is copied)
-// or the two 16-byte chunks that hold 8 pairs (half layout).
+// The place of a lane: the two 16-byte pieces that hold 8 pairs (half layout),
+// or one that holds 4 (interleaved), or one behind the rotated dims; 32 /
+// places heads at a time.
 template <typename T, bool kInterleaved>
-__global__ void __launch_bounds__(32 * kRotaryWarps) rotary_kernel(const __grid_constant__ RotaryParams a) {
+__global__ void __launch_bounds__(32 * kRotaryWarps, 3) rotary_kernel(const __grid_constant__ RotaryParams a) {
   __shared__ float2 s_cs[kRotaryWarps][FI_ROTARY_MAX_PAIRS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t w = int64_t(blockIdx.x) * kRotaryWarps + warp;
@@ -69,6 +73,46 @@ __global__ void __launch_bounds__(32 * kRotaryWarps) rotary_kernel(const __grid_
   if (t >= a.num_tokens) return;
   const int32_t pos = __ldg(a.positions + t);
   const int64_t slot = a.slots ? __ldg(a.slots + t) : t;
+
+  // this lane's place and first head (q heads, then k heads)
+  const int pair_places = kInterleaved ? a.rot_chunks : a.rot_chunks >> 1;
+  const int places = pair_places + a.head_chunks - a.rot_chunks;
+  const int at_once = 32 / places, h_off = lane / places, place = lane - h_off * places;
+  const bool pairs = place < pair_places, active = h_off < at_once;
+  const int off = 8 * (pairs ? place : place + a.rot_chunks - pair_places);
+  const int other = 8 * pair_places;  // from the first members of 8 pairs to the second
+  const int step = at_once * a.parts;
+  const uint16_t *q_in = a.q.in + t * a.q.in_tok + off, *k_in = a.k.in + t * a.k.in_tok + off;
+  const int heads = a.q.heads + a.k.heads;
+  uint4 lo[kRotaryAhead], hi[kRotaryAhead];
+  auto load = [&](int h0) {
+#pragma unroll
+    for (int u = 0; u < kRotaryAhead; ++u) {
+      const int h = h0 + u * step;
+      if (!active || h >= heads) continue;
+      const uint16_t* src = h < a.q.heads ? q_in + h * a.q.in_head : k_in + (h - a.q.heads) * a.k.in_head;
+      lo[u] = *reinterpret_cast<const uint4*>(src);
+      if (!kInterleaved && pairs) hi[u] = *reinterpret_cast<const uint4*>(src + other);
+    }
+  };
+  int h0 = part * at_once + h_off;
+  load(h0);
+  // v: 16-byte pieces, in order
+  const int v_tasks = a.v.heads * a.v_chunks, v_step = 32 * a.parts;
+  const uint16_t* v_in = a.v.in + t * a.v.in_tok;
+  uint4 vv[kValueAhead];
+  auto v_at = [&](int i, int64_t head, int64_t base) -> int64_t {
+    const int h = i / a.v_chunks;
+    return base + h * head + 8 * (i - h * a.v_chunks);
+  };
+  auto load_v = [&](int i0) {
+#pragma unroll
+    for (int u = 0; u < kValueAhead; ++u)
+      if (i0 + u * v_step < v_tasks) vv[u] = *reinterpret_cast<const uint4*>(v_in + v_at(i0 + u * v_step, a.v.in_head, 0));
+  };
+  int v0 = 32 * part + lane;
+  load_v(v0);
+
   float2* cs = s_cs[warp];
   for (int i = lane; i < a.rot_chunks * 4; i += 32) {
     const uint64_t turn = uint64_t(int64_t(pos)) * a.turns[i];  // modulo one turn
@@ -77,86 +121,63 @@ __global__ void __launch_bounds__(32 * kRotaryWarps) rotary_kernel(const __grid_
     cs[i] = make_float2(c * a.amplitude, sn * a.amplitude);
   }
   __syncwarp();
+  constexpr int kMine = kInterleaved ? 4 : 8;
+  float2 r[kMine];
+  if (pairs) {
+    const float4* mine = reinterpret_cast<const float4*>(cs + kMine * place);
+#pragma unroll
+    for (int e = 0; e < kMine / 2; ++e) {
+      const float4 x = mine[e];
+      r[2 * e] = make_float2(x.x, x.y);
+      r[2 * e + 1] = make_float2(x.z, x.w);
+    }
+  }
   const bool store_kv = !a.slots || (slot >= 0 && slot < a.num_slots);
   const int64_t page = a.slots ? slot >> a.log2_page : slot;
   const int64_t in_page = a.slots ? slot & ((int64_t(1) << a.log2_page) - 1) : 0;
-
-  const int pair_tasks = kInterleaved ? a.rot_chunks : a.rot_chunks >> 1;
-  const int per_head = pair_tasks + a.head_chunks - a.rot_chunks;
-  const int tasks = (a.q.heads + (store_kv ? a.k.heads : 0)) * per_head;
-  const int step = 32 * a.parts;
-  const uint16_t *q_in = a.q.in + t * a.q.in_tok, *k_in = a.k.in + t * a.k.in_tok;
-  uint16_t *q_out = a.q.out + t * a.q.out_tok, *k_out = a.k.out + page * a.k.out_tok + in_page * a.k.out_slot;
-  for (int i0 = 32 * part + lane; i0 < tasks; i0 += kRotaryAhead * step) {
-    uint4 lo[kRotaryAhead], hi[kRotaryAhead];
-    uint16_t* dst[kRotaryAhead];
-    int chunk[kRotaryAhead];
+  uint16_t* q_out = a.q.out + t * a.q.out_tok + off;
+  uint16_t* k_out = a.k.out + page * a.k.out_tok + in_page * a.k.out_slot + off;
+  for (; h0 < heads; h0 += kRotaryAhead * step) {
 #pragma unroll
     for (int u = 0; u < kRotaryAhead; ++u) {
-      const int i = i0 + u * step;
-      dst[u] = nullptr;
-      if (i < tasks) {
-        const int h = i / per_head, c = i - h * per_head;
-        const bool is_q = h < a.q.heads;
-        const uint16_t* src = is_q ? q_in + h * a.q.in_head : k_in + (h - a.q.heads) * a.k.in_head;
-        dst[u] = is_q ? q_out + h * a.q.out_head : k_out + (h - a.q.heads) * a.k.out_head;
-        chunk[u] = c < pair_tasks ? c : c + a.rot_chunks - pair_tasks;
-        lo[u] = *reinterpret_cast<const uint4*>(src + 8 * chunk[u]);
-        if (!kInterleaved && c < pair_tasks) hi[u] = *reinterpret_cast<const uint4*>(src + 8 * (c + pair_tasks));
-        dst[u] += 8 * chunk[u];
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kRotaryAhead; ++u) {
-      if (!dst[u]) continue;
-      if (chunk[u] < pair_tasks) {
+      const int h = h0 + u * step;
+      if (!active || h >= heads || (h >= a.q.heads && !store_kv)) continue;
+      uint16_t* dst = h < a.q.heads ? q_out + h * a.q.out_head : k_out + (h - a.q.heads) * a.k.out_head;
+      if (pairs) {
         float x[8];
         unpack<T>(lo[u], x);
         if (kInterleaved) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float2 r = cs[4 * chunk[u] + e];
             const float x0 = x[2 * e], x1 = x[2 * e + 1];
-            x[2 * e] = x0 * r.x - x1 * r.y;
-            x[2 * e + 1] = x1 * r.x + x0 * r.y;
+            x[2 * e] = x0 * r[e].x - x1 * r[e].y;
+            x[2 * e + 1] = x1 * r[e].x + x0 * r[e].y;
           }
         } else {
           float y[8];
           unpack<T>(hi[u], y);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float2 r = cs[8 * chunk[u] + e];
             const float x0 = x[e], x1 = y[e];
-            x[e] = x0 * r.x - x1 * r.y;
-            y[e] = x1 * r.x + x0 * r.y;
+            x[e] = x0 * r[e % kMine].x - x1 * r[e % kMine].y;
+            y[e] = x1 * r[e % kMine].x + x0 * r[e % kMine].y;
           }
-          *reinterpret_cast<uint4*>(dst[u] + 8 * pair_tasks) = pack<T>(y);
+          *reinterpret_cast<uint4*>(dst + other) = pack<T>(y);
         }
         lo[u] = pack<T>(x);
       }
-      *reinterpret_cast<uint4*>(dst[u]) = lo[u];
+      *reinterpret_cast<uint4*>(dst) = lo[u];
     }
+    load(h0 + kRotaryAhead * step);
   }
-  if (!store_kv || !a.v_chunks) return;
-  const int v_tasks = a.v.heads * a.v_chunks;
-  const uint16_t* v_in = a.v.in + t * a.v.in_tok;
-  uint16_t* v_out = a.v.out + page * a.v.out_tok + in_page * a.v.out_slot;
-  for (int i0 = 32 * part + lane; i0 < v_tasks; i0 += kRotaryAhead * step) {
-    uint4 x[kRotaryAhead];
-    uint16_t* dst[kRotaryAhead];
+  if (!store_kv) return;
+  const int64_t v_base = page * a.v.out_tok + in_page * a.v.out_slot;
+  for (; v0 < v_tasks; v0 += kValueAhead * v_step) {
 #pragma unroll
-    for (int u = 0; u < kRotaryAhead; ++u) {
-      const int i = i0 + u * step;
-      dst[u] = nullptr;
-      if (i < v_tasks) {
-        const int h = i / a.v_chunks, c = i - h * a.v_chunks;
-        x[u] = *reinterpret_cast<const uint4*>(v_in + h * a.v.in_head + 8 * c);
-        dst[u] = v_out + h * a.v.out_head + 8 * c;
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kRotaryAhead; ++u)
-      if (dst[u]) *reinterpret_cast<uint4*>(dst[u]) = x[u];
+    for (int u = 0; u < kValueAhead; ++u)
+      if (v0 + u * v_step < v_tasks)
+        *reinterpret_cast<uint4*>(a.v.out + v_at(v0 + u * v_step, a.v.out_head, v_base)) = vv[u];
+    load_v(v0 + kValueAhead * v_step);
   }
 }
 
@@ -167,12 +188,13 @@ cudaError_t launch_rotary(RotaryParams& a, const fi_rotary* rot, fi_dtype dtype,
   a.rot_chunks = rot->rot_dim / 8;
   a.amplitude = rot->amplitude;
   std::memcpy(a.turns, rot->turns, sizeof(uint64_t) * size_t(rot->rot_dim / 2));
-  // Few tokens: their tasks are spread over more warps, at least one task a lane
-  const int per_head = (rot->interleaved ? a.rot_chunks : a.rot_chunks / 2) + a.head_chunks - a.rot_chunks;
-  const int tasks = (a.q.heads + a.k.heads) * per_head, v_tasks = a.v.heads * a.v_chunks;
-  const int most = ((tasks > v_tasks ? tasks : v_tasks) + 31) / 32;
+  // Few tokens: a token's heads are spread over more warps, at least one head a lane
+  const int places = (rot->interleaved ? a.rot_chunks : a.rot_chunks / 2) + a.head_chunks - a.rot_chunks;
+  const int at_once = 32 / places, heads = a.q.heads + a.k.heads;
+  const int rot_parts = (heads + at_once - 1) / at_once, v_parts = (a.v.heads * a.v_chunks + 31) / 32;
+  const int most = rot_parts > v_parts ? rot_parts : v_parts;
   const int want = kPartWarps / a.num_tokens;
-  a.parts = want < 1 ? 1 : want > most ? (most > 0 ? most : 1) : want;
+  a.parts = want < 1 ? 1 : want > most ? most : want;
   const int64_t warps = int64_t(a.num_tokens) * a.parts;
   const unsigned blocks = unsigned((warps + kRotaryWarps - 1) / kRotaryWarps);
   const int threads = 32 * kRotaryWarps;
