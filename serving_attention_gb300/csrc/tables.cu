@@ -20,6 +20,7 @@ namespace {
 
 constexpr int kTableThreads = 512;
 constexpr int kTableWarps = kTableThreads / 32;
+constexpr int kTableAhead = 4;  // page-table entries a thread has in flight
 
 struct TableParams {
   const int32_t *qo_lens, *kv_lens;
@@ -41,12 +42,16 @@ struct Sums {
   int64_t qo, pages, taken;
 };
 
+// Shared arrays by request have a gap after every 8 entries: the threads that
+// sum 8 consecutive entries each would otherwise all meet in four banks.
+__host__ __device__ __forceinline__ int gap(int i) { return i + (i >> 3); }
+
 // The last entry of s[0 .. n] at or below x (s[0] <= x < s[n]).
 __device__ __forceinline__ int find(const int32_t* s, int n, int x) {
   int lo = 0, hi = n - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (s[mid] <= x)
+    if (s[gap(mid)] <= x)
       lo = mid;
     else
       hi = mid - 1;
@@ -57,7 +62,8 @@ __device__ __forceinline__ int find(const int32_t* s, int n, int x) {
 __global__ void __launch_bounds__(kTableThreads) step_tables_kernel(const __grid_constant__ TableParams a) {
   extern __shared__ int32_t smem[];
   const int B = a.batch, P = 1 << a.log2_page, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int32_t *s_qo = smem, *s_kv = smem + B + 1, *s_new = smem + 2 * (B + 1);
+  const int n_smem = gap(B) + 1;
+  int32_t *s_qo = smem, *s_kv = smem + n_smem, *s_new = smem + 2 * n_smem;
   __shared__ Sums s_warp[kTableWarps];
   __shared__ int s_bad;
   if (tid == 0) s_bad = 0;
@@ -65,22 +71,30 @@ __global__ void __launch_bounds__(kTableThreads) step_tables_kernel(const __grid
   const int32_t head = a.free_head ? __ldg(a.free_head) : 0;
   auto pages_of = [&](int32_t len) { return int32_t((int64_t(len) + P - 1) >> a.log2_page); };
 
-  // thread t sums requests [t * per, (t + 1) * per), then the threads are scanned
+  // The requests' counts, loaded side by side; then thread t sums requests
+  // [t * per, (t + 1) * per) and the threads are scanned.
+  bool bad = false;
+#pragma unroll 4
+  for (int b = tid; b < B; b += kTableThreads) {
+    int32_t q = __ldg(a.qo_lens + b), kv = __ldg(a.kv_lens + b);
+    if (q < 0 || q > kv || int64_t(kv) > (int64_t(a.table_width) << a.log2_page)) {
+      bad = true;
+      q = kv = 0;
+    }
+    s_qo[gap(b)] = q;
+    s_kv[gap(b)] = pages_of(kv);
+    s_new[gap(b)] = pages_of(kv) - pages_of(kv - q);
+  }
+  if (bad) s_bad = 1;
+  __syncthreads();
   const int per = (B + kTableThreads - 1) / kTableThreads;
   const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
   Sums mine{0, 0, 0};
-  bool bad = false;
   for (int b = b0; b < b1; ++b) {
-    const int32_t q = __ldg(a.qo_lens + b), kv = __ldg(a.kv_lens + b);
-    if (q < 0 || q > kv || int64_t(kv) > (int64_t(a.table_width) << a.log2_page)) {
-      bad = true;
-      continue;
-    }
-    mine.qo += q;
-    mine.pages += pages_of(kv);
-    mine.taken += pages_of(kv) - pages_of(kv - q);
+    mine.qo += s_qo[gap(b)];
+    mine.pages += s_kv[gap(b)];
+    mine.taken += s_new[gap(b)];
   }
-  if (bad) s_bad = 1;
   Sums inc = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -127,51 +141,64 @@ __global__ void __launch_bounds__(kTableThreads) step_tables_kernel(const __grid
     int32_t qo = int32_t(before.qo + inc.qo - mine.qo), kv = int32_t(before.pages + inc.pages - mine.pages),
             nw = int32_t(before.taken + inc.taken - mine.taken);
     for (int b = b0; b < b1; ++b) {
-      s_qo[b] = qo;
-      s_kv[b] = kv;
-      s_new[b] = nw;
-      const int32_t q = __ldg(a.qo_lens + b), len = __ldg(a.kv_lens + b);
-      if (blockIdx.x == 0) {
-        a.qo_indptr[b] = qo;
-        a.kv_indptr[b] = kv;
-        a.last_page_len[b] = len > 0 ? ((len - 1) & (P - 1)) + 1 : 0;
-      }
+      const int i = gap(b);
+      const int32_t q = s_qo[i], k = s_kv[i], n = s_new[i];
+      s_qo[i] = qo;
+      s_kv[i] = kv;
+      s_new[i] = nw;
       qo += q;
-      kv += pages_of(len);
-      nw += pages_of(len) - pages_of(len - q);
+      kv += k;
+      nw += n;
     }
     if (tid == 0) {
-      s_qo[B] = int32_t(total.qo);
-      s_kv[B] = int32_t(total.pages);
-      if (blockIdx.x == 0) {
-        a.qo_indptr[B] = int32_t(total.qo);
-        a.kv_indptr[B] = int32_t(total.pages);
-      }
+      s_qo[gap(B)] = int32_t(total.qo);
+      s_kv[gap(B)] = int32_t(total.pages);
+      s_new[gap(B)] = int32_t(total.taken);
     }
   }
   __syncthreads();
+  const int64_t threads = int64_t(gridDim.x) * kTableThreads, gtid = int64_t(blockIdx.x) * kTableThreads + tid;
+  for (int64_t b = gtid; b <= B; b += threads) {
+    a.qo_indptr[b] = s_qo[gap(int(b))];
+    a.kv_indptr[b] = s_kv[gap(int(b))];
+    if (b < B) {
+      const int32_t len = __ldg(a.kv_lens + b);
+      a.last_page_len[b] = len > 0 ? ((len - 1) & (P - 1)) + 1 : 0;
+    }
+  }
   // Page p of request b: in the table already, or the free list's (the blocks
   // that need a new page's id read the list, not one another's table writes).
-  auto page_id = [&](int b, int p, int had) {
-    return p < had ? a.table[b * a.table_stride + p] : __ldg(a.free_pages + head + s_new[b] + (p - had));
+  // had: the pages the request had before.
+  auto had_of = [&](int b) {
+    return (s_kv[gap(b + 1)] - s_kv[gap(b)]) - (s_new[gap(b + 1)] - s_new[gap(b)]);
   };
-  const int64_t threads = int64_t(gridDim.x) * kTableThreads, gtid = int64_t(blockIdx.x) * kTableThreads + tid;
-  // Four consecutive entries a thread: one search for the first of them.
-  for (int64_t e0 = 4 * gtid; e0 < total.pages; e0 += 4 * threads) {
-    int b = find(s_kv, B, int(e0));
-    int had = pages_of(__ldg(a.kv_lens + b) - __ldg(a.qo_lens + b));
-    const int n = int(min(int64_t(4), total.pages - e0));
-    for (int u = 0; u < n; ++u) {
-      const int e = int(e0) + u;
-      if (e >= s_kv[b + 1]) {
-        do ++b;
-        while (e >= s_kv[b + 1]);
-        had = pages_of(__ldg(a.kv_lens + b) - __ldg(a.qo_lens + b));
-      }
-      const int p = e - s_kv[b];
-      const int32_t id = page_id(b, p, had);
-      a.kv_indices[e] = id;
-      if (p >= had) a.table[b * a.table_stride + p] = id;
+  auto page_id = [&](int b, int p, int had) {
+    return p < had ? a.table[b * a.table_stride + p] : __ldg(a.free_pages + head + s_new[gap(b)] + (p - had));
+  };
+  // A warp takes 32 * kTableAhead entries in a row: one search for the first,
+  // a walk from there (short, but for requests without pages in between); the
+  // loads of all go out before the first is stored.
+  constexpr int kSpan = 32 * kTableAhead;
+  for (int64_t w0 = (gtid >> 5) * kSpan; w0 < total.pages; w0 += (threads >> 5) * kSpan) {
+    int32_t id[kTableAhead];
+    int32_t* slot[kTableAhead];  // of a new page in the table
+    int b = find(s_kv, B, int(w0));
+#pragma unroll
+    for (int u = 0; u < kTableAhead; ++u) {
+      const int64_t e = w0 + 32 * u + lane;
+      slot[u] = nullptr;
+      if (e >= total.pages) continue;
+      while (int(e) >= s_kv[gap(b + 1)]) ++b;
+      const int p = int(e) - s_kv[gap(b)], had = had_of(b);
+      id[u] = page_id(b, p, had);
+      if (p >= had) slot[u] = a.table + b * a.table_stride + p;
+    }
+#pragma unroll
+    for (int u = 0; u < kTableAhead; ++u) {
+      const int64_t e = w0 + 32 * u + lane;
+      if (e >= total.pages) continue;
+      a.kv_indices[e] = id[u];
+      if (slot[u]) *slot[u] = id[u];
     }
   }
   for (int64_t t = gtid; t < a.max_tokens; t += threads) {
@@ -179,7 +206,7 @@ __global__ void __launch_bounds__(kTableThreads) step_tables_kernel(const __grid
     if (t < total.qo) {
       const int b = find(s_qo, B, int(t));
       const int32_t old = __ldg(a.kv_lens + b) - __ldg(a.qo_lens + b);
-      pos = old + int32_t(t) - s_qo[b];
+      pos = old + int32_t(t) - s_qo[gap(b)];
       const int64_t at = int64_t(page_id(b, pos >> a.log2_page, pages_of(old))) * P + (pos & (P - 1));
       slot = at >= 0 && at <= INT_MAX ? int32_t(at) : -1;
     }
@@ -223,14 +250,14 @@ extern "C" fi_status fi_build_step_tables(const fi_step_tables_args* x, void* st
                 x->kv_indptr,     x->last_page_len,  x->kv_indices,     int32_t(x->max_pages),
                 x->positions,     x->slots,          int32_t(x->max_tokens), x->counts};
   while ((1 << a.log2_page) < P) ++a.log2_page;
-  const size_t smem = size_t(3) * (a.batch + 1) * 4;
+  const size_t smem = size_t(3) * (gap(a.batch) + 1) * 4;
   if (smem > 48 * 1024) {
     static bool configured[kMaxDevices] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return FI_ERR_CUDA;
     if (dev < 0 || dev >= kMaxDevices || !configured[dev]) {
       if (cudaFuncSetAttribute(step_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               3 * (FI_STEP_MAX_BATCH + 1) * 4) != cudaSuccess)
+                               3 * (gap(FI_STEP_MAX_BATCH) + 1) * 4) != cudaSuccess)
         return FI_ERR_CUDA;
       if (dev >= 0 && dev < kMaxDevices) configured[dev] = true;
     }
