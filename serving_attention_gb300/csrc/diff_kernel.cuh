@@ -365,12 +365,40 @@ __device__ __forceinline__ void diff_store_row(const DiffParams& dp, const float
     *reinterpret_cast<uint32_t*>(dst + 64 * h) = Elem<T>::from_float2(y[2 * h] * f[2 * h], y[2 * h + 1] * f[2 * h + 1]);
 }
 
-// One pass of an item's packed rows [prow0, prow0 + prows): the queries as
-// product operands, the item's stages, then the merge of the eight warps'
-// states and the output (or the fp32 partial states).
-template <typename T, bool kWide>
+// The queries of packed rows [prow0, prow0 + prows) of an item (at most 16) as
+// product operands of this thread: narrow (up to 8 rows) the pair of K16 step
+// e / 2 at offset 8 (e % 2), both maps in a row; wide the steps of this map's
+// 64 dims, rows g and g + 8 in turn.
+__device__ __forceinline__ void diff_load_q(const RunParams& p, const Item& item, int prow0, uint32_t (&qf)[16]) {
+  const int cw = (threadIdx.x >> 5) - kFirstConsumerWarp;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int prows = min(16, item.row1 - item.row0 - prow0);
+  const bool wide = prows > 8;
+  const uint16_t* src[2];
+  bool live[2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int r = wide ? g + 8 * x : g;
+    live[x] = r < prows;
+    const int row = item.row0 + prow0 + (live[x] ? r : 0), tq = row / p.group;
+    src[x] = p.q + int64_t(item.rq.qo_start + tq) * p.q_stride_tok +
+             int64_t(item.hk * p.group + (row - tq * p.group)) * p.q_stride_head + 2 * t + (wide ? 64 * (cw >> 2) : 0);
+  }
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const int x = wide ? e & 1 : 0;
+    const int dim = wide ? 16 * (e >> 2) + 8 * ((e >> 1) & 1) : 16 * (e >> 1) + 8 * (e & 1);
+    qf[e] = live[x] ? __ldg(reinterpret_cast<const uint32_t*>(src[x] + dim)) : 0u;
+  }
+}
+
+// One pass of an item's packed rows [prow0, prow0 + prows): the item's stages,
+// then the merge of the eight warps' states and the output (or the fp32
+// partial states).  ahead() loads what comes next, before the merge.
+template <typename T, bool kWide, typename Ahead>
 __device__ __forceinline__ uint32_t diff_pass(const DiffParams& dp, DiffSmem& sm, const Item& item, int prow0,
-                                              int prows, uint32_t it, int causal, const Variant& var) {
+                                              int prows, uint32_t it, int causal, const Variant& var,
+                                              const uint32_t (&qf)[16], Ahead ahead) {
   const RunParams& p = dp.run;
   DiffBufs& bufs = sm.dec;
   const int cw = (threadIdx.x >> 5) - kFirstConsumerWarp;
@@ -380,32 +408,16 @@ __device__ __forceinline__ uint32_t diff_pass(const DiffParams& dp, DiffSmem& sm
   const int nst = (item.kv1 - item.kv0 + kStageTokens - 1) >> kLog2StageTokens;
   const int map = kWide ? cw >> 2 : 0;
 
-  uint32_t qf[16];
   DiffRows rw;
-  {
-    const uint16_t* src[2];
-    bool live[2];
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int r = kWide ? g + 8 * x : g;  // packed row of tile row g + 8 x
-      live[x] = r < prows;
-      const int row = item.row0 + prow0 + (live[x] ? r : 0);
-      const int tq = row / G, head = item.hk * G + (row - tq * G);
-      src[x] = p.q + int64_t(rq.qo_start + tq) * p.q_stride_tok + int64_t(head) * p.q_stride_head + 2 * t;
-      const int pos = rq.kv_len - rq.qo_len + tq;
-      rw.lim[x] = live[x] ? min(causal ? pos : rq.kv_len - 1, item.kv1 - 1) : -1;
-      rw.lo[x] = window_low(var, pos);
-      rw.m[x] = -INFINITY;
-      rw.l[x] = 0.f;
-    }
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      // narrow: the pair of step e / 2 at offset 8 (e % 2), both maps in a row;
-      // wide: steps of 64 dims of this map, rows g and g + 8 in turn
-      const int x = kWide ? e & 1 : 0;
-      const int dim = kWide ? 64 * map + 16 * (e >> 2) + 8 * ((e >> 1) & 1) : 16 * (e >> 1) + 8 * (e & 1);
-      qf[e] = live[x] ? __ldg(reinterpret_cast<const uint32_t*>(src[x] + dim)) : 0u;
-    }
+  for (int x = 0; x < 2; ++x) {
+    const int r = kWide ? g + 8 * x : g;  // packed row of tile row g + 8 x
+    const bool live = r < prows;
+    const int pos = rq.kv_len - rq.qo_len + (item.row0 + prow0 + (live ? r : 0)) / G;
+    rw.lim[x] = live ? min(causal ? pos : rq.kv_len - 1, item.kv1 - 1) : -1;
+    rw.lo[x] = window_low(var, pos);
+    rw.m[x] = -INFINITY;
+    rw.l[x] = 0.f;
   }
   float o[16][4];
 #pragma unroll
@@ -428,6 +440,8 @@ __device__ __forceinline__ uint32_t diff_pass(const DiffParams& dp, DiffSmem& sm
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.empty[s]);
   }
+
+  ahead();
 
   // Merge of the warps' states, 64 dims at a time through shared memory.
   // Warp w finishes packed row w (and w + 8 of a wide tile).
@@ -512,16 +526,31 @@ __device__ __forceinline__ uint32_t diff_pass(const DiffParams& dp, DiffSmem& sm
 template <typename T>
 __device__ void diff_consume(const DiffParams& dp, DiffSmem& sm, int32_t item_begin, int32_t item_end,
                              int32_t off_items, int causal, const Variant& var) {
-  uint32_t it = 0;
+  // The next item's descriptor is loaded an item ahead, and the queries of the
+  // next pass before this one's states are merged.
+  uint32_t it = 0, qf[16];
+  if (item_begin >= item_end) return;
+  Item next = load_item(dp.run.iws, off_items, item_begin);
+  diff_load_q(dp.run, next, 0, qf);
   for (int32_t i = item_begin; i < item_end; ++i) {
-    const Item item = load_item(dp.run.iws, off_items, i);
+    const Item item = next;
+    if (i + 1 < item_end) next = load_item(dp.run.iws, off_items, i + 1);
     const int nrows = item.row1 - item.row0;
     for (int prow0 = 0; prow0 < nrows; prow0 += 16) {
       const int prows = min(16, nrows - prow0);
+      uint32_t qn[16];
+      auto ahead = [&] {
+        if (prow0 + 16 < nrows)
+          diff_load_q(dp.run, item, prow0 + 16, qn);
+        else if (i + 1 < item_end)
+          diff_load_q(dp.run, next, 0, qn);
+      };
       if (prows <= 8)
-        it = diff_pass<T, false>(dp, sm, item, prow0, prows, it, causal, var);
+        it = diff_pass<T, false>(dp, sm, item, prow0, prows, it, causal, var, qf, ahead);
       else
-        it = diff_pass<T, true>(dp, sm, item, prow0, prows, it, causal, var);
+        it = diff_pass<T, true>(dp, sm, item, prow0, prows, it, causal, var, qf, ahead);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) qf[e] = qn[e];
     }
   }
 }
@@ -647,6 +676,8 @@ __global__ void __launch_bounds__(kDiffThreads, 1) diff_attention_kernel(const _
   if (threadIdx.x == 0 && sm.abort) atomicOr(p.iws + FI_H_STATUS, sm.abort);
 }
 
+constexpr int kMergeAhead = 4;  // chunks whose partial outputs a warp has in flight
+
 // Merge of split units, launched behind the run: one warp per packed row, its
 // chunks' partial states of both maps in chunk order, then the row's output.
 // Counts come from the workspace, so a captured graph serves later plans.
@@ -668,34 +699,67 @@ __global__ void __launch_bounds__(256) diff_merge_kernel(const __grid_constant__
     const int4 u0 = __ldg(mu), u1 = __ldg(mu + 1);  // {b, hk, row0, row1}, {n, base, late, 0}
     const int pr = int(task % rows_max), nrows = u0.w - u0.z, n = u1.x;
     if (pr >= nrows) continue;
+    // Partial row of chunk c: row0[map] + c step.  Lane c holds chunk c's two
+    // log-sum-exps (32 at a time); the partial outputs are loaded kMergeAhead
+    // chunks ahead of their use.
+    const int64_t step = 2 * nrows, row0[2] = {int64_t(u1.y) + pr, int64_t(u1.y) + nrows + pr};
+    float M[2] = {-INFINITY, -INFINITY}, L[2] = {0.f, 0.f};
+    for (int c = lane; c < n; c += 32) {
+      M[0] = fmaxf(M[0], __ldcg(p.fws + row0[0] + c * step));
+      M[1] = fmaxf(M[1], __ldcg(p.fws + row0[1] + c * step));
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+      M[0] = fmaxf(M[0], __shfl_xor_sync(0xffffffffu, M[0], off));
+      M[1] = fmaxf(M[1], __shfl_xor_sync(0xffffffffu, M[1], off));
+    }
+    float2 a[2][2];
+#pragma unroll
+    for (int mp = 0; mp < 2; ++mp) a[mp][0] = a[mp][1] = make_float2(0.f, 0.f);
+    for (int c0 = 0; c0 < n; c0 += 32) {
+      float w[2];
+#pragma unroll
+      for (int mp = 0; mp < 2; ++mp) {
+        w[mp] = 0.f;
+        if (c0 + lane < n && M[mp] != -INFINITY)
+          w[mp] = ex2((__ldcg(p.fws + row0[mp] + (c0 + lane) * step) - M[mp]) * 1.4426950408889634f);
+        L[mp] += w[mp];
+      }
+      const int cn = min(32, n - c0);
+      for (int g = 0; g < cn; g += kMergeAhead) {
+        float2 v[kMergeAhead][2][2];
+#pragma unroll
+        for (int u = 0; u < kMergeAhead; ++u)
+#pragma unroll
+          for (int mp = 0; mp < 2; ++mp) {
+            const int64_t r = row0[mp] + min(c0 + g + u, n - 1) * step;
+            const float2* src = reinterpret_cast<const float2*>(p.fws + p.partial_o_offset + r * kHeadDim) + lane;
+            v[u][mp][0] = __ldcg(src);
+            v[u][mp][1] = __ldcg(src + 32);
+          }
+#pragma unroll
+        for (int u = 0; u < kMergeAhead; ++u)
+#pragma unroll
+          for (int mp = 0; mp < 2; ++mp) {
+            const float wu = __shfl_sync(0xffffffffu, w[mp], (g + u) & 31);
+            if (g + u < cn) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                a[mp][h].x += wu * v[u][mp][h].x;
+                a[mp][h].y += wu * v[u][mp][h].y;
+              }
+            }
+          }
+      }
+    }
     float2 s[2][2];
     float lse[2];
 #pragma unroll
     for (int mp = 0; mp < 2; ++mp) {
-      const int64_t row0 = int64_t(u1.y) + mp * nrows + pr, step = 2 * nrows;  // partial row of chunk c: row0 + c step
-      float M = -INFINITY;
-      for (int c = lane; c < n; c += 32) M = fmaxf(M, __ldcg(p.fws + row0 + c * step));
+      const float sum = warp_sum(L[mp]), inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-      float L = 0.f;
-      float2 a[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-      if (M != -INFINITY) {
-        for (int c = 0; c < n; ++c) {
-          const int64_t r = row0 + c * step;
-          const float w = ex2((__ldcg(p.fws + r) - M) * 1.4426950408889634f);
-          const float2* src = reinterpret_cast<const float2*>(p.fws + p.partial_o_offset + r * kHeadDim) + lane;
-          const float2 x = __ldcg(src), y = __ldcg(src + 32);
-          L += w;
-          a[0].x += w * x.x;
-          a[0].y += w * x.y;
-          a[1].x += w * y.x;
-          a[1].y += w * y.y;
-        }
-      }
-      const float inv = L > 0.f ? 1.f / L : 0.f;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) s[mp][h] = make_float2(a[h].x * inv, a[h].y * inv);
-      lse[mp] = L > 0.f ? M + __logf(L) : -INFINITY;
+      for (int h = 0; h < 2; ++h) s[mp][h] = make_float2(a[mp][h].x * inv, a[mp][h].y * inv);
+      lse[mp] = sum > 0.f ? M[mp] + __logf(sum) : -INFINITY;
     }
     const int row = u0.z + pr, tq = row / p.group, head = u0.y * p.group + (row - tq * p.group);
     const int64_t tok = int64_t(__ldg(reqs + FI_REQ_INTS * u0.x)) + tq;
