@@ -23,10 +23,11 @@
 // Roles: warp 0 loads Q (two buffers) and K, warp 2 V, by TMA; warp 1 issues
 // the products; warpgroups of warps 4..7, 8..11, 12..15 and 16..19 take 32
 // keys each of every 128-key tile, for both maps (thread = row =
-// tensor-memory lane).  Tensor memory: S of both maps (128 columns each), O
-// (128), two P buffers (64 each).  A thread takes its 64 logits into registers
+// tensor-memory lane).  Tensor memory: S of both maps (256 columns), O (128),
+// two P buffers (64 each); in pass 0, which needs neither O nor P, their
+// columns are a second S buffer.  A thread takes its 64 logits into registers
 // and gives S back, so the next tile's S runs while it computes; P has columns
-// of its own, so nothing waits for P V either.  Four softmax warps on each
+// of its own, so S does not wait for P V either.  Four softmax warps on each
 // scheduler: with two (64 keys each) a warp's waits, loads and stores were
 // not covered, and a step took twice its 1024 cycles of exponentials.
 #pragma once
@@ -61,8 +62,8 @@ struct DiffPrefillBufs {  // every [128][64] block is a 128-byte swizzled operan
 struct DiffPrefillBars {
   uint64_t q_full[2], q_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t v_clear[2];            // a tile's V rows past the request's end cleared
-  uint64_t s_full[2], s_free[2];  // [map]
-  uint64_t p_full[2][2];          // [buffer][key half]
+  uint64_t s_full[2], s_free[2];  // [S buffer]
+  uint64_t p_full[2];             // [buffer]
   uint64_t p_free[2];
   uint64_t o_ready, o_free, drain;
 };
@@ -92,8 +93,10 @@ __device__ void diff_pf_produce(const RunParams& p, DiffPrefillBufs& pf, DiffPre
   }
   uint32_t kt = 0, ni = 0;
   int armed[2] = {-1, -1}, q_armed[2] = {-1, -1};
+  Item ahead = load_item(p.iws, off_items, b0);
   for (int32_t i = b0; i < b1; ++i) {
-    const Item it = load_item(p.iws, off_items, i);
+    const Item it = ahead;
+    if (i + 1 < b1) ahead = load_item(p.iws, off_items, i + 1);
     const int ntiles = item_kv_tiles(it);
     if (ntiles == 0) continue;
     const int32_t* pages = kc.kv_indices + it.rq.page_start;
@@ -156,6 +159,32 @@ __device__ void diff_pf_produce(const RunParams& p, DiffPrefillBufs& pf, DiffPre
   __syncwarp();
 }
 
+// As warp_wait_all for up to four phases, but the warp keeps polling: the
+// wake-up of a sleeping wait is on the critical path of the products.
+__device__ __forceinline__ bool poll_wait(uint64_t* b0, uint32_t p0, uint64_t* b1, uint32_t p1, uint64_t* b2,
+                                          uint32_t p2, uint64_t* b3, uint32_t p3, volatile int* abort) {
+  const int lane = threadIdx.x & 31;
+  uint64_t* const bar = lane == 1 ? b1 : lane == 2 ? b2 : lane == 3 ? b3 : b0;
+  const uint32_t ph = lane == 1 ? p1 : lane == 2 ? p2 : lane == 3 ? p3 : p0;
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, ph))) return true;
+  const long long t0 = clock64();
+  while (true) {
+#pragma unroll 1
+    for (int k = 0; k < 64; ++k)
+      if (__all_sync(0xffffffffu, mbar_try_wait(bar, ph))) return true;
+    const int st = __shfl_sync(0xffffffffu, (*abort != 0 ? 2 : 0) | (clock64() - t0 > kWaitBudgetClocks ? 4 : 0), 0);
+    if (st & 2) return false;
+    if (st & 4) {
+      *abort = kStatusTimeout;
+      return false;
+    }
+  }
+}
+
+// The MMA warp's time goes into waits (some 300 cycles each, with the tensor
+// pipe using all of shared memory) as much as into products, so the blocks
+// are as large as they can be: 8 products of S behind one wait, 8 of P V
+// behind another.
 template <typename T>
 __device__ void diff_pf_mma(const RunParams& p, DiffPrefillBufs& pf, DiffPrefillBars& bar, volatile int* abort,
                             uint32_t tmem, int32_t b0, int32_t b1, int32_t off_items) {
@@ -168,47 +197,38 @@ __device__ void diff_pf_mma(const RunParams& p, DiffPrefillBufs& pf, DiffPrefill
   const uint64_t dq = tc::smem_desc_sw128(smem_u32(&pf.q[0][0][0][0]), 16, 1024);
   const uint64_t dk = tc::smem_desc_sw128(smem_u32(&pf.k[0][0][0][0]), 16, 1024);
   const uint64_t dv = tc::smem_desc_sw128(smem_u32(&pf.v[0][0][0][0]), 64 * kTileN * 2, 1024);
-  uint32_t kt = 0, vt = 0, ni = 0, no = 0;     // K tiles, V tiles, items, uses of O so far
-  uint32_t ns[2] = {0, 0}, np[2] = {0, 0};     // S products per map, uses of the P buffers
-  uint32_t cleared = 0;                        // bit st: parity of the cleared tails of V stage st
+  uint32_t kt = 0, vt = 0, ni = 0, no = 0;         // K tiles, V tiles, items, uses of O so far
+  uint32_t ns0 = 0, ns1 = 0, np0 = 0, np1 = 0;     // uses of the S and of the P buffers
+  uint32_t cleared = 0;                            // bit st: parity of the cleared tails of V stage st
   bool issued = false;
-  // The P V of a step, which follows the S of the next step.
-  struct Pv {
+  struct Pv {  // the P V of a step, which follows the S of the next step
     int kind, j;
     bool last, tail;
   } pv{0, 0, false, false};
   auto do_pv = [&]() -> bool {
     const int st = vt & 1, b = pv.kind == 1 ? pv.j & 1 : 0;
     const bool two = pv.kind != 1;  // hi in buffer 0, lo in buffer 1
-    uint64_t* const vb = pv.tail ? &bar.v_clear[st] : &bar.v_full[st];
-    const uint32_t vp = pv.tail ? (cleared >> st) & 1 : (vt >> 1) & 1;
+    uint64_t* const pb = &bar.p_full[b];
+    const uint32_t pp = (b ? np1 : np0) & 1;
+    if (!poll_wait(pb, pp, pv.tail ? &bar.v_clear[st] : &bar.v_full[st],
+                   pv.tail ? (cleared >> st) & 1 : (vt >> 1) & 1, pv.j == 0 ? &bar.o_free : pb,
+                   pv.j == 0 ? (no & 1) ^ 1 : pp, two ? &bar.p_full[1] : pb, two ? np1 & 1 : pp, abort))
+      return false;
+    tc::fence_after_sync();
     const uint64_t bv = dv + 2048u * st;
+    const uint32_t acol = tmem + kDiffTmemP + 64 * b;
 #pragma unroll
-    for (int wg = 0; wg < 2; ++wg) {  // the keys of two warpgroups
-      uint64_t* const pb = &bar.p_full[b][wg];
-      const uint32_t pp = np[b] & 1;
-      const bool first = wg == 0;
-      if (!warp_wait_all(4, pb, pp, two ? &bar.p_full[1][wg] : pb, two ? np[1] & 1 : pp, first ? vb : pb,
-                         first ? vp : pp, first && pv.j == 0 ? &bar.o_free : pb,
-                         first && pv.j == 0 ? (no & 1) ^ 1 : pp, abort))
-        return false;
-      tc::fence_after_sync();
+    for (int kk = 0; kk < 8; ++kk)  // P of keys 16 kk .. 16 kk + 15: columns 8 kk .. 8 kk + 7
+      tc::mma_ts_warp(tmem + kDiffTmemO, acol + 8 * kk, bv + 128u * kk, idesc_pv, (pv.j > 0 || kk > 0) ? 1u : 0u);
+    if (two) {
 #pragma unroll
-      for (int kk = 4 * wg; kk < 4 * wg + 4; ++kk)  // P of keys 16 kk .. 16 kk + 15: columns 8 kk .. 8 kk + 7
-        tc::mma_ts_warp(tmem + kDiffTmemO, tmem + kDiffTmemP + 64 * b + 8 * kk, bv + 128u * kk, idesc_pv,
-                        (pv.j > 0 || kk > 0) ? 1u : 0u);
-      if (two) {
-#pragma unroll
-        for (int kk = 4 * wg; kk < 4 * wg + 4; ++kk)
-          tc::mma_ts_warp(tmem + kDiffTmemO, tmem + kDiffTmemP + 64 + 8 * kk, bv + 128u * kk, idesc_pv, 1u);
-      }
+      for (int kk = 0; kk < 8; ++kk)
+        tc::mma_ts_warp(tmem + kDiffTmemO, acol + 64 + 8 * kk, bv + 128u * kk, idesc_pv, 1u);
     }
     tc::mma_commit_warp(&bar.p_free[b]);
-    ++np[b];
-    if (two) {
-      tc::mma_commit_warp(&bar.p_free[1]);
-      ++np[1];
-    }
+    if (two) tc::mma_commit_warp(&bar.p_free[1]);
+    np0 += two || b == 0;
+    np1 += two || b == 1;
     tc::mma_commit_warp(&bar.v_empty[st]);
     if (pv.last) {
       tc::mma_commit_warp(&bar.o_ready);
@@ -219,35 +239,40 @@ __device__ void diff_pf_mma(const RunParams& p, DiffPrefillBufs& pf, DiffPrefill
     return true;
   };
   bool ok = true;
+  Item next = load_item(p.iws, off_items, b0);
   for (int32_t i = b0; i < b1 && ok; ++i) {
-    const Item it = load_item(p.iws, off_items, i);
+    const Item it = next;
+    if (i + 1 < b1) next = load_item(p.iws, off_items, i + 1);
     const int ntiles = item_kv_tiles(it);
     if (ntiles == 0) continue;
     const bool tail = item_v_tail(it, p.kv[0].page_size);
     const int qb = ni & 1, last = last_pass(it);
+    const uint64_t a = dq + 2048u * qb;
     for (int kind = 0; kind <= last && ok; kind = kind == 0 ? first_pv_pass(it) : kind + 1) {
-      const bool s1 = kind != 3, s2 = kind != 2;
       for (int j = 0; j < ntiles && ok; ++j, ++kt) {
-        const int st = kt & 1;
+        const int st = kt & 1, x = kind == 0 ? j & 1 : 0;
         uint64_t* const kb = &bar.k_full[st];
         const uint32_t kp = (kt >> 1) & 1;
-        const bool q = kind == 0 && j == 0;
-        ok = warp_wait_all(4, kb, kp, q ? &bar.q_full[qb] : kb, q ? (ni >> 1) & 1 : kp, s1 ? &bar.s_free[0] : kb,
-                           s1 ? (ns[0] & 1) ^ 1 : kp, s2 ? &bar.s_free[1] : kb, s2 ? (ns[1] & 1) ^ 1 : kp, abort);
+        // the item's Q with its first S; O's and P's columns free (the item
+        // before read out) with its first S in the second buffer
+        uint64_t* const eb = kind != 0 || j > 1 ? kb : j == 0 ? &bar.q_full[qb] : &bar.o_free;
+        const uint32_t ep = kind != 0 || j > 1 ? kp : j == 0 ? (ni >> 1) & 1 : (no & 1) ^ 1;
+        ok = poll_wait(&bar.s_free[x], ((x ? ns1 : ns0) & 1) ^ 1, kb, kp, eb, ep, kb, kp, abort);
         if (!ok) break;
         tc::fence_after_sync();
-        const uint64_t a = dq + 2048u * qb, b = dk + 2048u * st;
+        const uint64_t b = dk + 2048u * st;
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
-          if (!(m == 0 ? s1 : s2)) continue;
+          if (kind == 3 - m) continue;  // kind 2: map 1 alone, kind 3: map 2 alone
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            tc::mma_ss_warp(tmem + m * kTileN, a + 1024u * m + 2u * kk, b + 1024u * m + 2u * kk, idesc_s,
-                            kk > 0 ? 1u : 0u);
-          tc::mma_commit_warp(&bar.s_full[m]);
-          ++ns[m];
+            tc::mma_ss_warp(tmem + 2 * kTileN * x + kTileN * m, a + 1024u * m + 2u * kk, b + 1024u * m + 2u * kk,
+                            idesc_s, kk > 0 ? 1u : 0u);
         }
+        tc::mma_commit_warp(&bar.s_full[x]);
         tc::mma_commit_warp(&bar.k_empty[st]);
+        ns0 += x == 0;
+        ns1 += x;
         issued = true;
         if (pv.kind) ok = do_pv();
         pv = {kind, j, j + 1 == ntiles, tail && j + 1 == ntiles};
@@ -296,8 +321,10 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
   const float2 cc = make_float2(sc, sc);
   uint32_t ns[2] = {0, 0}, np[2] = {0, 0}, no = 0, ni = 0;  // as in the MMA warp
   int q_held = -1;  // the Q buffer that this warpgroup's output store may still be reading
+  Item next = load_item(p.iws, off_items, b0);
   for (int32_t i = b0; i < b1; ++i) {
-    const Item item = load_item(p.iws, off_items, i);
+    const Item item = next;
+    if (i + 1 < b1) next = load_item(p.iws, off_items, i + 1);
     const Request& rq = item.rq;
     const int nrows = item.row1 - item.row0, ntiles = item_kv_tiles(item);
     const int row = item.row0 + r, tq = row / G, head = item.hk * G + (row - tq * G);
@@ -317,24 +344,22 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
       continue;
     }
     bool ok = true;
-    // This warpgroup's 32 logits a map of tile j (kinds 2 and 3: of one map),
-    // masked; S goes back to the MMA warp.  False: no row of the warp sees any.
-    auto load_s = [&](int j, bool m1, bool m2, uint32_t (&a)[32], uint32_t (&b)[32]) -> bool {
-      if (m1) ok = ok && warp_wait(&bar.s_full[0], ns[0] & 1, abort);
-      if (m2) ok = ok && warp_wait(&bar.s_full[1], ns[1] & 1, abort);
+    const float lam = live ? __ldg(dp.lambda + head) : 0.f;
+    // This warpgroup's 32 logits a map of tile j in S buffer x (kinds 2 and 3:
+    // of one map), masked; S goes back to the MMA warp.  False: no row of the
+    // warp sees any.
+    auto load_s = [&](int x, int j, bool m1, bool m2, uint32_t (&a)[32], uint32_t (&b)[32]) -> bool {
+      ok = ok && warp_wait(&bar.s_full[x], (x ? ns[1] : ns[0]) & 1, abort);
+      ns[0] += x == 0;
+      ns[1] += x;
       tc::fence_after_sync();
-      const uint32_t col = tl + kDiffKeys * wg;
+      const uint32_t col = tl + 2 * kTileN * x + kDiffKeys * wg;
       if (m1) tc::tmem_ld32(col, a);
       if (m2) tc::tmem_ld32(col + kTileN, b);
       tc::tmem_ld_wait();
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) {
-        if (m1) mbar_arrive(&bar.s_free[0]);
-        if (m2) mbar_arrive(&bar.s_free[1]);
-      }
-      ns[0] += m1;
-      ns[1] += m2;
+      if (lane == 0) mbar_arrive(&bar.s_free[x]);
       const int key0 = item.kv0 + j * kTileN + kDiffKeys * wg;
       if (key0 + kDiffKeys - 1 > lim || (kMask && key0 < lo)) {
 #pragma unroll
@@ -353,7 +378,7 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     for (int j = 0; j < ntiles && ok; ++j) {
       uint32_t s[2][32];
-      if (!load_s(j, true, true, s[0], s[1]) || !ok) continue;
+      if (!load_s(j & 1, j, true, true, s[0], s[1]) || !ok) continue;
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const float top = max32(s[x]) * sc;
@@ -407,7 +432,6 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
       // ---- pass 1: weights w_1 - lambda w_2, scaled by 2^sigma so that both
       // terms stay at or below 2^8 (the lazy maximum's slack) and the smallest
       // that matter inside an fp16's range
-      const float lam = live ? __ldg(dp.lambda + head) : 0.f;
       const float big = fabsf(lam) > 1.f ? __log2f(fabsf(lam)) : 0.f;
       const float sigma = fminf(log2l[0], log2l[1] - big);
       const float a1 = m[0] + log2l[0] - sigma, a2 = m[1] + log2l[1] - sigma;
@@ -415,7 +439,7 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
       for (int j = 0; j < ntiles && ok; ++j) {
         const int b = j & 1;
         uint32_t s1[32], s2[32], pk[16];
-        const bool any = load_s(j, true, true, s1, s2);
+        const bool any = load_s(0, j, true, true, s1, s2);
         if (any) {
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
@@ -435,7 +459,7 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
         tc::tmem_st_wait();
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.p_full[b][half]);
+        if (lane == 0) mbar_arrive(&bar.p_full[b]);
       }
       // ---- the output: this warpgroup's 32 dims of the row
       ok = ok && warp_wait(&bar.o_ready, no & 1, abort);
@@ -492,7 +516,7 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
         const float2 n = make_float2(-m[x], -m[x]);
         for (int j = 0; j < ntiles && ok; ++j) {
           uint32_t s[32], hi[16], low[16];
-          const bool any = load_s(j, x == 0, x == 1, s, s);
+          const bool any = load_s(0, j, x == 0, x == 1, s, s);
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const float2 y = fma2(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), cc, n);
@@ -512,8 +536,8 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
           tc::fence_before_sync();
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(&bar.p_full[0][half]);
-            mbar_arrive(&bar.p_full[1][half]);
+            mbar_arrive(&bar.p_full[0]);
+            mbar_arrive(&bar.p_full[1]);
           }
         }
         ok = ok && warp_wait(&bar.o_ready, no & 1, abort);
