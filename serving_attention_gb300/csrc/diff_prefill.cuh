@@ -42,6 +42,7 @@ constexpr int kDiffKeys = kTileN / kDiffGroups;        // keys of a tile, and di
 constexpr int kDiffSoftmaxThreads = 128 * kDiffGroups;
 constexpr int kDiffBarrier = 6;  // all softmax warpgroups (1: decode, 3: end of phase, 4 and 5: two warpgroups)
 constexpr int kDiffTmemO = 256, kDiffTmemP = 384;
+constexpr float kWeightScale = 13.f;  // softmax weights are multiplied by 2^13 before they are rounded
 // Register budgets, per thread (see kRegsLaunch): in the tensor-core phase
 // warps 0..3 and the softmax warpgroups, in the decode phase its consumers
 // (two warpgroups) and the other twelve warps.
@@ -321,19 +322,24 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
   const float2 cc = make_float2(sc, sc);
   uint32_t ns[2] = {0, 0}, np[2] = {0, 0}, no = 0, ni = 0;  // as in the MMA warp
   int q_held = -1;  // the Q buffer that this warpgroup's output store may still be reading
-  Item next = load_item(p.iws, off_items, b0);
   for (int32_t i = b0; i < b1; ++i) {
-    const Item item = next;
-    if (i + 1 < b1) next = load_item(p.iws, off_items, i + 1);
+    const Item item = load_item(p.iws, off_items, i);
     const Request& rq = item.rq;
     const int nrows = item.row1 - item.row0, ntiles = item_kv_tiles(item);
     const int row = item.row0 + r, tq = row / G, head = item.hk * G + (row - tq * G);
     const int64_t tok = int64_t(rq.qo_start) + tq;
     const int pos = rq.kv_len - rq.qo_len + tq;
-    // visible keys [lo, lim] and the sink (a padding row sees none)
-    const int lim = r < nrows ? min(causal ? pos : rq.kv_len - 1, item.kv1 - 1) : -1;
-    const int lo = kMask ? window_low(var, pos) : 0;
     const bool live = r < nrows;
+    // visible keys [lo, lim] and the sink (a padding row, never stored, sees
+    // all of the chunk, so that it does not make its warp mask every tile)
+    const int lim = live && causal ? min(pos, item.kv1 - 1) : item.kv1 - 1;
+    const int lo = kMask && live ? window_low(var, pos) : 0;
+    // tiles [c0, c1) need no mask for any row of the warp's keys; past c2 no
+    // row of the warp sees any
+    const int first = item.kv0 + kDiffKeys * wg;  // this warpgroup's first key
+    const int c1 = __reduce_min_sync(0xffffffffu, (lim + 1 - first - kDiffKeys + kTileN) >> 7);
+    const int c2 = __reduce_max_sync(0xffffffffu, (lim - first + kTileN) >> 7);
+    const int c0 = kMask ? (max(__reduce_max_sync(0xffffffffu, lo) - first, 0) + kTileN - 1) >> 7 : 0;
     uint16_t* out = p.o + tok * p.o_stride_tok + int64_t(head) * p.o_stride_head + kDiffKeys * wg;
     if (ntiles == 0) {  // no key: the output and log-sum-exps of an empty row
       if (live && item.part < 0) {
@@ -346,9 +352,8 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
     bool ok = true;
     const float lam = live ? __ldg(dp.lambda + head) : 0.f;
     // This warpgroup's 32 logits a map of tile j in S buffer x (kinds 2 and 3:
-    // of one map), masked; S goes back to the MMA warp.  False: no row of the
-    // warp sees any.
-    auto load_s = [&](int x, int j, bool m1, bool m2, uint32_t (&a)[32], uint32_t (&b)[32]) -> bool {
+    // of one map); S goes back to the MMA warp.
+    auto load_s = [&](int x, bool m1, bool m2, uint32_t (&a)[32], uint32_t (&b)[32]) {
       ok = ok && warp_wait(&bar.s_full[x], (x ? ns[1] : ns[0]) & 1, abort);
       ns[0] += x == 0;
       ns[1] += x;
@@ -360,25 +365,48 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.s_free[x]);
-      const int key0 = item.kv0 + j * kTileN + kDiffKeys * wg;
-      if (key0 + kDiffKeys - 1 > lim || (kMask && key0 < lo)) {
+    };
+    auto mask = [&](int j, uint32_t (&v)[32]) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const int key = key0 + e;
-          if (key > lim || (kMask && key < lo && key >= var.sink)) {
-            if (m1) a[e] = 0xff800000u;
-            if (m2) b[e] = 0xff800000u;
-          }
-        }
+      for (int e = 0; e < 32; ++e) {
+        const int key = first + j * kTileN + e;
+        if (key > lim || (kMask && key < lo && key >= var.sink)) v[e] = 0xff800000u;
       }
-      return __any_sync(0xffffffffu, key0 <= lim);
     };
 
-    // ---- pass 0: running maximum (log2 domain, moved lazily) and sum per map
+    // ---- pass 0: a reference m and the sum of 2^(s - m) per map.  The
+    // reference is the maximum of the first tile that the row sees; it only
+    // moves when a sum passes 2^100, so the loop has no maximum to take.
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    for (int j = 0; j < ntiles && ok; ++j) {
+    bool have_m = false;  // of every row of the warp
+    for (int j = 0; j < ntiles; ++j) {
       uint32_t s[2][32];
-      if (!load_s(j & 1, j, true, true, s[0], s[1]) || !ok) continue;
+      load_s(j & 1, true, true, s[0], s[1]);
+      if (j >= c2) continue;
+      if (j < c0 || j >= c1) {
+        mask(j, s[0]);
+        mask(j, s[1]);
+      }
+      if (have_m) {
+        const float2 n0 = make_float2(-m[0], -m[0]), n1 = make_float2(-m[1], -m[1]);
+        float2 sum[2][2];
+#pragma unroll
+        for (int a = 0; a < 2; ++a) sum[0][a] = sum[1][a] = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float2 x = fma2(make_float2(__uint_as_float(s[0][2 * e]), __uint_as_float(s[0][2 * e + 1])), cc, n0);
+          const float2 y = fma2(make_float2(__uint_as_float(s[1][2 * e]), __uint_as_float(s[1][2 * e + 1])), cc, n1);
+          sum[0][e & 1] = add2(sum[0][e & 1], make_float2(ex2(x.x), ex2(x.y)));
+          sum[1][e & 1] = add2(sum[1][e & 1], make_float2(ex2(y.x), ex2(y.y)));
+        }
+        const float2 t0 = add2(sum[0][0], sum[0][1]), t1 = add2(sum[1][0], sum[1][1]);
+        const float l0 = l[0] + (t0.x + t0.y), l1 = l[1] + (t1.x + t1.y);
+        if (!__any_sync(0xffffffffu, !(fmaxf(l0, l1) < 1.2676506e30f))) {  // 2^100
+          l[0] = l0;
+          l[1] = l1;
+          continue;
+        }
+      }
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const float top = max32(s[x]) * sc;
@@ -386,18 +414,10 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
         l[x] *= m_new == m[x] ? 1.f : ex2(m[x] - m_new);
         m[x] = m_new;
         const float ms = m_new == -INFINITY ? 0.f : m_new;
-        const float2 nms = make_float2(-ms, -ms);
-        float2 sum[4];
 #pragma unroll
-        for (int a = 0; a < 4; ++a) sum[a] = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float2 y = fma2(make_float2(__uint_as_float(s[x][2 * e]), __uint_as_float(s[x][2 * e + 1])), cc, nms);
-          sum[e & 3] = add2(sum[e & 3], make_float2(ex2(y.x), ex2(y.y)));
-        }
-        const float2 t = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
-        l[x] += t.x + t.y;
+        for (int e = 0; e < 32; ++e) l[x] += ex2(__uint_as_float(s[x][e]) * sc - ms);
       }
+      have_m = __all_sync(0xffffffffu, m[0] != -INFINITY && m[1] != -INFINITY);
     }
     // The warpgroups' statistics of a row together, in the same order in all.
     // (`stats` of the item before has been read: this item's S needed its
@@ -429,28 +449,25 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
     }
 
     if (item.part < 0) {
-      // ---- pass 1: weights w_1 - lambda w_2, scaled by 2^sigma so that both
-      // terms stay at or below 2^8 (the lazy maximum's slack) and the smallest
-      // that matter inside an fp16's range
-      const float big = fabsf(lam) > 1.f ? __log2f(fabsf(lam)) : 0.f;
-      const float sigma = fminf(log2l[0], log2l[1] - big);
+      // ---- pass 1: weights w_1 - lambda w_2, scaled by 2^sigma so that they
+      // stay below 2^14 and small ones inside an fp16's normal range
+      const float sigma = kWeightScale - (fabsf(lam) > 1.f ? __log2f(fabsf(lam)) : 0.f);
       const float a1 = m[0] + log2l[0] - sigma, a2 = m[1] + log2l[1] - sigma;
       const float2 n1 = make_float2(-a1, -a1), n2 = make_float2(-a2, -a2), nl = make_float2(-lam, -lam);
-      for (int j = 0; j < ntiles && ok; ++j) {
+      for (int j = 0; j < ntiles; ++j) {
         const int b = j & 1;
         uint32_t s1[32], s2[32], pk[16];
-        const bool any = load_s(0, j, true, true, s1, s2);
-        if (any) {
+        load_s(0, true, true, s1, s2);
+        if (j < c0 || j >= c1) {
+          mask(j, s1);
+          mask(j, s2);
+        }
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float2 x = fma2(make_float2(__uint_as_float(s1[2 * e]), __uint_as_float(s1[2 * e + 1])), cc, n1);
-            const float2 y = fma2(make_float2(__uint_as_float(s2[2 * e]), __uint_as_float(s2[2 * e + 1])), cc, n2);
-            const float2 w = fma2(make_float2(ex2(y.x), ex2(y.y)), nl, make_float2(ex2(x.x), ex2(x.y)));
-            pk[e] = tc::pack2<T>(w.x, w.y);
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) pk[e] = 0u;
+        for (int e = 0; e < 16; ++e) {
+          const float2 x = fma2(make_float2(__uint_as_float(s1[2 * e]), __uint_as_float(s1[2 * e + 1])), cc, n1);
+          const float2 y = fma2(make_float2(__uint_as_float(s2[2 * e]), __uint_as_float(s2[2 * e + 1])), cc, n2);
+          const float2 w = fma2(make_float2(ex2(y.x), ex2(y.y)), nl, make_float2(ex2(x.x), ex2(x.y)));
+          pk[e] = tc::pack2<T>(w.x, w.y);
         }
         ok = ok && warp_wait(&bar.p_free[b], (np[b] & 1) ^ 1, abort);
         ++np[b];
@@ -513,14 +530,16 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
       // ---- passes 2 and 3: each map's partial state, weights as hi + lo
 #pragma unroll 1
       for (int x = 0; x < 2; ++x) {
-        const float2 n = make_float2(-m[x], -m[x]);
-        for (int j = 0; j < ntiles && ok; ++j) {
+        const float a = m[x] + log2l[x] - kWeightScale;
+        const float2 n = make_float2(-a, -a);
+        for (int j = 0; j < ntiles; ++j) {
           uint32_t s[32], hi[16], low[16];
-          const bool any = load_s(0, j, x == 0, x == 1, s, s);
+          load_s(0, x == 0, x == 1, s, s);
+          if (j < c0 || j >= c1) mask(j, s);
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const float2 y = fma2(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), cc, n);
-            const float2 w = any ? make_float2(ex2(y.x), ex2(y.y)) : make_float2(0.f, 0.f);
+            const float2 w = make_float2(ex2(y.x), ex2(y.y));
             hi[e] = tc::pack2<T>(w.x, w.y);
             const float2 hf = Elem<T>::to_float2(hi[e]);
             low[e] = tc::pack2<T>(w.x - hf.x, w.y - hf.y);
@@ -544,7 +563,7 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
         ++no;
         tc::fence_after_sync();
         const int64_t prw = int64_t(item.part) + x * nrows + r;
-        const float inv = l[x] > 0.f ? 1.f / l[x] : 0.f;
+        const float inv = l[x] > 0.f ? ex2(-kWeightScale) : 0.f;
         uint32_t ov[32];
         tc::tmem_ld32(tl + kDiffTmemO + kDiffKeys * wg, ov);
         tc::tmem_ld_wait();
