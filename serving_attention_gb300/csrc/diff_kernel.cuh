@@ -365,40 +365,12 @@ __device__ __forceinline__ void diff_store_row(const DiffParams& dp, const float
     *reinterpret_cast<uint32_t*>(dst + 64 * h) = Elem<T>::from_float2(y[2 * h] * f[2 * h], y[2 * h + 1] * f[2 * h + 1]);
 }
 
-// The queries of packed rows [prow0, prow0 + prows) of an item (at most 16) as
-// product operands of this thread: narrow (up to 8 rows) the pair of K16 step
-// e / 2 at offset 8 (e % 2), both maps in a row; wide the steps of this map's
-// 64 dims, rows g and g + 8 in turn.
-__device__ __forceinline__ void diff_load_q(const RunParams& p, const Item& item, int prow0, uint32_t (&qf)[16]) {
-  const int cw = (threadIdx.x >> 5) - kFirstConsumerWarp;
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int prows = min(16, item.row1 - item.row0 - prow0);
-  const bool wide = prows > 8;
-  const uint16_t* src[2];
-  bool live[2];
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const int r = wide ? g + 8 * x : g;
-    live[x] = r < prows;
-    const int row = item.row0 + prow0 + (live[x] ? r : 0), tq = row / p.group;
-    src[x] = p.q + int64_t(item.rq.qo_start + tq) * p.q_stride_tok +
-             int64_t(item.hk * p.group + (row - tq * p.group)) * p.q_stride_head + 2 * t + (wide ? 64 * (cw >> 2) : 0);
-  }
-#pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    const int x = wide ? e & 1 : 0;
-    const int dim = wide ? 16 * (e >> 2) + 8 * ((e >> 1) & 1) : 16 * (e >> 1) + 8 * (e & 1);
-    qf[e] = live[x] ? __ldg(reinterpret_cast<const uint32_t*>(src[x] + dim)) : 0u;
-  }
-}
-
-// One pass of an item's packed rows [prow0, prow0 + prows): the item's stages,
-// then the merge of the eight warps' states and the output (or the fp32
-// partial states).  ahead() loads what comes next, before the merge.
-template <typename T, bool kWide, typename Ahead>
+// One pass of an item's packed rows [prow0, prow0 + prows): the queries as
+// product operands, the item's stages, then the merge of the eight warps'
+// states and the output (or the fp32 partial states).
+template <typename T, bool kWide>
 __device__ __forceinline__ uint32_t diff_pass(const DiffParams& dp, DiffSmem& sm, const Item& item, int prow0,
-                                              int prows, uint32_t it, int causal, const Variant& var,
-                                              const uint32_t (&qf)[16], Ahead ahead) {
+                                              int prows, uint32_t it, int causal, const Variant& var) {
   const RunParams& p = dp.run;
   DiffBufs& bufs = sm.dec;
   const int cw = (threadIdx.x >> 5) - kFirstConsumerWarp;
@@ -408,16 +380,32 @@ __device__ __forceinline__ uint32_t diff_pass(const DiffParams& dp, DiffSmem& sm
   const int nst = (item.kv1 - item.kv0 + kStageTokens - 1) >> kLog2StageTokens;
   const int map = kWide ? cw >> 2 : 0;
 
+  uint32_t qf[16];
   DiffRows rw;
+  {
+    const uint16_t* src[2];
+    bool live[2];
 #pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const int r = kWide ? g + 8 * x : g;  // packed row of tile row g + 8 x
-    const bool live = r < prows;
-    const int pos = rq.kv_len - rq.qo_len + (item.row0 + prow0 + (live ? r : 0)) / G;
-    rw.lim[x] = live ? min(causal ? pos : rq.kv_len - 1, item.kv1 - 1) : -1;
-    rw.lo[x] = window_low(var, pos);
-    rw.m[x] = -INFINITY;
-    rw.l[x] = 0.f;
+    for (int x = 0; x < 2; ++x) {
+      const int r = kWide ? g + 8 * x : g;  // packed row of tile row g + 8 x
+      live[x] = r < prows;
+      const int row = item.row0 + prow0 + (live[x] ? r : 0);
+      const int tq = row / G, head = item.hk * G + (row - tq * G);
+      src[x] = p.q + int64_t(rq.qo_start + tq) * p.q_stride_tok + int64_t(head) * p.q_stride_head + 2 * t;
+      const int pos = rq.kv_len - rq.qo_len + tq;
+      rw.lim[x] = live[x] ? min(causal ? pos : rq.kv_len - 1, item.kv1 - 1) : -1;
+      rw.lo[x] = window_low(var, pos);
+      rw.m[x] = -INFINITY;
+      rw.l[x] = 0.f;
+    }
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      // narrow: the pair of step e / 2 at offset 8 (e % 2), both maps in a row;
+      // wide: steps of 64 dims of this map, rows g and g + 8 in turn
+      const int x = kWide ? e & 1 : 0;
+      const int dim = kWide ? 64 * map + 16 * (e >> 2) + 8 * ((e >> 1) & 1) : 16 * (e >> 1) + 8 * (e & 1);
+      qf[e] = live[x] ? __ldg(reinterpret_cast<const uint32_t*>(src[x] + dim)) : 0u;
+    }
   }
   float o[16][4];
 #pragma unroll
@@ -440,8 +428,6 @@ __device__ __forceinline__ uint32_t diff_pass(const DiffParams& dp, DiffSmem& sm
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.empty[s]);
   }
-
-  ahead();
 
   // Merge of the warps' states, 64 dims at a time through shared memory.
   // Warp w finishes packed row w (and w + 8 of a wide tile).
@@ -526,31 +512,16 @@ __device__ __forceinline__ uint32_t diff_pass(const DiffParams& dp, DiffSmem& sm
 template <typename T>
 __device__ void diff_consume(const DiffParams& dp, DiffSmem& sm, int32_t item_begin, int32_t item_end,
                              int32_t off_items, int causal, const Variant& var) {
-  // The next item's descriptor is loaded an item ahead, and the queries of the
-  // next pass before this one's states are merged.
-  uint32_t it = 0, qf[16];
-  if (item_begin >= item_end) return;
-  Item next = load_item(dp.run.iws, off_items, item_begin);
-  diff_load_q(dp.run, next, 0, qf);
+  uint32_t it = 0;
   for (int32_t i = item_begin; i < item_end; ++i) {
-    const Item item = next;
-    if (i + 1 < item_end) next = load_item(dp.run.iws, off_items, i + 1);
+    const Item item = load_item(dp.run.iws, off_items, i);
     const int nrows = item.row1 - item.row0;
     for (int prow0 = 0; prow0 < nrows; prow0 += 16) {
       const int prows = min(16, nrows - prow0);
-      uint32_t qn[16];
-      auto ahead = [&] {
-        if (prow0 + 16 < nrows)
-          diff_load_q(dp.run, item, prow0 + 16, qn);
-        else if (i + 1 < item_end)
-          diff_load_q(dp.run, next, 0, qn);
-      };
       if (prows <= 8)
-        it = diff_pass<T, false>(dp, sm, item, prow0, prows, it, causal, var, qf, ahead);
+        it = diff_pass<T, false>(dp, sm, item, prow0, prows, it, causal, var);
       else
-        it = diff_pass<T, true>(dp, sm, item, prow0, prows, it, causal, var, qf, ahead);
-#pragma unroll
-      for (int e = 0; e < 16; ++e) qf[e] = qn[e];
+        it = diff_pass<T, true>(dp, sm, item, prow0, prows, it, causal, var);
     }
   }
 }
