@@ -37,6 +37,7 @@ extern "C" {
  *   lambda       fp32 [num_qo_heads], device;
  *   norm_weight  fp32 [128], device, or NULL: no norm (norm_eps is then not
  *                read);
+ *   sm_scale     positive (a normal fp32 number, its log2(e) multiple too);
  *   out_scale    factor on the output;
  *   lse          fp32 [q_num_tokens, num_qo_heads, 2], contiguous, the natural
  *                log-sum-exp of the two maps; may be NULL.

@@ -30,7 +30,10 @@ extern "C" fi_status fi_batch_paged_attention_run_differential(const fi_differen
   if (!a->k_cache || !a->v_cache || !a->kv_indices_dev || a->num_pages < 1) return FI_ERR_INVALID_ARG;
   if (!(info->variant & 8) || info->num_ctas < 1 || a->q_num_tokens < 1) return FI_ERR_INVALID_ARG;
   if (a->num_pages > INT32_MAX || a->q_num_tokens > INT32_MAX) return FI_ERR_INVALID_ARG;
-  if (!std::isfinite(a->sm_scale) || !std::isfinite(a->out_scale)) return FI_ERR_INVALID_ARG;
+  // masked logits are set to -inf before they are scaled: a factor of 0, below
+  // 0, or one the hardware flushes to 0 would turn them
+  const float scale_log2 = a->sm_scale * 1.4426950408889634f;
+  if (!std::isnormal(scale_log2) || scale_log2 < 0.f || !std::isfinite(a->out_scale)) return FI_ERR_INVALID_ARG;
   if (a->norm_weight && !(a->norm_eps >= 0.f && std::isfinite(a->norm_eps))) return FI_ERR_INVALID_ARG;
   if (info->num_partial_rows > 0 && !a->float_workspace_dev) return FI_ERR_INVALID_ARG;
   if (info->head_dim != kHeadDim) return FI_ERR_UNSUPPORTED;
@@ -64,7 +67,7 @@ extern "C" fi_status fi_batch_paged_attention_run_differential(const fi_differen
   p.partial_o_offset = fi_partial_o_offset(info->max_partial_rows);
   p.max_partial_rows = p.fws ? info->max_partial_rows : 0;
   p.q_num_tokens = int32_t(a->q_num_tokens);
-  p.scale_log2 = a->sm_scale * 1.4426950408889634f;
+  p.scale_log2 = scale_log2;
   p.num_qo_heads = info->num_qo_heads;
   p.num_kv_heads = info->num_kv_heads;
   p.group = info->num_qo_heads / info->num_kv_heads;

@@ -126,7 +126,8 @@ def _run(**kw):
 @pytest.mark.parametrize("kw,status", [
     (dict(info=0), 1), (dict(q=0), 1), (dict(o=0), 1), (dict(lam=0), 1), (dict(iws=0), 1), (dict(k=0), 1),
     (dict(v=0), 1), (dict(idx=0), 1), (dict(pages=0), 1), (dict(pages=1 << 31), 1), (dict(n=0), 1),
-    (dict(sm=float("nan")), 1), (dict(scale=float("inf")), 1), (dict(eps=-1.0), 1), (dict(eps=float("nan")), 1),
+    (dict(sm=float("nan")), 1), (dict(sm=0.0), 1), (dict(sm=-0.125), 1), (dict(sm=1e-40), 1), (dict(sm=3e38), 1),
+    (dict(scale=float("inf")), 1), (dict(eps=-1.0), 1), (dict(eps=float("nan")), 1),
     (dict(dt=fi.FP32), 2), (dict(q=18), 4), (dict(o=120), 4), (dict(lam=82), 4), (dict(lse=130), 4),
     (dict(qt=1020), 4), (dict(oh=0), 4), (dict(k1=250), 4), (dict(v2=-128), 4),
     (dict(variant=0), 1), (dict(variant=4), 1), (dict(num_ctas=0), 1), (dict(head_dim=64), 2),
