@@ -543,7 +543,8 @@ __global__ void __launch_bounds__(kDiffThreads, 1) diff_attention_kernel(const _
   const int32_t h_page = ws_header(iws, FI_H_PAGE_SIZE);
   bool bad = magic != FI_PLAN_MAGIC_DIFF || n_ctas != int32_t(gridDim.x) || (smem_u32(smem_raw) & 1023u) != 0 ||
              h_rows < 0 || h_rows > p.max_partial_rows || h_qo < 0 || h_qo > p.q_num_tokens ||
-             h_hq != p.num_qo_heads || h_hkv != p.num_kv_heads || h_page != p.kv[0].page_size;
+             h_hq != p.num_qo_heads || h_hkv != p.num_kv_heads || h_page != p.kv[0].page_size ||
+             (!kMask && ws_header(iws, FI_H_WINDOW_LEFT) >= 0);
   int32_t begin = 0, end = 0;
   if (!bad) {
     begin = __ldg(iws + off_cta + blockIdx.x);

@@ -236,6 +236,17 @@ def test_plans_of_the_other_kind_are_refused_on_the_device():
     assert fi.device_status(ws) == 6 and torch.isnan(o).all()
 
 
+def test_a_windowed_plan_is_refused_by_a_launch_without_a_window():
+    b, lam, w = _batch(14, [200, 1], [400, 50], 8, 2, 16, "bf16", causal=1)
+    o, lse, info, ws, kvi = _run(b, lam, w, _config())
+    ws.cfg = _config(window_left=20, sink_tokens=2)
+    fi.plan(ws, b.qo_indptr, b.kv_indptr, b.kv_indices, b.last_page_len, 8, 2, 128, 16, 1, b.num_pages)
+    o.fill_(float("nan"))
+    differential.run(ws, info, b.q, b.k, b.v, kvi, lam, o, lse, b.sm_scale)
+    torch.cuda.synchronize()
+    assert fi.device_status(ws) == 6 and torch.isnan(o).all()
+
+
 def test_bad_page_ids_read_as_zeros():
     """An id outside the cache is not followed: its keys and values are zeros."""
     b, lam, w = _batch(15, [1, 30], [40, 64], 8, 2, 16, "bf16", poison=False)
