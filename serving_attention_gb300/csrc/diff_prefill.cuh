@@ -160,19 +160,27 @@ __device__ void diff_pf_produce(const RunParams& p, DiffPrefillBufs& pf, DiffPre
   __syncwarp();
 }
 
-// As warp_wait_all for up to four phases, but the warp keeps polling: the
-// wake-up of a sleeping wait is on the critical path of the products.
-__device__ __forceinline__ bool poll_wait(uint64_t* b0, uint32_t p0, uint64_t* b1, uint32_t p1, uint64_t* b2,
-                                          uint32_t p2, uint64_t* b3, uint32_t p3, volatile int* abort) {
-  const int lane = threadIdx.x & 31;
-  uint64_t* const bar = lane == 1 ? b1 : lane == 2 ? b2 : lane == 3 ? b3 : b0;
-  const uint32_t ph = lane == 1 ? p1 : lane == 2 ? p2 : lane == 3 ? p3 : p0;
-  if (__all_sync(0xffffffffu, mbar_try_wait(bar, ph))) return true;
+// Waits for two phases, bounded as warp_wait is, but the warp keeps polling:
+// the wake-up of a sleeping wait is on the critical path of the products.  Odd
+// lanes poll the second.
+__device__ __forceinline__ bool poll_wait(uint32_t b0, uint32_t p0, uint32_t b1, uint32_t p1, volatile int* abort) {
+  const bool odd = threadIdx.x & 1;
+  const uint32_t bar = odd ? b1 : b0, ph = odd ? p1 : p0;
+  auto done = [&] {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(ph)
+        : "memory");
+    return __all_sync(0xffffffffu, ok != 0) != 0;
+  };
+  if (done()) return true;
   const long long t0 = clock64();
   while (true) {
 #pragma unroll 1
     for (int k = 0; k < 64; ++k)
-      if (__all_sync(0xffffffffu, mbar_try_wait(bar, ph))) return true;
+      if (done()) return true;
     const int st = __shfl_sync(0xffffffffu, (*abort != 0 ? 2 : 0) | (clock64() - t0 > kWaitBudgetClocks ? 4 : 0), 0);
     if (st & 2) return false;
     if (st & 4) {
@@ -182,10 +190,44 @@ __device__ __forceinline__ bool poll_wait(uint64_t* b0, uint32_t p0, uint64_t* b
   }
 }
 
-// The MMA warp's time goes into waits (some 300 cycles each, with the tensor
-// pipe using all of shared memory) as much as into products, so the blocks
-// are as large as they can be: 8 products of S behind one wait, 8 of P V
-// behind another.
+// Four products D (+)= A B of K 16 each behind one election; the operands
+// advance by constants.  A in shared memory (64 dims of Q) or, with kTmemA, in
+// tensor memory (64 keys' weights); B 64 dims of K, or 64 keys of V.
+template <bool kTmemA>
+__device__ __forceinline__ void mma4(uint32_t d, uint64_t a_desc, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                                     uint32_t accumulate) {
+  if (kTmemA)
+    asm volatile(
+        "{\n\t.reg .pred p, t, e;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, %3, %3;\n\t"
+        "add.s32 a1, %1, 8;\n\tadd.s32 a2, %1, 16;\n\tadd.s32 a3, %1, 24;\n\t"
+        "add.s64 b1, %2, 128;\n\tadd.s64 b2, %2, 256;\n\tadd.s64 b3, %2, 384;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t}" ::"r"(d),
+        "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, t, e;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, %3, %3;\n\t"
+        "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"
+        "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n\t}" ::"r"(d),
+        "l"(a_desc), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// The MMA warp shares its scheduler with four softmax warps, and an
+// instruction of it takes 5 to 10 cycles: a step's few hundred instructions
+// are what a step takes.  So its waits and products are kept short, and the
+// blocks large: 8 products of S behind one wait, 8 of P V behind another.
 template <typename T>
 __device__ void diff_pf_mma(const RunParams& p, DiffPrefillBufs& pf, DiffPrefillBars& bar, volatile int* abort,
                             uint32_t tmem, int32_t b0, int32_t b1, int32_t off_items) {
@@ -198,48 +240,68 @@ __device__ void diff_pf_mma(const RunParams& p, DiffPrefillBufs& pf, DiffPrefill
   const uint64_t dq = tc::smem_desc_sw128(smem_u32(&pf.q[0][0][0][0]), 16, 1024);
   const uint64_t dk = tc::smem_desc_sw128(smem_u32(&pf.k[0][0][0][0]), 16, 1024);
   const uint64_t dv = tc::smem_desc_sw128(smem_u32(&pf.v[0][0][0][0]), 64 * kTileN * 2, 1024);
-  uint32_t kt = 0, vt = 0, ni = 0, no = 0;         // K tiles, V tiles, items, uses of O so far
-  uint32_t ns0 = 0, ns1 = 0, np0 = 0, np1 = 0;     // uses of the S and of the P buffers
-  uint32_t cleared = 0;                            // bit st: parity of the cleared tails of V stage st
-  bool issued = false;
-  struct Pv {  // the P V of a step, which follows the S of the next step
-    int kind, j;
-    bool last, tail;
-  } pv{0, 0, false, false};
-  auto do_pv = [&]() -> bool {
-    const int st = vt & 1, b = pv.kind == 1 ? pv.j & 1 : 0;
-    const bool two = pv.kind != 1;  // hi in buffer 0, lo in buffer 1
-    uint64_t* const pb = &bar.p_full[b];
-    const uint32_t pp = (b ? np1 : np0) & 1;
-    if (!poll_wait(pb, pp, pv.tail ? &bar.v_clear[st] : &bar.v_full[st],
-                   pv.tail ? (cleared >> st) & 1 : (vt >> 1) & 1, pv.j == 0 ? &bar.o_free : pb,
-                   pv.j == 0 ? (no & 1) ^ 1 : pp, two ? &bar.p_full[1] : pb, two ? np1 & 1 : pp, abort))
-      return false;
+  const uint32_t k_full = smem_u32(&bar.k_full[0]), v_full = smem_u32(&bar.v_full[0]);
+  const uint32_t v_clear = smem_u32(&bar.v_clear[0]);
+  const uint32_t s_free = smem_u32(&bar.s_free[0]), p_full = smem_u32(&bar.p_full[0]), o_free = smem_u32(&bar.o_free);
+  uint32_t kt = 0, vt = 0, ni = 0, no = 0;  // K tiles, V tiles, items, uses of O so far
+  uint32_t ps = 3, pp = 0;                  // bit b: parity that S buffer b's next use, P buffer b's next product waits for
+  uint32_t cleared = 0;                     // bit st: parity of the cleared tails of V stage st
+  bool ok = true, issued = false;  // after a wait that ran out nothing more is issued
+  // S of a step in buffer x, of both maps or one
+  auto do_s = [&](uint64_t a, int x, bool m1, bool m2) {
+    const int st = kt & 1;
+    ok = ok && poll_wait(s_free + 8 * x, (ps >> x) & 1, k_full + 8 * st, (kt >> 1) & 1, abort);
+    if (!ok) return;
     tc::fence_after_sync();
-    const uint64_t bv = dv + 2048u * st;
-    const uint32_t acol = tmem + kDiffTmemP + 64 * b;
-#pragma unroll
-    for (int kk = 0; kk < 8; ++kk)  // P of keys 16 kk .. 16 kk + 15: columns 8 kk .. 8 kk + 7
-      tc::mma_ts_warp(tmem + kDiffTmemO, acol + 8 * kk, bv + 128u * kk, idesc_pv, (pv.j > 0 || kk > 0) ? 1u : 0u);
+    const uint64_t b = dk + 2048u * st;
+    const uint32_t d = tmem + 2 * kTileN * x;
+    if (m1) mma4<false>(d, a, 0, b, idesc_s, 0);
+    if (m2) mma4<false>(d + kTileN, a + 1024u, 0, b + 1024u, idesc_s, 0);
+    tc::mma_commit_warp(&bar.s_full[x]);
+    tc::mma_commit_warp(&bar.k_empty[st]);
+    ps ^= 1u << x;
+    ++kt;
+    issued = true;
+  };
+  // P V of a step: weights in buffer b, or (two) hi in buffer 0 and lo in 1
+  auto do_pv = [&](int b, bool two, bool first, bool last, bool tail) {
+    const int st = vt & 1;
+    if (first) ok = ok && poll_wait(o_free, (no & 1) ^ 1, o_free, (no & 1) ^ 1, abort);
+    if (two) ok = ok && poll_wait(p_full + 8, pp >> 1, p_full + 8, pp >> 1, abort);
+    ok = ok && poll_wait(p_full + 8 * b, (pp >> b) & 1, (tail ? v_clear : v_full) + 8 * st,
+                         tail ? (cleared >> st) & 1 : (vt >> 1) & 1, abort);
+    if (!ok) return;
+    tc::fence_after_sync();
+    const uint64_t v = dv + 2048u * st;
+    const uint32_t w = tmem + kDiffTmemP + 64 * b, d = tmem + kDiffTmemO;
+    mma4<true>(d, 0, w, v, idesc_pv, first ? 0u : 1u);
+    mma4<true>(d, 0, w + 32, v + 512u, idesc_pv, 1u);
     if (two) {
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk)
-        tc::mma_ts_warp(tmem + kDiffTmemO, acol + 64 + 8 * kk, bv + 128u * kk, idesc_pv, 1u);
+      mma4<true>(d, 0, w + 64, v, idesc_pv, 1u);
+      mma4<true>(d, 0, w + 96, v + 512u, idesc_pv, 1u);
+      tc::mma_commit_warp(&bar.p_free[1]);
+      pp ^= 2u;
     }
     tc::mma_commit_warp(&bar.p_free[b]);
-    if (two) tc::mma_commit_warp(&bar.p_free[1]);
-    np0 += two || b == 0;
-    np1 += two || b == 1;
     tc::mma_commit_warp(&bar.v_empty[st]);
-    if (pv.last) {
+    if (last) {
       tc::mma_commit_warp(&bar.o_ready);
       ++no;
     }
-    if (pv.tail) cleared ^= 1u << st;
+    if (tail) cleared ^= 1u << st;
+    pp ^= 1u << b;
     ++vt;
-    return true;
   };
-  bool ok = true;
+  // The P V of a step follows the S of the next step: what is pending across
+  // passes and items, if anything.
+  struct {
+    bool any, two, first, last, tail;
+    int b;
+  } pv{false, false, false, false, false, 0};
+  auto flush = [&] {
+    if (pv.any) do_pv(pv.b, pv.two, pv.first, pv.last, pv.tail);
+    pv.any = false;
+  };
   Item next = load_item(p.iws, off_items, b0);
   for (int32_t i = b0; i < b1 && ok; ++i) {
     const Item it = next;
@@ -247,41 +309,35 @@ __device__ void diff_pf_mma(const RunParams& p, DiffPrefillBufs& pf, DiffPrefill
     const int ntiles = item_kv_tiles(it);
     if (ntiles == 0) continue;
     const bool tail = item_v_tail(it, p.kv[0].page_size);
-    const int qb = ni & 1, last = last_pass(it);
+    const uint32_t qb = ni & 1, q_full = smem_u32(&bar.q_full[0]) + 8 * qb;
     const uint64_t a = dq + 2048u * qb;
-    for (int kind = 0; kind <= last && ok; kind = kind == 0 ? first_pv_pass(it) : kind + 1) {
-      for (int j = 0; j < ntiles && ok; ++j, ++kt) {
-        const int st = kt & 1, x = kind == 0 ? j & 1 : 0;
-        uint64_t* const kb = &bar.k_full[st];
-        const uint32_t kp = (kt >> 1) & 1;
-        // the item's Q with its first S; O's and P's columns free (the item
-        // before read out) with its first S in the second buffer
-        uint64_t* const eb = kind != 0 || j > 1 ? kb : j == 0 ? &bar.q_full[qb] : &bar.o_free;
-        const uint32_t ep = kind != 0 || j > 1 ? kp : j == 0 ? (ni >> 1) & 1 : (no & 1) ^ 1;
-        ok = poll_wait(&bar.s_free[x], ((x ? ns1 : ns0) & 1) ^ 1, kb, kp, eb, ep, kb, kp, abort);
-        if (!ok) break;
-        tc::fence_after_sync();
-        const uint64_t b = dk + 2048u * st;
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          if (kind == 3 - m) continue;  // kind 2: map 1 alone, kind 3: map 2 alone
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc::mma_ss_warp(tmem + 2 * kTileN * x + kTileN * m, a + 1024u * m + 2u * kk, b + 1024u * m + 2u * kk,
-                            idesc_s, kk > 0 ? 1u : 0u);
+    ok = poll_wait(q_full, (ni >> 1) & 1, q_full, (ni >> 1) & 1, abort);
+    do_s(a, 0, true, true);
+    flush();
+    for (int j = 1; j < ntiles && ok; ++j) {
+      // S buffer 1: O's and P's columns, once the item before is read out
+      if (j == 1) ok = poll_wait(o_free, (no & 1) ^ 1, o_free, (no & 1) ^ 1, abort);
+      do_s(a, j & 1, true, true);
+    }
+    if (it.part < 0) {
+      do_s(a, 0, true, true);
+      for (int j = 1; j < ntiles && ok; ++j) {
+        do_s(a, 0, true, true);
+        do_pv((j - 1) & 1, false, j == 1, false, false);
+      }
+      pv = {true, false, ntiles == 1, true, tail, (ntiles - 1) & 1};
+    } else {
+      for (int m = 0; m < 2; ++m) {
+        for (int j = 0; j < ntiles && ok; ++j) {
+          do_s(a, 0, m == 0, m == 1);
+          flush();
+          pv = {true, true, j == 0, j + 1 == ntiles, tail && j + 1 == ntiles, 0};
         }
-        tc::mma_commit_warp(&bar.s_full[x]);
-        tc::mma_commit_warp(&bar.k_empty[st]);
-        ns0 += x == 0;
-        ns1 += x;
-        issued = true;
-        if (pv.kind) ok = do_pv();
-        pv = {kind, j, j + 1 == ntiles, tail && j + 1 == ntiles};
       }
     }
     ++ni;
   }
-  if (ok && pv.kind) do_pv();
+  flush();
   if (issued) {  // no product may still run when the CTA leaves the phase
     tc::mma_commit_warp(&bar.drain);
     if (lane == 0) mbar_wait_drain(&bar.drain, 0);
