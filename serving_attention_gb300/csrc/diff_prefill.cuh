@@ -58,6 +58,7 @@ struct DiffPrefillBufs {  // every [128][64] block is a 128-byte swizzled operan
   uint16_t v[2][2][kTileN][64];
   float stats[kDiffGroups][4][kTileM];  // [warpgroup][max 1, sum 1, max 2, sum 2][row] over its keys
   float sq[kDiffGroups][kTileM];        // [dim quarter][row] sum of squares
+  float4 norm_w[kHeadDim / 4];
 };
 
 struct DiffPrefillBars {
@@ -378,8 +379,18 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
   const float2 cc = make_float2(sc, sc);
   uint32_t ns[2] = {0, 0}, np[2] = {0, 0}, no = 0, ni = 0;  // as in the MMA warp
   int q_held = -1;  // the Q buffer that this warpgroup's output store may still be reading
+  if (dp.norm_w && sw < 4) reinterpret_cast<float*>(pf.norm_w)[r] = __ldg(dp.norm_w + r);
+  named_barrier_sync(kDiffBarrier, kDiffSoftmaxThreads);
+  // Lane l holds word l of the next item's descriptor.
+  auto item_word = [&](int32_t i) {
+    return lane < 12 && i < b1 ? __ldg(p.iws + off_items + FI_ITEM_INTS * i + lane) : 0;
+  };
+  int32_t ahead = item_word(b0);
   for (int32_t i = b0; i < b1; ++i) {
-    const Item item = load_item(p.iws, off_items, i);
+    auto word = [&](int w) { return __shfl_sync(0xffffffffu, ahead, w); };
+    const Item item{word(0), word(1), word(2),  word(3),  word(4),
+                    word(5), word(6), word(7),  Request{word(8), word(9), word(10), word(11)}, 1};
+    ahead = item_word(i + 1);
     const Request& rq = item.rq;
     const int nrows = item.row1 - item.row0, ntiles = item_kv_tiles(item);
     const int row = item.row0 + r, tq = row / G, head = item.hk * G + (row - tq * G);
@@ -534,6 +545,7 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.p_full[b]);
       }
+      if (p.lse && wg < 2 && live && !*abort) p.lse[(tok * p.num_qo_heads + head) * 2 + wg] = lse;
       // ---- the output: this warpgroup's 32 dims of the row
       ok = ok && warp_wait(&bar.o_ready, no & 1, abort);
       ++no;
@@ -555,7 +567,13 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
         named_barrier_sync(kDiffBarrier, kDiffSoftmaxThreads);
         f *= rms_factor((pf.sq[0][r] + pf.sq[1][r]) + (pf.sq[2][r] + pf.sq[3][r]), dp.norm_eps);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(val(e) * __ldg(dp.norm_w + kDiffKeys * wg + e));
+        for (int e = 0; e < 8; ++e) {
+          const float4 w = pf.norm_w[kDiffKeys / 4 * wg + e];
+          y[4 * e] = __float_as_uint(val(4 * e) * w.x);
+          y[4 * e + 1] = __float_as_uint(val(4 * e + 1) * w.y);
+          y[4 * e + 2] = __float_as_uint(val(4 * e + 2) * w.z);
+          y[4 * e + 3] = __float_as_uint(val(4 * e + 3) * w.w);
+        }
       }
       auto pack8 = [&](int e) {
         return make_uint4(tc::pack2<T>(val(e) * f, val(e + 1) * f), tc::pack2<T>(val(e + 2) * f, val(e + 3) * f),
@@ -581,7 +599,6 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
           for (int c = 0; c < 4; ++c) reinterpret_cast<uint4*>(out)[c] = pack8(8 * c);
         }
       }
-      if (p.lse && wg < 2 && live && !*abort) p.lse[(tok * p.num_qo_heads + head) * 2 + wg] = lse;
     } else {
       // ---- passes 2 and 3: each map's partial state, weights as hi + lo
 #pragma unroll 1
