@@ -575,15 +575,15 @@ __global__ void __launch_bounds__(kDiffThreads, 1) diff_attention_kernel(const _
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bar.q_full[s], 1);
       mbar_init(&bar.q_empty[s], 2);  // one thread of each pair of softmax warpgroups
-      mbar_init(&bar.k_full[s], 1);
-      mbar_init(&bar.k_empty[s], 1);
-      mbar_init(&bar.v_full[s], 1);
-      mbar_init(&bar.v_empty[s], 1);
-      mbar_init(&bar.v_clear[s], 1);
       mbar_init(&bar.s_full[s], 1);
       mbar_init(&bar.s_free[s], 4 * kDiffGroups);  // every softmax warp
       mbar_init(&bar.p_full[s], 4 * kDiffGroups);
       mbar_init(&bar.p_free[s], 1);
+    }
+    for (int s = 0; s < kDiffStages; ++s) {
+      mbar_init(&bar.kv_full[s], 1);
+      mbar_init(&bar.kv_empty[s], 1);
+      mbar_init(&bar.v_clear[s], 1);
     }
     mbar_init(&bar.o_ready, 1);
     mbar_init(&bar.o_free, 4 * kDiffGroups);
@@ -601,15 +601,16 @@ __global__ void __launch_bounds__(kDiffThreads, 1) diff_attention_kernel(const _
   // Each branch returns to the launch's registers before the code paths meet
   // (an increase waits for the other warpgroups' release).
   if (tc_phase) {
+    uint32_t loads = 0;
     if (warp < kSoftmaxWarp0) {
       tc::setmaxnreg_dec<kDiffRegsLoader>();
       if (warp == 0) {
-        diff_pf_produce<false>(p, sm.pf, bar, &sm.abort, begin, mid, off_items);
+        loads = diff_pf_produce<false>(p, sm.pf, bar, &sm.abort, begin, mid, off_items);
       } else if (warp == kMmaWarp) {
         diff_pf_mma<T>(p, sm.pf, bar, &sm.abort, sm.tmem_base, begin, mid, off_items);
         __syncwarp();
       } else if (warp == kVWarp) {
-        diff_pf_produce<true>(p, sm.pf, bar, &sm.abort, begin, mid, off_items);
+        loads = diff_pf_produce<true>(p, sm.pf, bar, &sm.abort, begin, mid, off_items);
       }
       tc::fence_before_sync();
       named_barrier_sync_unaligned(kPhaseBarrier, kDiffThreads);
@@ -622,6 +623,10 @@ __global__ void __launch_bounds__(kDiffThreads, 1) diff_attention_kernel(const _
       tc::fence_before_sync();
       named_barrier_sync_unaligned(kPhaseBarrier, kDiffThreads);
       tc::fence_after_sync();
+    }
+    if (sm.abort) {  // no role is left that could set it: all threads take this branch or none
+      diff_pf_drain(bar, loads);
+      named_barrier_sync_unaligned(kPhaseBarrier, kDiffThreads);
     }
   }
   if (mid < end) {

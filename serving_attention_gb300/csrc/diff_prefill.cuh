@@ -41,6 +41,8 @@ constexpr int kDiffGroups = 4;                         // softmax warpgroups
 constexpr int kDiffKeys = kTileN / kDiffGroups;        // keys of a tile, and dims of the output, of each
 constexpr int kDiffSoftmaxThreads = 128 * kDiffGroups;
 constexpr int kDiffBarrier = 6;  // all softmax warpgroups (1: decode, 3: end of phase, 4 and 5: two warpgroups)
+constexpr int kDiffStages = 4;   // K and V tiles in one ring
+constexpr int kDiffLoadBarrier = 7;  // named barrier of the K and the V loader
 constexpr int kDiffTmemO = 256, kDiffTmemP = 384;
 constexpr float kWeightScale = 13.f;  // softmax weights are multiplied by 2^13 before they are rounded
 // Register budgets, per thread (see kRegsLaunch): in the tensor-core phase
@@ -54,16 +56,15 @@ static_assert(kDiffRegsOther * 384 + kDiffRegsConsumer * 256 <= kDiffRegsLaunch 
 
 struct DiffPrefillBufs {  // every [128][64] block is a 128-byte swizzled operand half (see PrefillBufs)
   uint16_t q[2][2][kTileM][64];  // [buffer][d half = map][row][dim]; an item's output leaves through its Q buffer
-  uint16_t k[2][2][kTileN][64];  // [stage][d half][token][dim]
-  uint16_t v[2][2][kTileN][64];
+  uint16_t kv[kDiffStages][2][kTileN][64];  // [stage][d half][token][dim]
   float stats[kDiffGroups][4][kTileM];  // [warpgroup][max 1, sum 1, max 2, sum 2][row] over its keys
   float sq[kDiffGroups][kTileM];        // [dim quarter][row] sum of squares
   float4 norm_w[kHeadDim / 4];
 };
 
 struct DiffPrefillBars {
-  uint64_t q_full[2], q_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t v_clear[2];            // a tile's V rows past the request's end cleared
+  uint64_t q_full[2], q_empty[2], kv_full[kDiffStages], kv_empty[kDiffStages];
+  uint64_t v_clear[kDiffStages];  // a tile's V rows past the request's end cleared
   uint64_t s_full[2], s_free[2];  // [S buffer]
   uint64_t p_full[2];             // [buffer]
   uint64_t p_free[2];
@@ -80,21 +81,30 @@ __device__ __forceinline__ bool item_v_tail(const Item& it, int page_size) {
   return (it.rq.kv_len & (page_size - 1)) != 0 && it.kv0 + item_kv_tiles(it) * kTileN > it.rq.kv_len;
 }
 
-// Warp 0 (kV false): Q and K tiles; warp 2 (kV true): V tiles.
+// Warp 0 (kV false): Q and K tiles; warp 2 (kV true): V tiles.  K and V tiles
+// share one ring, in the order in which the MMA warp takes them: in pass 0 all
+// its stages hold K.  With first = t the item's first place, and pending = 1
+// behind an item (whose last V comes after this item's first K):
+//   pass 0            K(0) t, K(j) t + pending + j
+//   later passes      from t1 = t + pending + tiles, their steps numbered q
+//                     through: K(0) t1, K(q) t1 + 2q - 1, V(q) t1 + 2q + 2
+//   the next item     t1 + 2 steps - 1.
+// Returns which stages this warp loaded, and above them the phases of the last
+// loads.
 template <bool kV>
-__device__ void diff_pf_produce(const RunParams& p, DiffPrefillBufs& pf, DiffPrefillBars& bar, volatile int* abort,
+__device__ uint32_t diff_pf_produce(const RunParams& p, DiffPrefillBufs& pf, DiffPrefillBars& bar, volatile int* abort,
                                 int32_t b0, int32_t b1, int32_t off_items) {
   const int lane = threadIdx.x & 31;
   const KvCache& kc = p.kv[0];
   const int G = p.group, lp = kc.log2_page, P = kc.page_size, ppt = kTileN >> lp;
   const CUtensorMap* map = kV ? &kc.tm_v : &kc.tm_k;
-  uint64_t *full = kV ? bar.v_full : bar.k_full, *empty = kV ? bar.v_empty : bar.k_empty;
   if (lane == 0) {
     tc::prefetch_tensormap(map);
     if (!kV) tc::prefetch_tensormap(&p.tm_q);
   }
-  uint32_t kt = 0, ni = 0;
-  int armed[2] = {-1, -1}, q_armed[2] = {-1, -1};
+  uint32_t t = 0, ni = 0;  // an item's first place, items
+  uint32_t armed = 0, armed_phase = 0;  // bit st: this warp loaded into stage st, and the phase of the last load
+  int q_armed[2] = {-1, -1};
   Item ahead = load_item(p.iws, off_items, b0);
   for (int32_t i = b0; i < b1; ++i) {
     const Item it = ahead;
@@ -120,44 +130,68 @@ __device__ void diff_pf_produce(const RunParams& p, DiffPrefillBufs& pf, DiffPre
         }
         q_armed[qb] = ph;
       }
-      ++ni;
     }
-    const int walks = kV ? last_pass(it) - first_pv_pass(it) + 1 : last_pass(it) - first_pv_pass(it) + 2;
-    for (int w = 0; w < walks; ++w) {
-      for (int j = 0; j < ntiles; ++j, ++kt) {
-        const int st = kt & 1;
-        const uint32_t ph = (kt >> 1) & 1;
-        const int32_t cur = next;
-        next = page_of(j + 1 < ntiles ? j + 1 : 0);
-        if (!warp_wait(&empty[st], ph ^ 1, abort)) continue;
-        if (lane == 0) mbar_arrive_expect_tx(&full[st], kKVBytes);
+    const int pending = ni > 0, steps = ntiles * (last_pass(it) - first_pv_pass(it) + 1);
+    const uint32_t t1 = t + pending + ntiles;
+    int j = 0;
+    for (int n = kV ? ntiles : 0; n < ntiles + steps; ++n) {
+      const int q = n - ntiles;  // step of the passes behind pass 0
+      const uint32_t at = q < 0 ? t + (n > 0 ? pending + n : 0) : kV ? t1 + 2 * q + 2 : t1 + (q > 0 ? 2 * q - 1 : 0);
+      const uint32_t st = at % kDiffStages, ph = (at / kDiffStages) & 1;
+      const int32_t cur = next;
+      const int tile = j;
+      j = j + 1 < ntiles ? j + 1 : 0;
+      next = page_of(j);
+      // A parity tells a phase from the next alone, so the V loads of an item
+      // begin once the K loads are that far: at K(0) behind pass 0, the tiles
+      // before t1 - 4 have been taken, and V(0)'s stage is at the phase before.
+      if (q == 0) {
+        if (kV)
+          named_barrier_sync(kDiffLoadBarrier, 64);
+        else
+          named_barrier_arrive(kDiffLoadBarrier, 64);
+      }
+      if (!warp_wait(&bar.kv_empty[st], ph ^ 1, abort)) continue;
+      if (lane == 0) mbar_arrive_expect_tx(&bar.kv_full[st], kKVBytes);
+      __syncwarp();
+      uint16_t(*buf)[kTileN][64] = pf.kv[st];
+      if (lane < ppt) {
+        tc::tma_load_4d(&buf[0][lane * P][0], map, &bar.kv_full[st], 0, it.hk, 0, cur);
+        tc::tma_load_4d(&buf[1][lane * P][0], map, &bar.kv_full[st], 64, it.hk, 0, cur);
+      }
+      armed |= 1u << st;
+      armed_phase = (armed_phase & ~(1u << st)) | (ph << st);
+      // The rows past the request's end are cleared once they have landed,
+      // and the MMA warp waits for that instead.  This warp does it because
+      // it alone starts the stage's next phase, so its wait cannot miss this
+      // one.
+      if (kV && tile + 1 == ntiles && item_v_tail(it, P) && warp_wait(&bar.kv_full[st], ph, abort)) {
+        for (int row = it.rq.kv_len - (it.kv0 + tile * kTileN) + (lane >> 4); row < kTileN; row += 2)
+          *reinterpret_cast<uint4*>(&buf[(lane >> 3) & 1][row][8 * (lane & 7)]) = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
         __syncwarp();
-        uint16_t(*buf)[kTileN][64] = kV ? pf.v[st] : pf.k[st];
-        if (lane < ppt) {
-          tc::tma_load_4d(&buf[0][lane * P][0], map, &full[st], 0, it.hk, 0, cur);
-          tc::tma_load_4d(&buf[1][lane * P][0], map, &full[st], 64, it.hk, 0, cur);
-        }
-        armed[st] = ph;
-        // The rows past the request's end are cleared once they have landed,
-        // and the MMA warp waits for that instead.  This warp does it because
-        // it alone starts the stage's next phase, so its wait cannot miss this
-        // one.
-        if (kV && j + 1 == ntiles && item_v_tail(it, P) && warp_wait(&full[st], ph, abort)) {
-          for (int row = it.rq.kv_len - (it.kv0 + j * kTileN) + (lane >> 4); row < kTileN; row += 2)
-            *reinterpret_cast<uint4*>(&buf[(lane >> 3) & 1][row][8 * (lane & 7)]) = make_uint4(0u, 0u, 0u, 0u);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar.v_clear[st]);
-        }
+        if (lane == 0) mbar_arrive(&bar.v_clear[st]);
       }
     }
+    t = t1 + 2 * steps - 1;
+    ++ni;
   }
-  if (lane == 0) {  // every load this warp armed has landed before the CTA moves on
-    for (int s = 0; s < 2; ++s) {
-      if (armed[s] >= 0) mbar_wait_drain(&full[s], armed[s]);
-      if (!kV && q_armed[s] >= 0) mbar_wait_drain(&bar.q_full[s], q_armed[s]);
-    }
+  if (!kV && lane == 0) {  // every Q load has landed before the CTA moves on
+    for (int s = 0; s < 2; ++s)
+      if (q_armed[s] >= 0) mbar_wait_drain(&bar.q_full[s], q_armed[s]);
   }
+  __syncwarp();
+  return armed | armed_phase << kDiffStages;
+}
+
+// After a phase that gave up: the tiles still on their way into the ring have
+// to land before its memory is used again.  (Otherwise the MMA warp has taken
+// them all.)  A wait for a phase that the other loader's tile has followed
+// runs into its bound.
+__device__ __forceinline__ void diff_pf_drain(DiffPrefillBars& bar, uint32_t loads) {
+  if ((threadIdx.x & 31) == 0)
+    for (int st = 0; st < kDiffStages; ++st)
+      if (loads >> st & 1) mbar_wait_drain(&bar.kv_full[st], (loads >> (kDiffStages + st)) & 1);
   __syncwarp();
 }
 
@@ -239,19 +273,18 @@ __device__ void diff_pf_mma(const RunParams& p, DiffPrefillBufs& pf, DiffPrefill
   // Start addresses count 16-byte units: a 64-dim half is 1024, a stage or Q
   // buffer 2048, 16 dims along a swizzled row 2, 16 V rows 128.
   const uint64_t dq = tc::smem_desc_sw128(smem_u32(&pf.q[0][0][0][0]), 16, 1024);
-  const uint64_t dk = tc::smem_desc_sw128(smem_u32(&pf.k[0][0][0][0]), 16, 1024);
-  const uint64_t dv = tc::smem_desc_sw128(smem_u32(&pf.v[0][0][0][0]), 64 * kTileN * 2, 1024);
-  const uint32_t k_full = smem_u32(&bar.k_full[0]), v_full = smem_u32(&bar.v_full[0]);
-  const uint32_t v_clear = smem_u32(&bar.v_clear[0]);
+  const uint64_t dk = tc::smem_desc_sw128(smem_u32(&pf.kv[0][0][0][0]), 16, 1024);
+  const uint64_t dv = tc::smem_desc_sw128(smem_u32(&pf.kv[0][0][0][0]), 64 * kTileN * 2, 1024);
+  const uint32_t kv_full = smem_u32(&bar.kv_full[0]), v_clear = smem_u32(&bar.v_clear[0]);
   const uint32_t s_free = smem_u32(&bar.s_free[0]), p_full = smem_u32(&bar.p_full[0]), o_free = smem_u32(&bar.o_free);
-  uint32_t kt = 0, vt = 0, ni = 0, no = 0;  // K tiles, V tiles, items, uses of O so far
+  uint32_t t = 0, ni = 0, no = 0;           // tiles taken from the ring, items, uses of O so far
   uint32_t ps = 3, pp = 0;                  // bit b: parity that S buffer b's next use, P buffer b's next product waits for
   uint32_t cleared = 0;                     // bit st: parity of the cleared tails of V stage st
   bool ok = true, issued = false;  // after a wait that ran out nothing more is issued
   // S of a step in buffer x, of both maps or one
   auto do_s = [&](uint64_t a, int x, bool m1, bool m2) {
-    const int st = kt & 1;
-    ok = ok && poll_wait(s_free + 8 * x, (ps >> x) & 1, k_full + 8 * st, (kt >> 1) & 1, abort);
+    const uint32_t st = t % kDiffStages;
+    ok = ok && poll_wait(s_free + 8 * x, (ps >> x) & 1, kv_full + 8 * st, (t / kDiffStages) & 1, abort);
     if (!ok) return;
     tc::fence_after_sync();
     const uint64_t b = dk + 2048u * st;
@@ -259,18 +292,18 @@ __device__ void diff_pf_mma(const RunParams& p, DiffPrefillBufs& pf, DiffPrefill
     if (m1) mma4<false>(d, a, 0, b, idesc_s, 0);
     if (m2) mma4<false>(d + kTileN, a + 1024u, 0, b + 1024u, idesc_s, 0);
     tc::mma_commit_warp(&bar.s_full[x]);
-    tc::mma_commit_warp(&bar.k_empty[st]);
+    tc::mma_commit_warp(&bar.kv_empty[st]);
     ps ^= 1u << x;
-    ++kt;
+    ++t;
     issued = true;
   };
   // P V of a step: weights in buffer b, or (two) hi in buffer 0 and lo in 1
   auto do_pv = [&](int b, bool two, bool first, bool last, bool tail) {
-    const int st = vt & 1;
+    const uint32_t st = t % kDiffStages;
     if (first) ok = ok && poll_wait(o_free, (no & 1) ^ 1, o_free, (no & 1) ^ 1, abort);
     if (two) ok = ok && poll_wait(p_full + 8, pp >> 1, p_full + 8, pp >> 1, abort);
-    ok = ok && poll_wait(p_full + 8 * b, (pp >> b) & 1, (tail ? v_clear : v_full) + 8 * st,
-                         tail ? (cleared >> st) & 1 : (vt >> 1) & 1, abort);
+    ok = ok && poll_wait(p_full + 8 * b, (pp >> b) & 1, (tail ? v_clear : kv_full) + 8 * st,
+                         tail ? (cleared >> st) & 1 : (t / kDiffStages) & 1, abort);
     if (!ok) return;
     tc::fence_after_sync();
     const uint64_t v = dv + 2048u * st;
@@ -284,14 +317,14 @@ __device__ void diff_pf_mma(const RunParams& p, DiffPrefillBufs& pf, DiffPrefill
       pp ^= 2u;
     }
     tc::mma_commit_warp(&bar.p_free[b]);
-    tc::mma_commit_warp(&bar.v_empty[st]);
+    tc::mma_commit_warp(&bar.kv_empty[st]);
     if (last) {
       tc::mma_commit_warp(&bar.o_ready);
       ++no;
     }
     if (tail) cleared ^= 1u << st;
     pp ^= 1u << b;
-    ++vt;
+    ++t;
   };
   // The P V of a step follows the S of the next step: what is pending across
   // passes and items, if anything.
@@ -338,6 +371,7 @@ __device__ void diff_pf_mma(const RunParams& p, DiffPrefillBufs& pf, DiffPrefill
     }
     ++ni;
   }
+  ++t;  // the place of the first K that a next item would have
   flush();
   if (issued) {  // no product may still run when the CTA leaves the phase
     tc::mma_commit_warp(&bar.drain);
