@@ -71,9 +71,8 @@ struct DiffPrefillBars {
   uint64_t o_ready, o_free, drain;
 };
 
-// Passes of an item: 0 then 1, or of a split unit's chunk 0, 2, 3.
-__device__ __forceinline__ int first_pv_pass(const Item& it) { return it.part >= 0 ? 2 : 1; }
-__device__ __forceinline__ int last_pass(const Item& it) { return it.part >= 0 ? 3 : 1; }
+// Passes of an item behind pass 0: pass 1, and of a split unit's chunk pass 2.
+__device__ __forceinline__ int pv_passes(const Item& it) { return it.part >= 0 ? 2 : 1; }
 
 // Whether the item's last KV tile reaches past the end of the request inside
 // a page: the V rows there may hold anything (0 * NaN would not be 0).
@@ -89,6 +88,7 @@ __device__ __forceinline__ bool item_v_tail(const Item& it, int page_size) {
 //   later passes      from t1 = t + pending + tiles, their steps numbered q
 //                     through: K(0) t1, K(q) t1 + 2q - 1, V(q) t1 + 2q + 2
 //   the next item     t1 + 2 steps - 1.
+// A split unit's chunk leaves nothing pending: its last V has the place before.
 // Returns which stages this warp loaded, and above them the phases of the last
 // loads.
 template <bool kV>
@@ -103,6 +103,7 @@ __device__ uint32_t diff_pf_produce(const RunParams& p, DiffPrefillBufs& pf, Dif
     if (!kV) tc::prefetch_tensormap(&p.tm_q);
   }
   uint32_t t = 0, ni = 0;  // an item's first place, items
+  int pending = 0;
   uint32_t armed = 0, armed_phase = 0;  // bit st: this warp loaded into stage st, and the phase of the last load
   int q_armed[2] = {-1, -1};
   Item ahead = load_item(p.iws, off_items, b0);
@@ -131,12 +132,14 @@ __device__ uint32_t diff_pf_produce(const RunParams& p, DiffPrefillBufs& pf, Dif
         q_armed[qb] = ph;
       }
     }
-    const int pending = ni > 0, steps = ntiles * (last_pass(it) - first_pv_pass(it) + 1);
+    const bool split = it.part >= 0;
+    const int steps = ntiles * pv_passes(it);
     const uint32_t t1 = t + pending + ntiles;
     int j = 0;
     for (int n = kV ? ntiles : 0; n < ntiles + steps; ++n) {
       const int q = n - ntiles;  // step of the passes behind pass 0
-      const uint32_t at = q < 0 ? t + (n > 0 ? pending + n : 0) : kV ? t1 + 2 * q + 2 : t1 + (q > 0 ? 2 * q - 1 : 0);
+      const uint32_t at = q < 0 ? t + (n > 0 ? pending + n : 0) : kV ? t1 + 2 * q + 2 - (split && q + 1 == steps)
+                                                                           : t1 + (q > 0 ? 2 * q - 1 : 0);
       const uint32_t st = at % kDiffStages, ph = (at / kDiffStages) & 1;
       const int32_t cur = next;
       const int tile = j;
@@ -173,7 +176,8 @@ __device__ uint32_t diff_pf_produce(const RunParams& p, DiffPrefillBufs& pf, Dif
         if (lane == 0) mbar_arrive(&bar.v_clear[st]);
       }
     }
-    t = t1 + 2 * steps - 1;
+    t = t1 + 2 * steps - (split ? 0 : 1);
+    pending = split ? 0 : 1;
     ++ni;
   }
   if (!kV && lane == 0) {  // every Q load has landed before the CTA moves on
@@ -281,41 +285,34 @@ __device__ void diff_pf_mma(const RunParams& p, DiffPrefillBufs& pf, DiffPrefill
   uint32_t ps = 3, pp = 0;                  // bit b: parity that S buffer b's next use, P buffer b's next product waits for
   uint32_t cleared = 0;                     // bit st: parity of the cleared tails of V stage st
   bool ok = true, issued = false;  // after a wait that ran out nothing more is issued
-  // S of a step in buffer x, of both maps or one
-  auto do_s = [&](uint64_t a, int x, bool m1, bool m2) {
+  // S of a step in buffer x, of both maps or of map 2 alone
+  auto do_s = [&](uint64_t a, int x, bool both) {
     const uint32_t st = t % kDiffStages;
     ok = ok && poll_wait(s_free + 8 * x, (ps >> x) & 1, kv_full + 8 * st, (t / kDiffStages) & 1, abort);
     if (!ok) return;
     tc::fence_after_sync();
     const uint64_t b = dk + 2048u * st;
     const uint32_t d = tmem + 2 * kTileN * x;
-    if (m1) mma4<false>(d, a, 0, b, idesc_s, 0);
-    if (m2) mma4<false>(d + kTileN, a + 1024u, 0, b + 1024u, idesc_s, 0);
+    if (both) mma4<false>(d, a, 0, b, idesc_s, 0);
+    mma4<false>(d + kTileN, a + 1024u, 0, b + 1024u, idesc_s, 0);
     tc::mma_commit_warp(&bar.s_full[x]);
     tc::mma_commit_warp(&bar.kv_empty[st]);
     ps ^= 1u << x;
     ++t;
     issued = true;
   };
-  // P V of a step: weights in buffer b, or (two) hi in buffer 0 and lo in 1
-  auto do_pv = [&](int b, bool two, bool first, bool last, bool tail) {
+  // P V of a step, weights in buffer b, accumulated at column d
+  auto do_pv = [&](uint32_t d, int b, bool first, bool last, bool tail) {
     const uint32_t st = t % kDiffStages;
     if (first) ok = ok && poll_wait(o_free, (no & 1) ^ 1, o_free, (no & 1) ^ 1, abort);
-    if (two) ok = ok && poll_wait(p_full + 8, pp >> 1, p_full + 8, pp >> 1, abort);
     ok = ok && poll_wait(p_full + 8 * b, (pp >> b) & 1, (tail ? v_clear : kv_full) + 8 * st,
                          tail ? (cleared >> st) & 1 : (t / kDiffStages) & 1, abort);
     if (!ok) return;
     tc::fence_after_sync();
     const uint64_t v = dv + 2048u * st;
-    const uint32_t w = tmem + kDiffTmemP + 64 * b, d = tmem + kDiffTmemO;
+    const uint32_t w = tmem + kDiffTmemP + 64 * b;
     mma4<true>(d, 0, w, v, idesc_pv, first ? 0u : 1u);
     mma4<true>(d, 0, w + 32, v + 512u, idesc_pv, 1u);
-    if (two) {
-      mma4<true>(d, 0, w + 64, v, idesc_pv, 1u);
-      mma4<true>(d, 0, w + 96, v + 512u, idesc_pv, 1u);
-      tc::mma_commit_warp(&bar.p_free[1]);
-      pp ^= 2u;
-    }
     tc::mma_commit_warp(&bar.p_free[b]);
     tc::mma_commit_warp(&bar.kv_empty[st]);
     if (last) {
@@ -329,13 +326,15 @@ __device__ void diff_pf_mma(const RunParams& p, DiffPrefillBufs& pf, DiffPrefill
   // The P V of a step follows the S of the next step: what is pending across
   // passes and items, if anything.
   struct {
-    bool any, two, first, last, tail;
+    bool any, first, last, tail;
     int b;
-  } pv{false, false, false, false, false, 0};
-  auto flush = [&] {
-    if (pv.any) do_pv(pv.b, pv.two, pv.first, pv.last, pv.tail);
+  } pv{false, false, false, false, 0};
+  auto flush = [&](uint32_t d) {
+    if (pv.any) do_pv(d, pv.b, pv.first, pv.last, pv.tail);
     pv.any = false;
   };
+  const uint32_t o_col = tmem + kDiffTmemO;
+  bool o2 = false;  // S_2 of a split unit's chunk is in the first S buffer
   Item next = load_item(p.iws, off_items, b0);
   for (int32_t i = b0; i < b1 && ok; ++i) {
     const Item it = next;
@@ -346,33 +345,36 @@ __device__ void diff_pf_mma(const RunParams& p, DiffPrefillBufs& pf, DiffPrefill
     const uint32_t qb = ni & 1, q_full = smem_u32(&bar.q_full[0]) + 8 * qb;
     const uint64_t a = dq + 2048u * qb;
     ok = poll_wait(q_full, (ni >> 1) & 1, q_full, (ni >> 1) & 1, abort);
-    do_s(a, 0, true, true);
-    flush();
+    if (ok && o2) ok = poll_wait(o_free, (no & 1) ^ 1, o_free, (no & 1) ^ 1, abort);
+    o2 = it.part >= 0;
+    do_s(a, 0, true);
+    flush(o_col);
     for (int j = 1; j < ntiles && ok; ++j) {
       // S buffer 1: O's and P's columns, once the item before is read out
       if (j == 1) ok = poll_wait(o_free, (no & 1) ^ 1, o_free, (no & 1) ^ 1, abort);
-      do_s(a, j & 1, true, true);
+      do_s(a, j & 1, true);
     }
-    if (it.part < 0) {
-      do_s(a, 0, true, true);
+    do_s(a, 0, true);
+    for (int j = 1; j < ntiles && ok; ++j) {
+      do_s(a, 0, true);
+      do_pv(o_col, (j - 1) & 1, j == 1, false, false);
+    }
+    pv = {true, ntiles == 1, it.part < 0, tail, (ntiles - 1) & 1};
+    if (it.part >= 0) {
+      // pass 2 accumulates in the columns of map 1's S, which it does not use
+      do_s(a, 0, false);
+      flush(o_col);
       for (int j = 1; j < ntiles && ok; ++j) {
-        do_s(a, 0, true, true);
-        do_pv((j - 1) & 1, false, j == 1, false, false);
+        do_s(a, 0, false);
+        do_pv(tmem, (j - 1) & 1, j == 1, false, false);
       }
-      pv = {true, false, ntiles == 1, true, tail, (ntiles - 1) & 1};
-    } else {
-      for (int m = 0; m < 2; ++m) {
-        for (int j = 0; j < ntiles && ok; ++j) {
-          do_s(a, 0, m == 0, m == 1);
-          flush();
-          pv = {true, true, j == 0, j + 1 == ntiles, tail && j + 1 == ntiles, 0};
-        }
-      }
+      pv = {true, ntiles == 1, true, tail, (ntiles - 1) & 1};
+      flush(tmem);
     }
     ++ni;
   }
-  ++t;  // the place of the first K that a next item would have
-  flush();
+  if (pv.any) ++t;  // the place of the first K that a next item would have
+  flush(o_col);
   if (issued) {  // no product may still run when the CTA leaves the phase
     tc::mma_commit_warp(&bar.drain);
     if (lane == 0) mbar_wait_drain(&bar.drain, 0);
@@ -452,16 +454,16 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
     }
     bool ok = true;
     const float lam = live ? __ldg(dp.lambda + head) : 0.f;
-    // This warpgroup's 32 logits a map of tile j in S buffer x (kinds 2 and 3:
-    // of one map); S goes back to the MMA warp.
-    auto load_s = [&](int x, bool m1, bool m2, uint32_t (&a)[32], uint32_t (&b)[32]) {
+    // This warpgroup's 32 logits of both maps (or of map 2 alone) of tile j in
+    // S buffer x; S goes back to the MMA warp.
+    auto load_s = [&](int x, bool both, uint32_t (&a)[32], uint32_t (&b)[32]) {
       ok = ok && warp_wait(&bar.s_full[x], (x ? ns[1] : ns[0]) & 1, abort);
       ns[0] += x == 0;
       ns[1] += x;
       tc::fence_after_sync();
       const uint32_t col = tl + 2 * kTileN * x + kDiffKeys * wg;
-      if (m1) tc::tmem_ld32(col, a);
-      if (m2) tc::tmem_ld32(col + kTileN, b);
+      if (both) tc::tmem_ld32(col, a);
+      tc::tmem_ld32(col + kTileN, b);
       tc::tmem_ld_wait();
       tc::fence_before_sync();
       __syncwarp();
@@ -475,6 +477,18 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
       }
     };
 
+    // This thread's weights into P buffer b.
+    auto store_p = [&](int b, const uint32_t (&pk)[16]) {
+      ok = ok && warp_wait(&bar.p_free[b], ((b ? np[1] : np[0]) & 1) ^ 1, abort);
+      np[0] += b == 0;
+      np[1] += b;
+      tc::fence_after_sync();
+      tc::tmem_st16(tl + kDiffTmemP + 64 * b + 16 * wg, pk);
+      tc::tmem_st_wait();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.p_full[b]);
+    };
     // ---- pass 0: a reference m and the sum of 2^(s - m) per map.  The
     // reference is the maximum of the first tile that the row sees; it only
     // moves when a sum passes 2^100, so the loop has no maximum to take.
@@ -482,14 +496,26 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
     bool have_m = false;  // of every row of the warp
     for (int j = 0; j < ntiles; ++j) {
       uint32_t s[2][32];
-      load_s(j & 1, true, true, s[0], s[1]);
+      load_s(j & 1, true, s[0], s[1]);
       if (j >= c2) continue;
       if (j < c0 || j >= c1) {
         mask(j, s[0]);
         mask(j, s[1]);
       }
-      if (have_m) {
-        const float2 n0 = make_float2(-m[0], -m[0]), n1 = make_float2(-m[1], -m[1]);
+      for (bool move = !have_m;; move = true) {
+        if (move) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float top = max32(s[x]) * sc;
+            if (top > m[x] + kLazyRescale) {
+              l[x] *= ex2(m[x] - top);  // 0 * 0 before the first key
+              m[x] = top;
+            }
+          }
+          have_m = __all_sync(0xffffffffu, m[0] != -INFINITY && m[1] != -INFINITY);
+        }
+        const float ms0 = m[0] == -INFINITY ? 0.f : m[0], ms1 = m[1] == -INFINITY ? 0.f : m[1];
+        const float2 n0 = make_float2(-ms0, -ms0), n1 = make_float2(-ms1, -ms1);
         float2 sum[2][2];
 #pragma unroll
         for (int a = 0; a < 2; ++a) sum[0][a] = sum[1][a] = make_float2(0.f, 0.f);
@@ -502,23 +528,12 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
         }
         const float2 t0 = add2(sum[0][0], sum[0][1]), t1 = add2(sum[1][0], sum[1][1]);
         const float l0 = l[0] + (t0.x + t0.y), l1 = l[1] + (t1.x + t1.y);
-        if (!__any_sync(0xffffffffu, !(fmaxf(l0, l1) < 1.2676506e30f))) {  // 2^100
+        if (move || !__any_sync(0xffffffffu, !(fmaxf(l0, l1) < 1.2676506e30f))) {  // 2^100
           l[0] = l0;
           l[1] = l1;
-          continue;
+          break;
         }
       }
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const float top = max32(s[x]) * sc;
-        const float m_new = top > m[x] + kLazyRescale ? top : m[x];
-        l[x] *= m_new == m[x] ? 1.f : ex2(m[x] - m_new);
-        m[x] = m_new;
-        const float ms = m_new == -INFINITY ? 0.f : m_new;
-#pragma unroll
-        for (int e = 0; e < 32; ++e) l[x] += ex2(__uint_as_float(s[x][e]) * sc - ms);
-      }
-      have_m = __all_sync(0xffffffffu, m[0] != -INFINITY && m[1] != -INFINITY);
     }
     // The warpgroups' statistics of a row together, in the same order in all.
     // (`stats` of the item before has been read: this item's S needed its
@@ -549,50 +564,64 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
       if (wg == x && ll > 0.f) lse = (m[x] + log2l[x]) * 0.69314718055994531f;
     }
 
-    if (item.part < 0) {
-      // ---- pass 1: weights w_1 - lambda w_2, scaled by 2^sigma so that they
-      // stay below 2^14 and small ones inside an fp16's normal range
-      const float sigma = kWeightScale - (fabsf(lam) > 1.f ? __log2f(fabsf(lam)) : 0.f);
-      const float a1 = m[0] + log2l[0] - sigma, a2 = m[1] + log2l[1] - sigma;
-      const float2 n1 = make_float2(-a1, -a1), n2 = make_float2(-a2, -a2), nl = make_float2(-lam, -lam);
+    // ---- pass 1: weights w_1 - lambda w_2, scaled by 2^sigma so that they
+    // stay below 2^14 and small ones inside an fp16's normal range
+    const float sigma = kWeightScale - (fabsf(lam) > 1.f ? __log2f(fabsf(lam)) : 0.f);
+    const float a1 = m[0] + log2l[0] - sigma, a2 = m[1] + log2l[1] - sigma;
+    const float2 n1 = make_float2(-a1, -a1), n2 = make_float2(-a2, -a2), nl = make_float2(-lam, -lam);
+    for (int j = 0; j < ntiles; ++j) {
+      const int b = j & 1;
+      uint32_t s1[32], s2[32], pk[16];
+      load_s(0, true, s1, s2);
+      if (j < c0 || j >= c1) {
+        mask(j, s1);
+        mask(j, s2);
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float2 x = fma2(make_float2(__uint_as_float(s1[2 * e]), __uint_as_float(s1[2 * e + 1])), cc, n1);
+        const float2 y = fma2(make_float2(__uint_as_float(s2[2 * e]), __uint_as_float(s2[2 * e + 1])), cc, n2);
+        const float2 w = fma2(make_float2(ex2(y.x), ex2(y.y)), nl, make_float2(ex2(x.x), ex2(x.y)));
+        pk[e] = tc::pack2<T>(w.x, w.y);
+      }
+      store_p(b, pk);
+    }
+    const float unscale = l[0] > 0.f ? ex2(-sigma) : 0.f;
+    if (item.part >= 0) {
+      // ---- pass 2, of a split unit's chunk: map 2 alone, accumulated beside
+      // pass 1's result (which is S_1 - lambda S_2 of the chunk)
+      const float a = m[1] + log2l[1] - kWeightScale;
+      const float2 n = make_float2(-a, -a);
       for (int j = 0; j < ntiles; ++j) {
-        const int b = j & 1;
-        uint32_t s1[32], s2[32], pk[16];
-        load_s(0, true, true, s1, s2);
-        if (j < c0 || j >= c1) {
-          mask(j, s1);
-          mask(j, s2);
-        }
+        uint32_t s[32], pk[16];
+        load_s(0, false, s, s);
+        if (j < c0 || j >= c1) mask(j, s);
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const float2 x = fma2(make_float2(__uint_as_float(s1[2 * e]), __uint_as_float(s1[2 * e + 1])), cc, n1);
-          const float2 y = fma2(make_float2(__uint_as_float(s2[2 * e]), __uint_as_float(s2[2 * e + 1])), cc, n2);
-          const float2 w = fma2(make_float2(ex2(y.x), ex2(y.y)), nl, make_float2(ex2(x.x), ex2(x.y)));
-          pk[e] = tc::pack2<T>(w.x, w.y);
+          const float2 x = fma2(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), cc, n);
+          pk[e] = tc::pack2<T>(ex2(x.x), ex2(x.y));
         }
-        ok = ok && warp_wait(&bar.p_free[b], (np[b] & 1) ^ 1, abort);
-        ++np[b];
-        tc::fence_after_sync();
-        tc::tmem_st16(tl + kDiffTmemP + 64 * b + 16 * wg, pk);
-        tc::tmem_st_wait();
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.p_full[b]);
+        store_p(j & 1, pk);
       }
-      if (p.lse && wg < 2 && live && !*abort) p.lse[(tok * p.num_qo_heads + head) * 2 + wg] = lse;
-      // ---- the output: this warpgroup's 32 dims of the row
-      ok = ok && warp_wait(&bar.o_ready, no & 1, abort);
-      ++no;
-      tc::fence_after_sync();
-      uint32_t y[32];
-      tc::tmem_ld32(tl + kDiffTmemO + kDiffKeys * wg, y);
+    }
+    // this warpgroup's 32 dims of the accumulators' rows
+    ok = ok && warp_wait(&bar.o_ready, no & 1, abort);
+    ++no;
+    tc::fence_after_sync();
+    uint32_t y[32];
+    tc::tmem_ld32(tl + kDiffTmemO + kDiffKeys * wg, y);
+    auto val = [&](int e) { return __uint_as_float(y[e]); };
+    auto release_o = [&] {
       tc::tmem_ld_wait();
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.o_free);
-      const float unscale = l[0] > 0.f ? ex2(-sigma) : 0.f;
+    };
+    if (item.part < 0) {
+      // ---- the output
+      release_o();
+      if (p.lse && wg < 2 && live && !*abort) p.lse[(tok * p.num_qo_heads + head) * 2 + wg] = lse;
       float f = unscale * dp.out_scale;
-      auto val = [&](int e) { return __uint_as_float(y[e]); };
       if (dp.norm_w) {
         float ss = 0.f;
 #pragma unroll
@@ -634,59 +663,28 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
         }
       }
     } else {
-      // ---- passes 2 and 3: each map's partial state, weights as hi + lo
-#pragma unroll 1
-      for (int x = 0; x < 2; ++x) {
-        const float a = m[x] + log2l[x] - kWeightScale;
-        const float2 n = make_float2(-a, -a);
-        for (int j = 0; j < ntiles; ++j) {
-          uint32_t s[32], hi[16], low[16];
-          load_s(0, x == 0, x == 1, s, s);
-          if (j < c0 || j >= c1) mask(j, s);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float2 y = fma2(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), cc, n);
-            const float2 w = make_float2(ex2(y.x), ex2(y.y));
-            hi[e] = tc::pack2<T>(w.x, w.y);
-            const float2 hf = Elem<T>::to_float2(hi[e]);
-            low[e] = tc::pack2<T>(w.x - hf.x, w.y - hf.y);
-          }
-          ok = ok && warp_wait(&bar.p_free[0], (np[0] & 1) ^ 1, abort);
-          ok = ok && warp_wait(&bar.p_free[1], (np[1] & 1) ^ 1, abort);
-          ++np[0];
-          ++np[1];
-          tc::fence_after_sync();
-          tc::tmem_st16(tl + kDiffTmemP + 16 * wg, hi);
-          tc::tmem_st16(tl + kDiffTmemP + 64 + 16 * wg, low);
-          tc::tmem_st_wait();
-          tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&bar.p_full[0]);
-            mbar_arrive(&bar.p_full[1]);
-          }
-        }
-        ok = ok && warp_wait(&bar.o_ready, no & 1, abort);
-        ++no;
-        tc::fence_after_sync();
-        const int64_t prw = int64_t(item.part) + x * nrows + r;
-        const float inv = l[x] > 0.f ? ex2(-kWeightScale) : 0.f;
-        uint32_t ov[32];
-        tc::tmem_ld32(tl + kDiffTmemO + kDiffKeys * wg, ov);
-        tc::tmem_ld_wait();
-        if (live && !*abort) {
-          float4* dst = reinterpret_cast<float4*>(p.fws + p.partial_o_offset + prw * kHeadDim + kDiffKeys * wg);
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            dst[e] = make_float4(__uint_as_float(ov[4 * e]) * inv, __uint_as_float(ov[4 * e + 1]) * inv,
-                                 __uint_as_float(ov[4 * e + 2]) * inv, __uint_as_float(ov[4 * e + 3]) * inv);
-        }
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.o_free);
-      }
+      // ---- both maps' partial states.  In what the merge adds up S_2 has the
+      // small weight lambda (W_1 - W_2), of the chunk's shares of the two maps,
+      // so the rounding of its weights is as small against the result.
+      uint32_t y2[32];
+      tc::tmem_ld32(tl + kDiffKeys * wg, y2);
+      release_o();
       if (elected) mbar_arrive(&bar.q_empty[ni & 1]);
-      if (wg < 2 && live && !*abort) p.fws[int64_t(item.part) + wg * nrows + r] = lse;
+      if (live && !*abort) {
+        const float unscale2 = l[1] > 0.f ? ex2(-kWeightScale) : 0.f;
+        float4* const dst =
+            reinterpret_cast<float4*>(p.fws + p.partial_o_offset + (int64_t(item.part) + r) * kHeadDim + kDiffKeys * wg);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float4 b = make_float4(__uint_as_float(y2[4 * e]) * unscale2, __uint_as_float(y2[4 * e + 1]) * unscale2,
+                                       __uint_as_float(y2[4 * e + 2]) * unscale2,
+                                       __uint_as_float(y2[4 * e + 3]) * unscale2);
+          dst[e] = make_float4(val(4 * e) * unscale + lam * b.x, val(4 * e + 1) * unscale + lam * b.y,
+                               val(4 * e + 2) * unscale + lam * b.z, val(4 * e + 3) * unscale + lam * b.w);
+          dst[nrows * (kHeadDim / 4) + e] = b;
+        }
+        if (wg < 2) p.fws[int64_t(item.part) + wg * nrows + r] = lse;
+      }
     }
     ++ni;
   }
