@@ -339,10 +339,9 @@ __device__ __forceinline__ void diff_slice(const uint16_t* ks, const uint16_t* v
 // each map at dims 64 h + 2 lane: the norm, the scale and the store.
 template <typename T>
 __device__ __forceinline__ void diff_store_row(const DiffParams& dp, const float2 (&s1)[2], const float2 (&s2)[2],
-                                               int64_t tok, int head) {
+                                               float lam, int64_t tok, int head) {
   const RunParams& p = dp.run;
   const int lane = threadIdx.x & 31;
-  const float lam = __ldg(dp.lambda + head);
   float y[4];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -490,7 +489,7 @@ __device__ __forceinline__ uint32_t diff_pass(const DiffParams& dp, DiffSmem& sm
       const int tq = row / G, head = item.hk * G + (row - tq * G);
       const int64_t tok = int64_t(rq.qo_start) + tq;
       const int nrows = item.row1 - item.row0;
-      if (item.part < 0) diff_store_row<T>(dp, acc[k][0], acc[k][1], tok, head);
+      if (item.part < 0) diff_store_row<T>(dp, acc[k][0], acc[k][1], __ldg(dp.lambda + head), tok, head);
 #pragma unroll
       for (int mp = 0; mp < 2; ++mp) {
         const float lse = wsum[k][mp] > 0.f ? (mmax[k][mp] + __log2f(wsum[k][mp])) * 0.69314718055994531f : -INFINITY;
@@ -662,27 +661,66 @@ __global__ void __launch_bounds__(256) diff_merge_kernel(const __grid_constant__
   const RunParams& p = dp.run;
   const int32_t* iws = p.iws;
   const int lane = threadIdx.x & 31;
-  const int32_t rows_max = iws[FI_H_CASCADE_ROWS_MAX];
-  const int64_t tasks = int64_t(iws[FI_H_NUM_MERGE]) * rows_max;
-  const int32_t* merge = iws + iws[FI_H_OFF_MERGE];
+  const int32_t rows_max = iws[FI_H_CASCADE_ROWS_MAX], units = iws[FI_H_NUM_MERGE];
+  const int4* merge = reinterpret_cast<const int4*>(iws + iws[FI_H_OFF_MERGE]);
   const int32_t* reqs = iws + iws[FI_H_OFF_REQUESTS];
-  const bool mine = iws[FI_H_MAGIC] == FI_PLAN_MAGIC_DIFF;
+  if (iws[FI_H_MAGIC] != FI_PLAN_MAGIC_DIFF || units < 1 || rows_max < 1) {
+    grid_dependency_wait();
+    return;
+  }
+  // Row pr of a unit per warp, rows_max rows a unit.  A unit's words are
+  // fetched a task ahead, the first before the run has ended.
+  const int32_t warps = int32_t(gridDim.x * (blockDim.x >> 5));
+  const int32_t me = int32_t(blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5));
+  const int32_t unit_step = warps / rows_max, row_step = warps % rows_max;
+  int32_t unit = me / rows_max, row = me % rows_max;
+  int4 next0 = make_int4(0, 0, 0, 0), next1 = next0;
+  auto fetch = [&] {
+    if (unit < units) {
+      next0 = __ldg(merge + FI_MERGE_INTS / 4 * int64_t(unit));
+      next1 = __ldg(merge + FI_MERGE_INTS / 4 * int64_t(unit) + 1);
+    }
+  };
+  fetch();
   grid_dependency_wait();
-  if (!mine || iws[FI_H_STATUS] != 0) return;
-  const int64_t warps = int64_t(gridDim.x) * (blockDim.x >> 5);
-  for (int64_t task = int64_t(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); task < tasks; task += warps) {
-    const int4* mu = reinterpret_cast<const int4*>(merge + FI_MERGE_INTS * (task / rows_max));
-    const int4 u0 = __ldg(mu), u1 = __ldg(mu + 1);  // {b, hk, row0, row1}, {n, base, late, 0}
-    const int pr = int(task % rows_max), nrows = u0.w - u0.z, n = u1.x;
+  if (iws[FI_H_STATUS] != 0) return;
+  while (unit < units) {
+    const int4 u0 = next0, u1 = next1;  // {b, hk, row0, row1}, {n, base, late, 0}
+    const int pr = row, nrows = u0.w - u0.z, n = u1.x;
+    unit += unit_step;
+    row += row_step;
+    if (row >= rows_max) {
+      row -= rows_max;
+      ++unit;
+    }
+    fetch();
     if (pr >= nrows) continue;
+    const int qrow = u0.z + pr, tq = qrow / p.group, head = u0.y * p.group + (qrow - tq * p.group);
+    const float lam = __ldg(dp.lambda + head);
+    const int64_t tok = int64_t(__ldg(reqs + FI_REQ_INTS * u0.x)) + tq;
     // Partial row of chunk c: row0[map] + c step.  Lane c holds chunk c's two
-    // log-sum-exps (32 at a time); the partial outputs are loaded kMergeAhead
-    // chunks ahead of their use.
+    // log-sum-exps (32 at a time); kMergeAhead chunks' partial outputs are in
+    // flight, the first of them beside the log-sum-exps.
     const int64_t step = 2 * nrows, row0[2] = {int64_t(u1.y) + pr, int64_t(u1.y) + nrows + pr};
-    float M[2] = {-INFINITY, -INFINITY}, L[2] = {0.f, 0.f};
-    for (int c = lane; c < n; c += 32) {
-      M[0] = fmaxf(M[0], __ldcg(p.fws + row0[0] + c * step));
-      M[1] = fmaxf(M[1], __ldcg(p.fws + row0[1] + c * step));
+    float2 v[kMergeAhead][2][2];
+    auto load = [&](int c) {
+#pragma unroll
+      for (int u = 0; u < kMergeAhead; ++u)
+#pragma unroll
+        for (int mp = 0; mp < 2; ++mp) {
+          const float2* src = reinterpret_cast<const float2*>(
+                                  p.fws + p.partial_o_offset + (row0[mp] + (c + u) * step) * kHeadDim) + lane;
+          v[u][mp][0] = c + u < n ? __ldcg(src) : make_float2(0.f, 0.f);
+          v[u][mp][1] = c + u < n ? __ldcg(src + 32) : make_float2(0.f, 0.f);
+        }
+    };
+    load(0);
+    auto lse_of = [&](int c, int mp) { return c < n ? __ldcg(p.fws + row0[mp] + c * step) : -INFINITY; };
+    const float e0[2] = {lse_of(lane, 0), lse_of(lane, 1)};
+    float M[2] = {e0[0], e0[1]}, L[2] = {0.f, 0.f};
+    for (int c = lane + 32; c < n; c += 32) {
+      M[0] = fmaxf(M[0], lse_of(c, 0));
+      M[1] = fmaxf(M[1], lse_of(c, 1));
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
@@ -692,41 +730,28 @@ __global__ void __launch_bounds__(256) diff_merge_kernel(const __grid_constant__
     float2 a[2][2];
 #pragma unroll
     for (int mp = 0; mp < 2; ++mp) a[mp][0] = a[mp][1] = make_float2(0.f, 0.f);
-    for (int c0 = 0; c0 < n; c0 += 32) {
-      float w[2];
+    float w[2] = {0.f, 0.f};
+    for (int c = 0; c < n; c += kMergeAhead) {
+      if ((c & 31) == 0) {
 #pragma unroll
-      for (int mp = 0; mp < 2; ++mp) {
-        w[mp] = 0.f;
-        if (c0 + lane < n && M[mp] != -INFINITY)
-          w[mp] = ex2((__ldcg(p.fws + row0[mp] + (c0 + lane) * step) - M[mp]) * 1.4426950408889634f);
-        L[mp] += w[mp];
+        for (int mp = 0; mp < 2; ++mp) {
+          const float e = c == 0 ? e0[mp] : lse_of(c + lane, mp);
+          w[mp] = M[mp] != -INFINITY ? ex2((e - M[mp]) * 1.4426950408889634f) : 0.f;
+          L[mp] += w[mp];
+        }
       }
-      const int cn = min(32, n - c0);
-      for (int g = 0; g < cn; g += kMergeAhead) {
-        float2 v[kMergeAhead][2][2];
 #pragma unroll
-        for (int u = 0; u < kMergeAhead; ++u)
+      for (int u = 0; u < kMergeAhead; ++u)
 #pragma unroll
-          for (int mp = 0; mp < 2; ++mp) {
-            const int64_t r = row0[mp] + min(c0 + g + u, n - 1) * step;
-            const float2* src = reinterpret_cast<const float2*>(p.fws + p.partial_o_offset + r * kHeadDim) + lane;
-            v[u][mp][0] = __ldcg(src);
-            v[u][mp][1] = __ldcg(src + 32);
+        for (int mp = 0; mp < 2; ++mp) {
+          const float wu = __shfl_sync(0xffffffffu, w[mp], (c + u) & 31);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            a[mp][h].x += wu * v[u][mp][h].x;
+            a[mp][h].y += wu * v[u][mp][h].y;
           }
-#pragma unroll
-        for (int u = 0; u < kMergeAhead; ++u)
-#pragma unroll
-          for (int mp = 0; mp < 2; ++mp) {
-            const float wu = __shfl_sync(0xffffffffu, w[mp], (g + u) & 31);
-            if (g + u < cn) {
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                a[mp][h].x += wu * v[u][mp][h].x;
-                a[mp][h].y += wu * v[u][mp][h].y;
-              }
-            }
-          }
-      }
+        }
+      if (c + kMergeAhead < n) load(c + kMergeAhead);
     }
     float2 s[2][2];
     float lse[2];
@@ -737,9 +762,7 @@ __global__ void __launch_bounds__(256) diff_merge_kernel(const __grid_constant__
       for (int h = 0; h < 2; ++h) s[mp][h] = make_float2(a[mp][h].x * inv, a[mp][h].y * inv);
       lse[mp] = sum > 0.f ? M[mp] + __logf(sum) : -INFINITY;
     }
-    const int row = u0.z + pr, tq = row / p.group, head = u0.y * p.group + (row - tq * p.group);
-    const int64_t tok = int64_t(__ldg(reqs + FI_REQ_INTS * u0.x)) + tq;
-    diff_store_row<T>(dp, s[0], s[1], tok, head);
+    diff_store_row<T>(dp, s[0], s[1], lam, tok, head);
     if (p.lse && lane < 2) p.lse[(tok * p.num_qo_heads + head) * 2 + lane] = lane ? lse[1] : lse[0];
   }
 }

@@ -282,7 +282,7 @@ __device__ void diff_pf_mma(const RunParams& p, DiffPrefillBufs& pf, DiffPrefill
   const uint32_t kv_full = smem_u32(&bar.kv_full[0]), v_clear = smem_u32(&bar.v_clear[0]);
   const uint32_t s_free = smem_u32(&bar.s_free[0]), p_full = smem_u32(&bar.p_full[0]), o_free = smem_u32(&bar.o_free);
   uint32_t t = 0, ni = 0, no = 0;           // tiles taken from the ring, items, uses of O so far
-  uint32_t ps = 3, pp = 0;                  // bit b: parity that S buffer b's next use, P buffer b's next product waits for
+  uint32_t ps = 3, pp = 0;                  // bit b: parity that the next use of S, P buffer b waits for
   uint32_t cleared = 0;                     // bit st: parity of the cleared tails of V stage st
   bool ok = true, issued = false;  // after a wait that ran out nothing more is issued
   // S of a step in buffer x, of both maps or of map 2 alone
@@ -672,8 +672,8 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
       if (elected) mbar_arrive(&bar.q_empty[ni & 1]);
       if (live && !*abort) {
         const float unscale2 = l[1] > 0.f ? ex2(-kWeightScale) : 0.f;
-        float4* const dst =
-            reinterpret_cast<float4*>(p.fws + p.partial_o_offset + (int64_t(item.part) + r) * kHeadDim + kDiffKeys * wg);
+        float4* const dst = reinterpret_cast<float4*>(p.fws + p.partial_o_offset +
+                                                      (int64_t(item.part) + r) * kHeadDim + kDiffKeys * wg);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float4 b = make_float4(__uint_as_float(y2[4 * e]) * unscale2, __uint_as_float(y2[4 * e + 1]) * unscale2,
