@@ -36,6 +36,8 @@ Rule:
     ctas = num_ctas, except for the decode class when the prefill-class
     items (n_pre of them: per 256-row unit, its ranges' chunk counts, at
     least 1) are at least one and at most num_ctas / 2: then num_ctas - n_pre.
+    A differential plan with fewer than three CTAs a prefill-class unit takes
+    four times the prefill class's min_chunk.
     A multi-head unit's chunk is max(granule, ceil(ceil(chunk / H) / granule)
     * granule) keys (the K/V bytes of a one-head chunk).
  4. A unit with kv_eff = 0 gives one empty item.  Otherwise each range
@@ -303,7 +305,9 @@ def _plan(cfg, reqs, num_shared, shared_page_size, block_of, total_qo, num_qo_he
         want = max(min_chunk, _ceil_div(total[T], ctas * cfg["split_factor"]))
         return _ceil_div(want, granule[T]) * granule[T]
 
-    chunk = {TILE_PREFILL: pick(TILE_PREFILL, cfg["prefill_min_chunk"], C)}
+    units_pre = sum(u[3] == TILE_PREFILL for u in units)
+    min_pre = cfg["prefill_min_chunk"] * (4 if diff and 3 * units_pre > C else 1)
+    chunk = {TILE_PREFILL: pick(TILE_PREFILL, min_pre, C)}
     # prefill-class items; the decode class counts the CTAs they leave free when they take at most half
     n_pre = sum(max(1, sum(_ceil_div(e - s, chunk[TILE_PREFILL]) for s, e in u[6]))
                 for u in units if u[3] == TILE_PREFILL)
