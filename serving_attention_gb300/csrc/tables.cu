@@ -175,14 +175,16 @@ __global__ void __launch_bounds__(kTableThreads) step_tables_kernel(const __grid
   auto page_id = [&](int b, int p, int had) {
     return p < had ? a.table[b * a.table_stride + p] : __ldg(a.free_pages + head + s_new[gap(b)] + (p - had));
   };
-  // A warp takes 32 * kTableAhead entries in a row: one search for the first,
-  // a walk from there (short, but for requests without pages in between); the
-  // loads of all go out before the first is stored.
+  // A warp takes a run of entries: one search for the first, a walk from there
+  // (short, but for requests without pages in between).  It goes 32 *
+  // kTableAhead entries at a time, whose loads go out before the first store.
   constexpr int kSpan = 32 * kTableAhead;
-  for (int64_t w0 = (gtid >> 5) * kSpan; w0 < total.pages; w0 += (threads >> 5) * kSpan) {
+  const int64_t warps = threads >> 5, run = (total.pages + warps * kSpan - 1) / (warps * kSpan) * kSpan;
+  const int64_t first = (gtid >> 5) * run, last = min(total.pages, first + run);
+  int b = first < last ? find(s_kv, B, int(first)) : 0;
+  for (int64_t w0 = first; w0 < last; w0 += kSpan) {
     int32_t id[kTableAhead];
     int32_t* slot[kTableAhead];  // of a new page in the table
-    int b = find(s_kv, B, int(w0));
 #pragma unroll
     for (int u = 0; u < kTableAhead; ++u) {
       const int64_t e = w0 + 32 * u + lane;
