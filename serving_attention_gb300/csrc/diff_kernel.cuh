@@ -104,24 +104,35 @@ __device__ __forceinline__ int diff_passes(int nrows) { return (nrows + 15) / 16
 
 // ---------------------------------------------------------------- producers
 
-// Warps 0..3 copy a stage's K and V rows with 16-byte asynchronous copies,
-// 32 tokens each, any page size and strides.  Lane l holds the page id of
-// token l (the next stage's loaded one stage ahead); half a warp copies one
+// Eight warps copy a stage's rows with 16-byte asynchronous copies, any page
+// size and strides: 32 tokens each, warps 0..3 of K and the first four behind
+// the consumers of V (a stage took four warps, both tensors each, 4900 cycles,
+// most of them between the instructions of a warp).  Lane l holds the page id
+// of token l (the next stage's loaded one stage ahead); half a warp copies one
 // 256-byte row.  Tokens past the chunk and pages outside the cache arrive as
 // zeros.
-static __device__ void diff_produce(const DiffParams& dp, DiffSmem& sm, int32_t item_begin, int32_t item_end,
-                                    int32_t off_items) {
+constexpr int kCopyWarps = 8;
+__device__ __forceinline__ int diff_copy_warp(int warp) {
+  constexpr int behind = kFirstConsumerWarp + kConsumerWarps;
+  return warp < kFirstConsumerWarp ? warp : warp >= behind && warp < behind + 4 ? warp - behind + 4 : -1;
+}
+
+template <bool kV>
+__device__ void diff_produce(const DiffParams& dp, DiffSmem& sm, int pw, int32_t item_begin, int32_t item_end,
+                             int32_t off_items) {
   const RunParams& p = dp.run;
   const KvCache& kc = p.kv[0];
-  DiffBufs& bufs = sm.dec;
-  const int lane = threadIdx.x & 31, pw = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
   const int c16 = lane & 15, hw = lane >> 4;
   const int lp = kc.log2_page, P = kc.page_size;
+  const int64_t page_stride = kV ? dp.v_strides[0] : dp.k_strides[0];
+  const int64_t slot_stride = kV ? dp.v_strides[1] : dp.k_strides[1];
   uint32_t it = 0;
   for (int32_t i = item_begin; i < item_end; ++i) {
     const Item item = load_item(p.iws, off_items, i);
     const int nst = (item.kv1 - item.kv0 + kStageTokens - 1) >> kLog2StageTokens;
     const int32_t* pages = kc.kv_indices + item.rq.page_start;
+    const uint16_t* head = (kV ? dp.v : dp.k) + item.hk * (kV ? dp.v_strides[2] : dp.k_strides[2]) + 8 * c16;
     auto token_page = [&](int st) -> int32_t {
       const int tok = item.kv0 + st * kStageTokens + 32 * pw + lane;
       const int32_t id = tok < item.kv1 ? __ldg(pages + (tok >> lp)) : -1;
@@ -136,19 +147,14 @@ static __device__ void diff_produce(const DiffParams& dp, DiffSmem& sm, int32_t 
         if (st + 1 < nst) next = token_page(st + 1);
         if (!warp_wait(&sm.empty[s], ((it / kStages) & 1) ^ 1, &sm.abort)) continue;
         const int tok0 = item.kv0 + st * kStageTokens + 32 * pw;
+        // lane l: where token l's row begins
+        const int64_t my_row = cur >= 0 ? cur * page_stride + ((tok0 + lane) & (P - 1)) * slot_stride : -1;
+        uint16_t(*half)[64] = (kV ? sm.dec.v : sm.dec.k)[s][c16 >> 3];
 #pragma unroll 8
         for (int r = 0; r < 16; ++r) {
           const int tt = 2 * r + hw, row = 32 * pw + tt;
-          const int32_t id = __shfl_sync(0xffffffffu, cur, tt);
-          const int slot = (tok0 + tt) & (P - 1);
-          const bool ok = id >= 0;
-          const uint16_t* ks = dp.k + (ok ? id * dp.k_strides[0] + slot * dp.k_strides[1] : 0) +
-                               item.hk * dp.k_strides[2] + 8 * c16;
-          const uint16_t* vs = dp.v + (ok ? id * dp.v_strides[0] + slot * dp.v_strides[1] : 0) +
-                               item.hk * dp.v_strides[2] + 8 * c16;
-          const int at = ((c16 & 7) ^ (row & 7)) * 8;
-          cp_async_16(&bufs.k[s][c16 >> 3][row][at], ks, ok ? 16u : 0u);
-          cp_async_16(&bufs.v[s][c16 >> 3][row][at], vs, ok ? 16u : 0u);
+          const int64_t at = __shfl_sync(0xffffffffu, my_row, tt);
+          cp_async_16(&half[row][((c16 & 7) ^ (row & 7)) * 8], head + (at >= 0 ? at : 0), at >= 0 ? 16u : 0u);
         }
         cp_async_mbar_arrive_noinc(&sm.full[s]);
       }
@@ -568,7 +574,7 @@ __global__ void __launch_bounds__(kDiffThreads, 1) diff_attention_kernel(const _
   DiffPrefillBars& bar = sm.bars;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&sm.full[s], boxes ? 1 : 32 * kFirstConsumerWarp);  // the producer, or every copying thread
+      mbar_init(&sm.full[s], boxes ? 1 : 32 * kCopyWarps);  // the producer, or every copying thread
       mbar_init(&sm.empty[s], kConsumerWarps);
     }
     for (int s = 0; s < 2; ++s) {
@@ -634,11 +640,13 @@ __global__ void __launch_bounds__(kDiffThreads, 1) diff_attention_kernel(const _
       diff_consume<T>(dp, sm, mid, end, off_items, causal, var);
     } else {
       tc::setmaxnreg_dec<kDiffRegsOther>();
-      if (warp < kFirstConsumerWarp) {
-        if (!boxes)
-          diff_produce(dp, sm, mid, end, off_items);
-        else if (warp == 0)
-          diff_produce_tma(dp, sm, mid, end, off_items);
+      const int copier = diff_copy_warp(warp);
+      if (boxes) {
+        if (warp == 0) diff_produce_tma(dp, sm, mid, end, off_items);
+      } else if (copier >= 4) {
+        diff_produce<true>(dp, sm, copier - 4, mid, end, off_items);
+      } else if (copier >= 0) {
+        diff_produce<false>(dp, sm, copier, mid, end, off_items);
       }
     }
   }

@@ -18,7 +18,9 @@
 namespace fi {
 namespace {
 
-constexpr int kTableThreads = 512;
+// 256 threads: a step of 64 requests takes 4.6 us a call (5.2 with 512), one of
+// 4096 requests 11.9 either way (19.2 with 128).
+constexpr int kTableThreads = 256;
 constexpr int kTableWarps = kTableThreads / 32;
 constexpr int kTableAhead = 4;  // page-table entries a thread has in flight
 
