@@ -5,31 +5,40 @@
 // multiplies dims 64 m .. 64 m + 63 of the one Q tile and of K; with the two
 // maps' weights w_1, w_2 the output is (w_1 - lambda w_2) V.  The keys are
 // walked twice:
-//   pass 0  logits of both maps, their running maxima and sums;
+//   pass 0  logits of both maps, their references and sums;
 //   pass 1  logits again, now with the normalisers known: one weight
 //           w_1 - lambda w_2 per key, rounded once, and one product with V.
 // The maps' common part cancels before any rounding, so the error is half a
 // step of the weights' type relative to the difference, however much of the
-// maps cancels; with each map's weights rounded on their own, the output was
-// 1.5 times further from the 64-bit result than its own rounding at random
-// keys, and further the more the maps agree.  It also takes fewer tensor
-// cycles than two accumulators would: per 128 keys 512 in pass 0 and 512 +
-// 512 in pass 1, against 512 + 1024, or 512 + 2048 with weights of two terms;
-// the second walk costs 128 exponentials a thread, which overlap with them.
-// A split unit's chunk needs both maps' outputs for the merge: after pass 0
-// it walks the keys once per map (passes 2 and 3) with weights of two 16-bit
-// terms, hi + lo, as the merge takes the difference.
+// maps cancels (1.38 times the error of rounding the result alone, at random
+// keys); with each map's weights rounded on their own it was 1.53 times, and
+// more the more the maps agree.  It also takes fewer tensor cycles than two
+// accumulators would: per 128 keys 512 in pass 0 and 512 + 512 in pass 1,
+// against 512 + 1024, or 512 + 2048 with weights of two terms; the second walk
+// costs 128 exponentials a thread, which overlap with them.
+// A split unit's chunk needs both maps' outputs for the merge: pass 2 walks
+// the keys for map 2 alone and accumulates S_2 beside pass 1's S_1 - lambda S_2
+// (with two-term weights of either map instead, the mixed step took 65 us
+// against 58).
 //
-// Roles: warp 0 loads Q (two buffers) and K, warp 2 V, by TMA; warp 1 issues
-// the products; warpgroups of warps 4..7, 8..11, 12..15 and 16..19 take 32
-// keys each of every 128-key tile, for both maps (thread = row =
-// tensor-memory lane).  Tensor memory: S of both maps (256 columns), O (128),
-// two P buffers (64 each); in pass 0, which needs neither O nor P, their
-// columns are a second S buffer.  A thread takes its 64 logits into registers
-// and gives S back, so the next tile's S runs while it computes; P has columns
-// of its own, so S does not wait for P V either.  Four softmax warps on each
+// Roles: warp 0 loads Q (two buffers) and K, warp 2 V, by TMA, into one ring
+// of four tiles (rings of two tiles each: 596 against 590 us for 11688 queries
+// of 8 prompts, 32 query heads, up to 3756 keys); warp 1 issues the products;
+// warpgroups of warps 4..7, 8..11, 12..15 and 16..19 take 32 keys each of
+// every 128-key tile, for both maps (thread = row = tensor-memory lane).
+// Tensor memory: S of both maps (256 columns), O (128), two P buffers (64
+// each); in pass 0, which needs neither O nor P, their columns are a second S
+// buffer (757 -> 663 us).  A thread takes its 64 logits into registers and
+// gives S back, so the next tile's S runs while it computes; P has columns of
+// its own, so S does not wait for P V either.  Four softmax warps on each
 // scheduler: with two (64 keys each) a warp's waits, loads and stores were
-// not covered, and a step took twice its 1024 cycles of exponentials.
+// not covered (792 us).
+//
+// What bounds it (571 us for that workload, of 417 for its tensor cycles): a
+// tile takes pass 0 some 1550 cycles and pass 1 1650, of which a softmax warp
+// waits, loads and hands back for 500 and shares its scheduler with three
+// others for the rest (64 exponentials a pass: 1024 cycles of the four); an
+// item ends in 6600 cycles from its last weights to the next item's first sums.
 #pragma once
 #include "attention_kernel.cuh"
 #include "diff_params.h"

