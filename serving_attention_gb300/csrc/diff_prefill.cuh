@@ -22,7 +22,7 @@
 // against 58).
 //
 // Roles: warp 0 loads Q (two buffers) and K, warp 2 V, by TMA, into one ring
-// of four tiles (rings of two tiles each: 596 against 590 us for 11688 queries
+// of four tiles (rings of two tiles each: 596 against 590 us for 12161 queries
 // of 8 prompts, 32 query heads, up to 3756 keys); warp 1 issues the products;
 // warpgroups of warps 4..7, 8..11, 12..15 and 16..19 take 32 keys each of
 // every 128-key tile, for both maps (thread = row = tensor-memory lane).
@@ -34,7 +34,7 @@
 // scheduler: with two (64 keys each) a warp's waits, loads and stores were
 // not covered (792 us).
 //
-// What bounds it (571 us for that workload, of 417 for its tensor cycles): a
+// What bounds it (571 us for that workload; its tiles' products alone would take 293): a
 // tile takes pass 0 some 1550 cycles and pass 1 1650, of which a softmax warp
 // waits, loads and hands back for 500 and shares its scheduler with three
 // others for the rest (64 exponentials a pass: 1024 cycles of the four); an
