@@ -43,7 +43,8 @@ extern "C" {
  *   kv_indices [max_pages]   page ids, request after request; entries past the
  *                            last are left as they were
  *   positions [max_tokens]   position of each new token in its request
- *   slots [max_tokens]       page id * page_size + slot of each new token;
+ *   slots [max_tokens]       page id * page_size + slot of each new token (-1
+ *                            for a negative page id or past INT32_MAX);
  *                            tokens past the last get position 0 and slot -1,
  *                            so that a step padded to a captured size appends
  *                            nothing for them
@@ -156,7 +157,8 @@ fi_status fi_rotary_setup(const fi_rotary_config* cfg, fi_rotary* out);
  *   may be 0.
  *   positions int32 [num_tokens], device; any value.
  * dtype FI_FP16 or FI_BF16; base pointers and strides are multiples of 16
- * bytes.  num_tokens 0 does nothing.
+ * bytes.  An input may be broadcast (stride 0), an output's rows must be apart.
+ * num_tokens 0 does nothing (no pointer is read or checked).
  */
 typedef struct {
     const fi_rotary* rotary;

@@ -232,6 +232,17 @@ fi_status check_rotary(const fi_rotary* rot, int64_t num_tokens, int64_t num_q_h
 
 bool rows_ok(const fi_rows& r) { return aligned(r.data, 16) && stride_ok(r.stride_tok) && stride_ok(r.stride_head); }
 
+// Rows that are written: no two of them in one place, and in place only with
+// the strides of the input.
+bool apart(int64_t n, int64_t stride) { return n < 2 || stride > 0; }
+bool output_ok(const fi_rows& in, const fi_rows& out, int64_t tokens, int64_t heads) {
+  return apart(tokens, out.stride_tok) && apart(heads, out.stride_head) &&
+         (in.data != out.data || (in.stride_tok == out.stride_tok && in.stride_head == out.stride_head));
+}
+bool cache_ok(const int64_t strides[3], int64_t pages, int64_t page_size, int64_t heads) {
+  return apart(pages, strides[0]) && apart(page_size, strides[1]) && apart(heads, strides[2]);
+}
+
 RotaryRows rows_of(const fi_rows& in, const fi_rows& out, int64_t heads) {
   return {static_cast<const uint16_t*>(in.data), in.stride_tok, in.stride_head, static_cast<uint16_t*>(out.data),
           out.stride_tok, out.stride_head, 0, int32_t(heads)};
@@ -289,12 +300,15 @@ extern "C" fi_status fi_rotary_apply(const fi_rotary_apply_args* x, void* stream
   const fi_status st = check_rotary(x->rotary, x->num_tokens, x->num_q_heads, x->num_kv_heads, x->dtype);
   if (st != FI_OK) return st;
   const bool q = x->num_q_heads > 0, k = x->num_kv_heads > 0;
+  if (x->num_tokens == 0 || (!q && !k)) return FI_OK;
   if (!x->positions || (q && (!x->q_in.data || !x->q_out.data)) || (k && (!x->k_in.data || !x->k_out.data)))
     return FI_ERR_INVALID_ARG;
   if (!aligned(x->positions, 4) || (q && (!rows_ok(x->q_in) || !rows_ok(x->q_out))) ||
       (k && (!rows_ok(x->k_in) || !rows_ok(x->k_out))))
     return FI_ERR_ALIGNMENT;
-  if (x->num_tokens == 0 || (!q && !k)) return FI_OK;
+  if ((q && !output_ok(x->q_in, x->q_out, x->num_tokens, x->num_q_heads)) ||
+      (k && !output_ok(x->k_in, x->k_out, x->num_tokens, x->num_kv_heads)))
+    return FI_ERR_INVALID_ARG;
   RotaryParams a;
   std::memset(&a, 0, sizeof a);
   a.q = rows_of(x->q_in, x->q_out, x->num_q_heads);
@@ -313,6 +327,7 @@ extern "C" fi_status fi_rotary_append(const fi_rotary_append_args* x, void* stre
   const int64_t P = x->page_size;
   if (x->v_dim < 0 || x->v_dim > 512 || x->v_dim % 8 || P < 1 || P > 128 || (P & (P - 1))) return FI_ERR_UNSUPPORTED;
   const bool q = x->num_q_heads > 0, v = x->v_dim > 0;
+  if (x->num_tokens == 0) return FI_OK;
   if (!x->positions || !x->slots || x->num_kv_heads < 1 || x->num_pages < 1 || x->num_pages > INT32_MAX ||
       !x->k_in.data || !x->k_cache || (q && (!x->q_in.data || !x->q_out.data)) ||
       (v && (!x->v_in.data || !x->v_cache)))
@@ -322,7 +337,10 @@ extern "C" fi_status fi_rotary_append(const fi_rotary_append_args* x, void* stre
     return FI_ERR_ALIGNMENT;
   for (int i = 0; i < 3; ++i)
     if (!stride_ok(x->k_strides[i]) || (v && !stride_ok(x->v_strides[i]))) return FI_ERR_ALIGNMENT;
-  if (x->num_tokens == 0) return FI_OK;
+  if ((q && !output_ok(x->q_in, x->q_out, x->num_tokens, x->num_q_heads)) ||
+      !cache_ok(x->k_strides, x->num_pages, P, x->num_kv_heads) ||
+      (v && !cache_ok(x->v_strides, x->num_pages, P, x->num_kv_heads)))
+    return FI_ERR_INVALID_ARG;
   RotaryParams a;
   std::memset(&a, 0, sizeof a);
   a.q = rows_of(x->q_in, x->q_out, x->num_q_heads);

@@ -100,6 +100,24 @@ def test_append_refusals(kw, status):
     assert _append(**kw) == status
 
 
+@pytest.mark.parametrize("kw", [dict(qot=0), dict(qoh=0), dict(kot=0), dict(koh=0), dict(qo=32, qot=2048),
+                                dict(ko=64, koh=256)])
+def test_apply_refuses_outputs_that_overlap(kw):
+    assert _apply(**kw) == 1
+
+
+@pytest.mark.parametrize("kw", [dict(qot=0), dict(qoh=0), dict(k0=0), dict(k1=0), dict(k2=0), dict(v0=0), dict(v1=0),
+                                dict(v2=0), dict(qo=32, qot=2048)])
+def test_append_refuses_outputs_that_overlap(kw):
+    assert _append(**kw) == 1
+
+
+def test_no_tokens_need_no_pointers():
+    """The rows of an empty tensor have no address."""
+    none = dict(n=0, pos=0, q=0, qo=0, k=0)
+    assert _apply(**none, ko=0) == 0 and _append(**none, slots=0, v=0) == 0
+
+
 def _tables(**kw):
     a = dict(q=16, kv=32, batch=4, page=16, table=48, stride=8, width=8, free=64, num_free=9, head=80, qp=96, kp=112,
              last=128, idx=144, max_pages=9, pos=160, slots=176, max_tokens=9, counts=192)
