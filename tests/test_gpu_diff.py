@@ -154,6 +154,49 @@ def test_split_prefill(dtype):
     _check(b, lam, w, o, lse, rounded=True)
 
 
+@pytest.mark.parametrize("split", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("order", ["up", "down", "spike"])
+def test_steep_logits(order, dtype, split):
+    """Logits that leave the first tile's far behind, in opposite orders in the
+    two maps.  Queries and keys have one dim each map, of few bits, so a logit
+    is exact; its factor log2(e) in fp32 is off by 2^-25, at most 1e-5 over 250."""
+    b, lam, w = _batch(17, [1, 40, 140], [900, 600, 1000], 8, 2, 16, dtype, causal=1, poison=False)
+    n = 1000
+    ramp = (torch.arange(n, device=DEV) // 4).float()
+    if order == "down":
+        ramp = 249 - ramp
+    if order == "spike":
+        ramp = torch.where(torch.arange(n, device=DEV) % 331 == 330, 200.0, 0.0)
+    b.q.zero_()
+    b.k.zero_()
+    b.q[..., 0] = 8
+    b.q[..., 64] = 8
+    for i in range(3):
+        ids = torch.as_tensor(b.kv_indices[b.kv_indptr[i]:b.kv_indptr[i + 1]], device=DEV).long()
+        for p in range(len(ids)):
+            part = ramp[16 * p:16 * p + 16]
+            for h in range(2):
+                b.k[ids[p], :len(part), h, 0] = part.to(b.k.dtype)
+                b.k[ids[p], :len(part), h, 64] = (250 - part).to(b.k.dtype)
+    b.sm_scale = 0.125
+    kw = dict(prefill_min_chunk=128, decode_min_chunk=64, split_factor=16) if split else {}
+    o, lse, info, ws, _ = _run(b, lam, w, _config(**kw))
+    assert fi.device_status(ws) == 0
+    _check(b, lam, w, o, lse, rounded=True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("ctas,kw", [(1, {}), (3, {}), (2, dict(prefill_min_chunk=128, split_factor=64)),
+                                     (3, dict(window_left=300, sink_tokens=4)), (5, dict(split_factor=4))])
+def test_few_ctas(ctas, kw, dtype):
+    """Many items a CTA: whole and split ones, ends of requests, empty requests, decode items behind them."""
+    b, lam, w = _batch(18, [130, 1, 33, 70, 1, 200, 20], [700, 600, 33, 301, 0, 520, 0], 8, 2, 16, dtype, causal=1)
+    o, lse, info, ws, _ = _run(b, lam, w, _config(num_ctas=ctas, **kw))
+    assert fi.device_status(ws) == 0
+    _check(b, lam, w, o, lse, window=kw.get("window_left", -1), sink=kw.get("sink_tokens", 0), rounded=True)
+
+
 def test_strides_and_padding_rows():
     """q and o inside wider rows, caches with a padding head, more buffer rows
     than the plan's, no lse."""
