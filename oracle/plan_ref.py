@@ -37,7 +37,9 @@ Rule:
     items (n_pre of them: per 256-row unit, its ranges' chunk counts, at
     least 1) are at least one and at most num_ctas / 2: then num_ctas - n_pre.
     A differential plan with fewer than three CTAs a prefill-class unit takes
-    four times the prefill class's min_chunk.
+    four times the prefill class's min_chunk, and where a prefill-class unit's
+    window is one chunk (pages of 8 tokens and more, G dividing 128), the tiles
+    of its sink are part of that chunk's item (item word 13).
     A multi-head unit's chunk is max(granule, ceil(ceil(chunk / H) / granule)
     * granule) keys (the K/V bytes of a one-head chunk).
  4. A unit with kv_eff = 0 gives one empty item.  Otherwise each range
@@ -308,8 +310,15 @@ def _plan(cfg, reqs, num_shared, shared_page_size, block_of, total_qo, num_qo_he
     units_pre = sum(u[3] == TILE_PREFILL for u in units)
     min_pre = cfg["prefill_min_chunk"] * (4 if diff and 3 * units_pre > C else 1)
     chunk = {TILE_PREFILL: pick(TILE_PREFILL, min_pre, C)}
+    def lead_of(T, rng):
+        # tiles of a sink that share the item of a one-chunk window (differential, tensor-core path)
+        if not diff or T != TILE_PREFILL or len(rng) != 2 or rng[1][1] - rng[1][0] > chunk[TILE_PREFILL] \
+                or page_size < 8 or TILE_PREFILL_DIFF % group:
+            return 0
+        return _ceil_div(rng[0][1], 128)
+
     # prefill-class items; the decode class counts the CTAs they leave free when they take at most half
-    n_pre = sum(max(1, sum(_ceil_div(e - s, chunk[TILE_PREFILL]) for s, e in u[6]))
+    n_pre = sum(max(1, sum(_ceil_div(e - s, chunk[TILE_PREFILL]) for s, e in u[6][1 if lead_of(u[3], u[6]) else 0:]))
                 for u in units if u[3] == TILE_PREFILL)
     chunk[TILE_DECODE] = pick(TILE_DECODE, cfg["decode_min_chunk"], C - n_pre if 0 < 2 * n_pre <= C else C)
     weight = {TILE_DECODE: cfg["decode_cost_weight"], TILE_PREFILL: cfg["prefill_cost_weight"]}
@@ -326,8 +335,9 @@ def _plan(cfg, reqs, num_shared, shared_page_size, block_of, total_qo, num_qo_he
         if T == TILE_PREFILL:
             prefill_caches |= 2 if b < num_shared else 1
         ck = chunk_mh if heads > 1 else chunk[T]
+        lead = lead_of(T, rng)
         pieces = [(s_ + i * ck, min(e_, s_ + (i + 1) * ck))
-                  for s_, e_ in rng for i in range(_ceil_div(e_ - s_, ck))]
+                  for s_, e_ in rng[1 if lead else 0:] for i in range(_ceil_div(e_ - s_, ck))]
         n = max(1, len(pieces))
         nrows = (r1 - r0) * (2 if diff else 1)  # partial rows of a chunk: one per row and map
         base, m = -1, -1
@@ -339,11 +349,11 @@ def _plan(cfg, reqs, num_shared, shared_page_size, block_of, total_qo, num_qo_he
             merges.append((b, hk, r0, r1, n, base, 0 if T == TILE_DECODE and not diff else 1, 0))
         unit_parts.append((base, n))
         for i, (k0, k1) in enumerate(pieces or [(0, 0)]):
-            cost = ((k1 - k0) * heads + ITEM_COST_TOKENS) * weight[T]
+            cost = ((k1 - k0 + 128 * lead) * heads + ITEM_COST_TOKENS) * weight[T]
             part = base + i * nrows if base >= 0 else -1
             # the request's table entry rides along with the item
             items.append(((-cost, -T, b, hk, qt, i),
-                          (b, hk, r0, r1, k0, k1, part, m, *reqs[b], heads if heads > 1 else 0, 0, 0, 0)))
+                          (b, hk, r0, r1, k0, k1, part, m, *reqs[b], heads if heads > 1 else 0, lead, 0, 0)))
 
     # cascade merge entries, per ordinary unit: runs of at most CASCADE_ROWS
     # rows counted from the unit's first row, cut again at the block's q-tile bounds
@@ -400,8 +410,8 @@ def _plan(cfg, reqs, num_shared, shared_page_size, block_of, total_qo, num_qo_he
 
     rope_off = (int_workspace_ints(cfg) * 4 + 255) // 256 * 256 // 4 if rope_max > 0 else 0
     n_dec = sum(1 for _, f in items if lq[f[0]] * group <= 16)
-    ws[:HEADER_INTS] = [MAGIC_DIFF if diff else MAGIC, n_items, n_merge, C, batch, causal, off_cta, off_items, off_merge,
-                        off_cnt, off_req, 0, num_qo_heads, num_kv_heads, page_size, total_ints,
+    ws[:HEADER_INTS] = [MAGIC_DIFF if diff else MAGIC, n_items, n_merge, C, batch, causal, off_cta, off_items,
+                        off_merge, off_cnt, off_req, 0, num_qo_heads, num_kv_heads, page_size, total_ints,
                         window, sink, bits(cap), rope_max,
                         bits(theta) if rope_max > 0 else 0, bits(rscale) if rope_max > 0 else 0, rope_off,
                         sum(1 for m in merges if m[6]), part_rows, total_qo, num_shared,

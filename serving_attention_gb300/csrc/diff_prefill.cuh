@@ -80,6 +80,21 @@ struct DiffPrefillBars {
   uint64_t o_ready, o_free, drain;
 };
 
+static_assert(FI_MIN_TMA_PAGE == kMinTmaPage, "the planner's smallest page of this path");
+
+// An item with the tiles of its sink: lead tiles from key 0 on, then those of
+// [kv0, kv1).
+struct DiffItem : Item {
+  int32_t lead;
+};
+__device__ __forceinline__ DiffItem load_diff_item(const int32_t* iws, int32_t off_items, int32_t i) {
+  return DiffItem{load_item(iws, off_items, i), __ldg(iws + off_items + FI_ITEM_INTS * i + FI_ITEM_LEAD)};
+}
+__device__ __forceinline__ int diff_tiles(const DiffItem& it) { return it.lead + item_kv_tiles(it); }
+__device__ __forceinline__ int diff_tile_key(const DiffItem& it, int j) {  // first key of tile j
+  return j < it.lead ? j * kTileN : it.kv0 + (j - it.lead) * kTileN;
+}
+
 // Passes of an item behind pass 0: pass 1, and of a split unit's chunk pass 2.
 __device__ __forceinline__ int pv_passes(const Item& it) { return it.part >= 0 ? 2 : 1; }
 
@@ -115,16 +130,16 @@ __device__ uint32_t diff_pf_produce(const RunParams& p, DiffPrefillBufs& pf, Dif
   int pending = 0;
   uint32_t armed = 0, armed_phase = 0;  // bit st: this warp loaded into stage st, and the phase of the last load
   int q_armed[2] = {-1, -1};
-  Item ahead = load_item(p.iws, off_items, b0);
+  DiffItem ahead = load_diff_item(p.iws, off_items, b0);
   for (int32_t i = b0; i < b1; ++i) {
-    const Item it = ahead;
-    if (i + 1 < b1) ahead = load_item(p.iws, off_items, i + 1);
-    const int ntiles = item_kv_tiles(it);
+    const DiffItem it = ahead;
+    if (i + 1 < b1) ahead = load_diff_item(p.iws, off_items, i + 1);
+    const int ntiles = diff_tiles(it);
     if (ntiles == 0) continue;
     const int32_t* pages = kc.kv_indices + it.rq.page_start;
     const int npages = (it.rq.kv_len + P - 1) >> lp;
     auto page_of = [&](int j) -> int32_t {
-      const int pg = ((it.kv0 + j * kTileN) >> lp) + lane;
+      const int pg = (diff_tile_key(it, j) >> lp) + lane;
       return lane < ppt && pg < npages ? __ldg(pages + pg) : kc.num_pages;  // out of bounds -> zeros
     };
     int32_t next = page_of(0);
@@ -178,7 +193,7 @@ __device__ uint32_t diff_pf_produce(const RunParams& p, DiffPrefillBufs& pf, Dif
       // it alone starts the stage's next phase, so its wait cannot miss this
       // one.
       if (kV && tile + 1 == ntiles && item_v_tail(it, P) && warp_wait(&bar.kv_full[st], ph, abort)) {
-        for (int row = it.rq.kv_len - (it.kv0 + tile * kTileN) + (lane >> 4); row < kTileN; row += 2)
+        for (int row = it.rq.kv_len - diff_tile_key(it, tile) + (lane >> 4); row < kTileN; row += 2)
           *reinterpret_cast<uint4*>(&buf[(lane >> 3) & 1][row][8 * (lane & 7)]) = make_uint4(0u, 0u, 0u, 0u);
         fence_proxy_async_smem();
         __syncwarp();
@@ -344,11 +359,11 @@ __device__ void diff_pf_mma(const RunParams& p, DiffPrefillBufs& pf, DiffPrefill
   };
   const uint32_t o_col = tmem + kDiffTmemO;
   bool o2 = false;  // S_2 of a split unit's chunk is in the first S buffer
-  Item next = load_item(p.iws, off_items, b0);
+  DiffItem next = load_diff_item(p.iws, off_items, b0);
   for (int32_t i = b0; i < b1 && ok; ++i) {
-    const Item it = next;
-    if (i + 1 < b1) next = load_item(p.iws, off_items, i + 1);
-    const int ntiles = item_kv_tiles(it);
+    const DiffItem it = next;
+    if (i + 1 < b1) next = load_diff_item(p.iws, off_items, i + 1);
+    const int ntiles = diff_tiles(it);
     if (ntiles == 0) continue;
     const bool tail = item_v_tail(it, p.kv[0].page_size);
     const uint32_t qb = ni & 1, q_full = smem_u32(&bar.q_full[0]) + 8 * qb;
@@ -428,16 +443,17 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
   named_barrier_sync(kDiffBarrier, kDiffSoftmaxThreads);
   // Lane l holds word l of the next item's descriptor.
   auto item_word = [&](int32_t i) {
-    return lane < 12 && i < b1 ? __ldg(p.iws + off_items + FI_ITEM_INTS * i + lane) : 0;
+    return lane <= FI_ITEM_LEAD && i < b1 ? __ldg(p.iws + off_items + FI_ITEM_INTS * i + lane) : 0;
   };
   int32_t ahead = item_word(b0);
   for (int32_t i = b0; i < b1; ++i) {
     auto word = [&](int w) { return __shfl_sync(0xffffffffu, ahead, w); };
-    const Item item{word(0), word(1), word(2),  word(3),  word(4),
-                    word(5), word(6), word(7),  Request{word(8), word(9), word(10), word(11)}, 1};
+    const DiffItem item{Item{word(0), word(1), word(2), word(3), word(4), word(5), word(6), word(7),
+                             Request{word(8), word(9), word(10), word(11)}, 1},
+                        word(FI_ITEM_LEAD)};
     ahead = item_word(i + 1);
     const Request& rq = item.rq;
-    const int nrows = item.row1 - item.row0, ntiles = item_kv_tiles(item);
+    const int nrows = item.row1 - item.row0, ntiles = diff_tiles(item);
     const int row = item.row0 + r, tq = row / G, head = item.hk * G + (row - tq * G);
     const int64_t tok = int64_t(rq.qo_start) + tq;
     const int pos = rq.kv_len - rq.qo_len + tq;
@@ -448,10 +464,10 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
     const int lo = kMask && live ? window_low(var, pos) : 0;
     // tiles [c0, c1) need no mask for any row of the warp's keys; past c2 no
     // row of the warp sees any
-    const int first = item.kv0 + kDiffKeys * wg;  // this warpgroup's first key
-    const int c1 = __reduce_min_sync(0xffffffffu, (lim + 1 - first - kDiffKeys + kTileN) >> 7);
-    const int c2 = __reduce_max_sync(0xffffffffu, (lim - first + kTileN) >> 7);
-    const int c0 = kMask ? (max(__reduce_max_sync(0xffffffffu, lo) - first, 0) + kTileN - 1) >> 7 : 0;
+    const int first = item.kv0 + kDiffKeys * wg;  // this warpgroup's first key behind the sink's tiles
+    const int c1 = item.lead + __reduce_min_sync(0xffffffffu, (lim + 1 - first - kDiffKeys + kTileN) >> 7);
+    const int c2 = item.lead + __reduce_max_sync(0xffffffffu, (lim - first + kTileN) >> 7);
+    const int c0 = kMask ? item.lead + ((max(__reduce_max_sync(0xffffffffu, lo) - first, 0) + kTileN - 1) >> 7) : 0;
     uint16_t* out = p.o + tok * p.o_stride_tok + int64_t(head) * p.o_stride_head + kDiffKeys * wg;
     if (ntiles == 0) {  // no key: the output and log-sum-exps of an empty row
       if (live && item.part < 0) {
@@ -478,14 +494,21 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.s_free[x]);
     };
-    auto mask = [&](int j, uint32_t (&v)[32]) {
-#pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        const int key = first + j * kTileN + e;
-        if (key > lim || (kMask && key < lo && key >= var.sink)) v[e] = 0xff800000u;
-      }
+    // Bit e: key e of this warpgroup's 32 of tile j is visible to the row (tests
+    // of the keys one by one took twice as long as the tile's sums).
+    auto visible = [&](int j) -> uint32_t {
+      const int key0 = diff_tile_key(item, j) + kDiffKeys * wg;
+      auto below = [&](int end) -> uint32_t {  // keys before end
+        const int n = end - key0;
+        return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+      };
+      return kMask ? below(lim + 1) & (~below(lo) | below(var.sink)) : below(lim + 1);
     };
-
+    auto mask = [&](uint32_t seen, uint32_t (&v)[32]) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        if (!(seen >> e & 1)) v[e] = 0xff800000u;
+    };
     // This thread's weights into P buffer b.
     auto store_p = [&](int b, const uint32_t (&pk)[16]) {
       ok = ok && warp_wait(&bar.p_free[b], ((b ? np[1] : np[0]) & 1) ^ 1, abort);
@@ -508,8 +531,9 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
       load_s(j & 1, true, s[0], s[1]);
       if (j >= c2) continue;
       if (j < c0 || j >= c1) {
-        mask(j, s[0]);
-        mask(j, s[1]);
+        const uint32_t seen = visible(j);
+        mask(seen, s[0]);
+        mask(seen, s[1]);
       }
       for (bool move = !have_m;; move = true) {
         if (move) {
@@ -583,8 +607,9 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
       uint32_t s1[32], s2[32], pk[16];
       load_s(0, true, s1, s2);
       if (j < c0 || j >= c1) {
-        mask(j, s1);
-        mask(j, s2);
+        const uint32_t seen = visible(j);
+        mask(seen, s1);
+        mask(seen, s2);
       }
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
@@ -604,7 +629,7 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
       for (int j = 0; j < ntiles; ++j) {
         uint32_t s[32], pk[16];
         load_s(0, false, s, s);
-        if (j < c0 || j >= c1) mask(j, s);
+        if (j < c0 || j >= c1) mask(visible(j), s);
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const float2 x = fma2(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), cc, n);

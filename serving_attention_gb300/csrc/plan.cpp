@@ -23,7 +23,8 @@
 //    CTAs left free by the prefill-class items when those take at most half
 //    of them and differential attention takes four times the prefill class's
 //    min_chunk unless there are three CTAs a unit; units longer than a chunk are split into chunks whose fp32
-//    partial states are merged by the kernel;
+//    partial states are merged by the kernel (a differential prefill-class
+//    unit whose window is one chunk has its sink's tiles in the same item);
 //  * chunks are dealt out longest-first to the least-loaded CTA (LPT); an
 //    item's cost is its KV length plus a fixed FI_ITEM_COST_TOKENS (the
 //    per-item latency of the kernel), times the class weight, so that many
@@ -280,8 +281,8 @@ fi_status plan_requests(const fi_plan_config* cfg, const std::vector<Req>& reqs,
   // A differential unit that is split walks its keys three times instead of
   // twice, so it gains only where at least three chunks a unit run at once:
   // with fewer CTAs a unit, four times the shortest chunk.  Measured, us a
-  // call: 56 units of some 4100 keys 50.6 whole, 59.8 in four, 62.3 in two;
-  // four prompt parts beside 24 decodes 60.4 against 68.7 in four.
+  // call: 56 units of some 4100 keys 50.4 whole, 59.8 in four, 62.3 in two;
+  // four prompt parts beside 24 decodes 60.2 against 68.7 in four.
   int64_t min_pre = cfg->prefill_min_chunk;
   if (diff) {
     int64_t units_pre = 0;
@@ -290,6 +291,16 @@ fi_status plan_requests(const fi_plan_config* cfg, const std::vector<Req>& reqs,
   }
   const int64_t chunk_pre = pick_chunk(total_pre, min_pre, std::max(max_page, FI_GRANULE_PREFILL),
                                        int64_t(cfg->num_ctas) * cfg->split_factor);
+  // A differential prefill-class unit with a sink range takes it into the item
+  // of its window, where that is one chunk and the tensor-core path runs it:
+  // as a chunk of its own it would make the unit a split one (four prompt
+  // parts and 24 decodes, window 1023, 4 sinks: 48.6 -> 31.7 us).
+  auto sink_tiles = [&](const Unit& u) -> int32_t {
+    if (!diff || u.tile != FI_TILE_PREFILL || u.n_ranges != 2 || u.r_end[1] - u.r_begin[1] > chunk_pre ||
+        page_size < FI_MIN_TMA_PAGE || FI_TILE_PREFILL_DIFF % group != 0)
+      return 0;
+    return int32_t(ceil_div(u.r_end[0], FI_GRANULE_PREFILL));
+  };
   // Prefill-class items are long; when they take at most half the CTAs, the
   // decode work is spread over the CTAs they leave free (finer decode chunks
   // would only add per-item costs beside them).
@@ -297,7 +308,7 @@ fi_status plan_requests(const fi_plan_config* cfg, const std::vector<Req>& reqs,
   for (const Unit& u : units) {
     if (u.tile != FI_TILE_PREFILL) continue;
     int64_t n = 0;
-    for (int r = 0; r < u.n_ranges; ++r) n += ceil_div(u.r_end[r] - u.r_begin[r], chunk_pre);
+    for (int r = sink_tiles(u) > 0 ? 1 : 0; r < u.n_ranges; ++r) n += ceil_div(u.r_end[r] - u.r_begin[r], chunk_pre);
     n_pre += std::max<int64_t>(n, 1);
   }
   const int64_t dec_ctas = (n_pre > 0 && 2 * n_pre <= cfg->num_ctas) ? cfg->num_ctas - n_pre : cfg->num_ctas;
@@ -320,15 +331,16 @@ fi_status plan_requests(const fi_plan_config* cfg, const std::vector<Req>& reqs,
   for (size_t ui = 0; ui < units.size(); ++ui) {
     const Unit& u = units[ui];
     const int64_t chunk = u.tile == FI_TILE_DECODE ? (u.heads > 1 ? chunk_mh : chunk_dec) : chunk_pre;
-    const int64_t weight = u.tile == FI_TILE_DECODE ? cfg->decode_cost_weight : cfg->prefill_cost_weight;
     if (u.tile == FI_TILE_PREFILL) prefill_caches |= u.b < num_shared ? 2 : 1;
+    const int32_t lead = sink_tiles(u);
     int64_t n = 0;
-    for (int r = 0; r < u.n_ranges; ++r) n += ceil_div(u.r_end[r] - u.r_begin[r], chunk);
+    for (int r = lead > 0 ? 1 : 0; r < u.n_ranges; ++r) n += ceil_div(u.r_end[r] - u.r_begin[r], chunk);
     const bool empty = n == 0;
     if (empty) n = 1;
     int32_t merge_id = -1;
     int64_t base = -1;
     const int32_t nrows = u.row1 - u.row0;
+    const int64_t weight = u.tile == FI_TILE_DECODE ? cfg->decode_cost_weight : cfg->prefill_cost_weight;
     if (n > 1 || cascade) {
       base = partial_rows;
       partial_rows += n * nrows * maps;
@@ -347,7 +359,7 @@ fi_status plan_requests(const fi_plan_config* cfg, const std::vector<Req>& reqs,
     int64_t i = 0;
     auto emit = [&](int64_t k0, int64_t k1) {
       Chunk c;
-      c.cost = ((k1 - k0) * u.heads + FI_ITEM_COST_TOKENS) * weight;
+      c.cost = ((k1 - k0 + int64_t(lead) * FI_GRANULE_PREFILL) * u.heads + FI_ITEM_COST_TOKENS) * weight;
       c.tile = u.tile;
       c.b = u.b;
       c.hk = u.hk;
@@ -358,7 +370,7 @@ fi_status plan_requests(const fi_plan_config* cfg, const std::vector<Req>& reqs,
                                        u.row1,      int32_t(k0), int32_t(k1),
                                        base >= 0 ? int32_t(base + i * nrows * maps) : -1, merge_id,
                                        rq.qo_start, rq.qo_len,   rq.page_start,
-                                       rq.kv_len,   u.heads > 1 ? u.heads : 0, 0,
+                                       rq.kv_len,   u.heads > 1 ? u.heads : 0, lead,
                                        0,           0};
       std::memcpy(c.fields, f, sizeof f);
       chunks.push_back(c);
@@ -367,7 +379,7 @@ fi_status plan_requests(const fi_plan_config* cfg, const std::vector<Req>& reqs,
     if (empty) {
       emit(0, 0);
     } else {
-      for (int r = 0; r < u.n_ranges; ++r)
+      for (int r = lead > 0 ? 1 : 0; r < u.n_ranges; ++r)
         for (int64_t k0 = u.r_begin[r]; k0 < u.r_end[r]; k0 += chunk) emit(k0, std::min(u.r_end[r], k0 + chunk));
     }
   }

@@ -47,6 +47,8 @@
 //                  fi_rope_init, never part of a plan's copy
 // Every section starts on a multiple of 4 ints (16 bytes).
 //
+// A differential plan's item word FI_ITEM_LEAD counts tiles of 128 keys from
+// key 0 that the item takes ahead of [kv0, kv1): a sink before its window.
 // A differential plan (its own magic) counts partial rows per softmax map:
 // chunk i of a merge unit of n rows wrote rows part_base + i * 2n + r for
 // map 1 and part_base + i * 2n + n + r for map 2, and all its merge units are
@@ -62,6 +64,8 @@
 #define FI_PLAN_MAGIC_DIFF 0x46495044  // a differential plan: read by its own run only
 #define FI_HEADER_INTS 32
 #define FI_ITEM_INTS 16
+#define FI_ITEM_LEAD 13
+#define FI_MIN_TMA_PAGE 8  // smallest page of the tensor-core path
 #define FI_MERGE_INTS 8
 #define FI_REQ_INTS 4
 #define FI_CASCADE_INTS 12

@@ -146,6 +146,16 @@ def test_window_and_sink(window, sink, split):
     _check(b, lam, w, o, lse, window=window, sink=sink, rounded=True)
 
 
+@pytest.mark.parametrize("page", [4, 16, 128])
+@pytest.mark.parametrize("window,sink", [(100, 1), (255, 128), (300, 130), (640, 300)])
+def test_sinks_before_a_window(window, sink, page):
+    """A sink's tiles in the item of its window (pages of 8 and more), up to sinks of several tiles."""
+    b, lam, w = _batch(16, [40, 200, 9], [1500, 900, 450], 8, 2, page, "bf16", causal=1)
+    o, lse, info, ws, _ = _run(b, lam, w, _config(window_left=window, sink_tokens=sink, num_ctas=4))
+    assert fi.device_status(ws) == 0
+    _check(b, lam, w, o, lse, window=window, sink=sink, rounded=True)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 def test_split_prefill(dtype):
     b, lam, w = _batch(8, [50, 129, 1], [1500, 700, 900], 8, 2, 16, dtype, causal=1)
