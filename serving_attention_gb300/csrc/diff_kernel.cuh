@@ -586,7 +586,6 @@ __global__ void __launch_bounds__(kDiffThreads, 1) diff_attention_kernel(const _
       mbar_init(&bar.s_full[s], 1);
       mbar_init(&bar.s_free[s], 4 * kDiffGroups);  // every softmax warp
       mbar_init(&bar.p_full[s], 4 * kDiffGroups);
-      mbar_init(&bar.p_free[s], 1);
     }
     for (int s = 0; s < kDiffStages; ++s) {
       mbar_init(&bar.kv_full[s], 1);

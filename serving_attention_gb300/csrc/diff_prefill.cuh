@@ -76,7 +76,6 @@ struct DiffPrefillBars {
   uint64_t v_clear[kDiffStages];  // a tile's V rows past the request's end cleared
   uint64_t s_full[2], s_free[2];  // [S buffer]
   uint64_t p_full[2];             // [buffer]
-  uint64_t p_free[2];
   uint64_t o_ready, o_free, drain;
 };
 
@@ -337,7 +336,6 @@ __device__ void diff_pf_mma(const RunParams& p, DiffPrefillBufs& pf, DiffPrefill
     const uint32_t w = tmem + kDiffTmemP + 64 * b;
     mma4<true>(d, 0, w, v, idesc_pv, first ? 0u : 1u);
     mma4<true>(d, 0, w + 32, v + 512u, idesc_pv, 1u);
-    tc::mma_commit_warp(&bar.p_free[b]);
     tc::mma_commit_warp(&bar.kv_empty[st]);
     if (last) {
       tc::mma_commit_warp(&bar.o_ready);
@@ -390,9 +388,9 @@ __device__ void diff_pf_mma(const RunParams& p, DiffPrefillBufs& pf, DiffPrefill
       flush(o_col);
       for (int j = 1; j < ntiles && ok; ++j) {
         do_s(a, 0, false);
-        do_pv(tmem, (j - 1) & 1, j == 1, false, false);
+        do_pv(tmem, (ntiles + j - 1) & 1, j == 1, false, false);
       }
-      pv = {true, ntiles == 1, true, tail, (ntiles - 1) & 1};
+      pv = {true, ntiles == 1, true, tail, 1};
       flush(tmem);
     }
     ++ni;
@@ -437,7 +435,7 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
   const int G = p.group;
   const float sc = p.scale_log2;
   const float2 cc = make_float2(sc, sc);
-  uint32_t ns[2] = {0, 0}, np[2] = {0, 0}, no = 0, ni = 0;  // as in the MMA warp
+  uint32_t s_phase = 0, no = 0, ni = 0;  // bit x: parity of S buffer x's next tile; uses of O, items
   int q_held = -1;  // the Q buffer that this warpgroup's output store may still be reading
   if (dp.norm_w && sw < 4) reinterpret_cast<float*>(pf.norm_w)[r] = __ldg(dp.norm_w + r);
   named_barrier_sync(kDiffBarrier, kDiffSoftmaxThreads);
@@ -482,9 +480,9 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
     // This warpgroup's 32 logits of both maps (or of map 2 alone) of tile j in
     // S buffer x; S goes back to the MMA warp.
     auto load_s = [&](int x, bool both, uint32_t (&a)[32], uint32_t (&b)[32]) {
-      ok = ok && warp_wait(&bar.s_full[x], (x ? ns[1] : ns[0]) & 1, abort);
-      ns[0] += x == 0;
-      ns[1] += x;
+      const uint32_t ph = (s_phase >> x) & 1;
+      if (!__all_sync(0xffffffffu, mbar_try_wait(&bar.s_full[x], ph))) ok = ok && warp_wait(&bar.s_full[x], ph, abort);
+      s_phase ^= 1u << x;
       tc::fence_after_sync();
       const uint32_t col = tl + 2 * kTileN * x + kDiffKeys * wg;
       if (both) tc::tmem_ld32(col, a);
@@ -509,12 +507,10 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
       for (int e = 0; e < 32; ++e)
         if (!(seen >> e & 1)) v[e] = 0xff800000u;
     };
-    // This thread's weights into P buffer b.
+    // This thread's weights into P buffer b, the other one of the step before.
+    // It is free: the step's S was issued behind the P V of two steps before,
+    // and a commit stands for everything issued before it.
     auto store_p = [&](int b, const uint32_t (&pk)[16]) {
-      ok = ok && warp_wait(&bar.p_free[b], ((b ? np[1] : np[0]) & 1) ^ 1, abort);
-      np[0] += b == 0;
-      np[1] += b;
-      tc::fence_after_sync();
       tc::tmem_st16(tl + kDiffTmemP + 64 * b + 16 * wg, pk);
       tc::tmem_st_wait();
       tc::fence_before_sync();
@@ -635,7 +631,7 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
           const float2 x = fma2(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), cc, n);
           pk[e] = tc::pack2<T>(ex2(x.x), ex2(x.y));
         }
-        store_p(j & 1, pk);
+        store_p((ntiles + j) & 1, pk);
       }
     }
     // this warpgroup's 32 dims of the accumulators' rows
