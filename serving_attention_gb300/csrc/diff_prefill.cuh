@@ -432,7 +432,7 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
   const uint32_t tl = tmem + (uint32_t(32 * (sw & 3)) << 16);
   const bool elected = (threadIdx.x & 255) == 128;  // one thread of each pair of warpgroups
   const int half = wg >> 1;                          // of the keys, and of the output's dims
-  const int G = p.group;
+  const int G = p.group, log2_g = __ffs(G) - 1;  // G divides 128 on this path
   const float sc = p.scale_log2;
   const float2 cc = make_float2(sc, sc);
   uint32_t s_phase = 0, no = 0, ni = 0;  // bit x: parity of S buffer x's next tile; uses of O, items
@@ -452,7 +452,7 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
     ahead = item_word(i + 1);
     const Request& rq = item.rq;
     const int nrows = item.row1 - item.row0, ntiles = diff_tiles(item);
-    const int row = item.row0 + r, tq = row / G, head = item.hk * G + (row - tq * G);
+    const int row = item.row0 + r, tq = row >> log2_g, head = item.hk * G + (row & (G - 1));
     const int64_t tok = int64_t(rq.qo_start) + tq;
     const int pos = rq.kv_len - rq.qo_len + tq;
     const bool live = r < nrows;
@@ -634,6 +634,7 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
         store_p((ntiles + j) & 1, pk);
       }
     }
+    if (p.lse && item.part < 0 && wg < 2 && live && !*abort) p.lse[(tok * p.num_qo_heads + head) * 2 + wg] = lse;
     // this warpgroup's 32 dims of the accumulators' rows
     ok = ok && warp_wait(&bar.o_ready, no & 1, abort);
     ++no;
@@ -650,7 +651,6 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
     if (item.part < 0) {
       // ---- the output
       release_o();
-      if (p.lse && wg < 2 && live && !*abort) p.lse[(tok * p.num_qo_heads + head) * 2 + wg] = lse;
       float f = unscale * dp.out_scale;
       if (dp.norm_w) {
         float ss = 0.f;
