@@ -23,7 +23,7 @@
 //
 // Roles: warp 0 loads Q (two buffers) and K, warp 2 V, by TMA, into one ring
 // of four tiles (rings of two tiles each: 596 against 590 us for 12161 queries
-// of 8 prompts, 32 query heads, up to 3756 keys); warp 1 issues the products;
+// of 8 prompts, 32 query heads, up to 3756 keys, in an earlier state); warp 1 issues the products;
 // warpgroups of warps 4..7, 8..11, 12..15 and 16..19 take 32 keys each of
 // every 128-key tile, for both maps (thread = row = tensor-memory lane).
 // Tensor memory: S of both maps (256 columns), O (128), two P buffers (64
@@ -34,11 +34,12 @@
 // scheduler: with two (64 keys each) a warp's waits, loads and stores were
 // not covered (792 us).
 //
-// What bounds it (571 us for that workload; its tiles' products alone would take 293): a
-// tile takes pass 0 some 1550 cycles and pass 1 1650, of which a softmax warp
-// waits, loads and hands back for 500 and shares its scheduler with three
-// others for the rest (64 exponentials a pass: 1024 cycles of the four); an
-// item ends in 6600 cycles from its last weights to the next item's first sums.
+// What bounds it (544 us for that workload; its tiles' products alone would
+// take 293): a tile takes some 3200 cycles of both passes, of which the
+// products read 160 KB of operands and TMA writes 96 KB through shared memory's
+// 128 bytes a cycle (2050 cycles), and the MMA and softmax warps hand S and P
+// to one another; leaving the arithmetic of either pass out gains 6 %.  An item
+// ends in some 6000 cycles from its last weights to the next one's first sums.
 #pragma once
 #include "attention_kernel.cuh"
 #include "diff_params.h"
