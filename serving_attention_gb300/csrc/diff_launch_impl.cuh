@@ -25,7 +25,7 @@ cudaError_t launch_diff(const DiffParams& dp, int num_ctas, cudaStream_t stream)
   }
   kern<<<num_ctas, kDiffThreads, kDiffSmemBytes, stream>>>(dp);
   e = cudaGetLastError();
-  return e == cudaSuccess ? launch_behind_run(diff_merge_kernel<T>, 4 * num_ctas, 256, stream, dp) : e;
+  return e == cudaSuccess ? launch_behind_run(diff_merge_kernel<T>, 2 * num_ctas, 256, stream, dp) : e;
 }
 
 }  // namespace fi
