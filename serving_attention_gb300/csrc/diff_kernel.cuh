@@ -166,7 +166,11 @@ __device__ void diff_produce(const DiffParams& dp, DiffSmem& sm, int pw, int32_t
   cp_async_wait_all();
 }
 
-// Pages of 8 tokens and more: warp 0 brings a stage with one 128-byte swizzled
+// Smallest page whose stages come by TMA boxes: with 8-token pages the 64 boxes
+// of a stage took 186.8 us for 753 MB of cache, the copies above 129.1.
+constexpr int kDiffMinBoxPage = 16;
+
+// Larger pages: warp 0 brings a stage with one 128-byte swizzled
 // TMA box (64 dims, 1 head, P slots, 1 page) per page, half and tensor -- the
 // boxes of the tensor-core path, in the layout that the copies above write by
 // hand.  Lane l issues pages l, l + 32, ...; the next stage's page ids are
@@ -178,7 +182,7 @@ static __device__ void diff_produce_tma(const DiffParams& dp, DiffSmem& sm, int3
   const KvCache& kc = p.kv[0];
   DiffBufs& bufs = sm.dec;
   const int lane = threadIdx.x & 31;
-  const int lp = kc.log2_page, P = kc.page_size, boxes = kStageTokens >> lp;  // 1 to 16
+  const int lp = kc.log2_page, P = kc.page_size, boxes = kStageTokens >> lp;  // 1 to 8
   if (lane == 0) {
     tc::prefetch_tensormap(&kc.tm_k);
     tc::prefetch_tensormap(&kc.tm_v);
@@ -573,7 +577,7 @@ __global__ void __launch_bounds__(kDiffThreads, 1) diff_attention_kernel(const _
   const int warp = threadIdx.x >> 5;
   const int32_t mid = first_cuda_core_item(p, begin, end, off_items, 0, 0);
   const bool tc_phase = mid > begin;
-  const bool boxes = p.kv[0].page_size >= kMinTmaPage;
+  const bool boxes = p.kv[0].page_size >= kDiffMinBoxPage;
   DiffPrefillBars& bar = sm.bars;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
