@@ -430,7 +430,7 @@ __device__ __forceinline__ uint32_t diff_pass(const DiffParams& dp, DiffSmem& sm
     const int j0 = item.kv0 + st * kStageTokens;
     if (warp_wait(&sm.full[s], (it / kStages) & 1, &sm.abort)) {
       const uint16_t *ks = &bufs.k[s][0][0][0], *vs = &bufs.v[s][0][0][0];
-#pragma unroll 1
+#pragma unroll
       for (int sl = 0; sl < (kWide ? 2 : 1); ++sl) {
         const int tok0 = kWide ? 32 * (cw & 3) + 16 * sl : 16 * cw;
         if (j0 + tok0 < item.kv1)
