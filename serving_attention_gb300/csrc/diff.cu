@@ -86,9 +86,9 @@ extern "C" fi_status fi_batch_paged_attention_run_differential(const fi_differen
     dp.k_strides[i] = a->k_strides[i];
     dp.v_strides[i] = a->v_strides[i];
   }
+  const CUtensorMapDataType tt =
+      a->dtype == FI_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   if (P >= kMinTmaPage) {
-    const CUtensorMapDataType tt =
-        a->dtype == FI_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     const uint64_t kd[4] = {uint64_t(kHeadDim), uint64_t(info->num_kv_heads), uint64_t(P), uint64_t(a->num_pages)};
     const int64_t ks[3] = {a->k_strides[2], a->k_strides[1], a->k_strides[0]};  // head, slot, page
     const int64_t vs[3] = {a->v_strides[2], a->v_strides[1], a->v_strides[0]};
@@ -96,15 +96,15 @@ extern "C" fi_status fi_batch_paged_attention_run_differential(const fi_differen
     if (!make_map(&kc.tm_k, tt, a->k_cache, 4, kd, ks, kb, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !make_map(&kc.tm_v, tt, a->v_cache, 4, kd, vs, kb, CU_TENSOR_MAP_SWIZZLE_128B))
       return FI_ERR_UNSUPPORTED;
-    kc.tc = kTileM % p.group == 0 ? 1 : 0;
-    if (kc.tc) {
-      const uint64_t qd[3] = {uint64_t(kHeadDim), uint64_t(info->num_qo_heads), uint64_t(a->q_num_tokens)};
-      const int64_t qs[2] = {a->q_stride_head, a->q_stride_tok}, os[2] = {a->o_stride_head, a->o_stride_tok};
-      const uint32_t qb[3] = {64u, uint32_t(p.group), uint32_t(kTileM / p.group)};
-      if (!make_map(&p.tm_q, tt, a->q, 3, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B) ||
-          !make_map(&p.tm_o, tt, a->o, 3, qd, os, qb, CU_TENSOR_MAP_SWIZZLE_128B))
-        return FI_ERR_UNSUPPORTED;
-    }
+  }
+  kc.tc = kTileM % p.group == 0 ? 1 : 0;
+  if (kc.tc) {
+    const uint64_t qd[3] = {uint64_t(kHeadDim), uint64_t(info->num_qo_heads), uint64_t(a->q_num_tokens)};
+    const int64_t qs[2] = {a->q_stride_head, a->q_stride_tok}, os[2] = {a->o_stride_head, a->o_stride_tok};
+    const uint32_t qb[3] = {64u, uint32_t(p.group), uint32_t(kTileM / p.group)};
+    if (!make_map(&p.tm_q, tt, a->q, 3, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_map(&p.tm_o, tt, a->o, 3, qd, os, qb, CU_TENSOR_MAP_SWIZZLE_128B))
+      return FI_ERR_UNSUPPORTED;
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool mask = (info->variant & 2) != 0;

@@ -540,6 +540,24 @@ __device__ void diff_consume(const DiffParams& dp, DiffSmem& sm, int32_t item_be
 
 // ---------------------------------------------------------------- kernel
 
+// Where the CTA's items leave the tensor cores: at the first of a request of
+// at most 16 packed rows, or, on pages below 8 tokens, of at most 32, which the
+// decode path takes in two passes: 16 requests on pages of one token took
+// 143 us with 32 rows each (on the tensor cores, where a tile is copied row by
+// row, 162), but 209 with 48 (164) and 341 with 80 (165).
+__device__ __forceinline__ int32_t diff_first_decode_item(const RunParams& p, int32_t begin, int32_t end,
+                                                          int32_t off_items) {
+  const int lane = threadIdx.x & 31;
+  const int most = p.kv[0].page_size < kMinTmaPage ? 32 : FI_TILE_DECODE;
+  for (int32_t i0 = begin; i0 < end; i0 += 32) {
+    const bool decode = i0 + lane >= end || !p.kv[0].tc ||
+                        __ldg(p.iws + off_items + FI_ITEM_INTS * (i0 + lane) + 9) * p.group <= most;  // its qo_len
+    const unsigned m = __ballot_sync(0xffffffffu, decode);
+    if (m) return min(end, i0 + __ffs(m) - 1);
+  }
+  return end;
+}
+
 template <typename T, bool kMask>
 __global__ void __launch_bounds__(kDiffThreads, 1) diff_attention_kernel(const __grid_constant__ DiffParams dp) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -575,7 +593,7 @@ __global__ void __launch_bounds__(kDiffThreads, 1) diff_attention_kernel(const _
   var.cap_a = var.cap_b = 0.f;
   var.rope_table = nullptr;
   const int warp = threadIdx.x >> 5;
-  const int32_t mid = first_cuda_core_item(p, begin, end, off_items, 0, 0);
+  const int32_t mid = diff_first_decode_item(p, begin, end, off_items);
   const bool tc_phase = mid > begin;
   const bool boxes = p.kv[0].page_size >= kDiffMinBoxPage;
   DiffPrefillBars& bar = sm.bars;
@@ -615,13 +633,18 @@ __global__ void __launch_bounds__(kDiffThreads, 1) diff_attention_kernel(const _
     uint32_t loads = 0;
     if (warp < kSoftmaxWarp0) {
       tc::setmaxnreg_dec<kDiffRegsLoader>();
-      if (warp == 0) {
-        loads = diff_pf_produce<false>(p, sm.pf, bar, &sm.abort, begin, mid, off_items);
+      const bool copies = p.kv[0].page_size < kMinTmaPage;
+      if (copies && (warp == 0 || warp == 3)) {
+        diff_pf_produce<false, true>(dp, sm.pf, bar, &sm.abort, begin, mid, off_items);
+      } else if (copies && warp == kVWarp) {
+        diff_pf_produce<true, true>(dp, sm.pf, bar, &sm.abort, begin, mid, off_items);
+      } else if (warp == 0) {
+        loads = diff_pf_produce<false, false>(dp, sm.pf, bar, &sm.abort, begin, mid, off_items);
       } else if (warp == kMmaWarp) {
         diff_pf_mma<T>(p, sm.pf, bar, &sm.abort, sm.tmem_base, begin, mid, off_items);
         __syncwarp();
       } else if (warp == kVWarp) {
-        loads = diff_pf_produce<true>(p, sm.pf, bar, &sm.abort, begin, mid, off_items);
+        loads = diff_pf_produce<true, false>(dp, sm.pf, bar, &sm.abort, begin, mid, off_items);
       }
       tc::fence_before_sync();
       named_barrier_sync_unaligned(kPhaseBarrier, kDiffThreads);

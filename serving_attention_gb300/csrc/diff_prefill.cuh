@@ -34,7 +34,7 @@
 // scheduler: with two (64 keys each) a warp's waits, loads and stores were
 // not covered (792 us).
 //
-// What bounds it (544 us for that workload; its tiles' products alone would
+// What bounds it (550 us for that workload; its tiles' products alone would
 // take 293): a tile takes some 3200 cycles of both passes, of which the
 // products read 160 KB of operands and TMA writes 96 KB through shared memory's
 // 128 bytes a cycle (2050 cycles), and the MMA and softmax warps hand S and P
@@ -52,6 +52,7 @@ constexpr int kDiffKeys = kTileN / kDiffGroups;        // keys of a tile, and di
 constexpr int kDiffSoftmaxThreads = 128 * kDiffGroups;
 constexpr int kDiffBarrier = 6;  // all softmax warpgroups (1: decode, 3: end of phase, 4 and 5: two warpgroups)
 constexpr int kDiffStages = 4;   // K and V tiles in one ring
+constexpr int kDiffCopyBarrier = 8;  // named barrier of the two warps that copy K tiles of small pages
 constexpr int kDiffLoadBarrier = 7;  // named barrier of the K and the V loader
 constexpr int kDiffTmemO = 256, kDiffTmemP = 384;
 constexpr float kWeightScale = 13.f;  // softmax weights are multiplied by 2^13 before they are rounded
@@ -80,8 +81,6 @@ struct DiffPrefillBars {
   uint64_t o_ready, o_free, drain;
 };
 
-static_assert(FI_MIN_TMA_PAGE == kMinTmaPage, "the planner's smallest page of this path");
-
 // An item with the tiles of its sink: lead tiles from key 0 on, then those of
 // [kv0, kv1).
 struct DiffItem : Item {
@@ -95,13 +94,16 @@ __device__ __forceinline__ int diff_tile_key(const DiffItem& it, int j) {  // fi
   return j < it.lead ? j * kTileN : it.kv0 + (j - it.lead) * kTileN;
 }
 
+static_assert(FI_MIN_TMA_PAGE == kMinTmaPage, "the planner's smallest page of this path's boxes");
+
 // Passes of an item behind pass 0: pass 1, and of a split unit's chunk pass 2.
 __device__ __forceinline__ int pv_passes(const Item& it) { return it.part >= 0 ? 2 : 1; }
 
 // Whether the item's last KV tile reaches past the end of the request inside
 // a page: the V rows there may hold anything (0 * NaN would not be 0).
 __device__ __forceinline__ bool item_v_tail(const Item& it, int page_size) {
-  return (it.rq.kv_len & (page_size - 1)) != 0 && it.kv0 + item_kv_tiles(it) * kTileN > it.rq.kv_len;
+  return page_size >= kMinTmaPage && (it.rq.kv_len & (page_size - 1)) != 0 &&
+         it.kv0 + item_kv_tiles(it) * kTileN > it.rq.kv_len;
 }
 
 // Warp 0 (kV false): Q and K tiles; warp 2 (kV true): V tiles.  K and V tiles
@@ -113,17 +115,55 @@ __device__ __forceinline__ bool item_v_tail(const Item& it, int page_size) {
 //                     through: K(0) t1, K(q) t1 + 2q - 1, V(q) t1 + 2q + 2
 //   the next item     t1 + 2 steps - 1.
 // A split unit's chunk leaves nothing pending: its last V has the place before.
+// Pages below 8 tokens, whose boxes would start inside a swizzle atom: the
+// rows are copied 16 bytes at a time into the same layout, K by warps 0 and 3,
+// 64 rows each, V by warp 2, and handed on once they have landed.  (Without
+// it such items took the 16-row tiles of the decode path: 4 prompts of 300 to
+// 512 queries on pages of one token took 477 us, now 101.)
+template <bool kV>
+__device__ __forceinline__ void diff_pf_copy(const DiffParams& dp, const DiffItem& it, uint16_t (*buf)[kTileN][64],
+                                             int key0, int row0, int rows) {
+  const KvCache& kc = dp.run.kv[0];
+  const int lane = threadIdx.x & 31, c16 = lane & 15, hw = lane >> 4;
+  const int lp = kc.log2_page, P = kc.page_size;
+  const int32_t* pages = kc.kv_indices + it.rq.page_start;
+  const int64_t page_stride = kV ? dp.v_strides[0] : dp.k_strides[0];
+  const int64_t slot_stride = kV ? dp.v_strides[1] : dp.k_strides[1];
+  const uint16_t* head = (kV ? dp.v : dp.k) + it.hk * (kV ? dp.v_strides[2] : dp.k_strides[2]) + 8 * c16;
+  auto page_of = [&](int row) -> int32_t {  // of this lane's row
+    const int key = key0 + row + lane;
+    const int32_t id = key < it.rq.kv_len ? __ldg(pages + (key >> lp)) : -1;
+    return uint32_t(id) < uint32_t(kc.num_pages) ? id : -1;
+  };
+  int32_t next = page_of(row0);
+  for (int g = row0; g < row0 + rows; g += 32) {
+    const int64_t my_row = next >= 0 ? next * page_stride + ((key0 + g + lane) & (P - 1)) * slot_stride : -1;
+    if (g + 32 < row0 + rows) next = page_of(g + 32);
+#pragma unroll 8
+    for (int r = 0; r < 16; ++r) {
+      const int tt = 2 * r + hw, row = g + tt;
+      const int64_t at = __shfl_sync(0xffffffffu, my_row, tt);
+      cp_async_16(&buf[c16 >> 3][row][((c16 & 7) ^ (row & 7)) * 8], head + (at >= 0 ? at : 0), at >= 0 ? 16u : 0u);
+    }
+  }
+  cp_async_wait_all();
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
 // Returns which stages this warp loaded, and above them the phases of the last
 // loads.
-template <bool kV>
-__device__ uint32_t diff_pf_produce(const RunParams& p, DiffPrefillBufs& pf, DiffPrefillBars& bar, volatile int* abort,
-                                int32_t b0, int32_t b1, int32_t off_items) {
+template <bool kV, bool kCopies>
+__device__ uint32_t diff_pf_produce(const DiffParams& dp, DiffPrefillBufs& pf, DiffPrefillBars& bar,
+                                    volatile int* abort, int32_t b0, int32_t b1, int32_t off_items) {
+  const RunParams& p = dp.run;
   const int lane = threadIdx.x & 31;
+  const bool second = kCopies && !kV && threadIdx.x >= 32;  // warp 3, which only copies
   const KvCache& kc = p.kv[0];
   const int G = p.group, lp = kc.log2_page, P = kc.page_size, ppt = kTileN >> lp;
   const CUtensorMap* map = kV ? &kc.tm_v : &kc.tm_k;
   if (lane == 0) {
-    tc::prefetch_tensormap(map);
+    if (!kCopies) tc::prefetch_tensormap(map);
     if (!kV) tc::prefetch_tensormap(&p.tm_q);
   }
   uint32_t t = 0, ni = 0;  // an item's first place, items
@@ -143,7 +183,7 @@ __device__ uint32_t diff_pf_produce(const RunParams& p, DiffPrefillBufs& pf, Dif
       return lane < ppt && pg < npages ? __ldg(pages + pg) : kc.num_pages;  // out of bounds -> zeros
     };
     int32_t next = page_of(0);
-    if (!kV) {
+    if (!kV && !second) {
       const int qb = ni & 1;
       const uint32_t ph = (ni >> 1) & 1;
       if (warp_wait(&bar.q_empty[qb], ph ^ 1, abort)) {
@@ -175,10 +215,17 @@ __device__ uint32_t diff_pf_produce(const RunParams& p, DiffPrefillBufs& pf, Dif
       if (q == 0) {
         if (kV)
           named_barrier_sync(kDiffLoadBarrier, 64);
-        else
+        else if (!second)
           named_barrier_arrive(kDiffLoadBarrier, 64);
       }
-      if (!warp_wait(&bar.kv_empty[st], ph ^ 1, abort)) continue;
+      const bool free = warp_wait(&bar.kv_empty[st], ph ^ 1, abort);
+      if (kCopies) {
+        if (free) diff_pf_copy<kV>(dp, it, pf.kv[st], diff_tile_key(it, tile), second ? 64 : 0, kV ? kTileN : 64);
+        if (!kV) named_barrier_sync(kDiffCopyBarrier, 64);
+        if (free && lane == 0 && !second) mbar_arrive(&bar.kv_full[st]);
+        continue;
+      }
+      if (!free) continue;
       if (lane == 0) mbar_arrive_expect_tx(&bar.kv_full[st], kKVBytes);
       __syncwarp();
       uint16_t(*buf)[kTileN][64] = pf.kv[st];

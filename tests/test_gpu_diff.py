@@ -207,6 +207,17 @@ def test_few_ctas(ctas, kw, dtype):
     _check(b, lam, w, o, lse, window=kw.get("window_left", -1), sink=kw.get("sink_tokens", 0), rounded=True)
 
 
+@pytest.mark.parametrize("page", [1, 2, 4])
+@pytest.mark.parametrize("ctas,kw", [(2, {}), (3, dict(prefill_min_chunk=128, split_factor=64)),
+                                     (2, dict(window_left=200, sink_tokens=5))])
+def test_prefill_on_small_pages(ctas, kw, page):
+    """Tiles copied row by row: many items a CTA, split ones, a sink's tile, decode items behind them."""
+    b, lam, w = _batch(19, [130, 1, 33, 70, 1, 200, 20], [700, 600, 33, 301, 0, 520, 7], 8, 2, page, "fp16", causal=1)
+    o, lse, info, ws, _ = _run(b, lam, w, _config(num_ctas=ctas, **kw))
+    assert fi.device_status(ws) == 0
+    _check(b, lam, w, o, lse, window=kw.get("window_left", -1), sink=kw.get("sink_tokens", 0), rounded=True)
+
+
 def test_strides_and_padding_rows():
     """q and o inside wider rows, caches with a padding head, more buffer rows
     than the plan's, no lse."""
