@@ -742,8 +742,9 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
       }
     } else {
       // ---- both maps' partial states.  In what the merge adds up S_2 has the
-      // small weight lambda (W_1 - W_2), of the chunk's shares of the two maps,
-      // so the rounding of its weights is as small against the result.
+      // weight lambda (W_1 - W_2), of the chunk's shares of the two maps: where
+      // they weigh the chunks alike the rounding of S_2's weights hardly counts;
+      // at worst, maps that look at different chunks, it is that of S_2 itself.
       uint32_t y2[32];
       tc::tmem_ld32(tl + kDiffKeys * wg, y2);
       release_o();
