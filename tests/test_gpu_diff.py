@@ -4,8 +4,8 @@ Tolerances come from roundings alone (oracle.diff.slack).  A logit is 64
 products summed in fp32: with |q|, |k| <= 5 and scale 1/8 its error is below
 64 * 2^-24 * 64 * 25 / 8 = 7.6e-4 in the worst order and some 1e-5 in earnest;
 exponent, weights and sums add less than 1e-5.  WEIGHT covers these with 1e-4.
-On the tensor cores a weight is rounded to the input type and the row's sum is
-of the rounded weights: at most eps / 2 each, so eps in all."""
+On the tensor cores a weight is rounded to the input type, w_1 - lambda w_2 once
+and in a split unit's chunk w_2 once more: at most eps / 2 each, so eps in all."""
 from __future__ import annotations
 
 import ctypes
