@@ -21,9 +21,10 @@
 // (with two-term weights of either map instead, the mixed step took 65 us
 // against 58).
 //
-// Roles: warp 0 loads Q (two buffers) and K, warp 2 V, by TMA, into one ring
-// of four tiles (rings of two tiles each: 596 against 590 us for 12161 queries
-// of 8 prompts, 32 query heads, up to 3756 keys, in an earlier state); warp 1 issues the products;
+// Roles: warp 0 loads Q (two buffers) and K, warp 2 V, by TMA (pages below 8
+// tokens: by copies, with warp 3), into one ring of four tiles (rings of two
+// tiles each took 596 us against 590, for 12161 queries of 8 prompts, 32 query
+// heads, up to 3756 keys, before later steps); warp 1 issues the products;
 // warpgroups of warps 4..7, 8..11, 12..15 and 16..19 take 32 keys each of
 // every 128-key tile, for both maps (thread = row = tensor-memory lane).
 // Tensor memory: S of both maps (256 columns), O (128), two P buffers (64
