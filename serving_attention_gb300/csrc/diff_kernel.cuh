@@ -605,6 +605,7 @@ __global__ void __launch_bounds__(kDiffThreads, 1) diff_attention_kernel(const _
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bar.q_full[s], 1);
       mbar_init(&bar.q_empty[s], 2);  // one thread of each pair of softmax warpgroups
+      mbar_init(&bar.v_go[s], 1);
       mbar_init(&bar.s_full[s], 1);
       mbar_init(&bar.s_free[s], 4 * kDiffGroups);  // every softmax warp
       mbar_init(&bar.p_full[s], 4 * kDiffGroups);

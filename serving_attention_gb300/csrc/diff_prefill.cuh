@@ -54,7 +54,6 @@ constexpr int kDiffSoftmaxThreads = 128 * kDiffGroups;
 constexpr int kDiffBarrier = 6;  // all softmax warpgroups (1: decode, 3: end of phase, 4 and 5: two warpgroups)
 constexpr int kDiffStages = 4;   // K and V tiles in one ring
 constexpr int kDiffCopyBarrier = 8;  // named barrier of the two warps that copy K tiles of small pages
-constexpr int kDiffLoadBarrier = 7;  // named barrier of the K and the V loader
 constexpr int kDiffTmemO = 256, kDiffTmemP = 384;
 constexpr float kWeightScale = 13.f;  // softmax weights are multiplied by 2^13 before they are rounded
 // Register budgets, per thread (see kRegsLaunch): in the tensor-core phase
@@ -77,6 +76,7 @@ struct DiffPrefillBufs {  // every [128][64] block is a 128-byte swizzled operan
 struct DiffPrefillBars {
   uint64_t q_full[2], q_empty[2], kv_full[kDiffStages], kv_empty[kDiffStages];
   uint64_t v_clear[kDiffStages];  // a tile's V rows past the request's end cleared
+  uint64_t v_go[2];               // [Q buffer] the K loader is past the item's pass 0
   uint64_t s_full[2], s_free[2];  // [S buffer]
   uint64_t p_full[2];             // [buffer]
   uint64_t o_ready, o_free, drain;
@@ -213,11 +213,14 @@ __device__ uint32_t diff_pf_produce(const DiffParams& dp, DiffPrefillBufs& pf, D
       // A parity tells a phase from the next alone, so the V loads of an item
       // begin once the K loads are that far: at K(0) behind pass 0, the tiles
       // before t1 - 4 have been taken, and V(0)'s stage is at the phase before.
+      // One barrier an item, two in turn: the arrival for item i + 2 follows
+      // this warp's wait for Q buffer i & 1, so the output of item i, so its V
+      // tiles, so the V loader's wait for item i, which cannot miss a phase.
       if (q == 0) {
         if (kV)
-          named_barrier_sync(kDiffLoadBarrier, 64);
-        else if (!second)
-          named_barrier_arrive(kDiffLoadBarrier, 64);
+          warp_wait(&bar.v_go[ni & 1], (ni >> 1) & 1, abort);
+        else if (!second && lane == 0)
+          mbar_arrive(&bar.v_go[ni & 1]);
       }
       const bool free = warp_wait(&bar.kv_empty[st], ph ^ 1, abort);
       if (kCopies) {

@@ -163,11 +163,6 @@ __device__ __forceinline__ void named_barrier_sync(uint32_t id, uint32_t threads
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// The arrival alone: the warp does not wait for the barrier's other threads.
-__device__ __forceinline__ void named_barrier_arrive(uint32_t id, uint32_t threads) {
-  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-
 // The same barrier reached from different places in the code (barrier.sync
 // without .aligned): the roles of a CTA meet here from their own branches.
 __device__ __forceinline__ void named_barrier_sync_unaligned(uint32_t id, uint32_t threads) {

@@ -207,6 +207,17 @@ def test_few_ctas(ctas, kw, dtype):
     _check(b, lam, w, o, lse, window=kw.get("window_left", -1), sink=kw.get("sink_tokens", 0), rounded=True)
 
 
+@pytest.mark.parametrize("page", [4, 8, 64])
+@pytest.mark.parametrize("ctas", [1, 3])
+def test_runs_of_short_prompts(ctas, page):
+    """Many items of one tile in a row, where nothing but their own barriers holds the K and V loaders together."""
+    kv = [int(x) for x in np.random.default_rng(ctas + page).integers(9, 129, size=40)]
+    b, lam, w = _batch(21, kv, kv, 4, 1, page, "bf16", causal=1)
+    o, lse, info, ws, _ = _run(b, lam, w, _config(num_ctas=ctas))
+    assert info.num_items >= 40 and fi.device_status(ws) == 0
+    _check(b, lam, w, o, lse, rounded=True)
+
+
 @pytest.mark.parametrize("page", [1, 2, 4])
 @pytest.mark.parametrize("ctas,kw", [(2, {}), (3, dict(prefill_min_chunk=128, split_factor=64)),
                                      (2, dict(window_left=200, sink_tokens=5))])
