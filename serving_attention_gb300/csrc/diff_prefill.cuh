@@ -16,10 +16,14 @@
 // accumulators would: per 128 keys 512 in pass 0 and 512 + 512 in pass 1,
 // against 512 + 1024, or 512 + 2048 with weights of two terms; the second walk
 // costs 128 exponentials a thread, which overlap with them.
-// A split unit's chunk needs both maps' outputs for the merge: pass 2 walks
-// the keys for map 2 alone and accumulates S_2 beside pass 1's S_1 - lambda S_2
-// (with two-term weights of either map instead, the mixed step took 65 us
-// against 58).
+// A split unit's chunk needs both maps' outputs, each to be weighed by its own
+// map's share of the chunk: pass 1 walks the keys for map 1 alone and pass 2 for
+// map 2, with weights of two 16-bit terms, p = hi + lo, so that what the maps
+// have in common cancels in the merge too (1.00 times the error of rounding the
+// result alone).  With S_1 - lambda S_2 in pass 1 and S_2 in pass 2, weights of
+// one term, a prompt part of 600 queries behind 20000 keys took 121 us for 131,
+// but S_1 then had the rounding of map 2's weights in the chunk, at full size
+// where map 2 looks at other chunks.
 //
 // Roles: warp 0 loads Q (two buffers) and K, warp 2 V, by TMA (pages below 8
 // tokens: by copies, with warp 3), into one ring of four tiles (rings of two
@@ -29,7 +33,8 @@
 // every 128-key tile, for both maps (thread = row = tensor-memory lane).
 // Tensor memory: S of both maps (256 columns), O (128), two P buffers (64
 // each); in pass 0, which needs neither O nor P, their columns are a second S
-// buffer (757 -> 663 us).  A thread takes its 64 logits into registers and
+// buffer (757 -> 663 us), and where a pass has one map alone the other map's S
+// columns hold the second terms of P.  A thread takes its 64 logits into registers and
 // gives S back, so the next tile's S runs while it computes; P has columns of
 // its own, so S does not wait for P V either.  Four softmax warps on each
 // scheduler: with two (64 keys each) a warp's waits, loads and stores were
@@ -112,10 +117,11 @@ __device__ __forceinline__ bool item_v_tail(const Item& it, int page_size) {
 // its stages hold K.  With first = t the item's first place, and pending = 1
 // behind an item (whose last V comes after this item's first K):
 //   pass 0            K(0) t, K(j) t + pending + j
-//   later passes      from t1 = t + pending + tiles, their steps numbered q
-//                     through: K(0) t1, K(q) t1 + 2q - 1, V(q) t1 + 2q + 2
-//   the next item     t1 + 2 steps - 1.
-// A split unit's chunk leaves nothing pending: its last V has the place before.
+//   pass 1            from t1 = t + pending + tiles: K(0) t1, K(j) t1 + 2j - 1,
+//                     V(j) t1 + 2j + 2
+//   the next item     t1 + 2 tiles - 1.
+// The passes 1 and 2 of a split unit's chunk leave nothing pending: their last V
+// has the place before, and the pass or item behind them begins 2 tiles on.
 // Pages below 8 tokens, whose boxes would start inside a swizzle atom: the
 // rows are copied 16 bytes at a time into the same layout, K by warps 0 and 3,
 // 64 rows each, V by warp 2, and handed on once they have landed.  (Without
@@ -202,12 +208,12 @@ __device__ uint32_t diff_pf_produce(const DiffParams& dp, DiffPrefillBufs& pf, D
     const uint32_t t1 = t + pending + ntiles;
     int j = 0;
     for (int n = kV ? ntiles : 0; n < ntiles + steps; ++n) {
-      const int q = n - ntiles;  // step of the passes behind pass 0
-      const uint32_t at = q < 0 ? t + (n > 0 ? pending + n : 0) : kV ? t1 + 2 * q + 2 - (split && q + 1 == steps)
-                                                                           : t1 + (q > 0 ? 2 * q - 1 : 0);
+      const int q = n - ntiles, tile = j;   // step of the passes behind pass 0
+      const uint32_t tp = t1 + 2 * (q - tile);  // first place of its pass
+      const uint32_t at = q < 0 ? t + (n > 0 ? pending + n : 0) : kV ? tp + 2 * tile + 2 - (split && tile + 1 == ntiles)
+                                                                           : tp + (tile > 0 ? 2 * tile - 1 : 0);
       const uint32_t st = at % kDiffStages, ph = (at / kDiffStages) & 1;
       const int32_t cur = next;
-      const int tile = j;
       j = j + 1 < ntiles ? j + 1 : 0;
       next = page_of(j);
       // A parity tells a phase from the next alone, so the V loads of an item
@@ -360,24 +366,26 @@ __device__ void diff_pf_mma(const RunParams& p, DiffPrefillBufs& pf, DiffPrefill
   uint32_t ps = 3, pp = 0;                  // bit b: parity that the next use of S, P buffer b waits for
   uint32_t cleared = 0;                     // bit st: parity of the cleared tails of V stage st
   bool ok = true, issued = false;  // after a wait that ran out nothing more is issued
-  // S of a step in buffer x, of both maps or of map 2 alone
-  auto do_s = [&](uint64_t a, int x, bool both) {
+  // S of a step in buffer x, of the maps m0 .. m1
+  auto do_s = [&](uint64_t a, int x, int m0, int m1) {
     const uint32_t st = t % kDiffStages;
     ok = ok && poll_wait(s_free + 8 * x, (ps >> x) & 1, kv_full + 8 * st, (t / kDiffStages) & 1, abort);
     if (!ok) return;
     tc::fence_after_sync();
     const uint64_t b = dk + 2048u * st;
     const uint32_t d = tmem + 2 * kTileN * x;
-    if (both) mma4<false>(d, a, 0, b, idesc_s, 0);
-    mma4<false>(d + kTileN, a + 1024u, 0, b + 1024u, idesc_s, 0);
+    if (m0 == 0) mma4<false>(d, a, 0, b, idesc_s, 0);
+    if (m1 == 1) mma4<false>(d + kTileN, a + 1024u, 0, b + 1024u, idesc_s, 0);
     tc::mma_commit_warp(&bar.s_full[x]);
     tc::mma_commit_warp(&bar.kv_empty[st]);
     ps ^= 1u << x;
     ++t;
     issued = true;
   };
-  // P V of a step, weights in buffer b, accumulated at column d
-  auto do_pv = [&](uint32_t d, int b, bool first, bool last, bool tail) {
+  // P V of a step, weights in buffer b, second terms (or none) at column lo
+  constexpr uint32_t kNoLo = ~0u;
+  const uint32_t o_col = tmem + kDiffTmemO;
+  auto do_pv = [&](uint32_t lo, int b, bool first, bool last, bool tail) {
     const uint32_t st = t % kDiffStages;
     if (first) ok = ok && poll_wait(o_free, (no & 1) ^ 1, o_free, (no & 1) ^ 1, abort);
     ok = ok && poll_wait(p_full + 8 * b, (pp >> b) & 1, (tail ? v_clear : kv_full) + 8 * st,
@@ -386,8 +394,12 @@ __device__ void diff_pf_mma(const RunParams& p, DiffPrefillBufs& pf, DiffPrefill
     tc::fence_after_sync();
     const uint64_t v = dv + 2048u * st;
     const uint32_t w = tmem + kDiffTmemP + 64 * b;
-    mma4<true>(d, 0, w, v, idesc_pv, first ? 0u : 1u);
-    mma4<true>(d, 0, w + 32, v + 512u, idesc_pv, 1u);
+    mma4<true>(o_col, 0, w, v, idesc_pv, first ? 0u : 1u);
+    mma4<true>(o_col, 0, w + 32, v + 512u, idesc_pv, 1u);
+    if (lo != kNoLo) {
+      mma4<true>(o_col, 0, lo + 64 * b, v, idesc_pv, 1u);
+      mma4<true>(o_col, 0, lo + 64 * b + 32, v + 512u, idesc_pv, 1u);
+    }
     tc::mma_commit_warp(&bar.kv_empty[st]);
     if (last) {
       tc::mma_commit_warp(&bar.o_ready);
@@ -397,18 +409,18 @@ __device__ void diff_pf_mma(const RunParams& p, DiffPrefillBufs& pf, DiffPrefill
     pp ^= 1u << b;
     ++t;
   };
-  // The P V of a step follows the S of the next step: what is pending across
-  // passes and items, if anything.
+  // The P V of a step follows the S of the next step: what is pending behind
+  // an item, if anything.
   struct {
-    bool any, first, last, tail;
+    bool any, first, tail;
     int b;
-  } pv{false, false, false, false, 0};
-  auto flush = [&](uint32_t d) {
-    if (pv.any) do_pv(d, pv.b, pv.first, pv.last, pv.tail);
+  } pv{false, false, false, 0};
+  auto flush = [&] {
+    if (pv.any) do_pv(kNoLo, pv.b, pv.first, true, pv.tail);
     pv.any = false;
   };
-  const uint32_t o_col = tmem + kDiffTmemO;
-  bool o2 = false;  // S_2 of a split unit's chunk is in the first S buffer
+  auto wait_o = [&] { ok = ok && poll_wait(o_free, (no & 1) ^ 1, o_free, (no & 1) ^ 1, abort); };
+  bool split_before = false;
   DiffItem next = load_diff_item(p.iws, off_items, b0);
   for (int32_t i = b0; i < b1 && ok; ++i) {
     const DiffItem it = next;
@@ -419,36 +431,37 @@ __device__ void diff_pf_mma(const RunParams& p, DiffPrefillBufs& pf, DiffPrefill
     const uint32_t qb = ni & 1, q_full = smem_u32(&bar.q_full[0]) + 8 * qb;
     const uint64_t a = dq + 2048u * qb;
     ok = poll_wait(q_full, (ni >> 1) & 1, q_full, (ni >> 1) & 1, abort);
-    if (ok && o2) ok = poll_wait(o_free, (no & 1) ^ 1, o_free, (no & 1) ^ 1, abort);
-    o2 = it.part >= 0;
-    do_s(a, 0, true);
-    flush(o_col);
+    if (split_before) wait_o();  // its second terms are where S goes
+    split_before = it.part >= 0;
+    do_s(a, 0, 0, 1);
+    flush();
     for (int j = 1; j < ntiles && ok; ++j) {
-      // S buffer 1: O's and P's columns, once the item before is read out
-      if (j == 1) ok = poll_wait(o_free, (no & 1) ^ 1, o_free, (no & 1) ^ 1, abort);
-      do_s(a, j & 1, true);
+      if (j == 1) wait_o();  // S buffer 1: O's and P's columns, once the item before is read out
+      do_s(a, j & 1, 0, 1);
     }
-    do_s(a, 0, true);
-    for (int j = 1; j < ntiles && ok; ++j) {
-      do_s(a, 0, true);
-      do_pv(o_col, (j - 1) & 1, j == 1, false, false);
-    }
-    pv = {true, ntiles == 1, it.part < 0, tail, (ntiles - 1) & 1};
-    if (it.part >= 0) {
-      // pass 2 accumulates in the columns of map 1's S, which it does not use
-      do_s(a, 0, false);
-      flush(o_col);
+    if (it.part < 0) {
+      do_s(a, 0, 0, 1);
       for (int j = 1; j < ntiles && ok; ++j) {
-        do_s(a, 0, false);
-        do_pv(tmem, (ntiles + j - 1) & 1, j == 1, false, false);
+        do_s(a, 0, 0, 1);
+        do_pv(kNoLo, (j - 1) & 1, j == 1, false, false);
       }
-      pv = {true, ntiles == 1, true, tail, 1};
-      flush(tmem);
+      pv = {true, ntiles == 1, tail, (ntiles - 1) & 1};
+    } else {
+      for (int x = 0; x < 2 && ok; ++x) {
+        if (x == 1) wait_o();  // map 1's second terms are where map 2's S goes
+        const uint32_t lo = tmem + (x == 0 ? kTileN : 0);
+        do_s(a, 0, x, x);
+        for (int j = 1; j < ntiles && ok; ++j) {
+          do_s(a, 0, x, x);
+          do_pv(lo, (j - 1) & 1, j == 1, false, false);
+        }
+        do_pv(lo, (ntiles - 1) & 1, ntiles == 1, true, tail);
+      }
     }
     ++ni;
   }
   if (pv.any) ++t;  // the place of the first K that a next item would have
-  flush(o_col);
+  flush();
   if (issued) {  // no product may still run when the CTA leaves the phase
     tc::mma_commit_warp(&bar.drain);
     if (lane == 0) mbar_wait_drain(&bar.drain, 0);
@@ -529,16 +542,16 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
     }
     bool ok = true;
     const float lam = live ? __ldg(dp.lambda + head) : 0.f;
-    // This warpgroup's 32 logits of both maps (or of map 2 alone) of tile j in
-    // S buffer x; S goes back to the MMA warp.
-    auto load_s = [&](int x, bool both, uint32_t (&a)[32], uint32_t (&b)[32]) {
+    // This warpgroup's 32 logits of a tile in S buffer x, of both maps or (into
+    // a) of map mp alone; S goes back to the MMA warp.
+    auto load_s = [&](int x, bool both, int mp, uint32_t (&a)[32], uint32_t (&b)[32]) {
       const uint32_t ph = (s_phase >> x) & 1;
       if (!__all_sync(0xffffffffu, mbar_try_wait(&bar.s_full[x], ph))) ok = ok && warp_wait(&bar.s_full[x], ph, abort);
       s_phase ^= 1u << x;
       tc::fence_after_sync();
       const uint32_t col = tl + 2 * kTileN * x + kDiffKeys * wg;
-      if (both) tc::tmem_ld32(col, a);
-      tc::tmem_ld32(col + kTileN, b);
+      tc::tmem_ld32(col + kTileN * mp, a);
+      if (both) tc::tmem_ld32(col + kTileN, b);
       tc::tmem_ld_wait();
       tc::fence_before_sync();
       __syncwarp();
@@ -559,11 +572,10 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
       for (int e = 0; e < 32; ++e)
         if (!(seen >> e & 1)) v[e] = 0xff800000u;
     };
-    // This thread's weights into P buffer b, the other one of the step before.
-    // It is free: the step's S was issued behind the P V of two steps before,
+    // This thread's weights are in P buffer b, the other one of the step before.
+    // It was free: the step's S was issued behind the P V of two steps before,
     // and a commit stands for everything issued before it.
-    auto store_p = [&](int b, const uint32_t (&pk)[16]) {
-      tc::tmem_st16(tl + kDiffTmemP + 64 * b + 16 * wg, pk);
+    auto signal_p = [&](int b) {
       tc::tmem_st_wait();
       tc::fence_before_sync();
       __syncwarp();
@@ -576,7 +588,7 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
     bool have_m = false;  // of every row of the warp
     for (int j = 0; j < ntiles; ++j) {
       uint32_t s[2][32];
-      load_s(j & 1, true, s[0], s[1]);
+      load_s(j & 1, true, 0, s[0], s[1]);
       if (j >= c2) continue;
       if (j < c0 || j >= c1) {
         const uint32_t seen = visible(j);
@@ -645,6 +657,59 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
       if (wg == x && ll > 0.f) lse = (m[x] + log2l[x]) * 0.69314718055994531f;
     }
 
+    uint32_t y[32];  // this warpgroup's 32 dims of a row of the accumulator, which goes back to the MMA warp
+    auto val = [&](int e) { return __uint_as_float(y[e]); };
+    auto load_o = [&] {
+      ok = ok && warp_wait(&bar.o_ready, no & 1, abort);
+      ++no;
+      tc::fence_after_sync();
+      tc::tmem_ld32(tl + kDiffTmemO + kDiffKeys * wg, y);
+      tc::tmem_ld_wait();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.o_free);
+    };
+    if (item.part >= 0) {
+      // ---- passes 1 and 2 of a split unit's chunk: one map's weights, scaled by
+      // 2^13, in two terms that keep 16 (bf16) or 22 (fp16) bits; its partial state
+#pragma unroll 1
+      for (int x = 0; x < 2; ++x) {
+        const float a = (x ? m[1] + log2l[1] : m[0] + log2l[0]) - kWeightScale;
+        const float2 n = make_float2(-a, -a);
+        const uint32_t lo_col = tl + (x ? 0 : kTileN) + 16 * wg;
+        for (int j = 0; j < ntiles; ++j) {
+          uint32_t s[32], hi[16], lo[16];
+          load_s(0, false, x, s, s);
+          if (j < c0 || j >= c1) mask(visible(j), s);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 z = fma2(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), cc, n);
+            const float w0 = ex2(z.x), w1 = ex2(z.y);
+            hi[e] = tc::pack2<T>(w0, w1);
+            const float2 h = Elem<T>::to_float2(hi[e]);
+            lo[e] = tc::pack2<T>(w0 - h.x, w1 - h.y);
+          }
+          tc::tmem_st16(tl + kDiffTmemP + 64 * (j & 1) + 16 * wg, hi);
+          tc::tmem_st16(lo_col + 64 * (j & 1), lo);
+          signal_p(j & 1);
+        }
+        load_o();
+        if (live && !*abort) {
+          const float unscale = l[0] > 0.f ? ex2(-kWeightScale) : 0.f;  // both maps see the same keys
+          const int64_t prw = int64_t(item.part) + x * nrows + r;
+          float4* const dst = reinterpret_cast<float4*>(p.fws + p.partial_o_offset + prw * kHeadDim + kDiffKeys * wg);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            dst[e] = make_float4(val(4 * e) * unscale, val(4 * e + 1) * unscale, val(4 * e + 2) * unscale,
+                                 val(4 * e + 3) * unscale);
+          if (wg == x) p.fws[prw] = lse;
+        }
+      }
+      if (elected) mbar_arrive(&bar.q_empty[ni & 1]);
+      ++ni;
+      continue;
+    }
+
     // ---- pass 1: weights w_1 - lambda w_2, scaled by 2^sigma so that they
     // stay below 2^14 and small ones inside an fp16's normal range
     const float sigma = kWeightScale - (fabsf(lam) > 1.f ? __log2f(fabsf(lam)) : 0.f);
@@ -653,7 +718,7 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
     for (int j = 0; j < ntiles; ++j) {
       const int b = j & 1;
       uint32_t s1[32], s2[32], pk[16];
-      load_s(0, true, s1, s2);
+      load_s(0, true, 0, s1, s2);
       if (j < c0 || j >= c1) {
         const uint32_t seen = visible(j);
         mask(seen, s1);
@@ -666,107 +731,52 @@ __device__ void diff_pf_softmax(const DiffParams& dp, DiffPrefillBufs& pf, DiffP
         const float2 w = fma2(make_float2(ex2(y.x), ex2(y.y)), nl, make_float2(ex2(x.x), ex2(x.y)));
         pk[e] = tc::pack2<T>(w.x, w.y);
       }
-      store_p(b, pk);
+      tc::tmem_st16(tl + kDiffTmemP + 64 * b + 16 * wg, pk);
+      signal_p(b);
     }
+    if (p.lse && wg < 2 && live && !*abort) p.lse[(tok * p.num_qo_heads + head) * 2 + wg] = lse;
     const float unscale = l[0] > 0.f ? ex2(-sigma) : 0.f;
-    if (item.part >= 0) {
-      // ---- pass 2, of a split unit's chunk: map 2 alone, accumulated beside
-      // pass 1's result (which is S_1 - lambda S_2 of the chunk)
-      const float a = m[1] + log2l[1] - kWeightScale;
-      const float2 n = make_float2(-a, -a);
-      for (int j = 0; j < ntiles; ++j) {
-        uint32_t s[32], pk[16];
-        load_s(0, false, s, s);
-        if (j < c0 || j >= c1) mask(visible(j), s);
+    load_o();
+    // ---- the output
+    float f = unscale * dp.out_scale;
+    if (dp.norm_w) {
+      float ss = 0.f;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float2 x = fma2(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), cc, n);
-          pk[e] = tc::pack2<T>(ex2(x.x), ex2(x.y));
-        }
-        store_p((ntiles + j) & 1, pk);
+      for (int e = 0; e < 32; ++e) ss += val(e) * val(e);
+      pf.sq[wg][r] = ss * unscale * unscale;
+      named_barrier_sync(kDiffBarrier, kDiffSoftmaxThreads);
+      f *= rms_factor((pf.sq[0][r] + pf.sq[1][r]) + (pf.sq[2][r] + pf.sq[3][r]), dp.norm_eps);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float4 w = pf.norm_w[kDiffKeys / 4 * wg + e];
+        y[4 * e] = __float_as_uint(val(4 * e) * w.x);
+        y[4 * e + 1] = __float_as_uint(val(4 * e + 1) * w.y);
+        y[4 * e + 2] = __float_as_uint(val(4 * e + 2) * w.z);
+        y[4 * e + 3] = __float_as_uint(val(4 * e + 3) * w.w);
       }
     }
-    if (p.lse && item.part < 0 && wg < 2 && live && !*abort) p.lse[(tok * p.num_qo_heads + head) * 2 + wg] = lse;
-    // this warpgroup's 32 dims of the accumulators' rows
-    ok = ok && warp_wait(&bar.o_ready, no & 1, abort);
-    ++no;
-    tc::fence_after_sync();
-    uint32_t y[32];
-    tc::tmem_ld32(tl + kDiffTmemO + kDiffKeys * wg, y);
-    auto val = [&](int e) { return __uint_as_float(y[e]); };
-    auto release_o = [&] {
-      tc::tmem_ld_wait();
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.o_free);
+    auto pack8 = [&](int e) {
+      return make_uint4(tc::pack2<T>(val(e) * f, val(e + 1) * f), tc::pack2<T>(val(e + 2) * f, val(e + 3) * f),
+                        tc::pack2<T>(val(e + 4) * f, val(e + 5) * f), tc::pack2<T>(val(e + 6) * f, val(e + 7) * f));
     };
-    if (item.part < 0) {
-      // ---- the output
-      release_o();
-      float f = unscale * dp.out_scale;
-      if (dp.norm_w) {
-        float ss = 0.f;
+    const int qb = ni & 1;
+    if (nrows == kTileM) {  // a whole tile leaves through the item's Q halves, by one TMA store each
+      uint16_t* stage = &pf.q[qb][half][0][0];
+      uint4* my_row = reinterpret_cast<uint4*>(stage + r * 64);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) ss += val(e) * val(e);
-        pf.sq[wg][r] = ss * unscale * unscale;
-        named_barrier_sync(kDiffBarrier, kDiffSoftmaxThreads);
-        f *= rms_factor((pf.sq[0][r] + pf.sq[1][r]) + (pf.sq[2][r] + pf.sq[3][r]), dp.norm_eps);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float4 w = pf.norm_w[kDiffKeys / 4 * wg + e];
-          y[4 * e] = __float_as_uint(val(4 * e) * w.x);
-          y[4 * e + 1] = __float_as_uint(val(4 * e + 1) * w.y);
-          y[4 * e + 2] = __float_as_uint(val(4 * e + 2) * w.z);
-          y[4 * e + 3] = __float_as_uint(val(4 * e + 3) * w.w);
-        }
+      for (int c = 0; c < 4; ++c) my_row[(4 * (wg & 1) + c) ^ (r & 7)] = pack8(8 * c);
+      fence_proxy_async_smem();
+      named_barrier_sync(kEpilogueBarrier0 + half, 256);
+      if (elected && !*abort) {
+        tc::tma_store_3d(&p.tm_o, stage, 64 * half, item.hk * G, rq.qo_start + item.row0 / G);
+        tc::bulk_commit();
       }
-      auto pack8 = [&](int e) {
-        return make_uint4(tc::pack2<T>(val(e) * f, val(e + 1) * f), tc::pack2<T>(val(e + 2) * f, val(e + 3) * f),
-                          tc::pack2<T>(val(e + 4) * f, val(e + 5) * f), tc::pack2<T>(val(e + 6) * f, val(e + 7) * f));
-      };
-      const int qb = ni & 1;
-      if (nrows == kTileM) {  // a whole tile leaves through the item's Q halves, by one TMA store each
-        uint16_t* stage = &pf.q[qb][half][0][0];
-        uint4* my_row = reinterpret_cast<uint4*>(stage + r * 64);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) my_row[(4 * (wg & 1) + c) ^ (r & 7)] = pack8(8 * c);
-        fence_proxy_async_smem();
-        named_barrier_sync(kEpilogueBarrier0 + half, 256);
-        if (elected && !*abort) {
-          tc::tma_store_3d(&p.tm_o, stage, 64 * half, item.hk * G, rq.qo_start + item.row0 / G);
-          tc::bulk_commit();
-        }
-        q_held = qb;
-      } else {
-        if (elected) mbar_arrive(&bar.q_empty[qb]);
-        if (live && !*abort) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) reinterpret_cast<uint4*>(out)[c] = pack8(8 * c);
-        }
-      }
+      q_held = qb;
     } else {
-      // ---- both maps' partial states.  In what the merge adds up S_2 has the
-      // weight lambda (W_1 - W_2), of the chunk's shares of the two maps: where
-      // they weigh the chunks alike the rounding of S_2's weights hardly counts;
-      // at worst, maps that look at different chunks, it is that of S_2 itself.
-      uint32_t y2[32];
-      tc::tmem_ld32(tl + kDiffKeys * wg, y2);
-      release_o();
-      if (elected) mbar_arrive(&bar.q_empty[ni & 1]);
+      if (elected) mbar_arrive(&bar.q_empty[qb]);
       if (live && !*abort) {
-        const float unscale2 = l[1] > 0.f ? ex2(-kWeightScale) : 0.f;
-        float4* const dst = reinterpret_cast<float4*>(p.fws + p.partial_o_offset +
-                                                      (int64_t(item.part) + r) * kHeadDim + kDiffKeys * wg);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float4 b = make_float4(__uint_as_float(y2[4 * e]) * unscale2, __uint_as_float(y2[4 * e + 1]) * unscale2,
-                                       __uint_as_float(y2[4 * e + 2]) * unscale2,
-                                       __uint_as_float(y2[4 * e + 3]) * unscale2);
-          dst[e] = make_float4(val(4 * e) * unscale + lam * b.x, val(4 * e + 1) * unscale + lam * b.y,
-                               val(4 * e + 2) * unscale + lam * b.z, val(4 * e + 3) * unscale + lam * b.w);
-          dst[nrows * (kHeadDim / 4) + e] = b;
-        }
-        if (wg < 2) p.fws[int64_t(item.part) + wg * nrows + r] = lse;
+        for (int c = 0; c < 4; ++c) reinterpret_cast<uint4*>(out)[c] = pack8(8 * c);
       }
     }
     ++ni;

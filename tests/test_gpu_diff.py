@@ -4,8 +4,8 @@ Tolerances come from roundings alone (oracle.diff.slack).  A logit is 64
 products summed in fp32: with |q|, |k| <= 5 and scale 1/8 its error is below
 64 * 2^-24 * 64 * 25 / 8 = 7.6e-4 in the worst order and some 1e-5 in earnest;
 exponent, weights and sums add less than 1e-5.  WEIGHT covers these with 1e-4.
-On the tensor cores a weight is rounded to the input type, w_1 - lambda w_2 once
-and in a split unit's chunk w_2 once more: at most eps / 2 each, so eps in all."""
+On the tensor cores w_1 - lambda w_2 is rounded to the input type, by at most
+eps / 2 (eps is allowed); a split unit's chunk has weights of two terms."""
 from __future__ import annotations
 
 import ctypes
@@ -162,6 +162,34 @@ def test_split_prefill(dtype):
     o, lse, info, ws, _ = _run(b, lam, w, _config(prefill_min_chunk=128, decode_min_chunk=64, split_factor=16))
     assert info.num_merge_units > 2 and fi.device_status(ws) == 0
     _check(b, lam, w, o, lse, rounded=True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("page", [4, 16])
+def test_a_chunk_that_one_map_leaves(page, dtype):
+    """Map 1 looks at the first chunk, map 2 at the fourth; in the first, map 2's
+    largest weight is that of a key with large values, which counts for nothing
+    in the whole (e^-30).  A chunk's weights are two terms, 2^-16 of a weight at
+    most, which WEIGHT covers: no rounding of one term."""
+    b, lam, w = _batch(22, [40, 1], [700, 640], 8, 2, page, dtype, causal=1, poison=False)
+    b.q.zero_()
+    b.k.zero_()
+    b.v.mul_(0.01)
+    b.q[..., 0] = 8
+    b.q[..., 64] = 8
+    b.sm_scale = 0.125  # a logit is the key's one dim
+    for i in range(2):
+        ids = torch.as_tensor(b.kv_indices[b.kv_indptr[i]:b.kv_indptr[i + 1]], device=DEV).long()
+        at = lambda key: (ids[key // page], key % page)  # noqa: E731
+        for key in range(128):
+            b.k[at(key)][:, 0] = 20
+            b.k[at(384 + key)][:, 64] = 40
+        b.k[at(5)][:, 0] = -20
+        b.k[at(5)][:, 64] = 10
+        b.v[at(5)] *= 8000
+    o, lse, info, ws, _ = _run(b, lam, None, _config(prefill_min_chunk=128, decode_min_chunk=64, split_factor=16))
+    assert info.num_merge_units > 2 and fi.device_status(ws) == 0
+    _check(b, lam, None, o, lse)
 
 
 @pytest.mark.parametrize("split", [False, True])
