@@ -60,9 +60,10 @@ extern "C" {
  * Checked on the device: 0 <= qo_lens[b] <= kv_lens[b] <=
  * block_table_width * page_size (counts[4] = FI_ERR_INVALID_ARG otherwise),
  * and that the pages and tokens fit max_pages and max_tokens and the free list
- * holds what is taken (FI_ERR_CAPACITY).  Then nothing but counts is written,
- * counts[0..2] being what the step would need (at most INT32_MAX) and
- * counts[3] = *free_head.
+ * holds what is taken (FI_ERR_CAPACITY).  Then counts[0..2] is what the step
+ * would need (at most INT32_MAX), counts[3] = *free_head, every token gets
+ * position 0 and slot -1 (so that an append behind the call in a captured step
+ * writes nothing to the cache) and nothing else is written.
  */
 typedef struct {
     const int32_t* qo_lens;

@@ -140,7 +140,16 @@ __global__ void __launch_bounds__(kTableThreads) step_tables_kernel(const __grid
                     : tid == 4 ? status
                                : 0;
   }
-  if (status != FI_OK) return;
+  const int64_t threads = int64_t(gridDim.x) * kTableThreads, gtid = int64_t(blockIdx.x) * kTableThreads + tid;
+  if (status != FI_OK) {
+    // the last step's slots must not stand: the append behind this call would
+    // write this step's keys and values over that step's
+    for (int64_t t = gtid; t < a.max_tokens; t += threads) {
+      a.positions[t] = 0;
+      a.slots[t] = -1;
+    }
+    return;
+  }
   {
     int32_t qo = int32_t(before.qo + inc.qo - mine.qo), kv = int32_t(before.pages + inc.pages - mine.pages),
             nw = int32_t(before.taken + inc.taken - mine.taken);
@@ -161,7 +170,6 @@ __global__ void __launch_bounds__(kTableThreads) step_tables_kernel(const __grid
     }
   }
   __syncthreads();
-  const int64_t threads = int64_t(gridDim.x) * kTableThreads, gtid = int64_t(blockIdx.x) * kTableThreads + tid;
   for (int64_t b = gtid; b <= B; b += threads) {
     a.qo_indptr[b] = s_qo[gap(int(b))];
     a.kv_indptr[b] = s_kv[gap(int(b))];

@@ -200,6 +200,42 @@ def test_tables_refuse_on_the_device(what):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("what", ["free", "tokens", "lengths"])
+def test_refused_tables_append_nothing(what):
+    """A step whose tables are refused behind one that was not: the append of the same captured
+    step leaves the cache, which holds the earlier step's keys at its slots, as it is."""
+    t = step.StepTables(3, 9, 600, DEV)
+    bt, free, head = _i32([[b] + 39 * [-1] for b in (1, 2, 3)]), _i32([4, 5]), _i32([0])
+    ql, kl = _i32([1, 2, 3]), _i32([10, 11, 12])
+    k = _randn((600, 2, 64), "bf16", 1)
+    kc, vc = (torch.zeros((8, 16, 2, 64), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    r = step.rotary_setup(64)
+
+    def device_step():
+        step.build_tables(t, ql, kl, bt, 16, free, head)
+        step.append(r, t.positions, t.slots, None, None, k, k, kc, vc)
+
+    device_step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        device_step()
+    assert int(t.counts[4]) == 0 and int((t.slots >= 0).sum()) == 6
+    before = [x.clone() for x in (kc, vc, bt, t.qo_indptr, t.kv_indptr, t.last_page_len, t.kv_indices)]
+    k.copy_(_randn((600, 2, 64), "bf16", 2))
+    if what == "free":
+        kl.copy_(_i32([17, 18, 19]))  # three pages of two
+    elif what == "tokens":
+        ql.copy_(_i32([1, 2, 598]))
+        kl.copy_(_i32([10, 11, 600]))
+    else:
+        kl.copy_(_i32([10, 1, 12]))
+    graph.replay()
+    assert int(t.counts[4]) != 0 and int(t.counts[3]) == 0
+    assert (t.slots == -1).all() and (t.positions == 0).all()
+    for a, b in zip(before, (kc, vc, bt, t.qo_indptr, t.kv_indptr, t.last_page_len, t.kv_indices)):
+        assert torch.equal(a, b)
+
+
 def test_tables_without_a_free_list():
     t = step.StepTables(2, 4, 2, DEV)
     step.build_tables(t, _i32([1, 1]), _i32([18, 5]), _i32([[3, 4], [5, 6]]), 16)
