@@ -25,6 +25,7 @@ namespace {
 constexpr int kTableThreads = 256;
 constexpr int kTableWarps = kTableThreads / 32;
 constexpr int kTableAhead = 4;  // page-table entries a thread has in flight
+constexpr size_t kPlainSmem = 47 * 1024;  // dynamic shared memory without an opt-in, beside the static arrays
 
 struct TableParams {
   const int32_t *qo_lens, *kv_lens;
@@ -265,7 +266,7 @@ extern "C" fi_status fi_build_step_tables(const fi_step_tables_args* x, void* st
                 x->positions,     x->slots,          int32_t(x->max_tokens), x->counts};
   while ((1 << a.log2_page) < P) ++a.log2_page;
   const size_t smem = size_t(3) * (gap(a.batch) + 1) * 4;
-  if (smem > 48 * 1024) {
+  if (smem > kPlainSmem) {
     static bool configured[kMaxDevices] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return FI_ERR_CUDA;

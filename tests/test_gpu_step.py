@@ -5,6 +5,10 @@ relative of its result or better; product sums in fp32 add 2 * 2^-24; so 1e-6
 times amplitude * (|a| + |b|), and half a step of the output type."""
 from __future__ import annotations
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -16,6 +20,7 @@ from serving_attention_gb300 import differential, step
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
 
 
@@ -198,6 +203,19 @@ def test_tables_refuse_on_the_device(what):
     assert bt.tolist() == table
     for a, b in zip(before, (t.qo_indptr, t.kv_indptr, t.last_page_len, t.kv_indices, t.positions, t.slots)):
         assert torch.equal(a, b)
+
+
+def test_tables_of_batches_around_the_shared_memory_opt_in():
+    """Lengths that fill the 48 KB of a launch without an opt-in but for the kernel's static arrays (3624 to
+    3640 requests).  In a process of its own: a larger batch before would opt in for all."""
+    code = ("import torch\nfrom serving_attention_gb300 import step\n"
+            "for n in range(3560, 3660, 4):\n"
+            "    t, one = step.StepTables(n, n, n), torch.ones(n, dtype=torch.int32, device='cuda')\n"
+            "    ids = torch.arange(n, device='cuda').int()\n"
+            "    step.build_tables(t, one, 2 * one, ids[:, None], 16)\n"
+            "    assert t.counts.tolist() == [n, n, 0, 0, 0, 0, 0, 0] and t.slots.equal(16 * ids + 1)\n")
+    got = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert got.returncode == 0, got.stderr
 
 
 @pytest.mark.parametrize("what", ["free", "tokens", "lengths"])
