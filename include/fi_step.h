@@ -158,7 +158,11 @@ fi_status fi_rotary_setup(const fi_rotary_config* cfg, fi_rotary* out);
  *   may be 0.
  *   positions int32 [num_tokens], device; any value.
  * dtype FI_FP16 or FI_BF16; base pointers and strides are multiples of 16
- * bytes.  An input may be broadcast (stride 0), an output's rows must be apart.
+ * bytes.  An input may be broadcast (stride 0).  An output's rows must be apart,
+ * its dimensions nested (the larger stride at least what the other dimension
+ * spans): refused otherwise (FI_ERR_INVALID_ARG), as are an output that overlaps
+ * its input at the same strides without being it, and one that begins where its
+ * input does at other strides.  Other overlaps are not looked for.
  * num_tokens 0 does nothing (no pointer is read or checked).
  */
 typedef struct {
@@ -185,8 +189,9 @@ fi_status fi_rotary_apply(const fi_rotary_apply_args* args, void* stream);
  *   below num_pages * page_size (padding) writes nothing to the caches; its q
  *   is rotated.  Two tokens of one call must not have the same slot.
  *   num_q_heads may be 0; v_in NULL with v_dim 0 appends keys alone.
- * Other arguments, dtypes and alignment as for fi_rotary_apply; page_size a
- * power of two in [1, 128].
+ * Other arguments, dtypes, alignment and output rows (of the caches too: pages,
+ * slots and heads nested) as for fi_rotary_apply; page_size a power of two in
+ * [1, 128].  The caches must not overlap the inputs.
  */
 typedef struct {
     const fi_rotary* rotary;

@@ -18,7 +18,9 @@
 
 #include <cmath>
 #include <cstdint>
+#include <cstdlib>
 #include <cstring>
+#include <utility>
 
 #include "../../include/fi_step.h"
 #include "ptx.cuh"
@@ -232,15 +234,50 @@ fi_status check_rotary(const fi_rotary* rot, int64_t num_tokens, int64_t num_q_h
 
 bool rows_ok(const fi_rows& r) { return aligned(r.data, 16) && stride_ok(r.stride_tok) && stride_ok(r.stride_head); }
 
-// Rows that are written: no two of them in one place, and in place only with
-// the strides of the input.
-bool apart(int64_t n, int64_t stride) { return n < 2 || stride > 0; }
-bool output_ok(const fi_rows& in, const fi_rows& out, int64_t tokens, int64_t heads) {
-  return apart(tokens, out.stride_tok) && apart(heads, out.stride_head) &&
-         (in.data != out.data || (in.stride_tok == out.stride_tok && in.stride_head == out.stride_head));
+// Rows that are written: no two of them in one place.  The dimensions of more
+// than one entry are nested: each one's stride is at least what those of smaller
+// strides span.  (Sorts the dimensions; one of a single entry goes last.)
+template <int N>
+bool nested(int64_t (&size)[N], int64_t (&stride)[N], int64_t dim) {
+  for (int i = 0; i < N; ++i)
+    if (size[i] < 2) stride[i] = INT64_MAX;
+  for (int i = 1; i < N; ++i)
+    for (int j = i; j > 0 && stride[j] < stride[j - 1]; --j) {
+      std::swap(stride[j], stride[j - 1]);
+      std::swap(size[j], size[j - 1]);
+    }
+  int64_t span = dim, more;
+  for (int i = 0; i < N && size[i] > 1; ++i)
+    if (stride[i] < span || __builtin_mul_overflow(stride[i], size[i] - 1, &more) ||
+        __builtin_add_overflow(span, more, &span))
+      return false;
+  return true;
 }
-bool cache_ok(const int64_t strides[3], int64_t pages, int64_t page_size, int64_t heads) {
-  return apart(pages, strides[0]) && apart(page_size, strides[1]) && apart(heads, strides[2]);
+
+// The rows of an input and an output are the same (in place) or do not meet.
+// At the same strides that is exact: rows i1 and i0 places apart in the outer
+// and the inner dimension meet if that is less than dim elements from how far
+// the two are apart.  Other strides are left to the caller.
+bool output_ok(const fi_rows& in, const fi_rows& out, int64_t tokens, int64_t heads, int64_t dim) {
+  int64_t size[2] = {tokens, heads}, stride[2] = {out.stride_tok, out.stride_head};
+  if (!nested(size, stride, dim)) return false;
+  const bool same = (tokens < 2 || in.stride_tok == out.stride_tok) && (heads < 2 || in.stride_head == out.stride_head);
+  if (in.data == out.data) return same;
+  if (!same) return true;
+  const int64_t apart = (reinterpret_cast<intptr_t>(out.data) - reinterpret_cast<intptr_t>(in.data)) / 2;
+  auto floor_div = [](int64_t x, int64_t y) { return x / y - (x % y < 0 ? 1 : 0); };
+  const int64_t k1 = floor_div(apart, stride[1]);
+  for (int64_t i1 = k1; i1 <= k1 + 1; ++i1) {  // no other can: the rows of one place span less than a stride
+    if (i1 <= -size[1] || i1 >= size[1]) continue;
+    const int64_t left = apart - i1 * stride[1], k0 = floor_div(left, stride[0]);
+    for (int64_t i0 = k0; i0 <= k0 + 1; ++i0)
+      if (i0 > -size[0] && i0 < size[0] && std::abs(left - i0 * stride[0]) < dim) return false;
+  }
+  return true;
+}
+bool cache_ok(const int64_t strides[3], int64_t pages, int64_t page_size, int64_t heads, int64_t dim) {
+  int64_t size[3] = {pages, page_size, heads}, stride[3] = {strides[0], strides[1], strides[2]};
+  return nested(size, stride, dim);
 }
 
 RotaryRows rows_of(const fi_rows& in, const fi_rows& out, int64_t heads) {
@@ -306,8 +343,8 @@ extern "C" fi_status fi_rotary_apply(const fi_rotary_apply_args* x, void* stream
   if (!aligned(x->positions, 4) || (q && (!rows_ok(x->q_in) || !rows_ok(x->q_out))) ||
       (k && (!rows_ok(x->k_in) || !rows_ok(x->k_out))))
     return FI_ERR_ALIGNMENT;
-  if ((q && !output_ok(x->q_in, x->q_out, x->num_tokens, x->num_q_heads)) ||
-      (k && !output_ok(x->k_in, x->k_out, x->num_tokens, x->num_kv_heads)))
+  if ((q && !output_ok(x->q_in, x->q_out, x->num_tokens, x->num_q_heads, x->rotary->head_dim)) ||
+      (k && !output_ok(x->k_in, x->k_out, x->num_tokens, x->num_kv_heads, x->rotary->head_dim)))
     return FI_ERR_INVALID_ARG;
   RotaryParams a;
   std::memset(&a, 0, sizeof a);
@@ -337,9 +374,9 @@ extern "C" fi_status fi_rotary_append(const fi_rotary_append_args* x, void* stre
     return FI_ERR_ALIGNMENT;
   for (int i = 0; i < 3; ++i)
     if (!stride_ok(x->k_strides[i]) || (v && !stride_ok(x->v_strides[i]))) return FI_ERR_ALIGNMENT;
-  if ((q && !output_ok(x->q_in, x->q_out, x->num_tokens, x->num_q_heads)) ||
-      !cache_ok(x->k_strides, x->num_pages, P, x->num_kv_heads) ||
-      (v && !cache_ok(x->v_strides, x->num_pages, P, x->num_kv_heads)))
+  if ((q && !output_ok(x->q_in, x->q_out, x->num_tokens, x->num_q_heads, x->rotary->head_dim)) ||
+      !cache_ok(x->k_strides, x->num_pages, P, x->num_kv_heads, x->rotary->head_dim) ||
+      (v && !cache_ok(x->v_strides, x->num_pages, P, x->num_kv_heads, x->v_dim)))
     return FI_ERR_INVALID_ARG;
   RotaryParams a;
   std::memset(&a, 0, sizeof a);

@@ -69,6 +69,31 @@ def test_rotate(dtype, dim, rot, interleaved, scaling):
     assert torch.equal(q, q_out)
 
 
+def test_rotate_beside_its_input():
+    """Outputs in the memory of their inputs, rows apart: columns behind or before the input's, rows behind all
+    of them, heads between the input's, one token or head with any stride; heads the outer dimension."""
+    r = step.rotary_setup(64)
+    T, H = 9, 3
+    pos = torch.arange(T, device=DEV).int()
+    wide, tall = _randn((T, 2 * H, 64), "bf16", 1), _randn((2 * T, H, 64), "bf16", 2)
+    outer = _randn((2 * H, T, 64), "bf16", 3).transpose(0, 1)
+    one = _randn((1, 4, 72), "bf16", 4)[:, :, :64]
+    for x, y in ((wide[:, :H], wide[:, H:]), (wide[:, H:], wide[:, :H]), (tall[:T], tall[T:]), (tall[T:], tall[:T]),
+                 (wide[:, ::2], wide[:, 1::2]), (wide[:, 1::2], wide[:, ::2]), (outer[:, :H], outer[:, H:]),
+                 (outer[:, 1::2], outer[:, ::2]), (wide[:, 1:2], wide[:, 5:6]), (wide[3:4], wide[2:3])):
+        want, p = torch.empty_like(x), pos[:x.shape[0]]
+        step.rotate(r, p, x, want)
+        step.rotate(r, p, x, y)
+        assert torch.equal(y, want)
+    want = torch.empty((1, 4, 64), dtype=torch.bfloat16, device=DEV)
+    step.rotate(r, pos[:1], one, want)
+    step.rotate(r, pos[:1], one, one.as_strided(one.shape, (8, 72, 1)))  # in place; one token has no token stride
+    assert torch.equal(one, want)
+    for x, y in ((wide[:, :H], wide[:, 1:1 + H]), (tall[:T], tall[2:2 + T]), (tall[5:5 + T], tall[:T])):
+        with pytest.raises(fi.FIError):
+            step.rotate(r, pos, x, y)
+
+
 @pytest.mark.parametrize("tokens", [1, 63, 700, 9001])
 def test_rotate_token_counts(tokens):
     r = step.rotary_setup(128)

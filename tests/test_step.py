@@ -112,6 +112,21 @@ def test_append_refuses_outputs_that_overlap(kw):
     assert _append(**kw) == 1
 
 
+@pytest.mark.parametrize("kw", [dict(qoh=8), dict(qoh=120), dict(qot=1016), dict(qot=128), dict(kot=128, koh=128),
+                                dict(qot=128, qoh=504), dict(qot=1 << 62), dict(qo=32 + 2048, qot=1024),
+                                dict(qo=32 + 256), dict(q=32 + 6144, qo=32), dict(q=32 + 6144 + 1792, qo=32),
+                                dict(ko=64 + 768), dict(qt=128, qh=512, qot=128, qoh=512, qo=32 + 2 * (3 * 512 + 384))])
+def test_apply_refuses_rows_that_meet(kw):
+    """Rows of 128 that overlap their neighbours; an output some tokens or heads from its input, at its strides."""
+    assert _apply(**kw) == 1
+
+
+@pytest.mark.parametrize("kw", [dict(k2=64), dict(k1=128), dict(k1=248), dict(k0=2048), dict(v2=64), dict(v0=4088),
+                                dict(k0=128, k1=1152, k2=128), dict(v0=1 << 61), dict(qo=32 + 256), dict(qoh=64)])
+def test_append_refuses_rows_that_meet(kw):
+    assert _append(**kw) == 1
+
+
 def test_no_tokens_need_no_pointers():
     """The rows of an empty tensor have no address."""
     none = dict(n=0, pos=0, q=0, qo=0, k=0)
