@@ -38,7 +38,8 @@ extern "C" fi_status fi_batch_paged_attention_run_differential(const fi_differen
   if (info->num_partial_rows > 0 && !a->float_workspace_dev) return FI_ERR_INVALID_ARG;
   if (info->head_dim != kHeadDim) return FI_ERR_UNSUPPORTED;
   if (a->dtype != FI_FP16 && a->dtype != FI_BF16) return FI_ERR_UNSUPPORTED;
-  if (info->num_kv_heads < 1 || info->num_qo_heads % info->num_kv_heads) return FI_ERR_UNSUPPORTED;
+  if (info->num_kv_heads < 1 || info->num_qo_heads < 1 || info->num_qo_heads % info->num_kv_heads)
+    return FI_ERR_UNSUPPORTED;
   const int P = info->page_size;
   if (P < 1 || P > 128 || (P & (P - 1))) return FI_ERR_UNSUPPORTED;
   if (!aligned16(a->q) || !aligned16(a->o) || !aligned16(a->k_cache) || !aligned16(a->v_cache) ||

@@ -136,6 +136,11 @@ def test_run_refusals(kw, status):
     assert _run(**kw) == status
 
 
+@pytest.mark.parametrize("heads", [0, -2])
+def test_run_refuses_a_plan_without_heads(heads):
+    assert _run(num_qo_heads=heads, page_size=4) == 2
+
+
 def test_run_refuses_no_arguments():
     assert differential.load().fi_batch_paged_attention_run_differential(None, None) == 1
 
