@@ -102,7 +102,8 @@ typedef struct {
      * difference of two softmax maps per query head; the other runs refuse
      * them (0, the default: ordinary attention).  A sliding window and sink
      * tokens apply; a soft-cap, RoPE or a cascade plan with it are
-     * FI_ERR_UNSUPPORTED, other values FI_ERR_INVALID_ARG. */
+     * FI_ERR_UNSUPPORTED, as is a request of more than INT32_MAX - 256 keys;
+     * other values FI_ERR_INVALID_ARG. */
     int32_t differential;
 } fi_plan_config;
 

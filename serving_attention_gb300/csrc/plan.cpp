@@ -203,6 +203,9 @@ fi_status plan_requests(const fi_plan_config* cfg, const std::vector<Req>& reqs,
   const bool diff = cfg->differential != 0;
   const int32_t maps = diff ? 2 : 1;
   const int32_t prefill_rows = diff ? FI_TILE_PREFILL_DIFF : FI_TILE_PREFILL;
+  // Its kernels count keys in 32 bits, up to two tiles past a request's end.
+  for (const Req& rq : reqs)
+    if (diff && rq.kv_len > INT32_MAX - 2 * FI_GRANULE_PREFILL) return FI_ERR_UNSUPPORTED;
   // Chunk boundaries fall on pages of every cache the plan reads.
   const int32_t max_page = std::max(page_size, cascade ? shared_page_size : page_size);
 

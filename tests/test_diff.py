@@ -102,6 +102,15 @@ def test_plan_refusals(field, value, status):
     assert plan_ref.make_plan(cfg.as_dict(), *args, 0)[0] == status
 
 
+@pytest.mark.parametrize("keys,status", [(2**31 - 1, 2), (2**31 - 256, 2), (2**31 - 257, 0)])
+def test_plan_refuses_requests_whose_tiles_pass_an_int32(keys, status):
+    cfg = fi.make_plan_config(8, differential=1)
+    args = (np.array([0, 1]), np.array([0, -(-keys // 128)]), np.array([0]), np.array([(keys - 1) % 128 + 1]), 8, 2,
+            128, 128, 0)
+    assert fi.plan_host(cfg, *args)[0] == status
+    assert plan_ref.make_plan(cfg.as_dict(), *args, 0)[0] == status
+
+
 def test_cascade_refuses_differential():
     cfg = fi.make_plan_config(8, differential=1)
     one = (np.array([0, 1]), np.array([0, 1]), np.array([0]), np.array([3]))
