@@ -146,6 +146,17 @@ def test_window_and_sink(window, sink, split):
     _check(b, lam, w, o, lse, window=window, sink=sink, rounded=True)
 
 
+@pytest.mark.parametrize("page", [1, 16])
+@pytest.mark.parametrize("window", [2**31 - 1, 2**31 - 20, 3])
+def test_widest_windows_of_queries_before_the_keys(window, page):
+    """More queries than keys without the causal mask: the first ones lie before key 0, and
+    their distance to the window's lowest key passes an int."""
+    b, lam, w = _batch(23, [40, 3, 2], [10, 1, 100], 8, 2, page, "bf16")
+    o, lse, info, ws, _ = _run(b, lam, w, _config(window_left=window))
+    assert fi.device_status(ws) == 0
+    _check(b, lam, w, o, lse, window=window, rounded=True)
+
+
 @pytest.mark.parametrize("page", [4, 16, 128])
 @pytest.mark.parametrize("window,sink", [(100, 1), (255, 128), (300, 130), (640, 300)])
 def test_sinks_before_a_window(window, sink, page):

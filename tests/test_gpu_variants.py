@@ -66,6 +66,15 @@ def test_variants_tensor_core_tiles(qo, kv, window, sink, cap):
     assert info.num_prefill_items > 0
 
 
+@pytest.mark.parametrize("page", [1, 16])
+@pytest.mark.parametrize("window", [2**31 - 1, 2**31 - 20, 3])
+def test_widest_windows_of_queries_before_the_keys(window, page):
+    """More queries than keys without the causal mask: the first ones lie before key 0, and
+    their distance to the window's lowest key passes an int."""
+    b = workloads.make_batch("wide", "bf16", [40, 3, 2], [10, 1, 100], 8, 2, page, 0, 500, DEV)
+    _full(b, window)
+
+
 def test_windowed_long_decode_sampled():
     """Llama-3-8B-shaped decode with a 4096-token window and 4 sink tokens."""
     b = workloads.llama8b_decode(device=DEV, batch=16)
