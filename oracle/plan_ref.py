@@ -58,7 +58,9 @@ Rule:
     load, ties to the smaller CTA index (longest processing time first).
     Differential plans (two softmax maps per row): prefill-class tiles hold
     128 rows, no multi-head units, every chunk of a merge unit takes 2 * rows
-    partial rows, and every merge unit carries the late flag.
+    partial rows, and every merge unit carries the late flag; on pages below 8
+    tokens a CTA's prefill-class items of requests of up to 32 rows come behind
+    its others.
  6. Output: header (with the variant: window, sink, soft-cap bits, and for
     RoPE its position capacity, theta and scale bits and the table offset;
     then the count of late units, the partial rows used, the batch's query
@@ -422,8 +424,11 @@ def _plan(cfg, reqs, num_shared, shared_page_size, block_of, total_qo, num_qo_he
     pos = 0
     for c in range(C):
         ws[off_cta + c] = pos
-        # prefill-class tiles first, then 16-row tiles, each in the order dealt
-        mine = [f for f in per_cta[c] if lq[f[0]] * group > 16] + [f for f in per_cta[c] if lq[f[0]] * group <= 16]
+        # prefill-class tiles first, then 16-row tiles, each in the order dealt; in between a
+        # differential plan's requests of up to 32 rows on pages below 8 tokens
+        cut = 32 if diff and page_size < 8 else 16
+        rows = [lq[f[0]] * group for f in per_cta[c]]
+        mine = [f for lo, hi in ((cut, 1 << 40), (16, cut), (0, 16)) for f, r in zip(per_cta[c], rows) if lo < r <= hi]
         for fields in mine:
             ws[off_items + ITEM_INTS * pos: off_items + ITEM_INTS * (pos + 1)] = fields
             pos += 1

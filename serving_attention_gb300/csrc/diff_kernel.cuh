@@ -544,11 +544,12 @@ __device__ void diff_consume(const DiffParams& dp, DiffSmem& sm, int32_t item_be
 // at most 16 packed rows, or, on pages below 8 tokens, of at most 32, which the
 // decode path takes in two passes: 16 requests on pages of one token took
 // 143 us with 32 rows each (on the tensor cores, where a tile is copied row by
-// row, 162), but 209 with 48 (164) and 341 with 80 (165).
+// row, 162), but 209 with 48 (164) and 341 with 80 (165).  The planner puts
+// these behind the CTA's larger items.
 __device__ __forceinline__ int32_t diff_first_decode_item(const RunParams& p, int32_t begin, int32_t end,
                                                           int32_t off_items) {
   const int lane = threadIdx.x & 31;
-  const int most = p.kv[0].page_size < kMinTmaPage ? 32 : FI_TILE_DECODE;
+  const int most = p.kv[0].page_size < kMinTmaPage ? FI_DIFF_SMALL_PAGE_ROWS : FI_TILE_DECODE;
   for (int32_t i0 = begin; i0 < end; i0 += 32) {
     const bool decode = i0 + lane >= end || !p.kv[0].tc ||
                         __ldg(p.iws + off_items + FI_ITEM_INTS * (i0 + lane) + 9) * p.group <= most;  // its qo_len

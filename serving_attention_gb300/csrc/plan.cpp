@@ -466,20 +466,26 @@ fi_status plan_requests(const fi_plan_config* cfg, const std::vector<Req>& reqs,
   std::memset(ws, 0, size_t(total_ints) * 4);
   // CTA c's items occupy [start[c], start[c+1]): its prefill-class items first,
   // then its 16-row items, each kept in the order the deal handed them out
-  // (one switch between the kernel's two tile paths per CTA at most).
+  // (one switch between the kernel's two tile paths per CTA at most; in between
+  // the prefill-class items that the differential kernel runs on its 16-row path).
+  const bool small_pages = diff && page_size < FI_MIN_TMA_PAGE;
+  auto part_of = [&](const DealKey& k) {
+    if (k.tile == FI_TILE_DECODE) return 2;
+    return small_pages && int64_t(reqs[k.b].qo_len) * group <= FI_DIFF_SMALL_PAGE_ROWS ? 1 : 0;
+  };
   std::vector<int32_t> start(C + 1, 0);
   for (int32_t c = 0; c < C; ++c) start[c + 1] = start[c] + per_cta[c];
   for (int32_t c = 0; c <= C; ++c) ws[off_cta + c] = start[c];
   std::vector<int32_t> fill(start.begin(), start.end() - 1);
   int64_t n_decode = 0;
-  for (int pass = 0; pass < 2; ++pass) {
-    const int32_t tile = pass == 0 ? FI_TILE_PREFILL : FI_TILE_DECODE;
+  for (int part = 0; part < 3; ++part) {
+    if (part == 1 && !small_pages) continue;
     for (size_t i = 0; i < order.size(); ++i) {
-      if (order[i].tile != tile) continue;
+      if (part_of(order[i]) != part) continue;
       const int32_t slot = fill[owner[i]]++;
       const Chunk& c = chunks[size_t(order[i].pos)];
       std::memcpy(ws + off_items + int64_t(FI_ITEM_INTS) * slot, c.fields, sizeof c.fields);
-      if (tile == FI_TILE_DECODE) ++n_decode;
+      if (part == 2) ++n_decode;
     }
   }
   if (n_merge) std::memcpy(ws + off_merge, merge_rows.data(), merge_rows.size() * 4);

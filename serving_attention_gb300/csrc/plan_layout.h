@@ -66,6 +66,7 @@
 #define FI_ITEM_INTS 16
 #define FI_ITEM_LEAD 13
 #define FI_MIN_TMA_PAGE 8  // smallest page of the tensor-core path
+#define FI_DIFF_SMALL_PAGE_ROWS 32  // differential, smaller pages: requests of up to so many packed rows leave it
 #define FI_MERGE_INTS 8
 #define FI_REQ_INTS 4
 #define FI_CASCADE_INTS 12

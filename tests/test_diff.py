@@ -93,6 +93,23 @@ def test_plan_matches_reference(seed):
     assert all(a[1] <= b[0] for a, b in zip(spans, spans[1:])) and all(s[1] <= info.num_partial_rows for s in spans)
 
 
+@pytest.mark.parametrize("page", [1, 4, 8])
+def test_requests_of_few_rows_come_behind_prompts(page):
+    """On pages below 8 tokens requests of 17 to 32 packed rows take the 16-row path, which a CTA does not leave
+    again: they come behind its larger ones, however long, and before those of up to 16 rows."""
+    qo, kv = [8, 100, 1, 5, 300, 7, 64], [9000, 300, 5000, 8000, 400, 6000, 64]
+    kvp, last = workloads._pages_for(np.asarray(kv), page)
+    cfg = fi.make_plan_config(3, differential=1)
+    args = (np.concatenate([[0], np.cumsum(qo)]), kvp, np.arange(int(kvp[-1])), last, 8, 2, 128, page, 1,
+            int(kvp[-1]) + 1)
+    st, ws, info = fi.plan_host(cfg, *args)
+    assert st == 0 and np.array_equal(ws, plan_ref.make_plan(cfg.as_dict(), *args)[1])
+    for c in range(3):
+        items = ws[ws[7] + 16 * ws[32 + c]:ws[7] + 16 * ws[33 + c]].reshape(-1, 16)
+        kinds = [0 if r > (32 if page < 8 else 16) else 1 if r > 16 else 2 for r in items[:, 9] * 4]
+        assert kinds == sorted(kinds)
+
+
 @pytest.mark.parametrize("field,value,status", [("differential", 2, 1), ("differential", -1, 1),
                                                 ("logits_soft_cap", 30.0, 2), ("rope_max_positions", 4096, 2)])
 def test_plan_refusals(field, value, status):

@@ -268,6 +268,16 @@ def test_prefill_on_small_pages(ctas, kw, page):
     _check(b, lam, w, o, lse, window=kw.get("window_left", -1), sink=kw.get("sink_tokens", 0), rounded=True)
 
 
+@pytest.mark.parametrize("page", [1, 4])
+@pytest.mark.parametrize("ctas", [1, 4])
+def test_few_rows_beside_prompts_on_small_pages(ctas, page):
+    """Requests of 17 to 32 packed rows, the longest of all, in a CTA with prompts and decodes."""
+    b, lam, w = _batch(24, [8, 100, 1, 5, 130, 7], [1500, 300, 900, 1100, 200, 700], 8, 2, page, "bf16", causal=1)
+    o, lse, info, ws, _ = _run(b, lam, w, _config(num_ctas=ctas))
+    assert fi.device_status(ws) == 0
+    _check(b, lam, w, o, lse, rounded=True)
+
+
 def test_strides_and_padding_rows():
     """q and o inside wider rows, caches with a padding head, more buffer rows
     than the plan's, no lse."""
