@@ -56,9 +56,10 @@ typedef struct {
     int32_t max_merge_units;     /* split units per plan */
     int64_t max_partial_rows;    /* rows of fp32 partial state (head_dim floats + 1 LSE each) */
     int32_t decode_min_chunk;    /* smallest KV chunk of a 16-row tile, tokens (default 256) */
-    int32_t prefill_min_chunk;   /* smallest KV chunk of a 256-row tile, tokens (default 1024) */
+    int32_t prefill_min_chunk;   /* smallest KV chunk of a 256-row tile, tokens (default 1024); of a differential
+                                    plan's 128-row tile four times that with fewer than three CTAs a tile */
     int32_t decode_cost_weight;  /* cost of one KV token in a 16-row tile (default 8) */
-    int32_t prefill_cost_weight; /* cost of one KV token in a 256-row tile (default 9) */
+    int32_t prefill_cost_weight; /* cost of one KV token in a 256-row (differential: 128-row) tile (default 9) */
     int32_t split_factor;        /* target chunks per CTA per tile class (default 1) */
     /* Mask and logit variant, constant for a model (FlashInfer 0.6 wiki page,
      * "Blackwell (SM100/SM103) 전용 경로 / CuTe-DSL GQA Decode 커널": sliding
@@ -116,7 +117,7 @@ typedef struct {
     int64_t num_partial_rows;
     int32_t num_qo_heads, num_kv_heads, head_dim, page_size, causal;
     int32_t chunk_decode;        /* KV tokens per chunk chosen for 16-row tiles */
-    int32_t chunk_prefill;       /* KV tokens per chunk chosen for 256-row tiles */
+    int32_t chunk_prefill;       /* KV tokens per chunk chosen for 256-row (differential: 128-row) tiles */
     int32_t num_decode_items, num_prefill_items;
     int32_t variant;             /* bit 0: logits soft-cap; bit 1: sliding window (and sink) mask; bit 2: RoPE;
                                     bit 3: differential */

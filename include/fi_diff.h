@@ -45,6 +45,13 @@ extern "C" {
  * a request's last page may hold anything, NaN included.  Page ids outside
  * [0, num_pages) read as zeros.
  *
+ * Requests of up to 16 packed rows (query tokens x group) read their keys once.
+ * Longer ones run on the tensor cores, tiles of 128 rows that walk their keys
+ * twice (three times in a split unit), whatever the rows in them, where the
+ * group divides 128; with another group (3, 5, 6, 7, ...) they run 16 rows at a
+ * time and are some eight times slower (4 prompts of 1000 queries and 2000 keys:
+ * 170 us with 32 query and 8 key heads, 1064 with 24 and 8).
+ *
  * A row's partial states take two rows of the float workspace (one per map).
  * Two launches on `stream`: the run and the merge of split units; both read
  * their counts from the workspace, so a captured graph serves later plans.

@@ -255,7 +255,7 @@ def _plan(cfg, reqs, num_shared, shared_page_size, block_of, total_qo, num_qo_he
     diff = bool(cfg.get("differential", 0))
     if diff and any(r[3] > 2**31 - 1 - 256 for r in reqs):  # its kernels count keys in 32 bits
         return UNSUPPORTED, None, None
-    # rows of a tile: with two maps per row, the two 128-row halves of a prefill tile are the maps
+    # rows of a tile: with two maps per row a prefill tile has 128 rows
     height = {TILE_DECODE: TILE_DECODE, TILE_PREFILL: TILE_PREFILL_DIFF if diff else TILE_PREFILL}
     C = cfg["num_ctas"]
     lq = [r[1] for r in reqs]

@@ -7,9 +7,12 @@
 //   y = S_1 - lambda_h S_2,   o = out_scale * y                        or
 //   o = out_scale * y / sqrt(mean(y^2) + eps) * w   (RMS norm over the 128 dims)
 //
-// Both maps read the same V rows, so K and V are read once: the cache layout,
-// its bytes and the work list are those of the ordinary run; a row's two maps
-// are kept apart as two rows of the matrix products.
+// Both maps read the same V rows, so the row tiles below read K and V once:
+// the cache layout, its bytes and the work list are those of the ordinary run; a
+// row's two maps are kept apart as two rows of the matrix products.  Requests of
+// more than 16 packed rows walk their keys twice or three times (see
+// diff_prefill.cuh) where the group divides 128; other groups take the row
+// tiles, 16 rows a pass over the chunk.
 //
 // Row tiles (mma.sync m16n8k16; this path is bound by the cache's bytes, 8
 // query rows fill the 16 rows of the smallest product exactly):

@@ -26,22 +26,21 @@
 // where map 2 looks at other chunks.
 //
 // Roles: warp 0 loads Q (two buffers) and K, warp 2 V, by TMA (pages below 8
-// tokens: by copies, with warp 3), into one ring of four tiles (rings of two
-// tiles each took 596 us against 590, for 12161 queries of 8 prompts, 32 query
-// heads, up to 3756 keys, before later steps); warp 1 issues the products;
+// tokens: by copies, with warp 3), into one ring of four tiles (two rings of two
+// tiles hold less of what is needed next); warp 1 issues the products;
 // warpgroups of warps 4..7, 8..11, 12..15 and 16..19 take 32 keys each of
 // every 128-key tile, for both maps (thread = row = tensor-memory lane).
 // Tensor memory: S of both maps (256 columns), O (128), two P buffers (64
 // each); in pass 0, which needs neither O nor P, their columns are a second S
-// buffer (757 -> 663 us), and where a pass has one map alone the other map's S
-// columns hold the second terms of P.  A thread takes its 64 logits into registers and
+// buffer, and where a pass has one map alone the other map's S columns hold the
+// second terms of P.  A thread takes its 64 logits into registers and
 // gives S back, so the next tile's S runs while it computes; P has columns of
 // its own, so S does not wait for P V either.  Four softmax warps on each
 // scheduler: with two (64 keys each) a warp's waits, loads and stores were
-// not covered (792 us).
+// not covered.
 //
-// What bounds it (550 us for that workload; its tiles' products alone would
-// take 293): a tile takes some 3200 cycles of both passes, of which the
+// What bounds it (556 us for 12161 queries of 8 prompts, 32 query heads, up to
+// 3756 keys; its tiles' products alone would take 293): a tile takes some 3200 cycles of both passes, of which the
 // products read 160 KB of operands and TMA writes 96 KB through shared memory's
 // 128 bytes a cycle (2050 cycles), and the MMA and softmax warps hand S and P
 // to one another; leaving the arithmetic of either pass out gains 6 %.  An item
@@ -112,21 +111,10 @@ __device__ __forceinline__ bool item_v_tail(const Item& it, int page_size) {
          it.kv0 + item_kv_tiles(it) * kTileN > it.rq.kv_len;
 }
 
-// Warp 0 (kV false): Q and K tiles; warp 2 (kV true): V tiles.  K and V tiles
-// share one ring, in the order in which the MMA warp takes them: in pass 0 all
-// its stages hold K.  With first = t the item's first place, and pending = 1
-// behind an item (whose last V comes after this item's first K):
-//   pass 0            K(0) t, K(j) t + pending + j
-//   pass 1            from t1 = t + pending + tiles: K(0) t1, K(j) t1 + 2j - 1,
-//                     V(j) t1 + 2j + 2
-//   the next item     t1 + 2 tiles - 1.
-// The passes 1 and 2 of a split unit's chunk leave nothing pending: their last V
-// has the place before, and the pass or item behind them begins 2 tiles on.
-// Pages below 8 tokens, whose boxes would start inside a swizzle atom: the
-// rows are copied 16 bytes at a time into the same layout, K by warps 0 and 3,
-// 64 rows each, V by warp 2, and handed on once they have landed.  (Without
-// it such items took the 16-row tiles of the decode path: 4 prompts of 300 to
-// 512 queries on pages of one token took 477 us, now 101.)
+// Pages below 8 tokens, whose boxes would start inside a swizzle atom: a tile's
+// rows are copied 16 bytes at a time into the boxes' layout, K by warps 0 and 3,
+// 64 rows each, V by warp 2, and handed on once they have landed.  4 prompts of
+// 300 to 512 queries: 38 us on pages of one token, 26 on pages of 16.
 template <bool kV>
 __device__ __forceinline__ void diff_pf_copy(const DiffParams& dp, const DiffItem& it, uint16_t (*buf)[kTileN][64],
                                              int key0, int row0, int rows) {
@@ -158,6 +146,16 @@ __device__ __forceinline__ void diff_pf_copy(const DiffParams& dp, const DiffIte
   __syncwarp();
 }
 
+// Warp 0 (kV false): Q and K tiles; warp 2 (kV true): V tiles.  K and V tiles
+// share one ring, in the order in which the MMA warp takes them: in pass 0 all
+// its stages hold K.  With t the item's first place, and pending = 1 behind an
+// item (whose last V comes after this item's first K):
+//   pass 0            K(0) t, K(j) t + pending + j
+//   pass 1            from t1 = t + pending + tiles: K(0) t1, K(j) t1 + 2j - 1,
+//                     V(j) t1 + 2j + 2
+//   the next item     t1 + 2 tiles - 1.
+// The passes 1 and 2 of a split unit's chunk leave nothing pending: their last V
+// has the place before, and the pass or item behind them begins 2 tiles on.
 // Returns which stages this warp loaded, and above them the phases of the last
 // loads.
 template <bool kV, bool kCopies>

@@ -197,9 +197,9 @@ fi_status plan_requests(const fi_plan_config* cfg, const std::vector<Req>& reqs,
   const float cap = cfg->logits_soft_cap;
   const int32_t rope_max = cfg->rope_max_positions;
   // Differential attention: each packed row has two softmax maps, so a
-  // prefill-class tile holds 128 rows (the two M tiles of the tensor-core path
-  // are the two maps of the same rows) and a row's partial state takes two
-  // partial rows, the maps' blocks of a chunk one after the other.
+  // prefill-class tile holds 128 rows (one M tile; the maps' logits are two
+  // column blocks of tensor memory) and a row's partial state takes two partial
+  // rows, the maps' blocks of a chunk one after the other.
   const bool diff = cfg->differential != 0;
   const int32_t maps = diff ? 2 : 1;
   const int32_t prefill_rows = diff ? FI_TILE_PREFILL_DIFF : FI_TILE_PREFILL;
@@ -282,10 +282,12 @@ fi_status plan_requests(const fi_plan_config* cfg, const std::vector<Req>& reqs,
   };
   const int64_t gran_dec = std::max(max_page, FI_GRANULE_DECODE);
   // A differential unit that is split walks its keys three times instead of
-  // twice, so it gains only where at least three chunks a unit run at once:
-  // with fewer CTAs a unit, four times the shortest chunk.  Measured, us a
-  // call: 56 units of some 4100 keys 50.4 whole, 59.8 in four, 62.3 in two;
-  // four prompt parts beside 24 decodes 60.2 against 68.7 in four.
+  // twice, with two products a key and map, so it gains only where at least
+  // three chunks a unit run at once: with fewer CTAs a unit, four times the
+  // shortest chunk.  Measured, us a call, units of 32 queries and 4100 keys: 56
+  // units 66 whole, 75 in two, 87 in three chunks; 48 units 65 whole, 57 in
+  // three; 24 units 64 whole, 44 in five; four prompt parts beside 24 decodes
+  // 107 whole, 119 in four.
   int64_t min_pre = cfg->prefill_min_chunk;
   if (diff) {
     int64_t units_pre = 0;
