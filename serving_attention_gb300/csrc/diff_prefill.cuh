@@ -220,9 +220,11 @@ __device__ uint32_t diff_pf_produce(const DiffParams& dp, DiffPrefillBufs& pf, D
       // One barrier an item, two in turn: the arrival for item i + 2 follows
       // this warp's wait for Q buffer i & 1, so the output of item i, so its V
       // tiles, so the V loader's wait for item i, which cannot miss a phase.
+      // The wait is as long as a pass 0, some 1600 cycles a tile of at most 2^24
+      // tiles, and has that for its bound: a K loader that gives up ends it.
       if (q == 0) {
         if (kV)
-          warp_wait(&bar.v_go[ni & 1], (ni >> 1) & 1, abort);
+          warp_wait<32 * kWaitBudgetClocks>(&bar.v_go[ni & 1], (ni >> 1) & 1, abort);
         else if (!second && lane == 0)
           mbar_arrive(&bar.v_go[ni & 1]);
       }

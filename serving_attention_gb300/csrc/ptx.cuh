@@ -79,6 +79,7 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
 // lane 0's view of completion, abort and budget is broadcast, so all lanes
 // leave on the same iteration with the same result: false when the budget ran
 // out (the abort flag is then set) or another role gave up.
+template <long long kBudget = kWaitBudgetClocks>
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
   // Fast path: one poll, no read of the abort flag (a shared-memory read is
   // slow while the tensor core streams its operands from shared memory).
@@ -90,7 +91,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
     for (int k = 0; k < kPollsPerCheck; ++k)
       if (__shfl_sync(0xffffffffu, mbar_try_wait_sleep(bar, parity) ? 1 : 0, 0)) return true;
     const int gave_up = *abort != 0 ? 2 : 0;
-    const int late = clock64() - t0 > kWaitBudgetClocks ? 4 : 0;
+    const int late = clock64() - t0 > kBudget ? 4 : 0;
     const int st = __shfl_sync(0xffffffffu, gave_up | late, 0);
     if (st & 2) return false;
     if (st & 4) {
