@@ -381,3 +381,41 @@ def test_steps_of_a_batch_captured_and_replayed():
         assert np.abs(f64(lse)[:total] - rl).max() <= 2e-2
         head.copy_(tabs.counts[3:4])
         lens = kvs
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("page", [1, 16])
+def test_a_step_against_the_cache_that_it_wrote(page, dtype):
+    """The same three calls, attention against the oracle over the rotated queries and the cache as they
+    are, so that its own roundings are all there is: 1e-4 of a weight for the exponentials and sums (as in the
+    tests of the attention alone), one rounding of a weight, half a step of the output."""
+    Hq, Hk, qs, kvs = 8, 2, [1, 40, 1, 9], [300, 200, 33, 9]
+    pages = [-(-x // page) for x in kvs]
+    n, pool = sum(qs), sum(pages) + 5
+    ids = np.random.default_rng(page).permutation(pool).astype(np.int32)
+    table = np.full((4, max(pages)), -1, np.int32)
+    for b in range(4):
+        had = -(-(kvs[b] - qs[b]) // page)
+        table[b, :had], ids = ids[:had], ids[had:]
+    t = step.StepTables(4, sum(pages), n + 3, DEV)
+    step.build_tables(t, _i32(qs), _i32(kvs), _i32(table.tolist()), page, _i32(ids.tolist()), _i32([0]))
+    q, k, v = (_randn((n + 3, h, 128), dtype, i) for i, h in enumerate((Hq, Hk, Hk)))
+    kc, vc = _randn((pool, page, Hk, 128), dtype, 3), _randn((pool, page, Hk, 128), dtype, 4)
+    half = lambda x: x.unflatten(2, (2, 64)).flatten(1, 2)  # noqa: E731
+    step.append(step.rotary_setup(64), t.positions, t.slots, half(q), half(q), half(k), half(v),
+                kc.view(pool, page, 2 * Hk, 64), vc.view(pool, page, 2 * Hk, 64))
+    lam, w = torch.rand(Hq, generator=_gen(5), device=DEV), 1 + 0.2 * torch.randn(128, generator=_gen(6), device=DEV)
+    ws = fi.Workspace(fi.default_plan_config(0, differential=1, max_items=1 << 12, max_merge_units=1 << 10,
+                                             max_partial_rows=1 << 14), device=DEV)
+    qop, kvp = np.cumsum([0] + qs), np.cumsum([0] + pages)
+    last = [x - (p - 1) * page for x, p in zip(kvs, pages)]
+    info = fi.plan(ws, qop, kvp, [], last, Hq, Hk, 128, page, 1)
+    o, lse = torch.empty_like(q), torch.empty((n + 3, Hq, 2), device=DEV)
+    differential.run(ws, info, q, kc, vc, t.kv_indices, lam, o, lse, 0.125, norm_weight=w)
+    assert fi.device_status(ws) == 0 and int(t.counts[4]) == 0
+    f64 = lambda x: x.double().cpu().numpy()  # noqa: E731
+    ro, rl, y, size = oracle_diff.attention(qop, kvp, t.kv_indices.cpu().numpy(), last, page, 1, 0.125, f64(q)[:n],
+                                            f64(kc), f64(vc), f64(lam), f64(w), 1e-5, 1.0, mag=True)
+    eps = torch.finfo(DT[dtype]).eps / 2
+    tol = oracle_diff.slack(ro, y, size, 1e-4 + eps, eps, f64(w)) + 1e-7
+    assert (np.abs(f64(o)[:n] - ro) <= tol).all() and np.abs(f64(lse)[:n] - rl).max() <= 1e-3
