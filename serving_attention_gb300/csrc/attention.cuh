@@ -177,11 +177,11 @@ __device__ __forceinline__ float tanh_approx(float x) {
   return y;
 }
 
-// Lowest visible key of a query at q_pos under the window (a bound below 0
-// when there is no window).  A query before its request's first key sees what
-// one at the first key would; the difference stays inside an int.
+// Lowest visible key of a query at q_pos under the window, 0 where that lies
+// before the first key (as it does for a query before it): differences from key
+// numbers stay inside an int.
 __device__ __forceinline__ int window_low(const Variant& v, int q_pos) {
-  return v.window_left >= 0 ? max(q_pos, 0) - v.window_left : -1;
+  return v.window_left >= 0 ? max(max(q_pos, 0) - v.window_left, 0) : 0;
 }
 
 struct Request {

@@ -157,6 +157,17 @@ def test_widest_windows_of_queries_before_the_keys(window, page):
     _check(b, lam, w, o, lse, window=window, rounded=True)
 
 
+@pytest.mark.parametrize("page", [4, 16])
+@pytest.mark.parametrize("causal", [0, 1])
+@pytest.mark.parametrize("window,sink", [(2**31 - 1, 0), (2**31 - 1, 4), (2**31 - 100, 300), (2**30, 2**31 - 1)])
+def test_widest_windows_over_several_tiles(window, sink, causal, page):
+    """The window's lowest key lies so far before a tile that their distance passes an int."""
+    b, lam, w = _batch(25, [40, 1, 130], [300, 255, 129], 8, 2, page, "fp16", causal)
+    o, lse, info, ws, _ = _run(b, lam, w, _config(window_left=window, sink_tokens=sink))
+    assert fi.device_status(ws) == 0
+    _check(b, lam, w, o, lse, window=window, sink=sink, rounded=True)
+
+
 @pytest.mark.parametrize("page", [4, 16, 128])
 @pytest.mark.parametrize("window,sink", [(100, 1), (255, 128), (300, 130), (640, 300)])
 def test_sinks_before_a_window(window, sink, page):
