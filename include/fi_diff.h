@@ -42,10 +42,9 @@ extern "C" {
  *   lse          fp32 [q_num_tokens, num_qo_heads, 2], contiguous, the natural
  *                log-sum-exp of the two maps; may be NULL.
  * A row with no visible key gets o = 0 and lse = -inf.  Slots past the end of
- * a request's last page may hold anything, NaN included; a request's own keys
- * and values that a row's mask hides beside visible ones are read with weight 0
- * and have to be finite (before a window: up to 127 keys, or a page, ahead of
- * it).  Page ids outside
+ * a request's last page may hold anything, NaN included; values of its own that
+ * a row's mask hides beside visible ones are read with weight 0 and have to be
+ * finite (before a window: up to 127 keys ahead of it).  Page ids outside
  * [0, num_pages) read as zeros.
  *
  * Requests of up to 16 packed rows (query tokens x group) read their keys once.
