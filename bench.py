@@ -54,11 +54,11 @@ def _peaks():
 
 
 def _kernel_hash() -> str:
-    """Hash of the sources the paged-attention kernel is built from (the MLA
-    files build other kernels and are left out)."""
+    """Hash of the sources the paged-attention kernel is built from (the files
+    of the MLA, differential, rotary and table kernels are left out)."""
     h = hashlib.sha256()
     for f in sorted(glob.glob(os.path.join(ROOT, "serving_attention_gb300", "csrc", "*"))):
-        if os.path.basename(f).startswith("mla") or not os.path.isfile(f):
+        if os.path.basename(f).startswith(("mla", "diff", "rotary", "tables")) or not os.path.isfile(f):
             continue
         with open(f, "rb") as fh:
             h.update(fh.read())

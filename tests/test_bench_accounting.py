@@ -57,3 +57,18 @@ def test_mix_decode_part_is_the_decode_requests():
     head = workloads.PagedBatch("h", b.dtype, b.qo_indptr[:4], b.kv_indptr[:4], b.kv_indices, b.last_page_len[:3],
                                 32, 8, 16, 1, b.sm_scale, b.q, b.k, b.v)
     assert bench.algorithmic(d)[0] + bench.algorithmic(head)[0] == bench.algorithmic(b)[0]
+
+
+def test_traffic_record_follows_its_own_kernel(tmp_path, monkeypatch):
+    """The record's hash covers the sources of the attention kernel, not those of the library's other kernels."""
+    src = tmp_path / "serving_attention_gb300" / "csrc"
+    src.mkdir(parents=True)
+    for f in ("attention.cu", "attention_kernel.cuh", "plan.cpp", "mla.cu", "diff_prefill.cuh", "rotary.cu", "tables.cu"):
+        (src / f).write_text(f)
+    monkeypatch.setattr(bench, "ROOT", str(tmp_path))
+    before = bench._kernel_hash()
+    for f in ("mla.cu", "diff_prefill.cuh", "rotary.cu", "tables.cu"):
+        (src / f).write_text("other")
+        assert bench._kernel_hash() == before
+    (src / "plan.cpp").write_text("other")
+    assert bench._kernel_hash() != before
