@@ -206,7 +206,7 @@ __device__ uint32_t diff_pf_produce(const DiffParams& dp, DiffPrefillBufs& pf, D
     const uint32_t t1 = t + pending + ntiles;
     int j = 0;
     for (int n = kV ? ntiles : 0; n < ntiles + steps; ++n) {
-      const int q = n - ntiles, tile = j;   // step of the passes behind pass 0
+      const int q = n - ntiles, tile = j;       // step of the passes behind pass 0
       const uint32_t tp = t1 + 2 * (q - tile);  // first place of its pass
       const uint32_t at = q < 0 ? t + (n > 0 ? pending + n : 0) : kV ? tp + 2 * tile + 2 - (split && tile + 1 == ntiles)
                                                                            : tp + (tile > 0 ? 2 * tile - 1 : 0);

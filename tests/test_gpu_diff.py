@@ -342,6 +342,43 @@ def test_graph_replays_other_plans_and_streams():
         _check(x, lam, w, o, lse)
 
 
+def test_plans_without_rows_write_nothing():
+    """No requests, and requests without queries, in buffers of a padded size."""
+    b, lam, w = _batch(26, [1, 2], [40, 50], 8, 2, 16, "bf16")
+    ws = fi.Workspace(_config(), device=DEV)
+    kvi = torch.zeros(9, dtype=torch.int32, device=DEV)
+    for qo, kvp, last in (([0], [0], []), ([0, 0, 0], [0, 3, 7], [4, 5])):
+        info = fi.plan(ws, np.array(qo), np.array(kvp), [], np.array(last, dtype=np.int32), 8, 2, 128, 16, 0)
+        o = torch.full_like(b.q, float("nan"))
+        differential.run(ws, info, b.q, b.k, b.v, kvi, lam, o, None, b.sm_scale)
+        assert fi.device_status(ws) == 0 and torch.isnan(o).all()
+
+
+def test_more_ctas_than_sms():
+    b, lam, w = _batch(27, [1, 300, 40, 1], [3000, 800, 900, 70], 16, 4, 16, "bf16", causal=1)
+    o, lse, info, ws, _ = _run(b, lam, w, _config(num_ctas=400, decode_min_chunk=64, prefill_min_chunk=128))
+    assert fi.device_status(ws) == 0
+    _check(b, lam, w, o, lse, rounded=True)
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, each with its workspace, give what they give alone."""
+    calls = [_batch(28, [1, 300, 40], [3000, 800, 900], 16, 4, 16, "bf16", causal=1),
+             _batch(29, [200, 1, 33], [500, 2000, 33], 8, 2, 4, "fp16", causal=1)]
+    alone = [_run(*c, _config()) for c in calls]
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(8):
+        for (b, lam, w), (o, _, info, ws, kvi), s in zip(calls, alone, streams):
+            with torch.cuda.stream(s):
+                x = torch.empty_like(o)
+                differential.run(ws, info, b.q, b.k, b.v, kvi, lam, x, None, b.sm_scale, norm_weight=w, stream=s)
+                got.append((x[:b.total_qo], o[:b.total_qo]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in got) and all(fi.device_status(a[3]) == 0 for a in alone)
+
+
 def test_repeats_give_the_same_bits():
     b, lam, w = _batch(13, [1, 100, 1, 1], [3000, 500, 70, 4000], 16, 4, 16, "bf16", causal=1)
     first = _run(b, lam, w, _config())
