@@ -211,6 +211,29 @@ typedef struct {
 
 fi_status fi_rotary_append(const fi_rotary_append_args* args, void* stream);
 
+/*
+ * fi_norm_rotary_append -- fi_rotary_append with an RMS norm of every query and
+ * key head before its rotation, in the same launch:
+ *   x / sqrt(mean(x^2) + eps) * weight
+ * over the head's head_dim dims, in fp32 up to the one rounding of the rotated
+ * value (v is copied).
+ *   q_weight, k_weight  fp32, device: head_dim weights for all heads
+ *     (stride 0), or head h's at h * stride (elements, at least head_dim,
+ *     a multiple of 4); 16-byte aligned.  NULL: that operand is not normed.
+ *   eps  finite, >= 0.
+ * Other arguments and checks as for fi_rotary_append.
+ */
+typedef struct {
+    fi_rotary_append_args append;
+    const float* q_weight;
+    int64_t q_weight_stride;
+    const float* k_weight;
+    int64_t k_weight_stride;
+    double eps;
+} fi_norm_rotary_append_args;
+
+fi_status fi_norm_rotary_append(const fi_norm_rotary_append_args* args, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,245 @@
+// norm_append.cu -- RMS norms of query and key heads, rotary positions and the
+// append of keys and values to the paged cache, in one launch.
+//
+// y = x r w with r = 1 / sqrt(mean(x^2) + eps) over a head, then the rotation of
+// rotary.cu.  A head has to be in registers whole before its first value can be
+// written, so the lanes that hold it are a power of two: lane l of such a group
+// takes place l (8 pairs, or 16 bytes), the sum of squares goes over the group
+// by shuffles, and the places past the head's last one add zeros.
+//
+// Bound by the bytes of q, k and v, each read and written once.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "rotary.h"
+
+namespace fi {
+namespace {
+
+constexpr int kNormWarps = 4;   // warps of a block
+constexpr int kNormAhead = 2;   // heads a lane has in flight
+constexpr int kValueAhead = 4;  // 16-byte pieces of v a lane has in flight
+
+struct NormParams {
+  RotaryRows q, k, v;
+  const float *q_weight, *k_weight;  // null: not normed
+  int64_t q_weight_stride, k_weight_stride;
+  const int32_t* positions;
+  const int32_t* slots;
+  int64_t num_slots;
+  int32_t num_tokens, parts;  // warps per token
+  int32_t log2_page, log2_group;
+  int32_t head_chunks, rot_chunks, v_chunks;  // 16-byte chunks of a head, of its rotated part, of a v row
+  float amplitude, eps, inv_dim;
+  uint64_t turns[FI_ROTARY_MAX_PAIRS];
+};
+
+__device__ __forceinline__ void load8(const float* w, float (&f)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(w)), b = __ldg(reinterpret_cast<const float4*>(w) + 1);
+  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+}
+
+template <typename T, bool kInterleaved>
+__global__ void __launch_bounds__(32 * kNormWarps, 4) norm_append_kernel(const __grid_constant__ NormParams a) {
+  __shared__ float2 s_cs[kNormWarps][FI_ROTARY_MAX_PAIRS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t w = int64_t(blockIdx.x) * kNormWarps + warp;
+  const int t = int(w / a.parts), part = int(w - int64_t(t) * a.parts);
+  if (t >= a.num_tokens) return;
+  const int32_t pos = __ldg(a.positions + t);
+  const int64_t slot = __ldg(a.slots + t);
+
+  // this lane's place and first head (q heads, then k heads)
+  const int pair_places = kInterleaved ? a.rot_chunks : a.rot_chunks >> 1;
+  const int places = pair_places + a.head_chunks - a.rot_chunks;
+  const int h_off = lane >> a.log2_group, place = lane & ((1 << a.log2_group) - 1), at_once = 32 >> a.log2_group;
+  const bool pairs = place < pair_places, active = place < places, two = !kInterleaved && pairs;
+  const int off = 8 * (pairs ? place : place + a.rot_chunks - pair_places);
+  const int other = 8 * pair_places;  // from the first members of 8 pairs to the second
+  const int step = at_once * a.parts;
+  const uint16_t *q_in = a.q.in + t * a.q.in_tok + off, *k_in = a.k.in + t * a.k.in_tok + off;
+  const int heads = a.q.heads + a.k.heads;
+  uint4 lo[kNormAhead], hi[kNormAhead];
+  auto load = [&](int h0) {
+#pragma unroll
+    for (int u = 0; u < kNormAhead; ++u) {
+      const int h = h0 + u * step;
+      lo[u] = hi[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (!active || h >= heads) continue;
+      const uint16_t* src = h < a.q.heads ? q_in + h * a.q.in_head : k_in + (h - a.q.heads) * a.k.in_head;
+      lo[u] = *reinterpret_cast<const uint4*>(src);
+      if (two) hi[u] = *reinterpret_cast<const uint4*>(src + other);
+    }
+  };
+  int h0 = part * at_once + h_off;
+  load(h0);
+  // v: 16-byte pieces, in order
+  const int v_tasks = a.v.heads * a.v_chunks, v_step = 32 * a.parts;
+  const uint16_t* v_in = a.v.in + t * a.v.in_tok;
+  uint4 vv[kValueAhead];
+  auto v_at = [&](int i, int64_t head, int64_t base) -> int64_t {
+    const int h = i / a.v_chunks;
+    return base + h * head + 8 * (i - h * a.v_chunks);
+  };
+  auto load_v = [&](int i0) {
+#pragma unroll
+    for (int u = 0; u < kValueAhead; ++u)
+      if (i0 + u * v_step < v_tasks) vv[u] = *reinterpret_cast<const uint4*>(v_in + v_at(i0 + u * v_step, a.v.in_head, 0));
+  };
+  int v0 = 32 * part + lane;
+  load_v(v0);
+
+  float2* cs = s_cs[warp];
+  for (int i = lane; i < a.rot_chunks * 4; i += 32) {
+    const uint64_t turn = uint64_t(int64_t(pos)) * a.turns[i];  // modulo one turn
+    float sn, c;
+    sincospif(float(int32_t(turn >> 32)) * 4.6566128730773926e-10f, &sn, &c);  // 2^-31: half turns in [-1, 1]
+    cs[i] = make_float2(c * a.amplitude, sn * a.amplitude);
+  }
+  __syncwarp();
+  constexpr int kMine = kInterleaved ? 4 : 8;
+  float2 r[kMine];
+  if (pairs) {
+    const float4* mine = reinterpret_cast<const float4*>(cs + kMine * place);
+#pragma unroll
+    for (int e = 0; e < kMine / 2; ++e) {
+      const float4 x = mine[e];
+      r[2 * e] = make_float2(x.x, x.y);
+      r[2 * e + 1] = make_float2(x.z, x.w);
+    }
+  }
+  const bool store_kv = slot >= 0 && slot < a.num_slots;
+  const int64_t page = slot >> a.log2_page, in_page = slot & ((int64_t(1) << a.log2_page) - 1);
+  uint16_t* q_out = a.q.out + t * a.q.out_tok + off;
+  uint16_t* k_out = a.k.out + page * a.k.out_tok + in_page * a.k.out_slot + off;
+  // the shuffles need every lane, so the loop runs while any head of the warp is left
+  for (; h0 - h_off < heads; h0 += kNormAhead * step) {
+#pragma unroll
+    for (int u = 0; u < kNormAhead; ++u) {
+      const int h = h0 + u * step;
+      if (h - h_off >= heads) break;  // of the whole warp
+      const bool is_q = h < a.q.heads;
+      float x[8], y[8];
+      unpack<T>(lo[u], x);
+      unpack<T>(hi[u], y);
+      const float* weight = is_q ? a.q_weight : a.k_weight;
+      float sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum = fmaf(x[e], x[e], fmaf(y[e], y[e], sum));
+      for (int m = 1 << a.log2_group >> 1; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+      if (!active || h >= heads || (!is_q && !store_kv)) continue;
+      uint16_t* dst = is_q ? q_out + h * a.q.out_head : k_out + (h - a.q.heads) * a.k.out_head;
+      if (weight) {
+        const float root = rsqrtf(fmaf(sum, a.inv_dim, a.eps));
+        weight += is_q ? h * a.q_weight_stride : (h - a.q.heads) * a.k_weight_stride;
+        float g[8];
+        load8(weight + off, g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] *= root * g[e];
+        if (two) {
+          load8(weight + off + other, g);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] *= root * g[e];
+        }
+      }
+      if (pairs) {
+        if (kInterleaved) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float x0 = x[2 * e], x1 = x[2 * e + 1];
+            x[2 * e] = x0 * r[e].x - x1 * r[e].y;
+            x[2 * e + 1] = x1 * r[e].x + x0 * r[e].y;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float x0 = x[e], x1 = y[e];
+            x[e] = x0 * r[e % kMine].x - x1 * r[e % kMine].y;
+            y[e] = x1 * r[e % kMine].x + x0 * r[e % kMine].y;
+          }
+          *reinterpret_cast<uint4*>(dst + other) = pack<T>(y);
+        }
+      }
+      *reinterpret_cast<uint4*>(dst) = pack<T>(x);
+    }
+    load(h0 + kNormAhead * step);
+  }
+  if (!store_kv) return;
+  const int64_t v_base = page * a.v.out_tok + in_page * a.v.out_slot;
+  for (; v0 < v_tasks; v0 += kValueAhead * v_step) {
+#pragma unroll
+    for (int u = 0; u < kValueAhead; ++u)
+      if (v0 + u * v_step < v_tasks)
+        *reinterpret_cast<uint4*>(a.v.out + v_at(v0 + u * v_step, a.v.out_head, v_base)) = vv[u];
+    load_v(v0 + kValueAhead * v_step);
+  }
+}
+
+// Warps wanted on the card before a token is left to one warp (see rotary.cu).
+constexpr int kPartWarps = 4096;
+
+}  // namespace
+}  // namespace fi
+
+using namespace fi;
+
+extern "C" fi_status fi_norm_rotary_append(const fi_norm_rotary_append_args* n, void* stream) {
+  if (!n) return FI_ERR_INVALID_ARG;
+  const fi_rotary_append_args* x = &n->append;
+  fi_status st = check_append(x);
+  if (st != FI_OK) return st;
+  if (!eps_ok(n->eps)) return FI_ERR_INVALID_ARG;
+  if (x->num_tokens == 0) return FI_OK;
+  const fi_rotary* rot = x->rotary;
+  st = check_weights(n->q_weight, n->q_weight_stride, rot->head_dim);
+  if (st == FI_OK) st = check_weights(n->k_weight, n->k_weight_stride, rot->head_dim);
+  if (st != FI_OK) return st;
+  NormParams a;
+  std::memset(&a, 0, sizeof a);
+  if (x->num_q_heads > 0) a.q = rows_of(x->q_in, x->q_out, x->num_q_heads);
+  a.k = rows_to_cache(x->k_in, x->k_cache, x->k_strides, x->num_kv_heads);
+  if (x->v_dim > 0) a.v = rows_to_cache(x->v_in, x->v_cache, x->v_strides, x->num_kv_heads);
+  a.v_chunks = int32_t(x->v_dim / 8);
+  a.q_weight = n->q_weight;
+  a.k_weight = n->k_weight;
+  a.q_weight_stride = n->q_weight_stride;
+  a.k_weight_stride = n->k_weight_stride;
+  a.positions = x->positions;
+  a.slots = x->slots;
+  a.num_slots = x->num_pages * x->page_size;
+  while ((1 << a.log2_page) < x->page_size) ++a.log2_page;
+  a.num_tokens = int32_t(x->num_tokens);
+  a.head_chunks = rot->head_dim / 8;
+  a.rot_chunks = rot->rot_dim / 8;
+  a.amplitude = rot->amplitude;
+  a.eps = float(n->eps);
+  a.inv_dim = 1.f / float(rot->head_dim);
+  std::memcpy(a.turns, rot->turns, sizeof(uint64_t) * size_t(rot->rot_dim / 2));
+  const int places = (rot->interleaved ? a.rot_chunks : a.rot_chunks / 2) + a.head_chunks - a.rot_chunks;
+  while ((1 << a.log2_group) < places) ++a.log2_group;
+  // Few tokens: a token's heads are spread over more warps, at least one head a lane
+  const int at_once = 32 >> a.log2_group, heads = a.q.heads + a.k.heads;
+  const int rot_parts = (heads + at_once - 1) / at_once, v_parts = (a.v.heads * a.v_chunks + 31) / 32;
+  const int most = rot_parts > v_parts ? rot_parts : v_parts;
+  const int want = kPartWarps / a.num_tokens;
+  a.parts = want < 1 ? 1 : want > most ? most : want;
+  const int64_t warps = int64_t(a.num_tokens) * a.parts;
+  const unsigned blocks = unsigned((warps + kNormWarps - 1) / kNormWarps);
+  const int threads = 32 * kNormWarps;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (x->dtype == FI_BF16) {
+    if (rot->interleaved)
+      norm_append_kernel<__nv_bfloat16, true><<<blocks, threads, 0, s>>>(a);
+    else
+      norm_append_kernel<__nv_bfloat16, false><<<blocks, threads, 0, s>>>(a);
+  } else {
+    if (rot->interleaved)
+      norm_append_kernel<__half, true><<<blocks, threads, 0, s>>>(a);
+    else
+      norm_append_kernel<__half, false><<<blocks, threads, 0, s>>>(a);
+  }
+  return cudaGetLastError() == cudaSuccess ? FI_OK : FI_ERR_CUDA;
+}

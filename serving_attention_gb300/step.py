@@ -6,6 +6,7 @@ append to the paged cache.  Argument marshalling only; there is no fallback.
     build_tables(tables, qo_lens, kv_lens, block_table, 16, free_pages, free_head)
     rot = rotary_setup(128, theta=500000.0)
     append(rot, tables.positions, tables.slots, q, q_rot, k, v, k_cache, v_cache)
+    norm_append(rot, tables.positions, tables.slots, q, q_rot, q_weight, k, k_weight, v, k_cache, v_cache)
 """
 from __future__ import annotations
 
@@ -17,7 +18,7 @@ import torch
 from . import _DTYPE, _check, load as _load_lib
 from .differential import _call
 
-EXPORTS = ["fi_build_step_tables", "fi_rotary_setup", "fi_rotary_apply", "fi_rotary_append"]
+EXPORTS = ["fi_build_step_tables", "fi_rotary_setup", "fi_rotary_apply", "fi_rotary_append", "fi_norm_rotary_append"]
 SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3, "yarn": 4}
 MAX_BATCH, COUNTS, MAX_PAIRS = 8192, 8, 128
 
@@ -35,14 +36,15 @@ class Rotary(ctypes.Structure):
                 ("turns", ctypes.c_uint64 * MAX_PAIRS)]
 
 
-_apply = _append = _tables = None
+_apply = _append = _norm_append = _tables = None
 _APPLY_ARGS = struct.Struct("=18q")   # fi_rotary_apply_args
 _APPEND_ARGS = struct.Struct("=30q")  # fi_rotary_append_args
+_NORM_ARGS = struct.Struct("=34qd")   # fi_norm_rotary_append_args
 _TABLE_ARGS = struct.Struct("=19q")   # fi_step_tables_args
 
 
 def load() -> ctypes.CDLL:
-    global _apply, _append, _tables
+    global _apply, _append, _norm_append, _tables
     lib = _load_lib()
     if _tables is None:
         lib.fi_rotary_setup.argtypes = [ctypes.POINTER(RotaryConfig), ctypes.POINTER(Rotary)]
@@ -52,6 +54,7 @@ def load() -> ctypes.CDLL:
             if name != "fi_rotary_setup":
                 fn.argtypes = [ctypes.c_char_p, ctypes.c_void_p]
         _apply, _append, _tables = lib.fi_rotary_apply, lib.fi_rotary_append, lib.fi_build_step_tables
+        _norm_append = lib.fi_norm_rotary_append
     return lib
 
 
@@ -116,14 +119,8 @@ def rotate(rot: Rotary, positions: torch.Tensor, q: torch.Tensor | None, q_out: 
           index, stream, "fi_rotary_apply")
 
 
-def append(rot: Rotary, positions: torch.Tensor, slots: torch.Tensor, q: torch.Tensor | None,
-           q_out: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor | None, k_cache: torch.Tensor,
-           v_cache: torch.Tensor | None, stream=None):
-    """Rotate q into q_out and k into k_cache, and copy v into v_cache, token t
-    at slot slots[t] = page * page_size + slot (outside the cache: not written).
-    Caches [pages, page_size, heads, dim]."""
-    if _append is None:
-        load()
+def _append_args(rot, positions, slots, q, q_out, k, v, k_cache, v_cache):
+    """Checks an append's tensors: (the fields of fi_rotary_append_args, device)."""
     dtype, index = k.dtype, k.get_device()
     code = _DTYPE.get(dtype)
     if code is None:
@@ -158,10 +155,45 @@ def append(rot: Rotary, positions: torch.Tensor, slots: torch.Tensor, q: torch.T
             raise ValueError("v is [tokens, heads of k, v_dim] and v_cache [pages, page_size, heads, v_dim], the last "
                              "dimension contiguous")
         v_ptr, vc_ptr = v.data_ptr(), v_cache.data_ptr()
-    _call(_append, _APPEND_ARGS.pack(ctypes.addressof(rot), positions.data_ptr(), slots.data_ptr(), tokens, *q_rows, hq,
-                                     k.data_ptr(), kt, kh, v_ptr, vt, vh, v_dim, hk, k_cache.data_ptr(), kcp, kcs, kch,
-                                     vc_ptr, vcp, vcs, vch, page_size, pages, code),
-          index, stream, "fi_rotary_append")
+    return (ctypes.addressof(rot), positions.data_ptr(), slots.data_ptr(), tokens, *q_rows, hq, k.data_ptr(), kt, kh, v_ptr,
+            vt, vh, v_dim, hk, k_cache.data_ptr(), kcp, kcs, kch, vc_ptr, vcp, vcs, vch, page_size, pages, code), index
+
+
+def append(rot: Rotary, positions: torch.Tensor, slots: torch.Tensor, q: torch.Tensor | None,
+           q_out: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor | None, k_cache: torch.Tensor,
+           v_cache: torch.Tensor | None, stream=None):
+    """Rotate q into q_out and k into k_cache, and copy v into v_cache, token t
+    at slot slots[t] = page * page_size + slot (outside the cache: not written).
+    Caches [pages, page_size, heads, dim]."""
+    if _append is None:
+        load()
+    args, index = _append_args(rot, positions, slots, q, q_out, k, v, k_cache, v_cache)
+    _call(_append, _APPEND_ARGS.pack(*args), index, stream, "fi_rotary_append")
+
+
+def _weight(w: torch.Tensor | None, heads: int, dim: int, index: int, what: str):
+    """(pointer, stride per head) of norm weights [dim] or [heads, dim]."""
+    if w is None:
+        return 0, 0
+    if w.dtype is not torch.float32 or w.get_device() != index or w.stride(-1) != 1:
+        raise TypeError(f"{what} must be fp32 on the tensors' device, the last dimension contiguous")
+    if w.shape != (dim,) and w.shape != (heads, dim):
+        raise ValueError(f"{what} is [{dim}] or [heads, {dim}]")
+    return w.data_ptr(), 0 if w.dim() == 1 or heads == 1 else w.stride(0)
+
+
+def norm_append(rot: Rotary, positions: torch.Tensor, slots: torch.Tensor, q: torch.Tensor | None,
+                q_out: torch.Tensor | None, q_weight: torch.Tensor | None, k: torch.Tensor,
+                k_weight: torch.Tensor | None, v: torch.Tensor | None, k_cache: torch.Tensor,
+                v_cache: torch.Tensor | None, eps: float = 1e-6, stream=None):
+    """As append, with an RMS norm of each head of q and k before its rotation:
+    x / sqrt(mean(x^2) + eps) * weight, weights fp32 [head_dim] or [heads, head_dim] (None: not normed)."""
+    if _norm_append is None:
+        load()
+    args, index = _append_args(rot, positions, slots, q, q_out, k, v, k_cache, v_cache)
+    qw = _weight(q_weight, 0 if q is None else q.shape[1], rot.head_dim, index, "q_weight")
+    kw = _weight(k_weight, k.shape[1], rot.head_dim, index, "k_weight")
+    _call(_norm_append, _NORM_ARGS.pack(*args, *qw, *kw, eps), index, stream, "fi_norm_rotary_append")
 
 
 # ------------------------------------------------------------------ tables
