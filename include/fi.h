@@ -106,6 +106,14 @@ typedef struct {
      * FI_ERR_UNSUPPORTED, as is a request of more than INT32_MAX - 256 keys;
      * other values FI_ERR_INVALID_ARG. */
     int32_t differential;
+    /* 4: plans for fi_batch_paged_attention_run_kv4 (fi_kv4.h), attention over
+     * the cache held in 4 bits; the other runs refuse them (0 or 16, the
+     * default: a 16-bit cache).  A sliding window and sink tokens apply; a
+     * soft-cap, RoPE, differential attention or a cascade plan with it are
+     * FI_ERR_UNSUPPORTED, as is a request of more than INT32_MAX - 256 keys;
+     * other values FI_ERR_INVALID_ARG.  A decode-class key moves a quarter of the
+     * bytes, so its cost weight is a quarter of decode_cost_weight, rounded up. */
+    int32_t kv_bits;
 } fi_plan_config;
 
 /* Plain data returned by fi_plan; passed to run by value semantics. */
@@ -120,7 +128,7 @@ typedef struct {
     int32_t chunk_prefill;       /* KV tokens per chunk chosen for 256-row (differential: 128-row) tiles */
     int32_t num_decode_items, num_prefill_items;
     int32_t variant;             /* bit 0: logits soft-cap; bit 1: sliding window (and sink) mask; bit 2: RoPE;
-                                    bit 3: differential */
+                                    bit 3: differential; bit 4: 4-bit cache */
     int64_t int_ws_bytes_used;   /* bytes of the int workspace written (and copied) by the plan */
     int64_t max_partial_rows;    /* capacity of the float workspace, from the config */
     int32_t num_late_merge_units; /* split units of prefill-class tiles: merged by a second launch */

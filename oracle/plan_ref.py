@@ -61,6 +61,8 @@ Rule:
     partial rows, and every merge unit carries the late flag; on pages below 8
     tokens a CTA's prefill-class items of requests of up to 32 rows come behind
     its others.
+    Plans over the 4-bit cache (kv_bits 4, a magic of their own): no multi-head
+    units, and a decode-class key costs ceil(decode_cost_weight / 4).
  6. Output: header (with the variant: window, sink, soft-cap bits, and for
     RoPE its position capacity, theta and scale bits and the table offset;
     then the count of late units, the partial rows used, the batch's query
@@ -78,7 +80,7 @@ import heapq
 
 import numpy as np
 
-MAGIC, MAGIC_DIFF = 0x46495031, 0x46495044
+MAGIC, MAGIC_DIFF, MAGIC_KV4 = 0x46495031, 0x46495044, 0x46495034
 TILE_DECODE, TILE_PREFILL, TILE_PREFILL_DIFF = 16, 256, 128
 HEADER_INTS = 32
 ROPE_PAIRS = 64
@@ -131,6 +133,10 @@ def _config_status(cfg, head_dim, num_qo_heads, num_kv_heads, page_size, causal)
     if diff not in (0, 1):
         return INVALID_ARG
     if diff and (cap > 0.0 or rope_max > 0):
+        return UNSUPPORTED
+    if cfg.get("kv_bits", 0) not in (0, 4, 16):
+        return INVALID_ARG
+    if cfg.get("kv_bits", 0) == 4 and (cap > 0.0 or rope_max > 0 or diff):
         return UNSUPPORTED
     theta = float(np.float32(cfg.get("rope_theta", 10000.0)))
     rscale = float(np.float32(cfg.get("rope_scale", 1.0)))
@@ -210,7 +216,8 @@ def make_cascade_plan(cfg: dict, shared_qo_indptr, shared_kv_indptr, shared_kv_i
         return st, None, None
     if not _pow2_page(shared_page_size):
         return UNSUPPORTED, None, None
-    if cfg.get("window_left", -1) >= 0 or cfg.get("rope_max_positions", 0) > 0 or cfg.get("differential", 0):
+    if cfg.get("window_left", -1) >= 0 or cfg.get("rope_max_positions", 0) > 0 or cfg.get("differential", 0) \
+            or cfg.get("kv_bits", 0) == 4:
         return UNSUPPORTED, None, None
     batch = len(qo_indptr) - 1
     if batch + num_shared > cfg["max_batch"]:
@@ -253,7 +260,8 @@ def _plan(cfg, reqs, num_shared, shared_page_size, block_of, total_qo, num_qo_he
     rscale = float(np.float32(cfg.get("rope_scale", 1.0)))
     batch = len(reqs)
     diff = bool(cfg.get("differential", 0))
-    if diff and any(r[3] > 2**31 - 1 - 256 for r in reqs):  # its kernels count keys in 32 bits
+    kv4 = cfg.get("kv_bits", 0) == 4
+    if (diff or kv4) and any(r[3] > 2**31 - 1 - 256 for r in reqs):  # their kernels count keys in 32 bits
         return UNSUPPORTED, None, None
     # rows of a tile: with two maps per row a prefill tile has 128 rows
     height = {TILE_DECODE: TILE_DECODE, TILE_PREFILL: TILE_PREFILL_DIFF if diff else TILE_PREFILL}
@@ -298,7 +306,7 @@ def _plan(cfg, reqs, num_shared, shared_page_size, block_of, total_qo, num_qo_he
         T = tile_of(b)
         cache_page = shared_page_size if b < num_shared else page_size
         heads = mh if (T == TILE_DECODE and lq[b] == 1 and cache_page == 1 and rope_max == 0
-                       and b >= num_shared and not diff) else 1
+                       and b >= num_shared and not diff and not kv4) else 1
         for hk in range(0, num_kv_heads, heads):
             for qt in range(_ceil_div(R, height[T])):
                 r0, r1 = (0, R * heads) if heads > 1 else (qt * height[T], min(R, (qt + 1) * height[T]))
@@ -325,7 +333,9 @@ def _plan(cfg, reqs, num_shared, shared_page_size, block_of, total_qo, num_qo_he
     n_pre = sum(max(1, sum(_ceil_div(e - s, chunk[TILE_PREFILL]) for s, e in u[6][1 if lead_of(u[3], u[6]) else 0:]))
                 for u in units if u[3] == TILE_PREFILL)
     chunk[TILE_DECODE] = pick(TILE_DECODE, cfg["decode_min_chunk"], C - n_pre if 0 < 2 * n_pre <= C else C)
-    weight = {TILE_DECODE: cfg["decode_cost_weight"], TILE_PREFILL: cfg["prefill_cost_weight"]}
+    # a key of the 4-bit cache moves a quarter of the bytes
+    weight = {TILE_DECODE: _ceil_div(cfg["decode_cost_weight"], 4) if kv4 else cfg["decode_cost_weight"],
+              TILE_PREFILL: cfg["prefill_cost_weight"]}
     # a multi-head unit's chunk holds the K/V bytes of a one-head chunk, rounded up to the granule
     g = granule[TILE_DECODE]
     chunk_mh = max(g, _ceil_div(_ceil_div(chunk[TILE_DECODE], mh), g) * g)
@@ -414,7 +424,7 @@ def _plan(cfg, reqs, num_shared, shared_page_size, block_of, total_qo, num_qo_he
 
     rope_off = (int_workspace_ints(cfg) * 4 + 255) // 256 * 256 // 4 if rope_max > 0 else 0
     n_dec = sum(1 for _, f in items if lq[f[0]] * group <= 16)
-    ws[:HEADER_INTS] = [MAGIC_DIFF if diff else MAGIC, n_items, n_merge, C, batch, causal, off_cta, off_items,
+    ws[:HEADER_INTS] = [MAGIC_DIFF if diff else MAGIC_KV4 if kv4 else MAGIC, n_items, n_merge, C, batch, causal, off_cta, off_items,
                         off_merge, off_cnt, off_req, 0, num_qo_heads, num_kv_heads, page_size, total_ints,
                         window, sink, bits(cap), rope_max,
                         bits(theta) if rope_max > 0 else 0, bits(rscale) if rope_max > 0 else 0, rope_off,
@@ -447,7 +457,7 @@ def _plan(cfg, reqs, num_shared, shared_page_size, block_of, total_qo, num_qo_he
                 chunk_prefill=chunk[TILE_PREFILL], num_decode_items=n_dec, num_prefill_items=n_items - n_dec,
                 int_ws_bytes_used=4 * total_ints, max_partial_rows=cfg["max_partial_rows"],
                 variant=(1 if cap > 0 else 0) | (2 if window >= 0 else 0) | (4 if rope_max > 0 else 0)
-                | (8 if diff else 0),
+                | (8 if diff else 0) | (16 if kv4 else 0),
                 num_shared=num_shared, num_cascade_merges=len(entries), prefill_caches=prefill_caches)
     return OK, ws, info
 

@@ -39,7 +39,8 @@ class PlanConfig(ctypes.Structure):
                 ("decode_cost_weight", ctypes.c_int32), ("prefill_cost_weight", ctypes.c_int32),
                 ("split_factor", ctypes.c_int32), ("window_left", ctypes.c_int32), ("sink_tokens", ctypes.c_int32),
                 ("logits_soft_cap", ctypes.c_float), ("rope_max_positions", ctypes.c_int32),
-                ("rope_theta", ctypes.c_float), ("rope_scale", ctypes.c_float), ("differential", ctypes.c_int32)]
+                ("rope_theta", ctypes.c_float), ("rope_scale", ctypes.c_float), ("differential", ctypes.c_int32),
+                ("kv_bits", ctypes.c_int32)]
 
     def as_dict(self) -> dict:
         return {f: getattr(self, f) for f, _ in self._fields_}

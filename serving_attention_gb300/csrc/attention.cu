@@ -164,6 +164,8 @@ cudaError_t launch_late_merge(const RunParams& p, int32_t blocks, cudaStream_t s
                            static_cast<const float*>(p.fws), p.partial_o_offset, reinterpret_cast<T*>(p.o),
                            p.o_stride_tok, p.o_stride_head, p.lse, int(p.num_qo_heads), int(p.group));
 }
+template cudaError_t launch_late_merge<__nv_bfloat16>(const RunParams&, int32_t, cudaStream_t);
+template cudaError_t launch_late_merge<__half>(const RunParams&, int32_t, cudaStream_t);
 
 // RoPE table: (cos, sin) of (pos / scale) * theta^(-2i/128) for pos <
 // max_pos, i < 64, computed in fp64 and rounded once to fp32.
@@ -533,6 +535,7 @@ extern "C" fi_status fi_default_plan_config(int device, fi_plan_config* out) {
   out->rope_theta = 10000.f;
   out->rope_scale = 1.f;
   out->differential = 0;
+  out->kv_bits = 0;
   return FI_OK;
 }
 
@@ -746,7 +749,7 @@ fi_status run_impl(const fi_plan_info* info, const void* q, int64_t q_stride_tok
   if (info->num_ctas < 1 || q_num_tokens < 1 || !std::isfinite(sm_scale)) return FI_ERR_INVALID_ARG;
   if (info->num_partial_rows > 0 && !float_workspace_dev) return FI_ERR_INVALID_ARG;
   if (info->num_shared > 0 && !shared) return FI_ERR_INVALID_ARG;  // a cascade plan needs the shared cache
-  if (info->variant & 8) return FI_ERR_INVALID_ARG;  // a differential plan has a run of its own
+  if (info->variant & 24) return FI_ERR_INVALID_ARG;  // differential plans and those over the 4-bit cache: own runs
   if (info->head_dim != kHeadDim) return FI_ERR_UNSUPPORTED;
   if (dtype != FI_FP16 && dtype != FI_BF16) return FI_ERR_UNSUPPORTED;
   if (info->num_kv_heads < 1 || info->num_qo_heads % info->num_kv_heads) return FI_ERR_UNSUPPORTED;

@@ -17,6 +17,10 @@ constexpr int kMaxDevices = 64;  // devices with per-device launch state
 template <typename T, bool kCap, bool kMask, bool kRope>
 cudaError_t launch_run(const RunParams& p, int num_ctas, cudaStream_t stream);
 
+// The row-parallel merge of a plan's late units, behind the run (attention.cu).
+template <typename T>
+cudaError_t launch_late_merge(const RunParams& p, int32_t blocks, cudaStream_t s);
+
 // Resident CTAs per SM of the plain bf16 kernel (the occupancy the plan's
 // default grid is sized by); sets the kernel's shared-memory opt-in.
 cudaError_t run_kernel_occupancy(int* per_sm);

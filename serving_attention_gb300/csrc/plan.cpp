@@ -175,6 +175,8 @@ fi_status check_config(const fi_plan_config* cfg, int32_t head_dim, int32_t num_
   if (cfg->window_left < -1 || cfg->sink_tokens < 0 || !(cap >= 0.f) || cap == HUGE_VALF) return FI_ERR_INVALID_ARG;
   if (cfg->differential != 0 && cfg->differential != 1) return FI_ERR_INVALID_ARG;
   if (cfg->differential && (cap > 0.f || cfg->rope_max_positions > 0)) return FI_ERR_UNSUPPORTED;
+  if (cfg->kv_bits != 0 && cfg->kv_bits != 4 && cfg->kv_bits != 16) return FI_ERR_INVALID_ARG;
+  if (cfg->kv_bits == 4 && (cap > 0.f || cfg->rope_max_positions > 0 || cfg->differential)) return FI_ERR_UNSUPPORTED;
   const int32_t rope_max = cfg->rope_max_positions;
   if (rope_max < 0 || (rope_max > 0 && !(cfg->rope_theta > 0.f && cfg->rope_theta < HUGE_VALF &&
                                          cfg->rope_scale > 0.f && cfg->rope_scale < HUGE_VALF)))
@@ -203,9 +205,10 @@ fi_status plan_requests(const fi_plan_config* cfg, const std::vector<Req>& reqs,
   const bool diff = cfg->differential != 0;
   const int32_t maps = diff ? 2 : 1;
   const int32_t prefill_rows = diff ? FI_TILE_PREFILL_DIFF : FI_TILE_PREFILL;
-  // Its kernels count keys in 32 bits, up to two tiles past a request's end.
+  const bool kv4 = cfg->kv_bits == 4;
+  // Their kernels count keys in 32 bits, up to two tiles past a request's end.
   for (const Req& rq : reqs)
-    if (diff && rq.kv_len > INT32_MAX - 2 * FI_GRANULE_PREFILL) return FI_ERR_UNSUPPORTED;
+    if ((diff || kv4) && rq.kv_len > INT32_MAX - 2 * FI_GRANULE_PREFILL) return FI_ERR_UNSUPPORTED;
   // Chunk boundaries fall on pages of every cache the plan reads.
   const int32_t max_page = std::max(page_size, cascade ? shared_page_size : page_size);
 
@@ -229,7 +232,7 @@ fi_status plan_requests(const fi_plan_config* cfg, const std::vector<Req>& reqs,
     // one token of all the unit's heads.
     const int32_t cache_page = b < num_shared ? shared_page_size : page_size;
     const int32_t heads = (tile == FI_TILE_DECODE && rq.qo_len == 1 && cache_page == 1 && rope_max == 0 &&
-                           b >= num_shared && !diff)
+                           b >= num_shared && !diff && !kv4)
                               ? fi_mh_heads(group, num_kv_heads)
                               : 1;
     for (int32_t hk = 0; hk < num_kv_heads; hk += heads) {
@@ -345,7 +348,9 @@ fi_status plan_requests(const fi_plan_config* cfg, const std::vector<Req>& reqs,
     int32_t merge_id = -1;
     int64_t base = -1;
     const int32_t nrows = u.row1 - u.row0;
-    const int64_t weight = u.tile == FI_TILE_DECODE ? cfg->decode_cost_weight : cfg->prefill_cost_weight;
+    const int64_t weight = u.tile != FI_TILE_DECODE ? cfg->prefill_cost_weight
+                           : kv4                    ? ceil_div(cfg->decode_cost_weight, 4)
+                                                    : cfg->decode_cost_weight;
     if (n > 1 || cascade) {
       base = partial_rows;
       partial_rows += n * nrows * maps;
@@ -507,7 +512,7 @@ fi_status plan_requests(const fi_plan_config* cfg, const std::vector<Req>& reqs,
   }
   const int32_t rope_off = rope_max > 0 ? int32_t(fi_rope_table_offset(fi::plan_capacity_ints(cfg)) / 4) : 0;
   const int32_t header[FI_HEADER_INTS] = {
-      diff ? FI_PLAN_MAGIC_DIFF : FI_PLAN_MAGIC, int32_t(n_items),   int32_t(n_merge),   C,
+      diff ? FI_PLAN_MAGIC_DIFF : kv4 ? FI_PLAN_MAGIC_KV4 : FI_PLAN_MAGIC, int32_t(n_items),   int32_t(n_merge),   C,
       batch,                causal,             int32_t(off_cta),   int32_t(off_items),
       int32_t(off_merge),   int32_t(off_cnt),   int32_t(off_req),   0,
       num_qo_heads,         num_kv_heads,       page_size,          int32_t(total_ints),
@@ -537,7 +542,8 @@ fi_status plan_requests(const fi_plan_config* cfg, const std::vector<Req>& reqs,
   info.num_prefill_items = int32_t(n_items - n_decode);
   info.int_ws_bytes_used = total_ints * 4;
   info.max_partial_rows = cfg->max_partial_rows;
-  info.variant = (cap > 0.f ? 1 : 0) | (window >= 0 ? 2 : 0) | (rope_max > 0 ? 4 : 0) | (diff ? 8 : 0);
+  info.variant = (cap > 0.f ? 1 : 0) | (window >= 0 ? 2 : 0) | (rope_max > 0 ? 4 : 0) | (diff ? 8 : 0) |
+                 (kv4 ? 16 : 0);
   info.num_shared = num_shared;
   info.num_cascade_merges = int32_t(n_cascade);
   info.prefill_caches = prefill_caches;
@@ -580,7 +586,8 @@ extern "C" fi_status fi_plan_cascade_host(
     return FI_ERR_UNSUPPORTED;
   // Positions of the two levels are not tied to one sequence here: the
   // position-dependent variants (sliding window, sink, RoPE) are not offered.
-  if (cfg->window_left >= 0 || cfg->rope_max_positions > 0 || cfg->differential) return FI_ERR_UNSUPPORTED;
+  if (cfg->window_left >= 0 || cfg->rope_max_positions > 0 || cfg->differential || cfg->kv_bits == 4)
+    return FI_ERR_UNSUPPORTED;
   if (int64_t(batch) + num_shared > cfg->max_batch) return FI_ERR_CAPACITY;
   if (workspace_bytes < size_t(fi::plan_capacity_ints(cfg)) * 4) return FI_ERR_CAPACITY;
   std::vector<Req> reqs;

@@ -62,6 +62,7 @@
 
 #define FI_PLAN_MAGIC 0x46495031
 #define FI_PLAN_MAGIC_DIFF 0x46495044  // a differential plan: read by its own run only
+#define FI_PLAN_MAGIC_KV4 0x46495034   // a plan over the 4-bit cache: read by its own run only
 #define FI_HEADER_INTS 32
 #define FI_ITEM_INTS 16
 #define FI_ITEM_LEAD 13
