@@ -130,7 +130,7 @@ fi_status fi_kv4_read(const fi_kv4_read_args* args, void* stream);
  * A row with no visible key gets o = 0 and lse = -inf.  Slots past the end of a
  * request's last page, and keys that a row's mask hides, may hold any bytes;
  * the words of visible keys hold a finite s.  Page ids outside [0, num_pages)
- * read as keys that no row sees.  Rows of q and o behind the plan's last
+ * read as zeros.  Rows of q and o behind the plan's last
  * token are left alone.
  *
  * One launch on `stream`, and behind it the merge of split prefill-class units

@@ -102,7 +102,7 @@ def norm_exact_order(x, w, eps):
 def attention(qo_indptr, kv_indptr, kv_indices, last_page_len, page_size, causal, scale, q, k, v, window=-1, sink=0,
               num_pages=None):
     """o [tokens, Hq, 128], lse [tokens, Hq] and sum_j p_j |v_j|, fp64; k, v [pages, P, Hkv, 128] as all_values gives
-    them.  Page ids outside [0, num_pages) hold no key."""
+    them.  Page ids outside [0, num_pages) read as zeros."""
     T, Hq, _ = q.shape
     Hkv = k.shape[2]
     G = Hq // Hkv
@@ -113,15 +113,15 @@ def attention(qo_indptr, kv_indptr, kv_indices, last_page_len, page_size, causal
         ids = np.asarray(kv_indices[kv_indptr[b]:kv_indptr[b + 1]], np.int64)
         n = (len(ids) - 1) * page_size + int(last_page_len[b]) if len(ids) else 0
         good = (ids >= 0) & (ids < num_pages)
-        there = np.repeat(good, page_size)[:n]
+        there = np.repeat(good, page_size)[:n, None, None]
         safe = np.where(good, ids, 0)
-        kb, vb = k[safe].reshape(-1, Hkv, D)[:n], v[safe].reshape(-1, Hkv, D)[:n]
+        kb, vb = (np.where(there, x[safe].reshape(-1, Hkv, D)[:n], 0) for x in (k, v))
         lq = int(qo_indptr[b + 1] - qo_indptr[b])
         if lq == 0 or n == 0:
             continue
         pos = np.arange(lq)[:, None] + (n - lq)
         key = np.arange(n)[None]
-        see = (key <= pos if causal else key < n + 0 * pos) & there[None]
+        see = key <= pos if causal else key < n + 0 * pos
         if window >= 0:
             see = see & ((key >= pos - window) | (key < sink))
         rows = slice(int(qo_indptr[b]), int(qo_indptr[b + 1]))

@@ -1,4 +1,5 @@
-// kv4_kernel.cuh -- attention over the paged cache held in 4 bits: 16-row tiles.
+// kv4_kernel.cuh -- attention over the paged cache held in 4 bits: the kernel and
+// its 16-row tiles (kv4_prefill.cuh has the larger ones).
 //
 // A value is s (n - z) (fi_kv4.h).  A code n in the low nibble of a 16-bit half
 // is, as it lies there, the fp16 subnormal n 2^-24, and in the next nibble n
@@ -14,12 +15,16 @@
 // columns), and O^T = V^T P^T has the dims as rows, so eight query rows cost one
 // product per 16 keys and 16 dims.  P^T comes from S^T by one 8 x 8 transpose
 // per 8 keys.  The zero point's sum is one more product whose rows all are z.
+// (tcgen05 would want the codes as 16-bit operands in shared memory, four times
+// the bytes that came, for a tile of which 8 of 128 rows are used.)
 //
-// Eight warps walk a chunk's keys in eight consecutive parts, each with a ring
-// of its own: 32 keys a stage, brought by one bulk copy a block (keys, values
-// and their words lie together), issued by the warp that consumed the stage
-// before, kKv4Depth stages ahead and across items.  No producer warp, no barrier
-// but the one that joins the eight states of an item.
+// Twelve warps compute, in three groups.  A long chunk's keys go over all of them
+// in consecutive parts; short chunks (up to kKv4GroupKeys keys), whose time is
+// latency and not bytes, go to the groups in turn, three at once.  Each computing
+// warp has a ring of stages of its own, 32 keys each; one loader warp fills them,
+// a lane a ring, one bulk copy a block (keys, values and their words lie
+// together), across items.  The only barriers are those that join an item's
+// states.
 #pragma once
 #include "attention_kernel.cuh"
 #include "kv4_layout.h"
@@ -27,23 +32,36 @@
 
 namespace fi {
 
-constexpr int kKv4Warps = 8;
-constexpr int kKv4Threads = 32 * kKv4Warps;
+constexpr int kKv4Threads = 512;       // warpgroup 0: loaders and MMA; 1 .. 3 compute
+constexpr int kKv4FirstWarp = 4;       // first computing warp
+constexpr int kKv4Warps = 12;          // computing warps of the 16-row tiles
+constexpr int kKv4GroupWarps = 4;      // warps of a group
+constexpr int kKv4Groups = kKv4Warps / kKv4GroupWarps;
+constexpr int kKv4GroupKeys = 1024;    // the longest chunk that one group takes
 constexpr int kKv4Stage = 32;          // keys of a stage
-constexpr int kKv4Depth = 4;           // stages a warp has in flight
+constexpr int kKv4Depth = 3;           // stages of a ring
 constexpr int kKv4StageBytes = 4608;   // 32 blocks of one slot, 144 bytes each
-constexpr int kKv4Tile = 16;           // packed query rows of a pass
+constexpr int kKv4Tile = 8;            // packed query rows of a pass
 constexpr int kKv4CombRow = 132;       // floats from row to row of a warp's state (128 and 4 against bank conflicts)
+constexpr int kKv4Barrier = 8;         // named barriers: of all computing warps, then of each group's
+// Registers per thread and warpgroup; each phase's sum is the launch's.
+constexpr int kKv4RegsLaunch = 128;
+constexpr int kKv4RegsDecode0 = 32, kKv4RegsDecode = 160;
+static_assert(kKv4RegsDecode0 + 3 * kKv4RegsDecode <= 4 * kKv4RegsLaunch, "register split exceeds the launch");
 
-struct alignas(128) Kv4Smem {
-  uint8_t ring[kKv4Warps][kKv4Depth][kKv4StageBytes];
+struct Kv4DecodeBufs {
+  alignas(128) uint8_t ring[kKv4Warps][kKv4Depth][kKv4StageBytes];
   float comb_o[kKv4Warps][kKv4Tile][kKv4CombRow];
   float comb_m[kKv4Warps][kKv4Tile];
   float comb_l[kKv4Warps][kKv4Tile];
-  uint32_t seen[kKv4Warps][kKv4Depth];  // keys of a stage that are there, a bit each
-  uint64_t full[kKv4Warps][kKv4Depth];
+  uint32_t good[kKv4Warps][kKv4Depth];  // keys of a stage whose page lies in the cache, a bit each
+};
+
+struct alignas(1024) Kv4Smem {
+  Kv4DecodeBufs dec;
+  uint64_t full[kKv4Warps][kKv4Depth], empty[kKv4Warps][kKv4Depth];
   volatile int abort;
-  int merge_last;
+  volatile int merge_last[kKv4Groups + 1];
 };
 constexpr size_t kKv4SmemBytes = sizeof(Kv4Smem);
 static_assert(kKv4SmemBytes <= 227 * 1024, "shared memory of the 4-bit kernel exceeds one CTA's limit");
@@ -67,6 +85,7 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                "l"(src), "r"(bytes), "r"(smem_u32(bar))
                : "memory");
 }
+__device__ __forceinline__ void prefetch_l1(const void* p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
 constexpr uint32_t kNibble0 = 0x000F000Fu, kNibble1 = 0x00F000F0u;
 
 // A word's two halves: the scale, and the zero point as n 2^-24 (the unit of the products).
@@ -75,250 +94,312 @@ __device__ __forceinline__ float word_zero(uint32_t w) { return __half2float(__u
 
 // ------------------------------------------------------------------- loads
 
-// A warp's walk over the stages of its CTA's items, ahead of their use.
-struct Kv4Loader {
-  const Kv4Params& kp;
-  Kv4Smem& sm;
-  const int32_t off_items, end;
-  const int warp, lane;
-  int32_t i;                    // item being loaded
-  int32_t pass, passes;         // of 16 rows
-  int32_t st, st_begin, st_end; // this warp's stages of it
-  int32_t kv0, kv1, npages, window;
-  const int32_t* pages;
-  const uint8_t* head;
-  int32_t ids, ids_next;        // page ids 32 window + lane, and of the next window
-  uint32_t issued;
+// The warps that share an item: all computing ones, or one group's.
+struct Kv4Team {
+  int rank, warps, threads, bar, flag;
+};
+__device__ __forceinline__ Kv4Team kv4_team(int warp, bool all) {
+  if (all) return Kv4Team{warp, kKv4Warps, 32 * kKv4Warps, kKv4Barrier, kKv4Groups};
+  const int g = warp / kKv4GroupWarps;
+  return Kv4Team{warp % kKv4GroupWarps, kKv4GroupWarps, 32 * kKv4GroupWarps, kKv4Barrier + 1 + g, g};
+}
+// A CTA's items [begin, shorts) go to all warps, those behind to the groups in turn.
+__device__ __forceinline__ int32_t kv4_next_item(int32_t i, int32_t shorts, int group) {
+  if (i + 1 < shorts) return i + 1;
+  return i < shorts ? shorts + group : i + kKv4Groups;
+}
+// First of the n stages that warp `rank` of `warps` takes: as few warps as have one each.
+__device__ __forceinline__ int kv4_share(int n, int rank, int warps) {
+  const int parts = min(n, warps);
+  return rank < parts ? n * rank / parts : n;
+}
+__device__ __forceinline__ int kv4_stages(const Item& it) { return (it.kv1 - it.kv0 + kKv4Stage - 1) / kKv4Stage; }
 
-  __device__ Kv4Loader(const Kv4Params& kp, Kv4Smem& sm, int32_t off_items, int32_t begin, int32_t end)
-      : kp(kp), sm(sm), off_items(off_items), end(end), warp((threadIdx.x >> 5) % kKv4Warps), lane(threadIdx.x & 31),
-        i(begin - 1), pass(0), passes(0), st(0), st_begin(0), st_end(0), window(-2), issued(0) {}
-
-  __device__ __forceinline__ int32_t load_ids(int32_t w) const {
-    const int32_t p = 32 * w + lane;
-    return p < npages ? __ldg(pages + p) : -1;
-  }
-  // The next stage of this warp; false after the last.
-  __device__ __forceinline__ bool more() {
-    while (st == st_end) {
-      if (++pass < passes) {
+// The loaders of the rings: lane u of a loader warp has ring first + u's place in
+// its items, and a round issues a stage for every ring whose next slot is free.
+// Stages of one or two blocks (kB = 32, 16) are issued by that lane, for all
+// rings at once, by one warp; stages of many small blocks (kB = 0) by the whole
+// warp, a lane a block, ring after ring, three rings a warp.  Page ids are loaded
+// a stage ahead, their lines a line ahead.
+template <int kB>
+__device__ void kv4_load(const Kv4Params& kp, Kv4Smem& sm, int loader, int32_t off_items, int32_t begin,
+                         int32_t shorts, int32_t end) {
+  constexpr int kRings = kKv4Warps / kKv4FirstWarp;
+  const RunParams& p = kp.run;
+  const KvCache& kc = p.kv[0];
+  const int lane = threadIdx.x & 31, w = loader * kRings + lane, group = w / kKv4GroupWarps;
+  const int log2_slots = kB == 32 ? 5 : kB == 16 ? 4 : kp.log2_block, bytes = kB ? kv4_block_bytes(kB) : kp.block_bytes;
+  const int blocks = kKv4Stage >> log2_slots;
+  const uint32_t block_keys = (2u << ((1 << log2_slots) - 1)) - 1;  // a block's keys in a stage's bits
+  int32_t i = begin - 1, passes = 0, st = 0, st_begin = 0, st_end = 0, kv0 = 0, kv1 = 0, npages = 0;
+  const int32_t* pages = nullptr;
+  const uint8_t* head = nullptr;
+  constexpr int kIds = kB == 16 ? 2 : kB == 32 ? 1 : kRings;
+  int32_t ids[kIds];  // of this lane's next stage; kB = 0: this lane's block of each ring's next stage
+  uint32_t issued = 0;
+  bool done = lane >= kRings, fresh = false;  // fresh: the next stage's ids are still to be fetched
+  long long seen_at = clock64();
+  while (true) {
+    while (!done && st == st_end) {  // this ring's next item, or the next rows of this one
+      fresh = true;
+      if (--passes > 0) {
         st = st_begin;
-        window = -2;
-        continue;
+        break;
       }
-      if (++i >= end) {
-        i = end;
-        passes = 0;
-        return false;
+      i = kv4_next_item(i, shorts, group);
+      if (i >= end) {
+        done = true;
+        fresh = false;
+        break;
       }
-      const Item it = load_item(kp.run.iws, off_items, i);
-      const int nst = (it.kv1 - it.kv0 + kKv4Stage - 1) / kKv4Stage;
-      st = st_begin = nst * warp / kKv4Warps;
-      st_end = nst * (warp + 1) / kKv4Warps;
-      pass = 0;
-      passes = (it.row1 - it.row0 + kKv4Tile - 1) / kKv4Tile;
+      const Item it = load_item(p.iws, off_items, i);
+      const Kv4Team team = kv4_team(w, i < shorts);
+      const int nst = kv4_stages(it);
+      st = st_begin = kv4_share(nst, team.rank, team.warps);
+      st_end = kv4_share(nst, team.rank + 1, team.warps);
+      passes = st < st_end ? (it.row1 - it.row0 + kKv4Tile - 1) / kKv4Tile : 0;
       kv0 = it.kv0;
       kv1 = it.kv1;
-      const KvCache& kc = kp.run.kv[0];
       npages = (it.rq.kv_len + kc.page_size - 1) >> kc.log2_page;
       pages = kc.kv_indices + it.rq.page_start;
       head = kp.cache + it.hk * kp.head_stride;
-      window = -2;
+      if (team.rank == 0 && issued > 0)  // the item's query rows on their way before the copies that would hold them up
+        for (int row = it.row0; row < it.row1; ++row) {
+          const int tok = row / p.group;
+          const uint16_t* q = p.q + (int64_t(it.rq.qo_start) + tok) * p.q_stride_tok +
+                              int64_t(it.hk * p.group + row - tok * p.group) * p.q_stride_head;
+          prefetch_l1(q);
+          prefetch_l1(q + 64);
+        }
     }
-    return true;
-  }
-  __device__ __forceinline__ void issue() {
-    if (!more()) return;
-    const KvCache& kc = kp.run.kv[0];
-    const int32_t j0 = kv0 + kKv4Stage * st;
-    const int32_t pg0 = j0 >> kc.log2_page;  // a stage's pages lie in one window of 32
-    if (pg0 >> 5 != window) {
-      ids = pg0 >> 5 == window + 1 ? ids_next : load_ids(pg0 >> 5);
-      window = pg0 >> 5;
-      ids_next = load_ids(window + 1);
+    const int32_t j0 = kv0 + kKv4Stage * st, pg0 = j0 >> kc.log2_page;
+    if (fresh && (pg0 & 31) < blocks && pg0 + 32 < npages) prefetch_l1(pages + pg0 + 32);
+    if constexpr (kB != 0) {
+      if (fresh)
+#pragma unroll
+        for (int b = 0; b < kIds; ++b) ids[b] = pg0 + b < npages ? __ldg(pages + pg0 + b) : -1;
+    } else {
+      const uint32_t which = __ballot_sync(0xffffffffu, fresh);
+#pragma unroll
+      for (int u = 0; u < kRings; ++u) {
+        if (!(which >> u & 1u)) continue;
+        const int32_t* at = reinterpret_cast<const int32_t*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(pages), u));
+        const int32_t pg = __shfl_sync(0xffffffffu, pg0, u) + lane, n = __shfl_sync(0xffffffffu, npages, u);
+        ids[u] = lane < blocks && pg < n ? __ldg(at + pg) : -1;
+      }
     }
-    const int32_t first = lane << kp.log2_block;  // of this lane's block in the stage
-    const int32_t id = __shfl_sync(0xffffffffu, ids, (pg0 + lane) & 31);
-    const bool mine = first < kKv4Stage && j0 + first < kv1 && id >= 0 && id < kc.num_pages;
-    const uint32_t blocks = __ballot_sync(0xffffffffu, mine);
-    const uint32_t keys = __ballot_sync(0xffffffffu, (blocks >> (lane >> kp.log2_block) & 1u) && j0 + lane < kv1);
+    fresh = false;
+    if (__all_sync(0xffffffffu, done)) break;
     const int slot = issued % kKv4Depth;
-    if (lane == 0) {
-      sm.seen[warp][slot] = keys;
-      mbar_arrive_expect_tx(&sm.full[warp][slot], __popc(blocks) * kp.block_bytes);
+    const bool free_slot = !done && mbar_test_wait(&sm.empty[w][slot], ((issued / kKv4Depth) & 1) ^ 1);
+    const uint32_t ready = __ballot_sync(0xffffffffu, free_slot);
+    if constexpr (kB != 0) {
+      if (free_slot) {
+        uint8_t* dst = sm.dec.ring[w][slot];
+        const uint8_t* src = head + int64_t((j0 & (kc.page_size - 1)) >> log2_slots) * bytes;
+        bool ok[kIds];
+        uint32_t good = 0;
+        int n = 0;
+#pragma unroll
+        for (int b = 0; b < kIds; ++b) {
+          ok[b] = uint32_t(ids[b]) < uint32_t(kc.num_pages) && j0 + b * kB < kv1;
+          n += ok[b];
+          good |= ok[b] ? block_keys << (b * kB) : 0u;
+        }
+        sm.dec.good[w][slot] = good;
+        mbar_arrive_expect_tx(&sm.full[w][slot], n * bytes);
+#pragma unroll
+        for (int b = 0; b < kIds; ++b)
+          if (ok[b]) bulk_load(dst + b * bytes, src + ids[b] * kp.page_stride, bytes, &sm.full[w][slot]);
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < kRings; ++u) {
+        if (!(ready >> u & 1u)) continue;
+        const int ring = loader * kRings + u, s = __shfl_sync(0xffffffffu, slot, u);
+        const int32_t key = __shfl_sync(0xffffffffu, j0, u), last = __shfl_sync(0xffffffffu, kv1, u);
+        const uint8_t* src = reinterpret_cast<const uint8_t*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(head), u));
+        const bool ok = uint32_t(ids[u]) < uint32_t(kc.num_pages) && lane < blocks && key + (lane << log2_slots) < last;
+        const uint32_t loads = __ballot_sync(0xffffffffu, ok);
+        const uint32_t good = __ballot_sync(0xffffffffu, loads >> (lane >> log2_slots) & 1u);
+        if (lane == 0) {
+          sm.dec.good[ring][s] = good;
+          mbar_arrive_expect_tx(&sm.full[ring][s], __popc(loads) * bytes);
+        }
+        __syncwarp();
+        if (ok) bulk_load(&sm.dec.ring[ring][s][lane * bytes], src + ids[u] * kp.page_stride, bytes, &sm.full[ring][s]);
+      }
     }
-    __syncwarp();
-    if (mine)
-      bulk_load(&sm.ring[warp][slot][lane * kp.block_bytes],
-                head + id * kp.page_stride + ((j0 & (kc.page_size - 1)) >> kp.log2_block) * kp.block_bytes,
-                kp.block_bytes, &sm.full[warp][slot]);
-    ++st;
-    ++issued;
+    if (free_slot) {
+      ++issued;
+      ++st;
+      fresh = st < st_end;
+    }
+    if (ready) {
+      seen_at = clock64();
+    } else {
+      __nanosleep(64);
+      const int stop = sm.abort != 0 ? 1 : clock64() - seen_at > kWaitBudgetClocks ? 2 : 0;
+      const int how = __shfl_sync(0xffffffffu, stop, 0);
+      if (how == 2) sm.abort = kStatusTimeout;
+      if (how) break;
+    }
   }
-};
+  // every copy has landed before the CTA leaves
+  if (lane < kRings)
+    for (uint32_t n = issued > kKv4Depth ? issued - kKv4Depth : 0; n < issued; ++n)
+      mbar_wait_drain(&sm.full[w][n % kKv4Depth], (n / kKv4Depth) & 1);
+  __syncwarp();
+}
 
 // ----------------------------------------------------------------- a stage
 
-// Where this lane (g = lane / 4, t = lane % 4) reads a block of 16 keys.  Row r
-// of the products is key r ^ (r >> 1 & 1): the rows that lanes t = 0 .. 3 of a
-// half warp read of v then alternate between the two halves of the 128-byte
-// lines (two ways instead of four).
+// Where this lane (g = lane / 4, t = lane % 4) reads in a stage.  Row r of the
+// products is key r ^ (r >> 1 & 1) of a run of 8: the rows of v that lanes t = 0 ..
+// 3 of a half warp read then alternate between the two halves of the 128-byte
+// lines (two ways instead of four).  The next 8 and the next 16 keys lie the same
+// distance on for every lane: numbers known to the compiler for blocks of kB =
+// 32 and 16 slots, uniform values otherwise (kB = 0).
+template <int kB>
 struct Kv4Places {
-  uint32_t k[2];        // rows of keys g and g + 8: 16 bytes, dims 32 t ..
-  uint32_t kw[2];       // their words (those of v: v_words further)
-  uint32_t v[4], vw[4]; // rows (8 bytes, dims 16 g ..) and words of keys 2t, 2t + 1, 2t + 8, 2t + 9
-  uint32_t v_words;
-  uint32_t next_rows, next_words;  // from the first 16 keys of a stage to the others
+  uint32_t k, w;      // of key g's row (16 bytes, dims 32 t ..) and word
+  uint32_t v[2];      // of the rows of keys 2t and 2t + 1 (8 bytes, dims 16 g ..)
+  uint32_t slots, bytes, log2_slots;
 
-  __device__ explicit Kv4Places(const Kv4Params& kp) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, B = kp.block_slots;
+  __device__ explicit Kv4Places(const Kv4Params& kp)
+      : slots(kB ? kB : kp.block_slots), bytes(kB ? kv4_block_bytes(kB) : kp.block_bytes),
+        log2_slots(kB == 32 ? 5 : kB == 16 ? 4 : kp.log2_block) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     auto key = [](int r) { return r ^ ((r >> 1) & 1); };
-    auto at = [&](int k, int row) { return (k >> kp.log2_block) * kp.block_bytes + (k & (B - 1)) * row; };
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      k[u] = at(key(g) + 8 * u, kKv4RowBytes) + 16 * t;
-      kw[u] = at(key(g) + 8 * u, 2) + kv4_k_word(B, 0);
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int c = key(2 * t + (u & 1)) + 8 * (u >> 1);
-      v[u] = at(c, kKv4RowBytes) + kv4_v_row(B, 0) + 8 * g;
-      vw[u] = at(c, 2) + kv4_v_word(B, 0);
-    }
-    v_words = 2 * B;
-    next_rows = B == 32 ? 16 * kKv4RowBytes : (16 >> kp.log2_block) * kp.block_bytes;
-    next_words = B == 32 ? 32 : next_rows;
+    auto at = [&](int k, int row) { return (k >> log2_slots) * bytes + (k & (slots - 1)) * row; };
+    k = at(key(g), kKv4RowBytes) + 16 * t;
+    w = at(key(g), 2) + kv4_k_word(slots, 0);
+    for (int u = 0; u < 2; ++u) v[u] = at(key(2 * t + u), kKv4RowBytes) + kv4_v_row(slots, 0) + 8 * g;
+  }
+  // n keys on (8 or 16 or 24), of rows of `row` bytes
+  __device__ __forceinline__ uint32_t on(int n, int row) const {
+    return (n >> log2_slots) * bytes + (n & (slots - 1)) * row;
   }
 };
 
-// Query rows 8 n + g as operand columns, and the states of rows 8 n + 2t, + 1.
-template <int NT>
-struct Kv4Rows16 {
-  uint32_t q[NT][8][2];  // of the 16 dims of step k
-  float c[NT][2];        // log2-domain factor of a row's products
-  float qs[NT][2];       // sum of the row's operand values
-  int lim[NT][2], lo[NT][2];
-  float m[NT][2], l[NT][2];
-  float o[NT][8][4];     // step i: dims 16 g + 8 (i / 4) + i % 4 (.., ..) and + 4
-  float z[NT][4];
-  float unit;            // the power of two that v's scales are multiplied by
+// Query row g as an operand column, and the states of rows 2t and 2t + 1.
+template <typename T>
+struct Kv4Rows {
+  uint32_t q[8][2];  // of the 16 dims of step k
+  float c[2];        // log2-domain factor of a row's products
+  float qs[2];       // sum of the row's operand values
+  int lim[2], lo[2];
+  float m[2], l[2];
+  float o[8][4];     // step i: dims 16 g + 8 (i / 4) + i % 4 (first two) and + 4 (last two)
+  float z[4];
+  float unit;        // the power of two that v's scales are multiplied by
 };
 
-template <typename T, int NT>
+template <typename T>
 __device__ __forceinline__ void kv4_load_rows(const Kv4Params& kp, const Item& it, int pass, int causal,
-                                              const Variant& var, Kv4Rows16<NT>& R) {
+                                              const Variant& var, Kv4Rows<T>& R) {
   const RunParams& p = kp.run;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, G = p.group;
+  const int row = it.row0 + kKv4Tile * pass + g;
+  uint4 u[4];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int row = it.row0 + kKv4Tile * pass + 8 * n + g;
-    uint4 u[4];
+  for (int j = 0; j < 4; ++j) u[j] = make_uint4(0u, 0u, 0u, 0u);
+  if (row < it.row1) {
+    const int tok = row / G;
+    const uint4* src = reinterpret_cast<const uint4*>(p.q + (int64_t(it.rq.qo_start) + tok) * p.q_stride_tok +
+                                                      int64_t(it.hk * G + row - tok * G) * p.q_stride_head + 32 * t);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) u[j] = make_uint4(0u, 0u, 0u, 0u);
-    if (row < it.row1) {
-      const int tok = row / G;
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + (int64_t(it.rq.qo_start) + tok) * p.q_stride_tok +
-                                                        int64_t(it.hk * G + row - tok * G) * p.q_stride_head + 32 * t);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) u[j] = __ldg(src + j);
-    }
-    float f[4][8], top = 0.f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t w[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 x = Elem<T>::to_float2(w[e]);
-        f[j][2 * e] = x.x;
-        f[j][2 * e + 1] = x.y;
-        top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
-      }
-    }
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    // the row times a power of two, its largest value in [2^14, 2^15): fp16 has
-    // room for the dims in the upper nibbles, which enter with 2^-4
-    int ex = int(__float_as_uint(top) >> 23) - 127;  // -127 for zero rows
-    ex = min(max(ex, -100), 100);
-    const float up = __int_as_float((127 + 14 - ex) << 23);
-    float sum = 0.f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      auto put = [&](uint32_t& dst, float a, float b, float unit) {
-        const __half2 h = __floats2half2_rn(a * (up * unit), b * (up * unit));
-        dst = *reinterpret_cast<const uint32_t*>(&h);
-        const float2 x = __half22float2(h);
-        sum += (x.x + x.y) / unit;
-      };
-      put(R.q[n][2 * j][0], f[j][0], f[j][4], 1.f);
-      put(R.q[n][2 * j][1], f[j][2], f[j][6], 1.f);
-      put(R.q[n][2 * j + 1][0], f[j][1], f[j][5], 0.0625f);
-      put(R.q[n][2 * j + 1][1], f[j][3], f[j][7], 0.0625f);
-    }
-    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-    const float c = p.scale_log2 * __int_as_float((127 + 10 + ex) << 23);  // 2^(ex - 14), and the products' 2^-24
-#pragma unroll
-    for (int u2 = 0; u2 < 2; ++u2) {
-      R.qs[n][u2] = __shfl_sync(0xffffffffu, sum, 8 * t + 4 * u2);
-      R.c[n][u2] = __shfl_sync(0xffffffffu, c, 8 * t + 4 * u2);
-      const int r = it.row0 + kKv4Tile * pass + 8 * n + 2 * t + u2;
-      const int pos = it.rq.kv_len - it.rq.qo_len + r / G;
-      R.lim[n][u2] = r < it.row1 ? (causal ? pos : it.rq.kv_len - 1) : -1;
-      R.lo[n][u2] = window_low(var, pos);
-      R.m[n][u2] = -INFINITY;
-      R.l[n][u2] = 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) R.o[n][i][e] = 0.f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) R.z[n][e] = 0.f;
+    for (int j = 0; j < 4; ++j) u[j] = __ldg(src + j);
   }
+  float top = 0.f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float f[8];
+    unpack8<T>(u[j], f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
+  }
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  // the row times a power of two, its largest value in [2^14, 2^15): fp16 has
+  // room for the dims in the upper nibbles, which enter with 2^-4
+  int ex = int(__float_as_uint(top) >> 23) - 127;  // -127 for rows of zeros
+  ex = min(max(ex, -100), 100);
+  const float up = __int_as_float((127 + 14 - ex) << 23);
+  float sum = 0.f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float f[8];
+    unpack8<T>(u[j], f);
+    auto put = [&](uint32_t& dst, float a, float b, float unit) {
+      const __half2 h = __floats2half2_rn(a * (up * unit), b * (up * unit));
+      dst = *reinterpret_cast<const uint32_t*>(&h);
+      const float2 x = __half22float2(h);
+      sum += (x.x + x.y) / unit;
+    };
+    put(R.q[2 * j][0], f[0], f[4], 1.f);
+    put(R.q[2 * j][1], f[2], f[6], 1.f);
+    put(R.q[2 * j + 1][0], f[1], f[5], 0.0625f);
+    put(R.q[2 * j + 1][1], f[3], f[7], 0.0625f);
+  }
+  sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+  sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+  const float c = p.scale_log2 * __int_as_float((127 + 10 + ex) << 23);  // 2^(ex - 14), and the products' 2^-24
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    R.qs[h] = __shfl_sync(0xffffffffu, sum, 8 * t + 4 * h);
+    R.c[h] = __shfl_sync(0xffffffffu, c, 8 * t + 4 * h);
+    const int r = it.row0 + kKv4Tile * pass + 2 * t + h;
+    const int pos = it.rq.kv_len - it.rq.qo_len + r / G;
+    R.lim[h] = r < it.row1 ? min(causal ? pos : it.rq.kv_len - 1, it.kv1 - 1) : -1;
+    R.lo[h] = window_low(var, pos);
+    R.m[h] = -INFINITY;
+    R.l[h] = 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) R.o[i][e] = 0.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) R.z[e] = 0.f;
   R.unit = __int_as_float((127 + 100) << 23);
 }
 
 // The 32 keys of a stage from key j0 on.  inside: every key of the stage is
-// there and visible to every row.
-template <int NT>
-__device__ __forceinline__ void kv4_stage(const uint8_t* stage, const Kv4Places& at, uint32_t seen, int j0, bool inside,
-                                          const Variant& var, Kv4Rows16<NT>& R) {
+// visible to every row and lies in the cache (good: one bit a key).
+template <typename T, int kB>
+__device__ __forceinline__ void kv4_stage(const uint8_t* stage, const Kv4Places<kB>& at, uint32_t good, int j0, bool inside,
+                                          const Variant& var, Kv4Rows<T>& R) {
   const int lane = threadIdx.x & 31, g = lane >> 2;
-  float s[2][NT][4];
+  float s[2][4];
   float vs[2][2];
+  uint32_t vz[2][2];  // zero points of v as operand rows: all of them, of two keys
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
-    const uint8_t* rows = stage + b * at.next_rows;
-    const uint8_t* words = stage + b * at.next_words;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[b][n][e] = 0.f;
-    const uint4 ka = *reinterpret_cast<const uint4*>(rows + at.k[0]);
-    const uint4 kb = *reinterpret_cast<const uint4*>(rows + at.k[1]);
+    for (int e = 0; e < 4; ++e) s[b][e] = 0.f;
+    const uint4 ka = *reinterpret_cast<const uint4*>(stage + at.k + at.on(16 * b, kKv4RowBytes));
+    const uint4 kb = *reinterpret_cast<const uint4*>(stage + at.k + at.on(16 * b + 8, kKv4RowBytes));
     const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const uint32_t ha = wa[j] >> 8, hb = wb[j] >> 8;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        mma16(s[b][n], wa[j] & kNibble0, wb[j] & kNibble0, ha & kNibble0, hb & kNibble0, R.q[n][2 * j][0],
-              R.q[n][2 * j][1]);
-        mma16(s[b][n], wa[j] & kNibble1, wb[j] & kNibble1, ha & kNibble1, hb & kNibble1, R.q[n][2 * j + 1][0],
-              R.q[n][2 * j + 1][1]);
-      }
+      mma16(s[b], wa[j] & kNibble0, wb[j] & kNibble0, ha & kNibble0, hb & kNibble0, R.q[2 * j][0], R.q[2 * j][1]);
+      mma16(s[b], wa[j] & kNibble1, wb[j] & kNibble1, ha & kNibble1, hb & kNibble1, R.q[2 * j + 1][0],
+            R.q[2 * j + 1][1]);
     }
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const uint32_t w = *reinterpret_cast<const uint16_t*>(words + at.kw[u]);
-      const uint32_t x = *reinterpret_cast<const uint16_t*>(words + at.kw[u] + at.v_words);
+      const uint8_t* word = stage + at.w + at.on(16 * b + 8 * u, 2);
+      const uint32_t w = *reinterpret_cast<const uint16_t*>(word);
+      const uint32_t x = *reinterpret_cast<const uint16_t*>(word + 2 * at.slots);
       const float ks = word_scale(w), kz = word_zero(w);
       vs[b][u] = word_scale(x);
+      vz[b][u] = transpose8((x & 15u) * 0x00010001u);
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) s[b][n][2 * u + h] = fmaf(-kz, R.qs[n][h], s[b][n][2 * u + h]) * ks;
+      for (int h = 0; h < 2; ++h) s[b][2 * u + h] = fmaf(-kz, R.qs[h], s[b][2 * u + h]) * ks;
     }
   }
   if (!inside) {
@@ -327,244 +408,310 @@ __device__ __forceinline__ void kv4_stage(const uint8_t* stage, const Kv4Places&
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int k = 16 * b + 8 * u + (g ^ ((g >> 1) & 1)), key = j0 + k;
-        const bool there = seen >> k & 1u;
+        const bool there = good >> k & 1u;  // other pages read as zeros
         bool any = false;
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const bool sees = there && key <= R.lim[n][h] && (key >= R.lo[n][h] || key < var.sink);
-            if (!sees) s[b][n][2 * u + h] = -INFINITY;
-            any |= sees;
-          }
-        if (!any) vs[b][u] = 0.f;  // a weight of 0 times any bytes, infinities included
+        for (int h = 0; h < 2; ++h) {
+          const bool sees = key <= R.lim[h] && (key >= R.lo[h] || key < var.sink);
+          s[b][2 * u + h] = !sees ? -INFINITY : there ? s[b][2 * u + h] : 0.f;
+          any |= sees;
+        }
+        if (!any || !there) vs[b][u] = 0.f;  // a weight of 0 times any bytes, infinities included
       }
   }
   // The running maxima move when a row's grows by more than 2^8, the unit of
   // the weights when a value scale would pass twice it.
-  float top[NT][2];
-  bool move = fmaxf(fmaxf(vs[0][0], vs[0][1]), fmaxf(vs[1][0], vs[1][1])) * R.unit >= 2.f;
+  float top[2];
+  float v = fmaxf(fmaxf(vs[0][0], vs[0][1]), fmaxf(vs[1][0], vs[1][1]));
+  bool move = v * R.unit >= 2.f;
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      top[n][h] = fmaxf(fmaxf(s[0][n][h], s[0][n][2 + h]), fmaxf(s[1][n][h], s[1][n][2 + h])) * R.c[n][h];
-      move |= top[n][h] > R.m[n][h] + kLazyRescale;
-    }
+  for (int h = 0; h < 2; ++h) {
+    top[h] = fmaxf(fmaxf(s[0][h], s[0][2 + h]), fmaxf(s[1][h], s[1][2 + h])) * R.c[h];
+    move |= top[h] > R.m[h] + kLazyRescale;
+  }
   if (__any_sync(0xffffffffu, move)) {
-    float v = fmaxf(fmaxf(vs[0][0], vs[0][1]), fmaxf(vs[1][0], vs[1][1]));
 #pragma unroll
     for (int x = 4; x < 32; x <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, x));
     float back = 1.f;
-    if (v * R.unit >= 2.f) {
-      const float unit = __int_as_float((254 << 23) - int(__float_as_uint(v) & 0x7F800000u));  // 1 / the power of two below v
+    if (v * R.unit >= 2.f) {  // the new unit: one over the power of two below v
+      const float unit = __int_as_float((254 << 23) - int(__float_as_uint(v) & 0x7F800000u));
       back = unit / R.unit;
       R.unit = unit;
     }
+    float f[2];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      float f[2];
+    for (int h = 0; h < 2; ++h) {
+      float x = top[h];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float x = top[n][h];
-#pragma unroll
-        for (int y = 4; y < 32; y <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, y));
-        f[h] = 1.f;
-        if (x > R.m[n][h] + kLazyRescale) {
-          f[h] = ex2(R.m[n][h] - x);
-          R.m[n][h] = x;
-        }
-        R.l[n][h] *= f[h];
-        f[h] *= back;
+      for (int y = 4; y < 32; y <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, y));
+      f[h] = 1.f;
+      if (x > R.m[h] + kLazyRescale) {
+        f[h] = ex2(R.m[h] - x);
+        R.m[h] = x;
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) R.o[n][i][e] *= f[e & 1];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) R.z[n][e] *= f[e & 1];
+      R.l[h] *= f[h];
+      f[h] *= back;
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) R.o[i][e] *= f[e & 1];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) R.z[e] *= f[e & 1];
   }
   // weights p s_v as operand columns: keys 2t, 2t + 1 and 2t + 8, 2t + 9 of row g
-  uint32_t w[2][NT][2];
+  uint32_t w[2][2];
+  const float m0 = R.m[0] == -INFINITY ? 0.f : R.m[0], m1 = R.m[1] == -INFINITY ? 0.f : R.m[1];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const float m0 = R.m[n][0] == -INFINITY ? 0.f : R.m[n][0], m1 = R.m[n][1] == -INFINITY ? 0.f : R.m[n][1];
+  for (int b = 0; b < 2; ++b)
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const float p0 = ex2(fmaf(s[b][n][2 * u], R.c[n][0], -m0)), p1 = ex2(fmaf(s[b][n][2 * u + 1], R.c[n][1], -m1));
-        R.l[n][0] += p0;
-        R.l[n][1] += p1;
-        const float x = vs[b][u] * R.unit;
-        w[b][n][u] = transpose8(tc::pack2<__half>(p0 * x, p1 * x));
-      }
-  }
+    for (int u = 0; u < 2; ++u) {
+      const float p0 = ex2(fmaf(s[b][2 * u], R.c[0], -m0)), p1 = ex2(fmaf(s[b][2 * u + 1], R.c[1], -m1));
+      R.l[0] += p0;
+      R.l[1] += p1;
+      const float x = vs[b][u] * R.unit;
+      w[b][u] = transpose8(tc::pack2<__half>(p0 * x, p1 * x));
+    }
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
-    const uint8_t* rows = stage + b * at.next_rows;
-    const uint8_t* words = stage + b * at.next_words;
-    uint32_t z[4];
-    uint2 v[4];
+    const uint32_t b0 = w[b][0], b1 = w[b][1];
+    uint2 v4[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      z[u] = *reinterpret_cast<const uint16_t*>(words + at.vw[u]);
-      v[u] = *reinterpret_cast<const uint2*>(rows + at.v[u]);
-    }
-    const uint32_t z0 = (z[0] | z[1] << 16) & kNibble0, z1 = (z[2] | z[3] << 16) & kNibble0;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) mma16(R.z[n], z0, z0, z1, z1, w[b][n][0], w[b][n][1]);
+    for (int u = 0; u < 4; ++u)
+      v4[u] = *reinterpret_cast<const uint2*>(stage + at.v[u & 1] + at.on(16 * b + 8 * (u >> 1), kKv4RowBytes));
+    mma16(R.z, vz[b][0], vz[b][0], vz[b][1], vz[b][1], b0, b1);
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      auto word = [&](int u) { return half ? v[u].y : v[u].x; };
+      auto word = [&](int u) { return half ? v4[u].y : v4[u].x; };
       const uint32_t a0 = __byte_perm(word(0), word(1), 0x5410), a1 = __byte_perm(word(0), word(1), 0x7632);
       const uint32_t a2 = __byte_perm(word(2), word(3), 0x5410), a3 = __byte_perm(word(2), word(3), 0x7632);
       const uint32_t h0 = a0 >> 8, h1 = a1 >> 8, h2 = a2 >> 8, h3 = a3 >> 8;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const uint32_t b0 = w[b][n][0], b1 = w[b][n][1];
-        mma16(R.o[n][4 * half], a0 & kNibble0, a1 & kNibble0, a2 & kNibble0, a3 & kNibble0, b0, b1);
-        mma16(R.o[n][4 * half + 1], a0 & kNibble1, a1 & kNibble1, a2 & kNibble1, a3 & kNibble1, b0, b1);
-        mma16(R.o[n][4 * half + 2], h0 & kNibble0, h1 & kNibble0, h2 & kNibble0, h3 & kNibble0, b0, b1);
-        mma16(R.o[n][4 * half + 3], h0 & kNibble1, h1 & kNibble1, h2 & kNibble1, h3 & kNibble1, b0, b1);
-      }
+      mma16(R.o[4 * half], a0 & kNibble0, a1 & kNibble0, a2 & kNibble0, a3 & kNibble0, b0, b1);
+      mma16(R.o[4 * half + 1], a0 & kNibble1, a1 & kNibble1, a2 & kNibble1, a3 & kNibble1, b0, b1);
+      mma16(R.o[4 * half + 2], h0 & kNibble0, h1 & kNibble0, h2 & kNibble0, h3 & kNibble0, b0, b1);
+      mma16(R.o[4 * half + 3], h0 & kNibble1, h1 & kNibble1, h2 & kNibble1, h3 & kNibble1, b0, b1);
     }
   }
 }
 
 // This warp's state of the pass into shared memory: o (not yet divided), max, sum.
-template <int NT>
-__device__ __forceinline__ void kv4_put_state(Kv4Smem& sm, int warp, Kv4Rows16<NT>& R, bool any) {
+template <typename T>
+__device__ __forceinline__ void kv4_put_state(Kv4Smem& sm, int warp, Kv4Rows<T>& R) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const float up = 16777216.f / R.unit;  // 2^24: codes and zero points came in as n 2^-24
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
+  for (int h = 0; h < 2; ++h) {
+    float l = R.l[h];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float l = R.l[n][h];
-#pragma unroll
-      for (int x = 4; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-      const int row = 8 * n + 2 * t + h;
-      if (g == 0) {
-        sm.comb_m[warp][row] = any ? R.m[n][h] : -INFINITY;
-        sm.comb_l[warp][row] = l;
-      }
-      if (!any) continue;
-      const float up = 16777216.f / R.unit;  // 2^24: codes and zero points came in as n 2^-24
-      float* dst = &sm.comb_o[warp][row][16 * g];
-#pragma unroll
-      for (int half = 0; half < 2; ++half)
-#pragma unroll
-        for (int hi = 0; hi < 2; ++hi) {
-          float x[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = ((i & 1 ? 0.0625f : 1.f) * R.o[n][4 * half + i][2 * hi + h] - R.z[n][h]) * up;
-          *reinterpret_cast<float4*>(dst + 8 * half + 4 * hi) = make_float4(x[0], x[1], x[2], x[3]);
-        }
+    for (int x = 4; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+    const int row = 2 * t + h;
+    if (g == 0) {
+      sm.dec.comb_m[warp][row] = R.m[h];
+      sm.dec.comb_l[warp][row] = l;
     }
-}
-
-template <typename T, int NT>
-__device__ __forceinline__ void kv4_pass(const Kv4Params& kp, Kv4Smem& sm, Kv4Loader& load, const Kv4Places& at,
-                                         const Item& it, int pass, int causal, const Variant& var, uint32_t& used) {
-  const int warp = load.warp;
-  Kv4Rows16<NT> R;
-  kv4_load_rows<T, NT>(kp, it, pass, causal, var, R);
-  // keys that every row of the pass sees
-  const int r0 = it.row0 + kKv4Tile * pass, r1 = min(it.row1, r0 + kKv4Tile) - 1, G = kp.run.group;
-  const int first = it.rq.kv_len - it.rq.qo_len + r0 / G, last = it.rq.kv_len - it.rq.qo_len + r1 / G;
-  const int lim = causal ? first : it.rq.kv_len - 1, lo = window_low(var, last);
-  const int nst = (it.kv1 - it.kv0 + kKv4Stage - 1) / kKv4Stage;
-  const int s0 = nst * warp / kKv4Warps, s1 = nst * (warp + 1) / kKv4Warps;
-  bool ok = !sm.abort;
-  ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0);
-  for (int st = s0; st < s1 && ok; ++st) {
-    const int slot = used % kKv4Depth;
-    ok = warp_wait(&sm.full[warp][slot], (used / kKv4Depth) & 1, &sm.abort);
-    if (!ok) break;
-    ++used;
-    const int j0 = it.kv0 + kKv4Stage * st;
-    const uint32_t seen = sm.seen[warp][slot];
-    const bool inside = seen == 0xffffffffu && j0 + kKv4Stage - 1 <= lim && j0 >= lo;
-    kv4_stage<NT>(sm.ring[warp][slot], at, seen, j0, inside, var, R);
-    __syncwarp();
-    load.issue();
+    float* dst = &sm.dec.comb_o[warp][row][16 * g];
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+      for (int hi = 0; hi < 2; ++hi) {
+        float x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = ((i & 1 ? 0.0625f : 1.f) * R.o[4 * half + i][2 * hi + h] - R.z[h]) * up;
+        *reinterpret_cast<float4*>(dst + 8 * half + 4 * hi) = make_float4(x[0], x[1], x[2], x[3]);
+      }
   }
-  kv4_put_state<NT>(sm, warp, R, s1 > s0);
 }
 
-// The items [begin, end) of a CTA; tid counts the kKv4Threads threads that run it.
+// One row of a split unit from its chunks' partial states, in chunk order, by a
+// warp: lane c has chunk c's log-sum-exp (32 at a time), eight chunks' partial
+// outputs are in flight.
 template <typename T>
-__device__ void kv4_consume(const Kv4Params& kp, Kv4Smem& sm, int tid, int32_t begin, int32_t end, int32_t off_items,
-                            int32_t off_merge, int32_t off_cnt, int causal, const Variant& var) {
+__device__ __forceinline__ void kv4_merge_row(const RunParams& p, const Item& it, int r, int n, int64_t base) {
+  const int lane = threadIdx.x & 31, nrows = it.row1 - it.row0;
+  const float* lse = p.fws + base + r;
+  const float4* part = reinterpret_cast<const float4*>(p.fws + p.partial_o_offset + (base + r) * kHeadDim) + lane;
+  const int64_t step = int64_t(nrows) * (kHeadDim / 4);
+  float M = -INFINITY;
+  for (int c = lane; c < n; c += 32) M = fmaxf(M, __ldcg(lse + int64_t(c) * nrows));
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+  float L = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (M != -INFINITY) {
+    for (int c0 = 0; c0 < n; c0 += 32) {
+      const float mine = c0 + lane < n ? ex2((__ldcg(lse + int64_t(c0 + lane) * nrows) - M) * 1.4426950408889634f) : 0.f;
+      for (int c1 = c0; c1 < min(n, c0 + 32); c1 += 8) {
+        float4 v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          v[u] = c1 + u < n ? __ldcg(part + (c1 + u) * step) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const float w = __shfl_sync(0xffffffffu, mine, (c1 + u) & 31);
+          L += w;
+          acc.x += w * v[u].x;
+          acc.y += w * v[u].y;
+          acc.z += w * v[u].z;
+          acc.w += w * v[u].w;
+        }
+      }
+    }
+  }
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const int row = it.row0 + r, t = row / p.group, head = it.hk * p.group + row - t * p.group;
+  const int64_t tok = int64_t(it.rq.qo_start) + t;
+  uint2 packed;
+  packed.x = Elem<T>::from_float2(acc.x * inv, acc.y * inv);
+  packed.y = Elem<T>::from_float2(acc.z * inv, acc.w * inv);
+  *reinterpret_cast<uint2*>(p.o + tok * p.o_stride_tok + int64_t(head) * p.o_stride_head + 4 * lane) = packed;
+  if (lane == 0 && p.lse) p.lse[tok * p.num_qo_heads + head] = L > 0.f ? M + __logf(L) : -INFINITY;
+}
+
+// Behind an item of a split unit: the team that completes the unit's counter
+// merges its chunks (units left to the late merge, where one follows, not).
+template <typename T>
+__device__ __forceinline__ void kv4_merge_unit(const RunParams& p, Kv4Smem& sm, const Item& it, const Kv4Team& team,
+                                               int32_t off_merge, int32_t off_cnt) {
+  const int32_t* unit = p.iws + off_merge + FI_MERGE_INTS * it.merge;
+  if (p.late_merge && __ldg(unit + FI_MERGE_LATE)) return;
+  const int n = __ldg(unit + 4);
+  const int64_t base = __ldg(unit + 5);
+  __threadfence();
+  named_barrier_sync(team.bar, team.threads);
+  if (team.rank == 0 && (threadIdx.x & 31) == 0)
+    sm.merge_last[team.flag] = !sm.abort && atomicAdd(p.iws + off_cnt + it.merge, 1) == n - 1;
+  named_barrier_sync(team.bar, team.threads);
+  if (sm.merge_last[team.flag]) {
+    __threadfence();
+    for (int r = team.rank; r < it.row1 - it.row0; r += team.warps) kv4_merge_row<T>(p, it, r, n, base);
+    if (team.rank == 0 && (threadIdx.x & 31) == 0) p.iws[off_cnt + it.merge] = 0;  // ready for the next run of this plan
+  }
+  named_barrier_sync(team.bar, team.threads);
+}
+
+// Rows [kKv4Tile pass, ..) of an item, by its team.  `after`: the team whose
+// states of the pass before may still be being joined; its barrier comes before
+// this warp's next state, so that a warp without a row to join goes on.
+template <typename T, int kB>
+__device__ __forceinline__ void kv4_pass(const Kv4Params& kp, Kv4Smem& sm, int warp, const Kv4Places<kB>& at,
+                                         const Item& it, int pass, const Kv4Team& team, Kv4Team& after, int causal,
+                                         const Variant& var, uint32_t& used) {
   const RunParams& p = kp.run;
-  const int G = p.group;
-  const Kv4Places at(kp);
-  Kv4Loader load(kp, sm, off_items, begin, end);
-  for (int d = 0; d < kKv4Depth; ++d) load.issue();
-  uint32_t used = 0;
-  for (int32_t i = begin; i < end; ++i) {
-    const Item it = load_item(p.iws, off_items, i);
-    const int nrows = it.row1 - it.row0;
-    for (int pass = 0; kKv4Tile * pass < nrows; ++pass) {
-      const int rows = min(kKv4Tile, nrows - kKv4Tile * pass);
-      if (rows <= 8)
-        kv4_pass<T, 1>(kp, sm, load, at, it, pass, causal, var, used);
-      else
-        kv4_pass<T, 2>(kp, sm, load, at, it, pass, causal, var, used);
-      named_barrier_sync(1, kKv4Threads);
-      if (!sm.abort) {
-        for (int task = tid; task < rows * 32; task += kKv4Threads) {
-          const int r = task >> 5, ch = task & 31;
-          float M = -INFINITY;
-#pragma unroll
-          for (int w = 0; w < kKv4Warps; ++w) M = fmaxf(M, sm.comb_m[w][r]);
-          float L = 0.f;
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (M != -INFINITY) {
-#pragma unroll
-            for (int w = 0; w < kKv4Warps; ++w) {
-              if (sm.comb_m[w][r] == -INFINITY) continue;  // no key, or no state at all
-              const float f = ex2(sm.comb_m[w][r] - M);
-              const float4 v = *reinterpret_cast<const float4*>(&sm.comb_o[w][r][4 * ch]);
-              L += f * sm.comb_l[w][r];
-              acc.x += f * v.x;
-              acc.y += f * v.y;
-              acc.z += f * v.z;
-              acc.w += f * v.w;
-            }
-          }
-          const float inv = L > 0.f ? 1.f / L : 0.f;
-          const float lse = L > 0.f ? (M + __log2f(L)) * 0.69314718055994531f : -INFINITY;
-          const int prow = kKv4Tile * pass + r;
-          if (it.part < 0) {
-            const int row = it.row0 + prow, t = row / G, head = it.hk * G + row - t * G;
-            const int64_t tok = int64_t(it.rq.qo_start) + t;
-            uint2 packed;
-            packed.x = Elem<T>::from_float2(acc.x * inv, acc.y * inv);
-            packed.y = Elem<T>::from_float2(acc.z * inv, acc.w * inv);
-            *reinterpret_cast<uint2*>(p.o + tok * p.o_stride_tok + int64_t(head) * p.o_stride_head + 4 * ch) = packed;
-            if (ch == 0 && p.lse) p.lse[tok * p.num_qo_heads + head] = lse;
-          } else {
-            const int64_t part = int64_t(it.part) + prow;
-            *reinterpret_cast<float4*>(p.fws + p.partial_o_offset + part * kHeadDim + 4 * ch) =
-                make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-            if (ch == 0) p.fws[part] = lse;
-          }
-        }
-      }
-      named_barrier_sync(1, kKv4Threads);
+  const int lane = threadIdx.x & 31, G = p.group;
+  const int rows = min(kKv4Tile, it.row1 - it.row0 - kKv4Tile * pass);
+  const int nst = kv4_stages(it), parts = min(nst, team.warps);
+  if (team.rank < parts) {
+    Kv4Rows<T> R;
+    kv4_load_rows<T>(kp, it, pass, causal, var, R);
+    // keys that every row of the pass sees
+    const int r0 = it.row0 + kKv4Tile * pass, r1 = r0 + rows - 1, pos = it.rq.kv_len - it.rq.qo_len;
+    const int lim = min(causal ? pos + r0 / G : it.rq.kv_len - 1, it.kv1 - 1), lo = window_low(var, pos + r1 / G);
+    const int s1 = kv4_share(nst, team.rank + 1, team.warps);
+    bool ok = __shfl_sync(0xffffffffu, sm.abort ? 0 : 1, 0);
+    for (int st = kv4_share(nst, team.rank, team.warps); st < s1 && ok; ++st) {
+      const int slot = used % kKv4Depth;
+      ok = warp_wait(&sm.full[warp][slot], (used / kKv4Depth) & 1, &sm.abort);
+      if (!ok) break;
+      ++used;
+      const int j0 = it.kv0 + kKv4Stage * st;
+      const uint32_t good = sm.dec.good[warp][slot];
+      const bool inside = good == 0xffffffffu && j0 + kKv4Stage - 1 <= lim && j0 >= lo;
+      kv4_stage<T, kB>(sm.dec.ring[warp][slot], at, good, j0, inside, var, R);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.empty[warp][slot]);
     }
-    if (it.merge >= 0)
-      merge_split_unit<T>(p, it, it.rq, off_merge, off_cnt, tid, kKv4Threads, 2, &sm.merge_last, sm.abort);
+    if (after.warps) named_barrier_sync(after.bar, after.threads);
+    kv4_put_state<T>(sm, warp, R);
+  } else if (after.warps) {
+    named_barrier_sync(after.bar, after.threads);
   }
-  // given up: the copies in flight have landed before the CTA leaves
-  if (load.lane == 0)
-    for (; used < load.issued; ++used) mbar_wait_drain(&sm.full[load.warp][used % kKv4Depth], (used / kKv4Depth) & 1);
-  __syncwarp();
+  named_barrier_sync(team.bar, team.threads);
+  const int w0 = warp - team.rank;  // the team's first warp
+  if (!sm.abort) {
+    for (int r = team.rank; r < rows; r += team.warps) {
+      // lane w has warp w's maximum and sum
+      const float m = lane < parts ? sm.dec.comb_m[w0 + lane][r] : -INFINITY;
+      float M = m;
+#pragma unroll
+      for (int x = 8; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+      M = __shfl_sync(0xffffffffu, M, 0);
+      const float f = m != -INFINITY ? ex2(m - M) : 0.f;
+      float L = lane < parts ? f * sm.dec.comb_l[w0 + lane][r] : 0.f;
+#pragma unroll
+      for (int x = 8; x > 0; x >>= 1) L += __shfl_xor_sync(0xffffffffu, L, x);
+      L = __shfl_sync(0xffffffffu, L, 0);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int w = 0; w < parts; ++w) {
+        const float4 v = *reinterpret_cast<const float4*>(&sm.dec.comb_o[w0 + w][r][4 * lane]);
+        const float fw = __shfl_sync(0xffffffffu, f, w);
+        acc.x += fw * v.x;
+        acc.y += fw * v.y;
+        acc.z += fw * v.z;
+        acc.w += fw * v.w;
+      }
+      const float inv = L > 0.f ? 1.f / L : 0.f;
+      const float lse = L > 0.f ? (M + __log2f(L)) * 0.69314718055994531f : -INFINITY;
+      const int prow = kKv4Tile * pass + r;
+      if (it.part < 0) {
+        const int row = it.row0 + prow, t = row / G, head = it.hk * G + row - t * G;
+        const int64_t tok = int64_t(it.rq.qo_start) + t;
+        uint2 packed;
+        packed.x = Elem<T>::from_float2(acc.x * inv, acc.y * inv);
+        packed.y = Elem<T>::from_float2(acc.z * inv, acc.w * inv);
+        *reinterpret_cast<uint2*>(p.o + tok * p.o_stride_tok + int64_t(head) * p.o_stride_head + 4 * lane) = packed;
+        if (lane == 0 && p.lse) p.lse[tok * p.num_qo_heads + head] = lse;
+      } else {
+        const int64_t part = int64_t(it.part) + prow;
+        *(reinterpret_cast<float4*>(p.fws + p.partial_o_offset + part * kHeadDim) + lane) =
+            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        if (lane == 0) p.fws[part] = lse;
+      }
+    }
+  }
+  after = team;
 }
 
-template <typename T>
+// The items [begin, end) of a CTA, by computing warp `warp`.
+template <typename T, int kB>
+__device__ void kv4_consume(const Kv4Params& kp, Kv4Smem& sm, int warp, int32_t begin, int32_t shorts, int32_t end,
+                            int32_t off_items, int32_t off_merge, int32_t off_cnt, int causal, const Variant& var) {
+  const RunParams& p = kp.run;
+  const Kv4Places<kB> at(kp);
+  uint32_t used = 0;
+  Kv4Team after{0, 0, 0, 0, 0};
+  for (int32_t i = kv4_next_item(begin - 1, shorts, warp / kKv4GroupWarps); i < end;
+       i = kv4_next_item(i, shorts, warp / kKv4GroupWarps)) {
+    const Item it = load_item(p.iws, off_items, i);
+    const Kv4Team team = kv4_team(warp, i < shorts);
+    for (int pass = 0; kKv4Tile * pass < it.row1 - it.row0; ++pass)
+      kv4_pass<T, kB>(kp, sm, warp, at, it, pass, team, after, causal, var, used);
+    if (it.merge >= 0) kv4_merge_unit<T>(p, sm, it, team, off_merge, off_cnt);
+  }
+  if (after.warps) named_barrier_sync(after.bar, after.threads);
+}
+
+// First item of [begin, end) that one group takes alone: a CTA's items of a
+// class come longest first, and a last one goes to all warps.  Whole warps; lane
+// l looks at item i0 + l.
+__device__ __forceinline__ int32_t kv4_first_short(const RunParams& p, int32_t begin, int32_t end, int32_t off_items) {
+  const int lane = threadIdx.x & 31;
+  for (int32_t i0 = begin; i0 < end; i0 += 32) {
+    bool is_short = true;
+    if (i0 + lane < end) {
+      const int2 kv = __ldg(reinterpret_cast<const int2*>(p.iws + off_items + FI_ITEM_INTS * (i0 + lane) + 4));
+      is_short = kv.y - kv.x <= kKv4GroupKeys;
+    }
+    const unsigned m = __ballot_sync(0xffffffffu, is_short);
+    if (m) {
+      const int32_t first = i0 + __ffs(m) - 1;
+      return first + 1 >= end ? end : first;
+    }
+  }
+  return end;
+}
+
+template <typename T, int kB>
 __global__ void __launch_bounds__(kKv4Threads, 1) kv4_attention_kernel(const __grid_constant__ Kv4Params kp) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   Kv4Smem& sm = *reinterpret_cast<Kv4Smem*>(smem_raw);
@@ -572,41 +719,46 @@ __global__ void __launch_bounds__(kKv4Threads, 1) kv4_attention_kernel(const __g
   const RunParams& p = kp.run;
   const int32_t* iws = p.iws;
   // The plan in the workspace has to be one over the 4-bit cache and fit this
-  // launch: nothing is written otherwise.
-  const int32_t n_items = ws_header(iws, FI_H_NUM_ITEMS), off_cta = ws_header(iws, FI_H_OFF_CTA);
+  // launch: nothing is written otherwise.  (A plan's CTA offsets and items lie
+  // where this grid has them: their loads do not wait for the header's.)
+  constexpr int32_t off_cta = FI_HEADER_INTS;
+  const int32_t off_items = off_cta + ((int32_t(gridDim.x) + 4) & ~3);
+  const int32_t begin = __ldg(iws + off_cta + blockIdx.x), end = __ldg(iws + off_cta + blockIdx.x + 1);
   const int32_t h_rows = ws_header(iws, FI_H_PARTIAL_ROWS), h_qo = ws_header(iws, FI_H_TOTAL_QO);
-  bool bad = ws_header(iws, FI_H_MAGIC) != FI_PLAN_MAGIC_KV4 || ws_header(iws, FI_H_NUM_CTAS) != int32_t(gridDim.x) ||
-             h_rows < 0 || h_rows > p.max_partial_rows || h_qo < 0 || h_qo > p.q_num_tokens ||
-             ws_header(iws, FI_H_NUM_QO_HEADS) != p.num_qo_heads ||
-             ws_header(iws, FI_H_NUM_KV_HEADS) != p.num_kv_heads ||
-             ws_header(iws, FI_H_PAGE_SIZE) != p.kv[0].page_size || (smem_u32(smem_raw) & 127u) != 0;
-  int32_t begin = 0, end = 0;
-  if (!bad) {
-    begin = __ldg(iws + off_cta + blockIdx.x);
-    end = __ldg(iws + off_cta + blockIdx.x + 1);
-    bad = begin < 0 || end < begin || end > n_items;
-  }
+  const bool bad = ws_header(iws, FI_H_MAGIC) != FI_PLAN_MAGIC_KV4 ||
+                   ws_header(iws, FI_H_NUM_CTAS) != int32_t(gridDim.x) || ws_header(iws, FI_H_OFF_CTA) != off_cta ||
+                   ws_header(iws, FI_H_OFF_ITEMS) != off_items || h_rows < 0 || h_rows > p.max_partial_rows ||
+                   h_qo < 0 || h_qo > p.q_num_tokens || ws_header(iws, FI_H_NUM_QO_HEADS) != p.num_qo_heads ||
+                   ws_header(iws, FI_H_NUM_KV_HEADS) != p.num_kv_heads ||
+                   ws_header(iws, FI_H_PAGE_SIZE) != p.kv[0].page_size || (smem_u32(smem_raw) & 1023u) != 0 ||
+                   begin < 0 || end < begin || end > ws_header(iws, FI_H_NUM_ITEMS);
   if (bad) {
     if (threadIdx.x == 0) atomicOr(p.iws + FI_H_STATUS, kStatusBadPlan);
     return;
   }
-  const int32_t off_items = ws_header(iws, FI_H_OFF_ITEMS), off_merge = ws_header(iws, FI_H_OFF_MERGE);
-  const int32_t off_cnt = ws_header(iws, FI_H_OFF_COUNTERS);
+  const int32_t off_merge = ws_header(iws, FI_H_OFF_MERGE), off_cnt = ws_header(iws, FI_H_OFF_COUNTERS);
   const int causal = ws_header(iws, FI_H_CAUSAL);
   Variant var;
   var.window_left = ws_header(iws, FI_H_WINDOW_LEFT);
   var.sink = ws_header(iws, FI_H_SINK_TOKENS);
   var.cap_a = var.cap_b = 0.f;
   var.rope_table = nullptr;
-  if (threadIdx.x == 0) {
-    for (int w = 0; w < kKv4Warps; ++w)
-      for (int s = 0; s < kKv4Depth; ++s) mbar_init(&sm.full[w][s], 1);
-    sm.abort = 0;
-    sm.merge_last = 0;
-    fence_mbar_init();
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x < kKv4Warps * kKv4Depth) {
+    mbar_init(&sm.full[0][threadIdx.x], 1);
+    mbar_init(&sm.empty[0][threadIdx.x], 1);
   }
+  if (threadIdx.x == 0) sm.abort = 0;
+  fence_mbar_init();
+  const int32_t shorts = kv4_first_short(p, begin, end, off_items);
   __syncthreads();
-  kv4_consume<T>(kp, sm, threadIdx.x, begin, end, off_items, off_merge, off_cnt, causal, var);
+  if (warp < kKv4FirstWarp) {
+    tc::setmaxnreg_dec<kKv4RegsDecode0>();
+    kv4_load<kB>(kp, sm, warp, off_items, begin, shorts, end);
+  } else {
+    tc::setmaxnreg_inc<kKv4RegsDecode>();
+    kv4_consume<T, kB>(kp, sm, warp - kKv4FirstWarp, begin, shorts, end, off_items, off_merge, off_cnt, causal, var);
+  }
   __syncthreads();
   if (threadIdx.x == 0 && sm.abort) atomicOr(p.iws + FI_H_STATUS, sm.abort);
 }
