@@ -29,6 +29,7 @@
 #include "attention_kernel.cuh"
 #include "kv4_layout.h"
 #include "kv4_params.h"
+#include "kv4_prefill.cuh"
 
 namespace fi {
 
@@ -46,8 +47,11 @@ constexpr int kKv4CombRow = 132;       // floats from row to row of a warp's sta
 constexpr int kKv4Barrier = 8;         // named barriers: of all computing warps, then of each group's
 // Registers per thread and warpgroup; each phase's sum is the launch's.
 constexpr int kKv4RegsLaunch = 128;
-constexpr int kKv4RegsDecode0 = 32, kKv4RegsDecode = 160;
+constexpr int kKv4RegsDecode0 = 56, kKv4RegsDecode = 152;
+constexpr int kKv4RegsMma = 80, kKv4RegsWiden = 64, kKv4RegsSoftmax = 184;
 static_assert(kKv4RegsDecode0 + 3 * kKv4RegsDecode <= 4 * kKv4RegsLaunch, "register split exceeds the launch");
+static_assert(kKv4RegsMma + kKv4RegsWiden + 2 * kKv4RegsSoftmax <= 4 * kKv4RegsLaunch,
+              "register split exceeds the launch");
 
 struct Kv4DecodeBufs {
   alignas(128) uint8_t ring[kKv4Warps][kKv4Depth][kKv4StageBytes];
@@ -58,10 +62,19 @@ struct Kv4DecodeBufs {
 };
 
 struct alignas(1024) Kv4Smem {
-  Kv4DecodeBufs dec;
+  union {
+    Kv4DecodeBufs dec;
+    Kv4PrefillBufs pf;
+  };
   uint64_t full[kKv4Warps][kKv4Depth], empty[kKv4Warps][kKv4Depth];
+  uint64_t raw_full[kKv4RawStages], raw_empty[kKv4RawStages];
+  uint64_t q_full, q_empty, drain;  // these and the next as in RunSmem
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t s_full[2], o_ready[2], o_free[2], p_full[2][2];
+  uint32_t tmem_base;
   volatile int abort;
   volatile int merge_last[kKv4Groups + 1];
+  int merge_last_pf;
 };
 constexpr size_t kKv4SmemBytes = sizeof(Kv4Smem);
 static_assert(kKv4SmemBytes <= 227 * 1024, "shared memory of the 4-bit kernel exceeds one CTA's limit");
@@ -78,12 +91,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
-}
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
 }
 __device__ __forceinline__ void prefetch_l1(const void* p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
 constexpr uint32_t kNibble0 = 0x000F000Fu, kNibble1 = 0x00F000F0u;
@@ -711,6 +718,19 @@ __device__ __forceinline__ int32_t kv4_first_short(const RunParams& p, int32_t b
   return end;
 }
 
+// A CTA's items come prefill-class first: the first of [begin, end) of at most
+// FI_TILE_DECODE packed rows.  Whole warps.
+__device__ __forceinline__ int32_t kv4_first_decode(const RunParams& p, int32_t begin, int32_t end, int32_t off_items) {
+  const int lane = threadIdx.x & 31;
+  for (int32_t i0 = begin; i0 < end; i0 += 32) {
+    const bool small = i0 + lane >= end ||
+                       __ldg(p.iws + off_items + FI_ITEM_INTS * (i0 + lane) + 9) * p.group <= FI_TILE_DECODE;
+    const unsigned m = __ballot_sync(0xffffffffu, small);
+    if (m) return min(end, i0 + __ffs(m) - 1);
+  }
+  return end;
+}
+
 template <typename T, int kB>
 __global__ void __launch_bounds__(kKv4Threads, 1) kv4_attention_kernel(const __grid_constant__ Kv4Params kp) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -748,18 +768,91 @@ __global__ void __launch_bounds__(kKv4Threads, 1) kv4_attention_kernel(const __g
     mbar_init(&sm.full[0][threadIdx.x], 1);
     mbar_init(&sm.empty[0][threadIdx.x], 1);
   }
-  if (threadIdx.x == 0) sm.abort = 0;
-  fence_mbar_init();
-  const int32_t shorts = kv4_first_short(p, begin, end, off_items);
-  __syncthreads();
-  if (warp < kKv4FirstWarp) {
-    tc::setmaxnreg_dec<kKv4RegsDecode0>();
-    kv4_load<kB>(kp, sm, warp, off_items, begin, shorts, end);
-  } else {
-    tc::setmaxnreg_inc<kKv4RegsDecode>();
-    kv4_consume<T, kB>(kp, sm, warp - kKv4FirstWarp, begin, shorts, end, off_items, off_merge, off_cnt, causal, var);
+  if (threadIdx.x == kKv4Warps * kKv4Depth) {
+    for (int s = 0; s < kKv4RawStages; ++s) {
+      mbar_init(&sm.raw_full[s], 1);
+      mbar_init(&sm.raw_empty[s], kKv4QuantWarps / 2);  // the two warps of a stage's keys
+    }
+    mbar_init(&sm.q_full, kKv4QuantWarps);
+    mbar_init(&sm.q_empty, 1);
+    mbar_init(&sm.drain, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sm.k_full[s], kKv4QuantWarps);
+      mbar_init(&sm.v_full[s], kKv4QuantWarps);
+      mbar_init(&sm.k_empty[s], 1);
+      mbar_init(&sm.v_empty[s], 1);
+      mbar_init(&sm.s_full[s], 1);
+      mbar_init(&sm.o_ready[s], 1);
+      mbar_init(&sm.o_free[s], 4);  // the warps of an M tile's softmax
+      mbar_init(&sm.p_full[s][0], 4);
+      mbar_init(&sm.p_full[s][1], 4);
+    }
+    sm.abort = 0;
+    sm.merge_last_pf = 0;
   }
+  fence_mbar_init();
+  const int32_t mid = kv4_first_decode(p, begin, end, off_items);
+  const int32_t shorts = kv4_first_short(p, mid, end, off_items);
+  const bool prefill = mid > begin;
+  if (prefill && warp == kMmaWarp) {
+    tc::tmem_alloc(&sm.tmem_base, kTmemCols);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
   __syncthreads();
+  tc::fence_after_sync();
+  // Every warpgroup leaves the first phase with the launch's registers: those
+  // that had more give them up before its barrier, the others take theirs behind
+  // it.
+  if (prefill) {
+    if (warp < kKv4QuantWarp0) {
+      tc::setmaxnreg_dec<kKv4RegsMma>();
+      if (warp == 0) {
+        kv4_pf_load<kB>(kp, sm, begin, mid, off_items);
+      } else if (warp == kMmaWarp) {
+        pf_mma<__half, false>(p, sm, begin, mid, off_items);
+        __syncwarp();
+      }
+      fence_proxy_async_smem();  // the second phase's copies go where these tiles were
+      tc::fence_before_sync();
+      named_barrier_sync_unaligned(kPhaseBarrier, kKv4Threads);
+      tc::fence_after_sync();
+      tc::setmaxnreg_inc<kKv4RegsLaunch>();
+    } else if (warp < kKv4SoftmaxWarp0) {
+      tc::setmaxnreg_dec<kKv4RegsWiden>();
+      kv4_pf_widen<T, kB>(kp, sm, begin, mid, off_items);
+      __syncwarp();
+      fence_proxy_async_smem();
+      named_barrier_sync_unaligned(kPhaseBarrier, kKv4Threads);
+      tc::setmaxnreg_inc<kKv4RegsLaunch>();
+    } else {
+      tc::setmaxnreg_inc<kKv4RegsSoftmax>();
+      if (var.window_left >= 0)
+        kv4_pf_softmax<T, true>(p, sm, begin, mid, off_items, off_merge, off_cnt, causal, var);
+      else
+        kv4_pf_softmax<T, false>(p, sm, begin, mid, off_items, off_merge, off_cnt, causal, var);
+      tc::setmaxnreg_dec<kKv4RegsLaunch>();
+      fence_proxy_async_smem();
+      tc::fence_before_sync();
+      named_barrier_sync_unaligned(kPhaseBarrier, kKv4Threads);
+      tc::fence_after_sync();
+    }
+  }
+  if (mid < end) {
+    if (warp < kKv4FirstWarp) {
+      tc::setmaxnreg_dec<kKv4RegsDecode0>();
+      kv4_load<kB>(kp, sm, warp, off_items, mid, shorts, end);
+    } else {
+      tc::setmaxnreg_inc<kKv4RegsDecode>();
+      kv4_consume<T, kB>(kp, sm, warp - kKv4FirstWarp, mid, shorts, end, off_items, off_merge, off_cnt, causal, var);
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (prefill && warp == kMmaWarp) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(sm.tmem_base, kTmemCols);
+  }
   if (threadIdx.x == 0 && sm.abort) atomicOr(p.iws + FI_H_STATUS, sm.abort);
 }
 

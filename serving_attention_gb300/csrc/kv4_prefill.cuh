@@ -1,0 +1,390 @@
+// kv4_prefill.cuh -- prefill-class items over the 4-bit cache, on the 5th-
+// generation tensor cores.
+//
+// Items, tiles and the order of the products are those of prefill_kernel.cuh: up
+// to two 128-row M tiles against 128-key tiles, S = Q K^T into tensor memory, P
+// over it as 16-bit pairs, O += P V.  What differs is where the operands come
+// from.  A value s (n - z) has seven significant bits of s times four of n - z:
+// eleven, an fp16 as it stands (fi_kv4.h), so K and V tiles are fp16 whatever the
+// type of q, and exact; a q row is brought into fp16 by a power of two of its
+// own, which its softmax takes back.
+//
+//  * warp 0 brings the pages' blocks, 64 keys a stage, into a ring of three raw
+//    stages (a bulk copy a block, page ids a stage ahead);
+//  * warps 4 .. 7 are the 128 keys of a tile: a thread has its key's scale and
+//    zero point in registers and turns two rows of 64 bytes into 256 bytes each,
+//    in the 128-byte swizzle that the products read: for eight codes one shift,
+//    four (x & m) | c (1024 + n and 64 + n as fp16), four subtractions of the
+//    same with z and four products with s.  The codes come out in the order 0, 4,
+//    1, 5, 2, 6, 3, 7 of each eight dims; Q is laid out in it too, and the output
+//    is put right where it is stored.  Q's rows are theirs as well, at an item's
+//    start.  Reads and writes of a quarter warp meet no bank twice: lane l starts
+//    with quarter l / 2 of its row.
+//  * warp 1 issues the products (pf_mma), warps 8 .. 15 the softmax.
+#pragma once
+#include "kv4_params.h"
+#include "attention_kernel.cuh"
+#include "kv4_layout.h"
+
+namespace fi {
+
+constexpr int kKv4RawKeys = 64;     // keys of a raw stage
+constexpr int kKv4RawStages = 3;
+constexpr int kKv4RawBytes = 9216;  // 64 blocks of one slot, 144 bytes each
+constexpr int kKv4QuantWarp0 = 4, kKv4QuantWarps = 4;
+constexpr int kKv4SoftmaxWarp0 = 8;
+
+struct Kv4PrefillBufs {
+  uint16_t q[2][2][kTileM][64];  // [M tile][d half][row][dim], and so on as in PrefillBufs
+  uint16_t k[2][2][kTileN][64];
+  uint16_t v[2][2][kTileN][64];
+  alignas(128) uint8_t raw[kKv4RawStages][kKv4RawBytes];
+  float q_scale[2][2 * kTileM];  // [item's parity][row]: log2-domain factor of the row's products
+  uint32_t good[kKv4RawStages][2];  // keys of a raw stage whose page lies in the cache, a bit each
+};
+
+// The raw stages of items [b0, b1), whole warp.
+template <int kB, typename Smem>
+__device__ void kv4_pf_load(const Kv4Params& kp, Smem& sm, int32_t b0, int32_t b1, int32_t off_items) {
+  const RunParams& p = kp.run;
+  const KvCache& kc = p.kv[0];
+  const int lane = threadIdx.x & 31;
+  const int log2_slots = kB == 32 ? 5 : kB == 16 ? 4 : kp.log2_block, bytes = kB ? kv4_block_bytes(kB) : kp.block_bytes;
+  const int blocks = kKv4RawKeys >> log2_slots;  // 2 .. 64: up to two a lane
+  uint32_t n = 0;
+  bool ok = true;
+  for (int32_t i = b0; i < b1 && ok; ++i) {
+    const Item it = load_item(p.iws, off_items, i);
+    const int stages = 2 * item_kv_tiles(it);  // a tile's second half may have no key
+    const int npages = (it.rq.kv_len + kc.page_size - 1) >> kc.log2_page;
+    const int32_t* pages = kc.kv_indices + it.rq.page_start;
+    const uint8_t* head = kp.cache + it.hk * kp.head_stride;
+    int32_t next[2];
+    auto fetch = [&](int st) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int b = lane + 32 * u, key = kKv4RawKeys * st + (b << log2_slots);
+        const int pg = (it.kv0 + key) >> kc.log2_page;
+        next[u] = b < blocks && key < it.kv1 - it.kv0 && pg < npages ? __ldg(pages + pg) : -1;
+      }
+    };
+    if (stages > 0) fetch(0);
+    for (int st = 0; st < stages; ++st, ++n) {
+      const int slot = n % kKv4RawStages;
+      const int32_t id[2] = {next[0], next[1]};
+      if (st + 1 < stages) fetch(st + 1);
+      ok = warp_wait(&sm.raw_empty[slot], ((n / kKv4RawStages) & 1) ^ 1, &sm.abort);
+      if (!ok) break;
+      const bool in0 = uint32_t(id[0]) < uint32_t(kc.num_pages), in1 = uint32_t(id[1]) < uint32_t(kc.num_pages);
+      const uint32_t m0 = __ballot_sync(0xffffffffu, in0), m1 = __ballot_sync(0xffffffffu, in1);
+      auto has = [&](int key) {
+        const int b = key >> log2_slots;
+        return ((b < 32 ? m0 : m1) >> (b & 31)) & 1u;
+      };
+      const uint32_t g0 = __ballot_sync(0xffffffffu, has(lane)), g1 = __ballot_sync(0xffffffffu, has(32 + lane));
+      if (lane == 0) {
+        sm.pf.good[slot][0] = g0;
+        sm.pf.good[slot][1] = g1;
+        mbar_arrive_expect_tx(&sm.raw_full[slot], (__popc(m0) + __popc(m1)) * bytes);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int b = lane + 32 * u, key = it.kv0 + kKv4RawKeys * st + (b << log2_slots);
+        if (u ? in1 : in0)
+          bulk_load(&sm.pf.raw[slot][b * bytes],
+                    head + id[u] * kp.page_stride + int64_t((key & (kc.page_size - 1)) >> log2_slots) * bytes, bytes,
+                    &sm.raw_full[slot]);
+      }
+    }
+  }
+  // every copy has landed before the CTA moves on
+  if (lane == 0)
+    for (uint32_t x = n > kKv4RawStages ? n - kKv4RawStages : 0; x < n; ++x)
+      mbar_wait_drain(&sm.raw_full[x % kKv4RawStages], (x / kKv4RawStages) & 1);
+  __syncwarp();
+}
+
+// One row of 64 bytes of codes to 256 bytes of fp16 in row r of a tile.
+__device__ __forceinline__ void kv4_widen(const uint8_t* row, uint32_t word, bool good, uint16_t (*tile)[kTileN][64],
+                                          int r) {
+  const int lane = threadIdx.x & 31;
+  // any bytes: a finite scale
+  const uint32_t bits = good ? min(word & 0xFFF0u, uint32_t(kKv4MaxScaleBits)) : 0u, z = word & 15u;
+  auto twice = [](uint32_t x) {
+    x |= x << 16;
+    return *reinterpret_cast<const __half2*>(&x);
+  };
+  const __half2 s = twice(bits), z0 = twice(0x6400u + z), z1 = twice(0x5400u + (z << 4));
+  auto value = [&](uint32_t codes, __half2 zero) {
+    const __half2 x = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&codes), zero), s);
+    return *reinterpret_cast<const uint32_t*>(&x);
+  };
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int quarter = (u + (lane >> 1)) & 3;
+    const uint4 c = *reinterpret_cast<const uint4*>(row + 16 * quarter);
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+    uint16_t* const dst = tile[quarter >> 1][r];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t h = w[e] >> 8;
+      uint4 out;
+      out.x = value((w[e] & 0x000F000Fu) | 0x64006400u, z0);
+      out.y = value((w[e] & 0x00F000F0u) | 0x54005400u, z1);
+      out.z = value((h & 0x000F000Fu) | 0x64006400u, z0);
+      out.w = value((h & 0x00F000F0u) | 0x54005400u, z1);
+      const int chunk = (4 * quarter + e) & 7;
+      *reinterpret_cast<uint4*>(dst + 8 * (chunk ^ (r & 7))) = out;
+    }
+  }
+}
+
+// Q, K and V tiles of items [b0, b1): thread = row of Q, key of a tile.
+template <typename T, int kB, typename Smem>
+__device__ void kv4_pf_widen(const Kv4Params& kp, Smem& sm, int32_t b0, int32_t b1, int32_t off_items) {
+  const RunParams& p = kp.run;
+  const int r = threadIdx.x - 32 * kKv4QuantWarp0, lane = threadIdx.x & 31, half = r / kKv4RawKeys;
+  const int slots = kB ? kB : kp.block_slots, log2_slots = kB == 32 ? 5 : kB == 16 ? 4 : kp.log2_block;
+  const int bytes = kB ? kv4_block_bytes(kB) : kp.block_bytes;
+  const int key = r % kKv4RawKeys, place = key & (slots - 1), block = (key >> log2_slots) * bytes;
+  const int G = p.group;
+  uint32_t kt = 0, pe = 0;
+  for (int32_t i = b0; i < b1; ++i) {
+    const Item it = load_item(p.iws, off_items, i);
+    const int ntiles = item_kv_tiles(it);
+    if (ntiles == 0) continue;
+    if (!warp_wait(&sm.q_empty, (pe & 1) ^ 1, &sm.abort)) return;
+    for (int m = 0; m < item_m_tiles(it); ++m) {
+      const int row = it.row0 + m * kTileM + r;
+      const bool there = row < it.row1;
+      const int tok = row / G;
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + (int64_t(it.rq.qo_start) + tok) * p.q_stride_tok +
+                                                        int64_t(it.hk * G + row - tok * G) * p.q_stride_head);
+      float top = 0.f;
+      if (there)
+#pragma unroll 8
+        for (int c = 0; c < 16; ++c) {
+          float f[8];
+          unpack8<T>(__ldg(src + c), f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
+        }
+      // a power of two that brings the row's largest value into [2^14, 2^15)
+      const int ex = min(max(int(__float_as_uint(top) >> 23) - 127, -100), 100);
+      const float up = __int_as_float((127 + 14 - ex) << 23);
+      sm.pf.q_scale[pe & 1][m * kTileM + r] = p.scale_log2 * __int_as_float((127 - 14 + ex) << 23);
+#pragma unroll 4
+      for (int c = 0; c < 16; ++c) {
+        float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (there) unpack8<T>(__ldg(src + c), f);
+        uint4 out;
+        out.x = tc::pack2<__half>(f[0] * up, f[4] * up);
+        out.y = tc::pack2<__half>(f[1] * up, f[5] * up);
+        out.z = tc::pack2<__half>(f[2] * up, f[6] * up);
+        out.w = tc::pack2<__half>(f[3] * up, f[7] * up);
+        *reinterpret_cast<uint4*>(&sm.pf.q[m][c >> 3][r][8 * ((c & 7) ^ (r & 7))]) = out;
+      }
+    }
+    fence_proxy_async_smem();  // read by the tensor core
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.q_full);
+    ++pe;
+    for (int j = 0; j < ntiles; ++j, ++kt) {
+      const int st = kt & 1;
+      const uint32_t ph = (kt >> 1) & 1, n = 2 * kt + half, slot = n % kKv4RawStages;
+      if (!warp_wait_all(2, &sm.raw_full[slot], (n / kKv4RawStages) & 1, &sm.k_empty[st], ph ^ 1, nullptr, 0, nullptr, 0,
+                         &sm.abort))
+        return;
+      const uint8_t* raw = sm.pf.raw[slot] + block;
+      const bool good = sm.pf.good[slot][key >> 5] >> (key & 31) & 1u;
+      const uint32_t kw = *reinterpret_cast<const uint16_t*>(raw + kv4_k_word(slots, place));
+      const uint32_t vw = *reinterpret_cast<const uint16_t*>(raw + kv4_v_word(slots, place));
+      kv4_widen(raw + kv4_k_row(slots, place), kw, good, sm.pf.k[st], r);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.k_full[st]);
+      if (!warp_wait(&sm.v_empty[st], ph ^ 1, &sm.abort)) return;
+      kv4_widen(raw + kv4_v_row(slots, place), vw, good, sm.pf.v[st], r);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&sm.v_full[st]);
+        mbar_arrive(&sm.raw_empty[slot]);
+      }
+    }
+  }
+}
+
+// The softmax of the M tiles (see pf_softmax): thread = row = TMEM lane.
+template <typename T, bool kMask, typename Smem>
+__device__ void kv4_pf_softmax(const RunParams& p, Smem& sm, int32_t b0, int32_t b1, int32_t off_items,
+                               int32_t off_merge, int32_t off_cnt, int causal, const Variant var) {
+  const int sw = (threadIdx.x >> 5) - kKv4SoftmaxWarp0, mt = sw >> 2, w = sw & 3, lane = threadIdx.x & 31;
+  const int r = 32 * w + lane, tid = mt * kTileM + r;
+  const uint32_t tl = sm.tmem_base + (uint32_t(32 * w) << 16);
+  const uint32_t s_cols = tl + mt * kTileN, o_cols = tl + kTmemO + mt * kHeadDim;
+  const int G = p.group;
+  uint32_t tiles = 0, items = 0, seq = 0;  // phases of s_full[mt] and o_ready[mt]; items with keys
+  for (int32_t i = b0; i < b1; ++i) {
+    const Item item = load_item(p.iws, off_items, i);
+    const Request& rq = item.rq;
+    const int nrows = item.row1 - item.row0;
+    const int ntiles = item_kv_tiles(item);
+    const int prow = mt * kTileM + r;  // packed row within the item
+    if (mt < item_m_tiles(item)) {
+      int lim = -1, lo = 0;  // visible keys of this row: [lo, lim] and the sink (lim -1: padding row)
+      if (prow < nrows) {
+        const int pos = rq.kv_len - rq.qo_len + (item.row0 + prow) / G;
+        lim = min(causal ? pos : rq.kv_len - 1, item.kv1 - 1);
+        if (kMask) lo = window_low(var, pos);
+      }
+      // lrun: sum of the fp32 P (for LSE); lrun_r: of the fp16 P that the product takes (for O)
+      float mrun = -INFINITY, lrun = 0.f, lrun_r = 0.f, c = 0.f;
+      bool ok = true;
+      for (int j = 0; j < ntiles; ++j) {
+        ok = ok && warp_wait(&sm.s_full[mt], tiles & 1, &sm.abort);
+        ++tiles;
+        if (!ok) continue;
+        tc::fence_after_sync();
+        if (j == 0) c = sm.pf.q_scale[seq & 1][prow];
+        uint32_t sv[4][32];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) tc::tmem_ld32(s_cols + 32 * h, sv[h]);
+        tc::tmem_ld_wait();
+        const int kbase = item.kv0 + j * kTileN;
+        if (kbase + kTileN - 1 > lim || (kMask && kbase < lo)) {  // causal diagonal, chunk end, padding row, window
+#pragma unroll
+          for (int h = 0; h < 4; ++h)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const int key = kbase + 32 * h + e;
+              if (key > lim || (kMask && key < lo && key >= var.sink)) sv[h][e] = 0xff800000u;  // -inf
+            }
+        }
+        // row max in eight independent chains of three-input maxima
+        auto sval = [&](int e) { return __uint_as_float(sv[e >> 5][e & 31]); };
+        float mx8[8];
+#pragma unroll
+        for (int a = 0; a < 8; ++a) mx8[a] = sval(a);
+#pragma unroll
+        for (int e = 8; e + 16 <= kTileN; e += 16)
+#pragma unroll
+          for (int a = 0; a < 8; ++a) mx8[a] = max3(mx8[a], sval(e + a), sval(e + 8 + a));
+#pragma unroll
+        for (int a = 0; a < 8; ++a) mx8[a] = fmaxf(mx8[a], sval(kTileN - 8 + a));
+        const float mx = max3(max3(mx8[0], mx8[1], mx8[2]), max3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])) * c;
+        const float m_old = mrun;
+        const float m_new = (mx > m_old + kLazyRescale) ? mx : m_old;
+        const bool rescale = (m_new != m_old) && j > 0;
+        if (__any_sync(0xffffffffu, rescale)) {
+          // O holds P V of every earlier tile (covered by this S's commit)
+          const float alpha = rescale ? ex2(m_old - m_new) : 1.f;
+#pragma unroll 1
+          for (int h = 0; h < 4; ++h) {
+            uint32_t ov[32];
+            tc::tmem_ld32(o_cols + 32 * h, ov);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+            tc::tmem_st32(o_cols + 32 * h, ov);
+          }
+          tc::tmem_st_wait();
+          if (rescale) {
+            lrun *= alpha;
+            lrun_r *= alpha;
+          }
+        }
+        // P = 2^(s c - m) as fp16 pairs over the first 64 columns of the S
+        // buffer, published in two halves of 64 keys each
+        const float msub = (m_new == -INFINITY) ? 0.f : m_new;
+        const float2 cc = make_float2(c, c), nms = make_float2(-msub, -msub);
+        float2 sum4[4], sumr[2];
+#pragma unroll
+        for (int a = 0; a < 4; ++a) sum4[a] = make_float2(0.f, 0.f);
+        sumr[0] = sumr[1] = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+          for (int h = 2 * half; h < 2 * half + 2; ++h) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float2 x =
+                  fma2(make_float2(__uint_as_float(sv[h][2 * e]), __uint_as_float(sv[h][2 * e + 1])), cc, nms);
+              const float2 pe = make_float2(ex2(x.x), ex2(x.y));
+              sum4[e & 3] = add2(sum4[e & 3], pe);
+              pk[e] = tc::pack2<__half>(pe.x, pe.y);
+              tc::add_packed2<__half>(sumr[e & 1], pk[e]);
+            }
+            tc::tmem_st16(s_cols + 16 * h, pk);
+          }
+          tc::tmem_st_wait();
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.p_full[mt][half]);
+        }
+        const float2 s01 = add2(sum4[0], sum4[1]), s23 = add2(sum4[2], sum4[3]), s4 = add2(s01, s23);
+        lrun += s4.x + s4.y;
+        const float2 sr = add2(sumr[0], sumr[1]);
+        lrun_r += sr.x + sr.y;
+        mrun = m_new;
+      }
+      bool have_o = false;
+      if (ntiles > 0) {
+        ok = ok && warp_wait(&sm.o_ready[mt], items & 1, &sm.abort);
+        ++items;
+        have_o = ok;
+      }
+      uint32_t ov[4][32];
+      if (have_o) {
+        tc::fence_after_sync();
+#pragma unroll
+        for (int h = 0; h < 4; ++h) tc::tmem_ld32(o_cols + 32 * h, ov[h]);
+        tc::tmem_ld_wait();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.o_free[mt]);
+      } else {
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) ov[h][e] = 0u;
+      }
+      if (prow < nrows && !sm.abort) {
+        const int row = item.row0 + prow, t = row / G, head = item.hk * G + (row - t * G);
+        const int64_t tok = int64_t(rq.qo_start) + t;
+        const float inv = lrun_r > 0.f ? 1.f / lrun_r : 0.f;
+        const float lse = lrun > 0.f ? (mrun + __log2f(lrun)) * 0.69314718055994531f : -INFINITY;
+        // dim d of each eight lies in column 2 d (d < 4) or 2 d - 7
+        auto dim = [&](int h, int e0, int d) { return __uint_as_float(ov[h][e0 + (d < 4 ? 2 * d : 2 * d - 7)]) * inv; };
+        if (item.part < 0) {
+          uint4* dst = reinterpret_cast<uint4*>(p.o + tok * p.o_stride_tok + int64_t(head) * p.o_stride_head);
+#pragma unroll
+          for (int h = 0; h < 4; ++h)
+#pragma unroll
+            for (int e = 0; e < 32; e += 8)
+              dst[4 * h + e / 8] = make_uint4(tc::pack2<T>(dim(h, e, 0), dim(h, e, 1)), tc::pack2<T>(dim(h, e, 2), dim(h, e, 3)),
+                                              tc::pack2<T>(dim(h, e, 4), dim(h, e, 5)), tc::pack2<T>(dim(h, e, 6), dim(h, e, 7)));
+          if (p.lse) p.lse[tok * p.num_qo_heads + head] = lse;
+        } else {
+          const int64_t part = int64_t(item.part) + prow;
+          float4* dst = reinterpret_cast<float4*>(p.fws + p.partial_o_offset + part * kHeadDim);
+#pragma unroll
+          for (int h = 0; h < 4; ++h)
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              dst[8 * h + e / 4] = make_float4(dim(h, e, 0), dim(h, e, 1), dim(h, e, 2), dim(h, e, 3));
+              dst[8 * h + e / 4 + 1] = make_float4(dim(h, e, 4), dim(h, e, 5), dim(h, e, 6), dim(h, e, 7));
+            }
+          p.fws[part] = lse;
+        }
+      }
+    }
+    if (ntiles > 0) ++seq;
+    if (item.merge >= 0)
+      merge_split_unit<T>(p, item, rq, off_merge, off_cnt, tid, kSoftmaxThreads, 2, &sm.merge_last_pf, sm.abort);
+  }
+}
+
+}  // namespace fi

@@ -239,8 +239,10 @@ __device__ __noinline__ void pf_rope(const RunParams& p, RunSmem& sm, int32_t b0
   if (f16x2_has_inf(amax)) atomicOr(p.iws + FI_H_STATUS, kStatusRange);
 }
 
-template <typename T, bool kRope>
-__device__ void pf_mma(const RunParams& p, RunSmem& sm, int32_t b0, int32_t b1, int32_t off_items) {
+// Smem: the run's shared memory, or another kernel's with the same operand tiles
+// and barriers.
+template <typename T, bool kRope, typename Smem = RunSmem>
+__device__ void pf_mma(const RunParams& p, Smem& sm, int32_t b0, int32_t b1, int32_t off_items) {
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   // rotated Q and K (RoPE, in the kernel or by a pass before it) are fp16
   // whatever the input type; P and V keep it
@@ -289,9 +291,14 @@ __device__ void pf_mma(const RunParams& p, RunSmem& sm, int32_t b0, int32_t b1, 
     const int nm = item_m_tiles(it);
     // with RoPE the operands are read once the rotation warp has released them
     // (operands rotated by a pass before the run arrive ready: the plain waits)
-    const bool rot_roles = kRope && !p.qk_prerotated;
-    uint64_t* const q_bar = rot_roles ? &sm.q_rot : &sm.q_full;
-    uint64_t* const k_bars = rot_roles ? sm.k_rot : sm.k_full;
+    uint64_t* q_bar = &sm.q_full;
+    uint64_t* k_bars = sm.k_full;
+    if constexpr (kRope) {
+      if (!p.qk_prerotated) {
+        q_bar = &sm.q_rot;
+        k_bars = sm.k_rot;
+      }
+    }
     bool ok = warp_wait_all(2, q_bar, pe & 1, &k_bars[kt & 1], (kt >> 1) & 1, nullptr, 0, nullptr, 0, &sm.abort);
     if (!ok) break;
     tc::fence_after_sync();
