@@ -10,6 +10,13 @@
 #include "kv4_params.h"
 #include "rotary.h"
 
+namespace fi {
+
+bool make_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, int rank, const uint64_t* dims,
+              const int64_t* strides_elems, const uint32_t* box, CUtensorMapSwizzle swizzle);  // attention.cu
+
+}  // namespace fi
+
 using namespace fi;
 
 namespace {
@@ -72,6 +79,15 @@ extern "C" fi_status fi_batch_paged_attention_run_kv4(const fi_kv4_args* a, void
   kp.block_slots = kv4_block_slots(info->page_size);
   while ((1 << kp.log2_block) < kp.block_slots) ++kp.log2_block;
   kp.block_bytes = kv4_block_bytes(kp.block_slots);
+  kc.tc = kTileM % p.group == 0 ? 1 : 0;  // tiles of whole tokens: Q by boxes
+  if (kc.tc) {
+    const uint64_t qd[3] = {uint64_t(kHeadDim), uint64_t(info->num_qo_heads), uint64_t(a->q_num_tokens)};
+    const int64_t qs[2] = {a->q_stride_head, a->q_stride_tok};
+    const uint32_t qb[3] = {64u, uint32_t(p.group), uint32_t(kTileM / p.group)};
+    if (!make_map(&p.tm_q, a->dtype == FI_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a->q, 3,
+                  qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B))
+      return FI_ERR_UNSUPPORTED;
+  }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = a->dtype == FI_BF16 ? launch_kv4<__nv_bfloat16>(kp, info->num_ctas, s)
                                       : launch_kv4<__half>(kp, info->num_ctas, s);

@@ -48,7 +48,7 @@ constexpr int kKv4Barrier = 8;         // named barriers: of all computing warps
 // Registers per thread and warpgroup; each phase's sum is the launch's.
 constexpr int kKv4RegsLaunch = 128;
 constexpr int kKv4RegsDecode0 = 56, kKv4RegsDecode = 152;
-constexpr int kKv4RegsMma = 80, kKv4RegsWiden = 64, kKv4RegsSoftmax = 184;
+constexpr int kKv4RegsMma = 88, kKv4RegsWiden = 72, kKv4RegsSoftmax = 176;
 static_assert(kKv4RegsDecode0 + 3 * kKv4RegsDecode <= 4 * kKv4RegsLaunch, "register split exceeds the launch");
 static_assert(kKv4RegsMma + kKv4RegsWiden + 2 * kKv4RegsSoftmax <= 4 * kKv4RegsLaunch,
               "register split exceeds the launch");
@@ -68,6 +68,7 @@ struct alignas(1024) Kv4Smem {
   };
   uint64_t full[kKv4Warps][kKv4Depth], empty[kKv4Warps][kKv4Depth];
   uint64_t raw_full[kKv4RawStages], raw_empty[kKv4RawStages];
+  uint64_t q_raw;                   // Q's rows have landed as they are
   uint64_t q_full, q_empty, drain;  // these and the next as in RunSmem
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t s_full[2], o_ready[2], o_free[2], p_full[2][2];
@@ -771,9 +772,10 @@ __global__ void __launch_bounds__(kKv4Threads, 1) kv4_attention_kernel(const __g
   if (threadIdx.x == kKv4Warps * kKv4Depth) {
     for (int s = 0; s < kKv4RawStages; ++s) {
       mbar_init(&sm.raw_full[s], 1);
-      mbar_init(&sm.raw_empty[s], kKv4QuantWarps / 2);  // the two warps of a stage's keys
+      mbar_init(&sm.raw_empty[s], kKv4QuantWarps / kKv4RawStages);  // the warps of a stage's keys
     }
-    mbar_init(&sm.q_full, kKv4QuantWarps);
+    mbar_init(&sm.q_full, 2 + kKv4QuantWarps);  // every warp that turns rows of it
+    mbar_init(&sm.q_raw, kp.run.kv[0].tc ? 1 : 2);  // its load, or the warps that copy it
     mbar_init(&sm.q_empty, 1);
     mbar_init(&sm.drain, 1);
     for (int s = 0; s < 2; ++s) {
@@ -811,6 +813,9 @@ __global__ void __launch_bounds__(kKv4Threads, 1) kv4_attention_kernel(const __g
         kv4_pf_load<kB>(kp, sm, begin, mid, off_items);
       } else if (warp == kMmaWarp) {
         pf_mma<__half, false>(p, sm, begin, mid, off_items);
+        __syncwarp();
+      } else {
+        kv4_pf_queries<T>(kp, sm, warp - 2, begin, mid, off_items);
         __syncwarp();
       }
       fence_proxy_async_smem();  // the second phase's copies go where these tiles were

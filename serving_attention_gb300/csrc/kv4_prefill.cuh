@@ -5,21 +5,25 @@
 // to two 128-row M tiles against 128-key tiles, S = Q K^T into tensor memory, P
 // over it as 16-bit pairs, O += P V.  What differs is where the operands come
 // from.  A value s (n - z) has seven significant bits of s times four of n - z:
-// eleven, an fp16 as it stands (fi_kv4.h), so K and V tiles are fp16 whatever the
-// type of q, and exact; a q row is brought into fp16 by a power of two of its
-// own, which its softmax takes back.
+// eleven, an fp16 as it stands (fi_kv4.h), so K and V tiles are exact fp16 tiles;
+// a bf16 row of Q is brought into fp16 by a power of two of its own, which its
+// softmax takes back.  (K as n - z in bf16 beside Q as it is, each key's s
+// multiplied to its column of S, was slower: the widening, whose warps are the
+// busiest, doubled for K.)
 //
-//  * warp 0 brings the pages' blocks, 64 keys a stage, into a ring of three raw
-//    stages (a bulk copy a block, page ids a stage ahead);
+//  * warp 0 brings the pages' blocks, 64 keys a stage, a raw stage for each half
+//    of a tile (a bulk copy a block, page ids a stage ahead);
 //  * warps 4 .. 7 are the 128 keys of a tile: a thread has its key's scale and
-//    zero point in registers and turns two rows of 64 bytes into 256 bytes each,
-//    in the 128-byte swizzle that the products read: for eight codes one shift,
-//    four (x & m) | c (1024 + n and 64 + n as fp16), four subtractions of the
-//    same with z and four products with s.  The codes come out in the order 0, 4,
-//    1, 5, 2, 6, 3, 7 of each eight dims; Q is laid out in it too, and the output
-//    is put right where it is stored.  Q's rows are theirs as well, at an item's
-//    start.  Reads and writes of a quarter warp meet no bank twice: lane l starts
-//    with quarter l / 2 of its row.
+//    zero point in registers and turns its two rows of 64 bytes into 256 bytes
+//    each, in the 128-byte swizzle that the products read: for eight codes one
+//    shift, four (x & m) | c (1024 + n and 64 + n as fp16), four subtractions of
+//    the same with z, four products with s.  The codes come out in the order 0, 4,
+//    1, 5, 2, 6, 3, 7 of each eight dims; Q's rows are put in it too, and the
+//    output right where it is stored.  Reads and writes of a quarter warp meet no
+//    bank twice: lane l starts with quarter l / 2 of its row;
+//  * warp 2 loads Q (one TMA box a 64-dim half of an M tile where the group
+//    divides 128, else warps 2 and 3 copy its rows), and warps 4 .. 7 turn the rows
+//    of M tile A, warps 2 and 3 those of B, a thread a row, in place;
 //  * warp 1 issues the products (pf_mma), warps 8 .. 15 the softmax.
 #pragma once
 #include "kv4_params.h"
@@ -29,7 +33,7 @@
 namespace fi {
 
 constexpr int kKv4RawKeys = 64;     // keys of a raw stage
-constexpr int kKv4RawStages = 3;
+constexpr int kKv4RawStages = kTileN / kKv4RawKeys;  // a stage's readers are the same two warps, tile after tile
 constexpr int kKv4RawBytes = 9216;  // 64 blocks of one slot, 144 bytes each
 constexpr int kKv4QuantWarp0 = 4, kKv4QuantWarps = 4;
 constexpr int kKv4SoftmaxWarp0 = 8;
@@ -70,7 +74,7 @@ __device__ void kv4_pf_load(const Kv4Params& kp, Smem& sm, int32_t b0, int32_t b
     };
     if (stages > 0) fetch(0);
     for (int st = 0; st < stages; ++st, ++n) {
-      const int slot = n % kKv4RawStages;
+      const int slot = n % kKv4RawStages;  // the half of the tile
       const int32_t id[2] = {next[0], next[1]};
       if (st + 1 < stages) fetch(st + 1);
       ok = warp_wait(&sm.raw_empty[slot], ((n / kKv4RawStages) & 1) ^ 1, &sm.abort);
@@ -105,17 +109,16 @@ __device__ void kv4_pf_load(const Kv4Params& kp, Smem& sm, int32_t b0, int32_t b
   __syncwarp();
 }
 
-// One row of 64 bytes of codes to 256 bytes of fp16 in row r of a tile.
-__device__ __forceinline__ void kv4_widen(const uint8_t* row, uint32_t word, bool good, uint16_t (*tile)[kTileN][64],
+// One row of 64 bytes of codes (c[u]: quarter u + lane / 2 modulo 4) to 256 bytes
+// of fp16 in row r of a tile.
+__device__ __forceinline__ void kv4_widen(const uint4 (&c)[4], uint32_t scale, uint32_t z, uint16_t (*tile)[kTileN][64],
                                           int r) {
   const int lane = threadIdx.x & 31;
-  // any bytes: a finite scale
-  const uint32_t bits = good ? min(word & 0xFFF0u, uint32_t(kKv4MaxScaleBits)) : 0u, z = word & 15u;
   auto twice = [](uint32_t x) {
     x |= x << 16;
     return *reinterpret_cast<const __half2*>(&x);
   };
-  const __half2 s = twice(bits), z0 = twice(0x6400u + z), z1 = twice(0x5400u + (z << 4));
+  const __half2 s = twice(scale), z0 = twice(0x6400u + z), z1 = twice(0x5400u + (z << 4));
   auto value = [&](uint32_t codes, __half2 zero) {
     const __half2 x = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&codes), zero), s);
     return *reinterpret_cast<const uint32_t*>(&x);
@@ -123,97 +126,167 @@ __device__ __forceinline__ void kv4_widen(const uint8_t* row, uint32_t word, boo
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const int quarter = (u + (lane >> 1)) & 3;
-    const uint4 c = *reinterpret_cast<const uint4*>(row + 16 * quarter);
-    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+    const uint32_t w[4] = {c[u].x, c[u].y, c[u].z, c[u].w};
     uint16_t* const dst = tile[quarter >> 1][r];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const uint32_t h = w[e] >> 8;
-      uint4 out;
-      out.x = value((w[e] & 0x000F000Fu) | 0x64006400u, z0);
-      out.y = value((w[e] & 0x00F000F0u) | 0x54005400u, z1);
-      out.z = value((h & 0x000F000Fu) | 0x64006400u, z0);
-      out.w = value((h & 0x00F000F0u) | 0x54005400u, z1);
+      const uint4 out = make_uint4(value((w[e] & 0x000F000Fu) | 0x64006400u, z0), value((w[e] & 0x00F000F0u) | 0x54005400u, z1),
+                                   value((h & 0x000F000Fu) | 0x64006400u, z0), value((h & 0x00F000F0u) | 0x54005400u, z1));
       const int chunk = (4 * quarter + e) & 7;
       *reinterpret_cast<uint4*>(dst + 8 * (chunk ^ (r & 7))) = out;
     }
   }
 }
 
-// Q, K and V tiles of items [b0, b1): thread = row of Q, key of a tile.
+// Row r of an M tile in place: the dims of each eight in the order 0, 4, 1, 5, ..,
+// and a bf16 row times a power of two that brings its largest value into [2^14,
+// 2^15), as fp16; returns the factor that takes it back.
+template <typename T>
+__device__ __forceinline__ float kv4_turn_query(uint16_t (*tile)[kTileM][64], int r) {
+  constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  float up = 1.f, back = 1.f;
+  if constexpr (kBf16) {
+    constexpr uint32_t kAbs = 0x7FFF7FFFu;
+    auto larger = [](uint32_t a, uint32_t b) {
+      const __nv_bfloat162 m =
+          __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+      return *reinterpret_cast<const uint32_t*>(&m);
+    };
+    uint32_t top = 0;
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {  // chunk order does not matter: c ^ r is every chunk once
+      const uint4 u = *reinterpret_cast<const uint4*>(tile[c >> 3][r] + 8 * ((c & 7) ^ (r & 7)));
+      top = larger(top, larger(larger(u.x & kAbs, u.y & kAbs), larger(u.z & kAbs, u.w & kAbs)));
+    }
+    top = larger(top, top >> 16);
+    const int ex = min(max(int(top >> 7 & 0xFF) - 127, -100), 100);
+    up = __int_as_float((127 + 14 - ex) << 23);
+    back = __int_as_float((127 - 14 + ex) << 23);
+  }
+#pragma unroll 4
+  for (int c = 0; c < 16; ++c) {
+    uint4* const at = reinterpret_cast<uint4*>(tile[c >> 3][r] + 8 * ((c & 7) ^ (r & 7)));
+    const uint4 u = *at;
+    if constexpr (kBf16) {
+      float f[8];
+      unpack8<T>(u, f);
+      *at = make_uint4(tc::pack2<__half>(f[0] * up, f[4] * up), tc::pack2<__half>(f[1] * up, f[5] * up),
+                       tc::pack2<__half>(f[2] * up, f[6] * up), tc::pack2<__half>(f[3] * up, f[7] * up));
+    } else {
+      *at = make_uint4(__byte_perm(u.x, u.z, 0x5410), __byte_perm(u.x, u.z, 0x7632), __byte_perm(u.y, u.w, 0x5410),
+                       __byte_perm(u.y, u.w, 0x7632));
+    }
+  }
+  return back;
+}
+
+// K and V tiles of items [b0, b1), thread = key of a tile; and M tile A's rows.
 template <typename T, int kB, typename Smem>
 __device__ void kv4_pf_widen(const Kv4Params& kp, Smem& sm, int32_t b0, int32_t b1, int32_t off_items) {
-  const RunParams& p = kp.run;
   const int r = threadIdx.x - 32 * kKv4QuantWarp0, lane = threadIdx.x & 31, half = r / kKv4RawKeys;
   const int slots = kB ? kB : kp.block_slots, log2_slots = kB == 32 ? 5 : kB == 16 ? 4 : kp.log2_block;
   const int bytes = kB ? kv4_block_bytes(kB) : kp.block_bytes;
-  const int key = r % kKv4RawKeys, place = key & (slots - 1), block = (key >> log2_slots) * bytes;
-  const int G = p.group;
+  const int key = r % kKv4RawKeys, place = key & (slots - 1);
+  const uint8_t* const raw = sm.pf.raw[half] + (key >> log2_slots) * bytes;
   uint32_t kt = 0, pe = 0;
   for (int32_t i = b0; i < b1; ++i) {
-    const Item it = load_item(p.iws, off_items, i);
+    const Item it = load_item(kp.run.iws, off_items, i);
     const int ntiles = item_kv_tiles(it);
-    if (ntiles == 0) continue;
-    if (!warp_wait(&sm.q_empty, (pe & 1) ^ 1, &sm.abort)) return;
-    for (int m = 0; m < item_m_tiles(it); ++m) {
-      const int row = it.row0 + m * kTileM + r;
-      const bool there = row < it.row1;
-      const int tok = row / G;
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + (int64_t(it.rq.qo_start) + tok) * p.q_stride_tok +
-                                                        int64_t(it.hk * G + row - tok * G) * p.q_stride_head);
-      float top = 0.f;
-      if (there)
-#pragma unroll 8
-        for (int c = 0; c < 16; ++c) {
-          float f[8];
-          unpack8<T>(__ldg(src + c), f);
+    for (int j = 0; j < ntiles; ++j, ++kt) {
+      const int st = kt & 1;
+      const uint32_t ph = (kt >> 1) & 1;
+      if (!warp_wait_all(2, &sm.raw_full[half], kt & 1, &sm.k_empty[st], ph ^ 1, nullptr, 0, nullptr, 0, &sm.abort)) return;
+      // the words, with a finite scale whatever the bytes; 0 outside the cache
+      const uint32_t good = sm.pf.good[half][key >> 5] >> (key & 31) & 1u ? 0xFFF0u : 0u;
+      const uint32_t kw = *reinterpret_cast<const uint16_t*>(raw + kv4_k_word(slots, place));
+      const uint32_t vw = *reinterpret_cast<const uint16_t*>(raw + kv4_v_word(slots, place));
+      const uint32_t ks = min(kw & good, uint32_t(kKv4MaxScaleBits)), vs = min(vw & good, uint32_t(kKv4MaxScaleBits));
+      uint4 c[4];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
-        }
-      // a power of two that brings the row's largest value into [2^14, 2^15)
-      const int ex = min(max(int(__float_as_uint(top) >> 23) - 127, -100), 100);
-      const float up = __int_as_float((127 + 14 - ex) << 23);
-      sm.pf.q_scale[pe & 1][m * kTileM + r] = p.scale_log2 * __int_as_float((127 - 14 + ex) << 23);
-#pragma unroll 4
-      for (int c = 0; c < 16; ++c) {
-        float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (there) unpack8<T>(__ldg(src + c), f);
-        uint4 out;
-        out.x = tc::pack2<__half>(f[0] * up, f[4] * up);
-        out.y = tc::pack2<__half>(f[1] * up, f[5] * up);
-        out.z = tc::pack2<__half>(f[2] * up, f[6] * up);
-        out.w = tc::pack2<__half>(f[3] * up, f[7] * up);
-        *reinterpret_cast<uint4*>(&sm.pf.q[m][c >> 3][r][8 * ((c & 7) ^ (r & 7))]) = out;
+      for (int u = 0; u < 4; ++u)
+        c[u] = *reinterpret_cast<const uint4*>(raw + kv4_k_row(slots, place) + 16 * ((u + (lane >> 1)) & 3));
+      kv4_widen(c, ks, kw & 15u, sm.pf.k[st], r);
+      fence_proxy_async_smem();  // read by the tensor core
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.k_full[st]);
+      // V's row is read before its tile is free, and the raw stage handed back
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        c[u] = *reinterpret_cast<const uint4*>(raw + kv4_v_row(slots, place) + 16 * ((u + (lane >> 1)) & 3));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.raw_empty[half]);
+      if (j == 0) {
+        if (!warp_wait(&sm.q_raw, pe & 1, &sm.abort)) return;
+        const float back = kv4_turn_query<T>(sm.pf.q[0], r);
+        sm.pf.q_scale[pe & 1][r] = kp.run.scale_log2 * back;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.q_full);
+        ++pe;
       }
+      if (!warp_wait(&sm.v_empty[st], ph ^ 1, &sm.abort)) return;
+      kv4_widen(c, vs, vw & 15u, sm.pf.v[st], r);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.v_full[st]);
     }
+  }
+}
+
+// Q of items [b0, b1) by warps 2 and 3 (which = 0, 1): its load, and M tile B's rows.
+template <typename T, typename Smem>
+__device__ void kv4_pf_queries(const Kv4Params& kp, Smem& sm, int which, int32_t b0, int32_t b1, int32_t off_items) {
+  const RunParams& p = kp.run;
+  const int lane = threadIdx.x & 31, c = lane & 15, G = p.group;
+  const bool boxes = p.kv[0].tc != 0;
+  uint32_t pe = 0;
+  int armed = -1;  // parity of the last load
+  for (int32_t i = b0; i < b1; ++i) {
+    const Item it = load_item(p.iws, off_items, i);
+    if (item_kv_tiles(it) == 0) continue;
+    const int nrows = it.row1 - it.row0, nm = item_m_tiles(it);
+    bool ok = warp_wait(&sm.q_empty, (pe & 1) ^ 1, &sm.abort);
+    if (!ok) break;
+    if (boxes) {
+      if (which == 0) {
+        if (lane == 0) {
+          fence_proxy_async_smem();
+          mbar_arrive_expect_tx(&sm.q_raw, nm * kQTileBytes);
+          for (int m = 0; m < nm; ++m) {
+            const int c1 = it.hk * G, c2 = it.rq.qo_start + (it.row0 + m * kTileM) / G;
+            tc::tma_load_3d(&sm.pf.q[m][0][0][0], &p.tm_q, &sm.q_raw, 0, c1, c2);
+            tc::tma_load_3d(&sm.pf.q[m][1][0][0], &p.tm_q, &sm.q_raw, 64, c1, c2);
+          }
+        }
+        armed = pe & 1;
+      }
+    } else {
+      const int first = it.row0 + 2 * which + (lane >> 4);
+      int tok = first / G, g = first - tok * G;
+      for (int row = 2 * which + (lane >> 4); row < nm * kTileM; row += 4) {
+        const uint16_t* src = row < nrows ? p.q + (int64_t(it.rq.qo_start) + tok) * p.q_stride_tok +
+                                                int64_t(it.hk * G + g) * p.q_stride_head + 8 * c
+                                          : p.q;
+        cp_async_16(&sm.pf.q[row / kTileM][c >> 3][row % kTileM][8 * ((c & 7) ^ (row & 7))], src, row < nrows ? 16u : 0u);
+        for (g += 4; g >= G; g -= G) ++tok;
+      }
+      cp_async_wait_all();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.q_raw);
+    }
+    ok = warp_wait(&sm.q_raw, pe & 1, &sm.abort);
+    if (!ok) break;
+    if (nm == 2)
+      for (int r = 32 * which + lane; r < kTileM; r += 64)
+        sm.pf.q_scale[pe & 1][kTileM + r] = p.scale_log2 * kv4_turn_query<T>(sm.pf.q[1], r);
     fence_proxy_async_smem();  // read by the tensor core
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.q_full);
     ++pe;
-    for (int j = 0; j < ntiles; ++j, ++kt) {
-      const int st = kt & 1;
-      const uint32_t ph = (kt >> 1) & 1, n = 2 * kt + half, slot = n % kKv4RawStages;
-      if (!warp_wait_all(2, &sm.raw_full[slot], (n / kKv4RawStages) & 1, &sm.k_empty[st], ph ^ 1, nullptr, 0, nullptr, 0,
-                         &sm.abort))
-        return;
-      const uint8_t* raw = sm.pf.raw[slot] + block;
-      const bool good = sm.pf.good[slot][key >> 5] >> (key & 31) & 1u;
-      const uint32_t kw = *reinterpret_cast<const uint16_t*>(raw + kv4_k_word(slots, place));
-      const uint32_t vw = *reinterpret_cast<const uint16_t*>(raw + kv4_v_word(slots, place));
-      kv4_widen(raw + kv4_k_row(slots, place), kw, good, sm.pf.k[st], r);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.k_full[st]);
-      if (!warp_wait(&sm.v_empty[st], ph ^ 1, &sm.abort)) return;
-      kv4_widen(raw + kv4_v_row(slots, place), vw, good, sm.pf.v[st], r);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&sm.v_full[st]);
-        mbar_arrive(&sm.raw_empty[slot]);
-      }
-    }
   }
+  if (armed >= 0 && lane == 0) mbar_wait_drain(&sm.q_raw, armed);
+  __syncwarp();
 }
 
 // The softmax of the M tiles (see pf_softmax): thread = row = TMEM lane.
