@@ -109,10 +109,12 @@ __device__ void kv4_pf_load(const Kv4Params& kp, Smem& sm, int32_t b0, int32_t b
   __syncwarp();
 }
 
-// One row of 64 bytes of codes (c[u]: quarter u + lane / 2 modulo 4) to 256 bytes
-// of fp16 in row r of a tile.
-__device__ __forceinline__ void kv4_widen(const uint4 (&c)[4], uint32_t scale, uint32_t z, uint16_t (*tile)[kTileN][64],
-                                          int r) {
+// One row of 64 bytes of codes to 256 bytes of fp16 in row r of the tile at `tile`
+// (shared-memory address); c0 .. c3: quarters lane / 2 .. lane / 2 + 3 modulo 4.
+// A loop of one quarter: its warps share the instruction caches with the softmax's,
+// whose loop is long.
+__device__ __forceinline__ void kv4_widen(uint4 c0, uint4 c1, uint4 c2, uint4 c3, uint32_t scale, uint32_t z,
+                                          uint32_t tile, int r) {
   const int lane = threadIdx.x & 31;
   auto twice = [](uint32_t x) {
     x |= x << 16;
@@ -123,19 +125,24 @@ __device__ __forceinline__ void kv4_widen(const uint4 (&c)[4], uint32_t scale, u
     const __half2 x = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&codes), zero), s);
     return *reinterpret_cast<const uint32_t*>(&x);
   };
-#pragma unroll
+  const uint32_t row = tile + r * 128 + 16 * (r & 7);  // 16-byte chunk c of the row lies at 16 (c ^ r % 8)
+#pragma unroll 1
   for (int u = 0; u < 4; ++u) {
     const int quarter = (u + (lane >> 1)) & 3;
-    const uint32_t w[4] = {c[u].x, c[u].y, c[u].z, c[u].w};
-    uint16_t* const dst = tile[quarter >> 1][r];
+    const uint32_t w[4] = {c0.x, c0.y, c0.z, c0.w};
+    const uint32_t at = (row ^ (64 * (quarter & 1))) + (quarter >> 1) * (kTileN * 128);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const uint32_t h = w[e] >> 8;
       const uint4 out = make_uint4(value((w[e] & 0x000F000Fu) | 0x64006400u, z0), value((w[e] & 0x00F000F0u) | 0x54005400u, z1),
                                    value((h & 0x000F000Fu) | 0x64006400u, z0), value((h & 0x00F000F0u) | 0x54005400u, z1));
-      const int chunk = (4 * quarter + e) & 7;
-      *reinterpret_cast<uint4*>(dst + 8 * (chunk ^ (r & 7))) = out;
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ (16 * e)), "r"(out.x), "r"(out.y), "r"(out.z),
+                   "r"(out.w)
+                   : "memory");
     }
+    c0 = c1;
+    c1 = c2;
+    c2 = c3;
   }
 }
 
@@ -190,48 +197,59 @@ __device__ void kv4_pf_widen(const Kv4Params& kp, Smem& sm, int32_t b0, int32_t 
   const int key = r % kKv4RawKeys, place = key & (slots - 1);
   const uint8_t* const raw = sm.pf.raw[half] + (key >> log2_slots) * bytes;
   uint32_t kt = 0, pe = 0;
+  // K of a tile goes before V of the tile before: V's buffer comes free late (P V
+  // of the tile two before), and the products want the next K before they start
+  // on this P.  So a thread holds V's row, its scale and zero point of one tile.
+  uint4 v[4] = {};
+  uint32_t v_scale = 0, v_zero = 0;
+  auto put_v = [&](uint32_t t) {
+    if (!warp_wait(&sm.v_empty[t & 1], ((t >> 1) & 1) ^ 1, &sm.abort)) return false;
+    kv4_widen(v[0], v[1], v[2], v[3], v_scale, v_zero, smem_u32(sm.pf.v[t & 1]), r);
+    fence_proxy_async_smem();  // read by the tensor core
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.v_full[t & 1]);
+    return true;
+  };
   for (int32_t i = b0; i < b1; ++i) {
     const Item it = load_item(kp.run.iws, off_items, i);
     const int ntiles = item_kv_tiles(it);
     for (int j = 0; j < ntiles; ++j, ++kt) {
       const int st = kt & 1;
-      const uint32_t ph = (kt >> 1) & 1;
-      if (!warp_wait_all(2, &sm.raw_full[half], kt & 1, &sm.k_empty[st], ph ^ 1, nullptr, 0, nullptr, 0, &sm.abort)) return;
+      if (!warp_wait(&sm.raw_full[half], kt & 1, &sm.abort)) return;
       // the words, with a finite scale whatever the bytes; 0 outside the cache
       const uint32_t good = sm.pf.good[half][key >> 5] >> (key & 31) & 1u ? 0xFFF0u : 0u;
       const uint32_t kw = *reinterpret_cast<const uint16_t*>(raw + kv4_k_word(slots, place));
       const uint32_t vw = *reinterpret_cast<const uint16_t*>(raw + kv4_v_word(slots, place));
-      const uint32_t ks = min(kw & good, uint32_t(kKv4MaxScaleBits)), vs = min(vw & good, uint32_t(kKv4MaxScaleBits));
-      uint4 c[4];
+      uint4 k[4], next[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        c[u] = *reinterpret_cast<const uint4*>(raw + kv4_k_row(slots, place) + 16 * ((u + (lane >> 1)) & 3));
-      kv4_widen(c, ks, kw & 15u, sm.pf.k[st], r);
-      fence_proxy_async_smem();  // read by the tensor core
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.k_full[st]);
-      // V's row is read before its tile is free, and the raw stage handed back
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        c[u] = *reinterpret_cast<const uint4*>(raw + kv4_v_row(slots, place) + 16 * ((u + (lane >> 1)) & 3));
+      for (int u = 0; u < 4; ++u) {
+        const int at = 16 * ((u + (lane >> 1)) & 3);
+        k[u] = *reinterpret_cast<const uint4*>(raw + kv4_k_row(slots, place) + at);
+        next[u] = *reinterpret_cast<const uint4*>(raw + kv4_v_row(slots, place) + at);
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.raw_empty[half]);
+      if (!warp_wait(&sm.k_empty[st], ((kt >> 1) & 1) ^ 1, &sm.abort)) return;
+      kv4_widen(k[0], k[1], k[2], k[3], min(kw & good, uint32_t(kKv4MaxScaleBits)), kw & 15u, smem_u32(sm.pf.k[st]), r);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.k_full[st]);
+      if (kt > 0 && !put_v(kt - 1)) return;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) v[u] = next[u];
+      v_scale = min(vw & good, uint32_t(kKv4MaxScaleBits));
+      v_zero = vw & 15u;
       if (j == 0) {
         if (!warp_wait(&sm.q_raw, pe & 1, &sm.abort)) return;
-        const float back = kv4_turn_query<T>(sm.pf.q[0], r);
-        sm.pf.q_scale[pe & 1][r] = kp.run.scale_log2 * back;
+        sm.pf.q_scale[pe & 1][r] = kp.run.scale_log2 * kv4_turn_query<T>(sm.pf.q[0], r);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.q_full);
         ++pe;
       }
-      if (!warp_wait(&sm.v_empty[st], ph ^ 1, &sm.abort)) return;
-      kv4_widen(c, vs, vw & 15u, sm.pf.v[st], r);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.v_full[st]);
     }
   }
+  if (kt > 0) put_v(kt - 1);
 }
 
 // Q of items [b0, b1) by warps 2 and 3 (which = 0, 1): its load, and M tile B's rows.
