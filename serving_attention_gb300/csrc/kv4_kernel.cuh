@@ -48,7 +48,7 @@ constexpr int kKv4Barrier = 8;         // named barriers: of all computing warps
 // Registers per thread and warpgroup; each phase's sum is the launch's.
 constexpr int kKv4RegsLaunch = 128;
 constexpr int kKv4RegsDecode0 = 56, kKv4RegsDecode = 152;
-constexpr int kKv4RegsMma = 88, kKv4RegsWiden = 72, kKv4RegsSoftmax = 176;
+constexpr int kKv4RegsMma = 112, kKv4RegsWiden = 80, kKv4RegsSoftmax = 160;
 static_assert(kKv4RegsDecode0 + 3 * kKv4RegsDecode <= 4 * kKv4RegsLaunch, "register split exceeds the launch");
 static_assert(kKv4RegsMma + kKv4RegsWiden + 2 * kKv4RegsSoftmax <= 4 * kKv4RegsLaunch,
               "register split exceeds the launch");

@@ -324,7 +324,9 @@ __device__ void kv4_pf_softmax(const RunParams& p, Smem& sm, int32_t b0, int32_t
     const int ntiles = item_kv_tiles(item);
     const int prow = mt * kTileM + r;  // packed row within the item
     if (mt < item_m_tiles(item)) {
-      int lim = -1, lo = 0;  // visible keys of this row: [lo, lim] and the sink (lim -1: padding row)
+      // visible keys of this row: [lo, lim] and the sink (a padding row, which is not stored: all, so that its warp has
+      // no key to hide)
+      int lim = INT32_MAX, lo = 0;
       if (prow < nrows) {
         const int pos = rq.kv_len - rq.qo_len + (item.row0 + prow) / G;
         lim = min(causal ? pos : rq.kv_len - 1, item.kv1 - 1);
@@ -339,32 +341,33 @@ __device__ void kv4_pf_softmax(const RunParams& p, Smem& sm, int32_t b0, int32_t
         if (!ok) continue;
         tc::fence_after_sync();
         if (j == 0) c = sm.pf.q_scale[seq & 1][prow];
-        uint32_t sv[4][32];
-#pragma unroll
-        for (int h = 0; h < 4; ++h) tc::tmem_ld32(s_cols + 32 * h, sv[h]);
-        tc::tmem_ld_wait();
         const int kbase = item.kv0 + j * kTileN;
-        if (kbase + kTileN - 1 > lim || (kMask && kbase < lo)) {  // causal diagonal, chunk end, padding row, window
+        const bool edge = kbase + kTileN - 1 > lim || (kMask && kbase < lo);  // causal diagonal, chunk end, window
+        uint32_t sv[2][32];
+        // 64 columns of S; the hidden keys of an edge tile -inf
+        auto load = [&](int half) {
+          tc::tmem_ld32(s_cols + 64 * half, sv[0]);
+          tc::tmem_ld32(s_cols + 64 * half + 32, sv[1]);
+          tc::tmem_ld_wait();
+          if (edge) {
+            const int k0 = kbase + 64 * half;
 #pragma unroll
-          for (int h = 0; h < 4; ++h)
+            for (int e = 0; e < 64; ++e)
+              if (k0 + e > lim || (kMask && k0 + e < lo && k0 + e >= var.sink)) sv[e >> 5][e & 31] = 0xff800000u;  // -inf
+          }
+        };
+        // row max in four independent chains of three-input maxima
+        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          load(half);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const int key = kbase + 32 * h + e;
-              if (key > lim || (kMask && key < lo && key >= var.sink)) sv[h][e] = 0xff800000u;  // -inf
-            }
+          for (int e = 0; e < 64; e += 8)
+#pragma unroll
+            for (int a = 0; a < 4; ++a)
+              mx4[a] = max3(mx4[a], __uint_as_float(sv[e >> 5][(e & 31) + a]), __uint_as_float(sv[e >> 5][(e & 31) + 4 + a]));
         }
-        // row max in eight independent chains of three-input maxima
-        auto sval = [&](int e) { return __uint_as_float(sv[e >> 5][e & 31]); };
-        float mx8[8];
-#pragma unroll
-        for (int a = 0; a < 8; ++a) mx8[a] = sval(a);
-#pragma unroll
-        for (int e = 8; e + 16 <= kTileN; e += 16)
-#pragma unroll
-          for (int a = 0; a < 8; ++a) mx8[a] = max3(mx8[a], sval(e + a), sval(e + 8 + a));
-#pragma unroll
-        for (int a = 0; a < 8; ++a) mx8[a] = fmaxf(mx8[a], sval(kTileN - 8 + a));
-        const float mx = max3(max3(mx8[0], mx8[1], mx8[2]), max3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])) * c;
+        const float mx = fmaxf(max3(mx4[0], mx4[1], mx4[2]), mx4[3]) * c;
         const float m_old = mrun;
         const float m_new = (mx > m_old + kLazyRescale) ? mx : m_old;
         const bool rescale = (m_new != m_old) && j > 0;
@@ -373,12 +376,11 @@ __device__ void kv4_pf_softmax(const RunParams& p, Smem& sm, int32_t b0, int32_t
           const float alpha = rescale ? ex2(m_old - m_new) : 1.f;
 #pragma unroll 1
           for (int h = 0; h < 4; ++h) {
-            uint32_t ov[32];
-            tc::tmem_ld32(o_cols + 32 * h, ov);
+            tc::tmem_ld32(o_cols + 32 * h, sv[0]);
             tc::tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-            tc::tmem_st32(o_cols + 32 * h, ov);
+            for (int e = 0; e < 32; ++e) sv[0][e] = __float_as_uint(__uint_as_float(sv[0][e]) * alpha);
+            tc::tmem_st32(o_cols + 32 * h, sv[0]);
           }
           tc::tmem_st_wait();
           if (rescale) {
@@ -394,21 +396,21 @@ __device__ void kv4_pf_softmax(const RunParams& p, Smem& sm, int32_t b0, int32_t
 #pragma unroll
         for (int a = 0; a < 4; ++a) sum4[a] = make_float2(0.f, 0.f);
         sumr[0] = sumr[1] = make_float2(0.f, 0.f);
-#pragma unroll
+#pragma unroll 1
         for (int half = 0; half < 2; ++half) {
+          load(half);
 #pragma unroll
-          for (int h = 2 * half; h < 2 * half + 2; ++h) {
+          for (int h = 0; h < 2; ++h) {
             uint32_t pk[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const float2 x =
-                  fma2(make_float2(__uint_as_float(sv[h][2 * e]), __uint_as_float(sv[h][2 * e + 1])), cc, nms);
+              const float2 x = fma2(make_float2(__uint_as_float(sv[h][2 * e]), __uint_as_float(sv[h][2 * e + 1])), cc, nms);
               const float2 pe = make_float2(ex2(x.x), ex2(x.y));
               sum4[e & 3] = add2(sum4[e & 3], pe);
               pk[e] = tc::pack2<__half>(pe.x, pe.y);
               tc::add_packed2<__half>(sumr[e & 1], pk[e]);
             }
-            tc::tmem_st16(s_cols + 16 * h, pk);
+            tc::tmem_st16(s_cols + 32 * half + 16 * h, pk);
           }
           tc::tmem_st_wait();
           tc::fence_before_sync();
