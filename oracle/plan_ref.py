@@ -62,7 +62,8 @@ Rule:
     tokens a CTA's prefill-class items of requests of up to 32 rows come behind
     its others.
     Plans over the 4-bit cache (kv_bits 4, a magic of their own): no multi-head
-    units, and a decode-class key costs ceil(decode_cost_weight / 4).
+    units, a decode-class key costs ceil(decode_cost_weight / 4), and behind the
+    merge counters (rounded up to a multiple of 4) are 16 per merge unit, one for each of its rows.
  6. Output: header (with the variant: window, sink, soft-cap bits, and for
     RoPE its position capacity, theta and scale bits and the table offset;
     then the count of late units, the partial rows used, the batch's query
@@ -86,6 +87,7 @@ HEADER_INTS = 32
 ROPE_PAIRS = 64
 ITEM_INTS = 16
 MERGE_INTS = 8
+KV4_ROW_COUNTERS = 16
 REQ_INTS = 4
 CASCADE_INTS = 12
 CASCADE_ROWS = 16
@@ -107,6 +109,7 @@ def _ceil_div(a: int, b: int) -> int:
 def int_workspace_ints(cfg: dict) -> int:
     return (HEADER_INTS + _align4(cfg["num_ctas"] + 1) + ITEM_INTS * cfg["max_items"]
             + MERGE_INTS * cfg["max_merge_units"] + _align4(cfg["max_merge_units"])
+            + (KV4_ROW_COUNTERS * cfg["max_merge_units"] if cfg.get("kv_bits", 0) == 4 else 0)
             + REQ_INTS * cfg["max_batch"] + CASCADE_INTS * cfg["max_merge_units"])
 
 
@@ -412,7 +415,7 @@ def _plan(cfg, reqs, num_shared, shared_page_size, block_of, total_qo, num_qo_he
     off_items = off_cta + _align4(C + 1)
     off_merge = off_items + ITEM_INTS * n_items
     off_cnt = off_merge + MERGE_INTS * n_merge
-    off_req = off_cnt + _align4(n_merge)
+    off_req = off_cnt + _align4(n_merge) + (KV4_ROW_COUNTERS * n_merge if kv4 else 0)
     off_cascade = off_req + REQ_INTS * batch
     total_ints = off_cascade + CASCADE_INTS * len(entries)
     if total_ints > int_workspace_ints(cfg):

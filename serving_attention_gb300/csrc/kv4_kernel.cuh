@@ -74,7 +74,6 @@ struct alignas(1024) Kv4Smem {
   uint64_t s_full[2], o_ready[2], o_free[2], p_full[2][2];
   uint32_t tmem_base;
   volatile int abort;
-  volatile int merge_last[kKv4Groups + 1];
   int merge_last_pf;
 };
 constexpr size_t kKv4SmemBytes = sizeof(Kv4Smem);
@@ -104,12 +103,12 @@ __device__ __forceinline__ float word_zero(uint32_t w) { return __half2float(__u
 
 // The warps that share an item: all computing ones, or one group's.
 struct Kv4Team {
-  int rank, warps, threads, bar, flag;
+  int rank, warps, threads, bar;
 };
 __device__ __forceinline__ Kv4Team kv4_team(int warp, bool all) {
-  if (all) return Kv4Team{warp, kKv4Warps, 32 * kKv4Warps, kKv4Barrier, kKv4Groups};
+  if (all) return Kv4Team{warp, kKv4Warps, 32 * kKv4Warps, kKv4Barrier};
   const int g = warp / kKv4GroupWarps;
-  return Kv4Team{warp % kKv4GroupWarps, kKv4GroupWarps, 32 * kKv4GroupWarps, kKv4Barrier + 1 + g, g};
+  return Kv4Team{warp % kKv4GroupWarps, kKv4GroupWarps, 32 * kKv4GroupWarps, kKv4Barrier + 1 + g};
 }
 // A CTA's items [begin, shorts) go to all warps, those behind to the groups in turn.
 __device__ __forceinline__ int32_t kv4_next_item(int32_t i, int32_t shorts, int group) {
@@ -126,9 +125,10 @@ __device__ __forceinline__ int kv4_stages(const Item& it) { return (it.kv1 - it.
 // The loaders of the rings: lane u of a loader warp has ring first + u's place in
 // its items, and a round issues a stage for every ring whose next slot is free.
 // Stages of one or two blocks (kB = 32, 16) are issued by that lane, for all
-// rings at once, by one warp; stages of many small blocks (kB = 0) by the whole
-// warp, a lane a block, ring after ring, three rings a warp.  Page ids are loaded
-// a stage ahead, their lines a line ahead.
+// rings at once; stages of many small blocks (kB = 0) by the whole warp, ring
+// after ring, in copies of 16 bytes (a bulk copy for each block of one slot kept
+// the copy engine busy longer than the keys did the warps).  Page ids are loaded a
+// stage ahead, their lines a line ahead.
 template <int kB>
 __device__ void kv4_load(const Kv4Params& kp, Kv4Smem& sm, int loader, int32_t off_items, int32_t begin,
                          int32_t shorts, int32_t end) {
@@ -144,6 +144,15 @@ __device__ void kv4_load(const Kv4Params& kp, Kv4Smem& sm, int loader, int32_t o
   const uint8_t* head = nullptr;
   constexpr int kIds = kB == 16 ? 2 : kB == 32 ? 1 : kRings;
   int32_t ids[kIds];  // of this lane's next stage; kB = 0: this lane's block of each ring's next stage
+  // kB = 0: the 16-byte pieces lane, lane + 32, .. of a stage, as block << 16 | place
+  constexpr int kPieces = kKv4StageBytes / 16 / 32;
+  uint32_t piece[kB ? 1 : kPieces];
+  if constexpr (kB == 0)
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+      const int x = lane + 32 * k, b = 16 * x / bytes;
+      piece[k] = b < blocks ? uint32_t(b) << 16 | uint32_t(16 * x - b * bytes) : 31u << 16;
+    }
   uint32_t issued = 0;
   bool done = lane >= kRings, fresh = false;  // fresh: the next stage's ids are still to be fetched
   long long seen_at = clock64();
@@ -171,14 +180,6 @@ __device__ void kv4_load(const Kv4Params& kp, Kv4Smem& sm, int loader, int32_t o
       npages = (it.rq.kv_len + kc.page_size - 1) >> kc.log2_page;
       pages = kc.kv_indices + it.rq.page_start;
       head = kp.cache + it.hk * kp.head_stride;
-      if (team.rank == 0 && issued > 0)  // the item's query rows on their way before the copies that would hold them up
-        for (int row = it.row0; row < it.row1; ++row) {
-          const int tok = row / p.group;
-          const uint16_t* q = p.q + (int64_t(it.rq.qo_start) + tok) * p.q_stride_tok +
-                              int64_t(it.hk * p.group + row - tok * p.group) * p.q_stride_head;
-          prefetch_l1(q);
-          prefetch_l1(q + 64);
-        }
     }
     const int32_t j0 = kv0 + kKv4Stage * st, pg0 = j0 >> kc.log2_page;
     if (fresh && (pg0 & 31) < blocks && pg0 + 32 < npages) prefetch_l1(pages + pg0 + 32);
@@ -232,12 +233,19 @@ __device__ void kv4_load(const Kv4Params& kp, Kv4Smem& sm, int loader, int32_t o
         const bool ok = uint32_t(ids[u]) < uint32_t(kc.num_pages) && lane < blocks && key + (lane << log2_slots) < last;
         const uint32_t loads = __ballot_sync(0xffffffffu, ok);
         const uint32_t good = __ballot_sync(0xffffffffu, loads >> (lane >> log2_slots) & 1u);
+        uint8_t* const dst = sm.dec.ring[ring][s];
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k) {
+          const int b = piece[k] >> 16;
+          const int32_t id = __shfl_sync(0xffffffffu, ids[u], b);
+          if ((loads >> b & 1u) && 16 * (lane + 32 * k) < blocks * bytes)
+            cp_async_16(dst + 16 * (lane + 32 * k), src + id * kp.page_stride + (piece[k] & 0xFFFFu), 16);
+        }
+        cp_async_mbar_arrive_noinc(&sm.full[ring][s]);
         if (lane == 0) {
           sm.dec.good[ring][s] = good;
-          mbar_arrive_expect_tx(&sm.full[ring][s], __popc(loads) * bytes);
+          mbar_arrive(&sm.full[ring][s]);
         }
-        __syncwarp();
-        if (ok) bulk_load(&sm.dec.ring[ring][s][lane * bytes], src + ids[u] * kp.page_stride, bytes, &sm.full[ring][s]);
       }
     }
     if (free_slot) {
@@ -305,22 +313,28 @@ struct Kv4Rows {
   float unit;        // the power of two that v's scales are multiplied by
 };
 
-template <typename T>
-__device__ __forceinline__ void kv4_load_rows(const Kv4Params& kp, const Item& it, int pass, int causal,
-                                              const Variant& var, Kv4Rows<T>& R) {
+// This lane's part of query row g of a pass: dims 32 t .. 32 t + 31.
+__device__ __forceinline__ void kv4_fetch_rows(const Kv4Params& kp, const Item& it, int pass, uint4 (&u)[4]) {
   const RunParams& p = kp.run;
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, G = p.group;
-  const int row = it.row0 + kKv4Tile * pass + g;
-  uint4 u[4];
+  const int lane = threadIdx.x & 31, G = p.group;
+  const int row = it.row0 + kKv4Tile * pass + (lane >> 2);
 #pragma unroll
   for (int j = 0; j < 4; ++j) u[j] = make_uint4(0u, 0u, 0u, 0u);
   if (row < it.row1) {
     const int tok = row / G;
     const uint4* src = reinterpret_cast<const uint4*>(p.q + (int64_t(it.rq.qo_start) + tok) * p.q_stride_tok +
-                                                      int64_t(it.hk * G + row - tok * G) * p.q_stride_head + 32 * t);
+                                                      int64_t(it.hk * G + row - tok * G) * p.q_stride_head) +
+                       4 * (lane & 3);
 #pragma unroll
     for (int j = 0; j < 4; ++j) u[j] = __ldg(src + j);
   }
+}
+
+template <typename T>
+__device__ __forceinline__ void kv4_set_rows(const Kv4Params& kp, const Item& it, int pass, int causal,
+                                             const Variant& var, const uint4 (&u)[4], Kv4Rows<T>& R) {
+  const RunParams& p = kp.run;
+  const int lane = threadIdx.x & 31, t = lane & 3, G = p.group;
   float top = 0.f;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -575,42 +589,25 @@ __device__ __forceinline__ void kv4_merge_row(const RunParams& p, const Item& it
   if (lane == 0 && p.lse) p.lse[tok * p.num_qo_heads + head] = L > 0.f ? M + __logf(L) : -INFINITY;
 }
 
-// Behind an item of a split unit: the team that completes the unit's counter
-// merges its chunks (units left to the late merge, where one follows, not).
-template <typename T>
-__device__ __forceinline__ void kv4_merge_unit(const RunParams& p, Kv4Smem& sm, const Item& it, const Kv4Team& team,
-                                               int32_t off_merge, int32_t off_cnt) {
-  const int32_t* unit = p.iws + off_merge + FI_MERGE_INTS * it.merge;
-  if (p.late_merge && __ldg(unit + FI_MERGE_LATE)) return;
-  const int n = __ldg(unit + 4);
-  const int64_t base = __ldg(unit + 5);
-  __threadfence();
-  named_barrier_sync(team.bar, team.threads);
-  if (team.rank == 0 && (threadIdx.x & 31) == 0)
-    sm.merge_last[team.flag] = !sm.abort && atomicAdd(p.iws + off_cnt + it.merge, 1) == n - 1;
-  named_barrier_sync(team.bar, team.threads);
-  if (sm.merge_last[team.flag]) {
-    __threadfence();
-    for (int r = team.rank; r < it.row1 - it.row0; r += team.warps) kv4_merge_row<T>(p, it, r, n, base);
-    if (team.rank == 0 && (threadIdx.x & 31) == 0) p.iws[off_cnt + it.merge] = 0;  // ready for the next run of this plan
-  }
-  named_barrier_sync(team.bar, team.threads);
-}
-
-// Rows [kKv4Tile pass, ..) of an item, by its team.  `after`: the team whose
-// states of the pass before may still be being joined; its barrier comes before
-// this warp's next state, so that a warp without a row to join goes on.
+// Rows [kKv4Tile pass, ..) of an item, by its team.  u: this lane's part of them;
+// on return of those of pass `next_pass` of item `next_i` (on their way while the
+// states are joined).  `after`: the team whose states of the pass before may still
+// be being joined; its barrier comes before this warp's next state, so that a warp
+// without a row to join goes on.  A row of a split unit is merged by the warp that
+// brings its last chunk, by a counter for each row: no warp waits for another's.
 template <typename T, int kB>
 __device__ __forceinline__ void kv4_pass(const Kv4Params& kp, Kv4Smem& sm, int warp, const Kv4Places<kB>& at,
-                                         const Item& it, int pass, const Kv4Team& team, Kv4Team& after, int causal,
-                                         const Variant& var, uint32_t& used) {
+                                         const Item& it, int pass, int32_t off_items, int32_t next_i, int next_pass,
+                                         int32_t end, const Kv4Team& team, Kv4Team& after, int32_t off_merge,
+                                         int32_t off_rows, int causal, const Variant& var, uint32_t& used,
+                                         uint4 (&u)[4]) {
   const RunParams& p = kp.run;
   const int lane = threadIdx.x & 31, G = p.group;
   const int rows = min(kKv4Tile, it.row1 - it.row0 - kKv4Tile * pass);
   const int nst = kv4_stages(it), parts = min(nst, team.warps);
   if (team.rank < parts) {
     Kv4Rows<T> R;
-    kv4_load_rows<T>(kp, it, pass, causal, var, R);
+    kv4_set_rows<T>(kp, it, pass, causal, var, u, R);
     // keys that every row of the pass sees
     const int r0 = it.row0 + kKv4Tile * pass, r1 = r0 + rows - 1, pos = it.rq.kv_len - it.rq.qo_len;
     const int lim = min(causal ? pos + r0 / G : it.rq.kv_len - 1, it.kv1 - 1), lo = window_low(var, pos + r1 / G);
@@ -633,6 +630,7 @@ __device__ __forceinline__ void kv4_pass(const Kv4Params& kp, Kv4Smem& sm, int w
   } else if (after.warps) {
     named_barrier_sync(after.bar, after.threads);
   }
+  if (next_i < end) kv4_fetch_rows(kp, load_item(p.iws, off_items, next_i), next_pass, u);
   named_barrier_sync(team.bar, team.threads);
   const int w0 = warp - team.rank;  // the team's first warp
   if (!sm.abort) {
@@ -674,6 +672,19 @@ __device__ __forceinline__ void kv4_pass(const Kv4Params& kp, Kv4Smem& sm, int w
         *(reinterpret_cast<float4*>(p.fws + p.partial_o_offset + part * kHeadDim) + lane) =
             make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
         if (lane == 0) p.fws[part] = lse;
+        const int32_t* unit = p.iws + off_merge + FI_MERGE_INTS * it.merge;
+        const int n = __ldg(unit + 4);
+        const int64_t base = __ldg(unit + 5);
+        int32_t* const count = p.iws + off_rows + FI_KV4_ROW_COUNTERS * it.merge + prow;
+        __threadfence();
+        __syncwarp();
+        int last = 0;
+        if (lane == 0) last = atomicAdd(count, 1) == n - 1;
+        if (__shfl_sync(0xffffffffu, last, 0)) {
+          __threadfence();
+          kv4_merge_row<T>(p, it, prow, n, base);
+          if (lane == 0) *count = 0;  // ready for the next run of this plan
+        }
       }
     }
   }
@@ -683,20 +694,28 @@ __device__ __forceinline__ void kv4_pass(const Kv4Params& kp, Kv4Smem& sm, int w
 // The items [begin, end) of a CTA, by computing warp `warp`.
 template <typename T, int kB>
 __device__ void kv4_consume(const Kv4Params& kp, Kv4Smem& sm, int warp, int32_t begin, int32_t shorts, int32_t end,
-                            int32_t off_items, int32_t off_merge, int32_t off_cnt, int causal, const Variant& var) {
+                            int32_t off_items, int32_t off_merge, int32_t off_rows, int causal, const Variant& var) {
   const RunParams& p = kp.run;
   const Kv4Places<kB> at(kp);
+  const int group = warp / kKv4GroupWarps;
   uint32_t used = 0;
-  Kv4Team after{0, 0, 0, 0, 0};
-  for (int32_t i = kv4_next_item(begin - 1, shorts, warp / kKv4GroupWarps); i < end;
-       i = kv4_next_item(i, shorts, warp / kKv4GroupWarps)) {
+  Kv4Team after{0, 0, 0, 0};
+  int32_t i = kv4_next_item(begin - 1, shorts, group);
+  if (i >= end) return;
+  int pass = 0;
+  uint4 u[4];
+  kv4_fetch_rows(kp, load_item(p.iws, off_items, i), 0, u);
+  while (i < end) {
     const Item it = load_item(p.iws, off_items, i);
-    const Kv4Team team = kv4_team(warp, i < shorts);
-    for (int pass = 0; kKv4Tile * pass < it.row1 - it.row0; ++pass)
-      kv4_pass<T, kB>(kp, sm, warp, at, it, pass, team, after, causal, var, used);
-    if (it.merge >= 0) kv4_merge_unit<T>(p, sm, it, team, off_merge, off_cnt);
+    const bool last = kKv4Tile * (pass + 1) >= it.row1 - it.row0;
+    const int32_t next_i = last ? kv4_next_item(i, shorts, group) : i;
+    const int next_pass = last ? 0 : pass + 1;
+    kv4_pass<T, kB>(kp, sm, warp, at, it, pass, off_items, next_i, next_pass, end, kv4_team(warp, i < shorts), after,
+                    off_merge, off_rows, causal, var, used, u);
+    i = next_i;
+    pass = next_pass;
   }
-  if (after.warps) named_barrier_sync(after.bar, after.threads);
+  named_barrier_sync(after.bar, after.threads);
 }
 
 // First item of [begin, end) that one group takes alone: a CTA's items of a
@@ -758,6 +777,7 @@ __global__ void __launch_bounds__(kKv4Threads, 1) kv4_attention_kernel(const __g
     return;
   }
   const int32_t off_merge = ws_header(iws, FI_H_OFF_MERGE), off_cnt = ws_header(iws, FI_H_OFF_COUNTERS);
+  const int32_t off_rows = off_cnt + ((ws_header(iws, FI_H_NUM_MERGE) + 3) & ~3);
   const int causal = ws_header(iws, FI_H_CAUSAL);
   Variant var;
   var.window_left = ws_header(iws, FI_H_WINDOW_LEFT);
@@ -766,7 +786,7 @@ __global__ void __launch_bounds__(kKv4Threads, 1) kv4_attention_kernel(const __g
   var.rope_table = nullptr;
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x < kKv4Warps * kKv4Depth) {
-    mbar_init(&sm.full[0][threadIdx.x], 1);
+    mbar_init(&sm.full[0][threadIdx.x], kB ? 1 : 33);  // the copies' bytes; or every copying lane, and one for the bits
     mbar_init(&sm.empty[0][threadIdx.x], 1);
   }
   if (threadIdx.x == kKv4Warps * kKv4Depth) {
@@ -849,7 +869,7 @@ __global__ void __launch_bounds__(kKv4Threads, 1) kv4_attention_kernel(const __g
       kv4_load<kB>(kp, sm, warp, off_items, mid, shorts, end);
     } else {
       tc::setmaxnreg_inc<kKv4RegsDecode>();
-      kv4_consume<T, kB>(kp, sm, warp - kKv4FirstWarp, mid, shorts, end, off_items, off_merge, off_cnt, causal, var);
+      kv4_consume<T, kB>(kp, sm, warp - kKv4FirstWarp, mid, shorts, end, off_items, off_merge, off_rows, causal, var);
     }
   }
   tc::fence_before_sync();

@@ -108,6 +108,7 @@ struct CtaHeap {
 int64_t fi::plan_capacity_ints(const fi_plan_config* cfg) {
   return FI_HEADER_INTS + round4(int64_t(cfg->num_ctas) + 1) + int64_t(FI_ITEM_INTS) * cfg->max_items +
          int64_t(FI_MERGE_INTS) * cfg->max_merge_units + round4(cfg->max_merge_units) +
+         (cfg->kv_bits == 4 ? int64_t(FI_KV4_ROW_COUNTERS) * cfg->max_merge_units : 0) +
          int64_t(FI_REQ_INTS) * cfg->max_batch + int64_t(FI_CASCADE_INTS) * cfg->max_merge_units;
 }
 
@@ -464,7 +465,7 @@ fi_status plan_requests(const fi_plan_config* cfg, const std::vector<Req>& reqs,
   const int64_t off_items = off_cta + round4(C + 1);
   const int64_t off_merge = off_items + FI_ITEM_INTS * n_items;
   const int64_t off_cnt = off_merge + FI_MERGE_INTS * n_merge;
-  const int64_t off_req = off_cnt + round4(n_merge);
+  const int64_t off_req = off_cnt + round4(n_merge) + (kv4 ? int64_t(FI_KV4_ROW_COUNTERS) * n_merge : 0);
   const int64_t off_cascade = off_req + int64_t(FI_REQ_INTS) * batch;
   const int64_t total_ints = off_cascade + int64_t(FI_CASCADE_INTS) * n_cascade;
   if (total_ints > fi::plan_capacity_ints(cfg)) return FI_ERR_CAPACITY;

@@ -29,6 +29,9 @@
 //                  late units merged after the run never touch theirs; when the run
 //                  is not followed by the late merge, as when a graph was captured
 //                  from a plan without late units, it merges them itself)
+//                  (a plan over the 4-bit cache: behind them, from a multiple of
+//                  4 ints on, FI_KV4_ROW_COUNTERS per merge unit, one for each
+//                  packed row of a 16-row unit, which its run uses instead)
 //   requests     FI_REQ_INTS each: {qo_start, qo_len, page_start, kv_len}
 //                  (a cascade plan numbers its shared blocks first: requests
 //                  b < num_shared read the shared KV cache and see every one
@@ -69,6 +72,7 @@
 #define FI_MIN_TMA_PAGE 8  // smallest page of the tensor-core path
 #define FI_DIFF_SMALL_PAGE_ROWS 32  // differential, smaller pages: requests of up to so many packed rows leave it
 #define FI_MERGE_INTS 8
+#define FI_KV4_ROW_COUNTERS 16  // FI_TILE_DECODE, as an int of the layout
 #define FI_REQ_INTS 4
 #define FI_CASCADE_INTS 12
 #define FI_CASCADE_ROWS 16  // packed rows per cascade merge entry, at most
