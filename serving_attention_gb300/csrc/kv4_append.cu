@@ -13,7 +13,11 @@
 // Bound by the bytes of q (read and written), k and v (read, a quarter
 // written).  A warp takes four heads at a time, q heads first, then k, then v,
 // each kind's heads filled up to a multiple of four so that a warp does one
-// thing; one warp per token, or per part of one when there are few tokens.
+// thing; one warp per token, or per part of one when there are few tokens.  The
+// next group's rows are in flight while one is turned and coded.  cos and sin
+// stay in shared memory and no second group is held: with more warps on an SM
+// 8192 tokens of 32 + 8 heads took 56 us (33 us of bytes at the copy rate)
+// where one or two groups ahead with 16 to 20 warps took 60 to 64.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -26,8 +30,8 @@
 namespace fi {
 namespace {
 
-constexpr int kAppendWarps = 4;  // warps of a block
-constexpr int kAppendAhead = 2;  // groups of four heads a warp has in flight
+constexpr int kAppendWarps = 4;   // warps of a block
+constexpr int kAppendBlocks = 7;  // blocks of an SM
 constexpr float kFifteenth = 1.f / 15.f;
 
 enum { kNoPairs = 0, kHalfPairs = 1, kNextPairs = 2, kPartHalfPairs = 3 };
@@ -71,7 +75,7 @@ __device__ __forceinline__ uint32_t codes8(const float (&x)[8], float inv, int z
 }
 
 template <typename T, int kPairs>
-__global__ void __launch_bounds__(32 * kAppendWarps, 4) kv4_append_kernel(const __grid_constant__ Kv4AppendParams a) {
+__global__ void __launch_bounds__(32 * kAppendWarps, kAppendBlocks) kv4_append_kernel(const __grid_constant__ Kv4AppendParams a) {
   __shared__ float2 s_cs[kAppendWarps][FI_KV4_HEAD_DIM / 2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t w = int64_t(blockIdx.x) * kAppendWarps + warp;
@@ -88,27 +92,22 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 4) kv4_append_kernel(const 
     const int h = 4 * (g < nq ? g : g < nq + nk ? g - nq : g - nq - nk) + sub;
     return h < operand(g).heads ? h : -1;
   };
-  uint4 lo[kAppendAhead], hi[kAppendAhead];
-  auto load = [&](int g0) {
-#pragma unroll
-    for (int u = 0; u < kAppendAhead; ++u) {
-      const int g = g0 + u * a.parts;
-      lo[u] = hi[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (g >= groups) continue;
-      const int h = head_of(g);
-      if (h < 0) continue;
-      const Kv4Rows& r = operand(g);
-      const uint16_t* src = r.in + t * r.in_tok + h * r.in_head + 8 * p;
-      lo[u] = *reinterpret_cast<const uint4*>(src);
-      hi[u] = *reinterpret_cast<const uint4*>(src + 64);
-    }
+  uint4 lo, hi;
+  auto load = [&](int g) {
+    lo = hi = make_uint4(0u, 0u, 0u, 0u);
+    if (g >= groups) return;
+    const int h = head_of(g);
+    if (h < 0) return;
+    const Kv4Rows& rows = operand(g);
+    const uint16_t* src = rows.in + t * rows.in_tok + h * rows.in_head + 8 * p;
+    lo = *reinterpret_cast<const uint4*>(src);
+    hi = *reinterpret_cast<const uint4*>(src + 64);
   };
   load(part);
 
-  // cos and sin of this lane's pairs
-  constexpr int kMine = kPairs == kHalfPairs ? 8 : kPairs == kNextPairs ? 4 : 1;
-  float2 r0[kMine], r1[kMine];  // of chunk p (half pairs: of chunk p with p + 8), of chunk p + 8
-  float2* cs = s_cs[warp];
+  // cos and sin of the token's pairs
+  constexpr int kMine = kPairs == kHalfPairs ? 8 : 4;
+  float2* const cs = s_cs[warp];
   if (kPairs != kNoPairs) {
     const int32_t pos = __ldg(a.positions + t);
     for (int i = lane; i < a.rot_chunks * 4; i += 32) {
@@ -118,14 +117,6 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 4) kv4_append_kernel(const 
       cs[i] = make_float2(__fmul_rn(cosf(x), a.amplitude), __fmul_rn(sinf(x), a.amplitude));
     }
     __syncwarp();
-#pragma unroll
-    for (int e = 0; e < kMine; ++e) {
-      if (kPairs == kHalfPairs) r0[e] = cs[8 * p + e];
-      if (kPairs == kNextPairs) {
-        r0[e] = p < a.rot_chunks ? cs[4 * p + e] : make_float2(1.f, 0.f);
-        r1[e] = p + 8 < a.rot_chunks ? cs[4 * (p + 8) + e] : make_float2(1.f, 0.f);
-      }
-    }
   }
   auto turn_pair = [](float& x, float& y, const float2& c) {
     const float x0 = x;
@@ -137,107 +128,102 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 4) kv4_append_kernel(const 
   const int in_page = int(slot) & ((1 << a.log2_page) - 1);
   const int block = in_page / a.block_slots, place = in_page - block * a.block_slots;
   uint8_t* const base = a.cache + page * a.page_stride + block * a.block_bytes;
-  for (int g0 = part; g0 < groups; g0 += kAppendAhead * a.parts) {
+  for (int g = part; g < groups; g += a.parts) {
+    const int h = head_of(g);
+    float x[8], y[8];
+    unpack<T>(lo, x);
+    unpack<T>(hi, y);
+    load(g + a.parts);  // in flight while this group is turned
+    const bool is_q = g < nq, is_v = g >= nq + nk;
+    const float* weight = is_v ? nullptr : is_q ? a.q_weight : a.k_weight;
+    if (weight) {
+      float sq[8];
 #pragma unroll
-    for (int u = 0; u < kAppendAhead; ++u) {
-      const int g = g0 + u * a.parts;
-      if (g >= groups) break;
-      const int h = head_of(g);
-      float x[8], y[8];
-      unpack<T>(lo[u], x);
-      unpack<T>(hi[u], y);
-      const bool is_q = g < nq, is_v = g >= nq + nk;
-      const float* weight = is_v ? nullptr : is_q ? a.q_weight : a.k_weight;
-      if (weight) {
-        float sq[8];
+      for (int e = 0; e < 8; ++e) sq[e] = __fadd_rn(__fmul_rn(x[e], x[e]), __fmul_rn(y[e], y[e]));
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sq[e] = __fadd_rn(__fmul_rn(x[e], x[e]), __fmul_rn(y[e], y[e]));
+      for (int d = 4; d > 0; d >>= 1)
 #pragma unroll
-        for (int d = 4; d > 0; d >>= 1)
+        for (int e = 0; e < d; ++e) sq[e] = __fadd_rn(sq[e], sq[e + d]);
 #pragma unroll
-          for (int e = 0; e < d; ++e) sq[e] = __fadd_rn(sq[e], sq[e + d]);
-#pragma unroll
-        for (int m = 4; m > 0; m >>= 1) sq[0] = __fadd_rn(sq[0], __shfl_xor_sync(0xffffffffu, sq[0], m));
-        const float f = __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(sq[0], 1.f / 128.f), a.eps)));
-        const float* mine = weight + max(h, 0) * (is_q ? a.q_weight_stride : a.k_weight_stride) + 8 * p;
-        const float4 w0 = __ldg(reinterpret_cast<const float4*>(mine)), w1 = __ldg(reinterpret_cast<const float4*>(mine + 4));
-        const float4 w2 = __ldg(reinterpret_cast<const float4*>(mine + 64)), w3 = __ldg(reinterpret_cast<const float4*>(mine + 68));
-        const float wx[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-        const float wy[8] = {w2.x, w2.y, w2.z, w2.w, w3.x, w3.y, w3.z, w3.w};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          x[e] = __fmul_rn(__fmul_rn(x[e], f), wx[e]);
-          y[e] = __fmul_rn(__fmul_rn(y[e], f), wy[e]);
-        }
-      }
-      if (!is_v) {
-        if (kPairs == kHalfPairs) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) turn_pair(x[e], y[e], r0[e % kMine]);
-        } else if (kPairs == kNextPairs) {
-          if (p < a.rot_chunks)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) turn_pair(x[2 * e], x[2 * e + 1], r0[e % kMine]);
-          if (p + 8 < a.rot_chunks)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) turn_pair(y[2 * e], y[2 * e + 1], r1[e % kMine]);
-        } else if (kPairs == kPartHalfPairs) {
-          // chunk c pairs with chunk c + half (c < half); the partner's values by shuffles
-          const int half = a.rot_chunks >> 1;
-          auto partner = [&](int c) { return c < half ? c + half : c < 2 * half ? c - half : c; };
-          const int c0 = partner(p), c1 = partner(p + 8);
-          const int from0 = (lane & 24) | (c0 & 7), from1 = (lane & 24) | (c1 & 7);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float a0 = __shfl_sync(0xffffffffu, x[e], from0), b0 = __shfl_sync(0xffffffffu, y[e], from0);
-            const float a1 = __shfl_sync(0xffffffffu, x[e], from1), b1 = __shfl_sync(0xffffffffu, y[e], from1);
-            const float ox = c0 < 8 ? a0 : b0, oy = c1 < 8 ? a1 : b1;
-            auto turned = [&](float mine, float other, int c) {
-              if (c >= 2 * half) return mine;
-              const float2 r = cs[8 * (c < half ? c : c - half) + e];
-              return c < half ? __fsub_rn(__fmul_rn(mine, r.x), __fmul_rn(other, r.y))
-                              : __fadd_rn(__fmul_rn(mine, r.x), __fmul_rn(other, r.y));
-            };
-            x[e] = turned(x[e], ox, p);
-            y[e] = turned(y[e], oy, p + 8);
-          }
-        }
-      }
-      if (is_q) {
-        if (h >= 0) {
-          uint16_t* dst = a.q_out + t * a.q_out_tok + h * a.q_out_head + 8 * p;
-          *reinterpret_cast<uint4*>(dst) = pack<T>(x);
-          *reinterpret_cast<uint4*>(dst + 64) = pack<T>(y);
-        }
-        continue;
-      }
-      float least = 0.f, most = 0.f;
+      for (int m = 4; m > 0; m >>= 1) sq[0] = __fadd_rn(sq[0], __shfl_xor_sync(0xffffffffu, sq[0], m));
+      const float f = __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(sq[0], 1.f / 128.f), a.eps)));
+      const float* mine = weight + max(h, 0) * (is_q ? a.q_weight_stride : a.k_weight_stride) + 8 * p;
+      const float4 w0 = __ldg(reinterpret_cast<const float4*>(mine)), w1 = __ldg(reinterpret_cast<const float4*>(mine + 4));
+      const float4 w2 = __ldg(reinterpret_cast<const float4*>(mine + 64)), w3 = __ldg(reinterpret_cast<const float4*>(mine + 68));
+      const float wx[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+      const float wy[8] = {w2.x, w2.y, w2.z, w2.w, w3.x, w3.y, w3.z, w3.w};
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        least = fminf(least, fminf(x[e], y[e]));
-        most = fmaxf(most, fmaxf(x[e], y[e]));
+        x[e] = __fmul_rn(__fmul_rn(x[e], f), wx[e]);
+        y[e] = __fmul_rn(__fmul_rn(y[e], f), wy[e]);
       }
-#pragma unroll
-      for (int m = 4; m > 0; m >>= 1) {
-        least = fminf(least, __shfl_xor_sync(0xffffffffu, least, m));
-        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, m));
-      }
-      const float range = __fmul_rn(__fsub_rn(most, least), kFifteenth);
-      int bits = __half_as_ushort(__float2half_rn(range));
-      bits = min((bits + 15) & ~15, kKv4MaxScaleBits);
-      const float s = __half2float(__ushort_as_half(uint16_t(bits)));
-      const float inv = bits ? __frcp_rn(s) : 0.f;
-      const int z = round_small(fminf(__fmul_rn(-least, inv), 15.f));
-      if (h < 0) continue;
-      uint8_t* to = base + h * a.head_stride;
-      uint32_t* row = reinterpret_cast<uint32_t*>(to + (is_v ? kv4_v_row(a.block_slots, place) : kv4_k_row(a.block_slots, place)));
-      row[p] = codes8(x, inv, z);
-      row[p + 8] = codes8(y, inv, z);
-      if (p == 0)
-        *reinterpret_cast<uint16_t*>(to + (is_v ? kv4_v_word(a.block_slots, place) : kv4_k_word(a.block_slots, place))) =
-            uint16_t(bits | z);
     }
-    load(g0 + kAppendAhead * a.parts);
+    if (!is_v) {
+      if (kPairs == kHalfPairs) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) turn_pair(x[e], y[e], cs[kMine * p + e]);
+      } else if (kPairs == kNextPairs) {
+        if (p < a.rot_chunks)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) turn_pair(x[2 * e], x[2 * e + 1], cs[kMine * p + e]);
+        if (p + 8 < a.rot_chunks)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) turn_pair(y[2 * e], y[2 * e + 1], cs[kMine * (p + 8) + e]);
+      } else if (kPairs == kPartHalfPairs) {
+        // chunk c pairs with chunk c + half (c < half); the partner's values by shuffles
+        const int half = a.rot_chunks >> 1;
+        auto partner = [&](int c) { return c < half ? c + half : c < 2 * half ? c - half : c; };
+        const int c0 = partner(p), c1 = partner(p + 8);
+        const int from0 = (lane & 24) | (c0 & 7), from1 = (lane & 24) | (c1 & 7);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float a0 = __shfl_sync(0xffffffffu, x[e], from0), b0 = __shfl_sync(0xffffffffu, y[e], from0);
+          const float a1 = __shfl_sync(0xffffffffu, x[e], from1), b1 = __shfl_sync(0xffffffffu, y[e], from1);
+          const float ox = c0 < 8 ? a0 : b0, oy = c1 < 8 ? a1 : b1;
+          auto turned = [&](float mine, float other, int c) {
+            if (c >= 2 * half) return mine;
+            const float2 r = cs[8 * (c < half ? c : c - half) + e];
+            return c < half ? __fsub_rn(__fmul_rn(mine, r.x), __fmul_rn(other, r.y))
+                            : __fadd_rn(__fmul_rn(mine, r.x), __fmul_rn(other, r.y));
+          };
+          x[e] = turned(x[e], ox, p);
+          y[e] = turned(y[e], oy, p + 8);
+        }
+      }
+    }
+    if (is_q) {
+      if (h >= 0) {
+        uint16_t* dst = a.q_out + t * a.q_out_tok + h * a.q_out_head + 8 * p;
+        *reinterpret_cast<uint4*>(dst) = pack<T>(x);
+        *reinterpret_cast<uint4*>(dst + 64) = pack<T>(y);
+      }
+      continue;
+    }
+    float least = 0.f, most = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      least = fminf(least, fminf(x[e], y[e]));
+      most = fmaxf(most, fmaxf(x[e], y[e]));
+    }
+#pragma unroll
+    for (int m = 4; m > 0; m >>= 1) {
+      least = fminf(least, __shfl_xor_sync(0xffffffffu, least, m));
+      most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, m));
+    }
+    const float range = __fmul_rn(__fsub_rn(most, least), kFifteenth);
+    int bits = __half_as_ushort(__float2half_rn(range));
+    bits = min((bits + 15) & ~15, kKv4MaxScaleBits);
+    const float s = __half2float(__ushort_as_half(uint16_t(bits)));
+    const float inv = bits ? __frcp_rn(s) : 0.f;
+    const int z = round_small(fminf(__fmul_rn(-least, inv), 15.f));
+    if (h < 0) continue;
+    uint8_t* to = base + h * a.head_stride;
+    uint32_t* row = reinterpret_cast<uint32_t*>(to + (is_v ? kv4_v_row(a.block_slots, place) : kv4_k_row(a.block_slots, place)));
+    row[p] = codes8(x, inv, z);
+    row[p + 8] = codes8(y, inv, z);
+    if (p == 0)
+      *reinterpret_cast<uint16_t*>(to + (is_v ? kv4_v_word(a.block_slots, place) : kv4_k_word(a.block_slots, place))) =
+          uint16_t(bits | z);
   }
 }
 
@@ -293,8 +279,8 @@ __global__ void __launch_bounds__(kReadThreads) kv4_read_kernel(const __grid_con
   }
 }
 
-// Warps wanted on the card before a token is left to one warp (see rotary.cu).
-constexpr int kPartWarps = 4096;
+// Warps wanted on the card before a token is left to one warp: about one wave.
+constexpr int kPartWarps = 152 * kAppendBlocks * kAppendWarps;
 
 template <typename T>
 void launch_append(const Kv4AppendParams& a, int pairs, unsigned blocks, cudaStream_t s) {
