@@ -718,37 +718,27 @@ __device__ void kv4_consume(const Kv4Params& kp, Kv4Smem& sm, int warp, int32_t 
   named_barrier_sync(after.bar, after.threads);
 }
 
-// First item of [begin, end) that one group takes alone: a CTA's items of a
-// class come longest first, and a last one goes to all warps.  Whole warps; lane
-// l looks at item i0 + l.
-__device__ __forceinline__ int32_t kv4_first_short(const RunParams& p, int32_t begin, int32_t end, int32_t off_items) {
+// A CTA's items come prefill-class first, longest first in a class.  mid: the
+// first of [begin, end) of at most FI_TILE_DECODE packed rows; shorts: the first
+// from there on that one group takes alone (a last one goes to all warps).  Whole
+// warps; lane l looks at item i0 + l.
+__device__ __forceinline__ void kv4_phases(const RunParams& p, int32_t begin, int32_t end, int32_t off_items, int32_t& mid,
+                                           int32_t& shorts) {
   const int lane = threadIdx.x & 31;
-  for (int32_t i0 = begin; i0 < end; i0 += 32) {
-    bool is_short = true;
+  mid = shorts = end;
+  for (int32_t i0 = begin; i0 < end && shorts == end; i0 += 32) {
+    bool small = false, is_short = false;
     if (i0 + lane < end) {
-      const int2 kv = __ldg(reinterpret_cast<const int2*>(p.iws + off_items + FI_ITEM_INTS * (i0 + lane) + 4));
-      is_short = kv.y - kv.x <= kKv4GroupKeys;
+      const int32_t* item = p.iws + off_items + FI_ITEM_INTS * (i0 + lane);
+      const int2 kv = __ldg(reinterpret_cast<const int2*>(item + 4));
+      small = __ldg(item + 9) * p.group <= FI_TILE_DECODE;
+      is_short = small && kv.y - kv.x <= kKv4GroupKeys;
     }
-    const unsigned m = __ballot_sync(0xffffffffu, is_short);
-    if (m) {
-      const int32_t first = i0 + __ffs(m) - 1;
-      return first + 1 >= end ? end : first;
-    }
+    const unsigned m = __ballot_sync(0xffffffffu, small), ms = __ballot_sync(0xffffffffu, is_short);
+    if (mid == end && m) mid = i0 + __ffs(m) - 1;
+    if (ms) shorts = i0 + __ffs(ms) - 1;
   }
-  return end;
-}
-
-// A CTA's items come prefill-class first: the first of [begin, end) of at most
-// FI_TILE_DECODE packed rows.  Whole warps.
-__device__ __forceinline__ int32_t kv4_first_decode(const RunParams& p, int32_t begin, int32_t end, int32_t off_items) {
-  const int lane = threadIdx.x & 31;
-  for (int32_t i0 = begin; i0 < end; i0 += 32) {
-    const bool small = i0 + lane >= end ||
-                       __ldg(p.iws + off_items + FI_ITEM_INTS * (i0 + lane) + 9) * p.group <= FI_TILE_DECODE;
-    const unsigned m = __ballot_sync(0xffffffffu, small);
-    if (m) return min(end, i0 + __ffs(m) - 1);
-  }
-  return end;
+  if (shorts + 1 >= end) shorts = end;
 }
 
 template <typename T, int kB>
@@ -813,8 +803,8 @@ __global__ void __launch_bounds__(kKv4Threads, 1) kv4_attention_kernel(const __g
     sm.merge_last_pf = 0;
   }
   fence_mbar_init();
-  const int32_t mid = kv4_first_decode(p, begin, end, off_items);
-  const int32_t shorts = kv4_first_short(p, mid, end, off_items);
+  int32_t mid, shorts;
+  kv4_phases(p, begin, end, off_items, mid, shorts);
   const bool prefill = mid > begin;
   if (prefill && warp == kMmaWarp) {
     tc::tmem_alloc(&sm.tmem_base, kTmemCols);

@@ -307,6 +307,13 @@ __device__ void kv4_pf_queries(const Kv4Params& kp, Smem& sm, int which, int32_t
   __syncwarp();
 }
 
+// The first n of 32 bits.
+__device__ __forceinline__ uint32_t kv4_below(int n) {
+  uint32_t rest;
+  asm("shl.b32 %0, %1, %2;" : "=r"(rest) : "r"(0xffffffffu), "r"(max(n, 0)));  // 0 from 32 on
+  return ~rest;
+}
+
 // The softmax of the M tiles (see pf_softmax): thread = row = TMEM lane.
 template <typename T, bool kMask, typename Smem>
 __device__ void kv4_pf_softmax(const RunParams& p, Smem& sm, int32_t b0, int32_t b1, int32_t off_items,
@@ -326,7 +333,7 @@ __device__ void kv4_pf_softmax(const RunParams& p, Smem& sm, int32_t b0, int32_t
     if (mt < item_m_tiles(item)) {
       // visible keys of this row: [lo, lim] and the sink (a padding row, which is not stored: all, so that its warp has
       // no key to hide)
-      int lim = INT32_MAX, lo = 0;
+      int lim = INT32_MAX - 1, lo = 0;
       if (prow < nrows) {
         const int pos = rq.kv_len - rq.qo_len + (item.row0 + prow) / G;
         lim = min(causal ? pos : rq.kv_len - 1, item.kv1 - 1);
@@ -342,31 +349,38 @@ __device__ void kv4_pf_softmax(const RunParams& p, Smem& sm, int32_t b0, int32_t
         tc::fence_after_sync();
         if (j == 0) c = sm.pf.q_scale[seq & 1][prow];
         const int kbase = item.kv0 + j * kTileN;
-        const bool edge = kbase + kTileN - 1 > lim || (kMask && kbase < lo);  // causal diagonal, chunk end, window
+        // causal diagonal, chunk end, window
+        const bool edge = __any_sync(0xffffffffu, kbase + kTileN - 1 > lim || (kMask && kbase < lo));
         uint32_t sv[2][32];
-        // 64 columns of S; the hidden keys of an edge tile -inf
-        auto load = [&](int half) {
+        auto load = [&](int half) {  // 64 columns of S
           tc::tmem_ld32(s_cols + 64 * half, sv[0]);
           tc::tmem_ld32(s_cols + 64 * half + 32, sv[1]);
           tc::tmem_ld_wait();
-          if (edge) {
-            const int k0 = kbase + 64 * half;
-#pragma unroll
-            for (int e = 0; e < 64; ++e)
-              if (k0 + e > lim || (kMask && k0 + e < lo && k0 + e >= var.sink)) sv[e >> 5][e & 31] = 0xff800000u;  // -inf
-          }
         };
         // row max in four independent chains of three-input maxima
         float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
           load(half);
+          if (edge) {  // the hidden keys' columns -inf, here and for the second pass over them
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int k0 = kbase + 64 * half + 32 * h;
+              uint32_t seen = kv4_below(lim - k0 + 1);
+              if (kMask) seen &= ~kv4_below(lo - k0) | kv4_below(var.sink - k0);
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!(seen & (1u << e))) sv[h][e] = 0xff800000u;  // -inf
+              tc::tmem_st32(s_cols + 64 * half + 32 * h, sv[h]);
+            }
+          }
 #pragma unroll
           for (int e = 0; e < 64; e += 8)
 #pragma unroll
             for (int a = 0; a < 4; ++a)
               mx4[a] = max3(mx4[a], __uint_as_float(sv[e >> 5][(e & 31) + a]), __uint_as_float(sv[e >> 5][(e & 31) + 4 + a]));
         }
+        if (edge) tc::tmem_st_wait();
         const float mx = fmaxf(max3(mx4[0], mx4[1], mx4[2]), mx4[3]) * c;
         const float m_old = mrun;
         const float m_new = (mx > m_old + kLazyRescale) ? mx : m_old;
@@ -429,49 +443,74 @@ __device__ void kv4_pf_softmax(const RunParams& p, Smem& sm, int32_t b0, int32_t
         ++items;
         have_o = ok;
       }
-      uint32_t ov[4][32];
-      if (have_o) {
-        tc::fence_after_sync();
+      // The row's values go back to tensor memory in their type, and from there to the lanes that store them: four lanes a
+      // row, 64 contiguous bytes (a lane a row met a cache line of its own in every store: 3 us an item).
+      const float inv = lrun_r > 0.f ? 1.f / lrun_r : 0.f;
+      const bool partial = item.part >= 0;
+      int64_t at = -1;  // of the row, in bytes
+      if (prow < nrows && !sm.abort) {
+        const float lse = lrun > 0.f ? (mrun + __log2f(lrun)) * 0.69314718055994531f : -INFINITY;
+        const int row = item.row0 + prow, t = row / G, head = item.hk * G + (row - t * G);
+        const int64_t tok = int64_t(rq.qo_start) + t, part = int64_t(item.part) + prow;
+        if (partial) {
+          at = 4 * kHeadDim * part;
+          p.fws[part] = lse;
+        } else {
+          at = 2 * (tok * p.o_stride_tok + int64_t(head) * p.o_stride_head);
+          if (p.lse) p.lse[tok * p.num_qo_heads + head] = lse;
+        }
+      }
+      if (have_o) tc::fence_after_sync();
+      // Word 4 i + e (e < 4) of 16 goes to column 2 i + e (e < 2) or 2 i + e + 6.  Dim d of each eight of O lies in column
+      // 2 d (d < 4) or 2 d - 7.
+      constexpr auto word_of = [](int column) { return (column & ~15) + 4 * ((column >> 1) & 3) + 2 * (column >> 3 & 1) + (column & 1); };
+      constexpr auto column_of = [](int dim) { return (dim & ~7) + ((dim & 7) < 4 ? 2 * (dim & 7) : 2 * (dim & 7) - 7); };
+      uint32_t ov[2][32], out[32];
 #pragma unroll
-        for (int h = 0; h < 4; ++h) tc::tmem_ld32(o_cols + 32 * h, ov[h]);
+      for (int e = 0; e < 64; ++e) ov[e >> 5][e & 31] = 0u;
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        if (have_o) {
+          tc::tmem_ld32(o_cols + 64 * h, ov[0]);
+          tc::tmem_ld32(o_cols + 64 * h + 32, ov[1]);
+          tc::tmem_ld_wait();
+        }
+        auto dim = [&](int d) { return __uint_as_float(ov[column_of(d) >> 5][column_of(d) & 31]) * inv; };
+        if (partial) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) out[e] = __float_as_uint(dim(word_of(32 * u + e)));
+            tc::tmem_st32(o_cols + 64 * h + 32 * u, out);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) out[e] = tc::pack2<T>(dim(2 * word_of(e)), dim(2 * word_of(e) + 1));
+          tc::tmem_st32(o_cols + 32 * h, out);
+        }
+      }
+      tc::tmem_st_wait();
+      uint8_t* const rows = partial ? reinterpret_cast<uint8_t*>(p.fws + p.partial_o_offset) : reinterpret_cast<uint8_t*>(p.o);
+#pragma unroll 1
+      for (int n = 0; n < (partial ? 4 : 2); ++n) {  // 16 rows, 256 bytes of each
+        tc::tmem_ld_quads(o_cols + (uint32_t(16 * (n & 1)) << 16) + 64 * (n >> 1), out);
         tc::tmem_ld_wait();
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int64_t to = __shfl_sync(0xffffffffu, at, 16 * (n & 1) + 8 * u + (lane >> 2));
+          if (to >= 0) {
+            uint4* const dst = reinterpret_cast<uint4*>(rows + to + 256 * (n >> 1)) + (lane & 3);
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+              dst[4 * g] = make_uint4(out[8 * g + 2 * u], out[8 * g + 2 * u + 1], out[8 * g + 4 + 2 * u], out[8 * g + 5 + 2 * u]);
+          }
+          __syncwarp();
+        }
+      }
+      if (have_o) {
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.o_free[mt]);
-      } else {
-#pragma unroll
-        for (int h = 0; h < 4; ++h)
-#pragma unroll
-          for (int e = 0; e < 32; ++e) ov[h][e] = 0u;
-      }
-      if (prow < nrows && !sm.abort) {
-        const int row = item.row0 + prow, t = row / G, head = item.hk * G + (row - t * G);
-        const int64_t tok = int64_t(rq.qo_start) + t;
-        const float inv = lrun_r > 0.f ? 1.f / lrun_r : 0.f;
-        const float lse = lrun > 0.f ? (mrun + __log2f(lrun)) * 0.69314718055994531f : -INFINITY;
-        // dim d of each eight lies in column 2 d (d < 4) or 2 d - 7
-        auto dim = [&](int h, int e0, int d) { return __uint_as_float(ov[h][e0 + (d < 4 ? 2 * d : 2 * d - 7)]) * inv; };
-        if (item.part < 0) {
-          uint4* dst = reinterpret_cast<uint4*>(p.o + tok * p.o_stride_tok + int64_t(head) * p.o_stride_head);
-#pragma unroll
-          for (int h = 0; h < 4; ++h)
-#pragma unroll
-            for (int e = 0; e < 32; e += 8)
-              dst[4 * h + e / 8] = make_uint4(tc::pack2<T>(dim(h, e, 0), dim(h, e, 1)), tc::pack2<T>(dim(h, e, 2), dim(h, e, 3)),
-                                              tc::pack2<T>(dim(h, e, 4), dim(h, e, 5)), tc::pack2<T>(dim(h, e, 6), dim(h, e, 7)));
-          if (p.lse) p.lse[tok * p.num_qo_heads + head] = lse;
-        } else {
-          const int64_t part = int64_t(item.part) + prow;
-          float4* dst = reinterpret_cast<float4*>(p.fws + p.partial_o_offset + part * kHeadDim);
-#pragma unroll
-          for (int h = 0; h < 4; ++h)
-#pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              dst[8 * h + e / 4] = make_float4(dim(h, e, 0), dim(h, e, 1), dim(h, e, 2), dim(h, e, 3));
-              dst[8 * h + e / 4 + 1] = make_float4(dim(h, e, 4), dim(h, e, 5), dim(h, e, 6), dim(h, e, 7));
-            }
-          p.fws[part] = lse;
-        }
       }
     }
     if (ntiles > 0) ++seq;
