@@ -197,19 +197,6 @@ __device__ void kv4_pf_widen(const Kv4Params& kp, Smem& sm, int32_t b0, int32_t 
   const int key = r % kKv4RawKeys, place = key & (slots - 1);
   const uint8_t* const raw = sm.pf.raw[half] + (key >> log2_slots) * bytes;
   uint32_t kt = 0, pe = 0;
-  // K of a tile goes before V of the tile before: V's buffer comes free late (P V
-  // of the tile two before), and the products want the next K before they start
-  // on this P.  So a thread holds V's row, its scale and zero point of one tile.
-  uint4 v[4] = {};
-  uint32_t v_scale = 0, v_zero = 0;
-  auto put_v = [&](uint32_t t) {
-    if (!warp_wait(&sm.v_empty[t & 1], ((t >> 1) & 1) ^ 1, &sm.abort)) return false;
-    kv4_widen(v[0], v[1], v[2], v[3], v_scale, v_zero, smem_u32(sm.pf.v[t & 1]), r);
-    fence_proxy_async_smem();  // read by the tensor core
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sm.v_full[t & 1]);
-    return true;
-  };
   for (int32_t i = b0; i < b1; ++i) {
     const Item it = load_item(kp.run.iws, off_items, i);
     const int ntiles = item_kv_tiles(it);
@@ -220,25 +207,20 @@ __device__ void kv4_pf_widen(const Kv4Params& kp, Smem& sm, int32_t b0, int32_t 
       const uint32_t good = sm.pf.good[half][key >> 5] >> (key & 31) & 1u ? 0xFFF0u : 0u;
       const uint32_t kw = *reinterpret_cast<const uint16_t*>(raw + kv4_k_word(slots, place));
       const uint32_t vw = *reinterpret_cast<const uint16_t*>(raw + kv4_v_word(slots, place));
-      uint4 k[4], next[4];
+      uint4 k[4], v[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int at = 16 * ((u + (lane >> 1)) & 3);
         k[u] = *reinterpret_cast<const uint4*>(raw + kv4_k_row(slots, place) + at);
-        next[u] = *reinterpret_cast<const uint4*>(raw + kv4_v_row(slots, place) + at);
+        v[u] = *reinterpret_cast<const uint4*>(raw + kv4_v_row(slots, place) + at);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.raw_empty[half]);
       if (!warp_wait(&sm.k_empty[st], ((kt >> 1) & 1) ^ 1, &sm.abort)) return;
       kv4_widen(k[0], k[1], k[2], k[3], min(kw & good, uint32_t(kKv4MaxScaleBits)), kw & 15u, smem_u32(sm.pf.k[st]), r);
-      fence_proxy_async_smem();
+      fence_proxy_async_smem();  // read by the tensor core
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.k_full[st]);
-      if (kt > 0 && !put_v(kt - 1)) return;
-#pragma unroll
-      for (int u = 0; u < 4; ++u) v[u] = next[u];
-      v_scale = min(vw & good, uint32_t(kKv4MaxScaleBits));
-      v_zero = vw & 15u;
       if (j == 0) {
         if (!warp_wait(&sm.q_raw, pe & 1, &sm.abort)) return;
         sm.pf.q_scale[pe & 1][r] = kp.run.scale_log2 * kv4_turn_query<T>(sm.pf.q[0], r);
@@ -247,9 +229,13 @@ __device__ void kv4_pf_widen(const Kv4Params& kp, Smem& sm, int32_t b0, int32_t 
         if (lane == 0) mbar_arrive(&sm.q_full);
         ++pe;
       }
+      if (!warp_wait(&sm.v_empty[st], ((kt >> 1) & 1) ^ 1, &sm.abort)) return;
+      kv4_widen(v[0], v[1], v[2], v[3], min(vw & good, uint32_t(kKv4MaxScaleBits)), vw & 15u, smem_u32(sm.pf.v[st]), r);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.v_full[st]);
     }
   }
-  if (kt > 0) put_v(kt - 1);
 }
 
 // Q of items [b0, b1) by warps 2 and 3 (which = 0, 1): its load, and M tile B's rows.
@@ -339,8 +325,10 @@ __device__ void kv4_pf_softmax(const RunParams& p, Smem& sm, int32_t b0, int32_t
         lim = min(causal ? pos : rq.kv_len - 1, item.kv1 - 1);
         if (kMask) lo = window_low(var, pos);
       }
-      // lrun: sum of the fp32 P (for LSE); lrun_r: of the fp16 P that the product takes (for O)
-      float mrun = -INFINITY, lrun = 0.f, lrun_r = 0.f, c = 0.f;
+      // lrun: sum of the fp32 P.  The product takes them in fp16, each off by at most half a step, 2^-11 of itself: O is then
+      // off by at most 2^-11 of the sum of P |V|, whichever sum divides it.  (The sum of the rounded ones, beside this one,
+      // took 7 % of the time.)
+      float mrun = -INFINITY, lrun = 0.f, c = 0.f;
       bool ok = true;
       for (int j = 0; j < ntiles; ++j) {
         ok = ok && warp_wait(&sm.s_full[mt], tiles & 1, &sm.abort);
@@ -397,19 +385,15 @@ __device__ void kv4_pf_softmax(const RunParams& p, Smem& sm, int32_t b0, int32_t
             tc::tmem_st32(o_cols + 32 * h, sv[0]);
           }
           tc::tmem_st_wait();
-          if (rescale) {
-            lrun *= alpha;
-            lrun_r *= alpha;
-          }
+          if (rescale) lrun *= alpha;
         }
         // P = 2^(s c - m) as fp16 pairs over the first 64 columns of the S
         // buffer, published in two halves of 64 keys each
         const float msub = (m_new == -INFINITY) ? 0.f : m_new;
         const float2 cc = make_float2(c, c), nms = make_float2(-msub, -msub);
-        float2 sum4[4], sumr[2];
+        float2 sum4[4];
 #pragma unroll
         for (int a = 0; a < 4; ++a) sum4[a] = make_float2(0.f, 0.f);
-        sumr[0] = sumr[1] = make_float2(0.f, 0.f);
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
           load(half);
@@ -422,7 +406,6 @@ __device__ void kv4_pf_softmax(const RunParams& p, Smem& sm, int32_t b0, int32_t
               const float2 pe = make_float2(ex2(x.x), ex2(x.y));
               sum4[e & 3] = add2(sum4[e & 3], pe);
               pk[e] = tc::pack2<__half>(pe.x, pe.y);
-              tc::add_packed2<__half>(sumr[e & 1], pk[e]);
             }
             tc::tmem_st16(s_cols + 32 * half + 16 * h, pk);
           }
@@ -433,8 +416,6 @@ __device__ void kv4_pf_softmax(const RunParams& p, Smem& sm, int32_t b0, int32_t
         }
         const float2 s01 = add2(sum4[0], sum4[1]), s23 = add2(sum4[2], sum4[3]), s4 = add2(s01, s23);
         lrun += s4.x + s4.y;
-        const float2 sr = add2(sumr[0], sumr[1]);
-        lrun_r += sr.x + sr.y;
         mrun = m_new;
       }
       bool have_o = false;
@@ -445,7 +426,7 @@ __device__ void kv4_pf_softmax(const RunParams& p, Smem& sm, int32_t b0, int32_t
       }
       // The row's values go back to tensor memory in their type, and from there to the lanes that store them: four lanes a
       // row, 64 contiguous bytes (a lane a row met a cache line of its own in every store: 3 us an item).
-      const float inv = lrun_r > 0.f ? 1.f / lrun_r : 0.f;
+      const float inv = lrun > 0.f ? 1.f / lrun : 0.f;
       const bool partial = item.part >= 0;
       int64_t at = -1;  // of the row, in bytes
       if (prow < nrows && !sm.abort) {
