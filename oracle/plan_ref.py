@@ -64,6 +64,12 @@ Rule:
     Plans over the 4-bit cache (kv_bits 4, a magic of their own): no multi-head
     units, a decode-class key costs ceil(decode_cost_weight / 4), and behind the
     merge counters (rounded up to a multiple of 4) are 16 per merge unit, one for each of its rows.
+    There a range of len > chunk keys goes into items of ceil(len / ceil(len /
+    chunk)) keys, rounded up to the granule.  And where split_factor is 1, a
+    class has at most `ctas` units but more items, c is the shortest longer
+    chunk (a multiple of the granule) with at most `ctas` items, and its longest
+    item plus 256 is less than the ctas-th and the next longest item of the
+    chunk of 3 plus 512, c is the class's chunk.
  6. Output: header (with the variant: window, sink, soft-cap bits, and for
     RoPE its position capacity, theta and scale bits and the table offset;
     then the count of late units, the partial rows used, the batch's query
@@ -322,9 +328,39 @@ def _plan(cfg, reqs, num_shared, shared_page_size, block_of, total_qo, num_qo_he
         want = max(min_chunk, _ceil_div(total[T], ctas * cfg["split_factor"]))
         return _ceil_div(want, granule[T]) * granule[T]
 
+    def piece(T, n, ck):
+        if not kv4 or n <= ck:
+            return ck
+        return _ceil_div(_ceil_div(n, _ceil_div(n, ck)), granule[T]) * granule[T]
+
+    def one_wave(T, c0, ctas):
+        lens = [[e - s for s, e in u[6]] for u in units if u[3] == T]
+        if not kv4 or cfg["split_factor"] != 1 or len(lens) > ctas:
+            return c0
+
+        def cut(ck):
+            return [min(piece(T, n, ck), n - k) for ns in lens for n in ns for k in range(0, n, piece(T, n, ck))]
+
+        def count(ck):
+            return sum(max(1, sum(_ceil_div(n, piece(T, n, ck)) for n in ns)) for ns in lens)
+
+        last = max([n for ns in lens for n in ns], default=0)
+        if count(c0) <= ctas or count(max(c0, _ceil_div(last, granule[T]) * granule[T])) > ctas:
+            return c0
+        lo, hi = c0 // granule[T], _ceil_div(last, granule[T])
+        while hi - lo > 1:
+            mid = (lo + hi) // 2
+            lo, hi = (mid, hi) if count(mid * granule[T]) > ctas else (lo, mid)
+        order = sorted(cut(c0), reverse=True)
+        if len(order) <= ctas:
+            return c0
+        c1 = hi * granule[T]
+        return c1 if max(cut(c1)) + ITEM_COST_TOKENS < order[ctas - 1] + order[ctas] + 2 * ITEM_COST_TOKENS else c0
+
     units_pre = sum(u[3] == TILE_PREFILL for u in units)
     min_pre = cfg["prefill_min_chunk"] * (4 if diff and 3 * units_pre > C else 1)
-    chunk = {TILE_PREFILL: pick(TILE_PREFILL, min_pre, C)}
+    chunk = {TILE_PREFILL: one_wave(TILE_PREFILL, pick(TILE_PREFILL, min_pre, C), C)}
+
     def lead_of(T, rng):
         # tiles of a sink that share the item of a one-chunk window (differential, tensor-core path)
         if not diff or T != TILE_PREFILL or len(rng) != 2 or rng[1][1] - rng[1][0] > chunk[TILE_PREFILL] \
@@ -333,9 +369,10 @@ def _plan(cfg, reqs, num_shared, shared_page_size, block_of, total_qo, num_qo_he
         return _ceil_div(rng[0][1], 128)
 
     # prefill-class items; the decode class counts the CTAs they leave free when they take at most half
-    n_pre = sum(max(1, sum(_ceil_div(e - s, chunk[TILE_PREFILL]) for s, e in u[6][1 if lead_of(u[3], u[6]) else 0:]))
-                for u in units if u[3] == TILE_PREFILL)
-    chunk[TILE_DECODE] = pick(TILE_DECODE, cfg["decode_min_chunk"], C - n_pre if 0 < 2 * n_pre <= C else C)
+    n_pre = sum(max(1, sum(_ceil_div(e - s, piece(TILE_PREFILL, e - s, chunk[TILE_PREFILL]))
+                           for s, e in u[6][1 if lead_of(u[3], u[6]) else 0:])) for u in units if u[3] == TILE_PREFILL)
+    dec_ctas = C - n_pre if 0 < 2 * n_pre <= C else C
+    chunk[TILE_DECODE] = one_wave(TILE_DECODE, pick(TILE_DECODE, cfg["decode_min_chunk"], dec_ctas), dec_ctas)
     # a key of the 4-bit cache moves a quarter of the bytes
     weight = {TILE_DECODE: _ceil_div(cfg["decode_cost_weight"], 4) if kv4 else cfg["decode_cost_weight"],
               TILE_PREFILL: cfg["prefill_cost_weight"]}
@@ -353,8 +390,8 @@ def _plan(cfg, reqs, num_shared, shared_page_size, block_of, total_qo, num_qo_he
             prefill_caches |= 2 if b < num_shared else 1
         ck = chunk_mh if heads > 1 else chunk[T]
         lead = lead_of(T, rng)
-        pieces = [(s_ + i * ck, min(e_, s_ + (i + 1) * ck))
-                  for s_, e_ in rng[1 if lead else 0:] for i in range(_ceil_div(e_ - s_, ck))]
+        pieces = [(k, min(e_, k + piece(T, e_ - s_, ck)))
+                  for s_, e_ in rng[1 if lead else 0:] for k in range(s_, e_, piece(T, e_ - s_, ck))]
         n = max(1, len(pieces))
         nrows = (r1 - r0) * (2 if diff else 1)  # partial rows of a chunk: one per row and map
         base, m = -1, -1

@@ -25,6 +25,11 @@
 //    min_chunk unless there are three CTAs a unit; units longer than a chunk are split into chunks whose fp32
 //    partial states are merged by the kernel (a differential prefill-class
 //    unit whose window is one chunk has its sink's tiles in the same item);
+//  * over the 4-bit cache, whose kernels read a key in a quarter of the time
+//    and so pay more for an item beside it, a range is split evenly and a class
+//    of at most as many units as CTAs takes chunks long enough to run all at
+//    once, where that ends sooner than two of the chunks above, one behind
+//    the other;
 //  * chunks are dealt out longest-first to the least-loaded CTA (LPT); an
 //    item's cost is its KV length plus a fixed FI_ITEM_COST_TOKENS (the
 //    per-item latency of the kernel), times the class weight, so that many
@@ -35,6 +40,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <functional>
 #include <utility>
 #include <vector>
 
@@ -284,7 +290,63 @@ fi_status plan_requests(const fi_plan_config* cfg, const std::vector<Req>& reqs,
     int64_t c = std::max<int64_t>(min_chunk, ceil_div(total, slots));
     return ceil_div(c, granule) * granule;
   };
-  const int64_t gran_dec = std::max(max_page, FI_GRANULE_DECODE);
+  const int64_t gran_dec = std::max(max_page, FI_GRANULE_DECODE), gran_pre = std::max(max_page, FI_GRANULE_PREFILL);
+  // Length of the pieces of a range of `len` keys: of a 4-bit cache as equal as the granule allows.  (Four prompt parts
+  // of a window beside 24 decodes: 31.0 -> 26.0 us: of 1024 and the rest of 1090 .. 1280 keys
+  // the longer piece was what the call waited for.)
+  auto piece = [&](int32_t tile, int64_t len, int64_t chunk) {
+    if (!kv4 || len <= chunk) return chunk;
+    const int64_t gran = tile == FI_TILE_DECODE ? gran_dec : gran_pre;
+    return ceil_div(ceil_div(len, ceil_div(len, chunk)), gran) * gran;
+  };
+  // The chunk of a class over the 4-bit cache that runs on `slots` CTAs at once, if that is worth it.  Among the slots + 1
+  // longest pieces two share a CTA, so the plan by c0 takes at least the shortest two of them.  (Two requests of 99991 to
+  // 131072 keys and 8 KV heads: 53.5 -> 48.4 us.)
+  auto one_wave = [&](int32_t tile, int64_t c0, int64_t slots) {
+    if (!kv4 || cfg->split_factor != 1) return c0;
+    const int64_t gran = tile == FI_TILE_DECODE ? gran_dec : gran_pre;
+    int64_t units_of = 0, longest = 0;
+    for (const Unit& u : units) {
+      if (u.tile != tile) continue;
+      ++units_of;
+      for (int r = 0; r < u.n_ranges; ++r) longest = std::max(longest, u.r_end[r] - u.r_begin[r]);
+    }
+    if (units_of > slots) return c0;
+    auto items_of = [&](int64_t c) {
+      int64_t n = 0;
+      for (const Unit& u : units) {
+        if (u.tile != tile) continue;
+        int64_t m = 0;
+        for (int r = 0; r < u.n_ranges; ++r) {
+          const int64_t len = u.r_end[r] - u.r_begin[r];
+          m += ceil_div(len, piece(tile, len, c));
+        }
+        n += std::max<int64_t>(m, 1);
+      }
+      return n;
+    };
+    int64_t lo = c0 / gran, hi = std::max(lo, ceil_div(longest, gran));  // items_of(lo gran) > slots >= items_of(hi gran)
+    if (items_of(c0) <= slots || items_of(hi * gran) > slots) return c0;
+    while (hi - lo > 1) {
+      const int64_t mid = lo + (hi - lo) / 2;
+      (items_of(mid * gran) > slots ? lo : hi) = mid;
+    }
+    std::vector<int64_t> lens;
+    int64_t one = 0;  // the longest piece of the one wave
+    for (const Unit& u : units) {
+      if (u.tile != tile) continue;
+      for (int r = 0; r < u.n_ranges; ++r) {
+        const int64_t len = u.r_end[r] - u.r_begin[r], step = piece(tile, len, c0);
+        for (int64_t k = 0; k < len; k += step) lens.push_back(std::min(step, len - k));
+        one = std::max(one, std::min(len, piece(tile, len, hi * gran)));
+      }
+    }
+    if (int64_t(lens.size()) <= slots) return c0;
+    std::nth_element(lens.begin(), lens.begin() + slots, lens.end(), std::greater<int64_t>());
+    const int64_t last = lens[size_t(slots)];
+    const int64_t before = *std::min_element(lens.begin(), lens.begin() + slots);
+    return one + FI_ITEM_COST_TOKENS < before + last + 2 * FI_ITEM_COST_TOKENS ? hi * gran : c0;
+  };
   // A differential unit that is split walks its keys three times instead of
   // twice, with two products a key and map, so it gains only where at least
   // three chunks a unit run at once: with fewer CTAs a unit, four times the
@@ -298,8 +360,9 @@ fi_status plan_requests(const fi_plan_config* cfg, const std::vector<Req>& reqs,
     for (const Unit& u : units) units_pre += u.tile == FI_TILE_PREFILL;
     if (3 * units_pre > cfg->num_ctas) min_pre *= 4;
   }
-  const int64_t chunk_pre = pick_chunk(total_pre, min_pre, std::max(max_page, FI_GRANULE_PREFILL),
-                                       int64_t(cfg->num_ctas) * cfg->split_factor);
+  const int64_t chunk_pre =
+      one_wave(FI_TILE_PREFILL, pick_chunk(total_pre, min_pre, gran_pre, int64_t(cfg->num_ctas) * cfg->split_factor),
+               cfg->num_ctas);
   // A differential prefill-class unit with a sink range takes it into the item
   // of its window, where that is one chunk and the tensor-core path runs it:
   // as a chunk of its own it would make the unit a split one (four prompt
@@ -317,11 +380,15 @@ fi_status plan_requests(const fi_plan_config* cfg, const std::vector<Req>& reqs,
   for (const Unit& u : units) {
     if (u.tile != FI_TILE_PREFILL) continue;
     int64_t n = 0;
-    for (int r = sink_tiles(u) > 0 ? 1 : 0; r < u.n_ranges; ++r) n += ceil_div(u.r_end[r] - u.r_begin[r], chunk_pre);
+    for (int r = sink_tiles(u) > 0 ? 1 : 0; r < u.n_ranges; ++r) {
+      const int64_t len = u.r_end[r] - u.r_begin[r];
+      n += ceil_div(len, piece(u.tile, len, chunk_pre));
+    }
     n_pre += std::max<int64_t>(n, 1);
   }
   const int64_t dec_ctas = (n_pre > 0 && 2 * n_pre <= cfg->num_ctas) ? cfg->num_ctas - n_pre : cfg->num_ctas;
-  const int64_t chunk_dec = pick_chunk(total_dec, cfg->decode_min_chunk, gran_dec, dec_ctas * cfg->split_factor);
+  const int64_t chunk_dec =
+      one_wave(FI_TILE_DECODE, pick_chunk(total_dec, cfg->decode_min_chunk, gran_dec, dec_ctas * cfg->split_factor), dec_ctas);
   // a multi-head unit's chunk: the K/V bytes of a one-head chunk, rounded up
   const int32_t mh = fi_mh_heads(group, num_kv_heads);
   const int64_t chunk_mh = std::max(gran_dec, ceil_div(ceil_div(chunk_dec, mh), gran_dec) * gran_dec);
@@ -343,7 +410,10 @@ fi_status plan_requests(const fi_plan_config* cfg, const std::vector<Req>& reqs,
     if (u.tile == FI_TILE_PREFILL) prefill_caches |= u.b < num_shared ? 2 : 1;
     const int32_t lead = sink_tiles(u);
     int64_t n = 0;
-    for (int r = lead > 0 ? 1 : 0; r < u.n_ranges; ++r) n += ceil_div(u.r_end[r] - u.r_begin[r], chunk);
+    for (int r = lead > 0 ? 1 : 0; r < u.n_ranges; ++r) {
+      const int64_t len = u.r_end[r] - u.r_begin[r];
+      n += ceil_div(len, piece(u.tile, len, chunk));
+    }
     const bool empty = n == 0;
     if (empty) n = 1;
     int32_t merge_id = -1;
@@ -390,8 +460,10 @@ fi_status plan_requests(const fi_plan_config* cfg, const std::vector<Req>& reqs,
     if (empty) {
       emit(0, 0);
     } else {
-      for (int r = lead > 0 ? 1 : 0; r < u.n_ranges; ++r)
-        for (int64_t k0 = u.r_begin[r]; k0 < u.r_end[r]; k0 += chunk) emit(k0, std::min(u.r_end[r], k0 + chunk));
+      for (int r = lead > 0 ? 1 : 0; r < u.n_ranges; ++r) {
+        const int64_t step = piece(u.tile, u.r_end[r] - u.r_begin[r], chunk);
+        for (int64_t k0 = u.r_begin[r]; k0 < u.r_end[r]; k0 += step) emit(k0, std::min(u.r_end[r], k0 + step));
+      }
     }
   }
   // Cascade merge entries, in ordinary-unit order: the rows of each unit in

@@ -132,6 +132,49 @@ def test_plan_matches_reference(seed):
     assert all(ws[int(ws[7]) + 16 * i + 12] == 0 for i in range(info.num_items))  # no multi-head units
 
 
+def _items(ws, info):
+    at = int(ws[7])
+    return [tuple(int(x) for x in ws[at + 16 * i:at + 16 * i + 6]) for i in range(info.num_items)]
+
+
+@pytest.mark.parametrize("qo,kv,hq,hkv,kw,ctas,most", [
+    ([1, 1], [99991, 131072], 64, 8, {}, 152, 152),                    # 160 items by the shares alone: one wave
+    ([1, 1, 1], [5000, 70000, 64], 8, 2, {}, 7, None),                 # one wave would leave 70000 keys to one CTA
+    ([400], [9000], 32, 8, {}, 152, 152),                              # prefill class
+    ([200, 60], [4000, 2500], 16, 4, {"window_left": 1023, "sink_tokens": 4}, 152, 152),
+    ([1] * 40, [3000] * 40, 8, 4, {}, 152, None),                      # more units than CTAs
+    ([1, 1], [99991, 131072], 64, 8, {"split_factor": 2}, 152, None),
+])
+def test_plan_splits_evenly_and_in_one_wave(qo, kv, hq, hkv, kw, ctas, most):
+    page = 16
+    pages = [-(-n // page) for n in kv]
+    args = (np.cumsum([0] + qo).astype(np.int32), np.cumsum([0] + pages).astype(np.int32), [],
+            np.array([n - (p - 1) * page for n, p in zip(kv, pages)], np.int32), hq, hkv, 128, page, 1)
+    cfg = fi.make_plan_config(ctas, kv_bits=4, **kw)
+    st, ws, info = fi.plan_host(cfg, *args)
+    st_ref, ws_ref, _ = plan_ref.make_plan(cfg.as_dict(), *args, 0)
+    assert st == st_ref == 0 and np.array_equal(ws[:len(ws_ref)], ws_ref)
+    if most:
+        assert info.num_items <= most
+    units = {}
+    for b, hk, r0, r1, k0, k1 in _items(ws, info):
+        units.setdefault((b, hk, r0), []).append((k0, k1))
+    granule = 64 if max(q * hq // hkv for q in qo) <= 16 else 128
+    for at in units.values():
+        runs = [[p] for p in sorted(at)[:1]]
+        for p in sorted(at)[1:]:  # a range's pieces follow one another
+            if runs[-1][-1][1] == p[0]:
+                runs[-1].append(p)
+            else:
+                runs.append([p])
+        for run in runs:
+            steps = {b - a for a, b in run[:-1]}
+            assert len(steps) <= 1
+            if steps:  # equal but for the granule, which the last piece makes up for
+                n, step = len(run), steps.pop()
+                assert step - (run[-1][1] - run[-1][0]) < n * granule
+
+
 @pytest.mark.parametrize("field,value,status", [("kv_bits", 3, 1), ("kv_bits", -4, 1), ("kv_bits", 8, 1),
                                                 ("logits_soft_cap", 30.0, 2), ("rope_max_positions", 4096, 2),
                                                 ("differential", 1, 2)])
