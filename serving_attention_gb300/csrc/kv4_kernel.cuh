@@ -21,10 +21,20 @@
 // Twelve warps compute, in three groups.  A long chunk's keys go over all of them
 // in consecutive parts; short chunks (up to kKv4GroupKeys keys), whose time is
 // latency and not bytes, go to the groups in turn, three at once.  Each computing
-// warp has a ring of stages of its own, 32 keys each; one loader warp fills them,
-// a lane a ring, one bulk copy a block (keys, values and their words lie
+// warp has a ring of stages of its own, 32 keys each; four loader warps fill three
+// rings each, a lane a ring, one bulk copy a block (keys, values and their words lie
 // together), across items.  The only barriers are those that join an item's
 // states.
+//
+// What bounds it: the bytes of a long cache, its 132 a key and head, for up to
+// eight query rows a key head; more rows go over the keys again, from L2, at half
+// that rate.  Beyond a request's first 8192 keys every further one costs what its
+// bytes do at 6.7 TB/s.  64 requests of 512 to 32768 keys, 32 + 8 heads: 123 us,
+// 5.3 TB/s (97 us at the copy rate); two of 99991 and 131072 keys, 64 + 8 heads: 48 us
+// (35).  One loader warp for all rings brought 4.4 TB/s; eight computing warps that
+// widened the codes took 157 us.  Short requests are latency: four of up to 512
+// keys, 8 + 2 heads, 6.6 us, of which the launch and the plan's loads are 3; 64 of
+// 64 to 512 keys on pages of one token 16 us, at 144 bytes a copy.
 #pragma once
 #include "attention_kernel.cuh"
 #include "kv4_layout.h"

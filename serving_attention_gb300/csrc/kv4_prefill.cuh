@@ -25,6 +25,19 @@
 //    divides 128, else warps 2 and 3 copy its rows), and warps 4 .. 7 turn the rows
 //    of M tile A, warps 2 and 3 those of B, a thread a row, in place;
 //  * warp 1 issues the products (pf_mma), warps 8 .. 15 the softmax.
+//
+// What bounds it: no one unit, but the chain of a tile of 128 keys, 3.3 thousand
+// clocks.  An M tile's S has no second buffer in tensor memory, so its softmax
+// (2.1 thousand) and its P V and next S (1.1) follow one another, the other M tile's
+// between them; widening a tile takes 2.3.  Tensor cores are busy for 1.1 of the 3.3,
+// issue slots for two thirds.  Eight prompts of 128 to 2048 tokens behind up to 2048,
+// 32 + 8 heads: 314 us, 1.1 PFLOP/s (188 us at the rate of plain bf16 products; 285 us
+// from a cache in 16 bits, four times the memory).  What it took: straight code
+// as short as can be (the roles' loops together are longer than the instruction
+// cache: the widening unrolled cost 80 us), one row sum (22 us), hidden keys as
+// bits and once a tile, and output by four lanes a row (together 22 us, and 6 of
+// every short call).  Not kept: units of 64 keys with S two units ahead, whose
+// products read Q twice as often and need half again the instructions (364 us).
 #pragma once
 #include "kv4_params.h"
 #include "attention_kernel.cuh"

@@ -291,9 +291,9 @@ fi_status plan_requests(const fi_plan_config* cfg, const std::vector<Req>& reqs,
     return ceil_div(c, granule) * granule;
   };
   const int64_t gran_dec = std::max(max_page, FI_GRANULE_DECODE), gran_pre = std::max(max_page, FI_GRANULE_PREFILL);
-  // Length of the pieces of a range of `len` keys: of a 4-bit cache as equal as the granule allows.  (Four prompt parts
-  // of a window beside 24 decodes: 31.0 -> 26.0 us: of 1024 and the rest of 1090 .. 1280 keys
-  // the longer piece was what the call waited for.)
+  // Length of the pieces of a range of `len` keys: over a 4-bit cache as equal as the granule allows, the longest is what
+  // the call waits for.  (Four prompt parts of a window beside 24 decodes, ranges of 1090 to 1280 keys in pieces of 1024 and
+  // the rest or in equal ones: 31.0 -> 26.0 us.)
   auto piece = [&](int32_t tile, int64_t len, int64_t chunk) {
     if (!kv4 || len <= chunk) return chunk;
     const int64_t gran = tile == FI_TILE_DECODE ? gran_dec : gran_pre;
