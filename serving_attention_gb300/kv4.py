@@ -64,10 +64,12 @@ def _cache(cache: torch.Tensor, page_size: int, heads: int, index: int):
         per_page = _page_bytes[page_size] = page_bytes(page_size)
     if cache.dtype is not torch.uint8 or cache.get_device() != index:
         raise TypeError("the cache must be uint8 on the tensors' device")
-    shape = cache.shape
-    if len(shape) != 3 or shape[1] != heads or shape[2] != per_page or cache.stride(2) != 1:
-        raise ValueError(f"the cache is [pages, {heads} heads, {per_page} bytes], the last dimension contiguous")
-    return cache.data_ptr(), cache.stride(0), cache.stride(1), shape[0]
+    if cache.dim() == 3:
+        pages, n, size = cache.shape
+        page_stride, head_stride, one = cache.stride()
+        if n == heads and size == per_page and one == 1:
+            return cache.data_ptr(), page_stride, head_stride, pages
+    raise ValueError(f"the cache is [pages, {heads} heads, {per_page} bytes], the last dimension contiguous")
 
 
 def append(rot: Rotary | None, positions: torch.Tensor | None, slots: torch.Tensor, q: torch.Tensor | None,
@@ -91,20 +93,35 @@ def append(rot: Rotary | None, positions: torch.Tensor | None, slots: torch.Tens
             raise ValueError("positions and slots have one entry per token")
         rot_ptr, pos_ptr = ctypes.addressof(rot), positions.data_ptr()
     hq, *q_rows = _rows(q, q_out, tokens, HEAD_DIM, dtype, index, "q")
-    shape = k.shape
-    kt, kh, kd = k.stride()
     if v.dtype is not dtype or v.get_device() != index:
         raise TypeError("k and v must share dtype and device")
-    vt, vh, vd = v.stride()
-    if shape != (tokens, shape[1], HEAD_DIM) or v.shape != shape or kd != 1 or vd != 1:
+    shape = k.shape
+    if len(shape) != 3 or v.shape != shape:
         raise ValueError("k and v are [tokens, heads, 128], the last dimension contiguous")
-    hk = shape[1]
+    n, hk, dim = shape
+    kt, kh, kd = k.stride()
+    vt, vh, vd = v.stride()
+    if n != tokens or dim != HEAD_DIM or kd != 1 or vd != 1:
+        raise ValueError("k and v are [tokens, heads, 128], the last dimension contiguous")
     c_ptr, cp, ch, pages = _cache(cache, page_size, hk, index)
     qw = _weight(q_weight, hq, HEAD_DIM, index, "q_weight")
     kw = _weight(k_weight, hk, HEAD_DIM, index, "k_weight")
     _call(_append, _APPEND_ARGS.pack(rot_ptr, pos_ptr, slots.data_ptr(), tokens, *q_rows, hq, k.data_ptr(), kt, kh,
                                      v.data_ptr(), vt, vh, hk, *qw, *kw, c_ptr, cp, ch, page_size, pages, code, eps),
           index, stream, "fi_kv4_append")
+
+
+def _out(out: torch.Tensor | None, dtype, index: int, shape):
+    """(pointer, token stride, head stride) of an output of read."""
+    if out is None:
+        return 0, 0, 0
+    if out.dtype is not dtype or out.get_device() != index:
+        raise TypeError("the outputs must share dtype and device")
+    if out.shape == shape:
+        row, head, one = out.stride()
+        if one == 1:
+            return out.data_ptr(), row, head
+    raise ValueError("the outputs are [slots, heads, 128], the last dimension contiguous")
 
 
 def read(slots: torch.Tensor, cache: torch.Tensor, page_size: int, k_out: torch.Tensor | None,
@@ -121,19 +138,16 @@ def read(slots: torch.Tensor, cache: torch.Tensor, page_size: int, k_out: torch.
     if code is None:
         raise TypeError(f"unsupported dtype {dtype}")
     rows = _index(slots, index, "slots")
-    outs = []
-    for out in (k_out, v_out):
-        if out is None:
-            outs += [0, 0, 0]
-            continue
-        if out.dtype is not dtype or out.get_device() != index:
-            raise TypeError("the outputs must share dtype and device")
-        if len(shape) != 3 or out.shape != shape or shape[0] != rows or shape[2] != HEAD_DIM or out.stride(2) != 1:
-            raise ValueError("the outputs are [slots, heads, 128], the last dimension contiguous")
-        outs += [out.data_ptr(), out.stride(0), out.stride(1)]
-    c_ptr, cp, ch, pages = _cache(cache, page_size, shape[1], index)
-    _call(_read, _READ_ARGS.pack(slots.data_ptr(), rows, *outs, shape[1], c_ptr, cp, ch, page_size, pages, code), index,
-          stream, "fi_kv4_read")
+    if len(shape) != 3:
+        raise ValueError("the outputs are [slots, heads, 128], the last dimension contiguous")
+    n, heads, dim = shape
+    kp, kt, kh = _out(k_out, dtype, index, shape)
+    vp, vt, vh = _out(v_out, dtype, index, shape)
+    if n != rows or dim != HEAD_DIM:
+        raise ValueError("the outputs are [slots, heads, 128], the last dimension contiguous")
+    c_ptr, cp, ch, pages = _cache(cache, page_size, heads, index)
+    _call(_read, _READ_ARGS.pack(slots.data_ptr(), rows, kp, kt, kh, vp, vt, vh, heads, c_ptr, cp, ch, page_size, pages,
+                                 code), index, stream, "fi_kv4_read")
 
 
 def run(ws: Workspace, info: PlanInfo, q: torch.Tensor, cache: torch.Tensor, kv_indices_dev: torch.Tensor,

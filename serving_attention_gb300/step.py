@@ -85,13 +85,16 @@ def _rows(x: torch.Tensor | None, y: torch.Tensor | None, tokens: int, dim: int,
     if x.dtype is not dtype or y.dtype is not dtype or x.get_device() != index or y.get_device() != index:
         raise TypeError(f"{what} and its output must have the dtype and device of the other tensors")
     shape = x.shape
-    if len(shape) != 3 or shape[0] != tokens or shape[2] != dim or y.shape != shape:
+    if len(shape) != 3 or y.shape != shape:
+        raise ValueError(f"{what} and its output are [tokens, heads, {dim}]")
+    n, heads, width = shape
+    if n != tokens or width != dim:
         raise ValueError(f"{what} and its output are [tokens, heads, {dim}]")
     xt, xh, xd = x.stride()
     yt, yh, yd = y.stride()
     if xd != 1 or yd != 1:
         raise ValueError(f"the last dimension of {what} and its output must be contiguous")
-    return shape[1], x.data_ptr(), xt, xh, y.data_ptr(), yt, yh
+    return heads, x.data_ptr(), xt, xh, y.data_ptr(), yt, yh
 
 
 def _index(t: torch.Tensor, index: int, what: str) -> int:
@@ -175,11 +178,16 @@ def _weight(w: torch.Tensor | None, heads: int, dim: int, index: int, what: str)
     """(pointer, stride per head) of norm weights [dim] or [heads, dim]."""
     if w is None:
         return 0, 0
-    if w.dtype is not torch.float32 or w.get_device() != index or w.stride(-1) != 1:
+    *strides, one = w.stride() or (0,)
+    if w.dtype is not torch.float32 or w.get_device() != index or one != 1:
         raise TypeError(f"{what} must be fp32 on the tensors' device, the last dimension contiguous")
-    if w.shape != (dim,) and w.shape != (heads, dim):
-        raise ValueError(f"{what} is [{dim}] or [heads, {dim}]")
-    return w.data_ptr(), 0 if w.dim() == 1 or heads == 1 else w.stride(0)
+    shape = w.shape
+    if not strides:
+        if shape[0] == dim:
+            return w.data_ptr(), 0
+    elif shape == (heads, dim):
+        return w.data_ptr(), 0 if heads == 1 else strides[0]
+    raise ValueError(f"{what} is [{dim}] or [heads, {dim}]")
 
 
 def norm_append(rot: Rotary, positions: torch.Tensor, slots: torch.Tensor, q: torch.Tensor | None,
