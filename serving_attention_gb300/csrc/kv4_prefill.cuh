@@ -29,7 +29,7 @@
 // What bounds it: no one unit, but the chain of a tile of 128 keys, 3.3 thousand
 // clocks.  An M tile's S has no second buffer in tensor memory, so its softmax
 // (2.1 thousand) and its P V and next S (1.1) follow one another, the other M tile's
-// between them; widening a tile takes 2.3.  Tensor cores are busy for 1.1 of the 3.3,
+// between them; widening a tile takes 2.3.  Tensor cores are busy half of that time,
 // issue slots for two thirds.  Eight prompts of 128 to 2048 tokens behind up to 2048,
 // 32 + 8 heads: 314 us, 1.1 PFLOP/s (188 us at the rate of plain bf16 products; 285 us
 // from a cache in 16 bits, four times the memory).  What it took: straight code
