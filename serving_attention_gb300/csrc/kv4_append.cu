@@ -15,9 +15,10 @@
 // each kind's heads filled up to a multiple of four so that a warp does one
 // thing; one warp per token, or per part of one when there are few tokens.  The
 // next group's rows are in flight while one is turned and coded.  cos and sin
-// stay in shared memory and no second group is held: with more warps on an SM
-// 8192 tokens of 32 + 8 heads took 56 us (33 us of bytes at the copy rate)
-// where one or two groups ahead with 16 to 20 warps took 60 to 64.
+// stay in shared memory, read without bank conflicts, and no second group is held:
+// 8192 tokens of 32 + 8 heads, with the 16-bit rows read back by a launch behind it,
+// took 50 us (33 us of bytes at the copy rate) where one or two groups ahead with 16
+// to 20 warps on an SM took 60 to 64, conflicts 6 more, clamps behind the rounding 1.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -64,19 +65,23 @@ __device__ __forceinline__ int round_small(float t) {
   return __float_as_int(__fadd_rn(t, 12582912.f)) - 0x4B400000;
 }
 
+// Eight codes rint(x inv) + z, kept within 0 .. 15 before the rounding (the bounds
+// are whole numbers; a NaN becomes 0), and summed modulo 2^32 with the rounded
+// numbers' bits as they are.
 __device__ __forceinline__ uint32_t codes8(const float (&x)[8], float inv, int z) {
-  uint32_t w = 0;
+  const float lo = float(-z), hi = float(15 - z);
+  uint32_t w = (uint32_t(z) - 0x4B400000u) * 0x11111111u;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float t = fminf(fmaxf(__fmul_rn(x[e], inv), -15.f), 15.f);
-    w |= uint32_t(min(max(round_small(t) + z, 0), 15)) << (4 * e);
+    const float t = fminf(fmaxf(__fmul_rn(x[e], inv), lo), hi);
+    w += __float_as_uint(__fadd_rn(t, 12582912.f)) << (4 * e);
   }
   return w;
 }
 
 template <typename T, int kPairs>
 __global__ void __launch_bounds__(32 * kAppendWarps, kAppendBlocks) kv4_append_kernel(const __grid_constant__ Kv4AppendParams a) {
-  __shared__ float2 s_cs[kAppendWarps][FI_KV4_HEAD_DIM / 2];
+  __shared__ alignas(16) float2 s_cs[kAppendWarps][FI_KV4_HEAD_DIM / 2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t w = int64_t(blockIdx.x) * kAppendWarps + warp;
   const int t = int(w / a.parts), part = int(w - int64_t(t) * a.parts);
@@ -106,15 +111,18 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendBlocks) kv4_append_k
   load(part);
 
   // cos and sin of the token's pairs
-  constexpr int kMine = kPairs == kHalfPairs ? 8 : 4;
+  // the two pairs of a float4 next to those of the other lanes: read without bank conflicts
+  constexpr int kMine = kPairs == kHalfPairs ? 8 : 4, kPlaces = kPairs == kHalfPairs ? 8 : 16;  // pairs of a chunk, chunks
+  auto spot = [](int i) { return kPairs == kPartHalfPairs ? i : 2 * ((i % kMine >> 1) * kPlaces + i / kMine) + (i & 1); };
   float2* const cs = s_cs[warp];
+  const float4* const cs2 = reinterpret_cast<const float4*>(s_cs[warp]);
   if (kPairs != kNoPairs) {
     const int32_t pos = __ldg(a.positions + t);
     for (int i = lane; i < a.rot_chunks * 4; i += 32) {
       const uint64_t turn = uint64_t(int64_t(pos)) * a.turns[i];  // modulo one turn
       // 2^-31: half turns in [-1, 1]; then the angle
       const float x = __fmul_rn(float(int32_t(turn >> 32)) * 4.6566128730773926e-10f, 3.14159265358979f);
-      cs[i] = make_float2(__fmul_rn(cosf(x), a.amplitude), __fmul_rn(sinf(x), a.amplitude));
+      cs[spot(i)] = make_float2(__fmul_rn(cosf(x), a.amplitude), __fmul_rn(sinf(x), a.amplitude));
     }
     __syncwarp();
   }
@@ -161,14 +169,22 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendBlocks) kv4_append_k
     if (!is_v) {
       if (kPairs == kHalfPairs) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) turn_pair(x[e], y[e], cs[kMine * p + e]);
+        for (int e = 0; e < 8; e += 2) {
+          const float4 r = cs2[e / 2 * kPlaces + p];
+          turn_pair(x[e], y[e], make_float2(r.x, r.y));
+          turn_pair(x[e + 1], y[e + 1], make_float2(r.z, r.w));
+        }
       } else if (kPairs == kNextPairs) {
-        if (p < a.rot_chunks)
+        auto turn_chunk = [&](float (&f)[8], int c) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) turn_pair(x[2 * e], x[2 * e + 1], cs[kMine * p + e]);
-        if (p + 8 < a.rot_chunks)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) turn_pair(y[2 * e], y[2 * e + 1], cs[kMine * (p + 8) + e]);
+          for (int e = 0; e < 4; e += 2) {
+            const float4 r = cs2[e / 2 * kPlaces + c];
+            turn_pair(f[2 * e], f[2 * e + 1], make_float2(r.x, r.y));
+            turn_pair(f[2 * e + 2], f[2 * e + 3], make_float2(r.z, r.w));
+          }
+        };
+        if (p < a.rot_chunks) turn_chunk(x, p);
+        if (p + 8 < a.rot_chunks) turn_chunk(y, p + 8);
       } else if (kPairs == kPartHalfPairs) {
         // chunk c pairs with chunk c + half (c < half); the partner's values by shuffles
         const int half = a.rot_chunks >> 1;

@@ -10,10 +10,11 @@
 // how many of them are in flight, so registers are few (cos and sin stay in
 // shared memory, v's rows of the heads' size go through the heads' loop) and a
 // head's successor is loaded before the head is turned.
-// Measured: 16384 tokens of 32 + 8 heads of 128 in 87 us, 4.6 TB/s (60 us at the
-// copy rate); 1111 tokens of 24 + 24 heads of 80 in 8.8 us, where four blocks on
-// an SM with cos and sin in registers took 16.3; 64 tokens in 4.0 us, the launch
-// and one chain of loads.
+// Measured: 16384 tokens of 32 + 8 heads of 128 in 71 us, 5.7 TB/s (60 us at the
+// copy rate; 87 before the turns' reads met no bank twice and the sum took no more
+// shuffles than a head has lanes for); 1111 tokens of 24 + 24 heads of 80 in 9.4 us,
+// where four blocks on an SM with cos and sin in registers took 16.3; 64 tokens in
+// 3.6 us, the launch and one chain of loads.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -37,7 +38,7 @@ struct NormParams {
   const int32_t* slots;
   int64_t num_slots;
   int32_t num_tokens, parts;  // warps per token
-  int32_t log2_page;
+  int32_t log2_page, half_places;  // half_places: the largest power of two below the places of a head (0: one place)
   int32_t v_like_heads;  // v's rows have the heads' size and go through their loop, as copies
   int32_t head_chunks, rot_chunks, v_chunks;  // 16-byte chunks of a head, of its rotated part, of a v row
   float amplitude, eps, inv_dim;
@@ -51,7 +52,7 @@ __device__ __forceinline__ void load8(const float* w, float (&f)[8]) {
 
 template <typename T, bool kInterleaved>
 __global__ void __launch_bounds__(32 * kNormWarps, kNormBlocks) norm_append_kernel(const __grid_constant__ NormParams a) {
-  __shared__ float2 s_cs[kNormWarps][FI_ROTARY_MAX_PAIRS];
+  __shared__ alignas(16) float2 s_cs[kNormWarps][FI_ROTARY_MAX_PAIRS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t w = int64_t(blockIdx.x) * kNormWarps + warp;
   const int t = int(w / a.parts), part = int(w - int64_t(t) * a.parts);
@@ -81,16 +82,17 @@ __global__ void __launch_bounds__(32 * kNormWarps, kNormBlocks) norm_append_kern
   const int first = part * at_once + h_off;
   load(first);
 
+  // pairs 2 e and 2 e + 1 of place p together, next to those of the other places: lanes read without bank conflicts
+  constexpr int kMine = kInterleaved ? 4 : 8;  // pairs of a place
   float2* cs = s_cs[warp];
   for (int i = lane; i < a.rot_chunks * 4; i += 32) {
     const uint64_t turn = uint64_t(int64_t(pos)) * a.turns[i];  // modulo one turn
     float sn, c;
     sincospif(float(int32_t(turn >> 32)) * 4.6566128730773926e-10f, &sn, &c);  // 2^-31: half turns in [-1, 1]
-    cs[i] = make_float2(c * a.amplitude, sn * a.amplitude);
+    cs[2 * ((i % kMine >> 1) * pair_places + i / kMine) + (i & 1)] = make_float2(c * a.amplitude, sn * a.amplitude);
   }
   __syncwarp();
-  constexpr int kMine = kInterleaved ? 4 : 8;
-  const float4* const mine = reinterpret_cast<const float4*>(cs + (pairs ? kMine * place : 0));
+  const float4* const mine = reinterpret_cast<const float4*>(cs) + (pairs ? place : 0);
   const int64_t page = slot >> a.log2_page, in_page = slot & ((int64_t(1) << a.log2_page) - 1);
   // the shuffles need every lane, so the loop runs while any head of the warp is left
   for (int h = first; h - h_off < heads; h += step) {
@@ -104,8 +106,8 @@ __global__ void __launch_bounds__(32 * kNormWarps, kNormBlocks) norm_append_kern
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum = fmaf(x[e], x[e], fmaf(y[e], y[e], sum));
     // over the head's lanes, into its first, and back
-#pragma unroll
-    for (int m = 16; m > 0; m >>= 1) {
+#pragma unroll 1
+    for (int m = a.half_places; m > 0; m >>= 1) {
       const float more = __shfl_down_sync(0xffffffffu, sum, m);
       if (place + m < places) sum += more;
     }
@@ -137,7 +139,7 @@ __global__ void __launch_bounds__(32 * kNormWarps, kNormBlocks) norm_append_kern
     if (pairs) {
 #pragma unroll
       for (int e = 0; e < kMine; e += 2) {
-        const float4 r = mine[e / 2];
+        const float4 r = mine[e / 2 * pair_places];
         if (kInterleaved) {
           const float x0 = x[2 * e], x1 = x[2 * e + 1], x2 = x[2 * e + 2], x3 = x[2 * e + 3];
           x[2 * e] = x0 * r.x - x1 * r.y;
@@ -218,6 +220,8 @@ extern "C" fi_status fi_norm_rotary_append(const fi_norm_rotary_append_args* n, 
   a.inv_dim = 1.f / float(rot->head_dim);
   std::memcpy(a.turns, rot->turns, sizeof(uint64_t) * size_t(rot->rot_dim / 2));
   const int places = (rot->interleaved ? a.rot_chunks : a.rot_chunks / 2) + a.head_chunks - a.rot_chunks;
+  while ((1 << a.half_places) < places) ++a.half_places;
+  a.half_places = (1 << a.half_places) >> 1;
   a.v_like_heads = x->v_dim == rot->head_dim ? 1 : 0;
   // Few tokens: a token's heads are spread over more warps, at least one head a lane
   const int at_once = 32 / places, heads = a.q.heads + a.k.heads + (a.v_like_heads ? a.v.heads : 0);
