@@ -52,6 +52,10 @@ constexpr int kKv4GroupKeys = 1024;    // the longest chunk that one group takes
 constexpr int kKv4Stage = 32;          // keys of a stage
 constexpr int kKv4Depth = 3;           // stages of a ring
 constexpr int kKv4StageBytes = 4608;   // 32 blocks of one slot, 144 bytes each
+// log2 of the smallest of the small pages that come by bulk copies, a page each; smaller ones in pieces of 16 bytes.
+// 64 requests of 512 to 32768 keys, us, by bulk copies and in pieces: pages of two tokens 240 and 221, of four 181 and
+// 215, of eight 155 and 210.
+constexpr int kKv4BulkLog2 = 2;
 constexpr int kKv4Tile = 8;            // packed query rows of a pass
 constexpr int kKv4CombRow = 132;       // floats from row to row of a warp's state (128 and 4 against bank conflicts)
 constexpr int kKv4Barrier = 8;         // named barriers: of all computing warps, then of each group's
@@ -136,9 +140,9 @@ __device__ __forceinline__ int kv4_stages(const Item& it) { return (it.kv1 - it.
 // its items, and a round issues a stage for every ring whose next slot is free.
 // Stages of one or two blocks (kB = 32, 16) are issued by that lane, for all
 // rings at once; stages of many small blocks (kB = 0) by the whole warp, ring
-// after ring, in copies of 16 bytes (a bulk copy for each block of one slot kept
-// the copy engine busy longer than the keys did the warps).  Page ids are loaded a
-// stage ahead, their lines a line ahead.
+// after ring, a bulk copy a lane or in pieces of 16 bytes (a bulk copy for each block
+// of one slot kept the copy engine busy longer than the keys did the warps).  Page
+// ids are loaded a stage ahead, their lines a line ahead.
 template <int kB>
 __device__ void kv4_load(const Kv4Params& kp, Kv4Smem& sm, int loader, int32_t off_items, int32_t begin,
                          int32_t shorts, int32_t end) {
@@ -244,14 +248,23 @@ __device__ void kv4_load(const Kv4Params& kp, Kv4Smem& sm, int loader, int32_t o
         const uint32_t loads = __ballot_sync(0xffffffffu, ok);
         const uint32_t good = __ballot_sync(0xffffffffu, loads >> (lane >> log2_slots) & 1u);
         uint8_t* const dst = sm.dec.ring[ring][s];
+        if (log2_slots >= kKv4BulkLog2) {
+          if (ok) {
+            mbar_arrive_expect_tx(&sm.full[ring][s], bytes);
+            bulk_load(dst + lane * bytes, src + ids[u] * kp.page_stride, bytes, &sm.full[ring][s]);
+          } else {
+            mbar_arrive(&sm.full[ring][s]);
+          }
+        } else {
 #pragma unroll
-        for (int k = 0; k < kPieces; ++k) {
-          const int b = piece[k] >> 16;
-          const int32_t id = __shfl_sync(0xffffffffu, ids[u], b);
-          if ((loads >> b & 1u) && 16 * (lane + 32 * k) < blocks * bytes)
-            cp_async_16(dst + 16 * (lane + 32 * k), src + id * kp.page_stride + (piece[k] & 0xFFFFu), 16);
+          for (int k = 0; k < kPieces; ++k) {
+            const int b = piece[k] >> 16;
+            const int32_t id = __shfl_sync(0xffffffffu, ids[u], b);
+            if ((loads >> b & 1u) && 16 * (lane + 32 * k) < blocks * bytes)
+              cp_async_16(dst + 16 * (lane + 32 * k), src + id * kp.page_stride + (piece[k] & 0xFFFFu), 16);
+          }
+          cp_async_mbar_arrive_noinc(&sm.full[ring][s]);
         }
-        cp_async_mbar_arrive_noinc(&sm.full[ring][s]);
         if (lane == 0) {
           sm.dec.good[ring][s] = good;
           mbar_arrive(&sm.full[ring][s]);
