@@ -426,6 +426,56 @@ def test_captured_step_replays_later_plans():
             assert np.abs(_f64(lse[b:b + 1]) - rl).max() <= 2e-4
 
 
+@pytest.mark.parametrize("first", [0, 1])
+def test_captured_run_serves_plans_of_the_other_class(first):
+    """A run captured on a plan of single tokens serves one whose prompt parts are split, and the other way round."""
+    bs = [Batch(50, [1] * 5, [300, 20, 700, 1, 64], 8, 2, 16, "bf16", 1),
+          Batch(51, [60, 1, 150], [900, 300, 260], 8, 2, 16, "bf16", 1)]
+    cfg = _config(prefill_min_chunk=128, decode_min_chunk=64, split_factor=4)
+    ws = fi.Workspace(cfg, device=DEV)
+    rows, pool = max(len(b.q) for b in bs), max(b.pool for b in bs)
+    q = torch.zeros((rows, 8, 128), dtype=torch.bfloat16, device=DEV)
+    cache = torch.zeros((pool, 2, kv4.page_bytes(16)), dtype=torch.uint8, device=DEV)
+    idx = torch.zeros(max(len(b.ids) for b in bs), dtype=torch.int32, device=DEV)
+    o, lse = torch.empty_like(q), torch.empty(q.shape[:2], device=DEV)
+
+    def stage(b):
+        q[:len(b.q)].copy_(b.q)
+        cache[:b.pool].copy_(b.cache)
+        idx[:len(b.ids)].copy_(_i32(b.ids))
+        o.fill_(float("nan"))
+        lse.fill_(float("nan"))
+        return b.plan(ws)
+
+    info = stage(bs[first])
+    assert (info.num_late_merge_units > 0) == (first == 1)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kv4.run(ws, info, q, cache, idx, o, lse, bs[0].scale)
+    for turn in (first, 1 - first, first, 1 - first):
+        b = bs[turn]
+        stage(b)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert fi.device_status(ws) == 0
+        b.check(o[:len(b.q)], lse[:len(b.q)])
+
+
+@pytest.mark.parametrize("group", [3, 4, 16])
+def test_strided_queries_and_outputs(group):
+    """Rows of q and o with room between heads and tokens: the values of contiguous ones, and nothing else written."""
+    b = Batch(60 + group, [1, 70, 5, 200], [400, 300, 5, 200], 2 * group, 2, 16, "bf16", 1)
+    o, lse, info, ws = b.run(_config())
+    n = int(b.qo[-1])
+    wide = [torch.full((len(b.q), 2 * group + 1, 136), 3.0, dtype=b.q.dtype, device=DEV) for _ in range(2)]
+    q, out = (x[:, 1:, :128] for x in wide)
+    q.copy_(b.q)
+    kv4.run(ws, info, q, b.cache, b.idx, out, None, b.scale)
+    assert torch.equal(out[:n], o[:n]) and fi.device_status(ws) == 0
+    assert (wide[1][n:] == 3).all() and (wide[1][:, 0] == 3).all() and (wide[1][..., 128:] == 3).all()
+
+
 def test_two_streams_at_once():
     """Calls with workspaces of their own on two streams give what each gives alone."""
     bs = [Batch(30 + i, [1] * 6 + [60], [500, 3, 900, 77, 1500, 31, 400], 8, 2, 16, "bf16", 1) for i in range(2)]

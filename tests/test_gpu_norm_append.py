@@ -91,3 +91,29 @@ def test_norm_append_without_weights_is_append():
             step.append(r, pos, pos, q, q_out, k, v, kc, vc)
         got.append((q_out, kc, vc))
     assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+@pytest.mark.parametrize("dim,v_dim", [(128, 128), (80, 80), (64, 128), (256, 256)])
+def test_norm_append_in_place_captured_and_in_parts(dim, v_dim):
+    """One call of many tokens, in place and replayed from a graph, does what small calls do, to the bit; v is copied
+    whatever its bits."""
+    T, H, Hk, P = 5001, 5, 3, 16
+    r = step.rotary_setup(dim, theta=1e6)
+    q, k, v = _randn((T, H, dim), "bf16", 1), _randn((T, Hk, dim), "bf16", 2), _randn((T, Hk, v_dim), "bf16", 3)
+    v.view(torch.int16).copy_(torch.randint(-2**15, 2**15, v.shape, generator=_gen(4), device=DEV).short())
+    w = [1 + 0.2 * torch.randn((n, dim), generator=_gen(5), device=DEV) for n in (H, Hk)]
+    pos = torch.arange(T, device=DEV).int()
+    slots = torch.randperm(-(-T // P) * P, generator=_gen(6), device=DEV)[:T].int()
+    small = [torch.empty_like(q), *(torch.zeros((-(-T // P), P, Hk, d), dtype=q.dtype, device=DEV) for d in (dim, v_dim))]
+    for a in range(0, T, 61):
+        b = min(T, a + 61)
+        step.norm_append(r, pos[a:b], slots[a:b], q[a:b], small[0][a:b], w[0], k[a:b], w[1], v[a:b], *small[1:])
+    turned, caches = q.clone(), [torch.zeros_like(x) for x in small[1:]]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step.norm_append(r, pos, slots, turned, turned, w[0], k, w[1], v, *caches)
+    for _ in range(2):
+        turned.copy_(q)
+        graph.replay()
+    for x, y in zip((turned, *caches), small):
+        assert torch.equal(x.view(torch.int16), y.view(torch.int16))
