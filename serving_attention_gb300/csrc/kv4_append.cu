@@ -17,8 +17,9 @@
 // next group's rows are in flight while one is turned and coded.  cos and sin
 // stay in shared memory, read without bank conflicts, and no second group is held:
 // 8192 tokens of 32 + 8 heads, with the 16-bit rows read back by a launch behind it,
-// took 50 us (33 us of bytes at the copy rate) where one or two groups ahead with 16
-// to 20 warps on an SM took 60 to 64, conflicts 6 more, clamps behind the rounding 1.
+// took 49 us (33 us of bytes at the copy rate) where one or two groups ahead with 16
+// to 20 warps on an SM took 60 to 64, conflicts 6 more, clamps behind the rounding 1 and
+// sums and products one at a time another 1.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -32,7 +33,7 @@ namespace fi {
 namespace {
 
 constexpr int kAppendWarps = 4;   // warps of a block
-constexpr int kAppendBlocks = 7;  // blocks of an SM
+constexpr int kAppendBlocks = 6;  // blocks of an SM
 constexpr float kFifteenth = 1.f / 15.f;
 
 enum { kNoPairs = 0, kHalfPairs = 1, kNextPairs = 2, kPartHalfPairs = 3 };
@@ -72,9 +73,12 @@ __device__ __forceinline__ uint32_t codes8(const float (&x)[8], float inv, int z
   const float lo = float(-z), hi = float(15 - z);
   uint32_t w = (uint32_t(z) - 0x4B400000u) * 0x11111111u;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float t = fminf(fmaxf(__fmul_rn(x[e], inv), lo), hi);
-    w += __float_as_uint(__fadd_rn(t, 12582912.f)) << (4 * e);
+  for (int e = 0; e < 8; e += 2) {
+    const float2 t = mul2(make_float2(x[e], x[e + 1]), make_float2(inv, inv));
+    const float2 n = add2(make_float2(fminf(fmaxf(t.x, lo), hi), fminf(fmaxf(t.y, lo), hi)),
+                          make_float2(12582912.f, 12582912.f));
+    w += __float_as_uint(n.x) << (4 * e);
+    w += __float_as_uint(n.y) << (4 * e + 4);
   }
   return w;
 }
@@ -111,7 +115,8 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendBlocks) kv4_append_k
   load(part);
 
   // cos and sin of the token's pairs
-  // the two pairs of a float4 next to those of the other lanes: read without bank conflicts
+  // the two pairs of a float4 next to those of the other lanes: read without bank conflicts; of the half layout both cosines,
+  // then both sines
   constexpr int kMine = kPairs == kHalfPairs ? 8 : 4, kPlaces = kPairs == kHalfPairs ? 8 : 16;  // pairs of a chunk, chunks
   auto spot = [](int i) { return kPairs == kPartHalfPairs ? i : 2 * ((i % kMine >> 1) * kPlaces + i / kMine) + (i & 1); };
   float2* const cs = s_cs[warp];
@@ -122,7 +127,14 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendBlocks) kv4_append_k
       const uint64_t turn = uint64_t(int64_t(pos)) * a.turns[i];  // modulo one turn
       // 2^-31: half turns in [-1, 1]; then the angle
       const float x = __fmul_rn(float(int32_t(turn >> 32)) * 4.6566128730773926e-10f, 3.14159265358979f);
-      cs[spot(i)] = make_float2(__fmul_rn(cosf(x), a.amplitude), __fmul_rn(sinf(x), a.amplitude));
+      const float c = __fmul_rn(cosf(x), a.amplitude), sn = __fmul_rn(sinf(x), a.amplitude);
+      if (kPairs == kHalfPairs) {
+        float* const at = &s_cs[warp][spot(i & ~1)].x + (i & 1);
+        at[0] = c;
+        at[2] = sn;
+      } else {
+        cs[spot(i)] = make_float2(c, sn);
+      }
     }
     __syncwarp();
   }
@@ -145,25 +157,31 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendBlocks) kv4_append_k
     const bool is_q = g < nq, is_v = g >= nq + nk;
     const float* weight = is_v ? nullptr : is_q ? a.q_weight : a.k_weight;
     if (weight) {
-      float sq[8];
+      float2 sq[4];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sq[e] = __fadd_rn(__fmul_rn(x[e], x[e]), __fmul_rn(y[e], y[e]));
+      for (int e = 0; e < 4; ++e) {
+        const float2 u = make_float2(x[2 * e], x[2 * e + 1]), v = make_float2(y[2 * e], y[2 * e + 1]);
+        sq[e] = add2(mul2(u, u), mul2(v, v));
+      }
+      const float2 four = add2(add2(sq[0], sq[2]), add2(sq[1], sq[3]));
+      float sum = __fadd_rn(four.x, four.y);
 #pragma unroll
-      for (int d = 4; d > 0; d >>= 1)
-#pragma unroll
-        for (int e = 0; e < d; ++e) sq[e] = __fadd_rn(sq[e], sq[e + d]);
-#pragma unroll
-      for (int m = 4; m > 0; m >>= 1) sq[0] = __fadd_rn(sq[0], __shfl_xor_sync(0xffffffffu, sq[0], m));
-      const float f = __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(sq[0], 1.f / 128.f), a.eps)));
+      for (int m = 4; m > 0; m >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, m));
+      const float f = __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(sum, 1.f / 128.f), a.eps)));
       const float* mine = weight + max(h, 0) * (is_q ? a.q_weight_stride : a.k_weight_stride) + 8 * p;
       const float4 w0 = __ldg(reinterpret_cast<const float4*>(mine)), w1 = __ldg(reinterpret_cast<const float4*>(mine + 4));
       const float4 w2 = __ldg(reinterpret_cast<const float4*>(mine + 64)), w3 = __ldg(reinterpret_cast<const float4*>(mine + 68));
       const float wx[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
       const float wy[8] = {w2.x, w2.y, w2.z, w2.w, w3.x, w3.y, w3.z, w3.w};
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x[e] = __fmul_rn(__fmul_rn(x[e], f), wx[e]);
-        y[e] = __fmul_rn(__fmul_rn(y[e], f), wy[e]);
+      for (int e = 0; e < 8; e += 2) {
+        const float2 ff = make_float2(f, f);
+        const float2 u = mul2(mul2(make_float2(x[e], x[e + 1]), ff), make_float2(wx[e], wx[e + 1]));
+        const float2 v = mul2(mul2(make_float2(y[e], y[e + 1]), ff), make_float2(wy[e], wy[e + 1]));
+        x[e] = u.x;
+        x[e + 1] = u.y;
+        y[e] = v.x;
+        y[e + 1] = v.y;
       }
     }
     if (!is_v) {
@@ -171,8 +189,13 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendBlocks) kv4_append_k
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
           const float4 r = cs2[e / 2 * kPlaces + p];
-          turn_pair(x[e], y[e], make_float2(r.x, r.y));
-          turn_pair(x[e + 1], y[e + 1], make_float2(r.z, r.w));
+          const float2 c = make_float2(r.x, r.y), sn = make_float2(r.z, r.w), less = make_float2(-r.z, -r.w);
+          const float2 u = make_float2(x[e], x[e + 1]), v = make_float2(y[e], y[e + 1]);
+          const float2 first = add2(mul2(u, c), mul2(v, less)), second = add2(mul2(v, c), mul2(u, sn));
+          x[e] = first.x;
+          x[e + 1] = first.y;
+          y[e] = second.x;
+          y[e + 1] = second.y;
         }
       } else if (kPairs == kNextPairs) {
         auto turn_chunk = [&](float (&f)[8], int c) {
