@@ -19,7 +19,7 @@
 // 8192 tokens of 32 + 8 heads, with the 16-bit rows read back by a launch behind it,
 // took 49 us (33 us of bytes at the copy rate) where one or two groups ahead with 16
 // to 20 warps on an SM took 60 to 64, conflicts 6 more, clamps behind the rounding 1 and
-// sums and products one at a time another 1.
+// sums and products one at a time, or a lane's two angles one behind the other, 1 each.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -114,20 +114,25 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendBlocks) kv4_append_k
   };
   load(part);
 
-  // cos and sin of the token's pairs
-  // the two pairs of a float4 next to those of the other lanes: read without bank conflicts; of the half layout both cosines,
-  // then both sines
+  // cos and sin of the token's pairs, the two pairs of a float4 next to those of the other lanes: read without bank
+  // conflicts; of the half layout both cosines, then both sines
   constexpr int kMine = kPairs == kHalfPairs ? 8 : 4, kPlaces = kPairs == kHalfPairs ? 8 : 16;  // pairs of a chunk, chunks
   auto spot = [](int i) { return kPairs == kPartHalfPairs ? i : 2 * ((i % kMine >> 1) * kPlaces + i / kMine) + (i & 1); };
   float2* const cs = s_cs[warp];
   const float4* const cs2 = reinterpret_cast<const float4*>(s_cs[warp]);
   if (kPairs != kNoPairs) {
     const int32_t pos = __ldg(a.positions + t);
-    for (int i = lane; i < a.rot_chunks * 4; i += 32) {
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const int i = lane + 32 * n;
+      if (i >= a.rot_chunks * 4) break;
       const uint64_t turn = uint64_t(int64_t(pos)) * a.turns[i];  // modulo one turn
       // 2^-31: half turns in [-1, 1]; then the angle
       const float x = __fmul_rn(float(int32_t(turn >> 32)) * 4.6566128730773926e-10f, 3.14159265358979f);
-      const float c = __fmul_rn(cosf(x), a.amplitude), sn = __fmul_rn(sinf(x), a.amplitude);
+      float c, sn;  // what cosf and sinf give, for every number up to pi (all of them compared)
+      sincosf(x, &sn, &c);
+      c = __fmul_rn(c, a.amplitude);
+      sn = __fmul_rn(sn, a.amplitude);
       if (kPairs == kHalfPairs) {
         float* const at = &s_cs[warp][spot(i & ~1)].x + (i & 1);
         at[0] = c;

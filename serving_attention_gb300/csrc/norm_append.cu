@@ -12,9 +12,9 @@
 // head's successor is loaded before the head is turned.
 // Measured: 16384 tokens of 32 + 8 heads of 128 in 71 us, 5.7 TB/s (60 us at the
 // copy rate; 87 before the turns' reads met no bank twice and the sum took no more
-// shuffles than a head has lanes for); 1111 tokens of 24 + 24 heads of 80 in 9.4 us,
+// shuffles than a head has lanes for); 1111 tokens of 24 + 24 heads of 80 in 9.2 us,
 // where four blocks on an SM with cos and sin in registers took 16.3; 64 tokens in
-// 3.6 us, the launch and one chain of loads.
+// 3.3 us, the launch and one chain of loads.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -85,6 +85,7 @@ __global__ void __launch_bounds__(32 * kNormWarps, kNormBlocks) norm_append_kern
   // pairs 2 e and 2 e + 1 of place p together, next to those of the other places: lanes read without bank conflicts
   constexpr int kMine = kInterleaved ? 4 : 8;  // pairs of a place
   float2* cs = s_cs[warp];
+#pragma unroll 2
   for (int i = lane; i < a.rot_chunks * 4; i += 32) {
     const uint64_t turn = uint64_t(int64_t(pos)) * a.turns[i];  // modulo one turn
     float sn, c;
