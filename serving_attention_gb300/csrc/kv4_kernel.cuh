@@ -4,7 +4,7 @@
 // A value is s (n - z) (fi_kv4.h).  A code n in the low nibble of a 16-bit half
 // is, as it lies there, the fp16 subnormal n 2^-24, and in the next nibble n
 // 2^-20; the tensor cores take subnormals exactly.  So a word of eight codes
-// becomes four operand registers with four ANDs and one shift, no conversion,
+// becomes four operand registers with four ANDs and a shift or two, no conversion,
 // and scale and zero point stay out of the products:
 //
 //   q . k_j = s_j ( sum_d q_d n_jd - z_j sum_d q_d )
@@ -15,6 +15,13 @@
 // columns), and O^T = V^T P^T has the dims as rows, so eight query rows cost one
 // product per 16 keys and 16 dims.  P^T comes from S^T by one 8 x 8 transpose
 // per 8 keys.  The zero point's sum is one more product whose rows all are z.
+// A product keeps its addends down to 2^-25 of the largest, a subnormal operand
+// counting as the smallest normal number, 2^-14: codes in the lowest bits lose ten
+// bits of those.  A value that a row holds as zero (n = z) has to cancel beside the
+// others' values of that dim, so v's codes go in three bits up, as n 2^-21 and n
+// 2^-17 (120.2 -> 120.8 us of the batch below; all as n 2^-17: 128).  k's stay where
+// they are: its logits are off by up to 6 10^-5, three bits up by up to 2 10^-5 and
+// the batch 4 us later.
 // (tcgen05 would want the codes as 16-bit operands in shared memory, four times
 // the bytes that came, for a tile of which 8 of 128 rows are used.)
 //
@@ -107,7 +114,8 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return y;
 }
 __device__ __forceinline__ void prefetch_l1(const void* p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
-constexpr uint32_t kNibble0 = 0x000F000Fu, kNibble1 = 0x00F000F0u;
+constexpr uint32_t kNibble0 = 0x000F000Fu, kNibble1 = 0x00F000F0u;      // n 2^-24, n 2^-20
+constexpr uint32_t kUpNibble0 = 0x00780078u, kUpNibble1 = 0x07800780u;  // n 2^-21, n 2^-17
 
 // A word's two halves: the scale, and the zero point as n 2^-24 (the unit of the products).
 __device__ __forceinline__ float word_scale(uint32_t w) { return __half2float(__ushort_as_half(uint16_t(w & 0xFFF0u))); }
@@ -442,7 +450,7 @@ __device__ __forceinline__ void kv4_stage(const uint8_t* stage, const Kv4Places<
       const uint32_t x = *reinterpret_cast<const uint16_t*>(word + 2 * at.slots);
       const float ks = word_scale(w), kz = word_zero(w);
       vs[b][u] = word_scale(x);
-      vz[b][u] = transpose8((x & 15u) * 0x00010001u);
+      vz[b][u] = transpose8((x & 15u) * 0x00800080u);
 #pragma unroll
       for (int h = 0; h < 2; ++h) s[b][2 * u + h] = fmaf(-kz, R.qs[h], s[b][2 * u + h]) * ks;
     }
@@ -530,11 +538,12 @@ __device__ __forceinline__ void kv4_stage(const uint8_t* stage, const Kv4Places<
       auto word = [&](int u) { return half ? v4[u].y : v4[u].x; };
       const uint32_t a0 = __byte_perm(word(0), word(1), 0x5410), a1 = __byte_perm(word(0), word(1), 0x7632);
       const uint32_t a2 = __byte_perm(word(2), word(3), 0x5410), a3 = __byte_perm(word(2), word(3), 0x7632);
-      const uint32_t h0 = a0 >> 8, h1 = a1 >> 8, h2 = a2 >> 8, h3 = a3 >> 8;
-      mma16(R.o[4 * half], a0 & kNibble0, a1 & kNibble0, a2 & kNibble0, a3 & kNibble0, b0, b1);
-      mma16(R.o[4 * half + 1], a0 & kNibble1, a1 & kNibble1, a2 & kNibble1, a3 & kNibble1, b0, b1);
-      mma16(R.o[4 * half + 2], h0 & kNibble0, h1 & kNibble0, h2 & kNibble0, h3 & kNibble0, b0, b1);
-      mma16(R.o[4 * half + 3], h0 & kNibble1, h1 & kNibble1, h2 & kNibble1, h3 & kNibble1, b0, b1);
+      const uint32_t l0 = a0 << 3, l1 = a1 << 3, l2 = a2 << 3, l3 = a3 << 3;
+      const uint32_t h0 = a0 >> 5, h1 = a1 >> 5, h2 = a2 >> 5, h3 = a3 >> 5;
+      mma16(R.o[4 * half], l0 & kUpNibble0, l1 & kUpNibble0, l2 & kUpNibble0, l3 & kUpNibble0, b0, b1);
+      mma16(R.o[4 * half + 1], l0 & kUpNibble1, l1 & kUpNibble1, l2 & kUpNibble1, l3 & kUpNibble1, b0, b1);
+      mma16(R.o[4 * half + 2], h0 & kUpNibble0, h1 & kUpNibble0, h2 & kUpNibble0, h3 & kUpNibble0, b0, b1);
+      mma16(R.o[4 * half + 3], h0 & kUpNibble1, h1 & kUpNibble1, h2 & kUpNibble1, h3 & kUpNibble1, b0, b1);
     }
   }
 }
@@ -543,7 +552,7 @@ __device__ __forceinline__ void kv4_stage(const uint8_t* stage, const Kv4Places<
 template <typename T>
 __device__ __forceinline__ void kv4_put_state(Kv4Smem& sm, int warp, Kv4Rows<T>& R) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const float up = 16777216.f / R.unit;  // 2^24: codes and zero points came in as n 2^-24
+  const float up = 131072.f / R.unit;  // 2^17: zero points came in as n 2^-17, codes as that or n 2^-21
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     float l = R.l[h];
@@ -561,7 +570,7 @@ __device__ __forceinline__ void kv4_put_state(Kv4Smem& sm, int warp, Kv4Rows<T>&
       for (int hi = 0; hi < 2; ++hi) {
         float x[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = ((i & 1 ? 0.0625f : 1.f) * R.o[4 * half + i][2 * hi + h] - R.z[h]) * up;
+        for (int i = 0; i < 4; ++i) x[i] = ((i & 1 ? 1.f : 16.f) * R.o[4 * half + i][2 * hi + h] - R.z[h]) * up;
         *reinterpret_cast<float4*>(dst + 8 * half + 4 * hi) = make_float4(x[0], x[1], x[2], x[3]);
       }
   }
