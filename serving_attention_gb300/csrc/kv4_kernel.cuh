@@ -43,6 +43,8 @@
 // keys, 8 + 2 heads, 6.6 us, of which the launch and the plan's loads are 3; 64 of
 // 64 to 512 keys on pages of one token 16 us, at 144 bytes a copy.
 #pragma once
+#include <cfloat>
+
 #include "attention_kernel.cuh"
 #include "kv4_layout.h"
 #include "kv4_params.h"
@@ -65,6 +67,9 @@ constexpr int kKv4StageBytes = 4608;   // 32 blocks of one slot, 144 bytes each
 constexpr int kKv4BulkLog2 = 2;
 constexpr int kKv4Tile = 8;            // packed query rows of a pass
 constexpr int kKv4CombRow = 132;       // floats from row to row of a warp's state (128 and 4 against bank conflicts)
+constexpr float kKv4NoMax = -FLT_MAX;    // the running maximum before any key
+constexpr float kKv4TopUnit = 0x1p100f;  // of the weights: the largest
+constexpr float kKv4TopWeight = 32768.f; // of the weights in their unit
 constexpr int kKv4Barrier = 8;         // named barriers: of all computing warps, then of each group's
 // Registers per thread and warpgroup; each phase's sum is the launch's.
 constexpr int kKv4RegsLaunch = 128;
@@ -341,7 +346,7 @@ struct Kv4Rows {
   float m[2], l[2];
   float o[8][4];     // step i: dims 16 g + 8 (i / 4) + i % 4 (first two) and + 4 (last two)
   float z[4];
-  float unit;        // the power of two that v's scales are multiplied by
+  float unit[2];     // what weights times v's scales are multiplied by
 };
 
 // This lane's part of query row g of a pass: dims 32 t .. 32 t + 31.
@@ -408,7 +413,7 @@ __device__ __forceinline__ void kv4_set_rows(const Kv4Params& kp, const Item& it
     const int pos = it.rq.kv_len - it.rq.qo_len + r / G;
     R.lim[h] = r < it.row1 ? min(causal ? pos : it.rq.kv_len - 1, it.kv1 - 1) : -1;
     R.lo[h] = window_low(var, pos);
-    R.m[h] = -INFINITY;
+    R.m[h] = kKv4NoMax;
     R.l[h] = 0.f;
   }
 #pragma unroll
@@ -417,7 +422,7 @@ __device__ __forceinline__ void kv4_set_rows(const Kv4Params& kp, const Item& it
     for (int e = 0; e < 4; ++e) R.o[i][e] = 0.f;
 #pragma unroll
   for (int e = 0; e < 4; ++e) R.z[e] = 0.f;
-  R.unit = __int_as_float((127 + 100) << 23);
+  R.unit[0] = R.unit[1] = kKv4TopUnit;
 }
 
 // The 32 keys of a stage from key j0 on.  inside: every key of the stage is
@@ -472,59 +477,83 @@ __device__ __forceinline__ void kv4_stage(const uint8_t* stage, const Kv4Places<
         if (!any || !there) vs[b][u] = 0.f;  // a weight of 0 times any bytes, infinities included
       }
   }
-  // The running maxima move when a row's grows by more than 2^8, the unit of
-  // the weights when a value scale would pass twice it.
-  float top[2];
-  float v = fmaxf(fmaxf(vs[0][0], vs[0][1]), fmaxf(vs[1][0], vs[1][1]));
-  bool move = v * R.unit >= 2.f;
+  // Weights p s_v as operand columns: keys 2t, 2t + 1 and 2t + 8, 2t + 9 of row g.  fp16 has few powers of two, so their
+  // unit follows a row's largest p s_v, whatever scales the values of keys without weight have: where that would pass 2^15
+  // it goes to 2^11, so that weights down to 2^-25 of the largest are rounded to 11 bits and those below are off by 2^-36
+  // of it at most.  A running maximum moves when the logits pass it by more than 2^8; what is summed so far stays as it is
+  // then, and the unit takes the factor.
+  float2 x[2][2], sum;
+  float pv[2][2][2], past, high;
+  auto weigh = [&]() {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    top[h] = fmaxf(fmaxf(s[0][h], s[0][2 + h]), fmaxf(s[1][h], s[1][2 + h])) * R.c[h];
-    move |= top[h] > R.m[h] + kLazyRescale;
-  }
-  if (__any_sync(0xffffffffu, move)) {
+    for (int b = 0; b < 2; ++b)
 #pragma unroll
-    for (int x = 4; x < 32; x <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, x));
-    float back = 1.f;
-    if (v * R.unit >= 2.f) {  // the new unit: one over the power of two below v
-      const float unit = __int_as_float((254 << 23) - int(__float_as_uint(v) & 0x7F800000u));
-      back = unit / R.unit;
-      R.unit = unit;
-    }
-    float f[2];
+      for (int u = 0; u < 2; ++u) {
+        x[b][u] = fma2(make_float2(s[b][2 * u], s[b][2 * u + 1]), make_float2(R.c[0], R.c[1]), make_float2(-R.m[0], -R.m[1]));
+        const float2 e = make_float2(ex2(x[b][u].x), ex2(x[b][u].y));
+        sum = b + u == 0 ? e : add2(sum, e);
+        pv[b][u][0] = e.x * vs[b][u];
+        pv[b][u][1] = e.y * vs[b][u];
+      }
+  };
+  auto most = [](float a, float b, float c, float d) { return fmaxf(max3(a, b, c), d); };
+  uint32_t w[2][2];
+  auto pack = [&]() {
+    const float2 unit = make_float2(R.unit[0], R.unit[1]);
+    float2 y[2][2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        y[b][u] = mul2(make_float2(pv[b][u][0], pv[b][u][1]), unit);
+        w[b][u] = tc::pack2<__half>(y[b][u].x, y[b][u].y);
+      }
+    high = max3(most(y[0][0].x, y[0][0].y, y[0][1].x, y[0][1].y), fmaxf(y[1][0].x, y[1][0].y), fmaxf(y[1][1].x, y[1][1].y));
+  };
+  weigh();
+  past = max3(most(x[0][0].x, x[0][0].y, x[0][1].x, x[0][1].y), fmaxf(x[1][0].x, x[1][0].y), fmaxf(x[1][1].x, x[1][1].y));
+  pack();
+  if (__any_sync(0xffffffffu, past > kLazyRescale || high >= kKv4TopWeight)) {
+    float back[2], was[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      float x = top[h];
+      float top = most(s[0][h], s[0][2 + h], s[1][h], s[1][2 + h]) * R.c[h];
 #pragma unroll
-      for (int y = 4; y < 32; y <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, y));
-      f[h] = 1.f;
-      if (x > R.m[h] + kLazyRescale) {
-        f[h] = ex2(R.m[h] - x);
-        R.m[h] = x;
+      for (int y = 4; y < 32; y <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, y));
+      back[h] = 1.f;
+      was[h] = R.unit[h];
+      if (top > R.m[h] + kLazyRescale) {
+        const float f = ex2(R.m[h] - top);
+        R.unit[h] = fminf(R.unit[h] * ex2(top - R.m[h]), kKv4TopUnit);
+        R.l[h] *= f;
+        back[h] = f;
+        R.m[h] = top;
       }
-      R.l[h] *= f[h];
-      f[h] *= back;
     }
+    weigh();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float top = most(pv[0][0][h], pv[0][1][h], pv[1][0][h], pv[1][1][h]);
+#pragma unroll
+      for (int y = 4; y < 32; y <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, y));
+      if (top * R.unit[h] >= kKv4TopWeight)  // 2^11 over the power of two of top
+        R.unit[h] = __int_as_float(((254 + 11) << 23) - int(__float_as_uint(top) & 0x7F800000u));
+      back[h] *= __fdividef(R.unit[h], was[h]);
+    }
+    pack();
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) R.o[i][e] *= f[e & 1];
+      for (int e = 0; e < 4; ++e) R.o[i][e] *= back[e & 1];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) R.z[e] *= f[e & 1];
+    for (int e = 0; e < 4; ++e) R.z[e] *= back[e & 1];
   }
-  // weights p s_v as operand columns: keys 2t, 2t + 1 and 2t + 8, 2t + 9 of row g
-  uint32_t w[2][2];
-  const float m0 = R.m[0] == -INFINITY ? 0.f : R.m[0], m1 = R.m[1] == -INFINITY ? 0.f : R.m[1];
+  R.l[0] += sum.x;
+  R.l[1] += sum.y;
 #pragma unroll
   for (int b = 0; b < 2; ++b)
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const float p0 = ex2(fmaf(s[b][2 * u], R.c[0], -m0)), p1 = ex2(fmaf(s[b][2 * u + 1], R.c[1], -m1));
-      R.l[0] += p0;
-      R.l[1] += p1;
-      const float x = vs[b][u] * R.unit;
-      w[b][u] = transpose8(tc::pack2<__half>(p0 * x, p1 * x));
-    }
+    for (int u = 0; u < 2; ++u) w[b][u] = transpose8(w[b][u]);
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
     const uint32_t b0 = w[b][0], b1 = w[b][1];
@@ -552,9 +581,9 @@ __device__ __forceinline__ void kv4_stage(const uint8_t* stage, const Kv4Places<
 template <typename T>
 __device__ __forceinline__ void kv4_put_state(Kv4Smem& sm, int warp, Kv4Rows<T>& R) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const float up = 131072.f / R.unit;  // 2^17: zero points came in as n 2^-17, codes as that or n 2^-21
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
+    const float up = __fdividef(131072.f, R.unit[h]);  // 2^17: zero points came in as n 2^-17, codes as that or n 2^-21
     float l = R.l[h];
 #pragma unroll
     for (int x = 4; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);

@@ -3,7 +3,9 @@
 Tolerances, with S = sum_j p_j |v_j|, P = sum_j p_j max_d |v_jd| (a quantised row holds a value of 7 s or more, for its
 range is at least 14 s: 15 sum_j p_j s_j <= 15 / 7 P) and n keys:
 
-* the weights' one rounding to fp16 is off by at most 2^-11 of each, fp32 logits, exponentials and sums by 1e-4 of S;
+* a weight (decode: p_j s_j) is rounded to fp16 once, in a unit that keeps the row's largest so far at 2^11 or more: off by
+  at most 2^-11 of itself, or, below 2^-14, by 2^-25 of the unit, 2^-36 of the largest: n 2^-36 15 / 7 P;
+* fp32 logits, exponentials and sums are off by less than 1e-4 of S;
 * decode sums weights times codes and weights times zero points apart, 16 keys a product.  A product keeps its addends, up
   to 16 and what is summed so far, down to 2^-25 of the largest's power of two, an operand below 2^-14 counting as that
   (so measured on a GB300).  Codes come in as n 2^-21 at the least: an addend loses at most 2^-14 2^-25 w, which is 2^-18
@@ -12,7 +14,7 @@ range is at least 14 s: 15 sum_j p_j s_j <= 15 / 7 P) and n keys:
   2 ceil(n / 128) products of a warp loses 17 2^-25 of it, twice (codes and zero points): 17 2^-24 15 / 7 P.
 
 |o - ref| <= (2^-11 + 1e-4) S + half a step of the output,
-for decode + ((min(n, 16) + 1) 17 / 16 2^-18 / 7 + 2 ceil(n / 128) 17 2^-24 15 / 7) P."""
+for decode + (n 2^-36 15 / 7 + (min(n, 16) + 1) 17 / 16 2^-18 / 7 + 2 ceil(n / 128) 17 2^-24 15 / 7) P."""
 from __future__ import annotations
 
 import numpy as np
@@ -25,6 +27,7 @@ from serving_attention_gb300 import kv4
 from test_gpu_kv4 import DEV, DT, Batch, _config, _f64, _gen, _i32, _randn
 
 pytestmark = pytest.mark.gpu
+SPLIT = dict(prefill_min_chunk=128, decode_min_chunk=64, split_factor=8)
 
 
 def _filled(b, kv, k, v):
@@ -50,7 +53,7 @@ def _check(b, cfg, window=-1, sink=0):
     n, decode = (np.repeat(x, np.diff(b.qo))[:, None, None] for x in (lens, rows <= 16))
     half = torch.finfo(o.dtype).eps / 2
     sums = (np.minimum(n, 16) + 1) * 17 / 16 * 2.0**-18 / 7 + 2 * np.ceil(n / 128) * 17 * 2.0**-24 * 15 / 7
-    tol = (2.0**-11 + 1e-4) * size + np.where(decode, sums, 0) * most
+    tol = (2.0**-11 + 1e-4) * size + np.where(decode, n * 2.0**-36 * 15 / 7 + sums, 0) * most
     tol = tol * (1 + half) + half * np.abs(ro) + torch.finfo(o.dtype).smallest_normal * 2 * half
     worst = float((np.abs(og - ro) / tol).max())
     assert worst <= 1, f"{worst:.2f} times the tolerance"
@@ -73,3 +76,65 @@ def test_dims_that_a_large_value_row_holds_as_zero(dtype, ratio, page):
         v[at, :, 3::16] *= ratio
         v[at].masked_fill_((torch.arange(128, device=DEV) % 16 != 3), 0)
     _check(_filled(b, kv, 0.5 * _randn((n, hkv, 128), dtype, 92), v.to(DT[dtype])), _config())
+
+
+# ------------------------------------------------ value scales far apart (decode)
+
+@pytest.mark.parametrize("dtype,std,large", [("fp16", 1.0, 61440.0), ("bf16", 2.0**-5, 61440.0), ("bf16", 2.0**-12, 61440.0),
+                                             ("bf16", 2.0**-12, 1.0), ("fp16", 2.0**-3, 4096.0)])
+@pytest.mark.parametrize("qo,page,split", [(1, 16, False), (4, 16, False), (1, 1, False), (4, 64, True)])
+def test_a_large_value_of_no_weight(dtype, std, large, qo, page, split):
+    """Logits of deviation 3 and one key some 60 below them, whose values are up to 2^28 times the others'."""
+    n, hkv, g = 4096, 2, 4
+    for at in (5, n // 2, n - 3):
+        b = Batch(100 + at, [qo], [n], hkv * g, hkv, page, dtype, 0)
+        base = _randn((hkv, 128), "fp16", 7).float()
+        b.q.copy_((base.repeat_interleave(g, 0) + 0.05 * torch.randn(b.q.shape, generator=_gen(8), device=DEV)).to(b.q.dtype))
+        k = 3 * torch.randn(n, hkv, 128, generator=_gen(9), device=DEV)
+        k[at] = -60 / (b.scale * base.square().sum(-1, keepdim=True)) * base
+        v = std * torch.randn(n, hkv, 128, generator=_gen(10), device=DEV)
+        v[at] = large * torch.where(torch.arange(128, device=DEV) % 2 == 0, 1.0, -1.0) * 0.5
+        _check(_filled(b, [n], k.to(DT[dtype]), v.to(DT[dtype])), _config(**(SPLIT if split else {})))
+
+
+@pytest.mark.parametrize("split", [False, True])
+@pytest.mark.parametrize("window,sink", [(-1, 0), (700, 5)])
+@pytest.mark.parametrize("first,last", [(-10, 8), (8, -10)])
+def test_values_that_grow_along_a_request(first, last, window, sink, split):
+    """Every stage of a warp brings values of another size, so its unit moves under what it holds."""
+    kv, hkv, g = [3000, 900, 64], 2, 4
+    b = Batch(120, [4, 1, 2], kv, hkv * g, hkv, 16, "bf16", 1)
+    k = torch.cat([_randn((n, hkv, 128), "bf16", 121 + n) for n in kv])
+    v = torch.cat([torch.randn(n, hkv, 128, generator=_gen(n), device=DEV) *
+                   torch.exp2(torch.linspace(first, last, n, device=DEV))[:, None, None] for n in kv]).to(torch.bfloat16)
+    _check(_filled(b, kv, k, v), _config(window_left=window, sink_tokens=sink, **(SPLIT if split else {})), window, sink)
+
+
+@pytest.mark.parametrize("split", [False, True])
+def test_large_values_that_some_rows_do_not_see(split):
+    """One query head a key head and 16 tokens, keys of equal weight: one of the last has values of 2^24 times the
+    others', which are all alike, and is hidden from all rows but the last five of a pass."""
+    kv, hkv = [1200, 40], 4
+    b = Batch(130, [16, 16], kv, hkv, hkv, 16, "fp16", 1)
+    v = (2.0**-9 * (1 + torch.arange(hkv, device=DEV)[:, None] * 0.3) *
+         (1 + torch.rand(128, generator=_gen(131), device=DEV))).expand(sum(kv), hkv, 128).half().clone()
+    for end in (1200, 1240):
+        v[end - 5] = (v[end - 5].float() * 2.0**24).clamp(max=61440.0).half()
+    k = torch.zeros_like(v)
+    _check(_filled(b, kv, k, v), _config(**(SPLIT if split else {})))
+
+
+# ------------------------------------------- a few keys far above a flat tail
+
+@pytest.mark.parametrize("qo", [1, 4])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("nats", [6, 12, 13.9, 15, 16, 16.5])
+def test_keys_far_below_others_without_values(qo, dtype, nats):
+    """Every 64th key is `nats` above all others and has no values: the output is that of the others."""
+    n, hkv, g = 3000, 2, 4
+    b = Batch(140, [qo], [n], hkv * g, hkv, 16, dtype, 0)
+    base = torch.where(torch.rand(hkv, 128, generator=_gen(3), device=DEV) < 0.5, -1.0, 1.0)
+    b.q.copy_(base.repeat_interleave(g, 0).expand(b.q.shape))
+    k, v = torch.zeros(n, hkv, 128, device=DEV), 2048 * (1 + torch.rand(n, hkv, 128, generator=_gen(4), device=DEV))
+    k[5::64], v[5::64] = nats / (b.scale * 128) * base, 0
+    _check(_filled(b, [n], k.to(DT[dtype]), v.to(DT[dtype])), _config())
