@@ -50,6 +50,8 @@ constexpr int kKv4RawStages = kTileN / kKv4RawKeys;  // a stage's readers are th
 constexpr int kKv4RawBytes = 9216;  // 64 blocks of one slot, 144 bytes each
 constexpr int kKv4QuantWarp0 = 4, kKv4QuantWarps = 4;
 constexpr int kKv4SoftmaxWarp0 = 8;
+constexpr float kKv4Lazy = 4.f, kKv4Room = 11.f;  // log2, of the weights: see kv4_pf_softmax
+static_assert(kKv4Lazy + kKv4Room <= 15.f, "weights pass fp16's end");
 
 struct Kv4PrefillBufs {
   uint16_t q[2][2][kTileM][64];  // [M tile][d half][row][dim], and so on as in PrefillBufs
@@ -338,9 +340,11 @@ __device__ void kv4_pf_softmax(const RunParams& p, Smem& sm, int32_t b0, int32_t
         lim = min(causal ? pos : rq.kv_len - 1, item.kv1 - 1);
         if (kMask) lo = window_low(var, pos);
       }
-      // lrun: sum of the fp32 P.  The product takes them in fp16, each off by at most half a step, 2^-11 of itself: O is then
-      // off by at most 2^-11 of the sum of P |V|, whichever sum divides it.  (The sum of the rounded ones, beside this one,
-      // took 7 % of the time.)
+      // lrun: sum of the fp32 P.  The product takes them in fp16, each off by at most half a step, 2^-11 of itself (what the
+      // roundings of a row have in common does not cancel, as it would in the sum of the rounded ones; that sum beside this
+      // one took 7 % of the time).  fp16 has few powers of two, so a row's P are held 2^kKv4Room up: those down to
+      // 2^-(14 + kKv4Room) of the largest are rounded to 11 bits, those below off by 2^-(25 + kKv4Room) at most.  Their
+      // largest is 2^(kKv4Lazy + kKv4Room), for the running maximum moves when the logits pass it by more than 2^kKv4Lazy.
       float mrun = -INFINITY, lrun = 0.f, c = 0.f;
       bool ok = true;
       for (int j = 0; j < ntiles; ++j) {
@@ -384,7 +388,7 @@ __device__ void kv4_pf_softmax(const RunParams& p, Smem& sm, int32_t b0, int32_t
         if (edge) tc::tmem_st_wait();
         const float mx = fmaxf(max3(mx4[0], mx4[1], mx4[2]), mx4[3]) * c;
         const float m_old = mrun;
-        const float m_new = (mx > m_old + kLazyRescale) ? mx : m_old;
+        const float m_new = (mx > m_old + kKv4Lazy) ? mx : m_old;
         const bool rescale = (m_new != m_old) && j > 0;
         if (__any_sync(0xffffffffu, rescale)) {
           // O holds P V of every earlier tile (covered by this S's commit)
@@ -400,9 +404,9 @@ __device__ void kv4_pf_softmax(const RunParams& p, Smem& sm, int32_t b0, int32_t
           tc::tmem_st_wait();
           if (rescale) lrun *= alpha;
         }
-        // P = 2^(s c - m) as fp16 pairs over the first 64 columns of the S
+        // P = 2^(s c - m + kKv4Room) as fp16 pairs over the first 64 columns of the S
         // buffer, published in two halves of 64 keys each
-        const float msub = (m_new == -INFINITY) ? 0.f : m_new;
+        const float msub = (m_new == -INFINITY) ? 0.f : m_new - kKv4Room;
         const float2 cc = make_float2(c, c), nms = make_float2(-msub, -msub);
         float2 sum4[4];
 #pragma unroll
@@ -443,7 +447,7 @@ __device__ void kv4_pf_softmax(const RunParams& p, Smem& sm, int32_t b0, int32_t
       const bool partial = item.part >= 0;
       int64_t at = -1;  // of the row, in bytes
       if (prow < nrows && !sm.abort) {
-        const float lse = lrun > 0.f ? (mrun + __log2f(lrun)) * 0.69314718055994531f : -INFINITY;
+        const float lse = lrun > 0.f ? (mrun - kKv4Room + __log2f(lrun)) * 0.69314718055994531f : -INFINITY;
         const int row = item.row0 + prow, t = row / G, head = item.hk * G + (row - t * G);
         const int64_t tok = int64_t(rq.qo_start) + t, part = int64_t(item.part) + prow;
         if (partial) {
