@@ -404,7 +404,8 @@ __device__ __forceinline__ void kv4_set_rows(const Kv4Params& kp, const Item& it
   }
   sum += __shfl_xor_sync(0xffffffffu, sum, 1);
   sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-  const float c = p.scale_log2 * __int_as_float((127 + 10 + ex) << 23);  // 2^(ex - 14), and the products' 2^-24
+  // 2^(ex - 14), and the products' 2^-24; above 0, or a hidden key's -inf would become a NaN
+  const float c = fmaxf(p.scale_log2 * __int_as_float((127 + 10 + ex) << 23), FLT_MIN);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     R.qs[h] = __shfl_sync(0xffffffffu, sum, 8 * t + 4 * h);

@@ -39,6 +39,8 @@
 // every short call).  Not kept: units of 64 keys with S two units ahead, whose
 // products read Q twice as often and need half again the instructions (364 us).
 #pragma once
+#include <cfloat>
+
 #include "kv4_params.h"
 #include "attention_kernel.cuh"
 #include "kv4_layout.h"
@@ -58,7 +60,8 @@ struct Kv4PrefillBufs {
   uint16_t k[2][2][kTileN][64];
   uint16_t v[2][2][kTileN][64];
   alignas(128) uint8_t raw[kKv4RawStages][kKv4RawBytes];
-  float q_scale[2][2 * kTileM];  // [item's parity][row]: log2-domain factor of the row's products
+  float q_scale[2][2 * kTileM];  // [item's parity][row]: log2-domain factor of the row's products, FLT_MIN at least (a hidden
+                                 // key's -inf times 0 would be a NaN; logits that small are 0)
   uint32_t good[kKv4RawStages][2];  // keys of a raw stage whose page lies in the cache, a bit each
 };
 
@@ -238,7 +241,7 @@ __device__ void kv4_pf_widen(const Kv4Params& kp, Smem& sm, int32_t b0, int32_t 
       if (lane == 0) mbar_arrive(&sm.k_full[st]);
       if (j == 0) {
         if (!warp_wait(&sm.q_raw, pe & 1, &sm.abort)) return;
-        sm.pf.q_scale[pe & 1][r] = kp.run.scale_log2 * kv4_turn_query<T>(sm.pf.q[0], r);
+        sm.pf.q_scale[pe & 1][r] = fmaxf(kp.run.scale_log2 * kv4_turn_query<T>(sm.pf.q[0], r), FLT_MIN);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.q_full);
@@ -298,7 +301,7 @@ __device__ void kv4_pf_queries(const Kv4Params& kp, Smem& sm, int which, int32_t
     if (!ok) break;
     if (nm == 2)
       for (int r = 32 * which + lane; r < kTileM; r += 64)
-        sm.pf.q_scale[pe & 1][kTileM + r] = p.scale_log2 * kv4_turn_query<T>(sm.pf.q[1], r);
+        sm.pf.q_scale[pe & 1][kTileM + r] = fmaxf(p.scale_log2 * kv4_turn_query<T>(sm.pf.q[1], r), FLT_MIN);
     fence_proxy_async_smem();  // read by the tensor core
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.q_full);

@@ -140,3 +140,18 @@ def test_keys_far_below_others_without_values(qo, dtype, nats):
     k, v = torch.zeros(n, hkv, 128, device=DEV), 2048 * (1 + torch.rand(n, hkv, 128, generator=_gen(4), device=DEV))
     k[5::64], v[5::64] = nats / (b.scale * 128) * base, 0
     _check(_filled(b, [n], k.to(DT[dtype]), v.to(DT[dtype])), _config())
+
+
+# --------------------------------------------------- small factors of the logits
+
+@pytest.mark.parametrize("qo", [4, 40])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("scale", [1e-9, 1e-12, 1e-20, 2.0**-124])
+def test_small_scales_and_rows_of_zeros(qo, dtype, scale):
+    """A row's factor, the scale times its power of two, stays above 0: what a mask hides stays hidden."""
+    b = Batch(150, [qo, 2], [300, 40], 8, 2, 16, dtype, 1, scale=scale)
+    b.q[::2] = 0
+    b.q[1::4] *= 2.0**-20
+    if dtype == "bf16":
+        b.q[3::4] *= 2.0**-110
+    _check(b, _config())
