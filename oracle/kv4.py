@@ -139,3 +139,23 @@ def attention(qo_indptr, kv_indptr, kv_indices, last_page_len, page_size, causal
                 o[rows, a], size[rows, a] = p @ vh, p @ np.abs(vh)
                 lse[rows, a] = np.where(ok, top + np.log(np.where(ok, l, 1)), -np.inf)
     return o, lse, size
+
+
+def row_faults(word, got, ref, size):
+    """What is wrong with a held row (values got [128], its word) of the fp64 row ref, which the quantiser met to within
+    `size`: names of the parts, none if it is as defined.
+
+    s is the range / 15 to fp16 (2^-11) and up by at most 15 of 1024 steps.  z is -lo / s rounded, behind two fp32 roundings
+    of up to 15 2^-24 each (below 2e-6).  A code is at most half a step off, or, kept within 0 .. 15 at the ends of the range
+    (15 s (1 + 2^-11) at most), 15 2^-11 < 2^-7 more."""
+    s, z = float(np.uint16(word & 0xFFF0).view(np.float16)), word & 15
+    lo, hi = min(ref.min(), 0.0), max(ref.max(), 0.0)
+    exact = (hi - lo) / 15
+    bad = []
+    if not exact * (1 - 2.0**-11) - size <= s <= exact * (1 + 2.0**-11 + 15 / 1024) + size:
+        bad.append("scale")
+    if abs(z - min(-lo / s, 15)) > 0.5 + size / s + 2e-6:
+        bad.append("zero point")
+    if (np.abs(got - ref) > s * (0.5 + 2.0**-7) + 3 * size).any():
+        bad.append("values")
+    return bad
