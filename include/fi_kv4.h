@@ -100,9 +100,10 @@ fi_status fi_kv4_append(const fi_kv4_append_args* args, void* stream);
  * fi_kv4_read -- the values held at num_rows slots, in 16 bits: row i of k_out
  * and v_out [num_rows, num_kv_heads, 128] is what slot slots[i] holds (exact in
  * fp16, rounded once in bf16), zeros for a slot outside the cache.  Either
- * output may have a NULL pointer: not written.  Slots may repeat.  Strides,
- * alignment and checks as above; the outputs must not overlap the cache or each
- * other.
+ * output may have a NULL pointer: not written.  Slots may repeat.  Strides and
+ * alignment as above.  Rows of an output are apart and nested, and outputs of the
+ * same strides do not meet (FI_ERR_INVALID_ARG); that outputs of other strides do
+ * not overlap each other, nor any output the cache, is the caller's to see to.
  */
 typedef struct {
     const int32_t* slots;

@@ -457,6 +457,9 @@ extern "C" fi_status fi_kv4_read(const fi_kv4_read_args* x, void* stream) {
     a.out_tok[v] = outs[v]->stride_tok;
     a.out_head[v] = outs[v]->stride_head;
   }
+  if (a.out[0] && a.out[1] &&
+      (a.out[0] == a.out[1] || !output_ok(x->k_out, x->v_out, x->num_rows, x->num_kv_heads, FI_KV4_HEAD_DIM)))
+    return FI_ERR_INVALID_ARG;
   a.slots = x->slots;
   a.cache = static_cast<const uint8_t*>(x->cache);
   a.page_stride = x->cache_strides[0];

@@ -66,3 +66,22 @@ def test_rotated_rows(dtype, rot, interleaved, norm):
             word = int(page[h, at]) + 256 * int(page[h, at + 1])
             got = oracle_kv4.get(raw, P, int(slots[t]), h)[0]
             assert oracle_kv4.row_faults(word, got, ref[t, h], size) == []
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+def test_read_into_one_buffer(rows):
+    """k and v rows side by side, heads inside or outside: apart, if one buffer."""
+    page, heads = 16, 3
+    cache = kv4.empty_cache(3, page, heads, DEV)
+    x, y = _randn((3 * page, heads, 128), "bf16", 1), _randn((3 * page, heads, 128), "bf16", 2)
+    kv4.append(None, None, _i32(range(3 * page)), None, None, x, y, cache, page)
+    slots = _i32(range(5, 5 + rows))
+    k, v = (torch.empty((rows, heads, 128), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    kv4.read(slots, cache, page, k, v)
+    for shape, cut in (((rows, heads, 2, 128), lambda b, i: b[:, :, i]), ((rows, 2, heads, 128), lambda b, i: b[:, i]),
+                       ((2, rows, heads, 128), lambda b, i: b[i])):
+        buf = torch.full(shape, 9.0, dtype=torch.bfloat16, device=DEV)
+        kv4.read(slots, cache, page, cut(buf, 0), cut(buf, 1))
+        assert torch.equal(cut(buf, 0), k) and torch.equal(cut(buf, 1), v)
+    with pytest.raises(RuntimeError):
+        kv4.read(slots, cache, page, k, k)

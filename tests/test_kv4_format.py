@@ -1,4 +1,4 @@
-"""Every word of the 4-bit format, and what the check of quantised rows finds (CPU)."""
+"""Every word of the 4-bit format, what the check of quantised rows finds, and outputs that a read refuses (CPU)."""
 from __future__ import annotations
 
 import math
@@ -6,8 +6,10 @@ import math
 import numpy as np
 import pytest
 
+import serving_attention_gb300 as fi
 from oracle import kv4 as oracle_kv4
 from oracle.kv4 import row_faults
+from serving_attention_gb300 import kv4
 
 
 def all_words():
@@ -72,3 +74,14 @@ def test_row_faults(seed):
         assert row_faults(word, np.where(np.arange(128) == 7, got[i] + 1.01 * got[i].std(), got[i]), x[i], size) == ["values"]
         double = word + 0x400
         assert row_faults(double, coded(x[i], double), x[i], size)[0] == "scale"
+
+
+@pytest.mark.parametrize("kw", [dict(v=64), dict(v=64 + 16), dict(v=64 + 256), dict(v=64 + 512 + 32), dict(v=64 - 512 * 3),
+                                dict(v=64, vt=512, vh=128), dict(v=64 + 128, kt=256, kh=256, vt=256, vh=256, hk=1),
+                                dict(v=64 + 16, n=1)])
+def test_read_refuses_outputs_that_meet(kw):
+    """Before any launch: the pointers are fake."""
+    a = dict(slots=32, n=4, k=64, kt=256, kh=128, v=1 << 20, vt=256, vh=128, hk=2, cache=128, cp=4224, ch=2112, page=16,
+             pages=10, dt=fi.BF16)
+    a.update(kw)
+    assert kv4.load().fi_kv4_read(kv4._READ_ARGS.pack(*a.values()), None) == 1
