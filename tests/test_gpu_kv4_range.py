@@ -112,6 +112,21 @@ def test_values_that_grow_along_a_request(first, last, window, sink, split):
     _check(_filled(b, kv, k, v), _config(window_left=window, sink_tokens=sink, **(SPLIT if split else {})), window, sink)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("qo,split", [(1, False), (4, True), (40, False)])
+@pytest.mark.parametrize("logits", [(-30, 30), (30, -30), (-3, 3)])
+@pytest.mark.parametrize("sizes", [(-9, 9), (9, -9)])
+def test_logits_and_values_that_grow_along_a_request(dtype, qo, split, logits, sizes):
+    """Maximum and unit move together or against each other, in nearly every stage."""
+    n, hkv, g = 2000, 2, 4
+    b = Batch(125, [qo], [n], hkv * g, hkv, 16, dtype, 0)
+    base = _randn((hkv, 128), "fp16", 126).float()
+    b.q.copy_((base.repeat_interleave(g, 0) + 0.05 * torch.randn(b.q.shape, generator=_gen(127), device=DEV)).to(b.q.dtype))
+    k = torch.linspace(*logits, n, device=DEV)[:, None, None] / (b.scale * base.square().sum(-1, keepdim=True)) * base
+    v = torch.randn(n, hkv, 128, generator=_gen(128), device=DEV) * torch.exp2(torch.linspace(*sizes, n, device=DEV))[:, None, None]
+    _check(_filled(b, [n], k.to(DT[dtype]), v.to(DT[dtype])), _config(**(SPLIT if split else {})))
+
+
 @pytest.mark.parametrize("split", [False, True])
 def test_large_values_that_some_rows_do_not_see(split):
     """One query head a key head and 16 tokens, keys of equal weight: one of the last has values of 2^24 times the
