@@ -125,9 +125,15 @@ fi_status fi_kv4_read(const fi_kv4_read_args* args, void* stream);
  * window and sink tokens as for fi_batch_paged_attention_run.
  *   q, o   [q_num_tokens, num_qo_heads, 128], dtype FI_FP16 or FI_BF16
  *     (a q row enters as fp16 times a power of two: exact down to 2^-24
- *     of its largest value).
+ *     of its largest value, which is finite and, in bf16, below 2^101).
  *   lse    fp32 [q_num_tokens, num_qo_heads], contiguous; may be NULL.
  *   sm_scale  positive (a normal fp32 number, its log2(e) multiple too).
+ * Logits, exponentials and sums are fp32.  Weights p_j (in a request of at most 16
+ * query tokens times query heads a key head: p_j times the scale s_j of v_j) are
+ * rounded to fp16 once: off by at most 2^-11 of themselves or, where that is more, by
+ * 2^-36 of the row's largest.  Those requests sum weights times codes and weights
+ * times zero points apart, so every dim is off by up to about 2^-14 of
+ * sum_j p_j s_j besides, which counts where the rows of weight hold zero in it.
  * A row with no visible key gets o = 0 and lse = -inf.  Slots past the end of a
  * request's last page, and keys that a row's mask hides, may hold any bytes;
  * the words of visible keys hold a finite s.  Page ids outside [0, num_pages)

@@ -16,10 +16,13 @@
 // thing; one warp per token, or per part of one when there are few tokens.  The
 // next group's rows are in flight while one is turned and coded.  cos and sin
 // stay in shared memory, read without bank conflicts, and no second group is held:
-// 8192 tokens of 32 + 8 heads, with the 16-bit rows read back by a launch behind it,
-// took 49 us (33 us of bytes at the copy rate) where one or two groups ahead with 16
-// to 20 warps on an SM took 60 to 64, conflicts 6 more, clamps behind the rounding 1 and
-// sums and products one at a time, or a lane's two angles one behind the other, 1 each.
+// 8192 tokens of 32 + 8 heads with norms and half pairs: 38.6 us (26.4 us of bytes at
+// the copy rate), without norms 35.1, neighbouring pairs 40.1.  Half pairs over 64
+// dims of a head 62: the other member of a pair is in another lane, 32 shuffles a
+// group.  (With the rows read back by a launch behind it, 49 us, one or two groups
+// ahead with 16 to 20 warps on an SM took 60 to 64, conflicts 6 more, clamps behind the
+// rounding 1 and sums and products one at a time, or a lane's two angles one behind
+// the other, 1 each.)
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -129,8 +132,8 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendBlocks) kv4_append_k
       const uint64_t turn = uint64_t(int64_t(pos)) * a.turns[i];  // modulo one turn
       // 2^-31: half turns in [-1, 1]; then the angle
       const float x = __fmul_rn(float(int32_t(turn >> 32)) * 4.6566128730773926e-10f, 3.14159265358979f);
-      float c, sn;  // what cosf and sinf give, for every number up to pi (all of them compared)
-      sincosf(x, &sn, &c);
+      float c, sn;
+      sincosf(x, &sn, &c);  // the same as sinf and cosf: once compared for every fp32 number up to pi
       c = __fmul_rn(c, a.amplitude);
       sn = __fmul_rn(sn, a.amplitude);
       if (kPairs == kHalfPairs) {
@@ -283,7 +286,8 @@ struct Kv4ReadParams {
 constexpr int kReadThreads = 256;
 
 // Eight lanes a row, each the words p and p + 8 of its codes: 128 contiguous
-// bytes of output a step.
+// bytes of output a step.  A lane has one row in flight, which waits for its slot,
+// then for codes and word: 8384 slots of 8 heads 10.2 us (6.5 at the copy rate).
 template <typename T>
 __global__ void __launch_bounds__(kReadThreads) kv4_read_kernel(const __grid_constant__ Kv4ReadParams a) {
   const int p = threadIdx.x & 7;

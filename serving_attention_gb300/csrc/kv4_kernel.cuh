@@ -36,12 +36,15 @@
 // What bounds it: the bytes of a long cache, its 132 a key and head, for up to
 // eight query rows a key head; more rows go over the keys again, from L2, at half
 // that rate.  Beyond a request's first 8192 keys every further one costs what its
-// bytes do at 6.7 TB/s.  64 requests of 512 to 32768 keys, 32 + 8 heads: 123 us,
-// 5.3 TB/s (97 us at the copy rate); two of 99991 and 131072 keys, 64 + 8 heads: 48 us
+// bytes do at 6.7 TB/s.  64 requests of 512 to 32768 keys, 32 + 8 heads: 121 us,
+// 5.4 TB/s (97 us at the copy rate); two of 99991 and 131072 keys, 64 + 8 heads: 48 us
 // (35).  One loader warp for all rings brought 4.4 TB/s; eight computing warps that
 // widened the codes took 157 us.  Short requests are latency: four of up to 512
-// keys, 8 + 2 heads, 6.6 us, of which the launch and the plan's loads are 3; 64 of
-// 64 to 512 keys on pages of one token 16 us, at 144 bytes a copy.
+// keys, 8 + 2 heads, 6.4 us, of which the launch and the plan's loads are 3; 64 of
+// 64 to 512 keys on pages of one token 16 us, at 144 bytes a copy.  The instance for
+// blocks below 16 slots, whose addresses are uniform values instead of numbers,
+// spills 120 bytes a thread at its 128 registers, and its loaders issue ring after
+// ring: the batch takes 229, 221, 182 and 156 us on pages of 1, 2, 4 and 8 tokens.
 #pragma once
 #include <cfloat>
 
@@ -57,13 +60,15 @@ constexpr int kKv4FirstWarp = 4;       // first computing warp
 constexpr int kKv4Warps = 12;          // computing warps of the 16-row tiles
 constexpr int kKv4GroupWarps = 4;      // warps of a group
 constexpr int kKv4Groups = kKv4Warps / kKv4GroupWarps;
-constexpr int kKv4GroupKeys = 1024;    // the longest chunk that one group takes
+// The longest chunk that one group takes.  152 requests of 1024 keys 41.4 us, with 512 here 57.9; 64 of 128 to 1024 keys 17.7
+// and 20.2.
+constexpr int kKv4GroupKeys = 1024;
 constexpr int kKv4Stage = 32;          // keys of a stage
 constexpr int kKv4Depth = 3;           // stages of a ring
 constexpr int kKv4StageBytes = 4608;   // 32 blocks of one slot, 144 bytes each
 // log2 of the smallest of the small pages that come by bulk copies, a page each; smaller ones in pieces of 16 bytes.
-// 64 requests of 512 to 32768 keys, us, by bulk copies and in pieces: pages of two tokens 240 and 221, of four 181 and
-// 215, of eight 155 and 210.
+// 64 requests of 512 to 32768 keys, us, by bulk copies and in pieces: pages of two tokens 240 and 221, of four 182 and
+// 215, of eight 156 and 210.
 constexpr int kKv4BulkLog2 = 2;
 constexpr int kKv4Tile = 8;            // packed query rows of a pass
 constexpr int kKv4CombRow = 132;       // floats from row to row of a warp's state (128 and 4 against bank conflicts)

@@ -12,9 +12,9 @@
 // head's successor is loaded before the head is turned.
 // Measured: 16384 tokens of 32 + 8 heads of 128 in 71 us, 5.7 TB/s (60 us at the
 // copy rate; 87 before the turns' reads met no bank twice and the sum took no more
-// shuffles than a head has lanes for); 1111 tokens of 24 + 24 heads of 80 in 9.2 us,
+// shuffles than a head has lanes for); 1111 tokens of 24 + 24 heads of 80 in 9.6 us,
 // where four blocks on an SM with cos and sin in registers took 16.3; 64 tokens in
-// 3.3 us, the launch and one chain of loads.
+// 3.5 us, the launch and one chain of loads.
 #include <cuda_runtime.h>
 
 #include <cmath>
