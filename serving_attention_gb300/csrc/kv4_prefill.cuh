@@ -32,11 +32,11 @@
 // between them; widening a tile takes 2.3.  Tensor cores are busy half of that time,
 // issue slots for 59 %.  Eight prompts of 128 to 2048 tokens behind up to 2048,
 // 32 + 8 heads: 318 us (in fp16 304), 1.1 PFLOP/s (188 us at the rate of plain bf16
-// products; 285 us from a cache in 16 bits, four times the memory).  What it took: straight code
-// as short as can be (the roles' loops together are longer than the instruction
-// cache: the widening unrolled cost 80 us), one row sum (22 us), hidden keys as
-// bits and once a tile, and output by four lanes a row (together 22 us, and 6 of
-// every short call).  Not kept: units of 64 keys with S two units ahead, whose
+// products; 285 us from a cache in 16 bits, four times the memory).  What it took:
+// straight code as short as can be (the roles' loops together are longer than the
+// instruction cache: the widening unrolled cost 80 us), one row sum (22 us), hidden
+// keys as bits and once a tile, and output by four lanes a row (together 22 us, and 6
+// of every short call).  Not kept: units of 64 keys with S two units ahead, whose
 // products read Q twice as often and need half again the instructions (364 us).
 #pragma once
 #include <cfloat>
